@@ -172,13 +172,13 @@ def prepare(case, seed):
 
 
 def _plan(case):
-    from gemm_matmulplan_broadcast_gb300 import GatedPlan, LayerNormPlan, TokenLogProbsPlan
+    import gemm_matmulplan_broadcast_gb300 as olc
     if case["op"] == "norm":
-        return LayerNormPlan(case["rows"], case["cols"], case["dtype"], eps=EPS)
+        return olc.LayerNormPlan(case["rows"], case["cols"], case["dtype"], eps=EPS)
     if case["op"] == "gate":
-        return GatedPlan(case["rows"], case["d_in"], case["d_hidden"], case["dtype"], act=case["act"],
-                         trans_w=case["trans_w"])
-    return TokenLogProbsPlan(case["rows"], case["vocab"], case["dtype"], top=case["top"])
+        return olc.GatedPlan(case["rows"], case["d_in"], case["d_hidden"], case["dtype"], act=case["act"],
+                             trans_w=case["trans_w"])
+    return olc.TokenLogProbsPlan(case["rows"], case["vocab"], case["dtype"], top=case["top"])
 
 
 def _run_own(s):
