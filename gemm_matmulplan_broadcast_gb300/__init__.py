@@ -9,4 +9,6 @@ raises (build with ``python -m gemm_matmulplan_broadcast_gb300.build``).
 
 from .binding import ALGORITHMS, GemmPlan, GroupedPlan, OlcError, Plan, gemm, load, matmul  # noqa: F401
 
-__all__ = ["Plan", "GemmPlan", "GroupedPlan", "matmul", "gemm", "load", "OlcError", "ALGORITHMS"]
+from .layers import LayerNormPlan, layer_norm  # noqa: F401
+
+__all__ = ["Plan", "GemmPlan", "GroupedPlan", "LayerNormPlan", "matmul", "layer_norm", "gemm", "load", "OlcError", "ALGORITHMS"]

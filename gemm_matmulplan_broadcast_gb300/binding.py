@@ -71,7 +71,7 @@ def load():
                 "libolc_matmul.so is not built; run `python -m gemm_matmulplan_broadcast_gb300.build` "
                 "(the CUDA library is required: there is no CPU fallback)")
         lib = ctypes.CDLL(LIB_PATH)
-        i64p = ctypes.POINTER(ctypes.c_int64)
+        i64, i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
         vp = ctypes.c_void_p
         sig = {
             "olc_matmul_plan_create": ([i64p, ctypes.c_int, i64p, ctypes.c_int, ctypes.c_int,
@@ -119,6 +119,12 @@ def load():
             "olc_matmul_plan_staging_copies": ([vp, vp, vp, vp, vp], ctypes.c_int),
             "olc_debug_alu_rate": ([ctypes.c_int, ctypes.c_int64, vp, ctypes.POINTER(ctypes.c_double)],
                                    ctypes.c_int),
+            "olc_layer_norm_plan_create": ([i64, i64, ctypes.c_double, ctypes.c_int,
+                                            ctypes.POINTER(vp)], ctypes.c_int),
+            "olc_layer_norm_plan_destroy": ([vp], None),
+            "olc_layer_norm_forward": ([vp, vp, i64, vp, vp, vp, i64, vp, vp, vp], ctypes.c_int),
+            "olc_layer_norm_backward": ([vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp],
+                                        ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)

@@ -1,0 +1,136 @@
+// What the plans beside the matrix products share: the device a plan is
+// bound to, and the device memory its calls write (workspaces).  Host only.
+#pragma once
+
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "olc_matmul.h"
+
+namespace olc {
+
+constexpr int kPlanDefaultSms = 152;   // GB300; used while no device is visible
+constexpr int64_t kPlanMaxBytes = int64_t(1) << 62;   // as for the matrix plans: offsets fit int64
+
+inline olc_status plan_status(cudaError_t e) {
+    if (e == cudaSuccess) return OLC_OK;
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? OLC_ERR_OOM : OLC_ERR_CUDA;
+}
+
+// a * b * bytes within the largest tensor the plans accept (a, b >= 0)
+inline bool plan_fits(int64_t a, int64_t b, int64_t bytes) {
+    int64_t n;
+    if (a == 0 || b == 0) return true;
+    return !__builtin_mul_overflow(a, b, &n) && !__builtin_mul_overflow(n, bytes, &n) && n <= kPlanMaxBytes;
+}
+
+inline int64_t plan_elem_bytes(olc_dtype dt) { return dt == OLC_FLOAT ? 4 : 2; }
+inline bool plan_dtype_ok(int dt) { return dt == OLC_FLOAT || dt == OLC_FLOAT16 || dt == OLC_BFLOAT16; }
+inline bool plan_misaligned(const void* p, int64_t bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) != 0;
+}
+inline bool plan_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Device binding and the plan's own device memory.  Calls that use that
+// memory are ordered across streams: one on another stream than the last
+// such call waits for it on the GPU (an event, created at the first use).
+// While a stream is capturing a graph nothing is recorded or waited for.
+struct PlanState {
+    int device;              // -1: made while no device was visible
+    int sm_count;
+    void* memory;
+    size_t bytes;
+    cudaEvent_t event;
+    cudaStream_t stream;
+    int event_live;
+
+    void init() {
+        std::memset(this, 0, sizeof *this);
+        device = -1;
+        sm_count = kPlanDefaultSms;
+        int n = 0, dev = 0, sms = 0;
+        if (cudaGetDeviceCount(&n) == cudaSuccess && n > 0 && cudaGetDevice(&dev) == cudaSuccess &&
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && sms > 0) {
+            device = dev;
+            sm_count = sms;
+        }
+        cudaGetLastError();
+    }
+
+    // the current device has to be the plan's
+    olc_status bind() {
+        int cur = -1;
+        if (cudaGetDevice(&cur) != cudaSuccess) return plan_status(cudaErrorNoDevice);
+        if (device < 0) device = cur;
+        return cur == device ? OLC_OK : OLC_ERR_WRONG_DEVICE;
+    }
+
+    // grow the plan's memory (the old one is freed first, which waits for
+    // the work that uses it)
+    olc_status ensure(size_t want) {
+        if (want <= bytes) return OLC_OK;
+        release_memory();
+        if (cudaMalloc(&memory, want) != cudaSuccess) {
+            cudaGetLastError();
+            memory = nullptr;
+            return OLC_ERR_OOM;
+        }
+        bytes = want;
+        return OLC_OK;
+    }
+
+    cudaError_t before_use(cudaStream_t s) {
+        if (!event_live || stream == s) return cudaSuccess;
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        cudaError_t e = cudaStreamIsCapturing(s, &cs);
+        if (e != cudaSuccess) return e;
+        if (cs != cudaStreamCaptureStatusNone) return cudaSuccess;
+        return cudaStreamWaitEvent(s, event, 0);
+    }
+
+    cudaError_t after_use(cudaStream_t s) {
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        cudaError_t e = cudaStreamIsCapturing(s, &cs);
+        if (e != cudaSuccess) return e;
+        if (cs != cudaStreamCaptureStatusNone) return cudaSuccess;
+        if (!event) {
+            e = cudaEventCreateWithFlags(&event, cudaEventDisableTiming);
+            if (e != cudaSuccess) {
+                event = nullptr;
+                return e;
+            }
+        }
+        e = cudaEventRecord(event, s);
+        if (e != cudaSuccess) return e;
+        stream = s;
+        event_live = 1;
+        return cudaSuccess;
+    }
+
+    void release_memory() {
+        if (memory) on_device([&] { cudaFree(memory); });
+        memory = nullptr;
+        bytes = 0;
+    }
+
+    void destroy() {
+        release_memory();
+        if (event) on_device([&] { cudaEventDestroy(event); });
+        event = nullptr;
+    }
+
+  private:
+    template <typename F>
+    void on_device(F&& f) {
+        int cur = -1;
+        cudaGetDevice(&cur);
+        if (device >= 0 && cur != device) cudaSetDevice(device);
+        f();
+        if (device >= 0 && cur >= 0 && cur != device) cudaSetDevice(cur);
+        cudaGetLastError();
+    }
+};
+
+}  // namespace olc

@@ -1,0 +1,141 @@
+"""Plans for the operators that stand around a language model's products
+(marshalling only, over the same library as ``binding``).
+
+    from gemm_matmulplan_broadcast_gb300 import LayerNormPlan
+
+A plan is made for fixed sizes and one element type ("float32", "float16" or
+"bfloat16"); its calls take CUDA tensors and outputs that the caller owns and
+enqueue kernels on ``stream`` (torch's current stream by default).  Row
+tensors are [rows, cols] (any leading dimensions when contiguous) with
+unit-stride columns; a two-dimensional one may have any row pitch.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+from .binding import DTYPE_CODES, _check, _stream_handle, load
+
+ROW_DTYPES = ("float32", "float16", "bfloat16")
+
+
+def _torch_dtype(name: str):
+    import torch
+    if name not in ROW_DTYPES:
+        raise ValueError("unsupported dtype %r" % (name,))
+    return getattr(torch, name)
+
+
+def _rows(name, t, rows, cols, dtype):
+    """Pointer and row pitch of a [rows, cols] tensor of the given type."""
+    if t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, the plan wants %s" % (name, t.dtype, dtype))
+    shape = t.shape
+    if not shape or shape[-1] != cols or t.numel() != rows * cols:
+        raise ValueError("%s has shape %s, the plan wants [%d, %d]" % (name, tuple(shape), rows, cols))
+    if t.numel() == 0:
+        return None, cols
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    if len(shape) != 2 or (cols > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be contiguous, or a matrix with unit-stride columns" % name)
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError("%s has overlapping rows" % name)
+    return t.data_ptr(), t.stride(0)
+
+
+def _flat(name, t, n, dtype):
+    """Pointer of a contiguous tensor of n elements (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError("%s has dtype %s, the plan wants %s" % (name, t.dtype, dtype))
+    if t.numel() != n:
+        raise ValueError("%s has %d elements, the plan wants %d" % (name, t.numel(), n))
+    if n == 0:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor" % name)
+    return t.data_ptr()
+
+
+class _PlanHandle:
+    """Lifetime of a library plan: closed explicitly, by ``with``, or with
+    the object."""
+
+    _destroy = ""
+
+    def _create(self, fn: str, *args):
+        self.lib = load()
+        h = ctypes.c_void_p()
+        _check(getattr(self.lib, fn)(*args, ctypes.byref(h)), fn)
+        self._h = h
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            getattr(self.lib, self._destroy)(self._h)
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class LayerNormPlan(_PlanHandle):
+    """Layer norm over the last axis of [rows, cols]: y = (x - mean) * rstd *
+    gamma + beta, and its gradients."""
+
+    _destroy = "olc_layer_norm_plan_destroy"
+
+    def __init__(self, rows: int, cols: int, dtype: str, eps: float = 1e-5):
+        import torch
+        self.rows, self.cols, self.dtype, self.eps = int(rows), int(cols), dtype, float(eps)
+        self._t, self._f32 = _torch_dtype(dtype), torch.float32
+        self._create("olc_layer_norm_plan_create", self.rows, self.cols, self.eps, DTYPE_CODES[dtype])
+
+    def forward(self, X, gamma, beta, Y, mean=None, rstd=None, stream=None):
+        """Y = layer norm of X.  gamma, beta: [cols] or None (ones, zeros);
+        mean, rstd: float32 [rows] outputs for the backward call, or None."""
+        rows, cols, t = self.rows, self.cols, self._t
+        x, xp = _rows("X", X, rows, cols, t)
+        y, yp = _rows("Y", Y, rows, cols, t)
+        st = self.lib.olc_layer_norm_forward(
+            self._h, x, xp, _flat("gamma", gamma, cols, t), _flat("beta", beta, cols, t), y, yp,
+            _flat("mean", mean, rows, self._f32), _flat("rstd", rstd, rows, self._f32), _stream_handle(stream))
+        _check(st, "olc_layer_norm_forward")
+        return Y
+
+    def backward(self, dY, X, gamma, mean, rstd, dX=None, dgamma=None, dbeta=None, stream=None):
+        """The gradients of X, gamma and beta (each None to skip it) from dY
+        and the forward call's mean and rstd."""
+        rows, cols, t = self.rows, self.cols, self._t
+        dy, dyp = _rows("dY", dY, rows, cols, t)
+        x, xp = _rows("X", X, rows, cols, t)
+        dx, dxp = (None, cols) if dX is None else _rows("dX", dX, rows, cols, t)
+        st = self.lib.olc_layer_norm_backward(
+            self._h, dy, dyp, x, xp, _flat("gamma", gamma, cols, t), _flat("mean", mean, rows, self._f32),
+            _flat("rstd", rstd, rows, self._f32), dx, dxp, _flat("dgamma", dgamma, cols, t),
+            _flat("dbeta", dbeta, cols, t), _stream_handle(stream))
+        _check(st, "olc_layer_norm_backward")
+        return dX, dgamma, dbeta
+
+
+def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out=None, stream=None):
+    """Layer norm of a CUDA tensor over its last axis through a fresh plan."""
+    import torch
+    if out is None:
+        out = torch.empty_like(X, memory_format=torch.contiguous_format)
+    cols = X.shape[-1] if X.dim() else 0
+    rows = X.numel() // cols if cols else 0
+    with LayerNormPlan(rows, cols, str(X.dtype).replace("torch.", ""), eps) as plan:
+        return plan.forward(X, gamma, beta, out, stream=stream)

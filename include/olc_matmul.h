@@ -384,6 +384,66 @@ int olc_grouped_plan_count(const olc_grouped_plan* plan);
 olc_status olc_grouped_execute(const olc_grouped_plan* plan, const void* const* A, const void* const* B,
                                void* const* Y, void* stream);
 
+/* ---- layer norm ----------------------------------------------------------
+ *
+ * The operators from here to the queries stand around a language model's
+ * products.  They take FLOAT, FLOAT16 and BFLOAT16 (OLC_ERR_DTYPE otherwise),
+ * compute in float32 whatever the element type, and round each result once
+ * with round-to-nearest-even.  Their plans follow the rules of the matrix
+ * plans: made for fixed sizes, bound to the device current at creation,
+ * executed asynchronously on any stream of it, not from two host threads at
+ * once; calls that use the plan's own device memory are ordered across
+ * streams by the plan, except inside a graph capture.  A pitch is the
+ * distance between the starts of two rows in elements (at least the row's
+ * length; not read for a single row).  Every pointer must be aligned to its
+ * element (OLC_ERR_INVALID); any such alignment and any pitch is taken, and
+ * rows that all start on 16-byte boundaries are moved fastest.
+ */
+typedef struct olc_layer_norm_plan olc_layer_norm_plan;
+
+/*
+ * Layer norm of each row of X [rows, cols]: with n = cols,
+ *     mean = sum_j x_j / n,   rstd = 1 / sqrt(sum_j (x_j - mean)^2 / n + eps),
+ *     y_j = (x_j - mean) * rstd * gamma_j + beta_j.
+ * rows >= 0, 1 <= cols < 2^31 - 65536, eps >= 0 (a row of equal values with
+ * eps = 0 gives NaN).  Errors: OLC_ERR_NULL, OLC_ERR_DTYPE,
+ * OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID (no columns, too many, a negative or
+ * NaN eps, more than 2^62 bytes), OLC_ERR_OOM.
+ */
+olc_status olc_layer_norm_plan_create(int64_t rows, int64_t cols, double eps, olc_dtype dtype,
+                                      olc_layer_norm_plan** out);
+
+/* NULL is accepted. */
+void olc_layer_norm_plan_destroy(olc_layer_norm_plan* plan);
+
+/*
+ * Forward.  gamma, beta: [cols] of the plan's type, NULL for ones and zeros.
+ * mean, rstd: [rows] float32, what the backward call reads; NULL to skip
+ * either.  Y may be X itself (same pointer and pitch).  Uses no device
+ * memory of the plan; with rows == 0 nothing is launched.  Errors:
+ * OLC_ERR_NULL, OLC_ERR_INVALID (a pitch below cols, a misaligned pointer),
+ * OLC_ERR_WRONG_DEVICE, OLC_ERR_CUDA.
+ */
+olc_status olc_layer_norm_forward(olc_layer_norm_plan* plan, const void* X, int64_t x_pitch, const void* gamma,
+                                  const void* beta, void* Y, int64_t y_pitch, float* mean, float* rstd,
+                                  void* stream);
+
+/*
+ * Backward: with xh = (x - mean) rstd and dxh = dy gamma,
+ *     dx = rstd (dxh - mean_j(dxh) - xh mean_j(dxh xh)),
+ *     dgamma = sum over rows of dy xh,   dbeta = sum over rows of dy.
+ * mean, rstd: the forward call's.  dX [rows, cols] (may be dY or X itself),
+ * dgamma, dbeta [cols]: NULL to skip any of them.  The column sums are
+ * float32 and are formed in an order that depends on the sizes and the
+ * device alone, so that results repeat bit for bit; with rows == 0 they are
+ * zeros.  The first call with dgamma or dbeta allocates the partial sums
+ * (cudaMalloc, kept by the plan): make it before any stream capture.
+ * Errors: as forward, and OLC_ERR_OOM.
+ */
+olc_status olc_layer_norm_backward(olc_layer_norm_plan* plan, const void* dY, int64_t dy_pitch, const void* X,
+                                   int64_t x_pitch, const void* gamma, const float* mean, const float* rstd, void* dX,
+                                   int64_t dx_pitch, void* dgamma, void* dbeta, void* stream);
+
 /* ---- queries ----------------------------------------------------------- */
 
 /* Output shape: writes up to `capacity` extents into shape[] and the rank

@@ -1,0 +1,46 @@
+"""Host-side checks of the layer plans (no GPU needed, no kernel launched):
+creation arguments, refusals by code."""
+
+import ctypes
+
+import pytest
+
+from gemm_matmulplan_broadcast_gb300 import LayerNormPlan, OlcError, binding
+
+CREATE_NORM = [
+    ((4, 0), "float32", 1e-5, "OLC_ERR_INVALID"),          # the mean of nothing
+    ((4, 2 ** 31), "float32", 1e-5, "OLC_ERR_INVALID"),
+    ((-1, 8), "float32", 1e-5, "OLC_ERR_NEGATIVE_DIM"),
+    ((4, -8), "float32", 1e-5, "OLC_ERR_NEGATIVE_DIM"),
+    ((4, 8), "float32", -1.0, "OLC_ERR_INVALID"),
+    ((4, 8), "float32", float("nan"), "OLC_ERR_INVALID"),
+    ((4, 8), "float32", float("inf"), "OLC_ERR_INVALID"),
+    ((2 ** 60, 2 ** 10), "float32", 1e-5, "OLC_ERR_INVALID"),
+]
+
+
+@pytest.mark.parametrize("shape,dtype,eps,error", CREATE_NORM)
+def test_layer_norm_plan_refuses(shape, dtype, eps, error):
+    with pytest.raises(OlcError) as e:
+        LayerNormPlan(*shape, dtype, eps)
+    assert e.value.name == error
+
+
+def test_layer_plans_take_three_types():
+    for dtype in ("float32", "float16", "bfloat16"):
+        LayerNormPlan(0, 1, dtype).close()
+    for dtype in ("float64", "float8_e4m3fn", "int8"):
+        with pytest.raises(ValueError):
+            LayerNormPlan(4, 8, dtype)
+    lib, h = binding.load(), ctypes.c_void_p()
+    for code in (11, 17, 0, -1):
+        assert lib.olc_layer_norm_plan_create(4, 8, 1e-5, code, ctypes.byref(h)) == 6 and not h.value
+    assert lib.olc_layer_norm_plan_create(4, 8, 1e-5, 1, None) == 1
+    lib.olc_layer_norm_plan_destroy(None)
+
+
+def test_layer_norm_plan_rows_of_zero_need_no_pointers():
+    with LayerNormPlan(0, 8, "bfloat16") as plan:
+        assert plan.lib.olc_layer_norm_forward(plan._h, None, 8, None, None, None, 8, None, None, None) == 0
+        assert plan.lib.olc_layer_norm_backward(plan._h, None, 8, None, 8, None, None, None, None, 8, None, None,
+                                                None) == 0
