@@ -119,6 +119,11 @@ def load():
             "olc_matmul_plan_staging_copies": ([vp, vp, vp, vp, vp], ctypes.c_int),
             "olc_debug_alu_rate": ([ctypes.c_int, ctypes.c_int64, vp, ctypes.POINTER(ctypes.c_double)],
                                    ctypes.c_int),
+            "olc_token_log_probs_plan_create": ([i64, i64, ctypes.c_int, ctypes.c_int,
+                                                 ctypes.POINTER(vp)], ctypes.c_int),
+            "olc_token_log_probs_plan_destroy": ([vp], None),
+            "olc_token_log_probs_forward": ([vp, vp, i64, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
+            "olc_token_log_probs_backward": ([vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp], ctypes.c_int),
             "olc_layer_norm_plan_create": ([i64, i64, ctypes.c_double, ctypes.c_int,
                                             ctypes.POINTER(vp)], ctypes.c_int),
             "olc_layer_norm_plan_destroy": ([vp], None),

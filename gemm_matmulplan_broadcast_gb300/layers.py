@@ -130,6 +130,49 @@ class LayerNormPlan(_PlanHandle):
         return dX, dgamma, dbeta
 
 
+class TokenLogProbsPlan(_PlanHandle):
+    """Log probabilities of given tokens from logits [rows, vocab], with the
+    entropy and the ``top`` most likely tokens of each row, and the gradient
+    of both."""
+
+    _destroy = "olc_token_log_probs_plan_destroy"
+
+    def __init__(self, rows: int, vocab: int, dtype: str, top: int = 0):
+        import torch
+        self.rows, self.vocab, self.dtype, self.top = int(rows), int(vocab), dtype, int(top)
+        self._t, self._f32, self._i64 = _torch_dtype(dtype), torch.float32, torch.int64
+        self._create("olc_token_log_probs_plan_create", self.rows, self.vocab, self.top, DTYPE_CODES[dtype])
+
+    def forward(self, logits, tokens, logprob, entropy=None, lse=None, top_logprob=None, top_index=None, stream=None):
+        """logprob[r] = log softmax(logits[r])[tokens[r]] (tokens: int64; a
+        negative one marks a row to ignore).  entropy, lse: float32 [rows];
+        top_logprob (float32), top_index (int64): [rows, top]; each may be
+        None."""
+        rows, f32 = self.rows, self._f32
+        z, pitch = _rows("logits", logits, rows, self.vocab, self._t)
+        n = rows * self.top
+        st = self.lib.olc_token_log_probs_forward(
+            self._h, z, pitch, _flat("tokens", tokens, rows, self._i64), _flat("logprob", logprob, rows, f32),
+            _flat("entropy", entropy, rows, f32), _flat("lse", lse, rows, f32),
+            _flat("top_logprob", top_logprob, n, f32), _flat("top_index", top_index, n, self._i64),
+            _stream_handle(stream))
+        _check(st, "olc_token_log_probs_forward")
+        return logprob
+
+    def backward(self, logits, tokens, lse, entropy, dlogprob, dlogits, dentropy=None, stream=None):
+        """dlogits from the gradients of logprob and entropy (either None for
+        zeros) and the forward call's lse and entropy."""
+        rows, f32 = self.rows, self._f32
+        z, pitch = _rows("logits", logits, rows, self.vocab, self._t)
+        dz, d_pitch = _rows("dlogits", dlogits, rows, self.vocab, self._t)
+        st = self.lib.olc_token_log_probs_backward(
+            self._h, z, pitch, _flat("tokens", tokens, rows, self._i64), _flat("lse", lse, rows, f32),
+            _flat("entropy", entropy, rows, f32), _flat("dlogprob", dlogprob, rows, f32),
+            _flat("dentropy", dentropy, rows, f32), dz, d_pitch, _stream_handle(stream))
+        _check(st, "olc_token_log_probs_backward")
+        return dlogits
+
+
 def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out=None, stream=None):
     """Layer norm of a CUDA tensor over its last axis through a fresh plan."""
     import torch
@@ -139,3 +182,16 @@ def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out=None, stream=Non
     rows = X.numel() // cols if cols else 0
     with LayerNormPlan(rows, cols, str(X.dtype).replace("torch.", ""), eps) as plan:
         return plan.forward(X, gamma, beta, out, stream=stream)
+
+
+def token_log_probs(logits, tokens, top: int = 0, stream=None):
+    """(logprob, entropy) of CUDA logits [rows, vocab], or (logprob, entropy,
+    top_logprob, top_index), through a fresh plan."""
+    import torch
+    rows, vocab = logits.shape
+    make = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=logits.device)  # noqa: E731
+    logprob, entropy = make(rows), make(rows)
+    best = (make(rows, top), make(rows, top, dtype=torch.int64)) if top else (None, None)
+    with TokenLogProbsPlan(rows, vocab, str(logits.dtype).replace("torch.", ""), top) as plan:
+        plan.forward(logits, tokens, logprob, entropy=entropy, top_logprob=best[0], top_index=best[1], stream=stream)
+    return (logprob, entropy) + (best if top else ())

@@ -444,6 +444,58 @@ olc_status olc_layer_norm_backward(olc_layer_norm_plan* plan, const void* dY, in
                                    int64_t x_pitch, const void* gamma, const float* mean, const float* rstd, void* dX,
                                    int64_t dx_pitch, void* dgamma, void* dbeta, void* stream);
 
+/* ---- log probabilities of given tokens ----------------------------------- */
+
+/* Most alternatives a plan reports for a row. */
+#define OLC_MAX_TOP 32
+
+typedef struct olc_token_log_probs_plan olc_token_log_probs_plan;
+
+/*
+ * For each row z of logits [rows, vocab] and a token t of its own:
+ *     lse = log sum_j e^(z_j),   logprob = z_t - lse,
+ *     entropy = -sum_j p_j log p_j  with p_j = e^(z_j - lse),
+ * and the `top` largest logits as log probabilities z_j - lse with their
+ * indices, in descending order, equal values by the lower index.
+ * Masked logits may be -inf or the type's lowest value.  A row of nothing but
+ * -inf gives lse = logprob = top_logprob = -inf and entropy 0, and a zero
+ * gradient.  A negative token marks a row to ignore: its logprob is 0 and has
+ * no gradient.  A token of vocab or more gives NaN (logprob, and the row's
+ * gradient from it).  A NaN or +inf logit makes the row's results NaN; a NaN
+ * ranks above every number.
+ * 0 <= rows < 2^27, 1 <= vocab < 2^31 - 65536, 0 <= top <= min(OLC_MAX_TOP,
+ * vocab).  Errors: OLC_ERR_NULL, OLC_ERR_DTYPE, OLC_ERR_NEGATIVE_DIM,
+ * OLC_ERR_INVALID, OLC_ERR_OOM.
+ */
+olc_status olc_token_log_probs_plan_create(int64_t rows, int64_t vocab, int top, olc_dtype dtype,
+                                           olc_token_log_probs_plan** out);
+
+/* NULL is accepted. */
+void olc_token_log_probs_plan_destroy(olc_token_log_probs_plan* plan);
+
+/*
+ * Forward.  tokens: [rows] int64; logprob: [rows] float32; entropy, lse
+ * [rows] float32, top_logprob [rows, top] float32 and top_index [rows, top]
+ * int64 may each be NULL.  Results repeat bit for bit.  Errors: OLC_ERR_NULL,
+ * OLC_ERR_INVALID (a pitch below vocab, a misaligned pointer),
+ * OLC_ERR_WRONG_DEVICE, OLC_ERR_CUDA.
+ */
+olc_status olc_token_log_probs_forward(olc_token_log_probs_plan* plan, const void* logits, int64_t pitch,
+                                       const int64_t* tokens, float* logprob, float* entropy, float* lse,
+                                       float* top_logprob, int64_t* top_index, void* stream);
+
+/*
+ * Backward: dz_j = dlogprob (1[j = t] - p_j) - dentropy p_j (log p_j + entropy).
+ * lse, entropy: the forward call's.  dlogprob, dentropy: [rows] float32, NULL
+ * for zeros (tokens is read with dlogprob only, entropy with dentropy only).
+ * dlogits may be the logits themselves (same pointer and pitch).  Errors: as
+ * forward; OLC_ERR_INVALID also for more than 2^31 - 1 blocks of work.
+ */
+olc_status olc_token_log_probs_backward(olc_token_log_probs_plan* plan, const void* logits, int64_t pitch,
+                                        const int64_t* tokens, const float* lse, const float* entropy,
+                                        const float* dlogprob, const float* dentropy, void* dlogits, int64_t d_pitch,
+                                        void* stream);
+
 /* ---- queries ----------------------------------------------------------- */
 
 /* Output shape: writes up to `capacity` extents into shape[] and the rank

@@ -5,7 +5,7 @@ import ctypes
 
 import pytest
 
-from gemm_matmulplan_broadcast_gb300 import LayerNormPlan, OlcError, binding
+from gemm_matmulplan_broadcast_gb300 import LayerNormPlan, OlcError, TokenLogProbsPlan, binding
 
 CREATE_NORM = [
     ((4, 0), "float32", 1e-5, "OLC_ERR_INVALID"),          # the mean of nothing
@@ -44,3 +44,33 @@ def test_layer_norm_plan_rows_of_zero_need_no_pointers():
         assert plan.lib.olc_layer_norm_forward(plan._h, None, 8, None, None, None, 8, None, None, None) == 0
         assert plan.lib.olc_layer_norm_backward(plan._h, None, 8, None, 8, None, None, None, None, 8, None, None,
                                                 None) == 0
+
+
+CREATE_SCORE = [
+    (4, 0, 0, "OLC_ERR_INVALID"),
+    (4, 2 ** 31, 0, "OLC_ERR_INVALID"),
+    (2 ** 27, 8, 0, "OLC_ERR_INVALID"),
+    (4, 8, 9, "OLC_ERR_INVALID"),               # more alternatives than tokens
+    (4, 100, 33, "OLC_ERR_INVALID"),
+    (4, 100, -1, "OLC_ERR_INVALID"),
+    (-4, 100, 0, "OLC_ERR_NEGATIVE_DIM"),
+    (4, -100, 0, "OLC_ERR_NEGATIVE_DIM"),
+]
+
+
+@pytest.mark.parametrize("rows,vocab,top,error", CREATE_SCORE)
+def test_token_log_probs_plan_refuses(rows, vocab, top, error):
+    with pytest.raises(OlcError) as e:
+        TokenLogProbsPlan(rows, vocab, "float16", top)
+    assert e.value.name == error
+
+
+def test_token_log_probs_plan_of_no_rows_needs_no_pointers():
+    lib, h = binding.load(), ctypes.c_void_p()
+    for code in (11, 17, 0):
+        assert lib.olc_token_log_probs_plan_create(4, 8, 0, code, ctypes.byref(h)) == 6 and not h.value
+    assert lib.olc_token_log_probs_plan_create(4, 8, 0, 1, None) == 1
+    lib.olc_token_log_probs_plan_destroy(None)
+    with TokenLogProbsPlan(0, 8, "bfloat16", 8) as plan:
+        assert lib.olc_token_log_probs_forward(plan._h, None, 8, None, None, None, None, None, None, None) == 0
+        assert lib.olc_token_log_probs_backward(plan._h, None, 8, None, None, None, None, None, None, 8, None) == 0
