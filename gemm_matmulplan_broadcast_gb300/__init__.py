@@ -9,7 +9,8 @@ raises (build with ``python -m gemm_matmulplan_broadcast_gb300.build``).
 
 from .binding import ALGORITHMS, GemmPlan, GroupedPlan, OlcError, Plan, gemm, load, matmul  # noqa: F401
 
-from .layers import LayerNormPlan, TokenLogProbsPlan, layer_norm, token_log_probs  # noqa: F401
+from .layers import (GatedPlan, LayerNormPlan, TokenLogProbsPlan, gated, layer_norm,  # noqa: F401
+                     token_log_probs)
 
-__all__ = ["Plan", "GemmPlan", "GroupedPlan", "LayerNormPlan", "TokenLogProbsPlan", "matmul",
-           "layer_norm", "token_log_probs", "gemm", "load", "OlcError", "ALGORITHMS"]
+__all__ = ["Plan", "GemmPlan", "GroupedPlan", "LayerNormPlan", "GatedPlan", "TokenLogProbsPlan",
+           "matmul", "layer_norm", "gated", "token_log_probs", "gemm", "load", "OlcError", "ALGORITHMS"]

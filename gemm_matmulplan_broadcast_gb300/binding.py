@@ -36,6 +36,7 @@ STATUS = {
     16: "OLC_ERR_NEEDS_RESIDUAL",
 }
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2}
+GATES = {"silu": 0, "gelu": 1, "relu": 2, "sigmoid": 3}
 MAX_RANK = 8
 
 _lock = threading.Lock()
@@ -119,6 +120,11 @@ def load():
             "olc_matmul_plan_staging_copies": ([vp, vp, vp, vp, vp], ctypes.c_int),
             "olc_debug_alu_rate": ([ctypes.c_int, ctypes.c_int64, vp, ctypes.POINTER(ctypes.c_double)],
                                    ctypes.c_int),
+            "olc_gated_plan_create": ([i64, i64, i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                       ctypes.POINTER(vp)], ctypes.c_int),
+            "olc_gated_plan_destroy": ([vp], None),
+            "olc_gated_forward": ([vp, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
+            "olc_gated_backward": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
             "olc_token_log_probs_plan_create": ([i64, i64, ctypes.c_int, ctypes.c_int,
                                                  ctypes.POINTER(vp)], ctypes.c_int),
             "olc_token_log_probs_plan_destroy": ([vp], None),

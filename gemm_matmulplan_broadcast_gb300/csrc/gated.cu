@@ -1,0 +1,948 @@
+// The gated feed-forward product and its gradient.
+//
+//   g = X Wg,  u = X Wu,  h = act(g) u                  X [M, D], W [D, F] (or stored [F, D])
+//   dg = dh u act'(g),  du = dh act(g)
+//   dX = dg Wg' + du Wu',  dWg = X' dg,  dWu = X' du
+//
+// FLOAT16 / BFLOAT16 run on tcgen05 CTA pairs with 256 x 256 accumulators in
+// TMEM, the mainloop of the general tiles with three choices of operands:
+//
+//   FWD  each CTA of the pair supplies half of the accumulator's columns: the
+//        first 128 columns of Wg, the second the same 128 columns of Wu.  So
+//        both CTAs hold g and u of the same outputs side by side and the
+//        epilogue forms act(g) u from float32 accumulators: neither product
+//        is written unless training asks for it.
+//   DX   one accumulator over both terms: the K loop runs through dg and Wg,
+//        then through du and Wu; nothing is added in memory.
+//   DW   both weights' gradients in one launch.
+//
+// dg and du are formed by one elementwise pass (five tensors of M x F moved,
+// no product) and rounded to 16 bits, because the tensor cores read 16-bit
+// operands: their rounding is of the size of the results' own.
+// Products bound these kernels (4 M D F operations forward, 8 backward) except
+// for few rows, where the weights' bytes do.
+#include <cstring>
+#include <new>
+
+#include "plan_state.h"
+#include "tc_ptx.cuh"
+
+namespace olc {
+namespace gated {
+
+using namespace olc::tc;
+
+enum Mode { FWD = 0, DX = 1, DW = 2 };
+
+// ---- activations ------------------------------------------------------------
+
+// act(g) and act'(g).  EXACT: float32 functions of full accuracy (FLOAT
+// tensors); otherwise the fast forms, good to about 2^-21, for results that
+// are rounded to 16 bits.
+template <bool EXACT>
+__device__ __forceinline__ float sigmoid(float g) {
+    if constexpr (EXACT) return 1.0f / (1.0f + expf(-g));
+    return __fdividef(1.0f, 1.0f + __expf(-g));
+}
+template <bool EXACT>
+__device__ __forceinline__ float gate_value(int act, float g) {
+    switch (act) {
+        case OLC_GATE_SILU: return g * sigmoid<EXACT>(g);
+        case OLC_GATE_GELU:
+            if constexpr (EXACT) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+            return gelu_f32(g);
+        case OLC_GATE_RELU: return g < 0.f ? 0.f : g;
+        default: return sigmoid<EXACT>(g);
+    }
+}
+template <bool EXACT>
+__device__ __forceinline__ void gate_slope(int act, float g, float& value, float& slope) {
+    switch (act) {
+        case OLC_GATE_SILU: {
+            const float s = sigmoid<EXACT>(g);
+            value = g * s;
+            slope = s * (1.0f + g * (1.0f - s));
+            return;
+        }
+        case OLC_GATE_GELU: {
+            // Phi(g) + g phi(g)
+            float cdf, phi;
+            if constexpr (EXACT) {
+                cdf = 0.5f * erfcf(g * -0.70710678118654752f);
+                phi = 0.39894228040143268f * expf(-0.5f * g * g);
+            } else {
+                cdf = 0.5f * gelu_one_plus_erf_f32(g);
+                phi = 0.39894228040143268f * __expf(-0.5f * g * g);
+            }
+            value = g * cdf;
+            slope = fmaf(g, phi, cdf);
+            return;
+        }
+        case OLC_GATE_RELU:
+            value = g < 0.f ? 0.f : g;
+            slope = g > 0.f ? 1.f : 0.f;
+            return;
+        default: {
+            const float s = sigmoid<EXACT>(g);
+            value = s;
+            slope = s * (1.0f - s);
+        }
+    }
+}
+
+// ---- the products on CTA pairs ------------------------------------------------
+
+constexpr int STAGES = 6;
+constexpr int A_BYTES = 128 * BK * 2;               // this CTA's 128 rows of A
+constexpr int B_BYTES = 128 * BK * 2;               // this CTA's 128 columns of B
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int PAIR_THREADS = 224;                   // A loader, MMA, 4 epilogue warps, B loader
+constexpr int STAGE_PITCH = 36;                     // 32-bit words per staged row
+constexpr int STAGING_BYTES = 4 * 32 * STAGE_PITCH * 4;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + 512;
+constexpr int TMEM_COLS = 512;                      // two accumulators
+constexpr int RASTER = 8;                           // pair rows a raster group
+
+struct Barriers {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+struct Params {
+    int64_t M, N;             // an output's rows and columns
+    int64_t tiles_m, tiles_n;
+    int64_t units;            // tiles x outputs x slices
+    int64_t k_blocks;         // K blocks of one operand pair
+    int64_t k_total;          // K blocks of an accumulator (DX: both pairs')
+    int64_t k_slice;          // K blocks a slice takes
+    int splits;               // K slices; > 1: float32 partial results
+    int items;                // outputs of their own operands (DW: 2)
+    int a_mn, b_k, b_blocks;
+    int is_bf16, act;
+    int aligned;              // every output row on a 16-byte boundary
+    void* Y[3];               // FWD: h, g, u (null: not kept); DX: dX; DW: dWg, dWu
+    float* partial;           // [split][plane][M][partial_pitch]
+    int64_t partial_pitch;
+    unsigned int* err;
+};
+
+struct Maps {
+    CUtensorMap a[2], b[2];
+};
+
+// one 16-bit row run through the warp's staging rows: 32 rows x 64 columns
+__device__ __forceinline__ void store_run(const Params& p, void* Y, uint32_t* rows, const uint32_t (&packed)[32],
+                                          int lane, int64_t row0, int64_t col0) {
+    uint4* mine = reinterpret_cast<uint4*>(rows + lane * STAGE_PITCH);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        mine[q] = make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]);
+    __syncwarp();
+    unsigned short* y = static_cast<unsigned short*>(Y);
+    if (p.aligned) {
+        const int cq = lane & 7;
+        const int64_t col = col0 + cq * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int rr = (lane >> 3) + 4 * j;
+            const uint4 w = *reinterpret_cast<const uint4*>(rows + rr * STAGE_PITCH + cq * 4);
+            if (row0 + rr < p.M && col < p.N) *reinterpret_cast<uint4*>(y + (row0 + rr) * p.N + col) = w;
+        }
+    } else {
+        const unsigned short* half = reinterpret_cast<const unsigned short*>(rows);
+        for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t col = col0 + lane + 32 * j;
+                if (col < p.N) y[(row0 + rr) * p.N + col] = half[rr * STAGE_PITCH * 2 + lane + 32 * j];
+            }
+        }
+    }
+    __syncwarp();                                    // the rows are rewritten by the next run
+}
+
+// 32 float32 columns of the warp's 32 rows into a partial plane
+__device__ __forceinline__ void store_partial(const Params& p, float* plane, uint32_t* rows, const uint32_t (&r)[32],
+                                              int lane, int64_t row0, int64_t col0) {
+    uint4* mine = reinterpret_cast<uint4*>(rows + lane * STAGE_PITCH);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) mine[q] = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+    __syncwarp();
+    const int cq = lane & 7;
+    const int64_t col = col0 + cq * 4;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int rr = (lane >> 3) + 4 * j;
+        const uint4 w = *reinterpret_cast<const uint4*>(rows + rr * STAGE_PITCH + cq * 4);
+        if (row0 + rr < p.M && col < p.partial_pitch)
+            *reinterpret_cast<uint4*>(plane + (row0 + rr) * p.partial_pitch + col) = w;
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int is_bf16) {
+    if (is_bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+pair_kernel(const __grid_constant__ Maps maps, const Params p) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* base =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint32_t* staging = reinterpret_cast<uint32_t*>(base + STAGES * STAGE_BYTES);
+    Barriers* s = reinterpret_cast<Barriers*>(base + STAGES * STAGE_BYTES + STAGING_BYTES);
+    volatile int* abort_flag = &s->abort_flag;
+    const uint32_t rank = pair::cluster_rank();
+    const bool leader = rank == 0;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&s->full[i], 2);        // the leader's A and B loaders arm it
+            mbar_init(&s->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s->acc_full[i], 1);
+            mbar_init(&s->acc_empty[i], 8);   // four epilogue warps in each CTA
+        }
+        mbar_init(&s->drain, 1);
+        s->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) pair::tmem_alloc2(&s->tmem_base, TMEM_COLS);
+    tc_fence_before();
+    pair::cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = s->tmem_base;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // unit -> K slice, output, tile (groups of RASTER pair rows, rows fastest)
+    const int64_t per_item = p.tiles_m * p.tiles_n;
+    auto coords = [&](int64_t u, int& slice, int& item, int64_t& mb, int64_t& nb) {
+        slice = (int)(u % p.splits);
+        const int64_t t = u / p.splits;
+        item = (int)(t / per_item);
+        const int64_t r = t % per_item;
+        const int64_t span = (int64_t)RASTER * p.tiles_n;
+        const int64_t first = r / span * RASTER;
+        const int64_t gm = min64(p.tiles_m - first, RASTER);
+        const int64_t in = r % span;
+        mb = first + in % gm;
+        nb = in / gm;
+    };
+
+    if (warp == 0 || warp == 6) {
+        if (lane == 0) {
+            const bool load_a = warp == 0;
+            const uint32_t stage0 = smem_u32(base);
+            const uint32_t full0_leader = pair::map_to(&s->full[0], 0);
+            uint32_t stage = 0, phase = 0, armed_bits = 0, parity_bits = 0;
+            bool ok = true;
+            for (int64_t u = pair::cluster_id(); u < p.units && ok; u += pair::cluster_count()) {
+                int slice, item;
+                int64_t mb, nb;
+                coords(u, slice, item, mb, nb);
+                const int m0 = (int)(mb * 256 + rank * 128);
+                const int n0 = (int)(MODE == FWD ? nb * 128 : nb * 256 + rank * 128);
+                const int64_t kb0 = slice * p.k_slice, kb1 = min64(p.k_total, kb0 + p.k_slice);
+                const uint32_t tx = load_a ? 2u * A_BYTES : 2u * B_BYTES;
+                for (int64_t kb = kb0; kb < kb1; ++kb) {
+                    // which operand pair, and where along its K
+                    int which = MODE == DW ? item : 0;
+                    int k0 = (int)kb * BK;
+                    if (MODE == DX && kb >= p.k_blocks) {
+                        which = 1;
+                        k0 = (int)(kb - p.k_blocks) * BK;
+                    }
+                    const CUtensorMap* map = load_a ? &maps.a[MODE == FWD ? 0 : which]
+                                                    : &maps.b[MODE == FWD ? (int)rank : which];
+                    if (!mbar_wait(&s->empty[stage], phase ^ 1, abort_flag, p.err)) { ok = false; break; }
+                    const uint32_t sa = stage0 + stage * STAGE_BYTES;
+                    const uint32_t sb = sa + A_BYTES;
+                    const uint32_t full_leader = full0_leader + stage * (uint32_t)sizeof(uint64_t);
+                    if (leader) {
+                        mbar_arrive_expect_tx(&s->full[stage], tx);
+                        armed_bits |= 1u << stage;
+                        parity_bits = (parity_bits & ~(1u << stage)) | (phase << stage);
+                    }
+                    if (load_a) {
+                        if (!p.a_mn) {
+                            pair::tma_load_3d_pair(sa, map, full_leader, k0, m0, 0);
+                        } else {
+                            pair::tma_load_3d_pair(sa, map, full_leader, m0, k0, 0);
+                            pair::tma_load_3d_pair(sa + 64 * BK * 2, map, full_leader, m0 + 64, k0, 0);
+                        }
+                    } else if (p.b_k) {
+                        pair::tma_load_3d_pair(sb, map, full_leader, k0, n0, 0);
+                    } else if (p.b_blocks) {
+                        pair::tma_load_4d_pair(sb, map, full_leader, 0, k0, n0 >> 6, 0);
+                    } else {
+                        pair::tma_load_3d_pair(sb, map, full_leader, n0, k0, 0);
+                        pair::tma_load_3d_pair(sb + 64 * BK * 2, map, full_leader, n0 + 64, k0, 0);
+                    }
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (*abort_flag && leader) {
+                for (int i = 0; i < STAGES; ++i)
+                    if ((armed_bits >> i) & 1u) mbar_wait_drain(&s->full[i], (parity_bits >> i) & 1u);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            const uint32_t idesc = instr_desc(p.is_bf16, 256, 256, p.a_mn, p.b_k ? 0 : 1);
+            const uint32_t stage0 = smem_u32(base);
+            const uint64_t a_desc0 =
+                p.a_mn ? smem_desc(stage0, 64 * BK * 2, 1024, 2u) : smem_desc(stage0, 16, 1024, 2u);
+            const uint64_t b_desc0 = p.b_k ? smem_desc(stage0 + A_BYTES, 16, 1024, 2u)
+                                           : smem_desc(stage0 + A_BYTES, 64 * BK * 2, 1024, 2u);
+            const uint64_t a_step = p.a_mn ? (UMMA_K * 128) >> 4 : (UMMA_K * 2) >> 4;
+            const uint64_t b_step = p.b_k ? (UMMA_K * 2) >> 4 : (UMMA_K * 128) >> 4;
+            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+            bool ok = true;
+            for (int64_t u = pair::cluster_id(); u < p.units && ok; u += pair::cluster_count()) {
+                const int64_t kb0 = (u % p.splits) * p.k_slice, kb1 = min64(p.k_total, kb0 + p.k_slice);
+                if (!mbar_wait(&s->acc_empty[acc], acc_phase ^ 1, abort_flag, p.err)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * 256;
+                uint32_t first = 0u;
+                for (int64_t kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&s->full[stage], phase, abort_flag, p.err)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t so = (uint64_t)((stage * STAGE_BYTES) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                        pair::mma2_f16(d_tmem, a_desc0 + so + kk * a_step, b_desc0 + so + kk * b_step, idesc,
+                                       kk > 0 ? 1u : first);
+                    first = 1u;
+                    pair::commit2_both(&s->empty[stage]);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                pair::commit2_both(&s->acc_full[acc]);
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            }
+            pair::commit2_local(&s->drain);
+            mbar_wait_drain(&s->drain, 0);
+        }
+    } else {
+        const int lane_group = warp & 3;
+        const uint32_t acc_empty_leader[2] = {pair::map_to(&s->acc_empty[0], 0), pair::map_to(&s->acc_empty[1], 0)};
+        uint32_t* rows = staging + lane_group * 32 * STAGE_PITCH;
+        uint32_t acc = 0, acc_phase = 0;
+        for (int64_t u = pair::cluster_id(); u < p.units; u += pair::cluster_count()) {
+            int slice, item;
+            int64_t mb, nb;
+            coords(u, slice, item, mb, nb);
+            if (!mbar_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err)) break;
+            tc_fence_after();
+            const int64_t row0 = mb * 256 + rank * 128 + lane_group * 32;     // the warp's first row
+            const uint32_t t_base = tmem_base + ((uint32_t)(lane_group * 32) << 16) + acc * 256;
+            if (p.splits > 1) {
+                const int planes = MODE == DX ? 1 : 2;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(t_base + c, r);
+                    const int plane = MODE == FWD ? c >> 7 : item;
+                    const int64_t col0 = MODE == FWD ? nb * 128 + (c & 127) : nb * 256 + c;
+                    if (row0 >= p.M || col0 >= p.N) continue;
+                    store_partial(p, p.partial + ((int64_t)slice * planes + plane) * p.M * p.partial_pitch, rows, r,
+                                  lane, row0, col0);
+                }
+            } else if constexpr (MODE == FWD) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 64) {
+                    uint32_t ph[32], pg[32], pu[32];
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t g[32], x[32];
+                        tmem_ld_32x32b_x32(t_base + c + hh * 32, g);
+                        tmem_ld_32x32b_x32(t_base + 128 + c + hh * 32, x);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
+                            const float u0 = __uint_as_float(x[2 * i]), u1 = __uint_as_float(x[2 * i + 1]);
+                            ph[hh * 16 + i] = pack16(gate_value<false>(p.act, g0) * u0,
+                                                     gate_value<false>(p.act, g1) * u1, p.is_bf16);
+                            pg[hh * 16 + i] = pack16(g0, g1, p.is_bf16);
+                            pu[hh * 16 + i] = pack16(u0, u1, p.is_bf16);
+                        }
+                    }
+                    const int64_t col0 = nb * 128 + c;
+                    if (row0 >= p.M || col0 >= p.N) continue;
+                    store_run(p, p.Y[0], rows, ph, lane, row0, col0);
+                    if (p.Y[1]) store_run(p, p.Y[1], rows, pg, lane, row0, col0);
+                    if (p.Y[2]) store_run(p, p.Y[2], rows, pu, lane, row0, col0);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 64) {
+                    uint32_t packed[32];
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(t_base + c + hh * 32, r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            packed[hh * 16 + i] =
+                                pack16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]), p.is_bf16);
+                    }
+                    const int64_t col0 = nb * 256 + c;
+                    if (row0 >= p.M || col0 >= p.N) continue;
+                    store_run(p, p.Y[MODE == DW ? item : 0], rows, packed, lane, row0, col0);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) pair::remote_arrive(acc_empty_leader[acc]);
+            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    pair::cluster_sync();          // no remote arrival may target a CTA that has left
+    tc_fence_after();
+    if (warp == 1) pair::tmem_dealloc2(tmem_base, TMEM_COLS);
+}
+
+// ---- elementwise passes ---------------------------------------------------------
+
+// Slices summed in slice order; FWD: h, g and u from the two planes' sums.
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const Params p, int mode) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int planes = mode == DX ? 1 : 2;
+    const int64_t groups = ceil_div(p.N, 4), plane_elems = p.M * p.partial_pitch;
+    const int64_t n = p.M * groups * (mode == DW ? 2 : 1);
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+        const int64_t item = e / (p.M * groups), in = e % (p.M * groups);
+        const int64_t row = in / groups, col = in % groups * 4;
+        float4 v[2];
+        for (int q = 0; q < (mode == FWD ? 2 : 1); ++q) {
+            const float* src = p.partial + (mode == FWD ? q : item) * plane_elems + row * p.partial_pitch + col;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s = 0; s < p.splits; ++s) {
+                const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)s * planes * plane_elems);
+                a.x += x.x;
+                a.y += x.y;
+                a.z += x.z;
+                a.w += x.w;
+            }
+            v[q] = a;
+        }
+        const float a[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        const int64_t at = row * p.N + col;
+        if (mode == FWD) {
+            const float b[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (col + i >= p.N) break;
+                static_cast<T*>(p.Y[0])[at + i] = Num<T>::from_acc(gate_value<false>(p.act, a[i]) * b[i]);
+                if (p.Y[1]) static_cast<T*>(p.Y[1])[at + i] = Num<T>::from_acc(a[i]);
+                if (p.Y[2]) static_cast<T*>(p.Y[2])[at + i] = Num<T>::from_acc(b[i]);
+            }
+        } else {
+            T* y = static_cast<T*>(p.Y[mode == DW ? item : 0]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + i < p.N) y[at + i] = Num<T>::from_acc(a[i]);
+        }
+    }
+}
+
+// dg = dh u act'(g), du = dh act(g); outputs with a row pitch.  V = 1: any
+// alignment, else 16 bytes an access.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) slope_kernel(const T* dH, const T* G, const T* U, T* dG, T* dU, int64_t rows,
+                                                    int64_t cols, int64_t pitch, int act) {
+    struct alignas(V * sizeof(T)) Pack { T v[V]; };
+    constexpr bool EXACT = sizeof(T) == 4;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t groups = cols / V;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < rows * groups; e += (int64_t)gridDim.x * 256) {
+        const int64_t row = e / groups, col = e % groups * V;
+        const Pack h = *reinterpret_cast<const Pack*>(dH + row * cols + col);
+        const Pack g = *reinterpret_cast<const Pack*>(G + row * cols + col);
+        const Pack u = *reinterpret_cast<const Pack*>(U + row * cols + col);
+        Pack a, b;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float value, slope;
+            gate_slope<EXACT>(act, Num<T>::to_acc(g.v[i]), value, slope);
+            const float d = Num<T>::to_acc(h.v[i]);
+            a.v[i] = Num<T>::from_acc(d * Num<T>::to_acc(u.v[i]) * slope);
+            b.v[i] = Num<T>::from_acc(d * value);
+        }
+        *reinterpret_cast<Pack*>(dG + row * pitch + col) = a;
+        *reinterpret_cast<Pack*>(dU + row * pitch + col) = b;
+    }
+}
+
+// FLOAT: h = act(g) u; h may be u
+__global__ void __launch_bounds__(256) product_kernel(const float* G, const float* U, float* H, int64_t n, int act) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256)
+        H[e] = gate_value<true>(act, G[e]) * U[e];
+}
+
+// ---- host side ---------------------------------------------------------------------
+
+constexpr int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
+constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// A stored matrix of 16-bit elements the TMA can read: base on a 16-byte
+// boundary, pitch a multiple of 8.
+struct Stored {
+    const void* base;
+    int64_t rows, cols, pitch;
+};
+
+// A product's K slices: enough that its units fill the pairs, each slice at
+// least four K blocks.
+int slices_of(int64_t tiles, int64_t k_total, int sm_count) {
+    const int64_t pairs = sm_count / 2;
+    if (tiles <= 0 || 2 * tiles > pairs) return 1;
+    const int64_t want = min64(pairs / tiles, k_total / 4);
+    if (want < 2) return 1;
+    return (int)ceil_div(k_total, ceil_div(k_total, want));    // no empty slice
+}
+
+struct Product {
+    int mode;
+    int64_t M, N, K;
+    Stored a[2], b[2];
+    bool a_mn, b_k;
+    void* Y[3];
+    int act;
+};
+
+int64_t tiles_of(int mode, int64_t M, int64_t N) {
+    return ceil_div(M, 256) * ceil_div(N, mode == FWD ? 128 : 256) * (mode == DW ? 2 : 1);
+}
+int product_slices(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
+    return slices_of(tiles_of(mode, M, N), ceil_div(K, BK) * (mode == DX ? 2 : 1), sm_count);
+}
+size_t product_partial_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
+    const int s = product_slices(mode, M, N, K, sm_count);
+    return s > 1 ? (size_t)s * (mode == DX ? 1 : 2) * (size_t)M * (size_t)pad8(N) * sizeof(float) : 0;
+}
+
+template <int MODE>
+cudaError_t launch_product(olc_dtype dt, const Product& w, float* partial, int sm_count, cudaStream_t s) {
+    const int bf = dt == OLC_BFLOAT16;
+    Maps maps;
+    std::memset(&maps, 0, sizeof maps);
+    bool blocks = !w.b_k;
+    for (int i = 0; i < 2 && blocks; ++i)
+        blocks = w.N % 64 == 0 && encode_b_blocks(&maps.b[i], w.b[i].base, bf, w.N, w.K, 1, w.b[i].pitch);
+    for (int i = 0; i < 2; ++i) {
+        const Stored &a = w.a[i], &b = w.b[i];
+        const bool ok_a = w.a_mn ? encode_3d(&maps.a[i], a.base, bf, a.cols, a.rows, 1, 64, BK,
+                                             CU_TENSOR_MAP_SWIZZLE_128B, a.pitch)
+                                 : encode_3d(&maps.a[i], a.base, bf, a.cols, a.rows, 1, BK, 128,
+                                             CU_TENSOR_MAP_SWIZZLE_128B, a.pitch);
+        const bool ok_b = blocks || (w.b_k ? encode_3d(&maps.b[i], b.base, bf, b.cols, b.rows, 1, BK, 128,
+                                                       CU_TENSOR_MAP_SWIZZLE_128B, b.pitch)
+                                           : encode_3d(&maps.b[i], b.base, bf, b.cols, b.rows, 1, 64, BK,
+                                                       CU_TENSOR_MAP_SWIZZLE_128B, b.pitch));
+        if (!ok_a || !ok_b) return cudaErrorInvalidValue;
+    }
+    Params p;
+    std::memset(&p, 0, sizeof p);
+    p.M = w.M;
+    p.N = w.N;
+    p.tiles_m = ceil_div(w.M, 256);
+    p.tiles_n = ceil_div(w.N, MODE == FWD ? 128 : 256);
+    p.items = MODE == DW ? 2 : 1;
+    p.k_blocks = ceil_div(w.K, BK);
+    p.k_total = p.k_blocks * (MODE == DX ? 2 : 1);
+    p.splits = product_slices(MODE, w.M, w.N, w.K, sm_count);
+    p.k_slice = ceil_div(p.k_total, p.splits);
+    p.units = p.tiles_m * p.tiles_n * p.items * p.splits;
+    p.a_mn = w.a_mn;
+    p.b_k = w.b_k;
+    p.b_blocks = blocks;
+    p.is_bf16 = bf;
+    p.act = w.act;
+    p.aligned = w.N % 8 == 0;
+    for (int i = 0; i < 3; ++i) {
+        p.Y[i] = w.Y[i];
+        if (w.Y[i] && !plan_aligned16(w.Y[i])) p.aligned = 0;
+    }
+    p.partial = partial;
+    p.partial_pitch = pad8(w.N);
+    p.err = device_error_word();
+    cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(pair_kernel<MODE>), SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    const int64_t clusters = min64(p.units, sm_count / 2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters));
+    cfg.blockDim = dim3(PAIR_THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, pair_kernel<MODE>, maps, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const int64_t work = p.M * ceil_div(p.N, 4) * p.items;
+    const dim3 grid((unsigned)min64(ceil_div(work, 256), (int64_t)sm_count * 8));
+    return bf ? launch_pdl(join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p, MODE)
+              : launch_pdl(join_kernel<__half>, grid, dim3(256), 0, s, p, MODE);
+}
+
+template <typename T>
+cudaError_t launch_slope(const void* dH, const void* G, const void* U, void* dG, void* dU, int64_t rows, int64_t cols,
+                         int64_t pitch, int act, int sm_count, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const bool wide = cols % V == 0 && plan_aligned16(dH) && plan_aligned16(G) && plan_aligned16(U);
+    const dim3 grid((unsigned)min64(ceil_div(rows * (wide ? cols / V : cols), 256), (int64_t)sm_count * 16));
+    auto run = [&](auto kernel) {
+        return launch_pdl(kernel, grid, dim3(256), 0, s, static_cast<const T*>(dH), static_cast<const T*>(G),
+                          static_cast<const T*>(U), static_cast<T*>(dG), static_cast<T*>(dU), rows, cols, pitch, act);
+    };
+    return wide ? run(slope_kernel<T, V>) : run(slope_kernel<T, 1>);
+}
+
+}  // namespace gated
+}  // namespace olc
+
+using namespace olc;
+
+struct olc_gated_plan {
+    PlanState state;
+    olc_dtype dtype;
+    int64_t M, D, F;
+    int act, trans_w;
+    // FLOAT: X W, dg W' (alone, and added to what is there), and X' dg or dg' X
+    olc_matmul_plan *forward, *dx, *dx_more, *dw;
+};
+
+namespace {
+
+// the FLOAT products, made when first needed
+olc_status float_forward(olc_gated_plan* p) {
+    if (p->forward) return OLC_OK;
+    const int64_t x[2] = {p->M, p->D}, w[2] = {p->trans_w ? p->F : p->D, p->trans_w ? p->D : p->F};
+    return olc_gemm_plan_create(x, w, 0, p->trans_w, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->forward);
+}
+olc_status float_backward(olc_gated_plan* p) {
+    const int64_t x[2] = {p->M, p->D}, h[2] = {p->M, p->F};
+    const int64_t w[2] = {p->trans_w ? p->F : p->D, p->trans_w ? p->D : p->F};
+    olc_status st = OLC_OK;
+    if (!p->dx) st = olc_gemm_plan_create(h, w, 0, !p->trans_w, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->dx);
+    if (st == OLC_OK && !p->dx_more) {
+        st = olc_gemm_plan_create(h, w, 0, !p->trans_w, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->dx_more);
+        if (st == OLC_OK) st = olc_matmul_plan_set_epilogue(p->dx_more, OLC_ACT_NONE, 1);
+        if (st != OLC_OK) {
+            olc_matmul_plan_destroy(p->dx_more);
+            p->dx_more = nullptr;
+        }
+    }
+    if (st == OLC_OK && !p->dw)
+        st = p->trans_w ? olc_gemm_plan_create(h, x, 1, 0, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->dw)
+                        : olc_gemm_plan_create(x, h, 1, 0, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->dw);
+    return st;
+}
+
+// One call's use of the plan's memory: pieces are taken in order, first to
+// size it, then to hand out addresses.
+struct Pieces {
+    size_t used = 0;
+    unsigned char* base = nullptr;
+    void* take(size_t bytes) {
+        void* at = base ? base + used : nullptr;
+        used += gated::round256(bytes);
+        return at;
+    }
+};
+
+// An operand as the TMA reads it: in place, or a copy with rows padded to 16
+// bytes in the plan's memory (copied when `s` is given).
+struct Operand {
+    const void* src;
+    int64_t rows, cols;
+    bool copy;
+    void* dst;
+    Operand(const void* p, int64_t r, int64_t c) : src(p), rows(r), cols(c), copy(!plan_aligned16(p) || c % 8 != 0), dst(nullptr) {}
+    void place(Pieces& m) {
+        if (copy) dst = m.take((size_t)(rows * gated::pad8(cols)) * 2);
+    }
+    gated::Stored stored() const {
+        return copy ? gated::Stored{dst, rows, cols, gated::pad8(cols)} : gated::Stored{src, rows, cols, cols};
+    }
+    cudaError_t fill(cudaStream_t s) const {
+        return copy ? launch_pad_rows16(src, dst, rows, cols, gated::pad8(cols), s) : cudaSuccess;
+    }
+};
+
+olc_status forward16(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
+                     cudaStream_t s) {
+    const int64_t wr = p->trans_w ? p->F : p->D, wc = p->trans_w ? p->D : p->F;
+    Operand x(X, p->M, p->D), wg(Wg, wr, wc), wu(Wu, wr, wc);
+    const size_t partial = gated::product_partial_bytes(gated::FWD, p->M, p->F, p->D, p->state.sm_count);
+    float* part = nullptr;
+    for (int pass = 0; pass < 2; ++pass) {
+        Pieces m;
+        m.base = pass ? static_cast<unsigned char*>(p->state.memory) : nullptr;
+        x.place(m);
+        wg.place(m);
+        wu.place(m);
+        part = static_cast<float*>(m.take(partial));
+        if (pass == 0) {
+            if (m.used == 0) break;
+            const olc_status st = p->state.ensure(m.used);
+            if (st != OLC_OK) return st;
+        }
+    }
+    const bool uses = x.copy || wg.copy || wu.copy || partial;
+    cudaError_t e = uses ? p->state.before_use(s) : cudaSuccess;
+    for (const Operand* o : {&x, &wg, &wu})
+        if (e == cudaSuccess) e = o->fill(s);
+    gated::Product w;
+    std::memset(&w, 0, sizeof w);
+    w.M = p->M;
+    w.N = p->F;
+    w.K = p->D;
+    w.a[0] = w.a[1] = x.stored();
+    w.b[0] = wg.stored();
+    w.b[1] = wu.stored();
+    w.b_k = p->trans_w;
+    w.Y[0] = H;
+    w.Y[1] = G;
+    w.Y[2] = U;
+    w.act = p->act;
+    if (e == cudaSuccess) e = gated::launch_product<gated::FWD>(p->dtype, w, part, p->state.sm_count, s);
+    if (e == cudaSuccess && uses) e = p->state.after_use(s);
+    return plan_status(e);
+}
+
+olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const void* Wg, const void* Wu, const void* G,
+                      const void* U, void* dX, void* dWg, void* dWu, cudaStream_t s) {
+    const int64_t wr = p->trans_w ? p->F : p->D, wc = p->trans_w ? p->D : p->F;
+    const int64_t pitch = gated::pad8(p->F);
+    const int sms = p->state.sm_count;
+    Operand x(X, p->M, p->D), wg(Wg, wr, wc), wu(Wu, wr, wc);
+    const int64_t wm = p->trans_w ? p->F : p->D, wn = p->trans_w ? p->D : p->F;
+    size_t partial = dX ? gated::product_partial_bytes(gated::DX, p->M, p->D, p->F, sms) : 0;
+    const size_t pw = dWg ? gated::product_partial_bytes(gated::DW, wm, wn, p->M, sms) : 0;
+    if (pw > partial) partial = pw;
+    void *dg = nullptr, *du = nullptr;
+    float* part = nullptr;
+    for (int pass = 0; pass < 2; ++pass) {
+        Pieces m;
+        m.base = pass ? static_cast<unsigned char*>(p->state.memory) : nullptr;
+        dg = m.take((size_t)(p->M * pitch) * 2);
+        du = m.take((size_t)(p->M * pitch) * 2);
+        if (dWg) x.place(m);
+        if (dX) {
+            wg.place(m);
+            wu.place(m);
+        }
+        part = static_cast<float*>(m.take(partial));
+        if (pass == 0) {
+            const olc_status st = p->state.ensure(m.used);
+            if (st != OLC_OK) return st;
+        }
+    }
+    cudaError_t e = p->state.before_use(s);
+    if (e == cudaSuccess)
+        e = p->dtype == OLC_BFLOAT16
+                ? gated::launch_slope<__nv_bfloat16>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s)
+                : gated::launch_slope<__half>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s);
+    const gated::Stored sg{dg, p->M, p->F, pitch}, su{du, p->M, p->F, pitch};
+    gated::Product w;
+    if (dX) {
+        if (e == cudaSuccess) e = wg.fill(s);
+        if (e == cudaSuccess) e = wu.fill(s);
+        std::memset(&w, 0, sizeof w);
+        w.M = p->M;
+        w.N = p->D;
+        w.K = p->F;
+        w.a[0] = sg;
+        w.a[1] = su;
+        w.b[0] = wg.stored();
+        w.b[1] = wu.stored();
+        w.b_k = !p->trans_w;
+        w.Y[0] = dX;
+        if (e == cudaSuccess) e = gated::launch_product<gated::DX>(p->dtype, w, part, sms, s);
+    }
+    if (dWg) {
+        if (e == cudaSuccess) e = x.fill(s);
+        std::memset(&w, 0, sizeof w);
+        w.M = wm;
+        w.N = wn;
+        w.K = p->M;
+        const gated::Stored sx = x.stored();
+        w.a[0] = p->trans_w ? sg : sx;
+        w.a[1] = p->trans_w ? su : sx;
+        w.b[0] = p->trans_w ? sx : sg;
+        w.b[1] = p->trans_w ? sx : su;
+        w.a_mn = true;
+        w.Y[0] = dWg;
+        w.Y[1] = dWu;
+        if (e == cudaSuccess) e = gated::launch_product<gated::DW>(p->dtype, w, part, sms, s);
+    }
+    if (e == cudaSuccess) e = p->state.after_use(s);
+    return plan_status(e);
+}
+
+olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
+                     cudaStream_t s) {
+    olc_status st = float_forward(p);
+    const int64_t n = p->M * p->F;
+    // what is not kept: g in the plan's memory, u in H
+    if (st == OLC_OK && !G) st = p->state.ensure((size_t)n * sizeof(float));
+    if (st != OLC_OK) return st;
+    if (!G) {
+        const cudaError_t e = p->state.before_use(s);
+        if (e != cudaSuccess) return plan_status(e);
+    }
+    void* g = G ? G : p->state.memory;
+    void* u = U ? U : H;
+    st = olc_gemm_execute(p->forward, X, Wg, nullptr, g, s);
+    if (st == OLC_OK) st = olc_gemm_execute(p->forward, X, Wu, nullptr, u, s);
+    if (st != OLC_OK) return st;
+    cudaError_t e = launch_pdl(gated::product_kernel, dim3((unsigned)min64(ceil_div(n, 256), (int64_t)p->state.sm_count * 16)),
+                               dim3(256), 0, s, static_cast<const float*>(g), static_cast<const float*>(u),
+                               static_cast<float*>(H), n, p->act);
+    if (e == cudaSuccess && !G) e = p->state.after_use(s);
+    return plan_status(e);
+}
+
+olc_status backward32(olc_gated_plan* p, const void* dH, const void* X, const void* Wg, const void* Wu, const void* G,
+                      const void* U, void* dX, void* dWg, void* dWu, cudaStream_t s) {
+    olc_status st = float_backward(p);
+    const size_t half = gated::round256((size_t)(p->M * p->F) * sizeof(float));
+    if (st == OLC_OK) st = p->state.ensure(2 * half);
+    if (st != OLC_OK) return st;
+    void *dg = p->state.memory, *du = static_cast<unsigned char*>(p->state.memory) + half;
+    cudaError_t e = p->state.before_use(s);
+    if (e == cudaSuccess)
+        e = gated::launch_slope<float>(dH, G, U, dg, du, p->M, p->F, p->F, p->act, p->state.sm_count, s);
+    if (e != cudaSuccess) return plan_status(e);
+    if (dX) {
+        st = olc_gemm_execute(p->dx, dg, Wg, nullptr, dX, s);
+        // the second term on top of the first: the residual is dX itself
+        if (st == OLC_OK) st = olc_matmul_execute_fused(p->dx_more, du, Wu, nullptr, dX, dX, s);
+    }
+    if (st == OLC_OK && dWg) {
+        st = olc_gemm_execute(p->dw, p->trans_w ? dg : X, p->trans_w ? X : dg, nullptr, dWg, s);
+        if (st == OLC_OK) st = olc_gemm_execute(p->dw, p->trans_w ? du : X, p->trans_w ? X : du, nullptr, dWu, s);
+    }
+    if (st != OLC_OK) return st;
+    return plan_status(p->state.after_use(s));
+}
+
+}  // namespace
+
+extern "C" {
+
+olc_status olc_gated_plan_create(int64_t rows, int64_t d_in, int64_t d_hidden, int activation, int trans_w,
+                                 olc_dtype dtype, olc_gated_plan** out) {
+    if (!out) return OLC_ERR_NULL;
+    *out = nullptr;
+    if (!plan_dtype_ok(dtype)) return OLC_ERR_DTYPE;
+    if (rows < 0 || d_in < 0 || d_hidden < 0) return OLC_ERR_NEGATIVE_DIM;
+    const int64_t most = (int64_t(1) << 31) - 65536;       // 32-bit tile coordinates
+    if (rows >= most || d_in >= most || d_hidden >= most) return OLC_ERR_INVALID;
+    if (activation < OLC_GATE_SILU || activation > OLC_GATE_SIGMOID) return OLC_ERR_INVALID;
+    if (!plan_fits(rows, d_in, 4) || !plan_fits(rows, d_hidden, 4) || !plan_fits(d_in, d_hidden, 4))
+        return OLC_ERR_INVALID;
+    olc_gated_plan* p = new (std::nothrow) olc_gated_plan;
+    if (!p) return OLC_ERR_OOM;
+    std::memset(static_cast<void*>(p), 0, sizeof *p);
+    p->state.init();
+    p->dtype = dtype;
+    p->M = rows;
+    p->D = d_in;
+    p->F = d_hidden;
+    p->act = activation;
+    p->trans_w = trans_w ? 1 : 0;
+    *out = p;
+    return OLC_OK;
+}
+
+void olc_gated_plan_destroy(olc_gated_plan* plan) {
+    if (!plan) return;
+    olc_matmul_plan_destroy(plan->forward);
+    olc_matmul_plan_destroy(plan->dx);
+    olc_matmul_plan_destroy(plan->dx_more);
+    olc_matmul_plan_destroy(plan->dw);
+    plan->state.destroy();
+    delete plan;
+}
+
+olc_status olc_gated_forward(olc_gated_plan* plan, const void* X, const void* Wg, const void* Wu, void* H, void* G,
+                             void* U, void* stream) {
+    if (!plan) return OLC_ERR_NULL;
+    olc_gated_plan* p = plan;
+    if (p->M == 0 || p->F == 0) return OLC_OK;
+    if (!H || (p->D > 0 && (!X || !Wg || !Wu))) return OLC_ERR_NULL;
+    const int64_t eb = plan_elem_bytes(p->dtype);
+    for (const void* q : {X, Wg, Wu, (const void*)H, (const void*)G, (const void*)U})
+        if (plan_misaligned(q, eb)) return OLC_ERR_INVALID;
+    const olc_status st = p->state.bind();
+    if (st != OLC_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p->D == 0) {                                       // empty sums: act(0) 0
+        cudaError_t e = cudaSuccess;
+        for (void* y : {H, G, U})
+            if (y && e == cudaSuccess) e = launch_zero_fill(y, p->M * p->F * eb, s);
+        return plan_status(e);
+    }
+    return p->dtype == OLC_FLOAT ? forward32(p, X, Wg, Wu, H, G, U, s) : forward16(p, X, Wg, Wu, H, G, U, s);
+}
+
+olc_status olc_gated_backward(olc_gated_plan* plan, const void* dH, const void* X, const void* Wg, const void* Wu,
+                              const void* G, const void* U, void* dX, void* dWg, void* dWu, void* stream) {
+    if (!plan) return OLC_ERR_NULL;
+    olc_gated_plan* p = plan;
+    if ((dWg == nullptr) != (dWu == nullptr)) return OLC_ERR_NULL;
+    if (p->M == 0 || p->D == 0) dX = nullptr;              // empty
+    if (p->D == 0 || p->F == 0) dWg = dWu = nullptr;
+    if (!dX && !dWg) return OLC_OK;
+    const int64_t eb = plan_elem_bytes(p->dtype);
+    const bool some = p->M > 0 && p->F > 0;                // terms to sum
+    if (some && (!dH || !G || !U || (dX && (!Wg || !Wu)) || (dWg && !X))) return OLC_ERR_NULL;
+    for (const void* q : {dH, X, Wg, Wu, G, U, (const void*)dX, (const void*)dWg, (const void*)dWu})
+        if (plan_misaligned(q, eb)) return OLC_ERR_INVALID;
+    const olc_status st = p->state.bind();
+    if (st != OLC_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!some) {
+        cudaError_t e = dX ? launch_zero_fill(dX, p->M * p->D * eb, s) : cudaSuccess;
+        if (dWg && e == cudaSuccess) e = launch_zero_fill(dWg, p->D * p->F * eb, s);
+        if (dWg && e == cudaSuccess) e = launch_zero_fill(dWu, p->D * p->F * eb, s);
+        return plan_status(e);
+    }
+    return p->dtype == OLC_FLOAT ? backward32(p, dH, X, Wg, Wu, G, U, dX, dWg, dWu, s)
+                                 : backward16(p, dH, X, Wg, Wu, G, U, dX, dWg, dWu, s);
+}
+
+}  // extern "C"

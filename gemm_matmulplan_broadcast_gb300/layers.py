@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import DTYPE_CODES, _check, _stream_handle, load
+from .binding import DTYPE_CODES, GATES, _check, _stream_handle, load
 
 ROW_DTYPES = ("float32", "float16", "bfloat16")
 
@@ -59,6 +59,16 @@ def _flat(name, t, n, dtype):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor" % name)
     return t.data_ptr()
+
+
+def _dense(name, t, rows, cols, dtype):
+    """Pointer of a contiguous [rows, cols] tensor (None stays None)."""
+    if t is None:
+        return None
+    ptr, pitch = _rows(name, t, rows, cols, dtype)
+    if rows > 1 and pitch != cols:
+        raise ValueError("%s must be contiguous" % name)
+    return ptr
 
 
 class _PlanHandle:
@@ -130,6 +140,47 @@ class LayerNormPlan(_PlanHandle):
         return dX, dgamma, dbeta
 
 
+class GatedPlan(_PlanHandle):
+    """The gated feed-forward product H = act(X Wg) * (X Wu) of X [rows,
+    d_in] with Wg and Wu [d_in, d_hidden] (stored [d_hidden, d_in] with
+    trans_w), and its gradients.  act: silu, gelu, relu or sigmoid."""
+
+    _destroy = "olc_gated_plan_destroy"
+
+    def __init__(self, rows: int, d_in: int, d_hidden: int, dtype: str, act: str = "silu", trans_w: bool = False):
+        if act not in GATES:
+            raise ValueError("act must be one of %s" % sorted(GATES))
+        self.rows, self.d_in, self.d_hidden = int(rows), int(d_in), int(d_hidden)
+        self.dtype, self.act, self.trans_w = dtype, act, bool(trans_w)
+        self._t = _torch_dtype(dtype)
+        self._w = (self.d_hidden, self.d_in) if self.trans_w else (self.d_in, self.d_hidden)
+        self._create("olc_gated_plan_create", self.rows, self.d_in, self.d_hidden, GATES[act], int(self.trans_w),
+                     DTYPE_CODES[dtype])
+
+    def forward(self, X, Wg, Wu, H, G=None, U=None, stream=None):
+        """H = act(X Wg) * (X Wu); G, U: the two products for the backward
+        call, or None."""
+        m, f, t, w = self.rows, self.d_hidden, self._t, self._w
+        st = self.lib.olc_gated_forward(
+            self._h, _dense("X", X, m, self.d_in, t), _dense("Wg", Wg, w[0], w[1], t),
+            _dense("Wu", Wu, w[0], w[1], t), _dense("H", H, m, f, t), _dense("G", G, m, f, t),
+            _dense("U", U, m, f, t), _stream_handle(stream))
+        _check(st, "olc_gated_forward")
+        return H
+
+    def backward(self, dH, X, Wg, Wu, G, U, dX=None, dWg=None, dWu=None, stream=None):
+        """The gradients of X (or None) and of both weights (or both None)
+        from dH and the forward call's G and U."""
+        m, d, f, t, w = self.rows, self.d_in, self.d_hidden, self._t, self._w
+        st = self.lib.olc_gated_backward(
+            self._h, _dense("dH", dH, m, f, t), _dense("X", X, m, d, t), _dense("Wg", Wg, w[0], w[1], t),
+            _dense("Wu", Wu, w[0], w[1], t), _dense("G", G, m, f, t), _dense("U", U, m, f, t),
+            _dense("dX", dX, m, d, t), _dense("dWg", dWg, w[0], w[1], t), _dense("dWu", dWu, w[0], w[1], t),
+            _stream_handle(stream))
+        _check(st, "olc_gated_backward")
+        return dX, dWg, dWu
+
+
 class TokenLogProbsPlan(_PlanHandle):
     """Log probabilities of given tokens from logits [rows, vocab], with the
     entropy and the ``top`` most likely tokens of each row, and the gradient
@@ -182,6 +233,16 @@ def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out=None, stream=Non
     rows = X.numel() // cols if cols else 0
     with LayerNormPlan(rows, cols, str(X.dtype).replace("torch.", ""), eps) as plan:
         return plan.forward(X, gamma, beta, out, stream=stream)
+
+
+def gated(X, Wg, Wu, act: str = "silu", trans_w: bool = False, out=None, stream=None):
+    """act(X Wg) * (X Wu) of CUDA tensors through a fresh plan."""
+    import torch
+    d, f = reversed(Wg.shape) if trans_w else Wg.shape
+    if out is None:
+        out = torch.empty(X.shape[:-1] + (f,), dtype=X.dtype, device=X.device)
+    with GatedPlan(X.numel() // d if d else X.shape[0], d, f, str(X.dtype).replace("torch.", ""), act, trans_w) as plan:
+        return plan.forward(X, Wg, Wu, out, stream=stream)
 
 
 def token_log_probs(logits, tokens, top: int = 0, stream=None):

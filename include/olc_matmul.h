@@ -444,6 +444,62 @@ olc_status olc_layer_norm_backward(olc_layer_norm_plan* plan, const void* dY, in
                                    int64_t x_pitch, const void* gamma, const float* mean, const float* rstd, void* dX,
                                    int64_t dx_pitch, void* dgamma, void* dbeta, void* stream);
 
+/* ---- gated feed-forward product -------------------------------------------- */
+
+/* Activation of the gate: g sigmoid(g), g Phi(g) (the exact form, with the
+ * normal distribution function), max(g, 0) (NaN stays NaN), sigmoid(g). */
+typedef enum {
+    OLC_GATE_SILU = 0,
+    OLC_GATE_GELU = 1,
+    OLC_GATE_RELU = 2,
+    OLC_GATE_SIGMOID = 3
+} olc_gate;
+
+typedef struct olc_gated_plan olc_gated_plan;
+
+/*
+ * H = act(X Wg) * (X Wu), elementwise product, for X [rows, d_in]; Wg and Wu
+ * are stored [d_in, d_hidden], or [d_hidden, d_in] with trans_w != 0.  All
+ * tensors are dense and of one type.  FLOAT16 / BFLOAT16 run on the tensor
+ * cores: both products are accumulated in float32, and activation and product
+ * formed from the accumulators, in one kernel.  Operands whose rows are not
+ * multiples of 16 bytes, or that do not start on a 16-byte boundary, are first
+ * copied into the plan's memory.  FLOAT runs on the FMA pipes.
+ * Extents of 0 are allowed (d_in = 0: g = u = 0).  Errors: OLC_ERR_NULL,
+ * OLC_ERR_DTYPE, OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID (an extent of 2^31 -
+ * 65536 or more, an unknown activation, more than 2^62 bytes), OLC_ERR_OOM.
+ */
+olc_status olc_gated_plan_create(int64_t rows, int64_t d_in, int64_t d_hidden, int activation, int trans_w,
+                                 olc_dtype dtype, olc_gated_plan** out);
+
+/* NULL is accepted. */
+void olc_gated_plan_destroy(olc_gated_plan* plan);
+
+/*
+ * Forward.  G, U [rows, d_hidden]: the two products, rounded to the plan's
+ * type, for the backward call; NULL for what is not kept (H is formed from
+ * the unrounded products either way).  No output may overlap another tensor.
+ * Operand copies, K slices and FLOAT's intermediate products live in device
+ * memory that the plan allocates at the first call that needs it: make that
+ * call before any stream capture.  Errors: OLC_ERR_NULL, OLC_ERR_INVALID,
+ * OLC_ERR_WRONG_DEVICE, OLC_ERR_OOM, OLC_ERR_CUDA.
+ */
+olc_status olc_gated_forward(olc_gated_plan* plan, const void* X, const void* Wg, const void* Wu, void* H, void* G,
+                             void* U, void* stream);
+
+/*
+ * Backward, from dH [rows, d_hidden] and the forward call's G and U:
+ *     dg = dH u act'(g),  du = dH act(g)     (act' of RELU at 0 is 0)
+ *     dX = dg Wg' + du Wu',  dWg = X' dg,  dWu = X' du  (stored as the weights).
+ * dX NULL skips it; dWg and dWu are both given or both NULL.  dg and du are
+ * kept in the plan's memory (2 x rows x d_hidden elements) and, for FLOAT16 /
+ * BFLOAT16, rounded to the type, which the tensor cores read; all sums are
+ * float32, in an order that depends on the sizes and the device alone.
+ * Errors: as forward.
+ */
+olc_status olc_gated_backward(olc_gated_plan* plan, const void* dH, const void* X, const void* Wg, const void* Wu,
+                              const void* G, const void* U, void* dX, void* dWg, void* dWu, void* stream);
+
 /* ---- log probabilities of given tokens ----------------------------------- */
 
 /* Most alternatives a plan reports for a row. */

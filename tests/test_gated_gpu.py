@@ -1,0 +1,278 @@
+"""The gated feed-forward product on the GPU, forward and backward, against
+the formulas in 64 bits.
+
+Tolerances.  A product's float32 accumulator takes K terms, sixteen at a time
+on the tensor cores, and every step rounds (or cuts) to 2^-23 of what has
+been summed in absolute values, S = |X| |W|: off by at most
+STEPS 2^-23 S with STEPS = K / 16 + 32 (K + 32 for FLOAT, whose steps are
+single terms rounded to 2^-24 in chains of at most K).  With dg = STEPS 2^-23 S:
+  h = act(g) u is off by |u| L dg + |act(g)| du, L <= 1.13 the largest slope of
+  the activations, plus 2^-19 |h| for the activation itself (FLOAT: 2^-21) and
+  the rounding to the type.  GELU's distribution function is good to 2e-7
+  absolutely.
+  The gradients' operands dg and du are rounded to the type first, so each
+  term of their sums is off by 2 roundings of itself and the activation's 2^-18
+  (FLOAT: 2^-20)."""
+
+import pytest
+import torch
+
+from gemm_matmulplan_broadcast_gb300 import GatedPlan, OlcError, gated
+from layers_ref import CANARY, DTYPES, F32, ROUND, TINY, TORCH, Guarded, assert_near, normal
+
+pytestmark = pytest.mark.gpu
+
+ACTS = ["silu", "gelu", "relu", "sigmoid"]
+F64 = torch.float64
+
+
+def act_of(name, g):
+    if name == "silu":
+        return g * torch.sigmoid(g)
+    if name == "gelu":
+        return 0.5 * g * torch.special.erfc(-g * 0.5 ** 0.5)
+    return torch.relu(g) if name == "relu" else torch.sigmoid(g)
+
+
+def steps(k, dtype):
+    return (k + 32) * F32 if dtype == "float32" else (k / 16 + 32) * 2 * F32
+
+
+def storage(rows, cols, dtype, offset, values=None):
+    return Guarded(rows, cols, dtype, None, offset, values)
+
+
+def inputs(m, d, f, dtype, trans_w, seed=1):
+    shape = (f, d) if trans_w else (d, f)
+    scale = max(d, 1) ** -0.5
+    return normal((m, d), dtype, seed), normal(shape, dtype, seed + 1, scale), normal(shape, dtype, seed + 2, scale)
+
+
+def check_forward(m, d, f, dtype, act="silu", trans_w=False, keep=True, offset=0):
+    x, wg, wu = inputs(m, d, f, dtype, trans_w)
+    gx, gg, gu = (storage(*t.shape, dtype, offset, t) for t in (x, wg, wu))
+    outs = [storage(m, f, dtype, offset) for _ in range(3 if keep else 1)]
+    with GatedPlan(m, d, f, dtype, act, trans_w) as plan:
+        for _ in range(2):
+            plan.forward(gx.t, gg.t, gu.t, *(o.t for o in outs))
+        torch.cuda.synchronize()
+    for o in [gx, gg, gu] + outs:
+        o.check_guards()
+    x, wg, wu = x.to(F64), wg.to(F64), wu.to(F64)
+    if trans_w:
+        wg, wu = wg.t(), wu.t()
+    g, u = x @ wg, x @ wu
+    e = steps(d, dtype)
+    dg, du = e * (x.abs() @ wg.abs()), e * (x.abs() @ wu.abs())
+    a = act_of(act, g)
+    h = a * u
+    r = ROUND[dtype]
+    fine = 2.0 ** (-21 if dtype == "float32" else -19)
+    off = u.abs() * (1.13 * dg + (2e-7 * g.abs() if act == "gelu" else 0)) + a.abs() * du + 2 * dg * du + fine * h.abs()
+    assert_near(outs[0].t, h, r * h.abs() + (1 + r) * off + TINY[dtype], "h")
+    if keep:
+        assert_near(outs[1].t, g, r * g.abs() + (1 + r) * dg + TINY[dtype], "g")
+        assert_near(outs[2].t, u, r * u.abs() + (1 + r) * du + TINY[dtype], "u")
+
+
+def check_backward(m, d, f, dtype, act="silu", trans_w=False, offset=0, parts=(True, True)):
+    x, wg, wu = inputs(m, d, f, dtype, trans_w, 11)
+    g, u, dh = normal((m, f), dtype, 14), normal((m, f), dtype, 15), normal((m, f), dtype, 16, 0.5)
+    given = [storage(*t.shape, dtype, offset, t) for t in (dh, x, wg, wu, g, u)]
+    dx = storage(m, d, dtype, offset) if parts[0] else None
+    dw = [storage(*wg.shape, dtype, offset) for _ in range(2)] if parts[1] else [None, None]
+    t = lambda o: None if o is None else o.t  # noqa: E731
+    with GatedPlan(m, d, f, dtype, act, trans_w) as plan:
+        for _ in range(2):
+            plan.backward(*(o.t for o in given), dX=t(dx), dWg=t(dw[0]), dWu=t(dw[1]))
+        torch.cuda.synchronize()
+    for o in given + [dx] + dw:
+        if o is not None:
+            o.check_guards()
+    x, wg, wu, g, u, dh = (v.to(F64) for v in (x, wg, wu, g, u, dh))
+    if trans_w:
+        wg, wu = wg.t(), wu.t()
+    g.requires_grad_()
+    value = act_of(act, g)
+    slope, = torch.autograd.grad(value.sum(), g)
+    value, g = value.detach(), g.detach()
+    dg, du = dh * u * slope, dh * value
+    r = ROUND[dtype]
+    fine = 2.0 ** (-20 if dtype == "float32" else -18)
+    # what dg and du are off by: their rounding, the activation's error (absolutely, slopes being at most 1.13)
+    eg = 2 * r * dg.abs() + fine * (dh * u).abs() + TINY[dtype]
+    eu = 2 * r * du.abs() + fine * dh.abs() * (1 + g.abs()) + TINY[dtype]
+
+    def near(got, terms, what):
+        want = sum(a @ b for a, b, _, _ in terms)
+        k = sum(a.shape[1] for a, _, _, _ in terms)
+        off = sum(ea @ b.abs() + a.abs() @ eb + steps(k, dtype) * (a.abs() @ b.abs()) for a, b, ea, eb in terms)
+        assert_near(got, want, r * want.abs() + (1 + r) * off + TINY[dtype], what)
+
+    no = lambda v: torch.zeros_like(v)  # noqa: E731
+    if parts[0]:
+        near(dx.t, [(dg, wg.t(), eg, no(wg.t())), (du, wu.t(), eu, no(wu.t()))], "dX")
+    if parts[1]:
+        for o, v, e, name in ((dw[0], dg, eg, "dWg"), (dw[1], du, eu, "dWu")):
+            got = o.t.t() if trans_w else o.t
+            near(got, [(x.t(), v, no(x.t()), e)], name)
+
+
+SIZES = [
+    (1, 1, 1), (1, 64, 128), (1, 1000, 520), (3, 7, 9), (5, 72, 72), (8, 4096, 64), (16, 512, 1000), (17, 100, 130),
+    (33, 264, 2056), (64, 1000, 333), (65, 128, 640), (128, 2048, 256), (255, 65, 64), (257, 130, 129), (300, 200, 1032),
+    (700, 64, 72), (1030, 520, 392),
+]
+
+
+@pytest.mark.parametrize("trans_w", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,d,f", SIZES)
+def test_forward(m, d, f, dtype, trans_w):
+    check_forward(m, d, f, dtype, ACTS[(m + d) % 4], trans_w)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m", [2, 40, 300])
+def test_forward_activations_without_keeping(m, act, dtype):
+    check_forward(m, 136, 264, dtype, act, keep=False)
+
+
+@pytest.mark.parametrize("trans_w", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,d,f,offset", [(1, 512, 256, 1), (20, 200, 320, 3), (300, 128, 264, 1), (90, 64, 72, 8)])
+def test_unaligned_tensors(m, d, f, offset, dtype, trans_w):
+    check_forward(m, d, f, dtype, "silu", trans_w, offset=offset)
+    check_backward(m, d, f, dtype, "silu", trans_w, offset=offset)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_forward_over_many_tiles(dtype):
+    check_forward(2000, 320, 5000, dtype, "silu", keep=True)
+    check_forward(1111, 256, 4096, dtype, "gelu", True, keep=False)
+
+
+@pytest.mark.parametrize("trans_w", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,d,f", SIZES)
+def test_backward(m, d, f, dtype, trans_w):
+    check_backward(m, d, f, dtype, ACTS[(m + d + 1) % 4], trans_w)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", ACTS)
+def test_backward_activations_and_parts(act, dtype):
+    check_backward(150, 136, 264, dtype, act)
+    check_backward(150, 136, 264, dtype, act, parts=(True, False))
+    check_backward(150, 136, 264, dtype, act, True, parts=(False, True))
+
+
+def test_backward_over_many_tiles():
+    check_backward(1500, 1288, 2600, "bfloat16", "silu")
+    check_backward(1500, 1288, 2600, "float16", "gelu", True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_empty_extents(dtype):
+    t = TORCH[dtype]
+    new = lambda *s: torch.full(s, CANARY, dtype=t, device="cuda")  # noqa: E731
+    for m, d, f in ((0, 8, 16), (5, 0, 16), (5, 8, 0), (0, 0, 0)):
+        for trans_w in (False, True):
+            w = (f, d) if trans_w else (d, f)
+            with GatedPlan(m, d, f, dtype, "sigmoid", trans_w) as plan:
+                h, g, u = new(m, f), new(m, f), new(m, f)
+                plan.forward(new(m, d), new(*w), new(*w), h, g, u)
+                dx, a, b = new(m, d), new(*w), new(*w)
+                plan.backward(h, new(m, d), new(*w), new(*w), g, u, dx, a, b)
+                torch.cuda.synchronize()
+                for o in (h, g, u, dx, a, b):
+                    assert not o.any()
+
+
+def test_activation_far_from_zero():
+    # saturated gates, and the tail where the distribution function is small; NaN and infinities stay in their outputs
+    for act in ACTS:
+        for dtype in DTYPES:
+            v = torch.tensor([-60000.0, -100.0, -20.0, -5.0, -1e-3, -0.0, 0.0, 1e-3, 5.0, 20.0, 100.0, 60000.0])
+            x = torch.eye(12).to(TORCH[dtype])
+            wg, wu = torch.diag(v).to(TORCH[dtype]), torch.eye(12).to(TORCH[dtype])
+            h = gated(x.cuda(), wg.cuda(), wu.cuda(), act).cpu()
+            g = wg.to(F64)
+            want = act_of(act, g) * wu.to(F64)
+            assert_near(h, want, ROUND[dtype] * want.abs() + 2.0 ** -19 * want.abs() + 3e-7 * (g.abs() + 1) * wu.to(F64) * (act == "gelu")
+                        + 1e-20 + TINY[dtype], act)
+            x[3, 5] = float("nan")
+            h = gated(x.cuda(), wg.cuda(), wu.cuda(), act).cpu()
+            assert torch.isnan(h[3]).all() and not torch.isnan(h[[0, 1, 2, 4]]).any()
+
+
+def test_gradient_matches_central_differences():
+    # L = sum w h in float64 from FLOAT outputs.  h = 2^-6 along a unit-variance direction: the central difference
+    # misses h^2 / 6 of the third derivative, a few |w| for these scales, and outputs' roundings over 2 h
+    m, d, f, step = 6, 24, 40, 2.0 ** -6
+    for act in ("silu", "gelu", "sigmoid"):
+        for trans_w in (False, True):
+            x, wg, wu = (t.cuda() for t in inputs(m, d, f, "float32", trans_w, 51))
+            w = normal((m, f), "float32", 54).cuda()
+            with GatedPlan(m, d, f, "float32", act, trans_w) as plan:
+                h, g, u = (torch.empty(m, f, device="cuda") for _ in range(3))
+
+                def loss(*args):
+                    return float((plan.forward(*args, h).double() * w.double()).sum())
+
+                plan.forward(x, wg, wu, h, g, u)
+                grads = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+                plan.backward(w, x, wg, wu, g, u, *grads)
+                for i in range(3):
+                    args = [x, wg, wu]
+                    v = normal(tuple(args[i].shape), "float32", 60 + i, float(args[i].std())).cuda()
+                    up, down = list(args), list(args)
+                    up[i], down[i] = args[i] + step * v, args[i] - step * v
+                    want = float((grads[i].double() * v.double()).sum())
+                    scale = float(w.double().norm()) * float((u.double().abs() + g.double().abs() + 1).norm())
+                    assert abs((loss(*up) - loss(*down)) / (2 * step) - want) <= 1e-3 * scale, (act, trans_w, i)
+
+
+def test_repeats_bit_for_bit_on_several_streams():
+    # 24 tiles of K = 4096: sliced along K, with partial results in the plan's memory
+    m, d, f = 200, 4096, 512
+    x, wg, wu = (t.cuda() for t in inputs(m, d, f, "bfloat16", False, 71))
+    g, u, dh = (normal((m, f), "bfloat16", 74 + i).cuda() for i in range(3))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    with GatedPlan(m, d, f, "bfloat16") as plan:
+        got = []
+        torch.cuda.synchronize()
+        for i in range(9):
+            o = [torch.empty(m, f, dtype=x.dtype, device="cuda"), torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)]
+            torch.cuda.synchronize() if i < 2 else None
+            plan.forward(x, wg if i % 2 else wu, wu, o[0], stream=streams[i % 3])
+            plan.backward(dh if i % 2 else g, x, wg, wu, g, u, *o[1:], stream=streams[i % 3])
+            got.append(o)
+        torch.cuda.synchronize()
+        for i in range(2, 9):
+            assert all(torch.equal(a, b) for a, b in zip(got[i], got[i % 2])), i
+        graph = torch.cuda.CUDAGraph()
+        o = [torch.zeros_like(t) for t in got[1]]
+        with torch.cuda.graph(graph):
+            plan.forward(x, wg, wu, o[0])
+            plan.backward(dh, x, wg, wu, g, u, *o[1:])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(o, got[1]))
+
+
+def test_refusals():
+    x, w, h = torch.zeros(4, 8, device="cuda"), torch.zeros(8, 16, device="cuda"), torch.zeros(4, 16, device="cuda")
+    with GatedPlan(4, 8, 16, "float32") as plan:
+        for bad in (x.half(), x[:, :4], torch.zeros(4, 8), torch.zeros(4, 16, device="cuda")[:, :8]):
+            with pytest.raises((TypeError, ValueError)):
+                plan.forward(bad, w, w, h)
+        with pytest.raises(ValueError):
+            plan.forward(x, w.t(), w, h)
+        with pytest.raises(OlcError) as e:
+            plan.backward(h, x, w, w, h, h, dX=x, dWg=w)
+        assert e.value.name == "OLC_ERR_NULL"
+        lib = plan.lib
+        assert lib.olc_gated_forward(plan._h, x.data_ptr() + 2, w.data_ptr(), w.data_ptr(), h.data_ptr(), None, None, None) == 13
+        assert lib.olc_gated_forward(plan._h, x.data_ptr(), None, w.data_ptr(), h.data_ptr(), None, None, None) == 1
