@@ -4,6 +4,7 @@
 //
 //   m = max_j z_j,  s = sum_j e^(z_j - m),  a = sum_j (z_j - m) e^(z_j - m)
 //   lse = m + log s,  logprob = z_token - lse,  H = log s - a / s
+//   (the sums in units of log 2, which is what the exponential unit takes)
 //   dz_j = dlogprob (1[j = token] - p_j) - dH p_j (log p_j + H)
 //
 // (a <= 0 <= log s, so the entropy's two terms never cancel.)  About six
@@ -22,6 +23,7 @@
 // elements reaches, and only the few threads whose maximum reaches it read
 // their elements again.  Order is by value, then by the lower index.
 #include <new>
+#include <type_traits>
 
 #include "common.cuh"
 #include "plan_state.h"
@@ -29,9 +31,9 @@
 namespace olc {
 namespace score {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kThreads / 4;       // four neighbouring threads share a maximum
+constexpr int kGroups = kThreads / 2;       // two neighbouring threads share a maximum
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBuffer = 1024;               // candidates above the bound, and as many at it
@@ -83,28 +85,126 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Distances below this one weigh nothing (e^-104 is 0 in float32), and their
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Distances below this one weigh nothing (2^-150 is 0 in float32), and their
 // product with a zero weight has to be 0 for masks of -inf and of the type's
 // lowest value alike.
 constexpr float kFar = -1.0e4f;
 
-// A running softmax over some elements of a row.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// A running softmax over some elements of a row, in units of log 2: with
+// R = m log2(e) (rounded; 0 while m is -inf), s = sum 2^(z log2(e) - R) and
+// a = sum (z log2(e) - R) 2^(z log2(e) - R).  The rounding of R cancels:
+// every result takes R, s and a together.  Maxima whose R could overflow are
+// subtracted before the scaling instead.
 struct Sums {
     float m, s, a;
 };
-__device__ __forceinline__ float reference_of(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ bool extreme(float m) { return fabsf(m) >= 1.0e38f && m != -INFINITY; }
+__device__ __forceinline__ float scaled_max(float m) { return m == -INFINITY ? 0.f : m * kLog2e; }
+// z log2(e) - R, not below kFar
+__device__ __forceinline__ float distance(float z, float m) {
+    return max_nan(extreme(m) ? (z - m) * kLog2e : fmaf(z, kLog2e, -scaled_max(m)), kFar);
+}
+
+// the same sums around another maximum (m >= q.m)
+__device__ __forceinline__ void move_to(Sums& q, float m) {
+    if (q.m != -INFINITY) {          // else nothing but zeros, or a NaN to keep
+        const float d = max_nan(extreme(q.m) || extreme(m) ? (q.m - m) * kLog2e : scaled_max(q.m) - scaled_max(m), kFar);
+        const float c = exp2_fast(d);
+        q.a = c * fmaf(d, q.s, q.a);
+        q.s *= c;
+    }
+    q.m = m;
+}
 
 // the sums of both sets of elements, in this order
-__device__ __forceinline__ Sums join(const Sums& x, const Sums& y) {
+__device__ __forceinline__ Sums join(Sums x, Sums y) {
     const float m = fmaxf(x.m, y.m);
-    const float r = reference_of(m);
-    const float dx = x.m - r, dy = y.m - r;         // 0 or negative; -inf where a side is empty
-    const float cx = __expf(dx), cy = __expf(dy);
-    Sums o;
-    o.m = m;
-    o.s = cx * x.s + cy * y.s;
-    o.a = cx * (x.a + max_nan(dx, kFar) * x.s) + cy * (y.a + max_nan(dy, kFar) * y.s);
-    return o;
+    move_to(x, m);
+    move_to(y, m);
+    return Sums{m, x.s + y.s, x.a + y.a};
+}
+
+// Two float32 lanes in one 64-bit register: one issue for both.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Operations on a 16-byte pack of elements as loaded: 16-bit types compare
+// two elements an instruction.
+template <typename T>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {      // NaN loses
+    if constexpr (sizeof(T) == 4) return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    uint32_t r;
+    if constexpr (std::is_same_v<T, __half>) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t floor_word(uint32_t a, uint32_t b) {    // max(a, b), NaN stays
+    if constexpr (sizeof(T) == 4) return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    uint32_t r;
+    if constexpr (std::is_same_v<T, __half>) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// both halves of a word hold `v` (float32: the word is v)
+template <typename T>
+__device__ __forceinline__ uint32_t splat(float v) {
+    if constexpr (sizeof(T) == 4) return __float_as_uint(v);
+    const T e = Num<T>::from_acc(v);
+    const uint32_t b = *reinterpret_cast<const unsigned short*>(&e);
+    return b | (b << 16);
+}
+// the larger of a word's elements
+template <typename T>
+__device__ __forceinline__ float word_max(uint32_t w) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    const unsigned short lo = (unsigned short)w, hi = (unsigned short)(w >> 16);
+    return fmaxf(Num<T>::to_acc(*reinterpret_cast<const T*>(&lo)), Num<T>::to_acc(*reinterpret_cast<const T*>(&hi)));
+}
+// the elements of words 2i, 2i + 1 (float32) or of word i (16-bit): one pair
+template <typename T>
+__device__ __forceinline__ F2 pair_of(const uint32_t (&w)[4], int i) {
+    if constexpr (sizeof(T) == 4) return pack_f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    if constexpr (std::is_same_v<T, __half>) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        return pack_f2(f.x, f.y);
+    } else {
+        return pack_f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+}
+// A row's values that lie kFar below `top` weigh nothing and are raised to
+// that floor, so that no infinity meets a zero; for a `top` in this range the
+// floor is a finite value of the type and nothing overflows.
+template <typename T>
+__device__ __forceinline__ bool has_floor(float top) {
+    return top > (std::is_same_v<T, __half> ? -5.0e4f : -1.0e38f) && top < 1.0e38f;      // not for NaN
+}
+template <typename T>
+__device__ __forceinline__ uint32_t floor_of(float top) {
+    return splat<T>(std::is_same_v<T, __half> ? fmaxf(top + kFar, -65504.f) : top + kFar);
 }
 
 template <typename T>
@@ -141,85 +241,118 @@ __device__ __forceinline__ void unpack(const uint4& k, float (&z)[16 / sizeof(T)
     for (int i = 0; i < (int)(16 / sizeof(T)); ++i) z[i] = Num<T>::to_acc(e[i]);
 }
 
-// every element of the slice that this thread owns: f(value, index)
-template <typename T, typename F>
-__device__ __forceinline__ void own_elements(const Slice<T>& s, F&& f) {
+// the largest of a pack's elements
+template <typename T>
+__device__ __forceinline__ float pack_max(const uint4& k) {
+    return word_max<T>(max_word<T>(max_word<T>(k.x, k.y), max_word<T>(k.z, k.w)));
+}
+
+// every element of the slice that this thread owns: f(value, index); packs
+// whose largest element is below `least` are passed over (ALL: none are)
+template <typename T, bool ALL, typename F>
+__device__ __forceinline__ void own_elements(const Slice<T>& s, float least, F&& f) {
     constexpr int V = Slice<T>::V;
     const int t = threadIdx.x;
     if (t < s.head) f(Num<T>::to_acc(s.row[t]), t);
     const uint4* body = reinterpret_cast<const uint4*>(s.row + s.body);
+#pragma unroll 4
     for (int v = s.v0 + t; v < s.v1; v += kThreads) {
+        const uint4 k = __ldg(body + v);
+        if (!ALL && !(pack_max<T>(k) >= least)) continue;
         float z[V];
-        unpack<T>(__ldg(body + v), z);
+        unpack<T>(k, z);
+#pragma unroll 1
+        for (int i = 0; i < V; ++i) {
+            float x = z[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i) f(z[i], s.body + v * V + i);
+            for (int j = 1; j < V; ++j) x = i == j ? z[j] : x;
+            f(x, s.body + v * V + i);
+        }
     }
     if (s.tail0 + t < s.tail1) f(Num<T>::to_acc(s.row[s.tail0 + t]), s.tail0 + t);
 }
 
-template <int N>
-__device__ __forceinline__ void take(Sums& q, const float (&z)[N]) {
-    float cm = z[0];
+// one element, any values
+__device__ __forceinline__ void take(Sums& q, float z) {
+    if (z > q.m) move_to(q, z);
+    const float d = distance(z, q.m);
+    const float e = exp2_fast(d);
+    q.s += e;
+    q.a = fmaf(d, e, q.a);
+}
+
+// N packs at once: the maximum first, then the sums around it, two elements
+// an instruction
+template <typename T, int N>
+__device__ __forceinline__ void take(Sums& q, const uint4 (&k)[N]) {
+    uint32_t top = max_word<T>(max_word<T>(k[0].x, k[0].y), max_word<T>(k[0].z, k[0].w));
 #pragma unroll
-    for (int i = 1; i < N; ++i) cm = fmaxf(cm, z[i]);
-    if (cm > q.m) {
-        if (q.m == -INFINITY) {
-            // nothing but -inf (0) or NaN (kept) so far
-        } else {
-            const float d = q.m - cm, c = __expf(d);
-            q.a = c * fmaf(max_nan(d, kFar), q.s, q.a);
-            q.s *= c;
+    for (int i = 1; i < N; ++i)
+        top = max_word<T>(top, max_word<T>(max_word<T>(k[i].x, k[i].y), max_word<T>(k[i].z, k[i].w)));
+    const float m = word_max<T>(top);
+    if (m > q.m) move_to(q, m);
+    if (!has_floor<T>(q.m)) {
+        // no maximum yet, or one near the type's lowest value
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) {
+            uint4 w = k[0];
+#pragma unroll
+            for (int j = 1; j < N; ++j) w = i == j ? k[j] : w;
+            float z[Slice<T>::V];
+            unpack<T>(w, z);
+#pragma unroll
+            for (int j = 0; j < Slice<T>::V; ++j) take(q, z[j]);
         }
-        q.m = cm;
+        return;
     }
-    const float r = reference_of(q.m);
+    const uint32_t low = floor_of<T>(q.m);
+    const float r = -q.m * kLog2e;
+    const F2 scale = pack_f2(kLog2e, kLog2e), shift = pack_f2(r, r);
+    F2 s = pack_f2(0.f, 0.f), a = s;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float d = max_nan(z[i] - r, kFar);
-        const float e = __expf(d);
-        q.s += e;
-        q.a = fmaf(d, e, q.a);
+        const uint32_t w[4] = {floor_word<T>(k[i].x, low), floor_word<T>(k[i].y, low), floor_word<T>(k[i].z, low),
+                               floor_word<T>(k[i].w, low)};
+#pragma unroll
+        for (int j = 0; j < (int)(8 / sizeof(T)); ++j) {
+            const F2 d = fma2(pair_of<T>(w, j), scale, shift);
+            float lo, hi;
+            unpack_f2(d, lo, hi);
+            const F2 e = pack_f2(exp2_fast(lo), exp2_fast(hi));
+            s = add2(s, e);
+            a = fma2(d, e, a);
+        }
     }
+    float lo, hi;
+    unpack_f2(s, lo, hi);
+    q.s += lo + hi;
+    unpack_f2(a, lo, hi);
+    q.a += lo + hi;
 }
 
 template <typename T>
 __device__ __forceinline__ Sums read_slice(const Slice<T>& s) {
-    constexpr int V = Slice<T>::V;
     Sums q{-INFINITY, 0.f, 0.f};
     const int t = threadIdx.x;
-    if (t < s.head) {
-        const float z[1] = {Num<T>::to_acc(s.row[t])};
-        take(q, z);
-    }
     const uint4* body = reinterpret_cast<const uint4*>(s.row + s.body);
-    int v = s.v0 + t;
-    for (; v + (kUnroll - 1) * kThreads < s.v1; v += kUnroll * kThreads) {
+    // -inf for packs past the slice's end: they weigh nothing
+    const uint32_t none = splat<T>(-INFINITY);
+    for (int v = s.v0 + t; v < s.v1; v += kUnroll * kThreads) {
         uint4 k[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) k[i] = __ldg(body + v + i * kThreads);
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            float z[V];
-            unpack<T>(k[i], z);
-            take(q, z);
-        }
+        for (int i = 0; i < kUnroll; ++i)
+            k[i] = i == 0 || v + i * kThreads < s.v1 ? __ldg(body + v + i * kThreads) : make_uint4(none, none, none, none);
+        take<T>(q, k);
     }
-    for (; v < s.v1; v += kThreads) {
-        float z[V];
-        unpack<T>(__ldg(body + v), z);
-        take(q, z);
-    }
-    if (s.tail0 + t < s.tail1) {
-        const float z[1] = {Num<T>::to_acc(s.row[s.tail0 + t])};
-        take(q, z);
-    }
+    if (t < s.head) take(q, Num<T>::to_acc(s.row[t]));
+    if (s.tail0 + t < s.tail1) take(q, Num<T>::to_acc(s.row[s.tail0 + t]));
     return q;
 }
 
 struct Shared {
-    Sums warp_sums[kWarps];
-    Sums sums;                               // of this block's slice
-    uint32_t group_max[kGroups];
+    float warp_max[kWarps];
+    float2 warp_sums[kWarps];
+    alignas(16) uint32_t group_max[kGroups];
     uint32_t bound;
     int above, at;
     uint32_t above_key[kBuffer];
@@ -230,9 +363,9 @@ struct Shared {
     uint32_t best_key[kMaxTop];              // this slice's best, in order
     int best_index[kMaxTop];
     int best_count;
-    uint32_t all_key[kMaxCluster * kMaxTop]; // the first block: every slice's
+    Sums slice_sums[kMaxCluster];            // the first block: every slice's
+    uint32_t all_key[kMaxCluster * kMaxTop];
     int all_index[kMaxCluster * kMaxTop];
-    int all_count;
 };
 
 __device__ __forceinline__ bool better(uint32_t ka, int ia, uint32_t kb, int ib) {
@@ -248,7 +381,7 @@ __device__ void top_by_rounds(const Slice<T>& s, int k, Shared& sh) {
     int n = 0;
     for (; n < k; ++n) {
         unsigned long long best = 0;
-        own_elements(s, [&](float z, int i) {
+        own_elements<T, true>(s, 0.f, [&](float z, int i) {
             // (key, lower index first); below ~0 whatever the key
             const unsigned long long c = ((unsigned long long)order_key(z) << 32) | (0x7FFFFFFFu - (uint32_t)i);
             if (c < last && c > best) best = c;
@@ -303,7 +436,7 @@ __device__ void lowest_at(const Slice<T>& s, uint32_t key, int k, Shared& sh) {
 }
 
 // The slice's k best elements in order, into best_*.  `mine`: this thread's
-// maximum; `plain`: no NaN was met.
+// maximum; the groups' maxima are in place; `plain`: no NaN was met.
 template <typename T>
 __device__ void top_of_slice(const Slice<T>& s, float mine, bool plain, int k, Shared& sh) {
     if (!plain) {                                    // uniform over the block
@@ -311,27 +444,25 @@ __device__ void top_of_slice(const Slice<T>& s, float mine, bool plain, int k, S
         return;
     }
     const int t = threadIdx.x;
-    const uint32_t own_key = order_key(mine);
-    uint32_t g = own_key;
-    g = max(g, __shfl_xor_sync(0xffffffffu, g, 1));
-    g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
-    if ((t & 3) == 0) sh.group_max[t >> 2] = g;
     if (t == 0) sh.above = sh.at = 0;
-    __syncthreads();
-    if (t < kGroups) {
-        const uint32_t me = sh.group_max[t];
+    {
+        // a group's rank among all: its two threads count half each
+        const int g = t >> 1, half = (t & 1) * (kGroups / 2);
+        const uint32_t me = sh.group_max[g];
         int rank = 0;
-#pragma unroll 8
-        for (int i = 0; i < kGroups; ++i) {
-            const uint32_t o = sh.group_max[i];
-            rank += o > me || (o == me && i < t);
+#pragma unroll
+        for (int i = half; i < half + kGroups / 2; i += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(&sh.group_max[i]);
+            rank += (o.x > me || (o.x == me && i < g)) + (o.y > me || (o.y == me && i + 1 < g)) +
+                    (o.z > me || (o.z == me && i + 2 < g)) + (o.w > me || (o.w == me && i + 3 < g));
         }
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
         if (rank == k - 1) sh.bound = me;
     }
     __syncthreads();
     const uint32_t bound = sh.bound;
-    if (own_key >= bound)
-        own_elements(s, [&](float z, int i) {
+    if (order_key(mine) >= bound)
+        own_elements<T, false>(s, key_value(bound), [&](float z, int i) {
             const uint32_t key = order_key(z);
             if (key > bound) {
                 const int at = atomicAdd(&sh.above, 1);
@@ -367,108 +498,107 @@ __device__ void top_of_slice(const Slice<T>& s, float mine, bool plain, int k, S
     }
 }
 
-__device__ __forceinline__ uint32_t remote(const void* local, int rank) {
-    uint32_t out;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-        : "=r"(out)
-        : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
-    return out;
+// store into the first block of the cluster
+__device__ __forceinline__ void give_first(const void* local, uint32_t value) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(local)));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(value) : "memory");
 }
-__device__ __forceinline__ uint32_t remote_u32(const void* local, int rank) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(local, rank)) : "memory");
-    return v;
-}
-__device__ __forceinline__ float remote_f32(const float* local, int rank) {
-    return __uint_as_float(remote_u32(local, rank));
-}
-__device__ __forceinline__ void cluster_barrier() {
+__device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) forward_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 6) forward_kernel(const Params p) {
     __shared__ Shared sh;
     const int parts = p.cluster;
     const int64_t row = blockIdx.x / parts;
     const int part = (int)(blockIdx.x % parts);      // = the block's rank in its cluster
     const int t = threadIdx.x;
+    if (parts > 1) cluster_arrive();
     grid_dependency_wait();
     grid_launch_dependents();
     const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
     const Slice<T> slice = slice_of(z, p.vocab, part, parts);
     Sums q = read_slice(slice);
     const float mine = q.m;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        Sums o;
-        o.m = __shfl_xor_sync(0xffffffffu, q.m, d);
-        o.s = __shfl_xor_sync(0xffffffffu, q.s, d);
-        o.a = __shfl_xor_sync(0xffffffffu, q.a, d);
-        q = (t & d) ? join(o, q) : join(q, o);
-    }
-    if ((t & 31) == 0) sh.warp_sums[t >> 5] = q;
-    __syncthreads();
-    if (t < 32) {
-        q = t < kWarps ? sh.warp_sums[t] : Sums{-INFINITY, 0.f, 0.f};
-#pragma unroll
-        for (int d = 1; d < kWarps; d <<= 1) {
-            Sums o;
-            o.m = __shfl_xor_sync(0xffffffffu, q.m, d);
-            o.s = __shfl_xor_sync(0xffffffffu, q.s, d);
-            o.a = __shfl_xor_sync(0xffffffffu, q.a, d);
-            q = (t & d) ? join(o, q) : join(q, o);
-        }
-        if (t == 0) sh.sums = q;
+    {
+        const uint32_t key = order_key(mine);
+        const uint32_t g = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+        const uint32_t w = __reduce_max_sync(0xffffffffu, key);
+        if ((t & 1) == 0) sh.group_max[t >> 1] = g;
+        if ((t & 31) == 0) sh.warp_max[t >> 5] = key_value(w);
     }
     __syncthreads();
-    if (p.top > 0) {
-        top_of_slice(slice, mine, sh.sums.s == sh.sums.s, p.top, sh);
-        __syncthreads();
+    float m = sh.warp_max[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.warp_max[w]);
+    move_to(q, m);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        q.s += __shfl_xor_sync(0xffffffffu, q.s, d);
+        q.a += __shfl_xor_sync(0xffffffffu, q.a, d);
     }
+    if ((t & 31) == 0) sh.warp_sums[t >> 5] = make_float2(q.s, q.a);
+    __syncthreads();
+    q.s = q.a = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        q.s += sh.warp_sums[w].x;
+        q.a += sh.warp_sums[w].y;
+    }
+    if (p.top > 0) top_of_slice(slice, mine, q.s == q.s, p.top, sh);
+    __syncthreads();
     if (parts > 1) {
-        cluster_barrier();                           // every slice's results are in its block's memory
-        if (part == 0) {
-            if (t == 0) {
-                q = sh.sums;
-                for (int r = 1; r < parts; ++r)
-                    q = join(q, Sums{remote_f32(&sh.sums.m, r), remote_f32(&sh.sums.s, r), remote_f32(&sh.sums.a, r)});
-                sh.warp_sums[0] = q;
-            }
-            if (p.top > 0) {
-                const int r = t / kMaxTop, i = t % kMaxTop;
-                if (t == 0) sh.all_count = 0;
-                __syncthreads();
-                if (r < parts && i < (int)remote_u32(&sh.best_count, r)) {
-                    const int at = atomicAdd(&sh.all_count, 1);
-                    sh.all_key[at] = remote_u32(&sh.best_key[i], r);
-                    sh.all_index[at] = (int)remote_u32(&sh.best_index[i], r);
+        // every slice's results go to the first block
+        cluster_wait();                              // all blocks of the cluster run
+        if (t == 0) {
+            give_first(&sh.slice_sums[part].m, __float_as_uint(q.m));
+            give_first(&sh.slice_sums[part].s, __float_as_uint(q.s));
+            give_first(&sh.slice_sums[part].a, __float_as_uint(q.a));
+        }
+        if (t < kMaxTop && p.top > 0) {
+            const bool some = t < sh.best_count;
+            give_first(&sh.all_key[part * kMaxTop + t], some ? sh.best_key[t] : 0u);      // 0: below every element
+            give_first(&sh.all_index[part * kMaxTop + t], some ? (uint32_t)sh.best_index[t] : 0u);
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (part != 0) return;
+        q = sh.slice_sums[0];
+        for (int r = 1; r < parts; ++r) q = join(q, sh.slice_sums[r]);
+        if (p.top > 0) {
+            // an element's rank: its place in its own slice, and in each other slice the elements that go before it
+            const int r = t / kMaxTop, i = t % kMaxTop;
+            if (r < parts && i < p.top) {
+                const uint32_t key = sh.all_key[t];
+                const int index = sh.all_index[t];
+                int rank = i;
+                for (int o = 0; o < parts; ++o) {
+                    if (o == r) continue;
+                    int n = 0;                       // in order: the count is a place, found by halving
+#pragma unroll
+                    for (int step = kMaxTop / 2; step > 0; step >>= 1)
+                        if (n + step <= p.top && better(sh.all_key[o * kMaxTop + n + step - 1],
+                                                        sh.all_index[o * kMaxTop + n + step - 1], key, index))
+                            n += step;
+                    if (n + 1 <= p.top && better(sh.all_key[o * kMaxTop + n], sh.all_index[o * kMaxTop + n], key, index)) ++n;
+                    rank += n;
                 }
-                __syncthreads();
-                const int n = sh.all_count;
-                if (t < n) {
-                    const uint32_t key = sh.all_key[t];
-                    const int index = sh.all_index[t];
-                    int rank = 0;
-                    for (int c = 0; c < n; ++c) rank += better(sh.all_key[c], sh.all_index[c], key, index);
-                    if (rank < p.top) {
-                        sh.best_key[rank] = key;
-                        sh.best_index[rank] = index;
-                    }
+                if (key != 0 && rank < p.top) {
+                    sh.best_key[rank] = key;
+                    sh.best_index[rank] = index;
                 }
             }
             __syncthreads();
         }
-        cluster_barrier();                           // no block leaves while its memory is read
-        if (part != 0) return;
-        q = sh.warp_sums[0];
-    } else {
-        q = sh.sums;
     }
-    const float log_s = logf(q.s);
+    const float log_s = log2f(q.s);
     const bool nothing = q.m == -INFINITY && q.s == 0.f;     // every logit is -inf
-    const float lse = nothing ? -INFINITY : q.m + log_s;
+    const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, extreme(q.m) ? q.m : scaled_max(q.m) * kLn2);
     if (t == 0) {
         const int64_t token = p.tokens[row];
         float lp;
@@ -477,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const Params p) {
         else lp = nothing ? -INFINITY : Num<T>::to_acc(z[token]) - lse;
         p.logprob[row] = lp;
         if (p.lse) p.lse[row] = lse;
-        if (p.entropy) p.entropy[row] = nothing ? 0.f : log_s - q.a / q.s;
+        if (p.entropy) p.entropy[row] = nothing ? 0.f : (log_s - q.a / q.s) * kLn2;
     }
     if (t < p.top) {
         const float v = key_value(sh.best_key[t]);
@@ -487,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 2) forward_kernel(const Params p) {
 }
 
 // One block takes a stretch of a row.  Every element is read and written by
-// the same thread, so dlogits may be the logits.
+// the same thread, so dlogits may be the logits.  With c = dlogprob + dH (H -
+// lse), dz = -p (c + dH z), and dlogprob more at the token.
 template <typename T>
 __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     constexpr int V = 16 / sizeof(T);
@@ -499,16 +630,17 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     T* d = static_cast<T*>(p.dlogits) + row * p.d_pitch;
     const Slice<T> s = slice_of(z, p.vocab, part, p.chunks);
     const float lse = p.lse[row];
-    const int64_t token = p.dlogprob ? p.tokens[row] : -1;
-    float dlp = p.dlogprob && token >= 0 ? p.dlogprob[row] : 0.f;
-    if (token >= p.vocab) dlp = __uint_as_float(0x7FC00000u);
+    const int64_t token64 = p.dlogprob ? p.tokens[row] : -1;
+    const int token = token64 < 0 || token64 >= p.vocab ? -1 : (int)token64;
+    float dlp = token64 >= 0 ? p.dlogprob[row] : 0.f;
+    if (token64 >= p.vocab) dlp = __uint_as_float(0x7FC00000u);
     const float dh = p.dentropy ? p.dentropy[row] : 0.f;
     const float h = p.dentropy ? p.entropy[row] : 0.f;
     const bool nothing = lse == -INFINITY;
-    auto grad = [&](float v, int i) -> float {
+    const float shift = -lse * kLog2e, c = fmaf(dh, h - lse, dlp);
+    auto grad = [&](float v, int i) -> float {           // any values
         if (nothing) return 0.f;
-        const float logp = v - lse;
-        const float q = __expf(logp);
+        const float logp = v - lse, q = exp2_fast(logp * kLog2e);
         // a probability of zero contributes nothing, whatever its logarithm
         float g = q == 0.f && dlp == dlp ? 0.f : -q * fmaf(dh, logp + h, dlp);
         if (i == token) g += dlp;
@@ -518,18 +650,58 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     if (t < s.head) d[t] = Num<T>::from_acc(grad(Num<T>::to_acc(z[t]), t));
     const uint4* body = reinterpret_cast<const uint4*>(z + s.body);
     const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+    const bool quick = has_floor<T>(lse) && same;
+    const uint32_t low = floor_of<T>(quick ? lse : 0.f);
+    const F2 scale2 = pack_f2(kLog2e, kLog2e), shift2 = pack_f2(shift, shift), c2 = pack_f2(-c, -c),
+             dh2 = pack_f2(-dh, -dh);
+#pragma unroll 4
     for (int v = s.v0 + t; v < s.v1; v += 256) {
-        float k[V];
-        unpack<T>(body[v], k);
-        uint4 o;
-        T* e = reinterpret_cast<T*>(&o);
+        const uint4 k = body[v];
+        const int at = s.body + v * V;
+        if (quick) {
+            const uint32_t w[4] = {floor_word<T>(k.x, low), floor_word<T>(k.y, low), floor_word<T>(k.z, low),
+                                   floor_word<T>(k.w, low)};
+            F2 g[V / 2];
 #pragma unroll
-        for (int i = 0; i < V; ++i) e[i] = Num<T>::from_acc(grad(k[i], s.body + v * V + i));
-        if (same) {
-            *reinterpret_cast<uint4*>(d + s.body + v * V) = o;
+            for (int j = 0; j < V / 2; ++j) {
+                const F2 x = pair_of<T>(w, j);
+                float lo, hi;
+                unpack_f2(fma2(x, scale2, shift2), lo, hi);
+                g[j] = mul2(pack_f2(exp2_fast(lo), exp2_fast(hi)), fma2(x, dh2, c2));
+            }
+            if ((unsigned)(token - at) < (unsigned)V) {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    float lo, hi;
+                    unpack_f2(g[j], lo, hi);
+                    if (token == at + 2 * j) lo += dlp;
+                    if (token == at + 2 * j + 1) hi += dlp;
+                    g[j] = pack_f2(lo, hi);
+                }
+            }
+            uint4 o;
+            uint32_t* e = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                float lo, hi;
+                unpack_f2(g[j], lo, hi);
+                if constexpr (sizeof(T) == 4) {
+                    e[2 * j] = __float_as_uint(lo);
+                    e[2 * j + 1] = __float_as_uint(hi);
+                } else if constexpr (std::is_same_v<T, __half>) {
+                    const __half2 y = __floats2half2_rn(lo, hi);
+                    e[j] = *reinterpret_cast<const uint32_t*>(&y);
+                } else {
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(lo, hi);
+                    e[j] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+            }
+            *reinterpret_cast<uint4*>(d + at) = o;
         } else {
+            float x[V];
+            unpack<T>(k, x);
 #pragma unroll
-            for (int i = 0; i < V; ++i) d[s.body + v * V + i] = e[i];
+            for (int i = 0; i < V; ++i) d[at + i] = Num<T>::from_acc(grad(x[i], at + i));
         }
     }
     if (s.tail0 + t < s.tail1) d[s.tail0 + t] = Num<T>::from_acc(grad(Num<T>::to_acc(z[s.tail0 + t]), s.tail0 + t));
