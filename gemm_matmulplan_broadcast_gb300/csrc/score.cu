@@ -25,19 +25,24 @@
 #include <new>
 #include <type_traits>
 
-#include "common.cuh"
 #include "plan_state.h"
+#include "tc_ptx.cuh"
 
 namespace olc {
 namespace score {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;               // consumers; one more warp issues the loads
 constexpr int kWarps = kThreads / 32;
+constexpr int kBlockThreads = kThreads + 32;
 constexpr int kGroups = kThreads / 2;       // two neighbouring threads share a maximum
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBuffer = 1024;               // candidates above the bound, and as many at it
-constexpr int kUnroll = 4;                  // 16-byte loads in flight a thread
+constexpr int kUnroll = 4;                  // 16-byte packs a thread takes of a chunk
+constexpr int kChunk = kThreads * kUnroll;  // packs of a chunk: 16 KiB
+constexpr int kStages = 3;                  // chunks in flight or in use a block
+constexpr int kBlocksPerSm = 3;
+constexpr int kGradPacks = 4;               // backward: packs a thread
 
 struct Params {
     const void* logits;
@@ -51,6 +56,8 @@ struct Params {
     int vocab;
     int top;
     int cluster;            // blocks a row
+    int64_t units;          // rows x cluster
+    unsigned int* err;
 };
 
 struct GradParams {
@@ -227,8 +234,9 @@ __device__ __forceinline__ Slice<T> slice_of(const T* row, int vocab, int part, 
     const int packs = (vocab - lead) / V;
     s.body = lead;
     s.head = part == 0 ? lead : 0;
-    s.v0 = (int)((int64_t)packs * part / parts);
-    s.v1 = (int)((int64_t)packs * (part + 1) / parts);
+    const int each = parts == 1 ? packs : packs / parts, extra = packs - each * parts;
+    s.v0 = each * part + min(part, extra);          // the first `extra` slices take one more
+    s.v1 = s.v0 + each + (part < extra ? 1 : 0);
     s.tail0 = part == parts - 1 ? lead + packs * V : vocab;
     s.tail1 = vocab;
     return s;
@@ -247,26 +255,53 @@ __device__ __forceinline__ float pack_max(const uint4& k) {
     return word_max<T>(max_word<T>(max_word<T>(k.x, k.y), max_word<T>(k.z, k.w)));
 }
 
-// every element of the slice that this thread owns: f(value, index); packs
-// whose largest element is below `least` are passed over (ALL: none are)
+// bit i: element i of the pack is at least the word's (NaN: no)
+template <typename T>
+__device__ __forceinline__ unsigned reaching(const uint4& k, uint32_t least) {
+    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+    unsigned m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            m |= (unsigned)(__uint_as_float(w[i]) >= __uint_as_float(least)) << i;
+        } else {
+            unsigned r;
+            if constexpr (std::is_same_v<T, __half>)
+                r = __hge2_mask(*reinterpret_cast<const __half2*>(&w[i]), *reinterpret_cast<const __half2*>(&least));
+            else
+                r = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
+                                *reinterpret_cast<const __nv_bfloat162*>(&least));
+            m |= ((r & 1u) | ((r >> 16) & 2u)) << (2 * i);
+        }
+    }
+    return m;
+}
+
+// every element of the slice that this thread owns and that is at least
+// `least` (ALL: any element): f(value, index)
 template <typename T, bool ALL, typename F>
 __device__ __forceinline__ void own_elements(const Slice<T>& s, float least, F&& f) {
     constexpr int V = Slice<T>::V;
     const int t = threadIdx.x;
+    const uint32_t bound = splat<T>(least);          // one of the row's own values: exact
     if (t < s.head) f(Num<T>::to_acc(s.row[t]), t);
     const uint4* body = reinterpret_cast<const uint4*>(s.row + s.body);
 #pragma unroll 4
     for (int v = s.v0 + t; v < s.v1; v += kThreads) {
         const uint4 k = __ldg(body + v);
         if (!ALL && !(pack_max<T>(k) >= least)) continue;
-        float z[V];
-        unpack<T>(k, z);
-#pragma unroll 1
-        for (int i = 0; i < V; ++i) {
-            float x = z[0];
-#pragma unroll
-            for (int j = 1; j < V; ++j) x = i == j ? z[j] : x;
-            f(x, s.body + v * V + i);
+        unsigned m = ALL ? (1u << V) - 1 : reaching<T>(k, bound);
+        while (m) {
+            const int i = __ffs(m) - 1;
+            m &= m - 1;
+            const int word = i * (int)sizeof(T) / 4;
+            const uint32_t w = word < 2 ? (word ? k.y : k.x) : (word == 2 ? k.z : k.w);
+            if constexpr (sizeof(T) == 4) {
+                f(__uint_as_float(w), s.body + v * V + i);
+            } else {
+                const unsigned short b = (unsigned short)(w >> (16 * (i & 1)));
+                f(Num<T>::to_acc(*reinterpret_cast<const T*>(&b)), s.body + v * V + i);
+            }
         }
     }
     if (s.tail0 + t < s.tail1) f(Num<T>::to_acc(s.row[s.tail0 + t]), s.tail0 + t);
@@ -330,30 +365,13 @@ __device__ __forceinline__ void take(Sums& q, const uint4 (&k)[N]) {
     q.a += lo + hi;
 }
 
-template <typename T>
-__device__ __forceinline__ Sums read_slice(const Slice<T>& s) {
-    Sums q{-INFINITY, 0.f, 0.f};
-    const int t = threadIdx.x;
-    const uint4* body = reinterpret_cast<const uint4*>(s.row + s.body);
-    // -inf for packs past the slice's end: they weigh nothing
-    const uint32_t none = splat<T>(-INFINITY);
-    for (int v = s.v0 + t; v < s.v1; v += kUnroll * kThreads) {
-        uint4 k[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-            k[i] = i == 0 || v + i * kThreads < s.v1 ? __ldg(body + v + i * kThreads) : make_uint4(none, none, none, none);
-        take<T>(q, k);
-    }
-    if (t < s.head) take(q, Num<T>::to_acc(s.row[t]));
-    if (s.tail0 + t < s.tail1) take(q, Num<T>::to_acc(s.row[s.tail0 + t]));
-    return q;
-}
-
 struct Shared {
+    uint64_t full[kStages], empty[kStages];
+    int abort_flag;
     float warp_max[kWarps];
     float2 warp_sums[kWarps];
     alignas(16) uint32_t group_max[kGroups];
-    uint32_t bound;
+    uint32_t bound;                          // the group maxima's smallest of the k largest
     int above, at;
     uint32_t above_key[kBuffer];
     int above_index[kBuffer];
@@ -371,6 +389,9 @@ struct Shared {
 __device__ __forceinline__ bool better(uint32_t ka, int ia, uint32_t kb, int ib) {
     return ka > kb || (ka == kb && ia < ib);
 }
+
+// the consumers' barrier
+__device__ __forceinline__ void sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 // k rounds, each the best element after the last one: right for any values,
 // taken where more elements than the buffer holds exceed the bound, or where
@@ -391,9 +412,9 @@ __device__ void top_by_rounds(const Slice<T>& s, int k, Shared& sh) {
             const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, d);
             best = o > best ? o : best;
         }
-        __syncthreads();
+        sync();
         if ((threadIdx.x & 31) == 0) sh.warp_best[threadIdx.x >> 5] = best;
-        __syncthreads();
+        sync();
         for (int w = 0; w < kWarps; ++w) best = sh.warp_best[w] > best ? sh.warp_best[w] : best;
         if (best == 0) break;                        // the slice holds no more elements
         if (threadIdx.x == 0) {
@@ -414,9 +435,9 @@ __device__ void lowest_at(const Slice<T>& s, uint32_t key, int k, Shared& sh) {
             const int i = base + (int)threadIdx.x;
             const bool hit = i < end && order_key(Num<T>::to_acc(s.row[i])) == key;
             const unsigned b = __ballot_sync(0xffffffffu, hit);
-            __syncthreads();
+            sync();
             if ((threadIdx.x & 31) == 0) sh.warp_count[threadIdx.x >> 5] = __popc(b);
-            __syncthreads();
+            sync();
             int before = found, all = found;
             for (int w = 0; w < kWarps; ++w) {
                 if (w < (int)(threadIdx.x >> 5)) before += sh.warp_count[w];
@@ -430,9 +451,9 @@ __device__ void lowest_at(const Slice<T>& s, uint32_t key, int k, Shared& sh) {
     scan(0, s.head);
     scan(s.body + s.v0 * Slice<T>::V, s.body + s.v1 * Slice<T>::V);
     scan(s.tail0, s.tail1);
-    __syncthreads();
+    sync();
     if (threadIdx.x == 0) sh.at = min(found, k);
-    __syncthreads();
+    sync();
 }
 
 // The slice's k best elements in order, into best_*.  `mine`: this thread's
@@ -444,22 +465,21 @@ __device__ void top_of_slice(const Slice<T>& s, float mine, bool plain, int k, S
         return;
     }
     const int t = threadIdx.x;
-    if (t == 0) sh.above = sh.at = 0;
     {
-        // a group's rank among all: its two threads count half each
+        // how many groups exceed a group's maximum: its two threads count half each
         const int g = t >> 1, half = (t & 1) * (kGroups / 2);
         const uint32_t me = sh.group_max[g];
-        int rank = 0;
+        int n = 0;
 #pragma unroll
         for (int i = half; i < half + kGroups / 2; i += 4) {
             const uint4 o = *reinterpret_cast<const uint4*>(&sh.group_max[i]);
-            rank += (o.x > me || (o.x == me && i < g)) + (o.y > me || (o.y == me && i + 1 < g)) +
-                    (o.z > me || (o.z == me && i + 2 < g)) + (o.w > me || (o.w == me && i + 3 < g));
+            n += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
         }
-        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-        if (rank == k - 1) sh.bound = me;
+        n += __shfl_xor_sync(0xffffffffu, n, 1);
+        const uint32_t low = __reduce_min_sync(0xffffffffu, n < k ? me : 0xFFFFFFFFu);
+        if ((t & 31) == 0) atomicMin(&sh.bound, low);
     }
-    __syncthreads();
+    sync();
     const uint32_t bound = sh.bound;
     if (order_key(mine) >= bound)
         own_elements<T, false>(s, key_value(bound), [&](float z, int i) {
@@ -475,7 +495,7 @@ __device__ void top_of_slice(const Slice<T>& s, float mine, bool plain, int k, S
                 if (at < kBuffer) sh.at_index[at] = i;
             }
         });
-    __syncthreads();
+    sync();
     const int above = sh.above;
     if (above > kBuffer) {
         top_by_rounds(s, k, sh);
@@ -511,108 +531,202 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Persistent blocks (a row cut over a cluster: one unit each).  The loading
+// warp copies chunk after chunk of the block's rows into a ring, whatever the
+// consumers are at: while they join a row's sums and look for its largest
+// elements, the next row is on its way.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 6) forward_kernel(const Params p) {
+__global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(const Params p) {
+    extern __shared__ __align__(128) unsigned char ring[];
     __shared__ Shared sh;
     const int parts = p.cluster;
-    const int64_t row = blockIdx.x / parts;
-    const int part = (int)(blockIdx.x % parts);      // = the block's rank in its cluster
     const int t = threadIdx.x;
+    volatile int* abort_flag = &sh.abort_flag;
+    if (t == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&sh.full[i], 1);
+            tc::mbar_init(&sh.empty[i], kWarps);
+        }
+        sh.abort_flag = 0;
+        sh.bound = 0xFFFFFFFFu;
+        sh.above = sh.at = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
     if (parts > 1) cluster_arrive();
     grid_dependency_wait();
     grid_launch_dependents();
-    const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
-    const Slice<T> slice = slice_of(z, p.vocab, part, parts);
-    Sums q = read_slice(slice);
-    const float mine = q.m;
-    {
-        const uint32_t key = order_key(mine);
-        const uint32_t g = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
-        const uint32_t w = __reduce_max_sync(0xffffffffu, key);
-        if ((t & 1) == 0) sh.group_max[t >> 1] = g;
-        if ((t & 31) == 0) sh.warp_max[t >> 5] = key_value(w);
-    }
-    __syncthreads();
-    float m = sh.warp_max[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.warp_max[w]);
-    move_to(q, m);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        q.s += __shfl_xor_sync(0xffffffffu, q.s, d);
-        q.a += __shfl_xor_sync(0xffffffffu, q.a, d);
-    }
-    if ((t & 31) == 0) sh.warp_sums[t >> 5] = make_float2(q.s, q.a);
-    __syncthreads();
-    q.s = q.a = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        q.s += sh.warp_sums[w].x;
-        q.a += sh.warp_sums[w].y;
-    }
-    if (p.top > 0) top_of_slice(slice, mine, q.s == q.s, p.top, sh);
-    __syncthreads();
-    if (parts > 1) {
-        // every slice's results go to the first block
-        cluster_wait();                              // all blocks of the cluster run
-        if (t == 0) {
-            give_first(&sh.slice_sums[part].m, __float_as_uint(q.m));
-            give_first(&sh.slice_sums[part].s, __float_as_uint(q.s));
-            give_first(&sh.slice_sums[part].a, __float_as_uint(q.a));
-        }
-        if (t < kMaxTop && p.top > 0) {
-            const bool some = t < sh.best_count;
-            give_first(&sh.all_key[part * kMaxTop + t], some ? sh.best_key[t] : 0u);      // 0: below every element
-            give_first(&sh.all_index[part * kMaxTop + t], some ? (uint32_t)sh.best_index[t] : 0u);
-        }
-        cluster_arrive();
-        cluster_wait();
-        if (part != 0) return;
-        q = sh.slice_sums[0];
-        for (int r = 1; r < parts; ++r) q = join(q, sh.slice_sums[r]);
-        if (p.top > 0) {
-            // an element's rank: its place in its own slice, and in each other slice the elements that go before it
-            const int r = t / kMaxTop, i = t % kMaxTop;
-            if (r < parts && i < p.top) {
-                const uint32_t key = sh.all_key[t];
-                const int index = sh.all_index[t];
-                int rank = i;
-                for (int o = 0; o < parts; ++o) {
-                    if (o == r) continue;
-                    int n = 0;                       // in order: the count is a place, found by halving
-#pragma unroll
-                    for (int step = kMaxTop / 2; step > 0; step >>= 1)
-                        if (n + step <= p.top && better(sh.all_key[o * kMaxTop + n + step - 1],
-                                                        sh.all_index[o * kMaxTop + n + step - 1], key, index))
-                            n += step;
-                    if (n + 1 <= p.top && better(sh.all_key[o * kMaxTop + n], sh.all_index[o * kMaxTop + n], key, index)) ++n;
-                    rank += n;
-                }
-                if (key != 0 && rank < p.top) {
-                    sh.best_key[rank] = key;
-                    sh.best_index[rank] = index;
+
+    if (t >= kThreads) {
+        if (t == kThreads) {
+            uint32_t stage = 0, phase = 0, armed = 0, parity = 0;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+                const T* z = static_cast<const T*>(p.logits) + u / parts * p.pitch;
+                const Slice<T> s = slice_of(z, p.vocab, (int)(u % parts), parts);
+                const uint4* body = reinterpret_cast<const uint4*>(z + s.body);
+                for (int v = s.v0; v < s.v1; v += kChunk) {
+                    if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bytes = (uint32_t)min(kChunk, s.v1 - v) * 16;
+                    tc::mbar_arrive_expect_tx(&sh.full[stage], bytes);
+                    armed |= 1u << stage;
+                    parity = (parity & ~(1u << stage)) | (phase << stage);
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                            tc::smem_u32(ring) + stage * (kChunk * 16)),
+                        "l"(body + v), "r"(bytes), "r"(tc::smem_u32(&sh.full[stage]))
+                        : "memory");
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
                 }
             }
-            __syncthreads();
+            if (*abort_flag)                         // nothing may land after the block has left
+                for (int i = 0; i < kStages; ++i)
+                    if ((armed >> i) & 1u) tc::mbar_wait_drain(&sh.full[i], (parity >> i) & 1u);
         }
+        __syncwarp();
+        if (parts > 1) {
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
+        }
+        return;
     }
-    const float log_s = log2f(q.s);
-    const bool nothing = q.m == -INFINITY && q.s == 0.f;     // every logit is -inf
-    const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, extreme(q.m) ? q.m : scaled_max(q.m) * kLn2);
-    if (t == 0) {
-        const int64_t token = p.tokens[row];
-        float lp;
-        if (token < 0) lp = 0.f;                             // ignored
-        else if (token >= p.vocab) lp = __uint_as_float(0x7FC00000u);
-        else lp = nothing ? -INFINITY : Num<T>::to_acc(z[token]) - lse;
-        p.logprob[row] = lp;
-        if (p.lse) p.lse[row] = lse;
-        if (p.entropy) p.entropy[row] = nothing ? 0.f : (log_s - q.a / q.s) * kLn2;
-    }
-    if (t < p.top) {
-        const float v = key_value(sh.best_key[t]);
-        if (p.top_logprob) p.top_logprob[row * p.top + t] = nothing ? -INFINITY : v - lse;
-        if (p.top_index) p.top_index[row * p.top + t] = sh.best_index[t];
+
+    uint32_t stage = 0, phase = 0;
+    const uint32_t none = splat<T>(-INFINITY);
+    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+        const int64_t row = u / parts;
+        const int part = (int)(u % parts);           // = the block's rank in its cluster
+        const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
+        const Slice<T> slice = slice_of(z, p.vocab, part, parts);
+        Sums q{-INFINITY, 0.f, 0.f};
+        if (t < slice.head) take(q, Num<T>::to_acc(z[t]));
+        if (slice.tail0 + t < slice.tail1) take(q, Num<T>::to_acc(z[slice.tail0 + t]));
+        for (int v = slice.v0; v < slice.v1; v += kChunk) {
+            if (tc::mbar_wait(&sh.full[stage], phase, abort_flag, p.err)) {
+                const uint4* chunk = reinterpret_cast<const uint4*>(ring + stage * (kChunk * 16));
+                if (v + t < slice.v1) {
+                    // -inf for packs past the slice's end: they weigh nothing
+                    uint4 k[kUnroll];
+#pragma unroll
+                    for (int i = 0; i < kUnroll; ++i)
+                        k[i] = i == 0 || v + t + i * kThreads < slice.v1 ? chunk[t + i * kThreads]
+                                                                         : make_uint4(none, none, none, none);
+                    take<T>(q, k);
+                }
+            }
+            __syncwarp();
+            if ((t & 31) == 0) tc::mbar_arrive(&sh.empty[stage]);
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        const float mine = q.m;
+        {
+            const uint32_t key = order_key(mine);
+            const uint32_t w = __reduce_max_sync(0xffffffffu, key);
+            if (p.top > 0) {
+                const uint32_t g = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
+                if ((t & 1) == 0) sh.group_max[t >> 1] = g;
+            }
+            if ((t & 31) == 0) sh.warp_max[t >> 5] = key_value(w);
+        }
+        sync();
+        float m = sh.warp_max[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.warp_max[w]);
+        move_to(q, m);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            q.s += __shfl_xor_sync(0xffffffffu, q.s, d);
+            q.a += __shfl_xor_sync(0xffffffffu, q.a, d);
+        }
+        if ((t & 31) == 0) sh.warp_sums[t >> 5] = make_float2(q.s, q.a);
+        sync();
+        q.s = q.a = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            q.s += sh.warp_sums[w].x;
+            q.a += sh.warp_sums[w].y;
+        }
+        if (p.top > 0) {
+            top_of_slice(slice, mine, q.s == q.s, p.top, sh);
+            sync();
+            if (t == 0) {                            // for the block's next row
+                sh.bound = 0xFFFFFFFFu;
+                sh.above = sh.at = 0;
+            }
+        }
+        if (parts > 1) {
+            // every slice's results go to the first block
+            cluster_wait();                          // all blocks of the cluster run
+            if (t == 0) {
+                give_first(&sh.slice_sums[part].m, __float_as_uint(q.m));
+                give_first(&sh.slice_sums[part].s, __float_as_uint(q.s));
+                give_first(&sh.slice_sums[part].a, __float_as_uint(q.a));
+            }
+            if (t < kMaxTop && p.top > 0) {
+                const bool some = t < sh.best_count;
+                give_first(&sh.all_key[part * kMaxTop + t], some ? sh.best_key[t] : 0u);      // 0: below every element
+                give_first(&sh.all_index[part * kMaxTop + t], some ? (uint32_t)sh.best_index[t] : 0u);
+            }
+            cluster_arrive();
+            cluster_wait();
+            if (part != 0) return;
+            q = sh.slice_sums[0];
+            for (int r = 1; r < parts; ++r) q = join(q, sh.slice_sums[r]);
+            if (p.top > 0) {
+                // an element's rank: its place in its own slice, and in each other slice the elements that go before it
+                const int r = t / kMaxTop, i = t % kMaxTop;
+                if (r < parts && i < p.top) {
+                    const uint32_t key = sh.all_key[t];
+                    const int index = sh.all_index[t];
+                    int rank = i;
+                    for (int o = 0; o < parts; ++o) {
+                        if (o == r) continue;
+                        int n = 0;                   // in order: the count is a place, found by halving
+                        const int b = o * kMaxTop;
+#pragma unroll
+                        for (int step = kMaxTop / 2; step > 0; step >>= 1)
+                            if (n + step <= p.top && better(sh.all_key[b + n + step - 1], sh.all_index[b + n + step - 1], key, index))
+                                n += step;
+                        if (n + 1 <= p.top && better(sh.all_key[b + n], sh.all_index[b + n], key, index)) ++n;
+                        rank += n;
+                    }
+                    if (key != 0 && rank < p.top) {
+                        sh.best_key[rank] = key;
+                        sh.best_index[rank] = index;
+                    }
+                }
+                sync();
+            }
+        }
+        const bool nothing = q.m == -INFINITY && q.s == 0.f;     // every logit is -inf
+        const float log_s = log2f(q.s);
+        const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, extreme(q.m) ? q.m : scaled_max(q.m) * kLn2);
+        if (t < p.top) {
+            const float v = key_value(sh.best_key[t]);
+            if (p.top_logprob) p.top_logprob[row * p.top + t] = nothing ? -INFINITY : v - lse;
+            if (p.top_index) p.top_index[row * p.top + t] = sh.best_index[t];
+        }
+        if (t == 32) {
+            const int64_t token = p.tokens[row];
+            float lp;
+            if (token < 0) lp = 0.f;                             // ignored
+            else if (token >= p.vocab) lp = __uint_as_float(0x7FC00000u);
+            else lp = nothing ? -INFINITY : Num<T>::to_acc(z[token]) - lse;
+            p.logprob[row] = lp;
+            if (p.lse) p.lse[row] = lse;
+            if (p.entropy) p.entropy[row] = nothing ? 0.f : (log_s - q.a / q.s) * kLn2;
+        }
     }
 }
 
@@ -629,6 +743,12 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
     T* d = static_cast<T*>(p.dlogits) + row * p.d_pitch;
     const Slice<T> s = slice_of(z, p.vocab, part, p.chunks);
+    const int t = threadIdx.x;
+    const uint4* body = reinterpret_cast<const uint4*>(z + s.body);
+    uint4 k4[kGradPacks];
+#pragma unroll
+    for (int i = 0; i < kGradPacks; ++i)
+        if (s.v0 + t + i * 256 < s.v1) k4[i] = body[s.v0 + t + i * 256];
     const float lse = p.lse[row];
     const int64_t token64 = p.dlogprob ? p.tokens[row] : -1;
     const int token = token64 < 0 || token64 >= p.vocab ? -1 : (int)token64;
@@ -646,17 +766,17 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
         if (i == token) g += dlp;
         return g;
     };
-    const int t = threadIdx.x;
     if (t < s.head) d[t] = Num<T>::from_acc(grad(Num<T>::to_acc(z[t]), t));
-    const uint4* body = reinterpret_cast<const uint4*>(z + s.body);
     const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     const bool quick = has_floor<T>(lse) && same;
     const uint32_t low = floor_of<T>(quick ? lse : 0.f);
     const F2 scale2 = pack_f2(kLog2e, kLog2e), shift2 = pack_f2(shift, shift), c2 = pack_f2(-c, -c),
              dh2 = pack_f2(-dh, -dh);
-#pragma unroll 4
-    for (int v = s.v0 + t; v < s.v1; v += 256) {
-        const uint4 k = body[v];
+#pragma unroll
+    for (int pack = 0; pack < kGradPacks; ++pack) {
+        const int v = s.v0 + t + pack * 256;
+        if (v >= s.v1) break;
+        const uint4 k = k4[pack];
         const int at = s.body + v * V;
         if (quick) {
             const uint32_t w[4] = {floor_word<T>(k.x, low), floor_word<T>(k.y, low), floor_word<T>(k.z, low),
@@ -728,10 +848,14 @@ inline int cluster_of(int64_t rows, int64_t vocab, int sm_count) {
 }
 
 template <typename T>
-cudaError_t launch_forward(const Params& p, int64_t rows, cudaStream_t s) {
+cudaError_t launch_forward(const Params& p, int sm_count, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * p.cluster));
-    cfg.blockDim = dim3(kThreads);
+    const int smem = kStages * kChunk * 16;
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(forward_kernel<T>), smem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(p.cluster > 1 ? p.units : min64(p.units, (int64_t)sm_count * kBlocksPerSm)));
+    cfg.blockDim = dim3(kBlockThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -799,11 +923,11 @@ olc_status olc_token_log_probs_forward(olc_token_log_probs_plan* plan, const voi
         return OLC_ERR_INVALID;
     const olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
+    const int cluster = score::cluster_of(plan->rows, plan->vocab, plan->state.sm_count);
     score::Params p{logits, tokens, logprob, entropy, lse, top_logprob, top_index, pitch, (int)plan->vocab,
-                    top_logprob || top_index ? plan->top : 0,
-                    score::cluster_of(plan->rows, plan->vocab, plan->state.sm_count)};
+                    top_logprob || top_index ? plan->top : 0, cluster, plan->rows * cluster, device_error_word()};
     return score::by_type(plan->dtype, [&](auto tag) {
-        return plan_status(score::launch_forward<decltype(tag)>(p, plan->rows, static_cast<cudaStream_t>(stream)));
+        return plan_status(score::launch_forward<decltype(tag)>(p, plan->state.sm_count, static_cast<cudaStream_t>(stream)));
     });
 }
 
@@ -824,9 +948,9 @@ olc_status olc_token_log_probs_backward(olc_token_log_probs_plan* plan, const vo
         return OLC_ERR_INVALID;
     const olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
-    // four packs a thread
-    const int64_t stretch = 256 * 4 * (16 / eb);
-    const int64_t chunks = ceil_div(plan->vocab, stretch);
+    // slices of at most kGradPacks packs a thread
+    const int64_t packs = plan->vocab / (16 / eb);
+    const int64_t chunks = max64(1, ceil_div(packs, 256 * score::kGradPacks));
     if (plan->rows * chunks > 0x7fffffffLL) return OLC_ERR_INVALID;
     score::GradParams p{logits, tokens, lse, entropy, dlogprob, dentropy, dlogits, pitch, d_pitch, plan->rows,
                         (int)plan->vocab, (int)chunks};
