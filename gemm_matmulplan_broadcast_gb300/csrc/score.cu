@@ -17,11 +17,11 @@
 // each take a slice of it; the first block joins the slices' sums in slice
 // order through distributed shared memory.
 //
-// The k largest need no second pass over the row.  k groups of threads whose
-// own maximum is at least t hold at least k elements >= t; so the k-th
-// largest of the groups' maxima is a bound that every one of the k largest
-// elements reaches, and only the few threads whose maximum reaches it read
-// their elements again.  Order is by value, then by the lower index.
+// The k largest need no second pass over the row.  k threads whose own maximum
+// is at least t hold at least k elements >= t; so the k-th largest of the
+// threads' maxima is a bound that every one of the k largest elements reaches.
+// Only stretches of a thread's elements whose maximum reaches it are read
+// again: a few packs of the row.  Order is by value, then by the lower index.
 #include <new>
 #include <type_traits>
 
@@ -31,17 +31,17 @@
 namespace olc {
 namespace score {
 
-constexpr int kThreads = 256;               // consumers; one more warp issues the loads
+constexpr int kThreads = 128;               // consumers; one more warp issues the loads, one finishes rows
 constexpr int kWarps = kThreads / 32;
-constexpr int kBlockThreads = kThreads + 32;
-constexpr int kGroups = kThreads / 2;       // two neighbouring threads share a maximum
+constexpr int kBlockThreads = kThreads + 64;
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBuffer = 1024;               // candidates above the bound, and as many at it
-constexpr int kUnroll = 4;                  // 16-byte packs a thread takes of a chunk
+constexpr int kBuffer = 512;                // candidates above the bound, and as many at it
+constexpr int kUnroll = 8;                  // 16-byte packs a thread takes of a chunk
 constexpr int kChunk = kThreads * kUnroll;  // packs of a chunk: 16 KiB
 constexpr int kStages = 3;                  // chunks in flight or in use a block
 constexpr int kBlocksPerSm = 3;
+constexpr int kSlots = 8;                   // stretches of a slice whose maxima each thread keeps
 constexpr int kGradPacks = 4;               // backward: packs a thread
 
 struct Params {
@@ -249,12 +249,6 @@ __device__ __forceinline__ void unpack(const uint4& k, float (&z)[16 / sizeof(T)
     for (int i = 0; i < (int)(16 / sizeof(T)); ++i) z[i] = Num<T>::to_acc(e[i]);
 }
 
-// the largest of a pack's elements
-template <typename T>
-__device__ __forceinline__ float pack_max(const uint4& k) {
-    return word_max<T>(max_word<T>(max_word<T>(k.x, k.y), max_word<T>(k.z, k.w)));
-}
-
 // bit i: element i of the pack is at least the word's (NaN: no)
 template <typename T>
 __device__ __forceinline__ unsigned reaching(const uint4& k, uint32_t least) {
@@ -277,34 +271,11 @@ __device__ __forceinline__ unsigned reaching(const uint4& k, uint32_t least) {
     return m;
 }
 
-// every element of the slice that this thread owns and that is at least
-// `least` (ALL: any element): f(value, index)
-template <typename T, bool ALL, typename F>
-__device__ __forceinline__ void own_elements(const Slice<T>& s, float least, F&& f) {
-    constexpr int V = Slice<T>::V;
-    const int t = threadIdx.x;
-    const uint32_t bound = splat<T>(least);          // one of the row's own values: exact
-    if (t < s.head) f(Num<T>::to_acc(s.row[t]), t);
-    const uint4* body = reinterpret_cast<const uint4*>(s.row + s.body);
-#pragma unroll 4
-    for (int v = s.v0 + t; v < s.v1; v += kThreads) {
-        const uint4 k = __ldg(body + v);
-        if (!ALL && !(pack_max<T>(k) >= least)) continue;
-        unsigned m = ALL ? (1u << V) - 1 : reaching<T>(k, bound);
-        while (m) {
-            const int i = __ffs(m) - 1;
-            m &= m - 1;
-            const int word = i * (int)sizeof(T) / 4;
-            const uint32_t w = word < 2 ? (word ? k.y : k.x) : (word == 2 ? k.z : k.w);
-            if constexpr (sizeof(T) == 4) {
-                f(__uint_as_float(w), s.body + v * V + i);
-            } else {
-                const unsigned short b = (unsigned short)(w >> (16 * (i & 1)));
-                f(Num<T>::to_acc(*reinterpret_cast<const T*>(&b)), s.body + v * V + i);
-            }
-        }
-    }
-    if (s.tail0 + t < s.tail1) f(Num<T>::to_acc(s.row[s.tail0 + t]), s.tail0 + t);
+// chunks a thread's stretch of the slice spans
+template <typename T>
+__device__ __forceinline__ int chunks_a_slot(const Slice<T>& s) {
+    const int chunks = (s.v1 - s.v0 + kChunk - 1) / kChunk;
+    return (chunks + kSlots - 1) / kSlots;
 }
 
 // one element, any values
@@ -316,10 +287,10 @@ __device__ __forceinline__ void take(Sums& q, float z) {
     q.a = fmaf(d, e, q.a);
 }
 
-// N packs at once: the maximum first, then the sums around it, two elements
-// an instruction
+// N packs at once: the maximum first (returned), then the sums around it, two
+// elements an instruction
 template <typename T, int N>
-__device__ __forceinline__ void take(Sums& q, const uint4 (&k)[N]) {
+__device__ __forceinline__ float take(Sums& q, const uint4 (&k)[N]) {
     uint32_t top = max_word<T>(max_word<T>(k[0].x, k[0].y), max_word<T>(k[0].z, k[0].w));
 #pragma unroll
     for (int i = 1; i < N; ++i)
@@ -338,7 +309,7 @@ __device__ __forceinline__ void take(Sums& q, const uint4 (&k)[N]) {
 #pragma unroll
             for (int j = 0; j < Slice<T>::V; ++j) take(q, z[j]);
         }
-        return;
+        return m;
     }
     const uint32_t low = floor_of<T>(q.m);
     const float r = -q.m * kLog2e;
@@ -363,21 +334,24 @@ __device__ __forceinline__ void take(Sums& q, const uint4 (&k)[N]) {
     q.s += lo + hi;
     unpack_f2(a, lo, hi);
     q.a += lo + hi;
+    return m;
 }
 
+// What the consumers leave of a row (or slice) to the finishing warp.
+struct Row {
+    float m[kThreads], s[kThreads], a[kThreads];
+    float slot_max[kSlots][kThreads];        // each thread's maxima over stretches of its packs
+};
+
 struct Shared {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages], empty[kStages];  // the ring's chunks
+    uint64_t row_full[2], row_empty[2];
     int abort_flag;
-    float warp_max[kWarps];
-    float2 warp_sums[kWarps];
-    alignas(16) uint32_t group_max[kGroups];
-    uint32_t bound;                          // the group maxima's smallest of the k largest
-    int above, at;
-    uint32_t above_key[kBuffer];
+    alignas(16) Row row[2];
+    uint32_t above_key[kBuffer];             // elements above the bound, in no order
     int above_index[kBuffer];
-    int at_index[kBuffer];
-    unsigned long long warp_best[kWarps];
-    int warp_count[kWarps];
+    int at_index[kBuffer];                   // elements at it
+    unsigned short hot[kSlots * kThreads];   // (slot, thread) whose maximum reaches the bound
     uint32_t best_key[kMaxTop];              // this slice's best, in order
     int best_index[kMaxTop];
     int best_count;
@@ -393,118 +367,183 @@ __device__ __forceinline__ bool better(uint32_t ka, int ia, uint32_t kb, int ib)
 // the consumers' barrier
 __device__ __forceinline__ void sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
+// The functions below run on one warp.
+
+template <typename T>
+__device__ __forceinline__ float element(const Slice<T>& s, int i) {
+    return Num<T>::to_acc(s.row[i]);
+}
+
 // k rounds, each the best element after the last one: right for any values,
 // taken where more elements than the buffer holds exceed the bound, or where
 // a NaN hides what the maxima say.
 template <typename T>
-__device__ void top_by_rounds(const Slice<T>& s, int k, Shared& sh) {
+__device__ __noinline__ void top_by_rounds(const Slice<T>& s, int k, Shared& sh) {
+    const int lane = threadIdx.x & 31;
     unsigned long long last = ~0ull;
     int n = 0;
     for (; n < k; ++n) {
         unsigned long long best = 0;
-        own_elements<T, true>(s, 0.f, [&](float z, int i) {
+        auto see = [&](float z, int i) {
             // (key, lower index first); below ~0 whatever the key
             const unsigned long long c = ((unsigned long long)order_key(z) << 32) | (0x7FFFFFFFu - (uint32_t)i);
             if (c < last && c > best) best = c;
-        });
+        };
+        if (lane < s.head) see(element(s, lane), lane);
+        const uint4* body = reinterpret_cast<const uint4*>(s.row + s.body);
+#pragma unroll 4
+        for (int v = s.v0 + lane; v < s.v1; v += 32) {
+            float z[Slice<T>::V];
+            unpack<T>(__ldg(body + v), z);
+#pragma unroll
+            for (int i = 0; i < Slice<T>::V; ++i) see(z[i], s.body + v * Slice<T>::V + i);
+        }
+        if (s.tail0 + lane < s.tail1) see(element(s, s.tail0 + lane), s.tail0 + lane);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
             const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, d);
             best = o > best ? o : best;
         }
-        sync();
-        if ((threadIdx.x & 31) == 0) sh.warp_best[threadIdx.x >> 5] = best;
-        sync();
-        for (int w = 0; w < kWarps; ++w) best = sh.warp_best[w] > best ? sh.warp_best[w] : best;
         if (best == 0) break;                        // the slice holds no more elements
-        if (threadIdx.x == 0) {
+        if (lane == 0) {
             sh.best_key[n] = (uint32_t)(best >> 32);
             sh.best_index[n] = (int)(0x7FFFFFFFu - (uint32_t)best);
         }
         last = best;
     }
-    if (threadIdx.x == 0) sh.best_count = n;
+    if (lane == 0) sh.best_count = n;
+    __syncwarp();
 }
 
-// the k lowest indices of elements with this key, in order, into at_index
+// the k lowest indices of elements with this key, in order, into at_index;
+// their number
 template <typename T>
-__device__ void lowest_at(const Slice<T>& s, uint32_t key, int k, Shared& sh) {
+__device__ __noinline__ int lowest_at(const Slice<T>& s, uint32_t key, int k, Shared& sh) {
+    const int lane = threadIdx.x & 31;
     int found = 0;
     auto scan = [&](int begin, int end) {
-        for (int base = begin; base < end && found < k; base += kThreads) {
-            const int i = base + (int)threadIdx.x;
-            const bool hit = i < end && order_key(Num<T>::to_acc(s.row[i])) == key;
+        for (int base = begin; base < end && found < k; base += 32) {
+            const int i = base + lane;
+            const bool hit = i < end && order_key(element(s, i)) == key;
             const unsigned b = __ballot_sync(0xffffffffu, hit);
-            sync();
-            if ((threadIdx.x & 31) == 0) sh.warp_count[threadIdx.x >> 5] = __popc(b);
-            sync();
-            int before = found, all = found;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < (int)(threadIdx.x >> 5)) before += sh.warp_count[w];
-                all += sh.warp_count[w];
-            }
-            before += __popc(b & ((1u << (threadIdx.x & 31)) - 1u));
-            if (hit && before < k) sh.at_index[before] = i;
-            found = all;
+            const int at = found + __popc(b & ((1u << lane) - 1u));
+            if (hit && at < k) sh.at_index[at] = i;
+            found += __popc(b);
         }
     };
     scan(0, s.head);
     scan(s.body + s.v0 * Slice<T>::V, s.body + s.v1 * Slice<T>::V);
     scan(s.tail0, s.tail1);
-    sync();
-    if (threadIdx.x == 0) sh.at = min(found, k);
-    sync();
+    __syncwarp();
+    return min(found, k);
 }
 
-// The slice's k best elements in order, into best_*.  `mine`: this thread's
-// maximum; the groups' maxima are in place; `plain`: no NaN was met.
+// The slice's k best elements in order, into best_*.  `plain`: no NaN was met.
 template <typename T>
-__device__ void top_of_slice(const Slice<T>& s, float mine, bool plain, int k, Shared& sh) {
-    if (!plain) {                                    // uniform over the block
+__device__ __forceinline__ void top_of_slice(const Slice<T>& s, const Row& r, bool plain, int k, Shared& sh) {
+    constexpr int V = Slice<T>::V;
+    if (!plain) {                                    // uniform over the warp
         top_by_rounds(s, k, sh);
         return;
     }
-    const int t = threadIdx.x;
-    {
-        // how many groups exceed a group's maximum: its two threads count half each
-        const int g = t >> 1, half = (t & 1) * (kGroups / 2);
-        const uint32_t me = sh.group_max[g];
-        int n = 0;
+    const int lane = threadIdx.x & 31;
+    // the bound: the k-th largest of 32 groups' maxima
+    const float4 m4 = reinterpret_cast<const float4*>(r.m)[lane];
+    const uint32_t me = order_key(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
+    int larger = 0;
 #pragma unroll
-        for (int i = half; i < half + kGroups / 2; i += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(&sh.group_max[i]);
-            n += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
+    for (int i = 0; i < 32; ++i) larger += __shfl_sync(0xffffffffu, me, i) > me;
+    const uint32_t bound = __reduce_min_sync(0xffffffffu, larger < k ? me : 0xFFFFFFFFu);
+    const float least = key_value(bound);
+
+    // the stretches of threads' packs that reach it
+    const int chunks = (s.v1 - s.v0 + kChunk - 1) / kChunk;
+    const int a_slot = chunks_a_slot(s);
+    const int slots = chunks ? (chunks + a_slot - 1) / a_slot : 0;
+    int n = 0;
+    for (int slot = 0; slot < slots; ++slot) {
+        const float4 x = reinterpret_cast<const float4*>(r.slot_max[slot])[lane];
+        const float q[4] = {x.x, x.y, x.z, x.w};
+        if (!__any_sync(0xffffffffu, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= least)) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool hit = q[j] >= least;
+            const unsigned b = __ballot_sync(0xffffffffu, hit);
+            if (hit) sh.hot[n + __popc(b & ((1u << lane) - 1u))] = (unsigned short)(slot * kThreads + lane * 4 + j);
+            n += __popc(b);
         }
-        n += __shfl_xor_sync(0xffffffffu, n, 1);
-        const uint32_t low = __reduce_min_sync(0xffffffffu, n < k ? me : 0xFFFFFFFFu);
-        if ((t & 31) == 0) atomicMin(&sh.bound, low);
     }
-    sync();
-    const uint32_t bound = sh.bound;
-    if (order_key(mine) >= bound)
-        own_elements<T, false>(s, key_value(bound), [&](float z, int i) {
-            const uint32_t key = order_key(z);
-            if (key > bound) {
-                const int at = atomicAdd(&sh.above, 1);
-                if (at < kBuffer) {
-                    sh.above_key[at] = key;
-                    sh.above_index[at] = i;
-                }
-            } else if (key == bound) {
-                const int at = atomicAdd(&sh.at, 1);
-                if (at < kBuffer) sh.at_index[at] = i;
+    __syncwarp();
+
+    int above = 0, at = 0;
+    auto collect = [&](bool have, float z, int i) {  // the whole warp calls it
+        const uint32_t key = order_key(z);
+        const unsigned low = (1u << lane) - 1u;
+        const unsigned ba = __ballot_sync(0xffffffffu, have && key > bound);
+        const unsigned be = __ballot_sync(0xffffffffu, have && key == bound);
+        if (have && key > bound) {
+            const int q = above + __popc(ba & low);
+            if (q < kBuffer) {
+                sh.above_key[q] = key;
+                sh.above_index[q] = i;
             }
-        });
-    sync();
-    const int above = sh.above;
+        } else if (have && key == bound) {
+            const int q = at + __popc(be & low);
+            if (q < kBuffer) sh.at_index[q] = i;
+        }
+        above += __popc(ba);
+        at += __popc(be);
+    };
+    const int ends = s.head + s.tail1 - s.tail0;     // at most 2 (V - 1) elements
+    if (ends > 0) {
+        const int i = lane < s.head ? lane : s.tail0 + lane - s.head;
+        collect(lane < ends, lane < ends ? element(s, i) : 0.f, i);
+    }
+    // every pack of those stretches, four loads in flight a lane
+    const uint32_t word = splat<T>(least);           // one of the row's own values: exact
+    const uint4* body = reinterpret_cast<const uint4*>(s.row + s.body);
+    const int each = a_slot * kUnroll, items = n * each;
+    for (int base = 0; base < items; base += 128) {
+        uint4 k4[4];
+        int v4[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int item = base + j * 32 + lane;
+            v4[j] = s.v1;
+            if (item < items) {
+                const int h = sh.hot[item / each];
+                v4[j] = s.v0 + h / kThreads * a_slot * kChunk + h % kThreads + item % each * kThreads;
+            }
+            if (v4[j] < s.v1) k4[j] = __ldg(body + v4[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            unsigned m = v4[j] < s.v1 ? reaching<T>(k4[j], word) : 0u;
+            while (__any_sync(0xffffffffu, m != 0)) {
+                const bool have = m != 0;
+                const int i = have ? __ffs(m) - 1 : 0;
+                m &= m - 1;
+                const int w4 = i * (int)sizeof(T) / 4;
+                const uint32_t w = w4 < 2 ? (w4 ? k4[j].y : k4[j].x) : (w4 == 2 ? k4[j].z : k4[j].w);
+                float z;
+                if constexpr (sizeof(T) == 4) {
+                    z = __uint_as_float(w);
+                } else {
+                    const unsigned short b = (unsigned short)(w >> (16 * (i & 1)));
+                    z = Num<T>::to_acc(*reinterpret_cast<const T*>(&b));
+                }
+                collect(have, z, s.body + v4[j] * V + i);
+            }
+        }
+    }
+    __syncwarp();
     if (above > kBuffer) {
         top_by_rounds(s, k, sh);
         return;
     }
-    if (sh.at > kBuffer) lowest_at(s, bound, k, sh);
-    const int at = sh.at;
-    if (t == 0) sh.best_count = min(k, above + at);
-    for (int c = t; c < above + at; c += kThreads) {
+    if (at > kBuffer) at = lowest_at(s, bound, k, sh);
+    if (lane == 0) sh.best_count = min(k, above + at);
+    for (int c = lane; c < above + at; c += 32) {
         const uint32_t key = c < above ? sh.above_key[c] : bound;
         const int index = c < above ? sh.above_index[c] : sh.at_index[c - above];
         int rank = 0;
@@ -515,6 +554,54 @@ __device__ void top_of_slice(const Slice<T>& s, float mine, bool plain, int k, S
             sh.best_key[rank] = key;
             sh.best_index[rank] = index;
         }
+    }
+    __syncwarp();
+}
+
+// the threads' sums joined: every lane gets them
+__device__ __forceinline__ Sums join_row(const Row& r) {
+    const int lane = threadIdx.x & 31;
+    const float4 m4 = reinterpret_cast<const float4*>(r.m)[lane], s4 = reinterpret_cast<const float4*>(r.s)[lane],
+                 a4 = reinterpret_cast<const float4*>(r.a)[lane];
+    const float ms[4] = {m4.x, m4.y, m4.z, m4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w}, as[4] = {a4.x, a4.y, a4.z, a4.w};
+    const uint32_t w = __reduce_max_sync(0xffffffffu, order_key(fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]))));
+    Sums q{key_value(w), 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        Sums x{ms[i], ss[i], as[i]};
+        move_to(x, q.m);
+        q.s += x.s;
+        q.a += x.a;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        q.s += __shfl_xor_sync(0xffffffffu, q.s, d);
+        q.a += __shfl_xor_sync(0xffffffffu, q.a, d);
+    }
+    return q;
+}
+
+// a row's results, by threads t = 0, 1, ... of at least kMaxTop
+template <typename T>
+__device__ __forceinline__ void write_row(const Params& p, int64_t row, const Sums& q, const Shared& sh, int t) {
+    const bool nothing = q.m == -INFINITY && q.s == 0.f;         // every logit is -inf
+    const float log_s = log2f(q.s);
+    const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, extreme(q.m) ? q.m : scaled_max(q.m) * kLn2);
+    if (t < p.top) {
+        const float v = key_value(sh.best_key[t]);
+        if (p.top_logprob) p.top_logprob[row * p.top + t] = nothing ? -INFINITY : v - lse;
+        if (p.top_index) p.top_index[row * p.top + t] = sh.best_index[t];
+    }
+    if (t == 0) {
+        const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
+        const int64_t token = p.tokens[row];
+        float lp;
+        if (token < 0) lp = 0.f;                                 // ignored
+        else if (token >= p.vocab) lp = __uint_as_float(0x7FC00000u);
+        else lp = nothing ? -INFINITY : Num<T>::to_acc(z[token]) - lse;
+        p.logprob[row] = lp;
+        if (p.lse) p.lse[row] = lse;
+        if (p.entropy) p.entropy[row] = nothing ? 0.f : (log_s - q.a / q.s) * kLn2;
     }
 }
 
@@ -531,10 +618,11 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Persistent blocks (a row cut over a cluster: one unit each).  The loading
-// warp copies chunk after chunk of the block's rows into a ring, whatever the
-// consumers are at: while they join a row's sums and look for its largest
-// elements, the next row is on its way.
+// Persistent blocks (a row cut over a cluster: one unit each) of three roles.
+// The loading warp copies chunk after chunk of the block's rows into a ring,
+// whatever the others are at; the consumers sum them up; the finishing warp
+// joins a row's sums and finds its largest elements while the consumers are
+// at the next row.
 template <typename T>
 __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(const Params p) {
     extern __shared__ __align__(128) unsigned char ring[];
@@ -547,9 +635,11 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
             tc::mbar_init(&sh.full[i], 1);
             tc::mbar_init(&sh.empty[i], kWarps);
         }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sh.row_full[i], kWarps);
+            tc::mbar_init(&sh.row_empty[i], 1);
+        }
         sh.abort_flag = 0;
-        sh.bound = 0xFFFFFFFFu;
-        sh.above = sh.at = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -558,6 +648,51 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
     grid_dependency_wait();
     grid_launch_dependents();
 
+    if (t >= kThreads + 32) {
+        // the finishing warp
+        const int lane = t & 31;
+        uint32_t buf = 0, phase = 0;
+        for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+            const int64_t row = u / parts;
+            const int part = (int)(u % parts);       // = the block's rank in its cluster
+            const Slice<T> slice = slice_of(static_cast<const T*>(p.logits) + row * p.pitch, p.vocab, part, parts);
+            const bool ok = tc::mbar_wait(&sh.row_full[buf], phase, abort_flag, p.err);
+            if (ok) {
+                const Sums q = join_row(sh.row[buf]);
+                if (p.top > 0) top_of_slice(slice, sh.row[buf], q.s == q.s, p.top, sh);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh.row_empty[buf]);
+                if (parts == 1) {
+                    write_row<T>(p, row, q, sh, lane);
+                } else {
+                    // every slice's results go to the first block
+                    cluster_wait();                  // all blocks of the cluster run
+                    if (lane == 0) {
+                        give_first(&sh.slice_sums[part].m, __float_as_uint(q.m));
+                        give_first(&sh.slice_sums[part].s, __float_as_uint(q.s));
+                        give_first(&sh.slice_sums[part].a, __float_as_uint(q.a));
+                    }
+                    if (p.top > 0) {
+                        const bool some = lane < sh.best_count;
+                        give_first(&sh.all_key[part * kMaxTop + lane], some ? sh.best_key[lane] : 0u);      // 0: below every element
+                        give_first(&sh.all_index[part * kMaxTop + lane], some ? (uint32_t)sh.best_index[lane] : 0u);
+                    }
+                }
+                __syncwarp();
+            } else if (parts > 1) {
+                cluster_wait();
+            }
+            if (++buf == 2) {
+                buf = 0;
+                phase ^= 1;
+            }
+        }
+        if (parts > 1) {
+            cluster_arrive();
+            cluster_wait();
+        }
+        return;
+    }
     if (t >= kThreads) {
         if (t == kThreads) {
             uint32_t stage = 0, phase = 0, armed = 0, parity = 0;
@@ -599,28 +734,35 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
         return;
     }
 
-    uint32_t stage = 0, phase = 0;
+    uint32_t stage = 0, phase = 0, buf = 0, row_phase = 0;
     const uint32_t none = splat<T>(-INFINITY);
     for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const int64_t row = u / parts;
-        const int part = (int)(u % parts);           // = the block's rank in its cluster
-        const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
-        const Slice<T> slice = slice_of(z, p.vocab, part, parts);
+        const T* z = static_cast<const T*>(p.logits) + u / parts * p.pitch;
+        const Slice<T> slice = slice_of(z, p.vocab, (int)(u % parts), parts);
         Sums q{-INFINITY, 0.f, 0.f};
         if (t < slice.head) take(q, Num<T>::to_acc(z[t]));
         if (slice.tail0 + t < slice.tail1) take(q, Num<T>::to_acc(z[slice.tail0 + t]));
-        for (int v = slice.v0; v < slice.v1; v += kChunk) {
+        const int a_slot = p.top > 0 ? chunks_a_slot(slice) : 0;
+        int left = a_slot, slot = 0;
+        float slot_top = -INFINITY;
+        // the buffer's last row has been finished
+        const bool ok = tc::mbar_wait(&sh.row_empty[buf], row_phase ^ 1, abort_flag, p.err);
+        Row& r = sh.row[buf];
+        for (int v = slice.v0; v < slice.v1 && ok; v += kChunk) {
             if (tc::mbar_wait(&sh.full[stage], phase, abort_flag, p.err)) {
-                const uint4* chunk = reinterpret_cast<const uint4*>(ring + stage * (kChunk * 16));
-                if (v + t < slice.v1) {
-                    // -inf for packs past the slice's end: they weigh nothing
-                    uint4 k[kUnroll];
+                const uint4* chunk = reinterpret_cast<const uint4*>(ring + stage * (kChunk * 16)) + t;
+                const int mine = slice.v1 - v - t;   // this thread's packs: at 0, kThreads, ... below this
+                uint4 k[kUnroll];
+                if (mine > (kUnroll - 1) * kThreads) {
+#pragma unroll
+                    for (int i = 0; i < kUnroll; ++i) k[i] = chunk[i * kThreads];
+                } else {
+                    // -inf past the slice's end: it weighs nothing
 #pragma unroll
                     for (int i = 0; i < kUnroll; ++i)
-                        k[i] = i == 0 || v + t + i * kThreads < slice.v1 ? chunk[t + i * kThreads]
-                                                                         : make_uint4(none, none, none, none);
-                    take<T>(q, k);
+                        k[i] = i * kThreads < mine ? chunk[i * kThreads] : make_uint4(none, none, none, none);
                 }
+                if (mine > 0) slot_top = fmaxf(slot_top, take<T>(q, k));
             }
             __syncwarp();
             if ((t & 31) == 0) tc::mbar_arrive(&sh.empty[stage]);
@@ -628,106 +770,57 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
                 stage = 0;
                 phase ^= 1;
             }
-        }
-        const float mine = q.m;
-        {
-            const uint32_t key = order_key(mine);
-            const uint32_t w = __reduce_max_sync(0xffffffffu, key);
-            if (p.top > 0) {
-                const uint32_t g = max(key, __shfl_xor_sync(0xffffffffu, key, 1));
-                if ((t & 1) == 0) sh.group_max[t >> 1] = g;
-            }
-            if ((t & 31) == 0) sh.warp_max[t >> 5] = key_value(w);
-        }
-        sync();
-        float m = sh.warp_max[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.warp_max[w]);
-        move_to(q, m);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            q.s += __shfl_xor_sync(0xffffffffu, q.s, d);
-            q.a += __shfl_xor_sync(0xffffffffu, q.a, d);
-        }
-        if ((t & 31) == 0) sh.warp_sums[t >> 5] = make_float2(q.s, q.a);
-        sync();
-        q.s = q.a = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            q.s += sh.warp_sums[w].x;
-            q.a += sh.warp_sums[w].y;
-        }
-        if (p.top > 0) {
-            top_of_slice(slice, mine, q.s == q.s, p.top, sh);
-            sync();
-            if (t == 0) {                            // for the block's next row
-                sh.bound = 0xFFFFFFFFu;
-                sh.above = sh.at = 0;
+            if (--left == 0 || (p.top > 0 && v + kChunk >= slice.v1)) {
+                r.slot_max[slot++][t] = slot_top;
+                slot_top = -INFINITY;
+                left = a_slot;
             }
         }
-        if (parts > 1) {
-            // every slice's results go to the first block
-            cluster_wait();                          // all blocks of the cluster run
-            if (t == 0) {
-                give_first(&sh.slice_sums[part].m, __float_as_uint(q.m));
-                give_first(&sh.slice_sums[part].s, __float_as_uint(q.s));
-                give_first(&sh.slice_sums[part].a, __float_as_uint(q.a));
-            }
-            if (t < kMaxTop && p.top > 0) {
-                const bool some = t < sh.best_count;
-                give_first(&sh.all_key[part * kMaxTop + t], some ? sh.best_key[t] : 0u);      // 0: below every element
-                give_first(&sh.all_index[part * kMaxTop + t], some ? (uint32_t)sh.best_index[t] : 0u);
-            }
-            cluster_arrive();
-            cluster_wait();
-            if (part != 0) return;
-            q = sh.slice_sums[0];
-            for (int r = 1; r < parts; ++r) q = join(q, sh.slice_sums[r]);
-            if (p.top > 0) {
-                // an element's rank: its place in its own slice, and in each other slice the elements that go before it
-                const int r = t / kMaxTop, i = t % kMaxTop;
-                if (r < parts && i < p.top) {
-                    const uint32_t key = sh.all_key[t];
-                    const int index = sh.all_index[t];
-                    int rank = i;
-                    for (int o = 0; o < parts; ++o) {
-                        if (o == r) continue;
-                        int n = 0;                   // in order: the count is a place, found by halving
-                        const int b = o * kMaxTop;
-#pragma unroll
-                        for (int step = kMaxTop / 2; step > 0; step >>= 1)
-                            if (n + step <= p.top && better(sh.all_key[b + n + step - 1], sh.all_index[b + n + step - 1], key, index))
-                                n += step;
-                        if (n + 1 <= p.top && better(sh.all_key[b + n], sh.all_index[b + n], key, index)) ++n;
-                        rank += n;
-                    }
-                    if (key != 0 && rank < p.top) {
-                        sh.best_key[rank] = key;
-                        sh.best_index[rank] = index;
-                    }
-                }
-                sync();
-            }
-        }
-        const bool nothing = q.m == -INFINITY && q.s == 0.f;     // every logit is -inf
-        const float log_s = log2f(q.s);
-        const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, extreme(q.m) ? q.m : scaled_max(q.m) * kLn2);
-        if (t < p.top) {
-            const float v = key_value(sh.best_key[t]);
-            if (p.top_logprob) p.top_logprob[row * p.top + t] = nothing ? -INFINITY : v - lse;
-            if (p.top_index) p.top_index[row * p.top + t] = sh.best_index[t];
-        }
-        if (t == 32) {
-            const int64_t token = p.tokens[row];
-            float lp;
-            if (token < 0) lp = 0.f;                             // ignored
-            else if (token >= p.vocab) lp = __uint_as_float(0x7FC00000u);
-            else lp = nothing ? -INFINITY : Num<T>::to_acc(z[token]) - lse;
-            p.logprob[row] = lp;
-            if (p.lse) p.lse[row] = lse;
-            if (p.entropy) p.entropy[row] = nothing ? 0.f : (log_s - q.a / q.s) * kLn2;
+        r.m[t] = q.m;
+        r.s[t] = q.s;
+        r.a[t] = q.a;
+        __syncwarp();
+        if ((t & 31) == 0) tc::mbar_arrive(&sh.row_full[buf]);
+        if (++buf == 2) {
+            buf = 0;
+            row_phase ^= 1;
         }
     }
+    if (parts == 1) return;
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    if (blockIdx.x % parts != 0) return;
+    // the first block's consumers join the slices
+    Sums q = sh.slice_sums[0];
+    for (int r = 1; r < parts; ++r) q = join(q, sh.slice_sums[r]);
+    if (p.top > 0) {
+        // an element's rank: its place in its own slice, and in each other slice the elements that go before it
+        for (int e = t; e < parts * kMaxTop; e += kThreads) {
+            const int r = e / kMaxTop;
+            const uint32_t key = sh.all_key[e];
+            const int index = sh.all_index[e];
+            if (key == 0) continue;
+            int rank = e % kMaxTop;
+            for (int o = 0; o < parts; ++o) {
+                if (o == r) continue;
+                int n = 0;                           // in order: the count is a place, found by halving
+                const int b = o * kMaxTop;
+#pragma unroll
+                for (int step = kMaxTop / 2; step > 0; step >>= 1)
+                    if (n + step <= p.top && better(sh.all_key[b + n + step - 1], sh.all_index[b + n + step - 1], key, index))
+                        n += step;
+                if (n + 1 <= p.top && better(sh.all_key[b + n], sh.all_index[b + n], key, index)) ++n;
+                rank += n;
+            }
+            if (rank < p.top) {
+                sh.best_key[rank] = key;
+                sh.best_index[rank] = index;
+            }
+        }
+        sync();
+    }
+    write_row<T>(p, blockIdx.x / parts, q, sh, t);
 }
 
 // One block takes a stretch of a row.  Every element is read and written by
