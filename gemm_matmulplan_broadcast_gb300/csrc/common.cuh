@@ -220,6 +220,25 @@ __device__ __forceinline__ void fma_f2(unsigned long long& d, unsigned long long
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 
+// The same pairs as values: two float32 lanes in one 64-bit register, one
+// issue slot for both.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // one element through the read-only path (8-bit float elements as bytes)
 template <typename T>
 __device__ __forceinline__ T ldg_elem(const T* p) {

@@ -14,9 +14,10 @@
 // read again, mostly from L2.  All sums and statistics are float32; y, dx,
 // dgamma and dbeta are rounded to the element type once.
 #include <new>
+#include <type_traits>
 
-#include "common.cuh"
 #include "plan_state.h"
+#include "tc_ptx.cuh"
 
 namespace olc {
 namespace norm {
@@ -32,6 +33,7 @@ struct FwdParams {
     int64_t rows, cols;
     float eps;
     float inv_cols;
+    unsigned int* err;
 };
 
 struct BwdParams {
@@ -46,26 +48,101 @@ struct BwdParams {
     int64_t rows, cols;
     float inv_cols;
     int threads_per_row;
+    unsigned int* err;
 };
 
-// V elements of T in one access (V = 1: any alignment; else 16 bytes)
+// V elements of T in one access (V = 1: any alignment; else 16 bytes), and
+// the same as pairs of float32 (V = 1: the second of the pair is not used).
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
     T v[V];
 };
-
-template <typename T, int V>
-__device__ __forceinline__ void load(float (&out)[V], const T* p) {
-    const Pack<T, V> k = *reinterpret_cast<const Pack<T, V>*>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = Num<T>::to_acc(k.v[i]);
+template <int V>
+constexpr int pairs() {
+    return V == 1 ? 1 : V / 2;
 }
 template <typename T, int V>
-__device__ __forceinline__ void store(T* p, const float (&in)[V]) {
+__device__ __forceinline__ Pack<T, V> load(const void* p) {
+    return *static_cast<const Pack<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void widen(F2 (&out)[pairs<V>()], const Pack<T, V>& k) {
+    if constexpr (V == 1) {
+        out[0] = pack_f2(Num<T>::to_acc(k.v[0]), 0.f);
+    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&k);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+            out[i] = pack_f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) out[i] = pack_f2(Num<T>::to_acc(k.v[2 * i]), Num<T>::to_acc(k.v[2 * i + 1]));
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const F2 (&in)[pairs<V>()]) {
     Pack<T, V> k;
 #pragma unroll
-    for (int i = 0; i < V; ++i) k.v[i] = Num<T>::from_acc(in[i]);
+    for (int i = 0; i < pairs<V>(); ++i) {
+        float lo, hi;
+        unpack_f2(in[i], lo, hi);
+        if constexpr (V == 1) {
+            k.v[0] = Num<T>::from_acc(lo);
+        } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+            reinterpret_cast<__nv_bfloat162*>(&k)[i] = __floats2bfloat162_rn(lo, hi);
+        } else if constexpr (std::is_same_v<T, __half>) {
+            reinterpret_cast<__half2*>(&k)[i] = __floats2half2_rn(lo, hi);
+        } else {
+            k.v[2 * i] = lo;
+            k.v[2 * i + 1] = hi;
+        }
+    }
     *reinterpret_cast<Pack<T, V>*>(p) = k;
+}
+template <int V>
+__device__ __forceinline__ float sum_of(F2 x) {
+    float lo, hi;
+    unpack_f2(x, lo, hi);
+    return V == 1 ? lo : lo + hi;
+}
+__device__ __forceinline__ F2 both(float v) { return pack_f2(v, v); }
+
+// y = (x - mean) rstd gamma + beta on one pack
+template <typename T, int V>
+__device__ __forceinline__ void finish(T* y, const Pack<T, V>& k, F2 minus_mean, F2 rstd, const T* gamma,
+                                       const T* beta) {
+    F2 x[pairs<V>()], w[pairs<V>()];
+    widen<T, V>(x, k);
+#pragma unroll
+    for (int i = 0; i < pairs<V>(); ++i) x[i] = mul2(add2(x[i], minus_mean), rstd);
+    if (gamma) {
+        widen<T, V>(w, load<T, V>(gamma));
+#pragma unroll
+        for (int i = 0; i < pairs<V>(); ++i) x[i] = mul2(x[i], w[i]);
+    }
+    if (beta) {
+        widen<T, V>(w, load<T, V>(beta));
+#pragma unroll
+        for (int i = 0; i < pairs<V>(); ++i) x[i] = add2(x[i], w[i]);
+    }
+    store<T, V>(y, x);
+}
+template <typename T, int V>
+__device__ __forceinline__ void add_elements(F2& s, const Pack<T, V>& k) {
+    F2 x[pairs<V>()];
+    widen<T, V>(x, k);
+#pragma unroll
+    for (int i = 0; i < pairs<V>(); ++i) s = add2(s, x[i]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void add_squares(F2& s, const Pack<T, V>& k, F2 minus_mean) {
+    F2 x[pairs<V>()];
+    widen<T, V>(x, k);
+#pragma unroll
+    for (int i = 0; i < pairs<V>(); ++i) {
+        const F2 d = add2(x[i], minus_mean);
+        s = fma2(d, d, s);
+    }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -106,27 +183,18 @@ forward_kernel(const FwdParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * W * 32) * V;
-        if (c < cols) k[i] = *reinterpret_cast<const Pack<T, V>*>(x + c);
+        if (c < cols) k[i] = load<T, V>(x + c);
     }
-    float s = 0.f;
+    F2 s = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if ((t + i * W * 32) * V < cols) {
-#pragma unroll
-            for (int q = 0; q < V; ++q) s += Num<T>::to_acc(k[i].v[q]);
-        }
-    const float mean = block_sum<W>(s, slots[0]) * p.inv_cols;
-    s = 0.f;
+        if ((t + i * W * 32) * V < cols) add_elements<T, V>(s, k[i]);
+    const float mean = block_sum<W>(sum_of<V>(s), slots[0]) * p.inv_cols;
+    s = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if ((t + i * W * 32) * V < cols) {
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float d = Num<T>::to_acc(k[i].v[q]) - mean;
-                s = fmaf(d, d, s);
-            }
-        }
-    const float rstd = 1.0f / sqrtf(fmaf(block_sum<W>(s, slots[1]), p.inv_cols, p.eps));
+        if ((t + i * W * 32) * V < cols) add_squares<T, V>(s, k[i], both(-mean));
+    const float rstd = 1.0f / sqrtf(fmaf(block_sum<W>(sum_of<V>(s), slots[1]), p.inv_cols, p.eps));
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -136,17 +204,102 @@ forward_kernel(const FwdParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * W * 32) * V;
-        if (c >= cols) continue;
-        float g[V], b[V], o[V];
-        if (gamma) load<T, V>(g, gamma + c);
-        if (beta) load<T, V>(b, beta + c);
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-            o[q] = (Num<T>::to_acc(k[i].v[q]) - mean) * rstd;
-            if (gamma) o[q] *= g[q];
-            if (beta) o[q] += b[q];
+        if (c < cols)
+            finish<T, V>(y + c, k[i], both(-mean), both(rstd), gamma ? gamma + c : nullptr, beta ? beta + c : nullptr);
+    }
+}
+
+// Many rows of 16-byte packs: persistent warps of a row each.  A warp copies
+// its next rows into its own two buffers of shared memory (one bulk copy a
+// row) while it works on one; gamma and beta sit in shared memory.  Nothing
+// in a row's way waits for another warp.
+constexpr int kRowWarps = 4;
+template <typename T, int NV>
+__global__ void __launch_bounds__(kRowWarps * 32) forward_rows_kernel(const FwdParams p) {
+    constexpr int V = 16 / sizeof(T);
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[kRowWarps][2];
+    __shared__ int abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cols = (int)p.cols;
+    const uint32_t row_bytes = (uint32_t)cols * sizeof(T);
+    T* gamma = reinterpret_cast<T*>(smem);
+    T* beta = reinterpret_cast<T*>(smem + row_bytes);
+    unsigned char* mine = smem + 2 * row_bytes + (size_t)warp * 2 * row_bytes;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRowWarps * 2; ++i) tc::mbar_init(&full[i >> 1][i & 1], 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t step = (int64_t)gridDim.x * kRowWarps;
+    auto fetch = [&](int64_t row, int stage) {       // one lane
+        if (row >= p.rows) return;
+        tc::mbar_arrive_expect_tx(&full[warp][stage], row_bytes);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                tc::smem_u32(mine + (size_t)stage * row_bytes)),
+            "l"(static_cast<const T*>(p.X) + row * p.x_pitch), "r"(row_bytes), "r"(tc::smem_u32(&full[warp][stage]))
+            : "memory");
+    };
+    int64_t row = (int64_t)blockIdx.x * kRowWarps + warp;
+    if (lane == 0) {
+        fetch(row, 0);
+        fetch(row + step, 1);
+    }
+    for (int c = threadIdx.x * V; c < cols; c += kRowWarps * 32 * V) {
+        if (p.gamma) *reinterpret_cast<uint4*>(gamma + c) = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.gamma) + c);
+        if (p.beta) *reinterpret_cast<uint4*>(beta + c) = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.beta) + c);
+    }
+    __syncthreads();
+    if (!p.gamma) gamma = nullptr;
+    if (!p.beta) beta = nullptr;
+    int stage = 0, phase = 0;
+    for (; row < p.rows; row += step) {
+        if (!tc::mbar_wait(&full[warp][stage], phase, &abort_flag, p.err)) {
+            // the copies in flight land before the block's memory goes
+            tc::mbar_wait_drain(&full[warp][stage], phase);
+            if (row + step < p.rows) tc::mbar_wait_drain(&full[warp][stage ^ 1], stage ? phase ^ 1 : phase);
+            break;
         }
-        store<T, V>(y + c, o);
+        const T* x = reinterpret_cast<const T*>(mine + (size_t)stage * row_bytes);
+        Pack<T, V> k[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * 32) * V;
+            if (c < cols) k[i] = load<T, V>(x + c);
+        }
+        __syncwarp();                                // the row is in registers: its buffer takes another
+        if (lane == 0) fetch(row + 2 * step, stage);
+        if (++stage == 2) {
+            stage = 0;
+            phase ^= 1;
+        }
+        F2 s = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((lane + i * 32) * V < cols) add_elements<T, V>(s, k[i]);
+        const float mean = warp_sum(sum_of<V>(s)) * p.inv_cols;
+        s = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((lane + i * 32) * V < cols) add_squares<T, V>(s, k[i], both(-mean));
+        const float rstd = 1.0f / sqrtf(fmaf(warp_sum(sum_of<V>(s)), p.inv_cols, p.eps));
+        if (lane == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        T* y = static_cast<T*>(p.Y) + row * p.y_pitch;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (lane + i * 32) * V;
+            if (c < cols)
+                finish<T, V>(y + c, k[i], both(-mean), both(rstd), gamma ? gamma + c : nullptr,
+                             beta ? beta + c : nullptr);
+        }
     }
 }
 
@@ -156,44 +309,27 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const FwdParams p) {
     __shared__ float slots[2][32];
     grid_dependency_wait();
     grid_launch_dependents();
+    const T* gamma = static_cast<const T*>(p.gamma);
+    const T* beta = static_cast<const T*>(p.beta);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
         T* y = static_cast<T*>(p.Y) + row * p.y_pitch;
-        float s = 0.f;
-        for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
-            float v[V];
-            load<T, V>(v, x + c);
-#pragma unroll
-            for (int q = 0; q < V; ++q) s += v[q];
-        }
-        const float mean = block_sum<32>(s, slots[0]) * p.inv_cols;
-        s = 0.f;
-        for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
-            float v[V];
-            load<T, V>(v, x + c);
-#pragma unroll
-            for (int q = 0; q < V; ++q) s = fmaf(v[q] - mean, v[q] - mean, s);
-        }
-        const float rstd = 1.0f / sqrtf(fmaf(block_sum<32>(s, slots[1]), p.inv_cols, p.eps));
+        F2 s = 0;
+#pragma unroll 4
+        for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) add_elements<T, V>(s, load<T, V>(x + c));
+        const float mean = block_sum<32>(sum_of<V>(s), slots[0]) * p.inv_cols;
+        s = 0;
+#pragma unroll 4
+        for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V)
+            add_squares<T, V>(s, load<T, V>(x + c), both(-mean));
+        const float rstd = 1.0f / sqrtf(fmaf(block_sum<32>(sum_of<V>(s), slots[1]), p.inv_cols, p.eps));
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
-        const T* gamma = static_cast<const T*>(p.gamma);
-        const T* beta = static_cast<const T*>(p.beta);
-        for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
-            float v[V], g[V], b[V];
-            load<T, V>(v, x + c);
-            if (gamma) load<T, V>(g, gamma + c);
-            if (beta) load<T, V>(b, beta + c);
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                v[q] = (v[q] - mean) * rstd;
-                if (gamma) v[q] *= g[q];
-                if (beta) v[q] += b[q];
-            }
-            store<T, V>(y + c, v);
-        }
+        for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V)
+            finish<T, V>(y + c, load<T, V>(x + c), both(-mean), both(rstd), gamma ? gamma + c : nullptr,
+                         beta ? beta + c : nullptr);
     }
 }
 
@@ -201,129 +337,255 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const FwdParams p) {
 // keeps the same NV * V columns of every row its group takes, so that the
 // column sums of dgamma and dbeta stay in its registers until the block's
 // last row; the groups' sums are then added in group order and written as
-// the block's partial sums.  The next row is loaded before this one's
-// reduction.
+// the block's partial sums.
+//
+// One row of a group: dxh and xh of the thread's columns, the two row sums
+// over the group (one block barrier), dx.
+template <typename T, int V, int NV>
+struct RowGrads {
+    F2 ag[NV][pairs<V>()], ab[NV][pairs<V>()];      // column sums of dy xh and dy
+    F2 xh[NV][pairs<V>()], dxh[NV][pairs<V>()];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < pairs<V>(); ++q) ag[i][q] = ab[i][q] = 0;
+    }
+    // packs past the row's end, and rows past the last one, have dy = 0 and
+    // add nothing
+    __device__ __forceinline__ float2 take(int i, const Pack<T, V>& x, const Pack<T, V>& dy, const Pack<T, V>& gamma,
+                                           bool has_gamma, F2 minus_mean, F2 rstd) {
+        F2 d[pairs<V>()], g[pairs<V>()], c1 = 0, c2 = 0;
+        widen<T, V>(xh[i], x);
+        widen<T, V>(d, dy);
+        if (has_gamma) widen<T, V>(g, gamma);
+#pragma unroll
+        for (int q = 0; q < pairs<V>(); ++q) {
+            xh[i][q] = mul2(add2(xh[i][q], minus_mean), rstd);
+            ag[i][q] = fma2(d[q], xh[i][q], ag[i][q]);
+            ab[i][q] = add2(ab[i][q], d[q]);
+            dxh[i][q] = has_gamma ? mul2(d[q], g[q]) : d[q];
+            c1 = add2(c1, dxh[i][q]);
+            c2 = fma2(dxh[i][q], xh[i][q], c2);
+        }
+        return make_float2(sum_of<V>(c1), sum_of<V>(c2));
+    }
+    // rstd (dxh - c1 - xh c2)
+    __device__ __forceinline__ void put(int i, T* dx, float c1, float c2, F2 rstd) const {
+        F2 o[pairs<V>()];
+#pragma unroll
+        for (int q = 0; q < pairs<V>(); ++q)
+            o[q] = mul2(add2(fma2(xh[i][q], both(-c2), dxh[i][q]), both(-c1)), rstd);
+        store<T, V>(dx, o);
+    }
+    // the block's partial sums; `shared`: groups x cols floats (groups > 1)
+    __device__ __forceinline__ void leave(float* out, float* shared, int cols, int grp, int groups, int t, int tpr) const {
+        for (int which = 0; which < 2; ++which) {
+            if (groups > 1) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (t + i * tpr) * V;
+                if (c >= cols) continue;
+                float* to = groups > 1 ? shared + grp * cols + c : out + which * cols + c;
+#pragma unroll
+                for (int q = 0; q < pairs<V>(); ++q) {
+                    float lo, hi;
+                    unpack_f2(which ? ab[i][q] : ag[i][q], lo, hi);
+                    to[2 * q] = lo;
+                    if (V > 1) to[2 * q + 1] = hi;
+                }
+            }
+            if (groups == 1) continue;
+            __syncthreads();
+            for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+                float s = 0.f;
+                for (int g = 0; g < groups; ++g) s += shared[g * cols + c];
+                out[which * cols + c] = s;
+            }
+        }
+    }
+};
+
+// the group's sums of (c1, c2), by one block barrier; slots alternate
+__device__ __forceinline__ float2 group_sum(float2 c, float2 (*slots)[32], int buf, int grp, int warps, float scale) {
+    c.x = warp_sum(c.x);
+    c.y = warp_sum(c.y);
+    if (warps > 1) {
+        if ((threadIdx.x & 31) == 0) slots[buf][threadIdx.x >> 5] = c;
+        __syncthreads();
+        c = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+            const float2 v = slots[buf][grp * warps + w];
+            c.x += v.x;
+            c.y += v.y;
+        }
+    }
+    return make_float2(c.x * scale, c.y * scale);
+}
+
+// Any alignment: the next row is loaded into registers before this one's sums.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(1024) backward_kernel(const BwdParams p) {
-    extern __shared__ float shared[];           // group sums: [groups][cols] x 2, one after the other
+    extern __shared__ float shared[];
     __shared__ float2 slots[2][32];
     const int tpr = p.threads_per_row;
     const int groups = blockDim.x / tpr;
     const int grp = threadIdx.x / tpr, t = threadIdx.x % tpr;
-    const int warps = tpr >> 5;
     const int cols = (int)p.cols;
-    const bool weights = p.partial != nullptr;
     const bool has_gamma = p.gamma != nullptr;
     grid_dependency_wait();
     grid_launch_dependents();
     Pack<T, V> kx[NV], kd[NV], kg[NV];
-    float ag[NV][V], ab[NV][V];
+    RowGrads<T, V, NV> r;
+    r.clear();
+    const Pack<T, V> zero{};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * tpr) * V;
-        if (has_gamma && c < cols) kg[i] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(p.gamma) + c);
-#pragma unroll
-        for (int q = 0; q < V; ++q) ag[i][q] = ab[i][q] = 0.f;
+        kg[i] = has_gamma && c < cols ? load<T, V>(static_cast<const T*>(p.gamma) + c) : zero;
     }
     const int64_t step = (int64_t)gridDim.x * groups;
+    float mean = 0.f, rstd = 0.f;
     auto fetch = [&](int64_t row) {
-        if (row >= p.rows) return;
+        const bool live = row < p.rows;
         const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
         const T* dy = static_cast<const T*>(p.dY) + row * p.dy_pitch;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * tpr) * V;
-            if (c < cols) {
-                kx[i] = *reinterpret_cast<const Pack<T, V>*>(x + c);
-                kd[i] = *reinterpret_cast<const Pack<T, V>*>(dy + c);
-            }
+            kx[i] = live && c < cols ? load<T, V>(x + c) : zero;
+            kd[i] = live && c < cols ? load<T, V>(dy + c) : zero;
         }
+        mean = live ? p.mean[row] : 0.f;
+        rstd = live ? p.rstd[row] : 0.f;
     };
     int64_t row = (int64_t)blockIdx.x * groups + grp;
     fetch(row);
     int buf = 0;
     // every group runs the same number of turns (the block's barriers)
     for (int64_t first = (int64_t)blockIdx.x * groups; first < p.rows; first += step, row += step, buf ^= 1) {
-        const bool live = row < p.rows;
-        const float mean = live ? p.mean[row] : 0.f, rstd = live ? p.rstd[row] : 0.f;
-        float xh[NV][V], dxh[NV][V];
-        float c1 = 0.f, c2 = 0.f;
+        const F2 scale = both(rstd);
+        float2 c = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = live && (t + i * tpr) * V < cols;
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float d = in ? Num<T>::to_acc(kd[i].v[q]) : 0.f;
-                xh[i][q] = in ? (Num<T>::to_acc(kx[i].v[q]) - mean) * rstd : 0.f;
-                if (weights) {
-                    ag[i][q] = fmaf(d, xh[i][q], ag[i][q]);
-                    ab[i][q] += d;
-                }
-                dxh[i][q] = has_gamma && in ? d * Num<T>::to_acc(kg[i].v[q]) : d;
-                c1 += dxh[i][q];
-                c2 = fmaf(dxh[i][q], xh[i][q], c2);
-            }
+            const float2 v = r.take(i, kx[i], kd[i], kg[i], has_gamma, both(-mean), scale);
+            // a pack past the row's end has xh <> 0 but dy = 0: its sums are 0
+            c.x += v.x;
+            c.y += v.y;
         }
         fetch(row + step);
         if (!p.dX) continue;                      // uniform over the grid
-        c1 = warp_sum(c1);
-        c2 = warp_sum(c2);
-        if (warps > 1) {
-            if ((threadIdx.x & 31) == 0) slots[buf][threadIdx.x >> 5] = make_float2(c1, c2);
-            __syncthreads();
-            c1 = c2 = 0.f;
-            for (int w = 0; w < warps; ++w) {
-                const float2 v = slots[buf][grp * warps + w];
-                c1 += v.x;
-                c2 += v.y;
-            }
-        }
-        c1 *= p.inv_cols;
-        c2 *= p.inv_cols;
-        if (live) {
+        c = group_sum(c, slots, buf, grp, tpr >> 5, p.inv_cols);
+        if (row < p.rows) {
             T* dx = static_cast<T*>(p.dX) + row * p.dx_pitch;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (t + i * tpr) * V;
-                if (c >= cols) continue;
-                float o[V];
-#pragma unroll
-                for (int q = 0; q < V; ++q) o[q] = rstd * (dxh[i][q] - c1 - xh[i][q] * c2);
-                store<T, V>(dx + c, o);
+                const int at = (t + i * tpr) * V;
+                if (at < cols) r.put(i, dx + at, c.x, c.y, scale);
             }
         }
     }
-    if (!weights) return;
-    float* out = p.partial + (int64_t)blockIdx.x * 2 * cols;
-    if (groups == 1) {
+    if (p.partial) r.leave(p.partial + (int64_t)blockIdx.x * 2 * cols, shared, cols, grp, groups, t, tpr);
+}
+
+// Rows of 16-byte packs: one row a block at a time, x and dy copied ahead into
+// a ring of kAhead rows by bulk copies.  The barrier of the row's sums also
+// tells that every thread has read the row: its buffer takes another.
+constexpr int kAhead = 3;
+template <typename T, int NV>
+__global__ void __launch_bounds__(512) backward_ring_kernel(const BwdParams p) {
+    constexpr int V = 16 / sizeof(T);
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ float2 slots[2][32];
+    __shared__ uint64_t full[kAhead];
+    __shared__ int abort_flag;
+    const int t = threadIdx.x, threads = blockDim.x;
+    const int cols = (int)p.cols;
+    const uint32_t row_bytes = (uint32_t)cols * sizeof(T);
+    const bool has_gamma = p.gamma != nullptr;
+    if (t == 0) {
+        for (int i = 0; i < kAhead; ++i) tc::mbar_init(&full[i], 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    auto fetch = [&](int64_t row, int stage) {    // one thread
+        if (row >= p.rows) return;
+        unsigned char* to = ring + (size_t)stage * 2 * row_bytes;
+        tc::mbar_arrive_expect_tx(&full[stage], 2 * row_bytes);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                tc::smem_u32(to)),
+            "l"(static_cast<const T*>(p.X) + row * p.x_pitch), "r"(row_bytes), "r"(tc::smem_u32(&full[stage]))
+            : "memory");
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                tc::smem_u32(to + row_bytes)),
+            "l"(static_cast<const T*>(p.dY) + row * p.dy_pitch), "r"(row_bytes), "r"(tc::smem_u32(&full[stage]))
+            : "memory");
+    };
+    int64_t row = blockIdx.x;
+    if (t == 0)
+        for (int i = 0; i < kAhead; ++i) fetch(row + (int64_t)i * gridDim.x, i);
+    Pack<T, V> kg[NV];
+    RowGrads<T, V, NV> r;
+    r.clear();
+    const Pack<T, V> zero{};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * threads) * V;
+        kg[i] = has_gamma && c < cols ? load<T, V>(static_cast<const T*>(p.gamma) + c) : zero;
+    }
+    int stage = 0, phase = 0, buf = 0;
+    float mean = row < p.rows ? p.mean[row] : 0.f, rstd = row < p.rows ? p.rstd[row] : 0.f;
+    for (; row < p.rows; row += gridDim.x, buf ^= 1) {
+        // a wait that runs out: the row's sums are of what is there, the error word tells
+        tc::mbar_wait(&full[stage], phase, &abort_flag, p.err);
+        const T* x = reinterpret_cast<const T*>(ring + (size_t)stage * 2 * row_bytes);
+        const T* dy = x + cols;
+        const F2 scale = both(rstd), minus_mean = both(-mean);
+        float2 c = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * V;
-            if (c >= cols) continue;
+            const int at = (t + i * threads) * V;
+            const bool in = at < cols;
+            const float2 v = r.take(i, in ? load<T, V>(x + at) : zero, in ? load<T, V>(dy + at) : zero, kg[i], has_gamma,
+                                    minus_mean, scale);
+            c.x += v.x;
+            c.y += v.y;
+        }
+        const int64_t next = row + gridDim.x;
+        mean = next < p.rows ? p.mean[next] : 0.f;
+        rstd = next < p.rows ? p.rstd[next] : 0.f;
+        c = group_sum(c, slots, buf, 0, threads >> 5, p.inv_cols);
+        if (threads == 32) __syncwarp();
+        if (t == 0) fetch(row + (int64_t)kAhead * gridDim.x, stage);
+        if (++stage == kAhead) {
+            stage = 0;
+            phase ^= 1;
+        }
+        if (p.dX) {
+            T* dx = static_cast<T*>(p.dX) + row * p.dx_pitch;
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                out[c + q] = ag[i][q];
-                out[cols + c + q] = ab[i][q];
+            for (int i = 0; i < NV; ++i) {
+                const int at = (t + i * threads) * V;
+                if (at < cols) r.put(i, dx + at, c.x, c.y, scale);
             }
         }
-        return;
     }
-    for (int which = 0; which < 2; ++which) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * V;
-            if (c >= cols) continue;
-#pragma unroll
-            for (int q = 0; q < V; ++q) shared[grp * cols + c + q] = which ? ab[i][q] : ag[i][q];
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
-            float s = 0.f;
-            for (int g = 0; g < groups; ++g) s += shared[g * cols + c];
-            out[which * cols + c] = s;
+    if (t == 0 && abort_flag) {
+        // nothing may land after the block has left: one more wait each for what was asked for
+        for (int i = 0; i < kAhead; ++i) {
+            tc::mbar_wait_drain(&full[i], 0);
+            tc::mbar_wait_drain(&full[i], 1);
         }
     }
+    if (p.partial) r.leave(p.partial + (int64_t)blockIdx.x * 2 * cols, nullptr, cols, 0, 1, t, threads);
 }
 
 // Rows wider than a block's registers hold: dx alone, two passes over the row.
@@ -338,32 +600,23 @@ __global__ void __launch_bounds__(1024) backward_long_rows_kernel(const BwdParam
         const T* dy = static_cast<const T*>(p.dY) + row * p.dy_pitch;
         T* dx = static_cast<T*>(p.dX) + row * p.dx_pitch;
         const float mean = p.mean[row], rstd = p.rstd[row];
+        const F2 scale = both(rstd), minus_mean = both(-mean);
+        RowGrads<T, V, 1> r;
+        r.clear();
+        const Pack<T, V> zero{};
         float c1 = 0.f, c2 = 0.f;
         for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
-            float a[V], d[V], g[V];
-            load<T, V>(a, x + c);
-            load<T, V>(d, dy + c);
-            if (gamma) load<T, V>(g, gamma + c);
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float dxh = gamma ? d[q] * g[q] : d[q];
-                c1 += dxh;
-                c2 = fmaf(dxh, (a[q] - mean) * rstd, c2);
-            }
+            const float2 v = r.take(0, load<T, V>(x + c), load<T, V>(dy + c), gamma ? load<T, V>(gamma + c) : zero,
+                                    gamma != nullptr, minus_mean, scale);
+            c1 += v.x;
+            c2 += v.y;
         }
         c1 = block_sum<32>(c1, slots[0]) * p.inv_cols;
         c2 = block_sum<32>(c2, slots[1]) * p.inv_cols;
         for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
-            float a[V], d[V], g[V];
-            load<T, V>(a, x + c);
-            load<T, V>(d, dy + c);
-            if (gamma) load<T, V>(g, gamma + c);
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float dxh = gamma ? d[q] * g[q] : d[q];
-                a[q] = rstd * (dxh - c1 - (a[q] - mean) * rstd * c2);
-            }
-            store<T, V>(dx + c, a);
+            r.take(0, load<T, V>(x + c), load<T, V>(dy + c), gamma ? load<T, V>(gamma + c) : zero, gamma != nullptr,
+                   minus_mean, scale);
+            r.put(0, dx + c, c1, c2, scale);
         }
     }
 }
@@ -388,12 +641,12 @@ __global__ void __launch_bounds__(256) backward_long_cols_kernel(const BwdParams
     p.partial[((int64_t)blockIdx.y * 2 + 1) * p.cols + c] = b;
 }
 
-// Column sums over the blocks' partial sums, in block order within each of
-// eight threads' shares and then in share order: the same for every run.
+// Column sums over the blocks' partial sums, in block order within each of 32
+// shares and then in share order: the same for every run.
 template <typename T>
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ partial, int blocks, int64_t cols,
-                                                         T* dgamma, T* dbeta) {
-    __shared__ float sums[8][33];
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int blocks, int64_t cols,
+                                                          T* dgamma, T* dbeta) {
+    __shared__ float sums[32][33];
     grid_dependency_wait();
     grid_launch_dependents();
     T* out = blockIdx.y ? dbeta : dgamma;
@@ -401,16 +654,16 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
     const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (c < cols)
-        for (int b = share; b < blocks; b += 8) s += partial[((int64_t)b * 2 + blockIdx.y) * cols + c];
+    if (c < cols) {
+#pragma unroll 10
+        for (int b = share; b < blocks; b += 32) s += partial[((int64_t)b * 2 + blockIdx.y) * cols + c];
+    }
     sums[share][lane] = s;
     __syncthreads();
-    if (share == 0 && c < cols) {
-        s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += sums[i][lane];
-        out[c] = Num<T>::from_acc(s);
-    }
+    // a warp a column: its 32 shares
+    s = warp_sum(sums[lane][share]);
+    const int64_t mine = (int64_t)blockIdx.x * 32 + share;
+    if (lane == 0 && mine < cols) out[mine] = Num<T>::from_acc(s);
 }
 
 // ---- host side -------------------------------------------------------------
@@ -425,13 +678,29 @@ olc_status by_type(olc_dtype dt, F&& f) {
     }
 }
 
+template <typename T, int NV>
+cudaError_t forward_rows(const FwdParams& p, int sm_count, cudaStream_t s) {
+    const int smem = (2 + 2 * kRowWarps) * (int)(p.cols * sizeof(T));
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(forward_rows_kernel<T, NV>), smem);
+    if (e != cudaSuccess) return e;
+    const int per_sm = (int)min64(8, (220 * 1024) / (smem + 1024));
+    const int64_t grid = min64(ceil_div(p.rows, kRowWarps), (int64_t)sm_count * per_sm);
+    return launch_pdl(forward_rows_kernel<T, NV>, dim3((unsigned)grid), dim3(kRowWarps * 32), (size_t)smem, s, p);
+}
+
 template <typename T, int V>
 cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     const int64_t packs = ceil_div(p.cols, V);
-    // one warp on a row while the row fits 16 packs a lane: no block barrier
-    // on the way.  Where such warps would leave SMs idle, and for longer
-    // rows, eight or 32 warps share a row.
-    const bool few = p.rows < 4 * (int64_t)sm_count;
+    if constexpr (V > 1) {
+        // enough rows for persistent warps to take several each
+        if (packs >= 64 && packs <= 512 && p.rows >= 16 * (int64_t)sm_count) {
+            if (packs <= 128) return forward_rows<T, 4>(p, sm_count, s);
+            if (packs <= 256) return forward_rows<T, 8>(p, sm_count, s);
+            return forward_rows<T, 16>(p, sm_count, s);
+        }
+    }
+    // one warp on a row while the row fits 4 packs a lane: no block barrier
+    // on the way; eight or 32 warps share longer rows
 #define OLC_FWD(W, NV)                                                                                       \
     return launch_pdl(forward_kernel<T, V, W, NV>, dim3((unsigned)(W == 1 ? ceil_div(p.rows, 4) : p.rows)),  \
                       dim3(W == 1 ? 128 : W * 32), 0, s, p)
@@ -439,8 +708,7 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
         if (packs <= 32) OLC_FWD(1, 1);
         if (packs <= 64) OLC_FWD(1, 2);
         if (packs <= 128) OLC_FWD(1, 4);
-        if (packs <= 256 && !few) OLC_FWD(1, 8);
-        if (packs <= 512 && !few) OLC_FWD(1, 16);
+        if (packs <= 256) OLC_FWD(8, 1);
         if (packs <= 512) OLC_FWD(8, 2);
         if (packs <= 1024) OLC_FWD(8, 4);
         if (packs <= 2048) OLC_FWD(8, 8);
@@ -459,6 +727,7 @@ struct BwdShape {
     int nv = 0;                          // 0: rows wider than a block's registers
     int tpr = 0, groups = 1, threads = 0;
     int64_t blocks = 0;
+    bool ring = false;
 };
 
 template <int V>
@@ -467,6 +736,16 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
     const int64_t packs = ceil_div(cols, V);
     if (packs > 1024 * (kColsPerThread / V)) {
         b.blocks = min64(max64(rows / 64, 1), max64(1, 8 * (int64_t)sm_count * 256 / cols));
+        return b;
+    }
+    // whole rows of 16-byte packs through the ring: 16 columns a thread, two
+    // blocks on an SM
+    const int64_t ring_threads = ceil_div(ceil_div(packs * V, kColsPerThread), 32) * 32;
+    if (V > 1 && packs >= 128 && ring_threads <= 512 && rows >= 4 * (int64_t)sm_count) {
+        b.ring = true;
+        b.nv = kColsPerThread / V;
+        b.tpr = b.threads = (int)ring_threads;
+        b.blocks = min64(rows, (int64_t)sm_count * 2);
         return b;
     }
     b.nv = 1;
@@ -498,6 +777,14 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
         if (e == cudaSuccess && p.dX)
             e = launch_pdl(backward_long_rows_kernel<T, V>, dim3((unsigned)min64(p.rows, (int64_t)sm_count * 2)),
                            dim3(1024), 0, s, p);
+    } else if (b.ring) {
+        if constexpr (V > 1) {
+            auto* kernel = backward_ring_kernel<T, kColsPerThread / V>;
+            const int smem = kAhead * 2 * (int)(p.cols * sizeof(T));
+            e = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+            if (e == cudaSuccess)
+                e = launch_pdl(kernel, dim3((unsigned)b.blocks), dim3((unsigned)b.threads), (size_t)smem, s, p);
+        }
     } else if (b.nv == 1) {
         e = backward_rows<T, V, 1>(p, b, s);
     } else if (b.nv == 2) {
@@ -510,7 +797,7 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
         if constexpr (V == 1) e = backward_rows<T, V, 16>(p, b, s);
     }
     if (e == cudaSuccess && p.partial)
-        e = launch_pdl(column_sum_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32), 2), dim3(256), 0, s,
+        e = launch_pdl(column_sum_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32), 2), dim3(1024), 0, s,
                        (const float*)p.partial, (int)b.blocks, p.cols, dgamma, dbeta);
     return e;
 }
@@ -571,7 +858,7 @@ olc_status olc_layer_norm_forward(olc_layer_norm_plan* plan, const void* X, int6
     const olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
     norm::FwdParams p{X, gamma, beta, Y, mean, rstd, x_pitch, y_pitch, plan->rows, plan->cols, plan->eps,
-                      (float)(1.0 / (double)plan->cols)};
+                      (float)(1.0 / (double)plan->cols), device_error_word()};
     // 16-byte packs need every row of every operand on a 16-byte boundary
     const bool wide = plan->cols * eb % 16 == 0 && plan_aligned16(X) && plan_aligned16(Y) && plan_aligned16(gamma) &&
                       plan_aligned16(beta) && (plan->rows == 1 || (x_pitch * eb % 16 == 0 && y_pitch * eb % 16 == 0));
@@ -611,7 +898,7 @@ olc_status olc_layer_norm_backward(olc_layer_norm_plan* plan, const void* dY, in
                       (rows == 1 || (x_pitch * eb % 16 == 0 && dy_pitch * eb % 16 == 0 &&
                                      (!dX || dx_pitch * eb % 16 == 0)));
     norm::BwdParams p{dY, X, gamma, mean, rstd, dX, nullptr, dy_pitch, x_pitch, dx_pitch, rows, cols,
-                      (float)(1.0 / (double)cols), 0};
+                      (float)(1.0 / (double)cols), 0, device_error_word()};
     const bool weights = dgamma || dbeta;
     if (weights) {
         // both layouts' partial sums fit: a call with other alignment does
