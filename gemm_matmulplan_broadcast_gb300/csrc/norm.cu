@@ -209,25 +209,26 @@ forward_kernel(const FwdParams p) {
     }
 }
 
-// Many rows of 16-byte packs: persistent warps of a row each.  A warp copies
-// its next rows into its own two buffers of shared memory (one bulk copy a
-// row) while it works on one; gamma and beta sit in shared memory.  Nothing
-// in a row's way waits for another warp.
-constexpr int kRowWarps = 4;
-template <typename T, int NV>
-__global__ void __launch_bounds__(kRowWarps * 32) forward_rows_kernel(const FwdParams p) {
+// Many rows of 16-byte packs: persistent warps of a row each.  A warp takes its
+// row from its buffer of shared memory into registers and lets a bulk copy
+// bring the next one there while it works on this one; gamma and beta sit in
+// shared memory.  Nothing in a row's way waits for another warp.  FULL: every
+// lane has NV packs.
+constexpr int kRowWarps = 8;
+template <typename T, int NV, bool FULL>
+__global__ void __launch_bounds__(kRowWarps * 32, NV == 16 ? 2 : (NV == 8 ? 3 : 4)) forward_rows_kernel(const FwdParams p) {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t full[kRowWarps][2];
+    __shared__ uint64_t full[kRowWarps];
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cols = (int)p.cols;
     const uint32_t row_bytes = (uint32_t)cols * sizeof(T);
     T* gamma = reinterpret_cast<T*>(smem);
     T* beta = reinterpret_cast<T*>(smem + row_bytes);
-    unsigned char* mine = smem + 2 * row_bytes + (size_t)warp * 2 * row_bytes;
+    const T* x = reinterpret_cast<const T*>(smem + (2 + (size_t)warp) * row_bytes);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRowWarps * 2; ++i) tc::mbar_init(&full[i >> 1][i & 1], 1);
+        for (int i = 0; i < kRowWarps; ++i) tc::mbar_init(&full[i], 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -236,20 +237,17 @@ __global__ void __launch_bounds__(kRowWarps * 32) forward_rows_kernel(const FwdP
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t step = (int64_t)gridDim.x * kRowWarps;
-    auto fetch = [&](int64_t row, int stage) {       // one lane
+    auto fetch = [&](int64_t row) {                  // one lane
         if (row >= p.rows) return;
-        tc::mbar_arrive_expect_tx(&full[warp][stage], row_bytes);
+        tc::mbar_arrive_expect_tx(&full[warp], row_bytes);
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                tc::smem_u32(mine + (size_t)stage * row_bytes)),
-            "l"(static_cast<const T*>(p.X) + row * p.x_pitch), "r"(row_bytes), "r"(tc::smem_u32(&full[warp][stage]))
+                tc::smem_u32(x)),
+            "l"(static_cast<const T*>(p.X) + row * p.x_pitch), "r"(row_bytes), "r"(tc::smem_u32(&full[warp]))
             : "memory");
     };
     int64_t row = (int64_t)blockIdx.x * kRowWarps + warp;
-    if (lane == 0) {
-        fetch(row, 0);
-        fetch(row + step, 1);
-    }
+    if (lane == 0) fetch(row);
     for (int c = threadIdx.x * V; c < cols; c += kRowWarps * 32 * V) {
         if (p.gamma) *reinterpret_cast<uint4*>(gamma + c) = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.gamma) + c);
         if (p.beta) *reinterpret_cast<uint4*>(beta + c) = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.beta) + c);
@@ -257,36 +255,30 @@ __global__ void __launch_bounds__(kRowWarps * 32) forward_rows_kernel(const FwdP
     __syncthreads();
     if (!p.gamma) gamma = nullptr;
     if (!p.beta) beta = nullptr;
-    int stage = 0, phase = 0;
+    int phase = 0;
     for (; row < p.rows; row += step) {
-        if (!tc::mbar_wait(&full[warp][stage], phase, &abort_flag, p.err)) {
-            // the copies in flight land before the block's memory goes
-            tc::mbar_wait_drain(&full[warp][stage], phase);
-            if (row + step < p.rows) tc::mbar_wait_drain(&full[warp][stage ^ 1], stage ? phase ^ 1 : phase);
+        if (!tc::mbar_wait(&full[warp], phase, &abort_flag, p.err)) {
+            tc::mbar_wait_drain(&full[warp], phase);     // the copy in flight lands before the block's memory goes
             break;
         }
-        const T* x = reinterpret_cast<const T*>(mine + (size_t)stage * row_bytes);
+        phase ^= 1;
         Pack<T, V> k[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + i * 32) * V;
-            if (c < cols) k[i] = load<T, V>(x + c);
+            if (FULL || c < cols) k[i] = load<T, V>(x + c);
         }
         __syncwarp();                                // the row is in registers: its buffer takes another
-        if (lane == 0) fetch(row + 2 * step, stage);
-        if (++stage == 2) {
-            stage = 0;
-            phase ^= 1;
-        }
+        if (lane == 0) fetch(row + step);
         F2 s = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if ((lane + i * 32) * V < cols) add_elements<T, V>(s, k[i]);
+            if (FULL || (lane + i * 32) * V < cols) add_elements<T, V>(s, k[i]);
         const float mean = warp_sum(sum_of<V>(s)) * p.inv_cols;
         s = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if ((lane + i * 32) * V < cols) add_squares<T, V>(s, k[i], both(-mean));
+            if (FULL || (lane + i * 32) * V < cols) add_squares<T, V>(s, k[i], both(-mean));
         const float rstd = 1.0f / sqrtf(fmaf(warp_sum(sum_of<V>(s)), p.inv_cols, p.eps));
         if (lane == 0) {
             if (p.mean) p.mean[row] = mean;
@@ -296,7 +288,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) forward_rows_kernel(const FwdP
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (lane + i * 32) * V;
-            if (c < cols)
+            if (FULL || c < cols)
                 finish<T, V>(y + c, k[i], both(-mean), both(rstd), gamma ? gamma + c : nullptr,
                              beta ? beta + c : nullptr);
         }
@@ -337,15 +329,19 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const FwdParams p) {
 // keeps the same NV * V columns of every row its group takes, so that the
 // column sums of dgamma and dbeta stay in its registers until the block's
 // last row; the groups' sums are then added in group order and written as
-// the block's partial sums.
-//
-// One row of a group: dxh and xh of the thread's columns, the two row sums
-// over the group (one block barrier), dx.
+// the block's partial sums.  A row is three steps: xh and dxh of the thread's
+// columns, the two row sums over the group (one block barrier), dx.
 template <typename T, int V, int NV>
 struct RowGrads {
     F2 ag[NV][pairs<V>()], ab[NV][pairs<V>()];      // column sums of dy xh and dy
     F2 xh[NV][pairs<V>()], dxh[NV][pairs<V>()];
+    F2 g[NV][pairs<V>()];                           // gamma, or ones
 
+    __device__ __forceinline__ void weights(int i, const T* gamma) {
+        if (gamma) widen<T, V>(g[i], load<T, V>(gamma));
+        else
+            for (int q = 0; q < pairs<V>(); ++q) g[i][q] = both(1.f);
+    }
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -354,109 +350,127 @@ struct RowGrads {
     }
     // packs past the row's end, and rows past the last one, have dy = 0 and
     // add nothing
-    __device__ __forceinline__ float2 take(int i, const Pack<T, V>& x, const Pack<T, V>& dy, const Pack<T, V>& gamma,
-                                           bool has_gamma, F2 minus_mean, F2 rstd) {
-        F2 d[pairs<V>()], g[pairs<V>()], c1 = 0, c2 = 0;
+    __device__ __forceinline__ void take(int i, const Pack<T, V>& x, const Pack<T, V>& dy, F2 minus_mean, F2 rstd,
+                                         F2& c1, F2& c2) {
+        F2 d[pairs<V>()];
         widen<T, V>(xh[i], x);
         widen<T, V>(d, dy);
-        if (has_gamma) widen<T, V>(g, gamma);
 #pragma unroll
         for (int q = 0; q < pairs<V>(); ++q) {
             xh[i][q] = mul2(add2(xh[i][q], minus_mean), rstd);
             ag[i][q] = fma2(d[q], xh[i][q], ag[i][q]);
             ab[i][q] = add2(ab[i][q], d[q]);
-            dxh[i][q] = has_gamma ? mul2(d[q], g[q]) : d[q];
+            dxh[i][q] = mul2(d[q], g[i][q]);
             c1 = add2(c1, dxh[i][q]);
             c2 = fma2(dxh[i][q], xh[i][q], c2);
         }
-        return make_float2(sum_of<V>(c1), sum_of<V>(c2));
     }
     // rstd (dxh - c1 - xh c2)
-    __device__ __forceinline__ void put(int i, T* dx, float c1, float c2, F2 rstd) const {
+    __device__ __forceinline__ void put(int i, T* dx, F2 minus_c1, F2 minus_c2, F2 rstd) const {
         F2 o[pairs<V>()];
 #pragma unroll
         for (int q = 0; q < pairs<V>(); ++q)
-            o[q] = mul2(add2(fma2(xh[i][q], both(-c2), dxh[i][q]), both(-c1)), rstd);
+            o[q] = mul2(add2(fma2(xh[i][q], minus_c2, dxh[i][q]), minus_c1), rstd);
         store<T, V>(dx, o);
     }
-    // the block's partial sums; `shared`: groups x cols floats (groups > 1)
-    __device__ __forceinline__ void leave(float* out, float* shared, int cols, int grp, int groups, int t, int tpr) const {
-        for (int which = 0; which < 2; ++which) {
-            if (groups > 1) __syncthreads();
+    // the block's partial sums
+    __device__ __forceinline__ void leave(float* out, int cols, int t, int threads) const {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (t + i * tpr) * V;
-                if (c >= cols) continue;
-                float* to = groups > 1 ? shared + grp * cols + c : out + which * cols + c;
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * threads) * V;
+            if (c >= cols) continue;
 #pragma unroll
-                for (int q = 0; q < pairs<V>(); ++q) {
-                    float lo, hi;
-                    unpack_f2(which ? ab[i][q] : ag[i][q], lo, hi);
-                    to[2 * q] = lo;
-                    if (V > 1) to[2 * q + 1] = hi;
-                }
-            }
-            if (groups == 1) continue;
-            __syncthreads();
-            for (int c = threadIdx.x; c < cols; c += blockDim.x) {
-                float s = 0.f;
-                for (int g = 0; g < groups; ++g) s += shared[g * cols + c];
-                out[which * cols + c] = s;
+            for (int q = 0; q < pairs<V>(); ++q) {
+                *reinterpret_cast<F2*>(out + c + 2 * q) = ag[i][q];
+                *reinterpret_cast<F2*>(out + cols + c + 2 * q) = ab[i][q];
             }
         }
     }
 };
 
-// the group's sums of (c1, c2), by one block barrier; slots alternate
-__device__ __forceinline__ float2 group_sum(float2 c, float2 (*slots)[32], int buf, int grp, int warps, float scale) {
-    c.x = warp_sum(c.x);
-    c.y = warp_sum(c.y);
-    if (warps > 1) {
-        if ((threadIdx.x & 31) == 0) slots[buf][threadIdx.x >> 5] = c;
-        __syncthreads();
-        c = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int w = 0; w < warps; ++w) {
-            const float2 v = slots[buf][grp * warps + w];
-            c.x += v.x;
-            c.y += v.y;
-        }
+// the sum of a block's slots (those of absent warps hold 0)
+template <int WARPS>
+__device__ __forceinline__ float2 sum_slots(const float2* slots) {
+    F2 s = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; w += 2) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(slots + w);
+        s = add2(add2(s, v.x), v.y);
     }
-    return make_float2(c.x * scale, c.y * scale);
+    float2 c;
+    unpack_f2(s, c.x, c.y);
+    return c;
 }
 
-// Any alignment: the next row is loaded into registers before this one's sums.
+// A thread's columns in backward_kernel: NV packs of V at (t + i tpr) V, or,
+// for rows of any alignment (V = 1), NV pairs of single elements tpr apart.
+template <typename T, int V>
+struct Columns {
+    static constexpr int PER = V == 1 ? 2 : V;      // columns of one i
+    static constexpr int P = PER / 2;
+    struct Raw {
+        T v[PER];
+    };
+    static __device__ __forceinline__ int at(int t, int i, int q, int tpr) {
+        return V == 1 ? t + (2 * i + q) * tpr : (t + i * tpr) * V + q;
+    }
+    static __device__ __forceinline__ Raw read(const T* row, int t, int i, int tpr, int cols, bool live) {
+        Raw r{};
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (live && at(t, i, q, tpr) < cols) r.v[q] = row[at(t, i, q, tpr)];
+        } else {
+            if (live && at(t, i, 0, tpr) < cols) {
+                const Pack<T, V> k = load<T, V>(row + at(t, i, 0, tpr));
+#pragma unroll
+                for (int q = 0; q < V; ++q) r.v[q] = k.v[q];
+            }
+        }
+        return r;
+    }
+    static __device__ __forceinline__ void pairs_of(F2 (&out)[P], const Raw& r) {
+#pragma unroll
+        for (int q = 0; q < P; ++q) out[q] = pack_f2(Num<T>::to_acc(r.v[2 * q]), Num<T>::to_acc(r.v[2 * q + 1]));
+    }
+};
+
+// Any alignment and few or short rows: the next row is loaded into registers
+// before this one's sums.
 template <typename T, int V, int NV>
-__global__ void __launch_bounds__(1024) backward_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
+    using C = Columns<T, V>;
+    constexpr int P = C::P;
     extern __shared__ float shared[];
-    __shared__ float2 slots[2][32];
+    __shared__ alignas(16) float2 slots[2][16];
     const int tpr = p.threads_per_row;
-    const int groups = blockDim.x / tpr;
-    const int grp = threadIdx.x / tpr, t = threadIdx.x % tpr;
+    const int groups = blockDim.x / tpr, warps = tpr >> 5;
+    const int grp = threadIdx.x / tpr, t = threadIdx.x - grp * tpr;
     const int cols = (int)p.cols;
-    const bool has_gamma = p.gamma != nullptr;
     grid_dependency_wait();
     grid_launch_dependents();
-    Pack<T, V> kx[NV], kd[NV], kg[NV];
-    RowGrads<T, V, NV> r;
-    r.clear();
-    const Pack<T, V> zero{};
+    typename C::Raw kx[NV], kd[NV];
+    F2 ag[NV][P], ab[NV][P], g[NV][P], xh[NV][P], dxh[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * V;
-        kg[i] = has_gamma && c < cols ? load<T, V>(static_cast<const T*>(p.gamma) + c) : zero;
+        if (p.gamma) C::pairs_of(g[i], C::read(static_cast<const T*>(p.gamma), t, i, tpr, cols, true));
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            if (!p.gamma) g[i][q] = both(1.f);
+            ag[i][q] = ab[i][q] = 0;
+        }
     }
     const int64_t step = (int64_t)gridDim.x * groups;
     float mean = 0.f, rstd = 0.f;
+    // packs past a row's end, and rows past the last one, have dy = 0 and add nothing
     auto fetch = [&](int64_t row) {
         const bool live = row < p.rows;
         const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
         const T* dy = static_cast<const T*>(p.dY) + row * p.dy_pitch;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * V;
-            kx[i] = live && c < cols ? load<T, V>(x + c) : zero;
-            kd[i] = live && c < cols ? load<T, V>(dy + c) : zero;
+            kx[i] = C::read(x, t, i, tpr, cols, live);
+            kd[i] = C::read(dy, t, i, tpr, cols, live);
         }
         mean = live ? p.mean[row] : 0.f;
         rstd = live ? p.rstd[row] : 0.f;
@@ -466,45 +480,96 @@ __global__ void __launch_bounds__(1024) backward_kernel(const BwdParams p) {
     int buf = 0;
     // every group runs the same number of turns (the block's barriers)
     for (int64_t first = (int64_t)blockIdx.x * groups; first < p.rows; first += step, row += step, buf ^= 1) {
-        const F2 scale = both(rstd);
-        float2 c = make_float2(0.f, 0.f);
+        const F2 scale = both(rstd), minus_mean = both(-mean);
+        F2 c1 = 0, c2 = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const float2 v = r.take(i, kx[i], kd[i], kg[i], has_gamma, both(-mean), scale);
-            // a pack past the row's end has xh <> 0 but dy = 0: its sums are 0
-            c.x += v.x;
-            c.y += v.y;
+            F2 d[P];
+            C::pairs_of(xh[i], kx[i]);
+            C::pairs_of(d, kd[i]);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                xh[i][q] = mul2(add2(xh[i][q], minus_mean), scale);
+                ag[i][q] = fma2(d[q], xh[i][q], ag[i][q]);
+                ab[i][q] = add2(ab[i][q], d[q]);
+                dxh[i][q] = mul2(d[q], g[i][q]);
+                c1 = add2(c1, dxh[i][q]);
+                c2 = fma2(dxh[i][q], xh[i][q], c2);
+            }
         }
         fetch(row + step);
         if (!p.dX) continue;                      // uniform over the grid
-        c = group_sum(c, slots, buf, grp, tpr >> 5, p.inv_cols);
+        float2 c = make_float2(warp_sum(sum_of<2>(c1)), warp_sum(sum_of<2>(c2)));
+        if (warps > 1) {
+            if ((threadIdx.x & 31) == 0) slots[buf][threadIdx.x >> 5] = c;
+            __syncthreads();
+            c = make_float2(0.f, 0.f);
+            for (int w = 0; w < warps; ++w) {
+                const float2 v = slots[buf][grp * warps + w];
+                c.x += v.x;
+                c.y += v.y;
+            }
+        }
         if (row < p.rows) {
+            const F2 m1 = both(-c.x * p.inv_cols), m2 = both(-c.y * p.inv_cols);
             T* dx = static_cast<T*>(p.dX) + row * p.dx_pitch;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int at = (t + i * tpr) * V;
-                if (at < cols) r.put(i, dx + at, c.x, c.y, scale);
+                F2 o[P];
+#pragma unroll
+                for (int q = 0; q < P; ++q) o[q] = mul2(add2(fma2(xh[i][q], m2, dxh[i][q]), m1), scale);
+                if constexpr (V == 1) {
+                    float lo, hi;
+                    unpack_f2(o[0], lo, hi);
+                    if (C::at(t, i, 0, tpr) < cols) dx[C::at(t, i, 0, tpr)] = Num<T>::from_acc(lo);
+                    if (C::at(t, i, 1, tpr) < cols) dx[C::at(t, i, 1, tpr)] = Num<T>::from_acc(hi);
+                } else if (C::at(t, i, 0, tpr) < cols) {
+                    store<T, V>(dx + C::at(t, i, 0, tpr), o);
+                }
             }
         }
     }
-    if (p.partial) r.leave(p.partial + (int64_t)blockIdx.x * 2 * cols, shared, cols, grp, groups, t, tpr);
+    if (!p.partial) return;
+    float* out = p.partial + (int64_t)blockIdx.x * 2 * cols;
+    for (int which = 0; which < 2; ++which) {
+        if (groups > 1) __syncthreads();
+        float* to = groups > 1 ? shared + grp * cols : out + which * cols;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                float v[2];
+                unpack_f2(which ? ab[i][q] : ag[i][q], v[0], v[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (C::at(t, i, 2 * q + h, tpr) < cols) to[C::at(t, i, 2 * q + h, tpr)] = v[h];
+            }
+        if (groups == 1) continue;
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+            float s = 0.f;
+            for (int k = 0; k < groups; ++k) s += shared[k * cols + c];
+            out[which * cols + c] = s;
+        }
+    }
 }
 
 // Rows of 16-byte packs: one row a block at a time, x and dy copied ahead into
 // a ring of kAhead rows by bulk copies.  The barrier of the row's sums also
 // tells that every thread has read the row: its buffer takes another.
+// FULL: every thread has NV packs.
 constexpr int kAhead = 3;
-template <typename T, int NV>
-__global__ void __launch_bounds__(512) backward_ring_kernel(const BwdParams p) {
+template <typename T, int NV, int WARPS, bool FULL>
+__global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdParams p) {
     constexpr int V = 16 / sizeof(T);
     extern __shared__ __align__(128) unsigned char ring[];
-    __shared__ float2 slots[2][32];
+    __shared__ alignas(16) float2 slots[2][WARPS];
     __shared__ uint64_t full[kAhead];
     __shared__ int abort_flag;
     const int t = threadIdx.x, threads = blockDim.x;
     const int cols = (int)p.cols;
     const uint32_t row_bytes = (uint32_t)cols * sizeof(T);
-    const bool has_gamma = p.gamma != nullptr;
+    if (t < WARPS) slots[0][t] = slots[1][t] = make_float2(0.f, 0.f);
     if (t == 0) {
         for (int i = 0; i < kAhead; ++i) tc::mbar_init(&full[i], 1);
         abort_flag = 0;
@@ -532,49 +597,51 @@ __global__ void __launch_bounds__(512) backward_ring_kernel(const BwdParams p) {
     int64_t row = blockIdx.x;
     if (t == 0)
         for (int i = 0; i < kAhead; ++i) fetch(row + (int64_t)i * gridDim.x, i);
-    Pack<T, V> kg[NV];
     RowGrads<T, V, NV> r;
     r.clear();
     const Pack<T, V> zero{};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * threads) * V;
-        kg[i] = has_gamma && c < cols ? load<T, V>(static_cast<const T*>(p.gamma) + c) : zero;
+        r.weights(i, p.gamma && c < cols ? static_cast<const T*>(p.gamma) + c : nullptr);
     }
     int stage = 0, phase = 0, buf = 0;
     float mean = row < p.rows ? p.mean[row] : 0.f, rstd = row < p.rows ? p.rstd[row] : 0.f;
-    for (; row < p.rows; row += gridDim.x, buf ^= 1) {
+    T* dx = p.dX ? static_cast<T*>(p.dX) + row * p.dx_pitch : nullptr;
+    const int64_t dx_step = gridDim.x * p.dx_pitch;
+    for (; row < p.rows; row += gridDim.x, buf ^= 1, dx += dx_step) {
         // a wait that runs out: the row's sums are of what is there, the error word tells
         tc::mbar_wait(&full[stage], phase, &abort_flag, p.err);
         const T* x = reinterpret_cast<const T*>(ring + (size_t)stage * 2 * row_bytes);
         const T* dy = x + cols;
         const F2 scale = both(rstd), minus_mean = both(-mean);
-        float2 c = make_float2(0.f, 0.f);
+        F2 c1 = 0, c2 = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int at = (t + i * threads) * V;
-            const bool in = at < cols;
-            const float2 v = r.take(i, in ? load<T, V>(x + at) : zero, in ? load<T, V>(dy + at) : zero, kg[i], has_gamma,
-                                    minus_mean, scale);
-            c.x += v.x;
-            c.y += v.y;
+            const bool in = FULL || at < cols;
+            r.take(i, in ? load<T, V>(x + at) : zero, in ? load<T, V>(dy + at) : zero, minus_mean, scale, c1, c2);
         }
         const int64_t next = row + gridDim.x;
-        mean = next < p.rows ? p.mean[next] : 0.f;
-        rstd = next < p.rows ? p.rstd[next] : 0.f;
-        c = group_sum(c, slots, buf, 0, threads >> 5, p.inv_cols);
-        if (threads == 32) __syncwarp();
+        if (next < p.rows) {
+            mean = p.mean[next];
+            rstd = p.rstd[next];
+        }
+        const float2 own = make_float2(warp_sum(sum_of<V>(c1)), warp_sum(sum_of<V>(c2)));
+        if ((t & 31) == 0) slots[buf][t >> 5] = own;
+        __syncthreads();
         if (t == 0) fetch(row + (int64_t)kAhead * gridDim.x, stage);
         if (++stage == kAhead) {
             stage = 0;
             phase ^= 1;
         }
         if (p.dX) {
-            T* dx = static_cast<T*>(p.dX) + row * p.dx_pitch;
+            const float2 c = sum_slots<WARPS>(slots[buf]);
+            const F2 m1 = both(-c.x * p.inv_cols), m2 = both(-c.y * p.inv_cols);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int at = (t + i * threads) * V;
-                if (at < cols) r.put(i, dx + at, c.x, c.y, scale);
+                if (FULL || at < cols) r.put(i, dx + at, m1, m2, scale);
             }
         }
     }
@@ -585,7 +652,7 @@ __global__ void __launch_bounds__(512) backward_ring_kernel(const BwdParams p) {
             tc::mbar_wait_drain(&full[i], 1);
         }
     }
-    if (p.partial) r.leave(p.partial + (int64_t)blockIdx.x * 2 * cols, nullptr, cols, 0, 1, t, threads);
+    if (p.partial) r.leave(p.partial + (int64_t)blockIdx.x * 2 * cols, cols, t, threads);
 }
 
 // Rows wider than a block's registers hold: dx alone, two passes over the row.
@@ -603,20 +670,17 @@ __global__ void __launch_bounds__(1024) backward_long_rows_kernel(const BwdParam
         const F2 scale = both(rstd), minus_mean = both(-mean);
         RowGrads<T, V, 1> r;
         r.clear();
-        const Pack<T, V> zero{};
-        float c1 = 0.f, c2 = 0.f;
+        F2 s1 = 0, s2 = 0;
         for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
-            const float2 v = r.take(0, load<T, V>(x + c), load<T, V>(dy + c), gamma ? load<T, V>(gamma + c) : zero,
-                                    gamma != nullptr, minus_mean, scale);
-            c1 += v.x;
-            c2 += v.y;
+            r.weights(0, gamma ? gamma + c : nullptr);
+            r.take(0, load<T, V>(x + c), load<T, V>(dy + c), minus_mean, scale, s1, s2);
         }
-        c1 = block_sum<32>(c1, slots[0]) * p.inv_cols;
-        c2 = block_sum<32>(c2, slots[1]) * p.inv_cols;
+        const float c1 = block_sum<32>(sum_of<V>(s1), slots[0]) * p.inv_cols;
+        const float c2 = block_sum<32>(sum_of<V>(s2), slots[1]) * p.inv_cols;
         for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
-            r.take(0, load<T, V>(x + c), load<T, V>(dy + c), gamma ? load<T, V>(gamma + c) : zero, gamma != nullptr,
-                   minus_mean, scale);
-            r.put(0, dx + c, c1, c2, scale);
+            r.weights(0, gamma ? gamma + c : nullptr);
+            r.take(0, load<T, V>(x + c), load<T, V>(dy + c), minus_mean, scale, s1, s2);
+            r.put(0, dx + c, both(-c1), both(-c2), scale);
         }
     }
 }
@@ -678,14 +742,20 @@ olc_status by_type(olc_dtype dt, F&& f) {
     }
 }
 
+template <typename T, int NV, bool FULL>
+cudaError_t forward_rows_as(const FwdParams& p, int sm_count, cudaStream_t s) {
+    const int smem = (2 + kRowWarps) * (int)(p.cols * sizeof(T));
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(forward_rows_kernel<T, NV, FULL>), smem);
+    if (e != cudaSuccess) return e;
+    // what registers (16 packs a lane: 128) and shared memory let reside
+    const int per_sm = (int)min64(NV == 16 ? 2 : (NV == 8 ? 3 : 4), (220 * 1024) / (smem + 1024));
+    const int64_t grid = min64(ceil_div(p.rows, kRowWarps), (int64_t)sm_count * per_sm);
+    return launch_pdl(forward_rows_kernel<T, NV, FULL>, dim3((unsigned)grid), dim3(kRowWarps * 32), (size_t)smem, s, p);
+}
 template <typename T, int NV>
 cudaError_t forward_rows(const FwdParams& p, int sm_count, cudaStream_t s) {
-    const int smem = (2 + 2 * kRowWarps) * (int)(p.cols * sizeof(T));
-    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(forward_rows_kernel<T, NV>), smem);
-    if (e != cudaSuccess) return e;
-    const int per_sm = (int)min64(8, (220 * 1024) / (smem + 1024));
-    const int64_t grid = min64(ceil_div(p.rows, kRowWarps), (int64_t)sm_count * per_sm);
-    return launch_pdl(forward_rows_kernel<T, NV>, dim3((unsigned)grid), dim3(kRowWarps * 32), (size_t)smem, s, p);
+    return p.cols * (int64_t)sizeof(T) == NV * 512 ? forward_rows_as<T, NV, true>(p, sm_count, s)
+                                                   : forward_rows_as<T, NV, false>(p, sm_count, s);
 }
 
 template <typename T, int V>
@@ -724,37 +794,36 @@ constexpr int kColsPerThread = 16;      // float32 column sums of dgamma and dbe
 
 // the backward launch of one shape: which kernel, how many threads
 struct BwdShape {
-    int nv = 0;                          // 0: rows wider than a block's registers
+    enum Kind { LONG, RING, ANY } kind = LONG;   // LONG: rows wider than a block's registers
+    int per_thread = 0;                          // columns
     int tpr = 0, groups = 1, threads = 0;
     int64_t blocks = 0;
-    bool ring = false;
 };
 
 template <int V>
 BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
     BwdShape b;
-    const int64_t packs = ceil_div(cols, V);
-    if (packs > 1024 * (kColsPerThread / V)) {
+    if (cols > 512 * kColsPerThread) {
         b.blocks = min64(max64(rows / 64, 1), max64(1, 8 * (int64_t)sm_count * 256 / cols));
         return b;
     }
-    // whole rows of 16-byte packs through the ring: 16 columns a thread, two
-    // blocks on an SM
-    const int64_t ring_threads = ceil_div(ceil_div(packs * V, kColsPerThread), 32) * 32;
-    if (V > 1 && packs >= 128 && ring_threads <= 512 && rows >= 4 * (int64_t)sm_count) {
-        b.ring = true;
-        b.nv = kColsPerThread / V;
-        b.tpr = b.threads = (int)ring_threads;
+    // whole rows of 16-byte packs through the ring, where a block takes
+    // several: two blocks on an SM
+    if (V > 1 && cols >= 1024 && rows >= 4 * (int64_t)sm_count) {
+        b.kind = BwdShape::RING;
+        b.per_thread = kColsPerThread;
+        b.tpr = b.threads = (int)(ceil_div(ceil_div(cols, kColsPerThread), 32) * 32);
         b.blocks = min64(rows, (int64_t)sm_count * 2);
         return b;
     }
-    b.nv = 1;
-    while (b.nv * V < kColsPerThread && packs > 512 * b.nv) b.nv *= 2;
-    b.tpr = (int)(ceil_div(ceil_div(packs, b.nv), 32) * 32);
+    b.kind = BwdShape::ANY;
+    const int least = V == 1 ? 2 : V;            // columns of a pack, or of a pair of single elements
+    b.per_thread = least;
+    while (b.per_thread < kColsPerThread && cols > 32 * b.per_thread) b.per_thread *= 2;
+    b.tpr = (int)(ceil_div(ceil_div(cols, b.per_thread), 32) * 32);
     b.groups = b.tpr >= 256 ? 1 : 256 / b.tpr;
     b.threads = b.tpr * b.groups;
-    const int per_sm = b.threads > 512 ? 1 : 2 * (512 / b.threads);
-    b.blocks = max64(1, min64(ceil_div(rows, b.groups), (int64_t)sm_count * per_sm));
+    b.blocks = max64(1, min64(ceil_div(rows, b.groups), (int64_t)sm_count * (b.threads > 256 ? 1 : 2)));
     return b;
 }
 
@@ -764,12 +833,21 @@ cudaError_t backward_rows(const BwdParams& p, const BwdShape& b, cudaStream_t s)
     return launch_pdl(backward_kernel<T, V, NV>, dim3((unsigned)b.blocks), dim3((unsigned)b.threads), smem, s, p);
 }
 
+template <typename T, int WARPS, bool FULL>
+cudaError_t backward_ring(const BwdParams& p, const BwdShape& b, cudaStream_t s) {
+    auto* kernel = backward_ring_kernel<T, kColsPerThread * sizeof(T) / 16, WARPS, FULL>;
+    const int smem = kAhead * 2 * (int)(p.cols * sizeof(T));
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)b.blocks), dim3((unsigned)b.threads), (size_t)smem, s, p);
+}
+
 template <typename T, int V>
 cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStream_t s) {
     const BwdShape b = backward_shape<V>(p.rows, p.cols, sm_count);
     cudaError_t e = cudaSuccess;
     p.threads_per_row = b.tpr;
-    if (b.nv == 0) {
+    if (b.kind == BwdShape::LONG) {
         // the column sums first: dX may be dY or X
         if (p.partial)
             e = launch_pdl(backward_long_cols_kernel<T>, dim3((unsigned)ceil_div(p.cols, 256), (unsigned)b.blocks),
@@ -777,24 +855,21 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
         if (e == cudaSuccess && p.dX)
             e = launch_pdl(backward_long_rows_kernel<T, V>, dim3((unsigned)min64(p.rows, (int64_t)sm_count * 2)),
                            dim3(1024), 0, s, p);
-    } else if (b.ring) {
+    } else if (b.kind == BwdShape::RING) {
         if constexpr (V > 1) {
-            auto* kernel = backward_ring_kernel<T, kColsPerThread / V>;
-            const int smem = kAhead * 2 * (int)(p.cols * sizeof(T));
-            e = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
-            if (e == cudaSuccess)
-                e = launch_pdl(kernel, dim3((unsigned)b.blocks), dim3((unsigned)b.threads), (size_t)smem, s, p);
+            const bool full = p.cols == (int64_t)b.threads * kColsPerThread;
+            if (b.threads <= 256)
+                e = full ? backward_ring<T, 8, true>(p, b, s) : backward_ring<T, 8, false>(p, b, s);
+            else
+                e = full ? backward_ring<T, 16, true>(p, b, s) : backward_ring<T, 16, false>(p, b, s);
         }
-    } else if (b.nv == 1) {
-        e = backward_rows<T, V, 1>(p, b, s);
-    } else if (b.nv == 2) {
-        e = backward_rows<T, V, 2>(p, b, s);
-    } else if (b.nv == 4) {
-        if constexpr (V <= 4) e = backward_rows<T, V, 4>(p, b, s);
-    } else if (b.nv == 8) {
-        if constexpr (V == 1) e = backward_rows<T, V, 8>(p, b, s);
-    } else {
-        if constexpr (V == 1) e = backward_rows<T, V, 16>(p, b, s);
+    } else if (b.per_thread == 16) {
+        e = backward_rows<T, V, V == 1 ? 8 : 16 / V>(p, b, s);
+    } else if (b.per_thread == 8) {
+        e = backward_rows<T, V, V == 1 ? 4 : 8 / V>(p, b, s);
+    } else if constexpr (V <= 4) {
+        if (b.per_thread == 4) e = backward_rows<T, V, V == 1 ? 2 : 1>(p, b, s);
+        else if constexpr (V == 1) e = backward_rows<T, 1, 1>(p, b, s);
     }
     if (e == cudaSuccess && p.partial)
         e = launch_pdl(column_sum_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32), 2), dim3(1024), 0, s,

@@ -26,11 +26,28 @@ def _torch_dtype(name: str):
     return getattr(torch, name)
 
 
+def _raw_stream(stream):
+    """Handle of ``stream``, or of torch's current stream (by the call that
+    makes no Stream object, where torch has it: one in five microseconds of a
+    small call)."""
+    if stream is None:
+        import torch
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            pass
+    return _stream_handle(stream)
+
+
 def _rows(name, t, rows, cols, dtype):
     """Pointer and row pitch of a [rows, cols] tensor of the given type."""
     if t.dtype is not dtype:
         raise TypeError("%s has dtype %s, the plan wants %s" % (name, t.dtype, dtype))
     shape = t.shape
+    if shape == (rows, cols) and t.is_cuda:      # the usual case
+        pitch, unit = t.stride()
+        if unit == 1 and pitch >= cols:
+            return t.data_ptr(), pitch
     if not shape or shape[-1] != cols or t.numel() != rows * cols:
         raise ValueError("%s has shape %s, the plan wants [%d, %d]" % (name, tuple(shape), rows, cols))
     if t.numel() == 0:
@@ -121,7 +138,7 @@ class LayerNormPlan(_PlanHandle):
         y, yp = _rows("Y", Y, rows, cols, t)
         st = self.lib.olc_layer_norm_forward(
             self._h, x, xp, _flat("gamma", gamma, cols, t), _flat("beta", beta, cols, t), y, yp,
-            _flat("mean", mean, rows, self._f32), _flat("rstd", rstd, rows, self._f32), _stream_handle(stream))
+            _flat("mean", mean, rows, self._f32), _flat("rstd", rstd, rows, self._f32), _raw_stream(stream))
         _check(st, "olc_layer_norm_forward")
         return Y
 
@@ -135,7 +152,7 @@ class LayerNormPlan(_PlanHandle):
         st = self.lib.olc_layer_norm_backward(
             self._h, dy, dyp, x, xp, _flat("gamma", gamma, cols, t), _flat("mean", mean, rows, self._f32),
             _flat("rstd", rstd, rows, self._f32), dx, dxp, _flat("dgamma", dgamma, cols, t),
-            _flat("dbeta", dbeta, cols, t), _stream_handle(stream))
+            _flat("dbeta", dbeta, cols, t), _raw_stream(stream))
         _check(st, "olc_layer_norm_backward")
         return dX, dgamma, dbeta
 
@@ -164,7 +181,7 @@ class GatedPlan(_PlanHandle):
         st = self.lib.olc_gated_forward(
             self._h, _dense("X", X, m, self.d_in, t), _dense("Wg", Wg, w[0], w[1], t),
             _dense("Wu", Wu, w[0], w[1], t), _dense("H", H, m, f, t), _dense("G", G, m, f, t),
-            _dense("U", U, m, f, t), _stream_handle(stream))
+            _dense("U", U, m, f, t), _raw_stream(stream))
         _check(st, "olc_gated_forward")
         return H
 
@@ -176,7 +193,7 @@ class GatedPlan(_PlanHandle):
             self._h, _dense("dH", dH, m, f, t), _dense("X", X, m, d, t), _dense("Wg", Wg, w[0], w[1], t),
             _dense("Wu", Wu, w[0], w[1], t), _dense("G", G, m, f, t), _dense("U", U, m, f, t),
             _dense("dX", dX, m, d, t), _dense("dWg", dWg, w[0], w[1], t), _dense("dWu", dWu, w[0], w[1], t),
-            _stream_handle(stream))
+            _raw_stream(stream))
         _check(st, "olc_gated_backward")
         return dX, dWg, dWu
 
@@ -206,7 +223,7 @@ class TokenLogProbsPlan(_PlanHandle):
             self._h, z, pitch, _flat("tokens", tokens, rows, self._i64), _flat("logprob", logprob, rows, f32),
             _flat("entropy", entropy, rows, f32), _flat("lse", lse, rows, f32),
             _flat("top_logprob", top_logprob, n, f32), _flat("top_index", top_index, n, self._i64),
-            _stream_handle(stream))
+            _raw_stream(stream))
         _check(st, "olc_token_log_probs_forward")
         return logprob
 
@@ -219,7 +236,7 @@ class TokenLogProbsPlan(_PlanHandle):
         st = self.lib.olc_token_log_probs_backward(
             self._h, z, pitch, _flat("tokens", tokens, rows, self._i64), _flat("lse", lse, rows, f32),
             _flat("entropy", entropy, rows, f32), _flat("dlogprob", dlogprob, rows, f32),
-            _flat("dentropy", dentropy, rows, f32), dz, d_pitch, _stream_handle(stream))
+            _flat("dentropy", dentropy, rows, f32), dz, d_pitch, _raw_stream(stream))
         _check(st, "olc_token_log_probs_backward")
         return dlogits
 
