@@ -33,7 +33,6 @@ struct FwdParams {
     int64_t rows, cols;
     float eps;
     float inv_cols;
-    unsigned int* err;
 };
 
 struct BwdParams {
@@ -165,11 +164,58 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
     return s;
 }
 
-// W warps on a row, NV packs of V elements a thread, in registers.  W == 1:
-// blocks of four independent warps.
+// A thread's columns of a row shared by tpr threads: packs of V at (t + i tpr) V, or,
+// for rows of any alignment (V = 1), pairs of single elements tpr apart: two
+// elements an instruction either way.
+template <typename T, int V>
+struct Columns {
+    static constexpr int PER = V == 1 ? 2 : V;      // columns of one i
+    static constexpr int P = PER / 2;
+    struct Raw {
+        T v[PER];
+    };
+    static __device__ __forceinline__ int at(int t, int i, int q, int tpr) {
+        return V == 1 ? t + (2 * i + q) * tpr : (t + i * tpr) * V + q;
+    }
+    static __device__ __forceinline__ Raw read(const T* row, int t, int i, int tpr, int cols, bool live) {
+        Raw r{};
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (live && at(t, i, q, tpr) < cols) r.v[q] = row[at(t, i, q, tpr)];
+        } else {
+            if (live && at(t, i, 0, tpr) < cols) {
+                const Pack<T, V> k = load<T, V>(row + at(t, i, 0, tpr));
+#pragma unroll
+                for (int q = 0; q < V; ++q) r.v[q] = k.v[q];
+            }
+        }
+        return r;
+    }
+    static __device__ __forceinline__ bool in(int t, int i, int q, int tpr, int cols) { return at(t, i, q, tpr) < cols; }
+    static __device__ __forceinline__ void write(T* row, int t, int i, int tpr, int cols, const F2 (&o)[P]) {
+        if constexpr (V == 1) {
+            float lo, hi;
+            unpack_f2(o[0], lo, hi);
+            if (in(t, i, 0, tpr, cols)) row[at(t, i, 0, tpr)] = Num<T>::from_acc(lo);
+            if (in(t, i, 1, tpr, cols)) row[at(t, i, 1, tpr)] = Num<T>::from_acc(hi);
+        } else if (in(t, i, 0, tpr, cols)) {
+            store<T, V>(row + at(t, i, 0, tpr), o);
+        }
+    }
+    static __device__ __forceinline__ void pairs_of(F2 (&out)[P], const Raw& r) {
+#pragma unroll
+        for (int q = 0; q < P; ++q) out[q] = pack_f2(Num<T>::to_acc(r.v[2 * q]), Num<T>::to_acc(r.v[2 * q + 1]));
+    }
+};
+
+// W warps on a row, NV packs (or pairs of elements) a thread, in registers.
+// W == 1: blocks of four independent warps.
 template <typename T, int V, int W, int NV>
 __global__ void __launch_bounds__(W == 1 ? 128 : W * 32)
 forward_kernel(const FwdParams p) {
+    using C = Columns<T, V>;
+    constexpr int P = C::P, TPR = W * 32;
     __shared__ float slots[2][W];
     const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
@@ -179,119 +225,59 @@ forward_kernel(const FwdParams p) {
     const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
     T* y = static_cast<T*>(p.Y) + row * p.y_pitch;
     const int cols = (int)p.cols;
-    Pack<T, V> k[NV];
+    typename C::Raw k[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) k[i] = C::read(x, t, i, TPR, cols, true);
+    F2 s = 0, v[P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * W * 32) * V;
-        if (c < cols) k[i] = load<T, V>(x + c);
-    }
-    F2 s = 0;
+        C::pairs_of(v, k[i]);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if ((t + i * W * 32) * V < cols) add_elements<T, V>(s, k[i]);
-    const float mean = block_sum<W>(sum_of<V>(s), slots[0]) * p.inv_cols;
+        for (int q = 0; q < P; ++q) s = add2(s, v[q]);     // zeros past the row's end
+    }
+    const float mean = block_sum<W>(sum_of<2>(s), slots[0]) * p.inv_cols;
+    const F2 minus_mean = both(-mean);
     s = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if ((t + i * W * 32) * V < cols) add_squares<T, V>(s, k[i], both(-mean));
-    const float rstd = 1.0f / sqrtf(fmaf(block_sum<W>(sum_of<V>(s), slots[1]), p.inv_cols, p.eps));
+    for (int i = 0; i < NV; ++i) {
+        C::pairs_of(v, k[i]);
+        if constexpr (V == 1) {
+            float lo, hi;
+            unpack_f2(add2(v[0], minus_mean), lo, hi);
+            v[0] = pack_f2(C::in(t, i, 0, TPR, cols) ? lo : 0.f, C::in(t, i, 1, TPR, cols) ? hi : 0.f);
+            s = fma2(v[0], v[0], s);
+        } else if (C::in(t, i, 0, TPR, cols)) {
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const F2 d = add2(v[q], minus_mean);
+                s = fma2(d, d, s);
+            }
+        }
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(block_sum<W>(sum_of<2>(s), slots[1]), p.inv_cols, p.eps));
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-    const T* gamma = static_cast<const T*>(p.gamma);
-    const T* beta = static_cast<const T*>(p.beta);
+    const F2 scale = both(rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * W * 32) * V;
-        if (c < cols)
-            finish<T, V>(y + c, k[i], both(-mean), both(rstd), gamma ? gamma + c : nullptr, beta ? beta + c : nullptr);
-    }
-}
-
-// Many rows of 16-byte packs: persistent warps of a row each.  A warp takes its
-// row from its buffer of shared memory into registers and lets a bulk copy
-// bring the next one there while it works on this one; gamma and beta sit in
-// shared memory.  Nothing in a row's way waits for another warp.  FULL: every
-// lane has NV packs.
-constexpr int kRowWarps = 8;
-template <typename T, int NV, bool FULL>
-__global__ void __launch_bounds__(kRowWarps * 32, NV == 16 ? 2 : (NV == 8 ? 3 : 4)) forward_rows_kernel(const FwdParams p) {
-    constexpr int V = 16 / sizeof(T);
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t full[kRowWarps];
-    __shared__ int abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cols = (int)p.cols;
-    const uint32_t row_bytes = (uint32_t)cols * sizeof(T);
-    T* gamma = reinterpret_cast<T*>(smem);
-    T* beta = reinterpret_cast<T*>(smem + row_bytes);
-    const T* x = reinterpret_cast<const T*>(smem + (2 + (size_t)warp) * row_bytes);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kRowWarps; ++i) tc::mbar_init(&full[i], 1);
-        abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    __syncthreads();
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int64_t step = (int64_t)gridDim.x * kRowWarps;
-    auto fetch = [&](int64_t row) {                  // one lane
-        if (row >= p.rows) return;
-        tc::mbar_arrive_expect_tx(&full[warp], row_bytes);
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                tc::smem_u32(x)),
-            "l"(static_cast<const T*>(p.X) + row * p.x_pitch), "r"(row_bytes), "r"(tc::smem_u32(&full[warp]))
-            : "memory");
-    };
-    int64_t row = (int64_t)blockIdx.x * kRowWarps + warp;
-    if (lane == 0) fetch(row);
-    for (int c = threadIdx.x * V; c < cols; c += kRowWarps * 32 * V) {
-        if (p.gamma) *reinterpret_cast<uint4*>(gamma + c) = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.gamma) + c);
-        if (p.beta) *reinterpret_cast<uint4*>(beta + c) = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.beta) + c);
-    }
-    __syncthreads();
-    if (!p.gamma) gamma = nullptr;
-    if (!p.beta) beta = nullptr;
-    int phase = 0;
-    for (; row < p.rows; row += step) {
-        if (!tc::mbar_wait(&full[warp], phase, &abort_flag, p.err)) {
-            tc::mbar_wait_drain(&full[warp], phase);     // the copy in flight lands before the block's memory goes
-            break;
-        }
-        phase ^= 1;
-        Pack<T, V> k[NV];
+        if (!C::in(t, i, 0, TPR, cols)) continue;
+        F2 w[P];
+        C::pairs_of(v, k[i]);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * 32) * V;
-            if (FULL || c < cols) k[i] = load<T, V>(x + c);
-        }
-        __syncwarp();                                // the row is in registers: its buffer takes another
-        if (lane == 0) fetch(row + step);
-        F2 s = 0;
+        for (int q = 0; q < P; ++q) v[q] = mul2(add2(v[q], minus_mean), scale);
+        if (p.gamma) {
+            C::pairs_of(w, C::read(static_cast<const T*>(p.gamma), t, i, TPR, cols, true));
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (FULL || (lane + i * 32) * V < cols) add_elements<T, V>(s, k[i]);
-        const float mean = warp_sum(sum_of<V>(s)) * p.inv_cols;
-        s = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (FULL || (lane + i * 32) * V < cols) add_squares<T, V>(s, k[i], both(-mean));
-        const float rstd = 1.0f / sqrtf(fmaf(warp_sum(sum_of<V>(s)), p.inv_cols, p.eps));
-        if (lane == 0) {
-            if (p.mean) p.mean[row] = mean;
-            if (p.rstd) p.rstd[row] = rstd;
+            for (int q = 0; q < P; ++q) v[q] = mul2(v[q], w[q]);
         }
-        T* y = static_cast<T*>(p.Y) + row * p.y_pitch;
+        if (p.beta) {
+            C::pairs_of(w, C::read(static_cast<const T*>(p.beta), t, i, TPR, cols, true));
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (lane + i * 32) * V;
-            if (FULL || c < cols)
-                finish<T, V>(y + c, k[i], both(-mean), both(rstd), gamma ? gamma + c : nullptr,
-                             beta ? beta + c : nullptr);
+            for (int q = 0; q < P; ++q) v[q] = add2(v[q], w[q]);
         }
+        C::write(y, t, i, TPR, cols, v);
     }
 }
 
@@ -402,39 +388,6 @@ __device__ __forceinline__ float2 sum_slots(const float2* slots) {
     return c;
 }
 
-// A thread's columns in backward_kernel: NV packs of V at (t + i tpr) V, or,
-// for rows of any alignment (V = 1), NV pairs of single elements tpr apart.
-template <typename T, int V>
-struct Columns {
-    static constexpr int PER = V == 1 ? 2 : V;      // columns of one i
-    static constexpr int P = PER / 2;
-    struct Raw {
-        T v[PER];
-    };
-    static __device__ __forceinline__ int at(int t, int i, int q, int tpr) {
-        return V == 1 ? t + (2 * i + q) * tpr : (t + i * tpr) * V + q;
-    }
-    static __device__ __forceinline__ Raw read(const T* row, int t, int i, int tpr, int cols, bool live) {
-        Raw r{};
-        if constexpr (V == 1) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                if (live && at(t, i, q, tpr) < cols) r.v[q] = row[at(t, i, q, tpr)];
-        } else {
-            if (live && at(t, i, 0, tpr) < cols) {
-                const Pack<T, V> k = load<T, V>(row + at(t, i, 0, tpr));
-#pragma unroll
-                for (int q = 0; q < V; ++q) r.v[q] = k.v[q];
-            }
-        }
-        return r;
-    }
-    static __device__ __forceinline__ void pairs_of(F2 (&out)[P], const Raw& r) {
-#pragma unroll
-        for (int q = 0; q < P; ++q) out[q] = pack_f2(Num<T>::to_acc(r.v[2 * q]), Num<T>::to_acc(r.v[2 * q + 1]));
-    }
-};
-
 // Any alignment and few or short rows: the next row is loaded into registers
 // before this one's sums.
 template <typename T, int V, int NV>
@@ -518,14 +471,7 @@ __global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
                 F2 o[P];
 #pragma unroll
                 for (int q = 0; q < P; ++q) o[q] = mul2(add2(fma2(xh[i][q], m2, dxh[i][q]), m1), scale);
-                if constexpr (V == 1) {
-                    float lo, hi;
-                    unpack_f2(o[0], lo, hi);
-                    if (C::at(t, i, 0, tpr) < cols) dx[C::at(t, i, 0, tpr)] = Num<T>::from_acc(lo);
-                    if (C::at(t, i, 1, tpr) < cols) dx[C::at(t, i, 1, tpr)] = Num<T>::from_acc(hi);
-                } else if (C::at(t, i, 0, tpr) < cols) {
-                    store<T, V>(dx + C::at(t, i, 0, tpr), o);
-                }
+                C::write(dx, t, i, tpr, cols, o);
             }
         }
     }
@@ -742,48 +688,33 @@ olc_status by_type(olc_dtype dt, F&& f) {
     }
 }
 
-template <typename T, int NV, bool FULL>
-cudaError_t forward_rows_as(const FwdParams& p, int sm_count, cudaStream_t s) {
-    const int smem = (2 + kRowWarps) * (int)(p.cols * sizeof(T));
-    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(forward_rows_kernel<T, NV, FULL>), smem);
-    if (e != cudaSuccess) return e;
-    // what registers (16 packs a lane: 128) and shared memory let reside
-    const int per_sm = (int)min64(NV == 16 ? 2 : (NV == 8 ? 3 : 4), (220 * 1024) / (smem + 1024));
-    const int64_t grid = min64(ceil_div(p.rows, kRowWarps), (int64_t)sm_count * per_sm);
-    return launch_pdl(forward_rows_kernel<T, NV, FULL>, dim3((unsigned)grid), dim3(kRowWarps * 32), (size_t)smem, s, p);
-}
-template <typename T, int NV>
-cudaError_t forward_rows(const FwdParams& p, int sm_count, cudaStream_t s) {
-    return p.cols * (int64_t)sizeof(T) == NV * 512 ? forward_rows_as<T, NV, true>(p, sm_count, s)
-                                                   : forward_rows_as<T, NV, false>(p, sm_count, s);
-}
-
+// Threads a row: with many rows a thread takes four packs of 16 bytes, so that
+// enough of the row is on its way at once and enough blocks reside
+// ([16384, 4096] BF16, us: 4 warps x 4 packs 42.4, 8 x 2 46.2, 2 x 8 44.6,
+// 16 x 1 69.9, 1 x 16 51.7, persistent warps fed by bulk copies 50.4; a plain
+// copy of the tensor 43.5); with few rows more warps share one ([4, 4096] FP16:
+// 8 x 2 2.49, 4 x 4 3.17, 2 x 8 4.53).  One warp needs no block barrier.
 template <typename T, int V>
 cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
-    const int64_t packs = ceil_div(p.cols, V);
-    if constexpr (V > 1) {
-        // enough rows for persistent warps to take several each
-        if (packs >= 64 && packs <= 512 && p.rows >= 16 * (int64_t)sm_count) {
-            if (packs <= 128) return forward_rows<T, 4>(p, sm_count, s);
-            if (packs <= 256) return forward_rows<T, 8>(p, sm_count, s);
-            return forward_rows<T, 16>(p, sm_count, s);
-        }
-    }
-    // one warp on a row while the row fits 4 packs a lane: no block barrier
-    // on the way; eight or 32 warps share longer rows
-#define OLC_FWD(W, NV)                                                                                       \
-    return launch_pdl(forward_kernel<T, V, W, NV>, dim3((unsigned)(W == 1 ? ceil_div(p.rows, 4) : p.rows)),  \
+    // single elements go in pairs, twice as many a thread as packs
+    const int64_t n = ceil_div(p.cols, V == 1 ? 4 : V);
+    constexpr int M = V == 1 ? 2 : 1;
+    const bool few = p.rows < 4 * (int64_t)sm_count;
+#define OLC_FWD(W, NV)                                                                                          \
+    return launch_pdl(forward_kernel<T, V, W, NV * M>, dim3((unsigned)(W == 1 ? ceil_div(p.rows, 4) : p.rows)), \
                       dim3(W == 1 ? 128 : W * 32), 0, s, p)
     if (p.rows <= 0x7fffffff) {
-        if (packs <= 32) OLC_FWD(1, 1);
-        if (packs <= 64) OLC_FWD(1, 2);
-        if (packs <= 128) OLC_FWD(1, 4);
-        if (packs <= 256) OLC_FWD(8, 1);
-        if (packs <= 512) OLC_FWD(8, 2);
-        if (packs <= 1024) OLC_FWD(8, 4);
-        if (packs <= 2048) OLC_FWD(8, 8);
-        if (packs <= 4096) OLC_FWD(32, 4);
-        if (packs <= 8192) OLC_FWD(32, 8);
+        if (n <= 32) OLC_FWD(1, 1);
+        if (n <= 64) OLC_FWD(1, 2);
+        if (n <= 128 && !few) OLC_FWD(1, 4);
+        if (n <= 256 && !few) OLC_FWD(2, 4);
+        if (n <= 256) OLC_FWD(8, 1);
+        if (n <= 512 && !few) OLC_FWD(4, 4);
+        if (n <= 512) OLC_FWD(8, 2);
+        if (n <= 1024) OLC_FWD(8, 4);
+        if (n <= 2048) OLC_FWD(16, 4);
+        if (n <= 4096) OLC_FWD(32, 4);
+        if (n <= 8192) OLC_FWD(32, 8);
     }
 #undef OLC_FWD
     const int64_t grid = min64(p.rows, (int64_t)sm_count * 2);
@@ -933,7 +864,7 @@ olc_status olc_layer_norm_forward(olc_layer_norm_plan* plan, const void* X, int6
     const olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
     norm::FwdParams p{X, gamma, beta, Y, mean, rstd, x_pitch, y_pitch, plan->rows, plan->cols, plan->eps,
-                      (float)(1.0 / (double)plan->cols), device_error_word()};
+                      (float)(1.0 / (double)plan->cols)};
     // 16-byte packs need every row of every operand on a 16-byte boundary
     const bool wide = plan->cols * eb % 16 == 0 && plan_aligned16(X) && plan_aligned16(Y) && plan_aligned16(gamma) &&
                       plan_aligned16(beta) && (plan->rows == 1 || (x_pitch * eb % 16 == 0 && y_pitch * eb % 16 == 0));
