@@ -144,6 +144,14 @@ __device__ __forceinline__ void add_squares(F2& s, const Pack<T, V>& k, F2 minus
     }
 }
 
+// bytes from global to shared memory (both on 16-byte boundaries), completing on a barrier
+__device__ __forceinline__ void bulk_copy(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     tc::smem_u32(to)),
+                 "l"(from), "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
@@ -278,6 +286,62 @@ forward_kernel(const FwdParams p) {
             for (int q = 0; q < P; ++q) v[q] = add2(v[q], w[q]);
         }
         C::write(y, t, i, TPR, cols, v);
+    }
+}
+
+// Rows of at most L packs: L lanes on a row, R rows a lane one after the
+// other, all of them on their way at once.
+template <typename T, int L, int R>
+__global__ void __launch_bounds__(128) forward_short_kernel(const FwdParams p) {
+    constexpr int V = 16 / sizeof(T), P = V / 2, ROWS = 128 / L;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int c = (int)(threadIdx.x % L) * V;
+    const bool in = c < (int)p.cols;
+    const int64_t first = (int64_t)blockIdx.x * (ROWS * R) + threadIdx.x / L;
+    const Pack<T, V> zero{};
+    Pack<T, V> k[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t row = first + r * ROWS;
+        k[r] = in && row < p.rows ? load<T, V>(static_cast<const T*>(p.X) + row * p.x_pitch + c) : zero;
+    }
+    F2 g[P], b[P];
+    if (p.gamma && in) widen<T, V>(g, load<T, V>(static_cast<const T*>(p.gamma) + c));
+    if (p.beta && in) widen<T, V>(b, load<T, V>(static_cast<const T*>(p.beta) + c));
+    auto sum = [](F2 x) {
+        float v = sum_of<2>(x);
+#pragma unroll
+        for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        return v;
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t row = first + r * ROWS;
+        F2 x[P], s = 0;
+        widen<T, V>(x, k[r]);
+#pragma unroll
+        for (int q = 0; q < P; ++q) s = add2(s, x[q]);
+        const float mean = sum(s) * p.inv_cols;
+        s = 0;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            x[q] = add2(x[q], both(-mean));
+            if (in) s = fma2(x[q], x[q], s);
+        }
+        const float rstd = 1.0f / sqrtf(fmaf(sum(s), p.inv_cols, p.eps));
+        if (row >= p.rows) continue;
+        if (c == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            x[q] = mul2(x[q], both(rstd));
+            if (p.gamma) x[q] = mul2(x[q], g[q]);
+            if (p.beta) x[q] = add2(x[q], b[q]);
+        }
+        if (in) store<T, V>(static_cast<T*>(p.Y) + row * p.y_pitch + c, x);
     }
 }
 
@@ -529,16 +593,8 @@ __global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdPara
         if (row >= p.rows) return;
         unsigned char* to = ring + (size_t)stage * 2 * row_bytes;
         tc::mbar_arrive_expect_tx(&full[stage], 2 * row_bytes);
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                tc::smem_u32(to)),
-            "l"(static_cast<const T*>(p.X) + row * p.x_pitch), "r"(row_bytes), "r"(tc::smem_u32(&full[stage]))
-            : "memory");
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                tc::smem_u32(to + row_bytes)),
-            "l"(static_cast<const T*>(p.dY) + row * p.dy_pitch), "r"(row_bytes), "r"(tc::smem_u32(&full[stage]))
-            : "memory");
+        bulk_copy(to, static_cast<const T*>(p.X) + row * p.x_pitch, row_bytes, &full[stage]);
+        bulk_copy(to + row_bytes, static_cast<const T*>(p.dY) + row * p.dy_pitch, row_bytes, &full[stage]);
     };
     int64_t row = blockIdx.x;
     if (t == 0)
@@ -599,6 +655,125 @@ __global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdPara
         }
     }
     if (p.partial) r.leave(p.partial + (int64_t)blockIdx.x * 2 * cols, cols, t, threads);
+}
+
+// Rows of 16-byte packs twice as wide: the row stays in the ring until the
+// next row's barrier and is read twice, once for the row sums and once for dx
+// and the column sums, so that registers hold the column sums alone.
+constexpr int kWideThreads = 512, kWideColumns = 32;
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads) backward_wide_kernel(const BwdParams p, int stages) {
+    constexpr int V = 16 / sizeof(T), P = V / 2, NV = kWideColumns / V, WARPS = kWideThreads / 32, MOST = 4;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ alignas(16) float2 slots[2][WARPS];
+    __shared__ uint64_t full[MOST];
+    __shared__ int abort_flag;
+    const int t = threadIdx.x;
+    const int cols = (int)p.cols;
+    const uint32_t row_bytes = (uint32_t)cols * sizeof(T);
+    if (t == 0) {
+        for (int i = 0; i < MOST; ++i) tc::mbar_init(&full[i], 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    auto fetch = [&](int64_t row, int stage) {    // one thread
+        if (row >= p.rows) return;
+        unsigned char* to = ring + (size_t)stage * 2 * row_bytes;
+        tc::mbar_arrive_expect_tx(&full[stage], 2 * row_bytes);
+        bulk_copy(to, static_cast<const T*>(p.X) + row * p.x_pitch, row_bytes, &full[stage]);
+        bulk_copy(to + row_bytes, static_cast<const T*>(p.dY) + row * p.dy_pitch, row_bytes, &full[stage]);
+    };
+    int64_t row = blockIdx.x;
+    if (t == 0)
+        for (int i = 0; i < stages; ++i) fetch(row + (int64_t)i * gridDim.x, i);
+    F2 ag[NV][P], ab[NV][P];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int q = 0; q < P; ++q) ag[i][q] = ab[i][q] = 0;
+    const T* gamma = static_cast<const T*>(p.gamma);
+    int stage = 0, phase = 0, buf = 0, last = -1;
+    for (; row < p.rows; row += gridDim.x, buf ^= 1) {
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        tc::mbar_wait(&full[stage], phase, &abort_flag, p.err);
+        const T* x = reinterpret_cast<const T*>(ring + (size_t)stage * 2 * row_bytes);
+        const T* dy = x + cols;
+        const F2 scale = both(rstd), minus_mean = both(-mean);
+        auto at_pack = [&](int c, F2 (&xh)[P], F2 (&d)[P], F2 (&dxh)[P]) {
+            F2 g[P];
+            widen<T, V>(xh, load<T, V>(x + c));
+            widen<T, V>(d, load<T, V>(dy + c));
+            if (gamma) widen<T, V>(g, load<T, V>(gamma + c));
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                xh[q] = mul2(add2(xh[q], minus_mean), scale);
+                dxh[q] = gamma ? mul2(d[q], g[q]) : d[q];
+            }
+        };
+        F2 c1 = 0, c2 = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * kWideThreads) * V;
+            if (c >= cols) break;
+            F2 xh[P], d[P], dxh[P];
+            at_pack(c, xh, d, dxh);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                c1 = add2(c1, dxh[q]);
+                c2 = fma2(dxh[q], xh[q], c2);
+            }
+        }
+        const float2 own = make_float2(warp_sum(sum_of<2>(c1)), warp_sum(sum_of<2>(c2)));
+        if ((t & 31) == 0) slots[buf][t >> 5] = own;
+        __syncthreads();
+        // every thread is done with the row before this one: its buffer takes another
+        if (t == 0 && last >= 0) fetch(row + (int64_t)(stages - 1) * gridDim.x, last);
+        last = stage;
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+        const float2 sums = sum_slots<WARPS>(slots[buf]);
+        const F2 m1 = both(-sums.x * p.inv_cols), m2 = both(-sums.y * p.inv_cols);
+        T* dx = static_cast<T*>(p.dX) + row * p.dx_pitch;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * kWideThreads) * V;
+            if (c >= cols) break;
+            F2 xh[P], d[P], dxh[P];
+            at_pack(c, xh, d, dxh);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                ag[i][q] = fma2(d[q], xh[q], ag[i][q]);
+                ab[i][q] = add2(ab[i][q], d[q]);
+                dxh[q] = mul2(add2(fma2(xh[q], m2, dxh[q]), m1), scale);
+            }
+            if (p.dX) store<T, V>(dx + c, dxh);
+        }
+    }
+    if (t == 0 && abort_flag) {
+        // nothing may land after the block has left: one more wait each for what was asked for
+        for (int i = 0; i < stages; ++i) {
+            tc::mbar_wait_drain(&full[i], 0);
+            tc::mbar_wait_drain(&full[i], 1);
+        }
+    }
+    if (!p.partial) return;
+    float* out = p.partial + (int64_t)blockIdx.x * 2 * cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * kWideThreads) * V;
+        if (c >= cols) break;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            *reinterpret_cast<F2*>(out + c + 2 * q) = ag[i][q];
+            *reinterpret_cast<F2*>(out + cols + c + 2 * q) = ab[i][q];
+        }
+    }
 }
 
 // Rows wider than a block's registers hold: dx alone, two passes over the row.
@@ -704,6 +879,17 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     return launch_pdl(forward_kernel<T, V, W, NV * M>, dim3((unsigned)(W == 1 ? ceil_div(p.rows, 4) : p.rows)), \
                       dim3(W == 1 ? 128 : W * 32), 0, s, p)
     if (p.rows <= 0x7fffffff) {
+        if constexpr (V > 1) {
+            // short rows in numbers: a warp takes 8 or more
+            if (n <= 32 && p.rows >= 32 * (int64_t)sm_count) {
+                auto run = [&](auto kernel, int rows) {
+                    return launch_pdl(kernel, dim3((unsigned)ceil_div(p.rows, rows)), dim3(128), 0, s, p);
+                };
+                if (n <= 8) return run(forward_short_kernel<T, 8, 4>, 64);
+                if (n <= 16) return run(forward_short_kernel<T, 16, 4>, 32);
+                return run(forward_short_kernel<T, 32, 4>, 16);
+            }
+        }
         if (n <= 32) OLC_FWD(1, 1);
         if (n <= 64) OLC_FWD(1, 2);
         if (n <= 128 && !few) OLC_FWD(1, 4);
@@ -721,11 +907,13 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     return launch_pdl(forward_long_kernel<T, V>, dim3((unsigned)grid), dim3(1024), 0, s, p);
 }
 
+constexpr int kRingSmem = kAhead * 2 * 512 * 16 * 4;     // rings of the widest float32 rows
+constexpr int64_t kWideSmem = 208 * 1024;   // ring of the wide rows
 constexpr int kColsPerThread = 16;      // float32 column sums of dgamma and dbeta: 32 registers
 
 // the backward launch of one shape: which kernel, how many threads
 struct BwdShape {
-    enum Kind { LONG, RING, ANY } kind = LONG;   // LONG: rows wider than a block's registers
+    enum Kind { LONG, WIDE, RING, ANY } kind = LONG;   // LONG: rows wider than a block's registers
     int per_thread = 0;                          // columns
     int tpr = 0, groups = 1, threads = 0;
     int64_t blocks = 0;
@@ -734,6 +922,13 @@ struct BwdShape {
 template <int V>
 BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
     BwdShape b;
+    constexpr int64_t size = V == 1 ? 0 : 16 / V;
+    if (V > 1 && cols > 512 * kColsPerThread && cols <= kWideThreads * kWideColumns &&
+        4 * cols * size <= kWideSmem && rows >= 2 * (int64_t)sm_count) {
+        b.kind = BwdShape::WIDE;
+        b.blocks = min64(rows, sm_count);
+        return b;
+    }
     if (cols > 512 * kColsPerThread) {
         b.blocks = min64(max64(rows / 64, 1), max64(1, 8 * (int64_t)sm_count * 256 / cols));
         return b;
@@ -744,7 +939,8 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
         b.kind = BwdShape::RING;
         b.per_thread = kColsPerThread;
         b.tpr = b.threads = (int)(ceil_div(ceil_div(cols, kColsPerThread), 32) * 32);
-        b.blocks = min64(rows, (int64_t)sm_count * 2);
+        // two blocks on an SM, more where they are small
+        b.blocks = min64(rows, (int64_t)sm_count * max64(2, min64(8, 512 / b.threads)));
         return b;
     }
     b.kind = BwdShape::ANY;
@@ -754,7 +950,7 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
     b.tpr = (int)(ceil_div(ceil_div(cols, b.per_thread), 32) * 32);
     b.groups = b.tpr >= 256 ? 1 : 256 / b.tpr;
     b.threads = b.tpr * b.groups;
-    b.blocks = max64(1, min64(ceil_div(rows, b.groups), (int64_t)sm_count * (b.threads > 256 ? 1 : 2)));
+    b.blocks = max64(1, min64(ceil_div(rows, b.groups), (int64_t)sm_count * (b.threads > 256 ? 1 : (b.per_thread > 8 ? 2 : 4))));
     return b;
 }
 
@@ -767,10 +963,10 @@ cudaError_t backward_rows(const BwdParams& p, const BwdShape& b, cudaStream_t s)
 template <typename T, int WARPS, bool FULL>
 cudaError_t backward_ring(const BwdParams& p, const BwdShape& b, cudaStream_t s) {
     auto* kernel = backward_ring_kernel<T, kColsPerThread * sizeof(T) / 16, WARPS, FULL>;
-    const int smem = kAhead * 2 * (int)(p.cols * sizeof(T));
-    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), kRingSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3((unsigned)b.blocks), dim3((unsigned)b.threads), (size_t)smem, s, p);
+    return launch_pdl(kernel, dim3((unsigned)b.blocks), dim3((unsigned)b.threads),
+                      kAhead * 2 * (size_t)p.cols * sizeof(T), s, p);
 }
 
 template <typename T, int V>
@@ -786,6 +982,15 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
         if (e == cudaSuccess && p.dX)
             e = launch_pdl(backward_long_rows_kernel<T, V>, dim3((unsigned)min64(p.rows, (int64_t)sm_count * 2)),
                            dim3(1024), 0, s, p);
+    } else if (b.kind == BwdShape::WIDE) {
+        if constexpr (V > 1) {
+            const int64_t row = 2 * p.cols * (int64_t)sizeof(T);
+            const int stages = (int)min64(4, kWideSmem / row);
+            e = set_smem_limit(reinterpret_cast<const void*>(backward_wide_kernel<T>), (int)kWideSmem);
+            if (e == cudaSuccess)
+                e = launch_pdl(backward_wide_kernel<T>, dim3((unsigned)b.blocks), dim3(kWideThreads),
+                               (size_t)(stages * row), s, p, stages);
+        }
     } else if (b.kind == BwdShape::RING) {
         if constexpr (V > 1) {
             const bool full = p.cols == (int64_t)b.threads * kColsPerThread;

@@ -22,6 +22,8 @@ DEPTH = 256
 EPS = 1e-5
 SIZES = [(1, 1), (3, 2), (5, 31), (7, 128), (700, 96), (4, 1001), (33, 4096), (1300, 512), (2, 12000), (9, 16384),
          (3, 20000), (2, 70001), (650, 2049)]
+# shapes of the kernels for many rows: short rows, rings of rows of full and of other widths, wide rows
+MANY = [(5000, 128), (4900, 40), (4870, 256), (700, 1024), (640, 1040), (610, 4096), (320, 12000), (310, 16384)]
 
 
 def reference(x, gamma, beta, eps=EPS):
@@ -65,7 +67,7 @@ def check_forward(x, gamma, beta, dtype, eps=EPS, **kw):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("rows,cols", SIZES + MANY)
 def test_forward(rows, cols, dtype):
     x = normal((rows, cols), dtype, 1, 1.5, 0.25)
     gamma, beta = normal((cols,), dtype, 2, 0.3, 1.0), normal((cols,), dtype, 3, 0.3)
@@ -158,7 +160,7 @@ def check_backward(rows, cols, dtype, pitch=None, offset=0, gamma=True, same=Non
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,cols", SIZES + [(2600, 256), (1, 5000), (3000, 33)])
+@pytest.mark.parametrize("rows,cols", SIZES + MANY + [(2600, 256), (1, 5000), (3000, 33)])
 def test_backward(rows, cols, dtype):
     check_backward(rows, cols, dtype)
 
@@ -171,7 +173,7 @@ def test_backward_pitches_and_offsets(cols, pitch, offset, dtype):
     check_backward(21, cols, dtype, pitch=pitch, offset=offset, same="x")
 
 
-@pytest.mark.parametrize("rows,cols", [(40, 96), (40, 18000), (0, 96)])
+@pytest.mark.parametrize("rows,cols", [(40, 96), (40, 18000), (0, 96), (620, 1040), (320, 10000)])
 def test_backward_in_parts_and_with_no_rows(rows, cols):
     x, dy = normal((rows, cols), "float32", 24).cuda(), normal((rows, cols), "float32", 25).cuda()
     mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
@@ -186,6 +188,12 @@ def test_backward_in_parts_and_with_no_rows(rows, cols):
         if rows == 0:
             plan.forward(x, None, None, x, mean=mean, rstd=rstd)
             assert not whole[1].any() and not whole[2].any()
+
+
+@pytest.mark.parametrize("rows,cols", [(640, 1040), (320, 9000)])
+def test_backward_rings_in_place_and_without_gamma(rows, cols):
+    check_backward(rows, cols, "bfloat16", gamma=False, same="dy")
+    check_backward(rows, cols, "float32", pitch=cols + 8, same="x")
 
 
 def test_backward_repeats_bit_for_bit_on_several_streams():
