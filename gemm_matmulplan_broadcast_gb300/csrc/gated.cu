@@ -24,6 +24,7 @@
 #include <cstring>
 #include <new>
 
+#include "gated_internal.h"
 #include "plan_state.h"
 #include "tc_ptx.cuh"
 
@@ -33,62 +34,6 @@ namespace gated {
 using namespace olc::tc;
 
 enum Mode { FWD = 0, DX = 1, DW = 2 };
-
-// ---- activations ------------------------------------------------------------
-
-// act(g) and act'(g).  EXACT: float32 functions of full accuracy (FLOAT
-// tensors); otherwise the fast forms, good to about 2^-21, for results that
-// are rounded to 16 bits.
-template <bool EXACT>
-__device__ __forceinline__ float sigmoid(float g) {
-    if constexpr (EXACT) return 1.0f / (1.0f + expf(-g));
-    return __fdividef(1.0f, 1.0f + __expf(-g));
-}
-template <bool EXACT>
-__device__ __forceinline__ float gate_value(int act, float g) {
-    switch (act) {
-        case OLC_GATE_SILU: return g * sigmoid<EXACT>(g);
-        case OLC_GATE_GELU:
-            if constexpr (EXACT) return 0.5f * g * erfcf(g * -0.70710678118654752f);
-            return gelu_f32(g);
-        case OLC_GATE_RELU: return g < 0.f ? 0.f : g;
-        default: return sigmoid<EXACT>(g);
-    }
-}
-template <bool EXACT>
-__device__ __forceinline__ void gate_slope(int act, float g, float& value, float& slope) {
-    switch (act) {
-        case OLC_GATE_SILU: {
-            const float s = sigmoid<EXACT>(g);
-            value = g * s;
-            slope = s * (1.0f + g * (1.0f - s));
-            return;
-        }
-        case OLC_GATE_GELU: {
-            // Phi(g) + g phi(g)
-            float cdf, phi;
-            if constexpr (EXACT) {
-                cdf = 0.5f * erfcf(g * -0.70710678118654752f);
-                phi = 0.39894228040143268f * expf(-0.5f * g * g);
-            } else {
-                cdf = 0.5f * gelu_one_plus_erf_f32(g);
-                phi = 0.39894228040143268f * __expf(-0.5f * g * g);
-            }
-            value = g * cdf;
-            slope = fmaf(g, phi, cdf);
-            return;
-        }
-        case OLC_GATE_RELU:
-            value = g < 0.f ? 0.f : g;
-            slope = g > 0.f ? 1.f : 0.f;
-            return;
-        default: {
-            const float s = sigmoid<EXACT>(g);
-            value = s;
-            slope = s * (1.0f - s);
-        }
-    }
-}
 
 // ---- the products on CTA pairs ------------------------------------------------
 
@@ -222,6 +167,7 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    __syncwarp();
     if (warp == 1) pair::tmem_alloc2(&s->tmem_base, TMEM_COLS);
     tc_fence_before();
     pair::cluster_sync();
@@ -302,6 +248,7 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
                     if ((armed_bits >> i) & 1u) mbar_wait_drain(&s->full[i], (parity_bits >> i) & 1u);
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && leader) {
             const uint32_t idesc = instr_desc(p.is_bf16, 256, 256, p.a_mn, p.b_k ? 0 : 1);
@@ -339,6 +286,7 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
             pair::commit2_local(&s->drain);
             mbar_wait_drain(&s->drain, 0);
         }
+        __syncwarp();
     } else {
         const int lane_group = warp & 3;
         const uint32_t acc_empty_leader[2] = {pair::map_to(&s->acc_empty[0], 0), pair::map_to(&s->acc_empty[1], 0)};
@@ -348,7 +296,8 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
             int slice, item;
             int64_t mb, nb;
             coords(u, slice, item, mb, nb);
-            if (!mbar_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err)) break;
+            const bool ok = mbar_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err);
+            if (!__all_sync(0xffffffffu, ok)) break;      // the warp stays together for tcgen05.ld
             tc_fence_after();
             const int64_t row0 = mb * 256 + rank * 128 + lane_group * 32;     // the warp's first row
             const uint32_t t_base = tmem_base + ((uint32_t)(lane_group * 32) << 16) + acc * 256;
@@ -415,6 +364,7 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
 
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
     pair::cluster_sync();          // no remote arrival may target a CTA that has left
     tc_fence_after();
@@ -509,13 +459,6 @@ __global__ void __launch_bounds__(256) product_kernel(const float* G, const floa
 constexpr int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// A stored matrix of 16-bit elements the TMA can read: base on a 16-byte
-// boundary, pitch a multiple of 8.
-struct Stored {
-    const void* base;
-    int64_t rows, cols, pitch;
-};
-
 // A product's K slices: enough that its units fill the pairs, each slice at
 // least four K blocks.
 int slices_of(int64_t tiles, int64_t k_total, int sm_count) {
@@ -525,15 +468,6 @@ int slices_of(int64_t tiles, int64_t k_total, int sm_count) {
     if (want < 2) return 1;
     return (int)ceil_div(k_total, ceil_div(k_total, want));    // no empty slice
 }
-
-struct Product {
-    int mode;
-    int64_t M, N, K;
-    Stored a[2], b[2];
-    bool a_mn, b_k;
-    void* Y[3];
-    int act;
-};
 
 int64_t tiles_of(int mode, int64_t M, int64_t N) {
     return ceil_div(M, 256) * ceil_div(N, mode == FWD ? 128 : 256) * (mode == DW ? 2 : 1);
@@ -705,7 +639,8 @@ olc_status forward16(olc_gated_plan* p, const void* X, const void* Wg, const voi
                      cudaStream_t s) {
     const int64_t wr = p->trans_w ? p->F : p->D, wc = p->trans_w ? p->D : p->F;
     Operand x(X, p->M, p->D), wg(Wg, wr, wc), wu(Wu, wr, wc);
-    const size_t partial = gated::product_partial_bytes(gated::FWD, p->M, p->F, p->D, p->state.sm_count);
+    const bool few = p->M <= gated::kFewRows;
+    const size_t partial = few ? 0 : gated::product_partial_bytes(gated::FWD, p->M, p->F, p->D, p->state.sm_count);
     float* part = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
         Pieces m;
@@ -737,7 +672,9 @@ olc_status forward16(olc_gated_plan* p, const void* X, const void* Wg, const voi
     w.Y[1] = G;
     w.Y[2] = U;
     w.act = p->act;
-    if (e == cudaSuccess) e = gated::launch_product<gated::FWD>(p->dtype, w, part, p->state.sm_count, s);
+    if (e == cudaSuccess)
+        e = few ? gated::launch_few(p->dtype, w, p->state.sm_count, s)
+                : gated::launch_product<gated::FWD>(p->dtype, w, part, p->state.sm_count, s);
     if (e == cudaSuccess && uses) e = p->state.after_use(s);
     return plan_status(e);
 }

@@ -1,0 +1,89 @@
+// What the kernels of the gated feed-forward product share: the activations
+// and how a product is described.
+#pragma once
+
+#include "common.cuh"
+
+namespace olc {
+namespace gated {
+
+// ---- activations ------------------------------------------------------------
+
+// act(g) and act'(g).  EXACT: float32 functions of full accuracy (FLOAT
+// tensors); otherwise the fast forms, good to about 2^-21, for results that
+// are rounded to 16 bits.
+template <bool EXACT>
+__device__ __forceinline__ float sigmoid(float g) {
+    if constexpr (EXACT) return 1.0f / (1.0f + expf(-g));
+    return __fdividef(1.0f, 1.0f + __expf(-g));
+}
+template <bool EXACT>
+__device__ __forceinline__ float gate_value(int act, float g) {
+    switch (act) {
+        case OLC_GATE_SILU: return g * sigmoid<EXACT>(g);
+        case OLC_GATE_GELU:
+            if constexpr (EXACT) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+            return gelu_f32(g);
+        case OLC_GATE_RELU: return g < 0.f ? 0.f : g;
+        default: return sigmoid<EXACT>(g);
+    }
+}
+template <bool EXACT>
+__device__ __forceinline__ void gate_slope(int act, float g, float& value, float& slope) {
+    switch (act) {
+        case OLC_GATE_SILU: {
+            const float s = sigmoid<EXACT>(g);
+            value = g * s;
+            slope = s * (1.0f + g * (1.0f - s));
+            return;
+        }
+        case OLC_GATE_GELU: {
+            // Phi(g) + g phi(g)
+            float cdf, phi;
+            if constexpr (EXACT) {
+                cdf = 0.5f * erfcf(g * -0.70710678118654752f);
+                phi = 0.39894228040143268f * expf(-0.5f * g * g);
+            } else {
+                cdf = 0.5f * gelu_one_plus_erf_f32(g);
+                phi = 0.39894228040143268f * __expf(-0.5f * g * g);
+            }
+            value = g * cdf;
+            slope = fmaf(g, phi, cdf);
+            return;
+        }
+        case OLC_GATE_RELU:
+            value = g < 0.f ? 0.f : g;
+            slope = g > 0.f ? 1.f : 0.f;
+            return;
+        default: {
+            const float s = sigmoid<EXACT>(g);
+            value = s;
+            slope = s * (1.0f - s);
+        }
+    }
+}
+
+// ---- products -------------------------------------------------------------------
+
+// A stored matrix of 16-bit elements the TMA can read: base on a 16-byte
+// boundary, pitch a multiple of 8.
+struct Stored {
+    const void* base;
+    int64_t rows, cols, pitch;
+};
+
+struct Product {
+    int mode;
+    int64_t M, N, K;
+    Stored a[2], b[2];
+    bool a_mn, b_k;
+    void* Y[3];
+    int act;
+};
+
+// few rows (w.M <= kFewRows), FWD operands: gated_few.cu
+constexpr int kFewRows = 64;
+cudaError_t launch_few(olc_dtype dt, const Product& w, int sm_count, cudaStream_t s);
+
+}  // namespace gated
+}  // namespace olc

@@ -44,7 +44,7 @@ def _rows(name, t, rows, cols, dtype):
     if t.dtype is not dtype:
         raise TypeError("%s has dtype %s, the plan wants %s" % (name, t.dtype, dtype))
     shape = t.shape
-    if shape == (rows, cols) and t.is_cuda:      # the usual case
+    if cols and shape == (rows, cols) and t.is_cuda:      # the usual case
         pitch, unit = t.stride()
         if unit == 1 and pitch >= cols:
             return t.data_ptr(), pitch
