@@ -139,9 +139,30 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int is_bf16) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 32 columns of g and u (accumulators) to packed h, g and u
+__device__ __forceinline__ void gate_run(const Params& p, const uint32_t (&g)[32], const uint32_t (&x)[32], uint32_t* ph,
+                                         uint32_t* pg, uint32_t* pu) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
+        const float u0 = __uint_as_float(x[2 * i]), u1 = __uint_as_float(x[2 * i + 1]);
+        ph[i] = pack16(gate_value<false>(p.act, g0) * u0, gate_value<false>(p.act, g1) * u1, p.is_bf16);
+        pg[i] = pack16(g0, g1, p.is_bf16);
+        pu[i] = pack16(u0, u1, p.is_bf16);
+    }
+}
+__device__ __forceinline__ void store_gated(const Params& p, uint32_t* rows, const uint32_t (&ph)[32],
+                                            const uint32_t (&pg)[32], const uint32_t (&pu)[32], int lane, int64_t row0,
+                                            int64_t col0) {
+    store_run(p, p.Y[0], rows, ph, lane, row0, col0);
+    if (p.Y[1]) store_run(p, p.Y[1], rows, pg, lane, row0, col0);
+    if (p.Y[2]) store_run(p, p.Y[2], rows, pu, lane, row0, col0);
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
-pair_kernel(const __grid_constant__ Maps maps, const Params p) {
+pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ CUtensorMap map_a1,
+            const __grid_constant__ CUtensorMap map_b0, const __grid_constant__ CUtensorMap map_b1, const Params p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* base =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -173,8 +194,6 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
     pair::cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = s->tmem_base;
-    grid_dependency_wait();
-    grid_launch_dependents();
 
     // unit -> K slice, output, tile (groups of RASTER pair rows, rows fastest)
     const int64_t per_item = p.tiles_m * p.tiles_n;
@@ -194,6 +213,9 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
     if (warp == 0 || warp == 6) {
         if (lane == 0) {
             const bool load_a = warp == 0;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(load_a ? &map_a0 : &map_b0)) : "memory");
+            if (MODE != FWD || !load_a)
+                asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(load_a ? &map_a1 : &map_b1)) : "memory");
             const uint32_t stage0 = smem_u32(base);
             const uint32_t full0_leader = pair::map_to(&s->full[0], 0);
             uint32_t stage = 0, phase = 0, armed_bits = 0, parity_bits = 0;
@@ -208,14 +230,13 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
                 const uint32_t tx = load_a ? 2u * A_BYTES : 2u * B_BYTES;
                 for (int64_t kb = kb0; kb < kb1; ++kb) {
                     // which operand pair, and where along its K
-                    int which = MODE == DW ? item : 0;
+                    int which = MODE == DW ? item : (MODE == FWD && !load_a ? (int)rank : 0);
                     int k0 = (int)kb * BK;
                     if (MODE == DX && kb >= p.k_blocks) {
                         which = 1;
                         k0 = (int)(kb - p.k_blocks) * BK;
                     }
-                    const CUtensorMap* map = load_a ? &maps.a[MODE == FWD ? 0 : which]
-                                                    : &maps.b[MODE == FWD ? (int)rank : which];
+                    const CUtensorMap* map = load_a ? (which ? &map_a1 : &map_a0) : (which ? &map_b1 : &map_b0);
                     if (!mbar_wait(&s->empty[stage], phase ^ 1, abort_flag, p.err)) { ok = false; break; }
                     const uint32_t sa = stage0 + stage * STAGE_BYTES;
                     const uint32_t sb = sa + A_BYTES;
@@ -322,21 +343,11 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
                         uint32_t g[32], x[32];
                         tmem_ld_32x32b_x32(t_base + c + hh * 32, g);
                         tmem_ld_32x32b_x32(t_base + 128 + c + hh * 32, x);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
-                            const float u0 = __uint_as_float(x[2 * i]), u1 = __uint_as_float(x[2 * i + 1]);
-                            ph[hh * 16 + i] = pack16(gate_value<false>(p.act, g0) * u0,
-                                                     gate_value<false>(p.act, g1) * u1, p.is_bf16);
-                            pg[hh * 16 + i] = pack16(g0, g1, p.is_bf16);
-                            pu[hh * 16 + i] = pack16(u0, u1, p.is_bf16);
-                        }
+                        gate_run(p, g, x, ph + hh * 16, pg + hh * 16, pu + hh * 16);
                     }
                     const int64_t col0 = nb * 128 + c;
                     if (row0 >= p.M || col0 >= p.N) continue;
-                    store_run(p, p.Y[0], rows, ph, lane, row0, col0);
-                    if (p.Y[1]) store_run(p, p.Y[1], rows, pg, lane, row0, col0);
-                    if (p.Y[2]) store_run(p, p.Y[2], rows, pu, lane, row0, col0);
+                    store_gated(p, rows, ph, pg, pu, lane, row0, col0);
                 }
             } else {
 #pragma unroll 1
@@ -371,13 +382,183 @@ pair_kernel(const __grid_constant__ Maps maps, const Params p) {
     if (warp == 1) pair::tmem_dealloc2(tmem_base, TMEM_COLS);
 }
 
+// ---- FWD on single CTAs -----------------------------------------------------------
+
+// 128 rows x 64 columns of both products a CTA (one 128 x 128 accumulator): a
+// quarter of the pair's tile, for products whose pair tiles would leave SMs
+// idle or make a last round of few.  Operands pass through shared memory at
+// its full bandwidth here (both CTAs of a pair share B), so large products
+// keep the pairs.
+namespace single {
+
+constexpr int COLS = 64;
+constexpr int A_BYTES1 = 128 * BK * 2;
+constexpr int W_BYTES1 = BK * COLS * 2;
+constexpr int STAGE1 = A_BYTES1 + 2 * W_BYTES1;     // 32 KiB
+constexpr int THREADS1 = 192;                       // loader, MMA, 4 epilogue warps
+constexpr int TMEM1 = 256;                          // two accumulators
+static_assert(STAGE1 == STAGE_BYTES, "the pair's ring and staging sizes hold");
+
+}  // namespace single
+
+__global__ void __launch_bounds__(single::THREADS1, 1)
+single_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
+              const __grid_constant__ CUtensorMap map_u, const Params p) {
+    using namespace single;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* base =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint32_t* staging = reinterpret_cast<uint32_t*>(base + STAGES * STAGE1);
+    Barriers* s = reinterpret_cast<Barriers*>(base + STAGES * STAGE1 + STAGING_BYTES);
+    volatile int* abort_flag = &s->abort_flag;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&s->full[i], 1);
+            mbar_init(&s->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s->acc_full[i], 1);
+            mbar_init(&s->acc_empty[i], 4);
+        }
+        mbar_init(&s->drain, 1);
+        s->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncwarp();
+    if (warp == 1) tmem_alloc(&s->tmem_base, TMEM1);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = s->tmem_base;
+
+    // unit -> K slice, tile (rows fastest: the row tiles of a column share its weights in L2)
+    auto coords = [&](int64_t u, int& slice, int64_t& mb, int64_t& nb) {
+        slice = (int)(u % p.splits);
+        const int64_t t = u / p.splits;
+        mb = t % p.tiles_m;
+        nb = t / p.tiles_m;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0, armed = 0, parity = 0;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+                int slice;
+                int64_t mb, nb;
+                coords(u, slice, mb, nb);
+                const int m0 = (int)(mb * 128), n0 = (int)(nb * COLS);
+                const int64_t kb0 = slice * p.k_slice, kb1 = min64(p.k_total, kb0 + p.k_slice);
+                for (int64_t kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&s->empty[stage], phase ^ 1, abort_flag, p.err)) { ok = false; break; }
+                    const uint32_t sa = smem_u32(base) + stage * STAGE1, bar = smem_u32(&s->full[stage]);
+                    const int k0 = (int)kb * BK;
+                    mbar_arrive_expect_tx(&s->full[stage], STAGE1);
+                    armed |= 1u << stage;
+                    parity = (parity & ~(1u << stage)) | (phase << stage);
+                    tma_load_3d(sa + A_BYTES1, &map_g, bar, p.b_k ? k0 : n0, p.b_k ? n0 : k0, 0);
+                    tma_load_3d(sa + A_BYTES1 + W_BYTES1, &map_u, bar, p.b_k ? k0 : n0, p.b_k ? n0 : k0, 0);
+                    tma_load_3d(sa, &map_x, bar, k0, m0, 0);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (*abort_flag)
+                for (int i = 0; i < STAGES; ++i)
+                    if ((armed >> i) & 1u) mbar_wait_drain(&s->full[i], (parity >> i) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = instr_desc(p.is_bf16, 128, 2 * COLS, 0, p.b_k ? 0 : 1);
+            const uint32_t stage0 = smem_u32(base);
+            const uint64_t a_desc0 = smem_desc(stage0, 16, 1024, 2u);
+            const uint64_t b_desc0 = p.b_k ? smem_desc(stage0 + A_BYTES1, 16, 1024, 2u)
+                                           : smem_desc(stage0 + A_BYTES1, W_BYTES1, 1024, 2u);
+            const uint64_t a_step = (UMMA_K * 2) >> 4;
+            const uint64_t b_step = p.b_k ? (UMMA_K * 2) >> 4 : (UMMA_K * 128) >> 4;
+            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; u < p.units && ok; u += gridDim.x) {
+                const int64_t kb0 = (u % p.splits) * p.k_slice, kb1 = min64(p.k_total, kb0 + p.k_slice);
+                if (!mbar_wait(&s->acc_empty[acc], acc_phase ^ 1, abort_flag, p.err)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * 128;
+                uint32_t first = 0u;
+                for (int64_t kb = kb0; kb < kb1; ++kb) {
+                    if (!mbar_wait(&s->full[stage], phase, abort_flag, p.err)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t so = (uint64_t)((stage * STAGE1) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                        mma_f16(d_tmem, a_desc0 + so + kk * a_step, b_desc0 + so + kk * b_step, idesc,
+                                kk > 0 ? 1u : first);
+                    first = 1u;
+                    mma_commit(&s->empty[stage]);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                mma_commit(&s->acc_full[acc]);
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            }
+            mma_commit(&s->drain);
+            mbar_wait_drain(&s->drain, 0);
+        }
+        __syncwarp();
+    } else {
+        const int lane_group = warp & 3;
+        uint32_t* rows = staging + lane_group * 32 * STAGE_PITCH;
+        uint32_t acc = 0, acc_phase = 0;
+        for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+            int slice;
+            int64_t mb, nb;
+            coords(u, slice, mb, nb);
+            const bool ok = mbar_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err);
+            if (!__all_sync(0xffffffffu, ok)) break;      // the warp stays together for tcgen05.ld
+            tc_fence_after();
+            const int64_t row0 = mb * 128 + lane_group * 32, col0 = nb * COLS;
+            const uint32_t t_base = tmem_base + ((uint32_t)(lane_group * 32) << 16) + acc * 128;
+            if (p.splits > 1) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(t_base + c, r);
+                    const int64_t col = col0 + (c & 63);
+                    if (row0 >= p.M || col >= p.N) continue;
+                    store_partial(p, p.partial + ((int64_t)slice * 2 + (c >> 6)) * p.M * p.partial_pitch, rows, r, lane,
+                                  row0, col);
+                }
+            } else {
+                uint32_t ph[32], pg[32], pu[32];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t g[32], x[32];
+                    tmem_ld_32x32b_x32(t_base + hh * 32, g);
+                    tmem_ld_32x32b_x32(t_base + COLS + hh * 32, x);
+                    gate_run(p, g, x, ph + hh * 16, pg + hh * 16, pu + hh * 16);
+                }
+                if (row0 < p.M) store_gated(p, rows, ph, pg, pu, lane, row0, col0);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s->acc_empty[acc]);
+            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, TMEM1);
+}
+
 // ---- elementwise passes ---------------------------------------------------------
 
 // Slices summed in slice order; FWD: h, g and u from the two planes' sums.
 template <typename T>
 __global__ void __launch_bounds__(256) join_kernel(const Params p, int mode) {
-    grid_dependency_wait();
-    grid_launch_dependents();
     const int planes = mode == DX ? 1 : 2;
     const int64_t groups = ceil_div(p.N, 4), plane_elems = p.M * p.partial_pitch;
     const int64_t n = p.M * groups * (mode == DW ? 2 : 1);
@@ -424,8 +605,6 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dH, const T* G, con
                                                     int64_t cols, int64_t pitch, int act) {
     struct alignas(V * sizeof(T)) Pack { T v[V]; };
     constexpr bool EXACT = sizeof(T) == 4;
-    grid_dependency_wait();
-    grid_launch_dependents();
     const int64_t groups = cols / V;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < rows * groups; e += (int64_t)gridDim.x * 256) {
         const int64_t row = e / groups, col = e % groups * V;
@@ -448,8 +627,6 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dH, const T* G, con
 
 // FLOAT: h = act(g) u; h may be u
 __global__ void __launch_bounds__(256) product_kernel(const float* G, const float* U, float* H, int64_t n, int act) {
-    grid_dependency_wait();
-    grid_launch_dependents();
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256)
         H[e] = gate_value<true>(act, G[e]) * U[e];
 }
@@ -459,33 +636,55 @@ __global__ void __launch_bounds__(256) product_kernel(const float* G, const floa
 constexpr int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// A product's K slices: enough that its units fill the pairs, each slice at
-// least four K blocks.
-int slices_of(int64_t tiles, int64_t k_total, int sm_count) {
-    const int64_t pairs = sm_count / 2;
-    if (tiles <= 0 || 2 * tiles > pairs) return 1;
-    const int64_t want = min64(pairs / tiles, k_total / 4);
+// K slices of a product whose units fill `slots` (CTA pairs, or SMs) at most
+// half: enough to fill them, each slice at least four K blocks.
+int slices_of(int64_t tiles, int64_t k_total, int64_t slots) {
+    if (tiles <= 0 || 2 * tiles > slots) return 1;
+    const int64_t want = min64(slots / tiles, k_total / 4);
     if (want < 2) return 1;
     return (int)ceil_div(k_total, ceil_div(k_total, want));    // no empty slice
 }
 
-int64_t tiles_of(int mode, int64_t M, int64_t N) {
-    return ceil_div(M, 256) * ceil_div(N, mode == FWD ? 128 : 256) * (mode == DW ? 2 : 1);
-}
-int product_slices(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
-    return slices_of(tiles_of(mode, M, N), ceil_div(K, BK) * (mode == DX ? 2 : 1), sm_count);
+// How a product is cut: on CTA pairs or (FWD) single CTAs, into how many tiles
+// and K slices.
+struct Cut {
+    bool single;
+    int64_t tiles_m, tiles_n;
+    int splits;
+};
+Cut cut_of(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
+    const int64_t kb = ceil_div(K, BK), pairs = sm_count / 2;
+    Cut c{false, ceil_div(M, 256), ceil_div(N, mode == FWD ? 128 : 256), 1};
+    if (mode == FWD) {
+        // rounds over the machine x the time of a unit: per K block 512 cycles
+        // of a pair's MMAs, half of that on a single CTA (a sixth more while
+        // shared memory feeds both operands to one SM), and about 3000 and
+        // 2000 cycles of a unit's fill and epilogue that nothing hides
+        const int64_t sm_tiles = ceil_div(M, 128) * ceil_div(N, single::COLS);
+        const int64_t on_pairs = ceil_div(c.tiles_m * c.tiles_n, pairs) * (kb * 512 + 3000);
+        const int64_t on_sms = ceil_div(sm_tiles, sm_count) * (kb * 300 + 2000);
+        if (on_sms < on_pairs) {
+            c = Cut{true, ceil_div(M, 128), ceil_div(N, single::COLS), slices_of(sm_tiles, kb, sm_count)};
+            return c;
+        }
+    }
+    c.splits = slices_of(c.tiles_m * c.tiles_n * (mode == DW ? 2 : 1), kb * (mode == DX ? 2 : 1), pairs);
+    return c;
 }
 size_t product_partial_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
-    const int s = product_slices(mode, M, N, K, sm_count);
+    const int s = cut_of(mode, M, N, K, sm_count).splits;
     return s > 1 ? (size_t)s * (mode == DX ? 1 : 2) * (size_t)M * (size_t)pad8(N) * sizeof(float) : 0;
 }
 
 template <int MODE>
 cudaError_t launch_product(olc_dtype dt, const Product& w, float* partial, int sm_count, cudaStream_t s) {
     const int bf = dt == OLC_BFLOAT16;
+    const Cut cut = cut_of(MODE, w.M, w.N, w.K, sm_count);
+    // rows of a box of a K-major operand B
+    const uint32_t b_rows = cut.single ? single::COLS : 128;
     Maps maps;
     std::memset(&maps, 0, sizeof maps);
-    bool blocks = !w.b_k;
+    bool blocks = !w.b_k && !cut.single;
     for (int i = 0; i < 2 && blocks; ++i)
         blocks = w.N % 64 == 0 && encode_b_blocks(&maps.b[i], w.b[i].base, bf, w.N, w.K, 1, w.b[i].pitch);
     for (int i = 0; i < 2; ++i) {
@@ -494,7 +693,7 @@ cudaError_t launch_product(olc_dtype dt, const Product& w, float* partial, int s
                                              CU_TENSOR_MAP_SWIZZLE_128B, a.pitch)
                                  : encode_3d(&maps.a[i], a.base, bf, a.cols, a.rows, 1, BK, 128,
                                              CU_TENSOR_MAP_SWIZZLE_128B, a.pitch);
-        const bool ok_b = blocks || (w.b_k ? encode_3d(&maps.b[i], b.base, bf, b.cols, b.rows, 1, BK, 128,
+        const bool ok_b = blocks || (w.b_k ? encode_3d(&maps.b[i], b.base, bf, b.cols, b.rows, 1, BK, b_rows,
                                                        CU_TENSOR_MAP_SWIZZLE_128B, b.pitch)
                                            : encode_3d(&maps.b[i], b.base, bf, b.cols, b.rows, 1, 64, BK,
                                                        CU_TENSOR_MAP_SWIZZLE_128B, b.pitch));
@@ -504,12 +703,12 @@ cudaError_t launch_product(olc_dtype dt, const Product& w, float* partial, int s
     std::memset(&p, 0, sizeof p);
     p.M = w.M;
     p.N = w.N;
-    p.tiles_m = ceil_div(w.M, 256);
-    p.tiles_n = ceil_div(w.N, MODE == FWD ? 128 : 256);
+    p.tiles_m = cut.tiles_m;
+    p.tiles_n = cut.tiles_n;
     p.items = MODE == DW ? 2 : 1;
     p.k_blocks = ceil_div(w.K, BK);
     p.k_total = p.k_blocks * (MODE == DX ? 2 : 1);
-    p.splits = product_slices(MODE, w.M, w.N, w.K, sm_count);
+    p.splits = cut.splits;
     p.k_slice = ceil_div(p.k_total, p.splits);
     p.units = p.tiles_m * p.tiles_n * p.items * p.splits;
     p.a_mn = w.a_mn;
@@ -525,29 +724,34 @@ cudaError_t launch_product(olc_dtype dt, const Product& w, float* partial, int s
     p.partial = partial;
     p.partial_pitch = pad8(w.N);
     p.err = device_error_word();
-    cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(pair_kernel<MODE>), SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    const int64_t clusters = min64(p.units, sm_count / 2);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * clusters));
-    cfg.blockDim = dim3(PAIR_THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, pair_kernel<MODE>, maps, p);
+    cudaError_t e;
+    if (cut.single) {
+        e = set_smem_limit(reinterpret_cast<const void*>(single_kernel), SMEM_BYTES);
+        if (e == cudaSuccess)
+            e = plan_launch(single_kernel, dim3((unsigned)min64(p.units, sm_count)), dim3(single::THREADS1),
+                           (size_t)SMEM_BYTES, s, maps.a[0], maps.b[0], maps.b[1], p);
+    } else {
+        e = set_smem_limit(reinterpret_cast<const void*>(pair_kernel<MODE>), SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(2 * min64(p.units, sm_count / 2)));
+        cfg.blockDim = dim3(PAIR_THREADS);
+        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, pair_kernel<MODE>, maps.a[0], maps.a[1], maps.b[0], maps.b[1], p);
+    }
     if (e != cudaSuccess || p.splits == 1) return e;
     const int64_t work = p.M * ceil_div(p.N, 4) * p.items;
     const dim3 grid((unsigned)min64(ceil_div(work, 256), (int64_t)sm_count * 8));
-    return bf ? launch_pdl(join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p, MODE)
-              : launch_pdl(join_kernel<__half>, grid, dim3(256), 0, s, p, MODE);
+    return bf ? plan_launch(join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p, (int)MODE)
+              : plan_launch(join_kernel<__half>, grid, dim3(256), 0, s, p, (int)MODE);
 }
 
 template <typename T>
@@ -557,8 +761,8 @@ cudaError_t launch_slope(const void* dH, const void* G, const void* U, void* dG,
     const bool wide = cols % V == 0 && plan_aligned16(dH) && plan_aligned16(G) && plan_aligned16(U);
     const dim3 grid((unsigned)min64(ceil_div(rows * (wide ? cols / V : cols), 256), (int64_t)sm_count * 16));
     auto run = [&](auto kernel) {
-        return launch_pdl(kernel, grid, dim3(256), 0, s, static_cast<const T*>(dH), static_cast<const T*>(G),
-                          static_cast<const T*>(U), static_cast<T*>(dG), static_cast<T*>(dU), rows, cols, pitch, act);
+        return plan_launch(kernel, grid, dim3(256), 0, s, static_cast<const T*>(dH), static_cast<const T*>(G),
+                           static_cast<const T*>(U), static_cast<T*>(dG), static_cast<T*>(dU), rows, cols, pitch, act);
     };
     return wide ? run(slope_kernel<T, V>) : run(slope_kernel<T, 1>);
 }
@@ -765,9 +969,9 @@ olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const voi
     st = olc_gemm_execute(p->forward, X, Wg, nullptr, g, s);
     if (st == OLC_OK) st = olc_gemm_execute(p->forward, X, Wu, nullptr, u, s);
     if (st != OLC_OK) return st;
-    cudaError_t e = launch_pdl(gated::product_kernel, dim3((unsigned)min64(ceil_div(n, 256), (int64_t)p->state.sm_count * 16)),
-                               dim3(256), 0, s, static_cast<const float*>(g), static_cast<const float*>(u),
-                               static_cast<float*>(H), n, p->act);
+    cudaError_t e = plan_launch(gated::product_kernel, dim3((unsigned)min64(ceil_div(n, 256), (int64_t)p->state.sm_count * 16)),
+                                dim3(256), 0, s, static_cast<const float*>(g), static_cast<const float*>(u),
+                                static_cast<float*>(H), n, p->act);
     if (e == cudaSuccess && !G) e = p->state.after_use(s);
     return plan_status(e);
 }

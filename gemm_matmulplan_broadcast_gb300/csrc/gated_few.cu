@@ -139,8 +139,6 @@ kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     __syncthreads();
-    grid_dependency_wait();
-    grid_launch_dependents();
     const int64_t kb0 = p.k_blocks * rank / cl, kb1 = p.k_blocks * (rank + 1) / cl;
     const uint32_t ring = smem_u32(base);
     float acc[2][NT][4];
@@ -327,15 +325,13 @@ cudaError_t launch_as(const Product& w, int sm_count, cudaStream_t s) {
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, k, mx, mg, mu, p);
 }
 

@@ -227,8 +227,6 @@ forward_kernel(const FwdParams p) {
     __shared__ float slots[2][W];
     const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
-    grid_dependency_wait();
-    grid_launch_dependents();
     if (row >= p.rows) return;      // whole warps (W == 1); never with W > 1
     const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
     T* y = static_cast<T*>(p.Y) + row * p.y_pitch;
@@ -294,8 +292,6 @@ forward_kernel(const FwdParams p) {
 template <typename T, int L, int R>
 __global__ void __launch_bounds__(128) forward_short_kernel(const FwdParams p) {
     constexpr int V = 16 / sizeof(T), P = V / 2, ROWS = 128 / L;
-    grid_dependency_wait();
-    grid_launch_dependents();
     const int c = (int)(threadIdx.x % L) * V;
     const bool in = c < (int)p.cols;
     const int64_t first = (int64_t)blockIdx.x * (ROWS * R) + threadIdx.x / L;
@@ -349,8 +345,6 @@ __global__ void __launch_bounds__(128) forward_short_kernel(const FwdParams p) {
 template <typename T, int V>
 __global__ void __launch_bounds__(1024) forward_long_kernel(const FwdParams p) {
     __shared__ float slots[2][32];
-    grid_dependency_wait();
-    grid_launch_dependents();
     const T* gamma = static_cast<const T*>(p.gamma);
     const T* beta = static_cast<const T*>(p.beta);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -464,8 +458,6 @@ __global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
     const int groups = blockDim.x / tpr, warps = tpr >> 5;
     const int grp = threadIdx.x / tpr, t = threadIdx.x - grp * tpr;
     const int cols = (int)p.cols;
-    grid_dependency_wait();
-    grid_launch_dependents();
     typename C::Raw kx[NV], kd[NV];
     F2 ag[NV][P], ab[NV][P], g[NV][P], xh[NV][P], dxh[NV][P];
 #pragma unroll
@@ -587,8 +579,6 @@ __global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdPara
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     __syncthreads();
-    grid_dependency_wait();
-    grid_launch_dependents();
     auto fetch = [&](int64_t row, int stage) {    // one thread
         if (row >= p.rows) return;
         unsigned char* to = ring + (size_t)stage * 2 * row_bytes;
@@ -678,8 +668,6 @@ __global__ void __launch_bounds__(kWideThreads) backward_wide_kernel(const BwdPa
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     __syncthreads();
-    grid_dependency_wait();
-    grid_launch_dependents();
     auto fetch = [&](int64_t row, int stage) {    // one thread
         if (row >= p.rows) return;
         unsigned char* to = ring + (size_t)stage * 2 * row_bytes;
@@ -780,8 +768,6 @@ __global__ void __launch_bounds__(kWideThreads) backward_wide_kernel(const BwdPa
 template <typename T, int V>
 __global__ void __launch_bounds__(1024) backward_long_rows_kernel(const BwdParams p) {
     __shared__ float slots[2][32];
-    grid_dependency_wait();
-    grid_launch_dependents();
     const T* gamma = static_cast<const T*>(p.gamma);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
@@ -810,8 +796,6 @@ __global__ void __launch_bounds__(1024) backward_long_rows_kernel(const BwdParam
 // a thread one column.
 template <typename T>
 __global__ void __launch_bounds__(256) backward_long_cols_kernel(const BwdParams p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= p.cols) return;
     const int64_t r0 = p.rows * blockIdx.y / gridDim.y, r1 = p.rows * (blockIdx.y + 1) / gridDim.y;
@@ -832,8 +816,6 @@ template <typename T>
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int blocks, int64_t cols,
                                                           T* dgamma, T* dbeta) {
     __shared__ float sums[32][33];
-    grid_dependency_wait();
-    grid_launch_dependents();
     T* out = blockIdx.y ? dbeta : dgamma;
     if (!out) return;
     const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
@@ -876,14 +858,14 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     constexpr int M = V == 1 ? 2 : 1;
     const bool few = p.rows < 4 * (int64_t)sm_count;
 #define OLC_FWD(W, NV)                                                                                          \
-    return launch_pdl(forward_kernel<T, V, W, NV * M>, dim3((unsigned)(W == 1 ? ceil_div(p.rows, 4) : p.rows)), \
+    return plan_launch(forward_kernel<T, V, W, NV * M>, dim3((unsigned)(W == 1 ? ceil_div(p.rows, 4) : p.rows)), \
                       dim3(W == 1 ? 128 : W * 32), 0, s, p)
     if (p.rows <= 0x7fffffff) {
         if constexpr (V > 1) {
             // short rows in numbers: a warp takes 8 or more
             if (n <= 32 && p.rows >= 32 * (int64_t)sm_count) {
                 auto run = [&](auto kernel, int rows) {
-                    return launch_pdl(kernel, dim3((unsigned)ceil_div(p.rows, rows)), dim3(128), 0, s, p);
+                    return plan_launch(kernel, dim3((unsigned)ceil_div(p.rows, rows)), dim3(128), 0, s, p);
                 };
                 if (n <= 8) return run(forward_short_kernel<T, 8, 4>, 64);
                 if (n <= 16) return run(forward_short_kernel<T, 16, 4>, 32);
@@ -904,7 +886,7 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     }
 #undef OLC_FWD
     const int64_t grid = min64(p.rows, (int64_t)sm_count * 2);
-    return launch_pdl(forward_long_kernel<T, V>, dim3((unsigned)grid), dim3(1024), 0, s, p);
+    return plan_launch(forward_long_kernel<T, V>, dim3((unsigned)grid), dim3(1024), 0, s, p);
 }
 
 constexpr int kRingSmem = kAhead * 2 * 512 * 16 * 4;     // rings of the widest float32 rows
@@ -957,7 +939,7 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
 template <typename T, int V, int NV>
 cudaError_t backward_rows(const BwdParams& p, const BwdShape& b, cudaStream_t s) {
     const size_t smem = b.groups > 1 ? (size_t)b.groups * p.cols * sizeof(float) : 0;
-    return launch_pdl(backward_kernel<T, V, NV>, dim3((unsigned)b.blocks), dim3((unsigned)b.threads), smem, s, p);
+    return plan_launch(backward_kernel<T, V, NV>, dim3((unsigned)b.blocks), dim3((unsigned)b.threads), smem, s, p);
 }
 
 template <typename T, int WARPS, bool FULL>
@@ -965,7 +947,7 @@ cudaError_t backward_ring(const BwdParams& p, const BwdShape& b, cudaStream_t s)
     auto* kernel = backward_ring_kernel<T, kColsPerThread * sizeof(T) / 16, WARPS, FULL>;
     const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), kRingSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3((unsigned)b.blocks), dim3((unsigned)b.threads),
+    return plan_launch(kernel, dim3((unsigned)b.blocks), dim3((unsigned)b.threads),
                       kAhead * 2 * (size_t)p.cols * sizeof(T), s, p);
 }
 
@@ -977,10 +959,10 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
     if (b.kind == BwdShape::LONG) {
         // the column sums first: dX may be dY or X
         if (p.partial)
-            e = launch_pdl(backward_long_cols_kernel<T>, dim3((unsigned)ceil_div(p.cols, 256), (unsigned)b.blocks),
+            e = plan_launch(backward_long_cols_kernel<T>, dim3((unsigned)ceil_div(p.cols, 256), (unsigned)b.blocks),
                            dim3(256), 0, s, p);
         if (e == cudaSuccess && p.dX)
-            e = launch_pdl(backward_long_rows_kernel<T, V>, dim3((unsigned)min64(p.rows, (int64_t)sm_count * 2)),
+            e = plan_launch(backward_long_rows_kernel<T, V>, dim3((unsigned)min64(p.rows, (int64_t)sm_count * 2)),
                            dim3(1024), 0, s, p);
     } else if (b.kind == BwdShape::WIDE) {
         if constexpr (V > 1) {
@@ -988,7 +970,7 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
             const int stages = (int)min64(4, kWideSmem / row);
             e = set_smem_limit(reinterpret_cast<const void*>(backward_wide_kernel<T>), (int)kWideSmem);
             if (e == cudaSuccess)
-                e = launch_pdl(backward_wide_kernel<T>, dim3((unsigned)b.blocks), dim3(kWideThreads),
+                e = plan_launch(backward_wide_kernel<T>, dim3((unsigned)b.blocks), dim3(kWideThreads),
                                (size_t)(stages * row), s, p, stages);
         }
     } else if (b.kind == BwdShape::RING) {
@@ -1008,7 +990,7 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
         else if constexpr (V == 1) e = backward_rows<T, 1, 1>(p, b, s);
     }
     if (e == cudaSuccess && p.partial)
-        e = launch_pdl(column_sum_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32), 2), dim3(1024), 0, s,
+        e = plan_launch(column_sum_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32), 2), dim3(1024), 0, s,
                        (const float*)p.partial, (int)b.blocks, p.cols, dgamma, dbeta);
     return e;
 }

@@ -26,6 +26,18 @@ inline bool plan_fits(int64_t a, int64_t b, int64_t bytes) {
     return !__builtin_mul_overflow(a, b, &n) && !__builtin_mul_overflow(n, bytes, &n) && n <= kPlanMaxBytes;
 }
 
+// A launch in full stream order.  The kernels of these plans neither start
+// before their predecessor has ended nor let a successor start early
+// (programmatic dependent launch): blocks that start early and wait hold
+// places on the SMs, and where kernels of many small blocks did so around
+// clusters that needed whole pairs of SMs, a stream came to a standstill.
+template <typename... KArgs, typename... Args>
+inline cudaError_t plan_launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                               Args&&... args) {
+    kernel<<<grid, block, smem, s>>>(static_cast<KArgs>(args)...);
+    return cudaGetLastError();
+}
+
 inline int64_t plan_elem_bytes(olc_dtype dt) { return dt == OLC_FLOAT ? 4 : 2; }
 inline bool plan_dtype_ok(int dt) { return dt == OLC_FLOAT || dt == OLC_FLOAT16 || dt == OLC_BFLOAT16; }
 inline bool plan_misaligned(const void* p, int64_t bytes) {

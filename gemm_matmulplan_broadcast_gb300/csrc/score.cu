@@ -657,8 +657,6 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
     }
     __syncthreads();
     if (parts > 1) cluster_arrive();
-    grid_dependency_wait();
-    grid_launch_dependents();
 
     if (t >= kThreads + 32) {
         // the finishing warps: every other row each, from the row buffer of its own
@@ -839,8 +837,6 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
 template <typename T>
 __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     constexpr int V = 16 / sizeof(T);
-    grid_dependency_wait();
-    grid_launch_dependents();
     const int64_t row = blockIdx.x / p.chunks;
     const int part = (int)(blockIdx.x % p.chunks);
     const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
@@ -963,15 +959,13 @@ cudaError_t launch_forward(const Params& p, int sm_count, cudaStream_t s) {
     cfg.blockDim = dim3(kBlockThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, forward_kernel<T>, p);
 }
 
@@ -1062,7 +1056,7 @@ olc_status olc_token_log_probs_backward(olc_token_log_probs_plan* plan, const vo
                         (int)plan->vocab, (int)chunks};
     return score::by_type(plan->dtype, [&](auto tag) {
         using T = decltype(tag);
-        return plan_status(launch_pdl(score::backward_kernel<T>, dim3((unsigned)(plan->rows * chunks)), dim3(256), 0,
+        return plan_status(plan_launch(score::backward_kernel<T>, dim3((unsigned)(plan->rows * chunks)), dim3(256), 0,
                                       static_cast<cudaStream_t>(stream), p));
     });
 }
