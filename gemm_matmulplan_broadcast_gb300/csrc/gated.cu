@@ -779,6 +779,7 @@ struct olc_gated_plan {
     int act, trans_w;
     // FLOAT: X W, dg W' (alone, and added to what is there), and X' dg or dg' X
     olc_matmul_plan *forward, *dx, *dx_more, *dw;
+    void* counters;          // FLOAT: arrivals at shared tiles
 };
 
 namespace {
@@ -955,6 +956,32 @@ olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const vo
 
 olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                      cudaStream_t s) {
+    // few rows: the matrix plan's row kernels stream each weight once; a
+    // 64-row tile would multiply mostly nothing (they take no transposed
+    // weights)
+    if (p->M > 4 || p->trans_w) {
+        const int sms = p->state.sm_count;
+        const size_t shares = gated::float_share_bytes(p->M, p->D, p->F, sms);
+        olc_status st = p->state.ensure(shares);
+        if (st != OLC_OK) return st;
+        if (shares && !p->counters) {
+            if (cudaMalloc(&p->counters, gated::float_counter_bytes(sms)) != cudaSuccess) {
+                cudaGetLastError();
+                p->counters = nullptr;
+                return OLC_ERR_OOM;
+            }
+            const cudaError_t e = cudaMemset(p->counters, 0, gated::float_counter_bytes(sms));
+            if (e != cudaSuccess) return plan_status(e);
+        }
+        cudaError_t e = shares ? p->state.before_use(s) : cudaSuccess;
+        if (e == cudaSuccess)
+            e = gated::launch_float(static_cast<const float*>(X), static_cast<const float*>(Wg),
+                                    static_cast<const float*>(Wu), static_cast<float*>(H), static_cast<float*>(G),
+                                    static_cast<float*>(U), p->M, p->D, p->F, p->trans_w, p->act, p->state.memory,
+                                    static_cast<unsigned int*>(p->counters), sms, s);
+        if (e == cudaSuccess && shares) e = p->state.after_use(s);
+        return plan_status(e);
+    }
     olc_status st = float_forward(p);
     const int64_t n = p->M * p->F;
     // what is not kept: g in the plan's memory, u in H
@@ -1035,6 +1062,7 @@ void olc_gated_plan_destroy(olc_gated_plan* plan) {
     olc_matmul_plan_destroy(plan->dx);
     olc_matmul_plan_destroy(plan->dx_more);
     olc_matmul_plan_destroy(plan->dw);
+    plan->state.release(plan->counters);
     plan->state.destroy();
     delete plan;
 }

@@ -121,6 +121,11 @@ struct PlanState {
         return cudaSuccess;
     }
 
+    // free another piece of device memory of the plan (null: nothing)
+    void release(void* p) {
+        if (p) on_device([&] { cudaFree(p); });
+    }
+
     void release_memory() {
         if (memory) on_device([&] { cudaFree(memory); });
         memory = nullptr;
