@@ -40,16 +40,16 @@ struct Params {
     unsigned int* arrived;    // [shared tiles], zero between launches
 };
 
-// four elements at a row of `n` elements (the row's element i..i+3), zeros
-// past the end; VEC: whole 16-byte vectors
+// the first four of n elements at `from`, zeros past the n-th; VEC: whole
+// 16-byte vectors
 template <bool VEC>
-__device__ __forceinline__ float4 four(const float* row, int64_t i, int64_t n) {
-    if constexpr (VEC) return i < n ? __ldg(reinterpret_cast<const float4*>(row + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+__device__ __forceinline__ float4 four(const float* from, int64_t n) {
+    if constexpr (VEC) return n > 0 ? __ldg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
     float4 v;
-    v.x = i < n ? __ldg(row + i) : 0.f;
-    v.y = i + 1 < n ? __ldg(row + i + 1) : 0.f;
-    v.z = i + 2 < n ? __ldg(row + i + 2) : 0.f;
-    v.w = i + 3 < n ? __ldg(row + i + 3) : 0.f;
+    v.x = n > 0 ? __ldg(from) : 0.f;
+    v.y = n > 1 ? __ldg(from + 1) : 0.f;
+    v.z = n > 2 ? __ldg(from + 2) : 0.f;
+    v.w = n > 3 ? __ldg(from + 3) : 0.f;
     return v;
 }
 
@@ -73,18 +73,15 @@ __device__ __forceinline__ void copy_async(float* to, const float* from, int byt
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
 }
-// elements i .. i+3 of a row of n (none if !live) into four floats of shared memory
+// the first four of n elements at `from` into four floats of shared memory,
+// zeros past the n-th (`any`: an address that can be formed when none is read)
 template <bool VEC>
-__device__ __forceinline__ void copy_four(float* to, const float* row, int64_t i, int64_t n, bool live) {
+__device__ __forceinline__ void copy_four(float* to, const float* from, const float* any, int64_t n) {
     if constexpr (VEC) {
-        const bool in = live && i < n;
-        copy_async<16>(to, in ? row + i : row, in ? 16 : 0);
+        copy_async<16>(to, n > 0 ? from : any, n > 0 ? 16 : 0);
     } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const bool in = live && i + q < n;
-            copy_async<4>(to + q, in ? row + i + q : row, in ? 4 : 0);
-        }
+        for (int q = 0; q < 4; ++q) copy_async<4>(to + q, q < n ? from + q : any, q < n ? 4 : 0);
     }
 }
 
@@ -103,44 +100,78 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
     float* const as = smem;
     float* const bs = smem + STAGES * A_FLOATS;
 
-    auto fetch = [&](int64_t k0, int stage) {
-        float* a = as + stage * A_FLOATS;
-        float* b = bs + stage * B_FLOATS;
+    // A slice's addresses advance by additions: this thread's rows of X are t /
+    // 4 + 16 q at K elements 4 (t % 4); its rows of the weights K elements t / 16
+    // + 4 q at columns 4 (t % 16), or (TRANS) one column of each at all sixteen.
+    const float *pa = nullptr, *pg = nullptr, *pu = nullptr;
+    int64_t ka = 0, kb = 0;          // their K elements
+    unsigned rows_in = 0;
+    bool col_in = false;
+    const int64_t da = 16 * p.D, db = 4 * p.F;
+    float* const a_to = as + (t >> 2) * AP + (t & 3) * 4;
+    float* const b_to = TRANS ? bs + t : bs + (t >> 4) * 2 * TN + (t & 15) * 4;
+    auto begin = [&](int64_t s0) {
+        const int64_t k0 = s0 * KS;
+        const int64_t row = m0 + (t >> 2);
+        rows_in = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int r = (t >> 2) + 16 * q, k = (t & 3) * 4;
-            const bool live = m0 + r < p.M;
-            copy_four<VEC>(a + r * AP + k, p.X + (live ? m0 + r : 0) * p.D, k0 + k, p.D, live);
+        for (int q = 0; q < 4; ++q) rows_in |= (unsigned)(row + 16 * q < p.M) << q;
+        ka = k0 + (t & 3) * 4;
+        pa = p.X + row * p.D + ka;
+        if constexpr (TRANS) {
+            const int64_t col = n0 + t;
+            col_in = col < p.F;
+            kb = k0;
+            pg = p.Wg + col * p.D + kb;
+            pu = p.Wu + col * p.D + kb;
+        } else {
+            const int64_t col = n0 + (t & 15) * 4;
+            col_in = col < p.F;
+            kb = k0 + (t >> 4);
+            pg = p.Wg + kb * p.F + col;
+            pu = p.Wu + kb * p.F + col;
         }
-        if constexpr (!TRANS) {
+    };
+    auto fetch = [&](int stage) {
+        float* a = a_to + stage * A_FLOATS;
+        float* b = b_to + stage * B_FLOATS;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int k = (t >> 4) + 4 * (q & 3), c = (t & 15) * 4;
-                const bool live = k0 + k < p.D;
-                copy_four<VEC>(b + k * 2 * TN + (q >> 2) * TN + c, (q < 4 ? p.Wg : p.Wu) + (live ? k0 + k : 0) * p.F,
-                               n0 + c, p.F, live);
+        for (int q = 0; q < 4; ++q)
+            copy_four<VEC>(a + 16 * q * AP, pa + q * da, p.X, (rows_in >> q) & 1u ? p.D - ka : 0);
+        pa += KS;
+        ka += KS;
+        if constexpr (!TRANS) {
+            const int64_t left = col_in ? p.F - (n0 + (t & 15) * 4) : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t n = kb + 4 * q < p.D ? left : 0;
+                copy_four<VEC>(b + 4 * q * 2 * TN, pg + q * db, p.Wg, n);
+                copy_four<VEC>(b + 4 * q * 2 * TN + TN, pu + q * db, p.Wu, n);
             }
+            pg += 4 * db;
+            pu += 4 * db;
+            kb += KS;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if constexpr (TRANS) {
-            // four vectors along K at a time, each one column's: a thread a column of each weight
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const float* W = q ? p.Wu : p.Wg;
-                const int64_t col = n0 + t;
+                const float* w = q ? pu : pg;
                 float4 v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = col < p.F ? four<VEC>(W + col * p.D, k0 + 4 * i, p.D) : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < 4; ++i) v[i] = four<VEC>(w + 4 * i, col_in ? p.D - kb - 4 * i : 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float* to = b + 4 * i * 2 * TN + q * TN + t;
+                    float* to = b + 4 * i * 2 * TN + q * TN;
                     to[0] = v[i].x;
                     to[2 * TN] = v[i].y;
                     to[4 * TN] = v[i].z;
                     to[6 * TN] = v[i].w;
                 }
             }
+            pg += KS;
+            pu += KS;
+            kb += KS;
         }
     };
 
@@ -154,8 +185,9 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[i][j] = 0;
         __syncthreads();             // all are done with the tile before
+        begin(s0);
         for (int i = 0; i < STAGES - 1; ++i) {
-            if (i < n) fetch((s0 + i) * KS, i);
+            if (i < n) fetch(i);
             else asm volatile("cp.async.commit_group;" ::: "memory");
         }
         int stage = 0;
@@ -163,7 +195,7 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
             asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
             __syncthreads();             // this slice is there for all, and all are done with the one before it
             const int next = i + STAGES - 1;
-            if (next < n) fetch((s0 + next) * KS, stage == 0 ? STAGES - 1 : stage - 1);
+            if (next < n) fetch(stage == 0 ? STAGES - 1 : stage - 1);
             else asm volatile("cp.async.commit_group;" ::: "memory");
             const float* a = as + stage * A_FLOATS + ty * AP;
             const float* b = bs + stage * B_FLOATS + tx * 4;
