@@ -33,8 +33,6 @@ namespace gated {
 
 using namespace olc::tc;
 
-enum Mode { FWD = 0, DX = 1, DW = 2 };
-
 // ---- the products on CTA pairs ------------------------------------------------
 
 constexpr int STAGES = 6;
@@ -777,36 +775,22 @@ struct olc_gated_plan {
     olc_dtype dtype;
     int64_t M, D, F;
     int act, trans_w;
-    // FLOAT: X W, dg W' (alone, and added to what is there), and X' dg or dg' X
-    olc_matmul_plan *forward, *dx, *dx_more, *dw;
-    void* counters;          // FLOAT: arrivals at shared tiles
+    olc_matmul_plan* forward;    // FLOAT, few rows: X W
+    void* counters;              // FLOAT: arrivals at shared tiles
 };
 
 namespace {
 
-// the FLOAT products, made when first needed
-olc_status float_forward(olc_gated_plan* p) {
-    if (p->forward) return OLC_OK;
-    const int64_t x[2] = {p->M, p->D}, w[2] = {p->trans_w ? p->F : p->D, p->trans_w ? p->D : p->F};
-    return olc_gemm_plan_create(x, w, 0, p->trans_w, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->forward);
-}
-olc_status float_backward(olc_gated_plan* p) {
-    const int64_t x[2] = {p->M, p->D}, h[2] = {p->M, p->F};
-    const int64_t w[2] = {p->trans_w ? p->F : p->D, p->trans_w ? p->D : p->F};
-    olc_status st = OLC_OK;
-    if (!p->dx) st = olc_gemm_plan_create(h, w, 0, !p->trans_w, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->dx);
-    if (st == OLC_OK && !p->dx_more) {
-        st = olc_gemm_plan_create(h, w, 0, !p->trans_w, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->dx_more);
-        if (st == OLC_OK) st = olc_matmul_plan_set_epilogue(p->dx_more, OLC_ACT_NONE, 1);
-        if (st != OLC_OK) {
-            olc_matmul_plan_destroy(p->dx_more);
-            p->dx_more = nullptr;
-        }
+// the FLOAT counters, made when first needed
+olc_status float_counters(olc_gated_plan* p) {
+    if (p->counters) return OLC_OK;
+    const size_t bytes = gated::float_counter_bytes(p->state.sm_count);
+    if (cudaMalloc(&p->counters, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        p->counters = nullptr;
+        return OLC_ERR_OOM;
     }
-    if (st == OLC_OK && !p->dw)
-        st = p->trans_w ? olc_gemm_plan_create(h, x, 1, 0, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->dw)
-                        : olc_gemm_plan_create(x, h, 1, 0, 1.0, 0.0, nullptr, -1, OLC_FLOAT, &p->dw);
-    return st;
+    return plan_status(cudaMemset(p->counters, 0, bytes));
 }
 
 // One call's use of the plan's memory: pieces are taken in order, first to
@@ -954,77 +938,115 @@ olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const vo
     return plan_status(e);
 }
 
-olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
-                     cudaStream_t s) {
-    // few rows: the matrix plan's row kernels stream each weight once; a
-    // 64-row tile would multiply mostly nothing (they take no transposed
-    // weights)
-    if (p->M > 4 || p->trans_w) {
-        const int sms = p->state.sm_count;
-        const size_t shares = gated::float_share_bytes(p->M, p->D, p->F, sms);
-        olc_status st = p->state.ensure(shares);
-        if (st != OLC_OK) return st;
-        if (shares && !p->counters) {
-            if (cudaMalloc(&p->counters, gated::float_counter_bytes(sms)) != cudaSuccess) {
-                cudaGetLastError();
-                p->counters = nullptr;
-                return OLC_ERR_OOM;
-            }
-            const cudaError_t e = cudaMemset(p->counters, 0, gated::float_counter_bytes(sms));
-            if (e != cudaSuccess) return plan_status(e);
-        }
-        cudaError_t e = shares ? p->state.before_use(s) : cudaSuccess;
-        if (e == cudaSuccess)
-            e = gated::launch_float(static_cast<const float*>(X), static_cast<const float*>(Wg),
-                                    static_cast<const float*>(Wu), static_cast<float*>(H), static_cast<float*>(G),
-                                    static_cast<float*>(U), p->M, p->D, p->F, p->trans_w, p->act, p->state.memory,
-                                    static_cast<unsigned int*>(p->counters), sms, s);
-        if (e == cudaSuccess && shares) e = p->state.after_use(s);
-        return plan_status(e);
+// FLOAT, few rows and weights [D, F]: the matrix plan's row kernels stream
+// each weight once, where a 64-row tile would multiply mostly nothing ([1, 1024]
+// x [1024, 2816]: 21.7 us against 44).
+constexpr int64_t kFewFloatRows = 4;
+olc_status forward32_few(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
+                         cudaStream_t s) {
+    olc_status st = OLC_OK;
+    if (!p->forward) {
+        const int64_t x[2] = {p->M, p->D}, w[2] = {p->D, p->F};
+        st = olc_matmul_plan_create(x, 2, w, 2, OLC_FLOAT, &p->forward);
     }
-    olc_status st = float_forward(p);
     const int64_t n = p->M * p->F;
     // what is not kept: g in the plan's memory, u in H
     if (st == OLC_OK && !G) st = p->state.ensure((size_t)n * sizeof(float));
     if (st != OLC_OK) return st;
-    if (!G) {
-        const cudaError_t e = p->state.before_use(s);
-        if (e != cudaSuccess) return plan_status(e);
-    }
+    cudaError_t e = G ? cudaSuccess : p->state.before_use(s);
+    if (e != cudaSuccess) return plan_status(e);
     void* g = G ? G : p->state.memory;
     void* u = U ? U : H;
-    st = olc_gemm_execute(p->forward, X, Wg, nullptr, g, s);
-    if (st == OLC_OK) st = olc_gemm_execute(p->forward, X, Wu, nullptr, u, s);
+    st = olc_matmul_execute(p->forward, X, Wg, g, s);
+    if (st == OLC_OK) st = olc_matmul_execute(p->forward, X, Wu, u, s);
     if (st != OLC_OK) return st;
-    cudaError_t e = plan_launch(gated::product_kernel, dim3((unsigned)min64(ceil_div(n, 256), (int64_t)p->state.sm_count * 16)),
-                                dim3(256), 0, s, static_cast<const float*>(g), static_cast<const float*>(u),
-                                static_cast<float*>(H), n, p->act);
+    e = plan_launch(gated::product_kernel, dim3((unsigned)min64(ceil_div(n, 256), (int64_t)p->state.sm_count * 16)),
+                    dim3(256), 0, s, static_cast<const float*>(g), static_cast<const float*>(u), static_cast<float*>(H),
+                    n, p->act);
     if (e == cudaSuccess && !G) e = p->state.after_use(s);
+    return plan_status(e);
+}
+
+olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
+                     cudaStream_t s) {
+    if (p->M <= kFewFloatRows && !p->trans_w) return forward32_few(p, X, Wg, Wu, H, G, U, s);
+    const int sms = p->state.sm_count;
+    const size_t shares = gated::float_share_bytes(gated::FWD, p->M, p->F, p->D, sms);
+    olc_status st = float_counters(p);
+    if (st == OLC_OK) st = p->state.ensure(shares);
+    if (st != OLC_OK) return st;
+    gated::Product w;
+    std::memset(&w, 0, sizeof w);
+    w.mode = gated::FWD;
+    w.M = p->M;
+    w.N = p->F;
+    w.K = p->D;
+    const int64_t wr = p->trans_w ? p->F : p->D, wc = p->trans_w ? p->D : p->F;
+    w.a[0] = w.a[1] = gated::Stored{X, p->M, p->D, p->D};
+    w.b[0] = gated::Stored{Wg, wr, wc, wc};
+    w.b[1] = gated::Stored{Wu, wr, wc, wc};
+    w.b_k = p->trans_w;
+    w.Y[0] = H;
+    w.Y[1] = G;
+    w.Y[2] = U;
+    w.act = p->act;
+    cudaError_t e = shares ? p->state.before_use(s) : cudaSuccess;
+    if (e == cudaSuccess)
+        e = gated::launch_float(w, p->state.memory, static_cast<unsigned int*>(p->counters), sms, s);
+    if (e == cudaSuccess && shares) e = p->state.after_use(s);
     return plan_status(e);
 }
 
 olc_status backward32(olc_gated_plan* p, const void* dH, const void* X, const void* Wg, const void* Wu, const void* G,
                       const void* U, void* dX, void* dWg, void* dWu, cudaStream_t s) {
-    olc_status st = float_backward(p);
-    const size_t half = gated::round256((size_t)(p->M * p->F) * sizeof(float));
-    if (st == OLC_OK) st = p->state.ensure(2 * half);
+    const int sms = p->state.sm_count;
+    const int64_t wr = p->trans_w ? p->F : p->D, wc = p->trans_w ? p->D : p->F;
+    const int64_t pitch = (p->F + 3) / 4 * 4;      // of dg and du: rows on 16-byte boundaries
+    size_t shares = dX ? gated::float_share_bytes(gated::DX, p->M, p->D, p->F, sms) : 0;
+    const size_t more = dWg ? gated::float_share_bytes(gated::DW, wr, wc, p->M, sms) : 0;
+    if (more > shares) shares = more;
+    const size_t half = gated::round256((size_t)(p->M * pitch) * sizeof(float));
+    olc_status st = float_counters(p);
+    if (st == OLC_OK) st = p->state.ensure(2 * half + shares);
     if (st != OLC_OK) return st;
-    void *dg = p->state.memory, *du = static_cast<unsigned char*>(p->state.memory) + half;
+    unsigned char* memory = static_cast<unsigned char*>(p->state.memory);
+    void *dg = memory, *du = memory + half, *part = memory + 2 * half;
+    unsigned int* counters = static_cast<unsigned int*>(p->counters);
     cudaError_t e = p->state.before_use(s);
-    if (e == cudaSuccess)
-        e = gated::launch_slope<float>(dH, G, U, dg, du, p->M, p->F, p->F, p->act, p->state.sm_count, s);
-    if (e != cudaSuccess) return plan_status(e);
+    if (e == cudaSuccess) e = gated::launch_slope<float>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s);
+    const gated::Stored sg{dg, p->M, p->F, pitch}, su{du, p->M, p->F, pitch}, sx{X, p->M, p->D, p->D};
+    gated::Product w;
     if (dX) {
-        st = olc_gemm_execute(p->dx, dg, Wg, nullptr, dX, s);
-        // the second term on top of the first: the residual is dX itself
-        if (st == OLC_OK) st = olc_matmul_execute_fused(p->dx_more, du, Wu, nullptr, dX, dX, s);
+        std::memset(&w, 0, sizeof w);
+        w.mode = gated::DX;
+        w.M = p->M;
+        w.N = p->D;
+        w.K = p->F;
+        w.a[0] = sg;
+        w.a[1] = su;
+        w.b[0] = gated::Stored{Wg, wr, wc, wc};
+        w.b[1] = gated::Stored{Wu, wr, wc, wc};
+        w.b_k = !p->trans_w;
+        w.Y[0] = dX;
+        if (e == cudaSuccess) e = gated::launch_float(w, part, counters, sms, s);
     }
-    if (st == OLC_OK && dWg) {
-        st = olc_gemm_execute(p->dw, p->trans_w ? dg : X, p->trans_w ? X : dg, nullptr, dWg, s);
-        if (st == OLC_OK) st = olc_gemm_execute(p->dw, p->trans_w ? du : X, p->trans_w ? X : du, nullptr, dWu, s);
+    if (dWg) {
+        std::memset(&w, 0, sizeof w);
+        w.mode = gated::DW;
+        w.M = wr;
+        w.N = wc;
+        w.K = p->M;
+        w.a[0] = p->trans_w ? sg : sx;
+        w.a[1] = p->trans_w ? su : sx;
+        w.b[0] = p->trans_w ? sx : sg;
+        w.b[1] = p->trans_w ? sx : su;
+        w.a_mn = true;
+        w.Y[0] = dWg;
+        w.Y[1] = dWu;
+        if (e == cudaSuccess) e = gated::launch_float(w, part, counters, sms, s);
     }
-    if (st != OLC_OK) return st;
-    return plan_status(p->state.after_use(s));
+    if (e == cudaSuccess) e = p->state.after_use(s);
+    return plan_status(e);
 }
 
 }  // namespace
@@ -1059,9 +1081,6 @@ olc_status olc_gated_plan_create(int64_t rows, int64_t d_in, int64_t d_hidden, i
 void olc_gated_plan_destroy(olc_gated_plan* plan) {
     if (!plan) return;
     olc_matmul_plan_destroy(plan->forward);
-    olc_matmul_plan_destroy(plan->dx);
-    olc_matmul_plan_destroy(plan->dx_more);
-    olc_matmul_plan_destroy(plan->dw);
     plan->state.release(plan->counters);
     plan->state.destroy();
     delete plan;

@@ -1,18 +1,25 @@
-// The gated feed-forward product in FLOAT: act(X Wg) (X Wu) on the FMA pipes,
+// The gated feed-forward product and its gradient in FLOAT, on the FMA pipes,
 // which keep float32 products exact to one rounding (the tensor cores round
 // their operands).
 //
-// 4 M D F operations at two a paired FMA bound it.  A block of 64 threads
-// takes 64 rows x 64 columns of both products: the shared-memory tile of B
-// holds 64 columns of Wg next to the same 64 of Wu, and a thread's
-// accumulators are 8 rows x 8 columns of each, so that it forms act(g) u of
-// its own outputs from registers.  With 8 x 16 accumulators a thread, 64 paired
-// FMAs take six 16-byte reads of shared memory, three quarters of its cycles
-// (8 x 8: all of them, which bounds that form).  64-row tiles, because their
-// last round over the SMs wastes less than that of 128 rows ([1024, 1024] x
-// [1024, 2816]: 704 tiles, 4.6 an SM, against 2.3).  Slices of K, 16 deep, come
-// through asynchronous copies two ahead; weights stored [F, D] are transposed
-// through registers.
+// Operations at two a paired FMA bound them.  A block of 64 threads takes 64 rows
+// x 128 columns, 8 x 16 accumulators a thread: 64 paired FMAs then take six
+// 16-byte reads of shared memory, three quarters of its cycles (8 x 8: all of
+// them, which bounds that form).  Slices of K, 16 deep, come through
+// asynchronous copies two ahead; an operand B stored with its K contiguous is
+// transposed through registers.  What the columns and the K are:
+//
+//   FWD  64 columns of Wg next to the same 64 of Wu: a thread holds g and u of the
+//        same outputs and forms act(g) u from registers
+//   DX   one accumulation through dg and Wg, then through du and Wu
+//   DW   x' dg and x' du as two outputs of one launch, x (or dg, du) read with its
+//        rows along K as it is
+//
+// Blocks are as many as reside.  Each takes as many whole tiles as there are
+// full rounds; the tiles of the last, partial round are cut along K into equal
+// shares, one a block, so that no SM idles through it ([1024, 1024] x [1024,
+// 2816]: 608 tiles whole and 96 in shares).  A tile's shares meet in the plan's
+// memory, and the block that brings the last one adds them in the order of K.
 #include "gated_internal.h"
 #include "plan_state.h"
 
@@ -20,21 +27,23 @@ namespace olc {
 namespace gated {
 namespace f32 {
 
-constexpr int TM = 64, TN = 64, KS = 16;          // rows, columns of each product, depth of a slice
+constexpr int TM = 64, TN = 64, KS = 16;          // rows, half of the columns, depth of a slice
 constexpr int THREADS = 64;
 constexpr int STAGES = 3;
-constexpr int AP = KS + 4;                        // floats between rows of X's tile: four rows in four bank groups
+constexpr int AP = KS + 4;                        // floats between rows of A's tile: four rows in four bank groups
 constexpr int A_FLOATS = TM * AP, B_FLOATS = KS * 2 * TN;
 constexpr int SMEM_BYTES = STAGES * (A_FLOATS + B_FLOATS) * 4;
 
 struct Params {
-    const float *X, *Wg, *Wu;
-    float *H, *G, *U;         // G, U may be null
-    int64_t M, D, F;
-    int64_t tiles_m, tiles;
+    const float *a[2], *b[2]; // FWD: a[0] = X, b = Wg, Wu; DX: dg, du and Wg, Wu; DW: the two outputs' operands
+    int64_t lda, ldb;
+    float* y[3];              // FWD: h, g, u (null: not kept); DX: dX; DW: dWg, dWu
+    int64_t M, N, K;          // rows and columns of an output, K of one operand pair
+    int64_t tiles_m, tiles_item, tiles;
     int64_t rounds;           // whole tiles a block
     int64_t sharers;          // blocks that share the rest, at least four slices each
-    int slices;               // of K a tile
+    int source_slices;        // slices of one operand pair
+    int slices;               // of a tile (DX: both pairs')
     int act;
     float4* shares;           // [2 blocks][32][threads]: partial sums of a block's first and last shared tile
     unsigned int* arrived;    // [shared tiles], zero between launches
@@ -43,7 +52,7 @@ struct Params {
 // the first four of n elements at `from`, zeros past the n-th; VEC: whole
 // 16-byte vectors
 template <bool VEC>
-__device__ __forceinline__ float4 four(const float* from, int64_t n) {
+__device__ __forceinline__ float4 four(const float* from, int n) {
     if constexpr (VEC) return n > 0 ? __ldg(reinterpret_cast<const float4*>(from)) : make_float4(0.f, 0.f, 0.f, 0.f);
     float4 v;
     v.x = n > 0 ? __ldg(from) : 0.f;
@@ -76,7 +85,7 @@ __device__ __forceinline__ void copy_async(float* to, const float* from, int byt
 // the first four of n elements at `from` into four floats of shared memory,
 // zeros past the n-th (`any`: an address that can be formed when none is read)
 template <bool VEC>
-__device__ __forceinline__ void copy_four(float* to, const float* from, const float* any, int64_t n) {
+__device__ __forceinline__ void copy_four(float* to, const float* from, const float* any, int n) {
     if constexpr (VEC) {
         copy_async<16>(to, n > 0 ? from : any, n > 0 ? 16 : 0);
     } else {
@@ -85,10 +94,10 @@ __device__ __forceinline__ void copy_four(float* to, const float* from, const fl
     }
 }
 
-// TRANS: the weights are stored [F, D]
-template <bool VEC, bool TRANS>
+// A_T: A is stored [K, M]; B_T: B is stored [N, K]
+template <int MODE, bool VEC, bool A_T, bool B_T>
 __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
-    extern __shared__ __align__(16) float smem[];     // stages of X [64 rows][k], B [k][64 of Wg, 64 of Wu]
+    extern __shared__ __align__(16) float smem[];     // stages of A [64 rows][k] (A_T: [k][64 rows]), B [k][2 x 64]
     __shared__ int last;
     const int t = threadIdx.x, tx = t & 7, ty = t >> 3;
     const int64_t grid = gridDim.x, block = blockIdx.x;
@@ -96,96 +105,98 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
     const int64_t whole = p.rounds * grid, steps = (p.tiles - whole) * p.slices, sharers = p.sharers;
     const int64_t share0 = block < sharers ? block * steps / sharers : 0;
     const int64_t share1 = block < sharers ? (block + 1) * steps / sharers : 0;
-    int64_t m0 = 0, n0 = 0;
+    constexpr int COLS = MODE == FWD ? TN : 2 * TN;
+    int m0 = 0, n0 = 0, item = 0;
+    const int M = (int)p.M, N = (int)p.N, K = (int)p.K;      // below 2^31
     float* const as = smem;
     float* const bs = smem + STAGES * A_FLOATS;
 
-    // A slice's addresses advance by additions: this thread's rows of X are t /
-    // 4 + 16 q at K elements 4 (t % 4); its rows of the weights K elements t / 16
-    // + 4 q at columns 4 (t % 16), or (TRANS) one column of each at all sixteen.
-    const float *pa = nullptr, *pg = nullptr, *pu = nullptr;
-    int64_t ka = 0, kb = 0;          // their K elements
+    // A slice's addresses advance by additions.  An operand with K contiguous:
+    // this thread takes rows t / 4 + 16 q of A at K elements 4 (t % 4), one row of
+    // each half of B at all sixteen; one with its rows along K: K elements t / 16
+    // + 4 q at elements 4 (t % 16).
+    const float *pa = nullptr, *pb[2] = {nullptr, nullptr};
+    int ka = 0, kb = 0;              // their K elements
     unsigned rows_in = 0;
-    bool col_in = false;
-    const int64_t da = 16 * p.D, db = 4 * p.F;
-    float* const a_to = as + (t >> 2) * AP + (t & 3) * 4;
-    float* const b_to = TRANS ? bs + t : bs + (t >> 4) * 2 * TN + (t & 15) * 4;
-    auto begin = [&](int64_t s0) {
-        const int64_t k0 = s0 * KS;
-        const int64_t row = m0 + (t >> 2);
-        rows_in = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) rows_in |= (unsigned)(row + 16 * q < p.M) << q;
-        ka = k0 + (t & 3) * 4;
-        pa = p.X + row * p.D + ka;
-        if constexpr (TRANS) {
-            const int64_t col = n0 + t;
-            col_in = col < p.F;
-            kb = k0;
-            pg = p.Wg + col * p.D + kb;
-            pu = p.Wu + col * p.D + kb;
+    int left_a = 0, left_b[2] = {0, 0};       // elements from this thread's to the row's end
+    const int64_t da = (A_T ? 4 : 16) * p.lda, db = 4 * p.ldb;
+    float* const a_to = A_T ? as + (t >> 4) * TM + (t & 15) * 4 : as + (t >> 2) * AP + (t & 3) * 4;
+    float* const b_to = B_T ? bs + t : bs + (t >> 4) * 2 * TN + (t & 15) * 4;
+    // from slice s0 of operand pair `source`
+    auto begin = [&](int source, int s0) {
+        const int k0 = s0 * KS;
+        const float* A = MODE == FWD ? p.a[0] : p.a[source];
+        if constexpr (A_T) {
+            const int row = m0 + (t & 15) * 4;
+            left_a = M - row;
+            ka = k0 + (t >> 4);
+            pa = A + (int64_t)ka * p.lda + row;
         } else {
-            const int64_t col = n0 + (t & 15) * 4;
-            col_in = col < p.F;
-            kb = k0 + (t >> 4);
-            pg = p.Wg + kb * p.F + col;
-            pu = p.Wu + kb * p.F + col;
+            const int row = m0 + (t >> 2);
+            rows_in = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) rows_in |= (unsigned)(row + 16 * q < M) << q;
+            ka = k0 + (t & 3) * 4;
+            pa = A + (int64_t)row * p.lda + ka;
+        }
+        kb = B_T ? k0 : k0 + (t >> 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float* B = MODE == FWD ? p.b[h] : p.b[source];
+            const int col = n0 + (MODE == FWD ? 0 : h * TN) + (B_T ? t : (t & 15) * 4);
+            left_b[h] = N - col;
+            pb[h] = B_T ? B + (int64_t)col * p.ldb + kb : B + (int64_t)kb * p.ldb + col;
         }
     };
     auto fetch = [&](int stage) {
         float* a = a_to + stage * A_FLOATS;
         float* b = b_to + stage * B_FLOATS;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            copy_four<VEC>(a + 16 * q * AP, pa + q * da, p.X, (rows_in >> q) & 1u ? p.D - ka : 0);
-        pa += KS;
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (A_T) copy_four<VEC>(a + 4 * q * TM, pa + q * da, p.a[0], ka + 4 * q < K ? left_a : 0);
+            else copy_four<VEC>(a + 16 * q * AP, pa + q * da, p.a[0], (rows_in >> q) & 1u ? K - ka : 0);
+        }
+        pa += A_T ? 4 * da : KS;
         ka += KS;
-        if constexpr (!TRANS) {
-            const int64_t left = col_in ? p.F - (n0 + (t & 15) * 4) : 0;
+        if constexpr (!B_T) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t n = kb + 4 * q < p.D ? left : 0;
-                copy_four<VEC>(b + 4 * q * 2 * TN, pg + q * db, p.Wg, n);
-                copy_four<VEC>(b + 4 * q * 2 * TN + TN, pu + q * db, p.Wu, n);
-            }
-            pg += 4 * db;
-            pu += 4 * db;
-            kb += KS;
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    copy_four<VEC>(b + 4 * q * 2 * TN + h * TN, pb[h] + q * db, p.b[0],
+                                   kb + 4 * q < K ? left_b[MODE == FWD ? 0 : h] : 0);
+            pb[0] += 4 * db;
+            pb[1] += 4 * db;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        if constexpr (TRANS) {
+        if constexpr (B_T) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float* w = q ? pu : pg;
+            for (int h = 0; h < 2; ++h) {
                 float4 v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = four<VEC>(w + 4 * i, col_in ? p.D - kb - 4 * i : 0);
+                for (int i = 0; i < 4; ++i) v[i] = four<VEC>(pb[h] + 4 * i, left_b[MODE == FWD ? 0 : h] > 0 ? K - kb - 4 * i : 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float* to = b + 4 * i * 2 * TN + q * TN;
+                    float* to = b + 4 * i * 2 * TN + h * TN;
                     to[0] = v[i].x;
                     to[2 * TN] = v[i].y;
                     to[4 * TN] = v[i].z;
                     to[6 * TN] = v[i].w;
                 }
             }
-            pg += KS;
-            pu += KS;
-            kb += KS;
+            pb[0] += KS;
+            pb[1] += KS;
         }
+        kb += KS;
     };
 
-    // rows ty + 8 i; columns 32 c + 4 tx + (0..3) of g (j = 0..3), then of u
+    // rows ty + 8 i (A_T: 8 ty + i); columns 32 c + 4 tx + (0..3) of the first half (j = 0..3), then of the second
     F2 acc[8][8];
 
-    // acc = the tile's products over slices [s0, s0 + n)
-    auto multiply = [&](int64_t s0, int n) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] = 0;
-        __syncthreads();             // all are done with the tile before
-        begin(s0);
+    // acc += the tile's products over slices [s0, s0 + n) of one operand pair
+    auto multiply_pair = [&](int source, int s0, int n) {
+        __syncthreads();             // all are done with what came before
+        begin(source, s0);
         for (int i = 0; i < STAGES - 1; ++i) {
             if (i < n) fetch(i);
             else asm volatile("cp.async.commit_group;" ::: "memory");
@@ -197,14 +208,15 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
             const int next = i + STAGES - 1;
             if (next < n) fetch(stage == 0 ? STAGES - 1 : stage - 1);
             else asm volatile("cp.async.commit_group;" ::: "memory");
-            const float* a = as + stage * A_FLOATS + ty * AP;
+            const float* a = as + stage * A_FLOATS + (A_T ? ty * 8 : ty * AP);
             const float* b = bs + stage * B_FLOATS + tx * 4;
             if (++stage == STAGES) stage = 0;
 #pragma unroll
             for (int k4 = 0; k4 < KS; k4 += 4) {
-                float4 x[8];
+                float4 x[8];     // row r at K elements k4 .. k4 + 3 (A_T: rows 4 (i % 2) .. at element k4 + i / 2)
 #pragma unroll
-                for (int r = 0; r < 8; ++r) x[r] = *reinterpret_cast<const float4*>(a + r * 8 * AP + k4);
+                for (int r = 0; r < 8; ++r)
+                    x[r] = *reinterpret_cast<const float4*>(A_T ? a + (k4 + (r >> 1)) * TM + (r & 1) * 4 : a + r * 8 * AP + k4);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     F2 w[8];
@@ -216,7 +228,9 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
                     }
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float e = k == 0 ? x[r].x : (k == 1 ? x[r].y : (k == 2 ? x[r].z : x[r].w));
+                        const float4& v = A_T ? x[2 * k + (r >> 2)] : x[r];
+                        const int at = A_T ? r & 3 : k;
+                        const float e = at == 0 ? v.x : (at == 1 ? v.y : (at == 2 ? v.z : v.w));
                         const F2 e2 = pack_f2(e, e);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) fma_f2(acc[r][j], e2, w[j]);
@@ -225,32 +239,57 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
             }
         }
     };
+    // acc = the tile's products over slices [s0, s0 + n)
+    auto multiply = [&](int s0, int n) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] = 0;
+        if constexpr (MODE == DX) {
+            const int s1 = s0 + n, half = p.source_slices;
+#pragma unroll 1
+            for (int source = 0; source < 2; ++source) {
+                const int from = max(s0, source * half), to = min(s1, (source + 1) * half);
+                if (from < to) multiply_pair(source, from - source * half, to - from);
+            }
+        } else {
+            multiply_pair(MODE == DW ? item : 0, s0, n);
+        }
+    };
     auto finish = [&] {
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const int64_t row = m0 + ty + 8 * r;
-            if (row >= p.M) continue;
+            const int64_t row = m0 + (A_T ? ty * 8 + r : ty + 8 * r);
+            if (row >= M) continue;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int64_t col = n0 + 32 * c + tx * 4;
-                if (col >= p.F) continue;
                 float g[4], u[4], h[4];
                 unpack_f2(acc[r][2 * c], g[0], g[1]);
                 unpack_f2(acc[r][2 * c + 1], g[2], g[3]);
                 unpack_f2(acc[r][4 + 2 * c], u[0], u[1]);
                 unpack_f2(acc[r][4 + 2 * c + 1], u[2], u[3]);
+                if constexpr (MODE == FWD) {
+                    if (col >= p.N) continue;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = gate_value<true>(p.act, g[j]) * u[j];
-                put_four<VEC>(p.H + row * p.F, col, p.F, h);
-                if (p.G) put_four<VEC>(p.G + row * p.F, col, p.F, g);
-                if (p.U) put_four<VEC>(p.U + row * p.F, col, p.F, u);
+                    for (int j = 0; j < 4; ++j) h[j] = gate_value<true>(p.act, g[j]) * u[j];
+                    put_four<VEC>(p.y[0] + row * p.N, col, p.N, h);
+                    if (p.y[1]) put_four<VEC>(p.y[1] + row * p.N, col, p.N, g);
+                    if (p.y[2]) put_four<VEC>(p.y[2] + row * p.N, col, p.N, u);
+                } else {
+                    float* y = p.y[MODE == DW ? item : 0] + row * p.N;
+                    if (col < p.N) put_four<VEC>(y, col, p.N, g);
+                    if (col + TN < p.N) put_four<VEC>(y, col + TN, p.N, u);
+                }
             }
         }
     };
     auto tile_at = [&](int64_t tile) {
-        // rows fastest: the row tiles of a column read its weights from L2
-        m0 = tile % p.tiles_m * TM;
-        n0 = tile / p.tiles_m * TN;
+        item = MODE == DW ? (int)(tile / p.tiles_item) : 0;
+        const int64_t in = tile - item * p.tiles_item;
+        // rows fastest: the row tiles of a column read its operand B from L2
+        m0 = (int)(in % p.tiles_m) * TM;
+        n0 = (int)(in / p.tiles_m) * COLS;
     };
 
     for (int64_t r = 0; r < p.rounds; ++r) {
@@ -259,7 +298,8 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
         finish();
     }
     for (int64_t s = share0; s < share1;) {
-        const int64_t tile = s / p.slices, s0 = s % p.slices;
+        const int64_t tile = s / p.slices;
+        const int s0 = (int)(s % p.slices);
         const int n = (int)min64(p.slices - s0, share1 - s);
         s += n;
         tile_at(whole + tile);
@@ -315,46 +355,83 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
 constexpr int kFloatPerSm = 4;            // blocks that reside (registers)
 
 namespace {
+
+// How a product is cut; rows and columns of one output, K of one operand pair.
 struct FloatShape {
-    int64_t tiles_m, tiles, grid, rounds, sharers;
-    int slices;
+    int64_t tiles_m, tiles_item, tiles, grid, rounds, sharers;
+    int source_slices, slices;
 };
-FloatShape float_shape(int64_t M, int64_t D, int64_t F, int sm_count) {
+FloatShape float_shape(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
     FloatShape f;
     f.tiles_m = ceil_div(M, f32::TM);
-    f.tiles = f.tiles_m * ceil_div(F, f32::TN);
-    f.slices = (int)ceil_div(D, f32::KS);
+    f.tiles_item = f.tiles_m * ceil_div(N, mode == FWD ? f32::TN : 2 * f32::TN);
+    f.tiles = f.tiles_item * (mode == DW ? 2 : 1);
+    f.source_slices = (int)ceil_div(K, f32::KS);
+    f.slices = f.source_slices * (mode == DX ? 2 : 1);
     f.grid = max64(1, min64((int64_t)kFloatPerSm * sm_count, f.tiles * max64(1, f.slices / 4)));
     f.rounds = f.tiles / f.grid;
-    // no share is empty
-    f.sharers = max64(1, min64(f.grid, (f.tiles - f.rounds * f.grid) * f.slices / 4));
+    // no share is empty, and at most about 16 meet in a tile
+    const int64_t least = max64(4, f.slices / 16);
+    f.sharers = max64(1, min64(f.grid, (f.tiles - f.rounds * f.grid) * f.slices / least));
     return f;
 }
+
+template <int MODE, bool A_T, bool B_T>
+cudaError_t launch_float_as(const f32::Params& p, bool vec, int64_t grid, cudaStream_t s) {
+    auto* kernel = vec ? f32::kernel<MODE, true, A_T, B_T> : f32::kernel<MODE, false, A_T, B_T>;
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), f32::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    return plan_launch(kernel, dim3((unsigned)grid), dim3(f32::THREADS), (size_t)f32::SMEM_BYTES, s, p);
+}
+
 }  // namespace
 
-size_t float_share_bytes(int64_t M, int64_t D, int64_t F, int sm_count) {
-    const FloatShape f = float_shape(M, D, F, sm_count);
+size_t float_share_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
+    const FloatShape f = float_shape(mode, M, N, K, sm_count);
     return f.tiles == f.rounds * f.grid ? 0 : (size_t)f.grid * 2 * f32::THREADS * 32 * sizeof(float4);
 }
 size_t float_counter_bytes(int sm_count) { return (size_t)kFloatPerSm * sm_count * sizeof(unsigned int); }
 
-cudaError_t launch_float(const float* X, const float* Wg, const float* Wu, float* H, float* G, float* U, int64_t M,
-                         int64_t D, int64_t F, int trans_w, int act, void* shares, unsigned int* counters,
-                         int sm_count, cudaStream_t s) {
-    const FloatShape f = float_shape(M, D, F, sm_count);
-    const f32::Params p{X, Wg, Wu, H, G, U, M, D, F, f.tiles_m, f.tiles, f.rounds, f.sharers, f.slices, act,
-                        static_cast<float4*>(shares), counters};
-    // whole vectors: along K of X and of transposed weights, along F of the others and of the results
-    bool vec = D % 4 == 0 && F % 4 == 0;
-    for (const void* q : {(const void*)X, (const void*)Wg, (const void*)Wu, (const void*)H, (const void*)G, (const void*)U})
-        vec = vec && plan_aligned16(q);
-    auto run = [&](auto kernel) {
-        const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), f32::SMEM_BYTES);
-        if (e != cudaSuccess) return e;
-        return plan_launch(kernel, dim3((unsigned)f.grid), dim3(f32::THREADS), (size_t)f32::SMEM_BYTES, s, p);
-    };
-    if (vec) return trans_w ? run(f32::kernel<true, true>) : run(f32::kernel<true, false>);
-    return trans_w ? run(f32::kernel<false, true>) : run(f32::kernel<false, false>);
+cudaError_t launch_float(const Product& w, void* shares, unsigned int* counters, int sm_count, cudaStream_t s) {
+    const FloatShape f = float_shape(w.mode, w.M, w.N, w.K, sm_count);
+    f32::Params p;
+    // whole vectors: every row of every operand and result starts on a 16-byte
+    // boundary and ends with a whole vector (K where it is contiguous, A's rows
+    // where they lie along K)
+    bool vec = w.N % 4 == 0 && (w.a_mn ? w.M : w.K) % 4 == 0;
+    for (int i = 0; i < 2; ++i) {
+        p.a[i] = static_cast<const float*>(w.a[i].base);
+        p.b[i] = static_cast<const float*>(w.b[i].base);
+        vec = vec && plan_aligned16(p.a[i]) && plan_aligned16(p.b[i]) && w.a[i].pitch % 4 == 0 && w.b[i].pitch % 4 == 0;
+    }
+    for (int i = 0; i < 3; ++i) {
+        p.y[i] = static_cast<float*>(w.Y[i]);
+        vec = vec && plan_aligned16(p.y[i]);
+    }
+    p.lda = w.a[0].pitch;
+    p.ldb = w.b[0].pitch;
+    p.M = w.M;
+    p.N = w.N;
+    p.K = w.K;
+    p.tiles_m = f.tiles_m;
+    p.tiles_item = f.tiles_item;
+    p.tiles = f.tiles;
+    p.rounds = f.rounds;
+    p.sharers = f.sharers;
+    p.source_slices = f.source_slices;
+    p.slices = f.slices;
+    p.act = w.act;
+    p.shares = static_cast<float4*>(shares);
+    p.arrived = counters;
+    switch (w.mode) {
+        case FWD:
+            return w.b_k ? launch_float_as<FWD, false, true>(p, vec, f.grid, s)
+                         : launch_float_as<FWD, false, false>(p, vec, f.grid, s);
+        case DX:
+            return w.b_k ? launch_float_as<DX, false, true>(p, vec, f.grid, s)
+                         : launch_float_as<DX, false, false>(p, vec, f.grid, s);
+        default: return launch_float_as<DW, true, false>(p, vec, f.grid, s);
+    }
 }
 
 }  // namespace gated

@@ -65,8 +65,10 @@ __device__ __forceinline__ void gate_slope(int act, float g, float& value, float
 
 // ---- products -------------------------------------------------------------------
 
-// A stored matrix of 16-bit elements the TMA can read: base on a 16-byte
-// boundary, pitch a multiple of 8.
+enum Mode { FWD = 0, DX = 1, DW = 2 };
+
+// A stored matrix (16-bit elements that the TMA reads: base on a 16-byte
+// boundary, pitch a multiple of 8).
 struct Stored {
     const void* base;
     int64_t rows, cols, pitch;
@@ -85,14 +87,12 @@ struct Product {
 constexpr int kFewRows = 64;
 cudaError_t launch_few(olc_dtype dt, const Product& w, int sm_count, cudaStream_t s);
 
-// FLOAT: gated_float.cu; dense operands of any alignment to their elements.
+// FLOAT: gated_float.cu; operands of any alignment to their elements.
 // shares: float_share_bytes of device memory; counters: float_counter_bytes
 // of it, zero before the first call (and after every call).
-size_t float_share_bytes(int64_t M, int64_t D, int64_t F, int sm_count);
+size_t float_share_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count);
 size_t float_counter_bytes(int sm_count);
-cudaError_t launch_float(const float* X, const float* Wg, const float* Wu, float* H, float* G, float* U, int64_t M,
-                         int64_t D, int64_t F, int trans_w, int act, void* shares, unsigned int* counters,
-                         int sm_count, cudaStream_t s);
+cudaError_t launch_float(const Product& w, void* shares, unsigned int* counters, int sm_count, cudaStream_t s);
 
 }  // namespace gated
 }  // namespace olc
