@@ -140,13 +140,18 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int is_bf16) {
 // 32 columns of g and u (accumulators) to packed h, g and u
 __device__ __forceinline__ void gate_run(const Params& p, const uint32_t (&g)[32], const uint32_t (&x)[32], uint32_t* ph,
                                          uint32_t* pg, uint32_t* pu) {
+    by_activation(p.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float h0 = gate_value<false, act.value>(__uint_as_float(g[2 * i])) * __uint_as_float(x[2 * i]);
+            const float h1 = gate_value<false, act.value>(__uint_as_float(g[2 * i + 1])) * __uint_as_float(x[2 * i + 1]);
+            ph[i] = pack16(h0, h1, p.is_bf16);
+        }
+    });
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
-        const float u0 = __uint_as_float(x[2 * i]), u1 = __uint_as_float(x[2 * i + 1]);
-        ph[i] = pack16(gate_value<false>(p.act, g0) * u0, gate_value<false>(p.act, g1) * u1, p.is_bf16);
-        pg[i] = pack16(g0, g1, p.is_bf16);
-        pu[i] = pack16(u0, u1, p.is_bf16);
+        pg[i] = pack16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]), p.is_bf16);
+        pu[i] = pack16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), p.is_bf16);
     }
 }
 __device__ __forceinline__ void store_gated(const Params& p, uint32_t* rows, const uint32_t (&ph)[32],
@@ -580,10 +585,15 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p, int mode) {
         const int64_t at = row * p.N + col;
         if (mode == FWD) {
             const float b[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+            float h[4];
+            by_activation(p.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = gate_value<false, act.value>(a[i]) * b[i];
+            });
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (col + i >= p.N) break;
-                static_cast<T*>(p.Y[0])[at + i] = Num<T>::from_acc(gate_value<false>(p.act, a[i]) * b[i]);
+                static_cast<T*>(p.Y[0])[at + i] = Num<T>::from_acc(h[i]);
                 if (p.Y[1]) static_cast<T*>(p.Y[1])[at + i] = Num<T>::from_acc(a[i]);
                 if (p.Y[2]) static_cast<T*>(p.Y[2])[at + i] = Num<T>::from_acc(b[i]);
             }
@@ -610,14 +620,16 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dH, const T* G, con
         const Pack g = *reinterpret_cast<const Pack*>(G + row * cols + col);
         const Pack u = *reinterpret_cast<const Pack*>(U + row * cols + col);
         Pack a, b;
+        by_activation(act, [&](auto which) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float value, slope;
-            gate_slope<EXACT>(act, Num<T>::to_acc(g.v[i]), value, slope);
-            const float d = Num<T>::to_acc(h.v[i]);
-            a.v[i] = Num<T>::from_acc(d * Num<T>::to_acc(u.v[i]) * slope);
-            b.v[i] = Num<T>::from_acc(d * value);
-        }
+            for (int i = 0; i < V; ++i) {
+                float value, slope;
+                gate_slope<EXACT, which.value>(Num<T>::to_acc(g.v[i]), value, slope);
+                const float d = Num<T>::to_acc(h.v[i]);
+                a.v[i] = Num<T>::from_acc(d * Num<T>::to_acc(u.v[i]) * slope);
+                b.v[i] = Num<T>::from_acc(d * value);
+            }
+        });
         *reinterpret_cast<Pack*>(dG + row * pitch + col) = a;
         *reinterpret_cast<Pack*>(dU + row * pitch + col) = b;
     }
@@ -625,8 +637,10 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dH, const T* G, con
 
 // FLOAT: h = act(g) u; h may be u
 __global__ void __launch_bounds__(256) product_kernel(const float* G, const float* U, float* H, int64_t n, int act) {
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256)
-        H[e] = gate_value<true>(act, G[e]) * U[e];
+    by_activation(act, [&](auto which) {
+        for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256)
+            H[e] = gate_value<true, which.value>(G[e]) * U[e];
+    });
 }
 
 // ---- host side ---------------------------------------------------------------------

@@ -267,8 +267,10 @@ kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtens
             v[m][3] = x.w;
         }
         float h[4];
+        by_activation(p.act, [&](auto act) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = gate_value<false>(p.act, v[0][i]) * v[1][i];
+            for (int i = 0; i < 4; ++i) h[i] = gate_value<false, act.value>(v[0][i]) * v[1][i];
+        });
         const int64_t at = row * p.F + col;
         put4(static_cast<T*>(p.H) + at, h, p.F - col, p.quads);
         if (p.G) put4(static_cast<T*>(p.G) + at, v[0], p.F - col, p.quads);

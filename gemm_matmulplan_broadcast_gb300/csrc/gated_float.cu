@@ -271,8 +271,10 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
                 unpack_f2(acc[r][4 + 2 * c + 1], u[2], u[3]);
                 if constexpr (MODE == FWD) {
                     if (col >= p.N) continue;
+                    by_activation(p.act, [&](auto act) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = gate_value<true>(p.act, g[j]) * u[j];
+                        for (int j = 0; j < 4; ++j) h[j] = gate_value<true, act.value>(g[j]) * u[j];
+                    });
                     put_four<VEC>(p.y[0] + row * p.N, col, p.N, h);
                     if (p.y[1]) put_four<VEC>(p.y[1] + row * p.N, col, p.N, g);
                     if (p.y[2]) put_four<VEC>(p.y[2] + row * p.N, col, p.N, u);

@@ -2,6 +2,8 @@
 // and how a product is described.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace olc {
@@ -17,49 +19,43 @@ __device__ __forceinline__ float sigmoid(float g) {
     if constexpr (EXACT) return 1.0f / (1.0f + expf(-g));
     return __fdividef(1.0f, 1.0f + __expf(-g));
 }
-template <bool EXACT>
-__device__ __forceinline__ float gate_value(int act, float g) {
-    switch (act) {
-        case OLC_GATE_SILU: return g * sigmoid<EXACT>(g);
-        case OLC_GATE_GELU:
-            if constexpr (EXACT) return 0.5f * g * erfcf(g * -0.70710678118654752f);
-            return gelu_f32(g);
-        case OLC_GATE_RELU: return g < 0.f ? 0.f : g;
-        default: return sigmoid<EXACT>(g);
+template <bool EXACT, int ACT>
+__device__ __forceinline__ float gate_value(float g) {
+    if constexpr (ACT == OLC_GATE_SILU) return g * sigmoid<EXACT>(g);
+    else if constexpr (ACT == OLC_GATE_GELU) return EXACT ? 0.5f * g * erfcf(g * -0.70710678118654752f) : gelu_f32(g);
+    else if constexpr (ACT == OLC_GATE_RELU) return g < 0.f ? 0.f : g;
+    else return sigmoid<EXACT>(g);
+}
+template <bool EXACT, int ACT>
+__device__ __forceinline__ void gate_slope(float g, float& value, float& slope) {
+    if constexpr (ACT == OLC_GATE_SILU) {
+        const float s = sigmoid<EXACT>(g);
+        value = g * s;
+        slope = s * (1.0f + g * (1.0f - s));
+    } else if constexpr (ACT == OLC_GATE_GELU) {
+        // Phi(g) + g phi(g)
+        const float cdf = EXACT ? 0.5f * erfcf(g * -0.70710678118654752f) : 0.5f * gelu_one_plus_erf_f32(g);
+        const float phi = 0.39894228040143268f * (EXACT ? expf(-0.5f * g * g) : __expf(-0.5f * g * g));
+        value = g * cdf;
+        slope = fmaf(g, phi, cdf);
+    } else if constexpr (ACT == OLC_GATE_RELU) {
+        value = g < 0.f ? 0.f : g;
+        slope = g > 0.f ? 1.f : 0.f;
+    } else {
+        const float s = sigmoid<EXACT>(g);
+        value = s;
+        slope = s * (1.0f - s);
     }
 }
-template <bool EXACT>
-__device__ __forceinline__ void gate_slope(int act, float g, float& value, float& slope) {
+// f(the activation as a constant): one branch around a whole
+// run of elements instead of one at each
+template <typename F>
+__device__ __forceinline__ void by_activation(int act, F&& f) {
     switch (act) {
-        case OLC_GATE_SILU: {
-            const float s = sigmoid<EXACT>(g);
-            value = g * s;
-            slope = s * (1.0f + g * (1.0f - s));
-            return;
-        }
-        case OLC_GATE_GELU: {
-            // Phi(g) + g phi(g)
-            float cdf, phi;
-            if constexpr (EXACT) {
-                cdf = 0.5f * erfcf(g * -0.70710678118654752f);
-                phi = 0.39894228040143268f * expf(-0.5f * g * g);
-            } else {
-                cdf = 0.5f * gelu_one_plus_erf_f32(g);
-                phi = 0.39894228040143268f * __expf(-0.5f * g * g);
-            }
-            value = g * cdf;
-            slope = fmaf(g, phi, cdf);
-            return;
-        }
-        case OLC_GATE_RELU:
-            value = g < 0.f ? 0.f : g;
-            slope = g > 0.f ? 1.f : 0.f;
-            return;
-        default: {
-            const float s = sigmoid<EXACT>(g);
-            value = s;
-            slope = s * (1.0f - s);
-        }
+        case OLC_GATE_SILU: f(std::integral_constant<int, OLC_GATE_SILU>{}); break;
+        case OLC_GATE_GELU: f(std::integral_constant<int, OLC_GATE_GELU>{}); break;
+        case OLC_GATE_RELU: f(std::integral_constant<int, OLC_GATE_RELU>{}); break;
+        default: f(std::integral_constant<int, OLC_GATE_SIGMOID>{});
     }
 }
 

@@ -593,9 +593,23 @@ __device__ __forceinline__ Sums join_row(const Row& r) {
     return q;
 }
 
-// a row's results, by threads t = 0, 1, ... of at least kMaxTop
+// A row's token and its logit, asked for before the row's sums are there.
+struct Given {
+    int64_t token;
+    float logit;
+};
 template <typename T>
-__device__ __forceinline__ void write_row(const Params& p, int64_t row, const Sums& q, const Best& sh, int t) {
+__device__ __forceinline__ Given given_of(const Params& p, int64_t row) {
+    Given g;
+    g.token = p.tokens[row];
+    const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
+    g.logit = g.token >= 0 && g.token < p.vocab ? Num<T>::to_acc(z[g.token]) : 0.f;
+    return g;
+}
+
+// a row's results, by threads t = 0, 1, ... of at least kMaxTop
+__device__ __forceinline__ void write_row(const Params& p, int64_t row, const Given& g, const Sums& q, const Best& sh,
+                                          int t) {
     const bool nothing = q.m == -INFINITY && q.s == 0.f;         // every logit is -inf
     const float log_s = log2f(q.s);
     const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, extreme(q.m) ? q.m : scaled_max(q.m) * kLn2);
@@ -605,12 +619,10 @@ __device__ __forceinline__ void write_row(const Params& p, int64_t row, const Su
         if (p.top_index) p.top_index[row * p.top + t] = sh.best_index[t];
     }
     if (t == 0) {
-        const T* z = static_cast<const T*>(p.logits) + row * p.pitch;
-        const int64_t token = p.tokens[row];
         float lp;
-        if (token < 0) lp = 0.f;                                 // ignored
-        else if (token >= p.vocab) lp = __uint_as_float(0x7FC00000u);
-        else lp = nothing ? -INFINITY : Num<T>::to_acc(z[token]) - lse;
+        if (g.token < 0) lp = 0.f;                               // ignored
+        else if (g.token >= p.vocab) lp = __uint_as_float(0x7FC00000u);
+        else lp = nothing ? -INFINITY : g.logit - lse;
         p.logprob[row] = lp;
         if (p.lse) p.lse[row] = lse;
         if (p.entropy) p.entropy[row] = nothing ? 0.f : (log_s - q.a / q.s) * kLn2;
@@ -667,13 +679,15 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
             const int64_t row = u / parts;
             const int part = (int)(u % parts);       // = the block's rank in its cluster
             const Slice<T> slice = slice_of(static_cast<const T*>(p.logits) + row * p.pitch, p.vocab, part, parts);
+            const Given given = parts == 1 ? given_of<T>(p, row) : Given{0, 0.f};
             if (!tc::mbar_wait(&sh.row_full[buf], phase, abort_flag, p.err)) break;
+            __syncwarp();
             const Sums q = join_row(sh.row[buf]);
             if (p.top > 0) top_of_slice(slice, sh.row[buf], q.s == q.s, p.top, best);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sh.row_empty[buf]);
             if (parts == 1) {
-                write_row<T>(p, row, q, best, lane);
+                write_row(p, row, given, q, best, lane);
                 __syncwarp();
             } else {
                 // every slice's results go to the first block
@@ -743,6 +757,7 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
 
     uint32_t stage = 0, phase = 0, buf = 0, row_phase = 0;
     const uint32_t none = splat<T>(-INFINITY);
+    const Given given = parts > 1 && blockIdx.x % parts == 0 ? given_of<T>(p, blockIdx.x / parts) : Given{0, 0.f};
     for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
         const T* z = static_cast<const T*>(p.logits) + u / parts * p.pitch;
         const Slice<T> slice = slice_of(z, p.vocab, (int)(u % parts), parts);
@@ -828,7 +843,7 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
         }
         sync();
     }
-    write_row<T>(p, blockIdx.x / parts, q, sh.best[0], t);
+    write_row(p, blockIdx.x / parts, given, q, sh.best[0], t);
 }
 
 // One block takes a stretch of a row.  Every element is read and written by
