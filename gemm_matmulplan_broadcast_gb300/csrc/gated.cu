@@ -795,16 +795,20 @@ struct olc_gated_plan {
 
 namespace {
 
-// the FLOAT counters, made when first needed
+// the FLOAT counters, made when first needed; zero before any stream goes on
 olc_status float_counters(olc_gated_plan* p) {
     if (p->counters) return OLC_OK;
     const size_t bytes = gated::float_counter_bytes(p->state.sm_count);
-    if (cudaMalloc(&p->counters, bytes) != cudaSuccess) {
+    void* counters = nullptr;
+    if (cudaMalloc(&counters, bytes) != cudaSuccess) {
         cudaGetLastError();
-        p->counters = nullptr;
         return OLC_ERR_OOM;
     }
-    return plan_status(cudaMemset(p->counters, 0, bytes));
+    cudaError_t e = cudaMemset(counters, 0, bytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
+    if (e == cudaSuccess) p->counters = counters;
+    else p->state.release(counters);
+    return plan_status(e);
 }
 
 // One call's use of the plan's memory: pieces are taken in order, first to

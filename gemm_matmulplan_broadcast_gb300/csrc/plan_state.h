@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstring>
+#include <new>
 
 #include <cuda_runtime.h>
 
@@ -50,10 +51,15 @@ inline bool plan_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(
 // such call waits for it on the GPU (an event, created at the first use).
 // While a stream is capturing a graph nothing is recorded or waited for.
 struct PlanState {
+    struct Earlier {
+        void* memory;
+        Earlier* next;
+    };
     int device;              // -1: made while no device was visible
     int sm_count;
     void* memory;
     size_t bytes;
+    Earlier* earlier;        // smaller blocks that `memory` has replaced
     cudaEvent_t event;
     cudaStream_t stream;
     int event_live;
@@ -79,16 +85,19 @@ struct PlanState {
         return cur == device ? OLC_OK : OLC_ERR_WRONG_DEVICE;
     }
 
-    // grow the plan's memory (the old one is freed first, which waits for
-    // the work that uses it)
+    // Grow the plan's memory.  A graph captured earlier may name the smaller
+    // block: it is kept until the plan is destroyed.
     olc_status ensure(size_t want) {
         if (want <= bytes) return OLC_OK;
-        release_memory();
-        if (cudaMalloc(&memory, want) != cudaSuccess) {
+        Earlier* const keep = memory ? new (std::nothrow) Earlier{memory, earlier} : nullptr;
+        void* larger = nullptr;
+        if ((memory && !keep) || cudaMalloc(&larger, want) != cudaSuccess) {
+            delete keep;
             cudaGetLastError();
-            memory = nullptr;
             return OLC_ERR_OOM;
         }
+        if (keep) earlier = keep;
+        memory = larger;
         bytes = want;
         return OLC_OK;
     }
@@ -126,14 +135,16 @@ struct PlanState {
         if (p) on_device([&] { cudaFree(p); });
     }
 
-    void release_memory() {
-        if (memory) on_device([&] { cudaFree(memory); });
+    void destroy() {
+        release(memory);
         memory = nullptr;
         bytes = 0;
-    }
-
-    void destroy() {
-        release_memory();
+        while (earlier) {
+            Earlier* const e = earlier;
+            earlier = e->next;
+            release(e->memory);
+            delete e;
+        }
         if (event) on_device([&] { cudaEventDestroy(event); });
         event = nullptr;
     }

@@ -262,6 +262,22 @@ def test_repeats_bit_for_bit_on_several_streams():
         assert all(torch.equal(a, b) for a, b in zip(o, got[1]))
 
 
+@pytest.mark.parametrize("dtype,m,d,f", [("float16", 200, 100, 90), ("float32", 2, 96, 64), ("float32", 70, 2000, 100)])
+def test_a_captured_graph_outlives_the_growth_of_the_plans_memory(dtype, m, d, f):
+    x, wg, wu = (t.cuda() for t in inputs(m, d, f, dtype, False, 81))
+    g, u, dh = (normal((m, f), dtype, 84 + i).cuda() for i in range(3))
+    with GatedPlan(m, d, f, dtype) as plan:
+        h, again = torch.empty_like(dh), torch.zeros_like(dh)
+        plan.forward(x, wg, wu, h)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            plan.forward(x, wg, wu, again)
+        plan.backward(dh, x, wg, wu, g, u, dX=torch.empty_like(x), dWg=torch.empty_like(wg), dWu=torch.empty_like(wu))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h, again)
+
+
 def test_refusals():
     x, w, h = torch.zeros(4, 8, device="cuda"), torch.zeros(8, 16, device="cuda"), torch.zeros(4, 16, device="cuda")
     with GatedPlan(4, 8, 16, "float32") as plan:
