@@ -68,6 +68,7 @@ struct Params {
     int a_mn, b_k, b_blocks;
     int is_bf16, act;
     int aligned;              // every output row on a 16-byte boundary
+    int paired;               // every output row on a 4-byte boundary
     void* Y[3];               // FWD: h, g, u (null: not kept); DX: dX; DW: dWg, dWu
     float* partial;           // [split][plane][M][partial_pitch]
     int64_t partial_pitch;
@@ -78,50 +79,66 @@ struct Maps {
     CUtensorMap a[2], b[2];
 };
 
-// one 16-bit row run through the warp's staging rows: 32 rows x 64 columns
-__device__ __forceinline__ void store_run(const Params& p, void* Y, uint32_t* rows, const uint32_t (&packed)[32],
+// A warp's 32 rows of W packed pairs of 16-bit columns through its staging
+// rows, so that a row's run is stored whole.
+template <int W>
+__device__ __forceinline__ void store_run(const Params& p, void* Y, uint32_t* rows, const uint32_t (&packed)[W],
                                           int lane, int64_t row0, int64_t col0) {
-    uint4* mine = reinterpret_cast<uint4*>(rows + lane * STAGE_PITCH);
+    constexpr int PITCH = W + 4, LANES = W / 4;      // lanes on a row
+    uint4* mine = reinterpret_cast<uint4*>(rows + lane * PITCH);
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
+    for (int q = 0; q < LANES; ++q)
         mine[q] = make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]);
     __syncwarp();
     unsigned short* y = static_cast<unsigned short*>(Y);
     if (p.aligned) {
-        const int cq = lane & 7;
+        const int cq = lane % LANES;
         const int64_t col = col0 + cq * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int rr = (lane >> 3) + 4 * j;
-            const uint4 w = *reinterpret_cast<const uint4*>(rows + rr * STAGE_PITCH + cq * 4);
+        for (int j = 0; j < LANES; ++j) {
+            const int rr = lane / LANES + 32 / LANES * j;
+            const uint4 w = *reinterpret_cast<const uint4*>(rows + rr * PITCH + cq * 4);
             if (row0 + rr < p.M && col < p.N) *reinterpret_cast<uint4*>(y + (row0 + rr) * p.N + col) = w;
+        }
+    } else if (p.paired) {
+        const int cw = lane % W;
+        const int64_t col = col0 + cw * 2;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const int rr = lane / W + 32 / W * j;
+            const uint32_t w = rows[rr * PITCH + cw];
+            if (row0 + rr < p.M && col < p.N) *reinterpret_cast<uint32_t*>(y + (row0 + rr) * p.N + col) = w;
         }
     } else {
         const unsigned short* half = reinterpret_cast<const unsigned short*>(rows);
-        for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr) {
+#pragma unroll 8
+        for (int rr = 0; rr < 32; ++rr) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < W / 16; ++j) {
                 const int64_t col = col0 + lane + 32 * j;
-                if (col < p.N) y[(row0 + rr) * p.N + col] = half[rr * STAGE_PITCH * 2 + lane + 32 * j];
+                if (row0 + rr < p.M && col < p.N)
+                    y[(row0 + rr) * p.N + col] = half[rr * PITCH * 2 + lane + 32 * j];
             }
         }
     }
     __syncwarp();                                    // the rows are rewritten by the next run
 }
 
-// 32 float32 columns of the warp's 32 rows into a partial plane
-__device__ __forceinline__ void store_partial(const Params& p, float* plane, uint32_t* rows, const uint32_t (&r)[32],
+// W float32 columns of the warp's 32 rows into a partial plane
+template <int W>
+__device__ __forceinline__ void store_partial(const Params& p, float* plane, uint32_t* rows, const uint32_t* r,
                                               int lane, int64_t row0, int64_t col0) {
-    uint4* mine = reinterpret_cast<uint4*>(rows + lane * STAGE_PITCH);
+    constexpr int PITCH = W + 4, LANES = W / 4;
+    uint4* mine = reinterpret_cast<uint4*>(rows + lane * PITCH);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) mine[q] = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+    for (int q = 0; q < LANES; ++q) mine[q] = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
     __syncwarp();
-    const int cq = lane & 7;
+    const int cq = lane % LANES;
     const int64_t col = col0 + cq * 4;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int rr = (lane >> 3) + 4 * j;
-        const uint4 w = *reinterpret_cast<const uint4*>(rows + rr * STAGE_PITCH + cq * 4);
+    for (int j = 0; j < LANES; ++j) {
+        const int rr = lane / LANES + 32 / LANES * j;
+        const uint4 w = *reinterpret_cast<const uint4*>(rows + rr * PITCH + cq * 4);
         if (row0 + rr < p.M && col < p.partial_pitch)
             *reinterpret_cast<uint4*>(plane + (row0 + rr) * p.partial_pitch + col) = w;
     }
@@ -154,8 +171,9 @@ __device__ __forceinline__ void gate_run(const Params& p, const uint32_t (&g)[32
         pu[i] = pack16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), p.is_bf16);
     }
 }
-__device__ __forceinline__ void store_gated(const Params& p, uint32_t* rows, const uint32_t (&ph)[32],
-                                            const uint32_t (&pg)[32], const uint32_t (&pu)[32], int lane, int64_t row0,
+template <int W>
+__device__ __forceinline__ void store_gated(const Params& p, uint32_t* rows, const uint32_t (&ph)[W],
+                                            const uint32_t (&pg)[W], const uint32_t (&pu)[W], int lane, int64_t row0,
                                             int64_t col0) {
     store_run(p, p.Y[0], rows, ph, lane, row0, col0);
     if (p.Y[1]) store_run(p, p.Y[1], rows, pg, lane, row0, col0);
@@ -334,7 +352,7 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ 
                     const int plane = MODE == FWD ? c >> 7 : item;
                     const int64_t col0 = MODE == FWD ? nb * 128 + (c & 127) : nb * 256 + c;
                     if (row0 >= p.M || col0 >= p.N) continue;
-                    store_partial(p, p.partial + ((int64_t)slice * planes + plane) * p.M * p.partial_pitch, rows, r,
+                    store_partial<32>(p, p.partial + ((int64_t)slice * planes + plane) * p.M * p.partial_pitch, rows, r,
                                   lane, row0, col0);
                 }
             } else if constexpr (MODE == FWD) {
@@ -389,18 +407,23 @@ pair_kernel(const __grid_constant__ CUtensorMap map_a0, const __grid_constant__ 
 
 // 128 rows x 64 columns of both products a CTA (one 128 x 128 accumulator): a
 // quarter of the pair's tile, for products whose pair tiles would leave SMs
-// idle or make a last round of few.  Operands pass through shared memory at
-// its full bandwidth here (both CTAs of a pair share B), so large products
-// keep the pairs.
+// idle.  Operands pass through shared memory at its full bandwidth here (32
+// KiB in and out a K block for 256 cycles of MMAs; both CTAs of a pair share
+// B), so large products keep the pairs.  Eight warps form the outputs, since
+// nothing hides the only tile's epilogue.
 namespace single {
 
 constexpr int COLS = 64;
 constexpr int A_BYTES1 = 128 * BK * 2;
 constexpr int W_BYTES1 = BK * COLS * 2;
 constexpr int STAGE1 = A_BYTES1 + 2 * W_BYTES1;     // 32 KiB
-constexpr int THREADS1 = 192;                       // loader, MMA, 4 epilogue warps
+constexpr int EPI_WARPS = 8;                        // 32 rows x 32 columns each
+constexpr int THREADS1 = (2 + EPI_WARPS) * 32;      // + loader, MMA
+constexpr int ROW_WORDS = 16;                       // words of a staged row
+constexpr int STAGING1 = EPI_WARPS * 32 * (ROW_WORDS + 4) * 4;
+constexpr int SMEM1 = STAGES * STAGE_BYTES + STAGING1 + 1024 + 512;
 constexpr int TMEM1 = 256;                          // two accumulators
-static_assert(STAGE1 == STAGE_BYTES, "the pair's ring and staging sizes hold");
+static_assert(STAGE1 == STAGE_BYTES, "the pair's ring sizes hold");
 
 }  // namespace single
 
@@ -412,7 +435,7 @@ single_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     unsigned char* base =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint32_t* staging = reinterpret_cast<uint32_t*>(base + STAGES * STAGE1);
-    Barriers* s = reinterpret_cast<Barriers*>(base + STAGES * STAGE1 + STAGING_BYTES);
+    Barriers* s = reinterpret_cast<Barriers*>(base + STAGES * STAGE1 + STAGING1);
     volatile int* abort_flag = &s->abort_flag;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -423,7 +446,7 @@ single_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s->acc_full[i], 1);
-            mbar_init(&s->acc_empty[i], 4);
+            mbar_init(&s->acc_empty[i], EPI_WARPS);
         }
         mbar_init(&s->drain, 1);
         s->abort_flag = 0;
@@ -511,8 +534,8 @@ single_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         }
         __syncwarp();
     } else {
-        const int lane_group = warp & 3;
-        uint32_t* rows = staging + lane_group * 32 * STAGE_PITCH;
+        const int lane_group = warp & 3, half = (warp - 2) >> 2;      // rows, columns
+        uint32_t* rows = staging + (warp - 2) * 32 * (ROW_WORDS + 4);
         uint32_t acc = 0, acc_phase = 0;
         for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
             int slice;
@@ -521,27 +544,24 @@ single_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
             const bool ok = mbar_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err);
             if (!__all_sync(0xffffffffu, ok)) break;      // the warp stays together for tcgen05.ld
             tc_fence_after();
-            const int64_t row0 = mb * 128 + lane_group * 32, col0 = nb * COLS;
-            const uint32_t t_base = tmem_base + ((uint32_t)(lane_group * 32) << 16) + acc * 128;
+            const int64_t row0 = mb * 128 + lane_group * 32, col0 = nb * COLS + half * 32;
+            const uint32_t t_base = tmem_base + ((uint32_t)(lane_group * 32) << 16) + acc * 128 + half * 32;
             if (p.splits > 1) {
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
+                for (int plane = 0; plane < 2; ++plane) {
                     uint32_t r[32];
-                    tmem_ld_32x32b_x32(t_base + c, r);
-                    const int64_t col = col0 + (c & 63);
-                    if (row0 >= p.M || col >= p.N) continue;
-                    store_partial(p, p.partial + ((int64_t)slice * 2 + (c >> 6)) * p.M * p.partial_pitch, rows, r, lane,
-                                  row0, col);
+                    tmem_ld_32x32b_x32(t_base + plane * COLS, r);
+                    if (row0 >= p.M || col0 >= p.N) continue;
+                    float* to = p.partial + ((int64_t)slice * 2 + plane) * p.M * p.partial_pitch;
+#pragma unroll
+                    for (int c = 0; c < 32; c += ROW_WORDS)
+                        store_partial<ROW_WORDS>(p, to, rows, r + c, lane, row0, col0 + c);
                 }
             } else {
-                uint32_t ph[32], pg[32], pu[32];
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t g[32], x[32];
-                    tmem_ld_32x32b_x32(t_base + hh * 32, g);
-                    tmem_ld_32x32b_x32(t_base + COLS + hh * 32, x);
-                    gate_run(p, g, x, ph + hh * 16, pg + hh * 16, pu + hh * 16);
-                }
+                uint32_t ph[ROW_WORDS], pg[ROW_WORDS], pu[ROW_WORDS], g[32], x[32];
+                tmem_ld_32x32b_x32(t_base, g);
+                tmem_ld_32x32b_x32(t_base + COLS, x);
+                gate_run(p, g, x, ph, pg, pu);
                 if (row0 < p.M) store_gated(p, rows, ph, pg, pu, lane, row0, col0);
             }
             tc_fence_before();
@@ -649,11 +669,14 @@ constexpr int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // K slices of a product whose units fill `slots` (CTA pairs, or SMs) at most
-// half: enough to fill them, each slice at least four K blocks.
+// half: enough to fill them, each slice at least four K blocks, if a unit is
+// spared more than the pass that joins the slices takes, about 12 K blocks
+// (BF16, us: [65, 1024] x [1024, 2816] 8.6 whole, 9.2 in three slices; [128,
+// 4096] x [4096, 1024] 22.2 whole, 10.7 in nine).
 int slices_of(int64_t tiles, int64_t k_total, int64_t slots) {
     if (tiles <= 0 || 2 * tiles > slots) return 1;
     const int64_t want = min64(slots / tiles, k_total / 4);
-    if (want < 2) return 1;
+    if (want < 2 || k_total - ceil_div(k_total, want) < 12) return 1;
     return (int)ceil_div(k_total, ceil_div(k_total, want));    // no empty slice
 }
 
@@ -666,21 +689,25 @@ struct Cut {
 };
 Cut cut_of(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
     const int64_t kb = ceil_div(K, BK), pairs = sm_count / 2;
+    const int64_t k_total = kb * (mode == DX ? 2 : 1);
     Cut c{false, ceil_div(M, 256), ceil_div(N, mode == FWD ? 128 : 256), 1};
+    c.splits = slices_of(c.tiles_m * c.tiles_n * (mode == DW ? 2 : 1), k_total, pairs);
     if (mode == FWD) {
-        // rounds over the machine x the time of a unit: per K block 512 cycles
-        // of a pair's MMAs, half of that on a single CTA (a sixth more while
-        // shared memory feeds both operands to one SM), and about 3000 and
-        // 2000 cycles of a unit's fill and epilogue that nothing hides
-        const int64_t sm_tiles = ceil_div(M, 128) * ceil_div(N, single::COLS);
-        const int64_t on_pairs = ceil_div(c.tiles_m * c.tiles_n, pairs) * (kb * 512 + 3000);
-        const int64_t on_sms = ceil_div(sm_tiles, sm_count) * (kb * 300 + 2000);
-        if (on_sms < on_pairs) {
-            c = Cut{true, ceil_div(M, 128), ceil_div(N, single::COLS), slices_of(sm_tiles, kb, sm_count)};
-            return c;
-        }
+        // A K block of a unit takes about 550 cycles on both: the pair's MMAs,
+        // or a single CTA's operands on their way into and out of shared
+        // memory (twice its MMAs' time).  What surrounds a unit's K blocks
+        // takes some 5500 cycles more on a pair.  So single CTAs take what
+        // fits them in no more rounds (us: [333, 4000] x [4000, 2736] FP16
+        // 22.8 against 25.7; BF16 [512, 1024] x [1024, 4096] 14.4 against
+        // 12.8, [2048, 1024] x [1024, 4096] 40.3 against 30.0, [256, 4096] x
+        // [4096, 14336] 60.6 against 52.7).
+        Cut one{true, ceil_div(M, 128), ceil_div(N, single::COLS), 1};
+        one.splits = slices_of(one.tiles_m * one.tiles_n, k_total, sm_count);
+        auto cycles = [&](const Cut& x, int64_t slots) {
+            return ceil_div(x.tiles_m * x.tiles_n * x.splits, slots) * ceil_div(k_total, x.splits) * 550;
+        };
+        if (cycles(one, sm_count) < cycles(c, pairs) + 5500) return one;
     }
-    c.splits = slices_of(c.tiles_m * c.tiles_n * (mode == DW ? 2 : 1), kb * (mode == DX ? 2 : 1), pairs);
     return c;
 }
 size_t product_partial_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
@@ -729,19 +756,21 @@ cudaError_t launch_product(olc_dtype dt, const Product& w, float* partial, int s
     p.is_bf16 = bf;
     p.act = w.act;
     p.aligned = w.N % 8 == 0;
+    p.paired = w.N % 2 == 0;
     for (int i = 0; i < 3; ++i) {
         p.Y[i] = w.Y[i];
         if (w.Y[i] && !plan_aligned16(w.Y[i])) p.aligned = 0;
+        if (w.Y[i] && plan_misaligned(w.Y[i], 4)) p.paired = 0;
     }
     p.partial = partial;
     p.partial_pitch = pad8(w.N);
     p.err = device_error_word();
     cudaError_t e;
     if (cut.single) {
-        e = set_smem_limit(reinterpret_cast<const void*>(single_kernel), SMEM_BYTES);
+        e = set_smem_limit(reinterpret_cast<const void*>(single_kernel), single::SMEM1);
         if (e == cudaSuccess)
             e = plan_launch(single_kernel, dim3((unsigned)min64(p.units, sm_count)), dim3(single::THREADS1),
-                           (size_t)SMEM_BYTES, s, maps.a[0], maps.b[0], maps.b[1], p);
+                           (size_t)single::SMEM1, s, maps.a[0], maps.b[0], maps.b[1], p);
     } else {
         e = set_smem_limit(reinterpret_cast<const void*>(pair_kernel<MODE>), SMEM_BYTES);
         if (e != cudaSuccess) return e;
