@@ -556,25 +556,32 @@ __global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
     }
 }
 
-// Rows of 16-byte packs: one row a block at a time, x and dy copied ahead into
-// a ring of kAhead rows by bulk copies.  The barrier of the row's sums also
-// tells that every thread has read the row: its buffer takes another.
+// Rows of 16-byte packs: a group of threads takes one row at a time, x and dy
+// copied ahead into its own ring of kAhead rows by bulk copies.  The barrier
+// of the row's sums also tells that every thread has read the row: its buffer
+// takes another.  The groups of a block join their column sums in group order,
+// so that an SM leaves one set of partial sums.  WARPS: at least a group's;
 // FULL: every thread has NV packs.
 constexpr int kAhead = 3;
+constexpr int kMaxGroups = 16;        // 512 threads, a warp or more on a row
 template <typename T, int NV, int WARPS, bool FULL>
-__global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(512) backward_ring_kernel(const BwdParams p) {
     constexpr int V = 16 / sizeof(T);
-    extern __shared__ __align__(128) unsigned char ring[];
-    __shared__ alignas(16) float2 slots[2][WARPS];
-    __shared__ uint64_t full[kAhead];
+    extern __shared__ __align__(128) unsigned char rings[];
+    __shared__ alignas(16) float2 all_slots[kMaxGroups][2][WARPS];
+    __shared__ uint64_t all_full[kMaxGroups][kAhead];
     __shared__ int abort_flag;
-    const int t = threadIdx.x, threads = blockDim.x;
+    const int threads = p.threads_per_row, groups = blockDim.x / threads;
+    const int grp = threadIdx.x / threads, t = threadIdx.x - grp * threads;
     const int cols = (int)p.cols;
     const uint32_t row_bytes = (uint32_t)cols * sizeof(T);
+    unsigned char* const ring = rings + (size_t)grp * kAhead * 2 * row_bytes;
+    float2(&slots)[2][WARPS] = all_slots[grp];
+    uint64_t(&full)[kAhead] = all_full[grp];
     if (t < WARPS) slots[0][t] = slots[1][t] = make_float2(0.f, 0.f);
+    if (threadIdx.x == 0) abort_flag = 0;
     if (t == 0) {
         for (int i = 0; i < kAhead; ++i) tc::mbar_init(&full[i], 1);
-        abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -586,9 +593,10 @@ __global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdPara
         bulk_copy(to, static_cast<const T*>(p.X) + row * p.x_pitch, row_bytes, &full[stage]);
         bulk_copy(to + row_bytes, static_cast<const T*>(p.dY) + row * p.dy_pitch, row_bytes, &full[stage]);
     };
-    int64_t row = blockIdx.x;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + grp;
     if (t == 0)
-        for (int i = 0; i < kAhead; ++i) fetch(row + (int64_t)i * gridDim.x, i);
+        for (int i = 0; i < kAhead; ++i) fetch(row + i * step, i);
     RowGrads<T, V, NV> r;
     r.clear();
     const Pack<T, V> zero{};
@@ -600,8 +608,8 @@ __global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdPara
     int stage = 0, phase = 0, buf = 0;
     float mean = row < p.rows ? p.mean[row] : 0.f, rstd = row < p.rows ? p.rstd[row] : 0.f;
     T* dx = p.dX ? static_cast<T*>(p.dX) + row * p.dx_pitch : nullptr;
-    const int64_t dx_step = gridDim.x * p.dx_pitch;
-    for (; row < p.rows; row += gridDim.x, buf ^= 1, dx += dx_step) {
+    const int64_t dx_step = step * p.dx_pitch;
+    for (; row < p.rows; row += step, buf ^= 1, dx += dx_step) {
         // a wait that runs out: the row's sums are of what is there, the error word tells
         tc::mbar_wait(&full[stage], phase, &abort_flag, p.err);
         const T* x = reinterpret_cast<const T*>(ring + (size_t)stage * 2 * row_bytes);
@@ -614,15 +622,17 @@ __global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdPara
             const bool in = FULL || at < cols;
             r.take(i, in ? load<T, V>(x + at) : zero, in ? load<T, V>(dy + at) : zero, minus_mean, scale, c1, c2);
         }
-        const int64_t next = row + gridDim.x;
+        const int64_t next = row + step;
         if (next < p.rows) {
             mean = p.mean[next];
             rstd = p.rstd[next];
         }
         const float2 own = make_float2(warp_sum(sum_of<V>(c1)), warp_sum(sum_of<V>(c2)));
         if ((t & 31) == 0) slots[buf][t >> 5] = own;
-        __syncthreads();
-        if (t == 0) fetch(row + (int64_t)kAhead * gridDim.x, stage);
+        __syncwarp();
+        // the group (named barriers 1 to 15 suffice: 16 groups are warps)
+        if (threads > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(threads) : "memory");
+        if (t == 0) fetch(row + kAhead * step, stage);
         if (++stage == kAhead) {
             stage = 0;
             phase ^= 1;
@@ -644,7 +654,26 @@ __global__ void __launch_bounds__(WARPS * 32) backward_ring_kernel(const BwdPara
             tc::mbar_wait_drain(&full[i], 1);
         }
     }
-    if (p.partial) r.leave(p.partial + (int64_t)blockIdx.x * 2 * cols, cols, t, threads);
+    if (!p.partial) return;
+    float* const out = p.partial + (int64_t)blockIdx.x * 2 * cols;
+    if (groups == 1) {
+        r.leave(out, cols, t, threads);
+        return;
+    }
+    __syncthreads();                                 // every row has been read: the rings' memory is free
+    r.leave(reinterpret_cast<float*>(rings) + (size_t)grp * 2 * cols, cols, t, threads);
+    __syncthreads();
+    for (int c = threadIdx.x * 4; c < 2 * cols; c += blockDim.x * 4) {
+        float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(rings) + c);
+        for (int g = 1; g < groups; ++g) {
+            const float4 b = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(rings) + (size_t)g * 2 * cols + c);
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+        }
+        *reinterpret_cast<float4*>(out + c) = a;
+    }
 }
 
 // Rows of 16-byte packs twice as wide: the row stays in the ring until the
@@ -810,27 +839,33 @@ __global__ void __launch_bounds__(256) backward_long_cols_kernel(const BwdParams
     p.partial[((int64_t)blockIdx.y * 2 + 1) * p.cols + c] = b;
 }
 
-// Column sums over the blocks' partial sums, in block order within each of 32
-// shares and then in share order: the same for every run.
-template <typename T>
+// Column sums over the blocks' partial sums, C columns a block: in block order
+// within each share of them and then in share order, the same for every run.
+template <typename T, int C>
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int blocks, int64_t cols,
                                                           T* dgamma, T* dbeta) {
-    __shared__ float sums[32][33];
+    constexpr int SHARES = 1024 / C;
+    __shared__ float sums[SHARES][C + 1];
     T* out = blockIdx.y ? dbeta : dgamma;
     if (!out) return;
-    const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int col = threadIdx.x % C, share = threadIdx.x / C;
+    const int64_t c = (int64_t)blockIdx.x * C + col;
     float s = 0.f;
     if (c < cols) {
 #pragma unroll 10
-        for (int b = share; b < blocks; b += 32) s += partial[((int64_t)b * 2 + blockIdx.y) * cols + c];
+        for (int b = share; b < blocks; b += SHARES) s += partial[((int64_t)b * 2 + blockIdx.y) * cols + c];
     }
-    sums[share][lane] = s;
+    sums[share][col] = s;
     __syncthreads();
-    // a warp a column: its 32 shares
-    s = warp_sum(sums[lane][share]);
-    const int64_t mine = (int64_t)blockIdx.x * 32 + share;
-    if (lane == 0 && mine < cols) out[mine] = Num<T>::from_acc(s);
+    // a warp a column
+    const int lane = threadIdx.x & 31, mine = threadIdx.x >> 5;
+    if (mine >= C) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < SHARES / 32; ++i) s += sums[lane + 32 * i][mine];
+    s = warp_sum(s);
+    const int64_t to = (int64_t)blockIdx.x * C + mine;
+    if (lane == 0 && to < cols) out[to] = Num<T>::from_acc(s);
 }
 
 // ---- host side -------------------------------------------------------------
@@ -889,6 +924,16 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     return plan_launch(forward_long_kernel<T, V>, dim3((unsigned)grid), dim3(1024), 0, s, p);
 }
 
+// Rows of 16-byte packs go through the ring from this width on ([16384, 512]
+// BF16: 14.0 us, from registers 21.4; [16384, 256]: 10.8 and 12.6; [16384, 128]:
+// 10.8 and 11.4, but [2048, 128] FLOAT 6.3 and 5.1).
+constexpr int64_t kRingCols = 256;
+// A group takes at least this many rows: more blocks read faster, fewer leave
+// fewer partial sums ([608, 4096] BF16: 9.9 us; at least one row 13.1, eight 11.5).
+constexpr int64_t kLeastRows = 4;
+// Up to this width the column sums are split eight columns a block, above it 32
+// ([16384, 1024] BF16 27.0 and 28.0 us, [16384, 4096] 72.4 and 68.9).
+constexpr int64_t kNarrowCols = 2048;
 constexpr int kRingSmem = kAhead * 2 * 512 * 16 * 4;     // rings of the widest float32 rows
 constexpr int64_t kWideSmem = 208 * 1024;   // ring of the wide rows
 constexpr int kColsPerThread = 16;      // float32 column sums of dgamma and dbeta: 32 registers
@@ -906,23 +951,27 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
     BwdShape b;
     constexpr int64_t size = V == 1 ? 0 : 16 / V;
     if (V > 1 && cols > 512 * kColsPerThread && cols <= kWideThreads * kWideColumns &&
-        4 * cols * size <= kWideSmem && rows >= 2 * (int64_t)sm_count) {
+        4 * cols * size <= kWideSmem && rows >= kLeastRows * sm_count) {
+        // ([4096, 12288] BF16: 83 us; in passes over rows and columns 162)
         b.kind = BwdShape::WIDE;
-        b.blocks = min64(rows, sm_count);
+        b.blocks = sm_count;
         return b;
     }
     if (cols > 512 * kColsPerThread) {
         b.blocks = min64(max64(rows / 64, 1), max64(1, 8 * (int64_t)sm_count * 256 / cols));
         return b;
     }
-    // whole rows of 16-byte packs through the ring, where a block takes
-    // several: two blocks on an SM
-    if (V > 1 && cols >= 1024 && rows >= 4 * (int64_t)sm_count) {
+    // whole rows of 16-byte packs through the ring, as many groups as rows
+    // suffice for ([16384, 4096] BF16: 66.5 us, 403 MB of x, dy and dx at 6.1
+    // TB/s; with blocks of one group 68.9; [2048, 1024]: 7.8 and 9.9)
+    if (V > 1 && cols >= kRingCols) {
         b.kind = BwdShape::RING;
         b.per_thread = kColsPerThread;
-        b.tpr = b.threads = (int)(ceil_div(ceil_div(cols, kColsPerThread), 32) * 32);
-        // two blocks on an SM, more where they are small
-        b.blocks = min64(rows, (int64_t)sm_count * max64(2, min64(8, 512 / b.threads)));
+        b.tpr = (int)(ceil_div(ceil_div(cols, kColsPerThread), 32) * 32);
+        b.groups = (int)max64(1, min64(512 / b.tpr, ceil_div(rows, kLeastRows * sm_count)));
+        b.threads = b.tpr * b.groups;
+        // 512 threads an SM, or two blocks of wider rows
+        b.blocks = max64(1, min64(ceil_div(rows, kLeastRows * b.groups), (int64_t)sm_count * (b.tpr > 256 ? 2 : 1)));
         return b;
     }
     b.kind = BwdShape::ANY;
@@ -930,9 +979,9 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
     b.per_thread = least;
     while (b.per_thread < kColsPerThread && cols > 32 * b.per_thread) b.per_thread *= 2;
     b.tpr = (int)(ceil_div(ceil_div(cols, b.per_thread), 32) * 32);
-    b.groups = b.tpr >= 256 ? 1 : 256 / b.tpr;
+    b.groups = (int)max64(1, min64(512 / b.tpr, ceil_div(2 * rows, sm_count)));
     b.threads = b.tpr * b.groups;
-    b.blocks = max64(1, min64(ceil_div(rows, b.groups), (int64_t)sm_count * (b.threads > 256 ? 1 : (b.per_thread > 8 ? 2 : 4))));
+    b.blocks = max64(1, min64(ceil_div(rows, b.groups), (int64_t)sm_count * (b.per_thread > 8 ? 1 : 2)));
     return b;
 }
 
@@ -948,7 +997,7 @@ cudaError_t backward_ring(const BwdParams& p, const BwdShape& b, cudaStream_t s)
     const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), kRingSmem);
     if (e != cudaSuccess) return e;
     return plan_launch(kernel, dim3((unsigned)b.blocks), dim3((unsigned)b.threads),
-                      kAhead * 2 * (size_t)p.cols * sizeof(T), s, p);
+                      b.groups * kAhead * 2 * (size_t)p.cols * sizeof(T), s, p);
 }
 
 template <typename T, int V>
@@ -975,8 +1024,8 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
         }
     } else if (b.kind == BwdShape::RING) {
         if constexpr (V > 1) {
-            const bool full = p.cols == (int64_t)b.threads * kColsPerThread;
-            if (b.threads <= 256)
+            const bool full = p.cols == (int64_t)b.tpr * kColsPerThread;
+            if (b.tpr <= 256)
                 e = full ? backward_ring<T, 8, true>(p, b, s) : backward_ring<T, 8, false>(p, b, s);
             else
                 e = full ? backward_ring<T, 16, true>(p, b, s) : backward_ring<T, 16, false>(p, b, s);
@@ -989,9 +1038,13 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
         if (b.per_thread == 4) e = backward_rows<T, V, V == 1 ? 2 : 1>(p, b, s);
         else if constexpr (V == 1) e = backward_rows<T, 1, 1>(p, b, s);
     }
-    if (e == cudaSuccess && p.partial)
-        e = plan_launch(column_sum_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32), 2), dim3(1024), 0, s,
-                       (const float*)p.partial, (int)b.blocks, p.cols, dgamma, dbeta);
+    if (e == cudaSuccess && p.partial) {
+        auto run = [&](auto kernel, int c) {
+            return plan_launch(kernel, dim3((unsigned)ceil_div(p.cols, c), 2), dim3(1024), 0, s,
+                               (const float*)p.partial, (int)b.blocks, p.cols, dgamma, dbeta);
+        };
+        e = p.cols <= kNarrowCols ? run(column_sum_kernel<T, 8>, 8) : run(column_sum_kernel<T, 32>, 32);
+    }
     return e;
 }
 
