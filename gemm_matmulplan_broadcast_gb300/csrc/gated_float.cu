@@ -2,12 +2,17 @@
 // which keep float32 products exact to one rounding (the tensor cores round
 // their operands).
 //
-// Operations at two a paired FMA bound them.  A block of 64 threads takes 64 rows
-// x 128 columns, 8 x 16 accumulators a thread: 64 paired FMAs then take six
-// 16-byte reads of shared memory, three quarters of its cycles (8 x 8: all of
-// them, which bounds that form).  Slices of K, 16 deep, come through
-// asynchronous copies two ahead; an operand B stored with its K contiguous is
-// transposed through registers.  What the columns and the K are:
+// Operations at two a paired FMA bound them.  A block takes 64 rows x 128
+// columns: 64 threads with 8 x 16 accumulators each, or 128 with 8 x 8 where
+// there are few tiles.  64 paired FMAs (128 cycles) then take six 16-byte reads
+// of shared memory and the copies that make pairs of A's elements.  Slices of K,
+// 16 deep, come through asynchronous copies two ahead; an operand B stored with
+// its K contiguous is transposed through registers.  Measured at [1024, 1024] x
+// [1024, 2816]: 237 us, 50 TFLOP/s of the pipes' 79.5; the pipes are busy 68 % of
+// the active cycles, two warps on a scheduler (the accumulators' registers)
+// leaving the rest to dependent issues and the last round's unequal ends.
+// [2048, 2048] x [2048, 5632]: 1700 us, 55.6 TFLOP/s.  What the columns and the K
+// are:
 //
 //   FWD  64 columns of Wg next to the same 64 of Wu: a thread holds g and u of the
 //        same outputs and forms act(g) u from registers
@@ -28,11 +33,14 @@ namespace gated {
 namespace f32 {
 
 constexpr int TM = 64, TN = 64, KS = 16;          // rows, half of the columns, depth of a slice
-constexpr int THREADS = 64;
 constexpr int STAGES = 3;
 constexpr int AP = KS + 4;                        // floats between rows of A's tile: four rows in four bank groups
 constexpr int A_FLOATS = TM * AP, B_FLOATS = KS * 2 * TN;
+constexpr int TILE_VECS = TM * 2 * TN / 4;        // 16-byte vectors of a tile's sums
 constexpr int SMEM_BYTES = STAGES * (A_FLOATS + B_FLOATS) * 4;
+
+// blocks that reside (registers)
+constexpr int per_sm(int threads) { return threads == 64 ? 4 : 3; }
 
 struct Params {
     const float *a[2], *b[2]; // FWD: a[0] = X, b = Wg, Wu; DX: dg, du and Wg, Wu; DW: the two outputs' operands
@@ -45,7 +53,7 @@ struct Params {
     int source_slices;        // slices of one operand pair
     int slices;               // of a tile (DX: both pairs')
     int act;
-    float4* shares;           // [2 blocks][32][threads]: partial sums of a block's first and last shared tile
+    float4* shares;           // [2 blocks][TILE_VECS]: partial sums of a block's first and last shared tile
     unsigned int* arrived;    // [shared tiles], zero between launches
 };
 
@@ -94,12 +102,23 @@ __device__ __forceinline__ void copy_four(float* to, const float* from, const fl
     }
 }
 
-// A_T: A is stored [K, M]; B_T: B is stored [N, K]
-template <int MODE, bool VEC, bool A_T, bool B_T>
-__global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
+// A_T: A is stored [K, M]; B_T: B is stored [N, K].  THREADS: 64 with 8 x 16
+// accumulators each, or 128 with 8 x 8.
+template <int MODE, bool VEC, bool A_T, bool B_T, int THREADS>
+__global__ void __launch_bounds__(THREADS, per_sm(THREADS)) kernel(const Params p) {
     extern __shared__ __align__(16) float smem[];     // stages of A [64 rows][k] (A_T: [k][64 rows]), B [k][2 x 64]
     __shared__ int last;
-    const int t = threadIdx.x, tx = t & 7, ty = t >> 3;
+    const int t = threadIdx.x;
+    // A warp's lanes over its rows and columns.  SPREAD: lanes two apart read the
+    // same columns and neighbours the same rows, which lets a 16-byte read of
+    // shared memory serve half a warp at once (two wavefronts a read instead of
+    // four); otherwise columns along the lanes, which stores faster.  us of
+    // [1024, 1024] x [1024, 2816], SPREAD and not: forward 240 and 236, with
+    // weights stored [F, D] 280 and 291, gradient 489 and 505.
+    constexpr bool SPREAD = MODE != FWD || B_T;
+    constexpr int CG = 128 / THREADS;         // groups of 32 columns a thread has of each half
+    const int tx = SPREAD ? (t & 1) | ((t >> 1) & 6) | (CG == 1 ? (t >> 2) & 8 : 0) : t % (16 / CG);
+    const int ty = SPREAD ? ((t >> 1) & 1) | ((t >> 3) & 2) | (t / (THREADS / 2)) * 4 : t / (16 / CG);
     const int64_t grid = gridDim.x, block = blockIdx.x;
     // the shared tiles' slices, laid end to end
     const int64_t whole = p.rounds * grid, steps = (p.tiles - whole) * p.slices, sharers = p.sharers;
@@ -112,14 +131,15 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
     float* const bs = smem + STAGES * A_FLOATS;
 
     // A slice's addresses advance by additions.  An operand with K contiguous:
-    // this thread takes rows t / 4 + 16 q of A at K elements 4 (t % 4), one row of
-    // each half of B at all sixteen; one with its rows along K: K elements t / 16
-    // + 4 q at elements 4 (t % 16).
+    // this thread takes rows t / 4 + AR q of A at K elements 4 (t % 4), one row of
+    // (each half of) B at all sixteen; one with its rows along K: K elements t / 16
+    // + KR q at elements 4 (t % 16).
+    constexpr int Q = 256 / THREADS, AR = THREADS / 4, KR = THREADS / 16;
     const float *pa = nullptr, *pb[2] = {nullptr, nullptr};
     int ka = 0, kb = 0;              // their K elements
     unsigned rows_in = 0;
     int left_a = 0, left_b[2] = {0, 0};       // elements from this thread's to the row's end
-    const int64_t da = (A_T ? 4 : 16) * p.lda, db = 4 * p.ldb;
+    const int64_t da = (A_T ? KR : AR) * p.lda, db = KR * p.ldb;
     float* const a_to = A_T ? as + (t >> 4) * TM + (t & 15) * 4 : as + (t >> 2) * AP + (t & 3) * 4;
     float* const b_to = B_T ? bs + t : bs + (t >> 4) * 2 * TN + (t & 15) * 4;
     // from slice s0 of operand pair `source`
@@ -135,43 +155,44 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
             const int row = m0 + (t >> 2);
             rows_in = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) rows_in |= (unsigned)(row + 16 * q < M) << q;
+            for (int q = 0; q < Q; ++q) rows_in |= (unsigned)(row + AR * q < M) << q;
             ka = k0 + (t & 3) * 4;
             pa = A + (int64_t)row * p.lda + ka;
         }
         kb = B_T ? k0 : k0 + (t >> 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int q = 0; q < (B_T ? CG : 2); ++q) {
+            const int h = B_T ? (t + q * THREADS) / TN : q;
             const float* B = MODE == FWD ? p.b[h] : p.b[source];
-            const int col = n0 + (MODE == FWD ? 0 : h * TN) + (B_T ? t : (t & 15) * 4);
-            left_b[h] = N - col;
-            pb[h] = B_T ? B + (int64_t)col * p.ldb + kb : B + (int64_t)kb * p.ldb + col;
+            const int col = n0 + (MODE == FWD ? 0 : h * TN) + (B_T ? t % TN : (t & 15) * 4);
+            left_b[q] = N - col;
+            pb[q] = B_T ? B + (int64_t)col * p.ldb + kb : B + (int64_t)kb * p.ldb + col;
         }
     };
     auto fetch = [&](int stage) {
         float* a = a_to + stage * A_FLOATS;
         float* b = b_to + stage * B_FLOATS;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if constexpr (A_T) copy_four<VEC>(a + 4 * q * TM, pa + q * da, p.a[0], ka + 4 * q < K ? left_a : 0);
-            else copy_four<VEC>(a + 16 * q * AP, pa + q * da, p.a[0], (rows_in >> q) & 1u ? K - ka : 0);
+        for (int q = 0; q < Q; ++q) {
+            if constexpr (A_T) copy_four<VEC>(a + KR * q * TM, pa + q * da, p.a[0], ka + KR * q < K ? left_a : 0);
+            else copy_four<VEC>(a + AR * q * AP, pa + q * da, p.a[0], (rows_in >> q) & 1u ? K - ka : 0);
         }
-        pa += A_T ? 4 * da : KS;
+        pa += A_T ? Q * da : KS;
         ka += KS;
         if constexpr (!B_T) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < Q; ++q)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    copy_four<VEC>(b + 4 * q * 2 * TN + h * TN, pb[h] + q * db, p.b[0],
-                                   kb + 4 * q < K ? left_b[MODE == FWD ? 0 : h] : 0);
-            pb[0] += 4 * db;
-            pb[1] += 4 * db;
+                    copy_four<VEC>(b + KR * q * 2 * TN + h * TN, pb[h] + q * db, p.b[0],
+                                   kb + KR * q < K ? left_b[MODE == FWD ? 0 : h] : 0);
+            pb[0] += Q * db;
+            pb[1] += Q * db;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if constexpr (B_T) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < CG; ++h) {
                 float4 v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = four<VEC>(pb[h] + 4 * i, left_b[MODE == FWD ? 0 : h] > 0 ? K - kb - 4 * i : 0);
@@ -185,13 +206,14 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
                 }
             }
             pb[0] += KS;
-            pb[1] += KS;
+            if constexpr (CG == 2) pb[1] += KS;
         }
         kb += KS;
     };
 
-    // rows ty + 8 i (A_T: 8 ty + i); columns 32 c + 4 tx + (0..3) of the first half (j = 0..3), then of the second
-    F2 acc[8][8];
+    // rows ty + 8 i (A_T: 8 ty + i); columns 32 c + 4 tx + (0..3) of the first half (j < 2 CG), then of the second
+    constexpr int J = 4 * CG;
+    F2 acc[8][J];
 
     // acc += the tile's products over slices [s0, s0 + n) of one operand pair
     auto multiply_pair = [&](int source, int s0, int n) {
@@ -219,10 +241,10 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
                     x[r] = *reinterpret_cast<const float4*>(A_T ? a + (k4 + (r >> 1)) * TM + (r & 1) * 4 : a + r * 8 * AP + k4);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    F2 w[8];
+                    F2 w[J];
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(b + (k4 + k) * 2 * TN + h * 32);
+                    for (int h = 0; h < J / 2; ++h) {
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(b + (k4 + k) * 2 * TN + h * (32 * 2 / CG));
                         w[2 * h] = v.x;
                         w[2 * h + 1] = v.y;
                     }
@@ -233,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
                         const float e = at == 0 ? v.x : (at == 1 ? v.y : (at == 2 ? v.z : v.w));
                         const F2 e2 = pack_f2(e, e);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) fma_f2(acc[r][j], e2, w[j]);
+                        for (int j = 0; j < J; ++j) fma_f2(acc[r][j], e2, w[j]);
                     }
                 }
             }
@@ -244,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] = 0;
+            for (int j = 0; j < J; ++j) acc[i][j] = 0;
         if constexpr (MODE == DX) {
             const int s1 = s0 + n, half = p.source_slices;
 #pragma unroll 1
@@ -262,13 +284,13 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
             const int64_t row = m0 + (A_T ? ty * 8 + r : ty + 8 * r);
             if (row >= M) continue;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < CG; ++c) {
                 const int64_t col = n0 + 32 * c + tx * 4;
                 float g[4], u[4], h[4];
                 unpack_f2(acc[r][2 * c], g[0], g[1]);
                 unpack_f2(acc[r][2 * c + 1], g[2], g[3]);
-                unpack_f2(acc[r][4 + 2 * c], u[0], u[1]);
-                unpack_f2(acc[r][4 + 2 * c + 1], u[2], u[3]);
+                unpack_f2(acc[r][J / 2 + 2 * c], u[0], u[1]);
+                unpack_f2(acc[r][J / 2 + 2 * c + 1], u[2], u[3]);
                 if constexpr (MODE == FWD) {
                     if (col >= p.N) continue;
                     by_activation(p.act, [&](auto act) {
@@ -314,17 +336,17 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
         const int64_t u0 = tile * p.slices, u1 = u0 + p.slices - 1;
         const int64_t c0 = ((u0 + 1) * sharers - 1) / steps, c1 = ((u1 + 1) * sharers - 1) / steps;
         auto slot = [&](int64_t c) {          // where block c left this tile: its first shared tile, or its last
-            return p.shares + (2 * c + (c * steps / sharers / p.slices == tile ? 0 : 1)) * (32 * THREADS) + t;
+            return p.shares + (2 * c + (c * steps / sharers / p.slices == tile ? 0 : 1)) * TILE_VECS + t;
         };
         float4* mine = slot(block);
 #pragma unroll
         for (int r = 0; r < 8; ++r)
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
+            for (int j = 0; j < J; j += 2) {
                 float4 v;
                 unpack_f2(acc[r][j], v.x, v.y);
                 unpack_f2(acc[r][j + 1], v.z, v.w);
-                __stcg(mine + (r * 4 + j / 2) * THREADS, v);
+                __stcg(mine + (r * (J / 2) + j / 2) * THREADS, v);
             }
         __threadfence();
         __syncthreads();
@@ -335,14 +357,14 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] = 0;
+            for (int j = 0; j < J; ++j) acc[i][j] = 0;
         for (int64_t c = c0; c <= c1; ++c) {
             const float4* from = slot(c);
 #pragma unroll
             for (int r = 0; r < 8; ++r)
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float4 v = __ldcg(from + (r * 4 + j / 2) * THREADS);
+                for (int j = 0; j < J; j += 2) {
+                    const float4 v = __ldcg(from + (r * (J / 2) + j / 2) * THREADS);
                     acc[r][j] = add2(acc[r][j], pack_f2(v.x, v.y));
                     acc[r][j + 1] = add2(acc[r][j + 1], pack_f2(v.z, v.w));
                 }
@@ -354,12 +376,11 @@ __global__ void __launch_bounds__(THREADS, 4) kernel(const Params p) {
 
 }  // namespace f32
 
-constexpr int kFloatPerSm = 4;            // blocks that reside (registers)
-
 namespace {
 
 // How a product is cut; rows and columns of one output, K of one operand pair.
 struct FloatShape {
+    int threads;
     int64_t tiles_m, tiles_item, tiles, grid, rounds, sharers;
     int source_slices, slices;
 };
@@ -370,7 +391,12 @@ FloatShape float_shape(int mode, int64_t M, int64_t N, int64_t K, int sm_count) 
     f.tiles = f.tiles_item * (mode == DW ? 2 : 1);
     f.source_slices = (int)ceil_div(K, f32::KS);
     f.slices = f.source_slices * (mode == DX ? 2 : 1);
-    f.grid = max64(1, min64((int64_t)kFloatPerSm * sm_count, f.tiles * max64(1, f.slices / 4)));
+    // less than a round of the blocks that multiply fastest: twice the warps on
+    // a tile, 8 x 8 accumulators a thread ([300, 1000] x [1000, 2730]: 91 us,
+    // with 64 threads 107; [16, 1024] x [1024, 2816]: 32 and 40; [2048, 2048] x
+    // [2048, 5632]: 1755 and 1700)
+    f.threads = f.tiles < (int64_t)f32::per_sm(64) * sm_count ? 128 : 64;
+    f.grid = max64(1, min64((int64_t)f32::per_sm(f.threads) * sm_count, f.tiles * max64(1, f.slices / 4)));
     f.rounds = f.tiles / f.grid;
     // no share is empty, and at most about 16 meet in a tile
     const int64_t least = max64(4, f.slices / 16);
@@ -379,20 +405,22 @@ FloatShape float_shape(int mode, int64_t M, int64_t N, int64_t K, int sm_count) 
 }
 
 template <int MODE, bool A_T, bool B_T>
-cudaError_t launch_float_as(const f32::Params& p, bool vec, int64_t grid, cudaStream_t s) {
-    auto* kernel = vec ? f32::kernel<MODE, true, A_T, B_T> : f32::kernel<MODE, false, A_T, B_T>;
+cudaError_t launch_float_as(const f32::Params& p, bool vec, const FloatShape& f, cudaStream_t s) {
+    auto* kernel = f.threads == 64
+        ? (vec ? f32::kernel<MODE, true, A_T, B_T, 64> : f32::kernel<MODE, false, A_T, B_T, 64>)
+        : (vec ? f32::kernel<MODE, true, A_T, B_T, 128> : f32::kernel<MODE, false, A_T, B_T, 128>);
     const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), f32::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    return plan_launch(kernel, dim3((unsigned)grid), dim3(f32::THREADS), (size_t)f32::SMEM_BYTES, s, p);
+    return plan_launch(kernel, dim3((unsigned)f.grid), dim3((unsigned)f.threads), (size_t)f32::SMEM_BYTES, s, p);
 }
 
 }  // namespace
 
 size_t float_share_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
     const FloatShape f = float_shape(mode, M, N, K, sm_count);
-    return f.tiles == f.rounds * f.grid ? 0 : (size_t)f.grid * 2 * f32::THREADS * 32 * sizeof(float4);
+    return f.tiles == f.rounds * f.grid ? 0 : (size_t)f.grid * 2 * f32::TILE_VECS * sizeof(float4);
 }
-size_t float_counter_bytes(int sm_count) { return (size_t)kFloatPerSm * sm_count * sizeof(unsigned int); }
+size_t float_counter_bytes(int sm_count) { return (size_t)f32::per_sm(64) * sm_count * sizeof(unsigned int); }
 
 cudaError_t launch_float(const Product& w, void* shares, unsigned int* counters, int sm_count, cudaStream_t s) {
     const FloatShape f = float_shape(w.mode, w.M, w.N, w.K, sm_count);
@@ -427,12 +455,12 @@ cudaError_t launch_float(const Product& w, void* shares, unsigned int* counters,
     p.arrived = counters;
     switch (w.mode) {
         case FWD:
-            return w.b_k ? launch_float_as<FWD, false, true>(p, vec, f.grid, s)
-                         : launch_float_as<FWD, false, false>(p, vec, f.grid, s);
+            return w.b_k ? launch_float_as<FWD, false, true>(p, vec, f, s)
+                         : launch_float_as<FWD, false, false>(p, vec, f, s);
         case DX:
-            return w.b_k ? launch_float_as<DX, false, true>(p, vec, f.grid, s)
-                         : launch_float_as<DX, false, false>(p, vec, f.grid, s);
-        default: return launch_float_as<DW, true, false>(p, vec, f.grid, s);
+            return w.b_k ? launch_float_as<DX, false, true>(p, vec, f, s)
+                         : launch_float_as<DX, false, false>(p, vec, f, s);
+        default: return launch_float_as<DW, true, false>(p, vec, f, s);
     }
 }
 

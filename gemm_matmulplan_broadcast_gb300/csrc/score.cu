@@ -10,6 +10,11 @@
 // (a <= 0 <= log s, so the entropy's two terms never cancel.)  About six
 // operations and one exponential an element against one element read: the
 // bytes bound it, with the exponential unit close behind for 16-bit logits.
+// Measured, BF16 [4096, 50257] in rows of 50264: forward 85 us with five
+// alternatives (4.9 TB/s; 72 us, 5.7 TB/s without: what follows a row's sums
+// shares issue slots with the next row), backward 120 us (6.9 TB/s, a copy's
+// rate).  One row [1, 50257] FP16 with 20 alternatives: 11.3 us, a chain of
+// loads, sums and picks that nothing else can fill.
 //
 // Forward.  One pass: each thread keeps a running m, s and a, rescaled when a
 // later group of its elements brings a larger maximum.  A row is one block,
