@@ -174,9 +174,11 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
     return s;
 }
 
-// A thread's columns of a row shared by tpr threads: packs of V at (t + i tpr) V, or,
-// for rows of any alignment (V = 1), pairs of single elements tpr apart: two
-// elements an instruction either way.
+// A thread's columns of a row: packs of V at (base + i stride) V, or, for rows of
+// any alignment (V = 1), pairs of single elements `stride` apart: two elements
+// an instruction either way.  Single elements are addressed and tested one by
+// one only where the row ends: `full` tells that the i-th pair of every lane of
+// the warp lies inside the row.
 template <typename T, int V>
 struct Columns {
     static constexpr int PER = V == 1 ? 2 : V;      // columns of one i
@@ -184,33 +186,40 @@ struct Columns {
     struct Raw {
         T v[PER];
     };
-    static __device__ __forceinline__ int at(int t, int i, int q, int tpr) {
-        return V == 1 ? t + (2 * i + q) * tpr : (t + i * tpr) * V + q;
+    static __device__ __forceinline__ int at(int base, int i, int q, int stride) {
+        return V == 1 ? base + (2 * i + q) * stride : (base + i * stride) * V + q;
     }
-    static __device__ __forceinline__ Raw read(const T* row, int t, int i, int tpr, int cols, bool live) {
+    static __device__ __forceinline__ Raw read(const T* row, int base, int i, int stride, int cols, bool live, bool full) {
         Raw r{};
         if constexpr (V == 1) {
+            if (live && full) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                if (live && at(t, i, q, tpr) < cols) r.v[q] = row[at(t, i, q, tpr)];
+                for (int q = 0; q < 2; ++q) r.v[q] = row[at(base, i, q, stride)];
+            } else if (live) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (at(base, i, q, stride) < cols) r.v[q] = row[at(base, i, q, stride)];
+            }
         } else {
-            if (live && at(t, i, 0, tpr) < cols) {
-                const Pack<T, V> k = load<T, V>(row + at(t, i, 0, tpr));
+            if (live && at(base, i, 0, stride) < cols) {
+                const Pack<T, V> k = load<T, V>(row + at(base, i, 0, stride));
 #pragma unroll
                 for (int q = 0; q < V; ++q) r.v[q] = k.v[q];
             }
         }
         return r;
     }
-    static __device__ __forceinline__ bool in(int t, int i, int q, int tpr, int cols) { return at(t, i, q, tpr) < cols; }
-    static __device__ __forceinline__ void write(T* row, int t, int i, int tpr, int cols, const F2 (&o)[P]) {
+    static __device__ __forceinline__ bool in(int base, int i, int q, int stride, int cols) {
+        return at(base, i, q, stride) < cols;
+    }
+    static __device__ __forceinline__ void write(T* row, int base, int i, int stride, int cols, const F2 (&o)[P], bool full) {
         if constexpr (V == 1) {
             float lo, hi;
             unpack_f2(o[0], lo, hi);
-            if (in(t, i, 0, tpr, cols)) row[at(t, i, 0, tpr)] = Num<T>::from_acc(lo);
-            if (in(t, i, 1, tpr, cols)) row[at(t, i, 1, tpr)] = Num<T>::from_acc(hi);
-        } else if (in(t, i, 0, tpr, cols)) {
-            store<T, V>(row + at(t, i, 0, tpr), o);
+            if (full || in(base, i, 0, stride, cols)) row[at(base, i, 0, stride)] = Num<T>::from_acc(lo);
+            if (full || in(base, i, 1, stride, cols)) row[at(base, i, 1, stride)] = Num<T>::from_acc(hi);
+        } else if (in(base, i, 0, stride, cols)) {
+            store<T, V>(row + at(base, i, 0, stride), o);
         }
     }
     static __device__ __forceinline__ void pairs_of(F2 (&out)[P], const Raw& r) {
@@ -232,10 +241,12 @@ forward_kernel(const FwdParams p) {
     if (row >= p.rows) return;      // whole warps (W == 1); never with W > 1
     const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
     T* y = static_cast<T*>(p.Y) + row * p.y_pitch;
-    const int cols = (int)p.cols;
+    const int cols = (int)p.cols, whole = V == 1 && W > 1 ? cols / (2 * TPR) : 0;
     typename C::Raw k[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) k[i] = C::read(x, t, i, TPR, cols, true);
+    for (int i = 0; i < NV; ++i) {
+        k[i] = C::read(x, t, i, TPR, cols, true, i < whole);
+    }
     F2 s = 0, v[P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -250,9 +261,12 @@ forward_kernel(const FwdParams p) {
     for (int i = 0; i < NV; ++i) {
         C::pairs_of(v, k[i]);
         if constexpr (V == 1) {
-            float lo, hi;
-            unpack_f2(add2(v[0], minus_mean), lo, hi);
-            v[0] = pack_f2(C::in(t, i, 0, TPR, cols) ? lo : 0.f, C::in(t, i, 1, TPR, cols) ? hi : 0.f);
+            v[0] = add2(v[0], minus_mean);
+            if (i >= whole) {
+                float lo, hi;
+                unpack_f2(v[0], lo, hi);
+                v[0] = pack_f2(C::in(t, i, 0, TPR, cols) ? lo : 0.f, C::in(t, i, 1, TPR, cols) ? hi : 0.f);
+            }
             s = fma2(v[0], v[0], s);
         } else if (C::in(t, i, 0, TPR, cols)) {
 #pragma unroll
@@ -270,22 +284,22 @@ forward_kernel(const FwdParams p) {
     const F2 scale = both(rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (!C::in(t, i, 0, TPR, cols)) continue;
+        if (i >= whole && !C::in(t, i, 0, TPR, cols)) continue;
         F2 w[P];
         C::pairs_of(v, k[i]);
 #pragma unroll
         for (int q = 0; q < P; ++q) v[q] = mul2(add2(v[q], minus_mean), scale);
         if (p.gamma) {
-            C::pairs_of(w, C::read(static_cast<const T*>(p.gamma), t, i, TPR, cols, true));
+            C::pairs_of(w, C::read(static_cast<const T*>(p.gamma), t, i, TPR, cols, true, i < whole));
 #pragma unroll
             for (int q = 0; q < P; ++q) v[q] = mul2(v[q], w[q]);
         }
         if (p.beta) {
-            C::pairs_of(w, C::read(static_cast<const T*>(p.beta), t, i, TPR, cols, true));
+            C::pairs_of(w, C::read(static_cast<const T*>(p.beta), t, i, TPR, cols, true, i < whole));
 #pragma unroll
             for (int q = 0; q < P; ++q) v[q] = add2(v[q], w[q]);
         }
-        C::write(y, t, i, TPR, cols, v);
+        C::write(y, t, i, TPR, cols, v, i < whole);
     }
 }
 
@@ -460,11 +474,15 @@ __global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
     const int groups = blockDim.x / tpr, warps = tpr >> 5;
     const int grp = threadIdx.x / tpr, t = threadIdx.x - grp * tpr;
     const int cols = (int)p.cols;
+    // single elements: a warp's columns lie together, so that their offsets are constants
+    const int warp_base = (t >> 5) * (64 * NV);
+    const int base = V == 1 ? warp_base + (t & 31) : t, stride = V == 1 ? 32 : tpr;
+    const int whole = V == 1 ? (cols - warp_base) / 64 : 0;
     typename C::Raw kx[NV], kd[NV];
     F2 ag[NV][P], ab[NV][P], g[NV][P], xh[NV][P], dxh[NV][P];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (p.gamma) C::pairs_of(g[i], C::read(static_cast<const T*>(p.gamma), t, i, tpr, cols, true));
+        if (p.gamma) C::pairs_of(g[i], C::read(static_cast<const T*>(p.gamma), base, i, stride, cols, true, i < whole));
 #pragma unroll
         for (int q = 0; q < P; ++q) {
             if (!p.gamma) g[i][q] = both(1.f);
@@ -480,8 +498,8 @@ __global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
         const T* dy = static_cast<const T*>(p.dY) + row * p.dy_pitch;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            kx[i] = C::read(x, t, i, tpr, cols, live);
-            kd[i] = C::read(dy, t, i, tpr, cols, live);
+            kx[i] = C::read(x, base, i, stride, cols, live, i < whole);
+            kd[i] = C::read(dy, base, i, stride, cols, live, i < whole);
         }
         mean = live ? p.mean[row] : 0.f;
         rstd = live ? p.rstd[row] : 0.f;
@@ -489,7 +507,8 @@ __global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
     int64_t row = (int64_t)blockIdx.x * groups + grp;
     fetch(row);
     int buf = 0;
-    // every group runs the same number of turns (the block's barriers)
+    // every group runs the same number of turns: one barrier for the block (one a
+    // group: [2049, 1001] FLOAT 14.7 us, so 12.6)
     for (int64_t first = (int64_t)blockIdx.x * groups; first < p.rows; first += step, row += step, buf ^= 1) {
         const F2 scale = both(rstd), minus_mean = both(-mean);
         F2 c1 = 0, c2 = 0;
@@ -529,7 +548,7 @@ __global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
                 F2 o[P];
 #pragma unroll
                 for (int q = 0; q < P; ++q) o[q] = mul2(add2(fma2(xh[i][q], m2, dxh[i][q]), m1), scale);
-                C::write(dx, t, i, tpr, cols, o);
+                C::write(dx, base, i, stride, cols, o, i < whole);
             }
         }
     }
@@ -546,7 +565,7 @@ __global__ void __launch_bounds__(512) backward_kernel(const BwdParams p) {
                 unpack_f2(which ? ab[i][q] : ag[i][q], v[0], v[1]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    if (C::at(t, i, 2 * q + h, tpr) < cols) to[C::at(t, i, 2 * q + h, tpr)] = v[h];
+                    if (C::at(base, i, 2 * q + h, stride) < cols) to[C::at(base, i, 2 * q + h, stride)] = v[h];
             }
         if (groups == 1) continue;
         __syncthreads();
