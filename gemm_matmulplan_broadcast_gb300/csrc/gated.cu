@@ -26,6 +26,7 @@
 // the library product's burst rate) and 2.40 ms back to back (1605, under the
 // power limit); [8192, 4096] backward 2.26 and 2.50 ms.
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include "gated_internal.h"
@@ -660,6 +661,85 @@ __global__ void __launch_bounds__(256) slope_kernel(const T* dH, const T* G, con
     }
 }
 
+// Operands that the TMA cannot read in place (rows off 16-byte boundaries) into
+// rows of 16-byte groups, up to three in one launch.  A warp takes 32 groups of
+// a row at a time, several on their way at once.  Elements come in the widest
+// words that the row's address allows; a row two bytes off a word takes five
+// words a group and shifts them (the word at either end holds a neighbouring
+// element; where the tensor itself ends there, single elements are read).
+// Bytes bound it: two tensors [4095, 14335] about 100 us, 4.7 TB/s read and
+// written, [4096, 14334] (rows on words) 78 us, 6.0 TB/s.
+struct Copies {
+    struct One {
+        const unsigned short* src;
+        uint4* dst;
+        int64_t rows, cols, chunks;      // chunks of a row
+        int64_t first;                   // its first unit
+    } one[3];
+    int64_t units;
+};
+__device__ __forceinline__ uint4 group_of(const unsigned short* at, int64_t left, bool edge) {
+    const uint32_t low = (uint32_t)reinterpret_cast<uintptr_t>(at) & 15u;
+    if (left >= 8 && !(edge && (low & 3))) {
+        if (low == 0) return __ldg(reinterpret_cast<const uint4*>(at));
+        if ((low & 7) == 0) {
+            const uint2 a = __ldg(reinterpret_cast<const uint2*>(at)), b = __ldg(reinterpret_cast<const uint2*>(at) + 1);
+            return make_uint4(a.x, a.y, b.x, b.y);
+        }
+        uint32_t w[5];
+        const bool odd = low & 2;
+        const uint32_t* words = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t(3));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __ldg(words + j);
+        if (!odd) return make_uint4(w[0], w[1], w[2], w[3]);
+        w[4] = __ldg(words + 4);
+        return make_uint4(__byte_perm(w[0], w[1], 0x5432), __byte_perm(w[1], w[2], 0x5432),
+                          __byte_perm(w[2], w[3], 0x5432), __byte_perm(w[3], w[4], 0x5432));
+    }
+    uint32_t e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = j < left ? __ldg(at + j) : 0u;
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+__global__ void __launch_bounds__(256) copy_rows_kernel(const Copies c) {
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 31;
+    // consecutive units a warp: one division, then steps
+    const int64_t per = ceil_div(c.units, (int64_t)gridDim.x * 8);
+    int64_t u = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * per;
+    const int64_t end = min64(c.units, u + per);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        const Copies::One& o = c.one[n];
+        const int64_t last = min64(end, o.first + o.rows * o.chunks);
+        if (u >= last) continue;
+        int64_t row = (u - o.first) / o.chunks, chunk = (u - o.first) - row * o.chunks;
+        while (u < last) {
+            uint4 v[U];
+            uint4* to[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                to[i] = nullptr;
+                if (u >= last) continue;
+                const int64_t group = chunk * 32 + lane, left = o.cols - group * 8;
+                if (left > 0) {
+                    v[i] = group_of(o.src + row * o.cols + group * 8, left,
+                                    (row == 0 && group == 0) || (row == o.rows - 1 && left <= 8));
+                    to[i] = o.dst + row * ceil_div(o.cols, 8) + group;
+                }
+                ++u;
+                if (++chunk == o.chunks) {
+                    chunk = 0;
+                    ++row;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (to[i]) *to[i] = v[i];
+        }
+    }
+}
+
 // FLOAT: h = act(g) u; h may be u
 __global__ void __launch_bounds__(256) product_kernel(const float* G, const float* U, float* H, int64_t n, int act) {
     by_activation(act, [&](auto which) {
@@ -858,7 +938,7 @@ struct Pieces {
 };
 
 // An operand as the TMA reads it: in place, or a copy with rows padded to 16
-// bytes in the plan's memory (copied when `s` is given).
+// bytes in the plan's memory.
 struct Operand {
     const void* src;
     int64_t rows, cols;
@@ -871,10 +951,22 @@ struct Operand {
     gated::Stored stored() const {
         return copy ? gated::Stored{dst, rows, cols, gated::pad8(cols)} : gated::Stored{src, rows, cols, cols};
     }
-    cudaError_t fill(cudaStream_t s) const {
-        return copy ? launch_pad_rows16(src, dst, rows, cols, gated::pad8(cols), s) : cudaSuccess;
-    }
 };
+// the copies of those that need one
+cudaError_t fill(std::initializer_list<const Operand*> operands, int sm_count, cudaStream_t s) {
+    gated::Copies c;
+    std::memset(&c, 0, sizeof c);
+    int n = 0;
+    for (const Operand* o : operands) {
+        if (!o->copy || o->rows == 0 || o->cols == 0) continue;
+        c.one[n++] = gated::Copies::One{static_cast<const unsigned short*>(o->src), static_cast<uint4*>(o->dst),
+                                        o->rows, o->cols, ceil_div(o->cols, 256), c.units};
+        c.units += o->rows * ceil_div(o->cols, 256);
+    }
+    if (n == 0) return cudaSuccess;
+    return plan_launch(gated::copy_rows_kernel, dim3((unsigned)min64(ceil_div(c.units, 8), (int64_t)sm_count * 8)),
+                       dim3(256), 0, s, c);
+}
 
 olc_status forward16(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                      cudaStream_t s) {
@@ -898,8 +990,7 @@ olc_status forward16(olc_gated_plan* p, const void* X, const void* Wg, const voi
     }
     const bool uses = x.copy || wg.copy || wu.copy || partial;
     cudaError_t e = uses ? p->state.before_use(s) : cudaSuccess;
-    for (const Operand* o : {&x, &wg, &wu})
-        if (e == cudaSuccess) e = o->fill(s);
+    if (e == cudaSuccess) e = fill({&x, &wg, &wu}, p->state.sm_count, s);
     gated::Product w;
     std::memset(&w, 0, sizeof w);
     w.M = p->M;
@@ -956,8 +1047,7 @@ olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const vo
     const gated::Stored sg{dg, p->M, p->F, pitch}, su{du, p->M, p->F, pitch};
     gated::Product w;
     if (dX) {
-        if (e == cudaSuccess) e = wg.fill(s);
-        if (e == cudaSuccess) e = wu.fill(s);
+        if (e == cudaSuccess) e = fill({&wg, &wu}, sms, s);
         std::memset(&w, 0, sizeof w);
         w.M = p->M;
         w.N = p->D;
@@ -971,7 +1061,7 @@ olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const vo
         if (e == cudaSuccess) e = gated::launch_product<gated::DX>(p->dtype, w, part, sms, s);
     }
     if (dWg) {
-        if (e == cudaSuccess) e = x.fill(s);
+        if (e == cudaSuccess) e = fill({&x}, sms, s);
         std::memset(&w, 0, sizeof w);
         w.M = wm;
         w.N = wn;

@@ -292,3 +292,28 @@ def test_refusals():
         lib = plan.lib
         assert lib.olc_gated_forward(plan._h, x.data_ptr() + 2, w.data_ptr(), w.data_ptr(), h.data_ptr(), None, None, None) == 13
         assert lib.olc_gated_forward(plan._h, x.data_ptr(), None, w.data_ptr(), h.data_ptr(), None, None, None) == 1
+
+
+@pytest.mark.parametrize("offset", [0, 1, 2, 4, 7])
+@pytest.mark.parametrize("m,d,f", [(1, 1, 1), (3, 7, 9), (2, 513, 300), (70, 255, 257), (1, 2051, 10), (5, 12, 2052)])
+def test_operands_of_any_alignment_equal_aligned_ones(m, d, f, offset):
+    """The copies that bring rows to 16-byte boundaries keep every element: the
+    results are those of operands laid out with padded rows' worth of zeros."""
+    x, wg, wu = inputs(m, d, f, "bfloat16", False, 91)
+
+    def at_offset(t):
+        buf = torch.full((t.numel() + offset + 8,), float("nan"), dtype=t.dtype, device="cuda")
+        buf[offset:offset + t.numel()] = t.reshape(-1).cuda()
+        return buf[offset:offset + t.numel()].view(t.shape)
+
+    def padded(t, rows, cols):
+        out = torch.zeros(rows, cols, dtype=t.dtype)
+        out[:t.shape[0], :t.shape[1]] = t
+        return out.cuda()
+
+    d8, f8 = (d + 7) // 8 * 8, (f + 7) // 8 * 8
+    h, h8 = torch.empty(m, f, dtype=x.dtype, device="cuda"), torch.empty(m, f8, dtype=x.dtype, device="cuda")
+    with GatedPlan(m, d, f, "bfloat16") as plan, GatedPlan(m, d8, f8, "bfloat16") as plan8:
+        plan.forward(at_offset(x), at_offset(wg), at_offset(wu), h)
+        plan8.forward(padded(x, m, d8), padded(wg, d8, f8), padded(wu, d8, f8), h8)
+    assert torch.equal(h, h8[:, :f])
