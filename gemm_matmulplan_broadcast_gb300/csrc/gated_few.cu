@@ -51,7 +51,7 @@ struct Bars {
 struct Params {
     int64_t M, F;
     int64_t k_blocks;
-    int trans_w, is_bf16, act;
+    int trans_w, act;
     int quads;                // outputs stored four at a time (8-byte boundaries)
     int cluster;
     void *H, *G, *U;
@@ -310,7 +310,6 @@ cudaError_t launch_as(const Product& w, int sm_count, cudaStream_t s) {
     p.F = w.N;
     p.k_blocks = ceil_div(w.K, BK);
     p.trans_w = w.b_k;
-    p.is_bf16 = BF16;
     p.act = w.act;
     p.H = w.Y[0];
     p.G = w.Y[1];
