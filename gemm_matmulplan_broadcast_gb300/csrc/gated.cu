@@ -972,7 +972,7 @@ olc_status forward16(olc_gated_plan* p, const void* X, const void* Wg, const voi
                      cudaStream_t s) {
     const int64_t wr = p->trans_w ? p->F : p->D, wc = p->trans_w ? p->D : p->F;
     Operand x(X, p->M, p->D), wg(Wg, wr, wc), wu(Wu, wr, wc);
-    const bool few = p->M <= gated::kFewRows;
+    const bool few = gated::takes_few(p->M, p->F, p->state.sm_count);
     const size_t partial = few ? 0 : gated::product_partial_bytes(gated::FWD, p->M, p->F, p->D, p->state.sm_count);
     float* part = nullptr;
     for (int pass = 0; pass < 2; ++pass) {

@@ -79,8 +79,14 @@ struct Product {
     int act;
 };
 
-// few rows (w.M <= kFewRows), FWD operands: gated_few.cu
-constexpr int kFewRows = 64;
+// few rows, FWD operands: gated_few.cu.  Up to 32 rows, and up to 64 where the
+// single CTAs' 64-column tiles would take more than a round (BF16, us, few-row
+// kernel and tiles: 32 rows [1024] x [1024, 2816] 7.6 and 8.5, [4096] x [4096,
+// 14336] 40.0 and 47.3; 64 rows 10.1 and 8.4, 43.0 and 47.5; 64 rows [2048] x
+// [2048, 5632] 17.3 and 14.2).
+inline bool takes_few(int64_t M, int64_t F, int sm_count) {
+    return M <= 32 || (M <= 64 && ceil_div(F, 64) > sm_count);
+}
 cudaError_t launch_few(olc_dtype dt, const Product& w, int sm_count, cudaStream_t s);
 
 // FLOAT: gated_float.cu; operands of any alignment to their elements.

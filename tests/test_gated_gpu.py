@@ -317,3 +317,8 @@ def test_operands_of_any_alignment_equal_aligned_ones(m, d, f, offset):
         plan.forward(at_offset(x), at_offset(wg), at_offset(wu), h)
         plan8.forward(padded(x, m, d8), padded(wg, d8, f8), padded(wu, d8, f8), h8)
     assert torch.equal(h, h8[:, :f])
+
+
+@pytest.mark.parametrize("m,d,f,trans_w", [(33, 72, 9800, False), (64, 65, 9736, True), (32, 200, 131, False), (48, 40, 10000, True)])
+def test_forward_around_the_few_row_kernel(m, d, f, trans_w):
+    check_forward(m, d, f, "float16" if trans_w else "bfloat16", "silu", trans_w)
