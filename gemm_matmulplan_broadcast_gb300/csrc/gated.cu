@@ -1082,8 +1082,8 @@ olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const vo
 
 // FLOAT, few rows and weights [D, F]: the matrix plan's row kernels stream
 // each weight once, where a 64-row tile would multiply mostly nothing (us of
-// [rows, 1024] x [1024, 2816], device: 4 rows 15.8 against 32, 8 rows 31.7
-// against 32, 16 rows 90 against 32).
+// [rows, 1024] x [1024, 2816], device: 4 rows 15.8 against 30, 8 rows 31.7
+// against 30, 16 rows 90 against 30).
 constexpr int64_t kFewFloatRows = 4;
 olc_status forward32_few(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                          cudaStream_t s) {
@@ -1114,9 +1114,8 @@ olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const voi
                      cudaStream_t s) {
     if (p->M <= kFewFloatRows && !p->trans_w) return forward32_few(p, X, Wg, Wu, H, G, U, s);
     const int sms = p->state.sm_count;
-    const size_t shares = gated::float_share_bytes(gated::FWD, p->M, p->F, p->D, sms);
     olc_status st = float_counters(p);
-    if (st == OLC_OK) st = p->state.ensure(shares);
+    if (st == OLC_OK) st = p->state.ensure(gated::float_sum_bytes(gated::FWD, p->M, p->F, p->D, sms));
     if (st != OLC_OK) return st;
     gated::Product w;
     std::memset(&w, 0, sizeof w);
@@ -1133,10 +1132,10 @@ olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const voi
     w.Y[1] = G;
     w.Y[2] = U;
     w.act = p->act;
-    cudaError_t e = shares ? p->state.before_use(s) : cudaSuccess;
+    cudaError_t e = p->state.before_use(s);          // the counters, if nothing else
     if (e == cudaSuccess)
         e = gated::launch_float(w, p->state.memory, static_cast<unsigned int*>(p->counters), sms, s);
-    if (e == cudaSuccess && shares) e = p->state.after_use(s);
+    if (e == cudaSuccess) e = p->state.after_use(s);
     return plan_status(e);
 }
 
@@ -1145,12 +1144,12 @@ olc_status backward32(olc_gated_plan* p, const void* dH, const void* X, const vo
     const int sms = p->state.sm_count;
     const int64_t wr = p->trans_w ? p->F : p->D, wc = p->trans_w ? p->D : p->F;
     const int64_t pitch = (p->F + 3) / 4 * 4;      // of dg and du: rows on 16-byte boundaries
-    size_t shares = dX ? gated::float_share_bytes(gated::DX, p->M, p->D, p->F, sms) : 0;
-    const size_t more = dWg ? gated::float_share_bytes(gated::DW, wr, wc, p->M, sms) : 0;
-    if (more > shares) shares = more;
+    size_t sums = dX ? gated::float_sum_bytes(gated::DX, p->M, p->D, p->F, sms) : 0;
+    const size_t more = dWg ? gated::float_sum_bytes(gated::DW, wr, wc, p->M, sms) : 0;
+    if (more > sums) sums = more;
     const size_t half = gated::round256((size_t)(p->M * pitch) * sizeof(float));
     olc_status st = float_counters(p);
-    if (st == OLC_OK) st = p->state.ensure(2 * half + shares);
+    if (st == OLC_OK) st = p->state.ensure(2 * half + sums);
     if (st != OLC_OK) return st;
     unsigned char* memory = static_cast<unsigned char*>(p->state.memory);
     void *dg = memory, *du = memory + half, *part = memory + 2 * half;

@@ -8,11 +8,9 @@
 // of shared memory and the copies that make pairs of A's elements.  Slices of K,
 // 16 deep, come through asynchronous copies two ahead; an operand B stored with
 // its K contiguous is transposed through registers.  Measured at [1024, 1024] x
-// [1024, 2816]: 237 us, 50 TFLOP/s of the pipes' 79.5; the pipes are busy 68 % of
-// the active cycles, two warps on a scheduler (the accumulators' registers)
-// leaving the rest to dependent issues and the last round's unequal ends.
-// [2048, 2048] x [2048, 5632]: 1700 us, 55.6 TFLOP/s.  What the columns and the K
-// are:
+// [1024, 2816]: 221 us, 54 TFLOP/s of the pipes' 79.5; [2048, 2048] x [2048, 5632]:
+// 1566 us, 60 TFLOP/s.  Two warps on a scheduler (the accumulators' registers)
+// leave the rest to dependent issues, counters say.  What the columns and the K are:
 //
 //   FWD  64 columns of Wg next to the same 64 of Wu: a thread holds g and u of the
 //        same outputs and forms act(g) u from registers
@@ -20,11 +18,13 @@
 //   DW   x' dg and x' du as two outputs of one launch, x (or dg, du) read with its
 //        rows along K as it is
 //
-// Blocks are as many as reside.  Each takes as many whole tiles as there are
-// full rounds; the tiles of the last, partial round are cut along K into equal
-// shares, one a block, so that no SM idles through it ([1024, 1024] x [1024,
-// 2816]: 608 tiles whole and 96 in shares).  A tile's shares meet in the plan's
-// memory, and the block that brings the last one adds them in the order of K.
+// Blocks are as many as reside, and each takes the next piece of work when it is
+// done with one: first whole tiles, as many as there are full rounds, then the
+// other tiles cut along K into pieces, so that no SM idles and blocks that an SM's
+// schedulers favoured take more ([1024, 1024] x [1024, 2816]: 608 tiles whole, 96
+// in pieces; equal shares given out beforehand: 237 us).  A tile's pieces meet in
+// the plan's memory, and the block that brings the last one adds them in the order
+// of K: who computed which does not show.
 #include "gated_internal.h"
 #include "plan_state.h"
 
@@ -48,13 +48,16 @@ struct Params {
     float* y[3];              // FWD: h, g, u (null: not kept); DX: dX; DW: dWg, dWu
     int64_t M, N, K;          // rows and columns of an output, K of one operand pair
     int64_t tiles_m, tiles_item, tiles;
-    int64_t rounds;           // whole tiles a block
-    int64_t sharers;          // blocks that share the rest, at least four slices each
+    int64_t whole;            // tiles taken whole
+    int64_t works;            // and the pieces of the others
+    int pieces;               // of a tile
     int source_slices;        // slices of one operand pair
     int slices;               // of a tile (DX: both pairs')
     int act;
-    float4* shares;           // [2 blocks][TILE_VECS]: partial sums of a block's first and last shared tile
-    unsigned int* arrived;    // [shared tiles], zero between launches
+    float4* sums;             // [pieces of all cut tiles][TILE_VECS]
+    unsigned int* taken;      // pieces of work taken beyond the first of each block; zero between launches, like
+    unsigned int* left;       // blocks that have left
+    unsigned int* arrived;    // [cut tiles] pieces that are there
 };
 
 // the first four of n elements at `from`, zeros past the n-th; VEC: whole
@@ -108,22 +111,18 @@ template <int MODE, bool VEC, bool A_T, bool B_T, int THREADS>
 __global__ void __launch_bounds__(THREADS, per_sm(THREADS)) kernel(const Params p) {
     extern __shared__ __align__(16) float smem[];     // stages of A [64 rows][k] (A_T: [k][64 rows]), B [k][2 x 64]
     __shared__ int last;
+    __shared__ unsigned int turn;
     const int t = threadIdx.x;
     // A warp's lanes over its rows and columns.  SPREAD: lanes two apart read the
     // same columns and neighbours the same rows, which lets a 16-byte read of
     // shared memory serve half a warp at once (two wavefronts a read instead of
     // four); otherwise columns along the lanes, which stores faster.  us of
-    // [1024, 1024] x [1024, 2816], SPREAD and not: forward 240 and 236, with
-    // weights stored [F, D] 280 and 291, gradient 489 and 505.
+    // [1024, 1024] x [1024, 2816], SPREAD and not: forward 225 and 221, with
+    // weights stored [F, D] 266 and 278, gradient 492 and 544.
     constexpr bool SPREAD = MODE != FWD || B_T;
     constexpr int CG = 128 / THREADS;         // groups of 32 columns a thread has of each half
     const int tx = SPREAD ? (t & 1) | ((t >> 1) & 6) | (CG == 1 ? (t >> 2) & 8 : 0) : t % (16 / CG);
     const int ty = SPREAD ? ((t >> 1) & 1) | ((t >> 3) & 2) | (t / (THREADS / 2)) * 4 : t / (16 / CG);
-    const int64_t grid = gridDim.x, block = blockIdx.x;
-    // the shared tiles' slices, laid end to end
-    const int64_t whole = p.rounds * grid, steps = (p.tiles - whole) * p.slices, sharers = p.sharers;
-    const int64_t share0 = block < sharers ? block * steps / sharers : 0;
-    const int64_t share1 = block < sharers ? (block + 1) * steps / sharers : 0;
     constexpr int COLS = MODE == FWD ? TN : 2 * TN;
     int m0 = 0, n0 = 0, item = 0;
     const int M = (int)p.M, N = (int)p.N, K = (int)p.K;      // below 2^31
@@ -308,69 +307,75 @@ __global__ void __launch_bounds__(THREADS, per_sm(THREADS)) kernel(const Params 
             }
         }
     };
-    auto tile_at = [&](int64_t tile) {
-        item = MODE == DW ? (int)(tile / p.tiles_item) : 0;
-        const int64_t in = tile - item * p.tiles_item;
+    auto tile_at = [&](int tile) {
+        item = MODE == DW ? tile / (int)p.tiles_item : 0;
+        const int in = tile - item * (int)p.tiles_item;
         // rows fastest: the row tiles of a column read its operand B from L2
-        m0 = (int)(in % p.tiles_m) * TM;
-        n0 = (int)(in / p.tiles_m) * COLS;
+        m0 = in % (int)p.tiles_m * TM;
+        n0 = in / (int)p.tiles_m * COLS;
     };
 
-    for (int64_t r = 0; r < p.rounds; ++r) {
-        tile_at(block + r * grid);
-        multiply(0, p.slices);
-        finish();
-    }
-    for (int64_t s = share0; s < share1;) {
-        const int64_t tile = s / p.slices;
-        const int s0 = (int)(s % p.slices);
-        const int n = (int)min64(p.slices - s0, share1 - s);
-        s += n;
-        tile_at(whole + tile);
-        multiply(s0, n);
-        if (n == p.slices) {
-            finish();
-            continue;
+    const int whole = (int)p.whole, pieces = p.pieces;
+    for (int work = blockIdx.x; work < (int)p.works;) {
+        if (work < whole) {
+            tile_at(work);
+            multiply(0, p.slices);
+        } else {
+            const int cut = (work - whole) / pieces, piece = (work - whole) - cut * pieces;
+            const int s0 = (int)((int64_t)piece * p.slices / pieces), s1 = (int)((int64_t)(piece + 1) * p.slices / pieces);
+            tile_at(whole + cut);
+            multiply(s0, s1 - s0);
         }
-        // the blocks whose shares hold the tile's first and last slice
-        const int64_t u0 = tile * p.slices, u1 = u0 + p.slices - 1;
-        const int64_t c0 = ((u0 + 1) * sharers - 1) / steps, c1 = ((u1 + 1) * sharers - 1) / steps;
-        auto slot = [&](int64_t c) {          // where block c left this tile: its first shared tile, or its last
-            return p.shares + (2 * c + (c * steps / sharers / p.slices == tile ? 0 : 1)) * TILE_VECS + t;
-        };
-        float4* mine = slot(block);
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int j = 0; j < J; j += 2) {
-                float4 v;
-                unpack_f2(acc[r][j], v.x, v.y);
-                unpack_f2(acc[r][j + 1], v.z, v.w);
-                __stcg(mine + (r * (J / 2) + j / 2) * THREADS, v);
-            }
-        __threadfence();
-        __syncthreads();
-        if (t == 0) last = atomicAdd(p.arrived + tile, 1u) == (unsigned int)(c1 - c0);
-        __syncthreads();
-        if (!last) continue;
-        __threadfence();
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < J; ++j) acc[i][j] = 0;
-        for (int64_t c = c0; c <= c1; ++c) {
-            const float4* from = slot(c);
+        bool complete = work < whole || pieces == 1;
+        if (!complete) {
+            const int cut = (work - whole) / pieces, piece = (work - whole) - cut * pieces;
+            float4* const sums = p.sums + (int64_t)cut * pieces * TILE_VECS + t;
 #pragma unroll
             for (int r = 0; r < 8; ++r)
 #pragma unroll
                 for (int j = 0; j < J; j += 2) {
-                    const float4 v = __ldcg(from + (r * (J / 2) + j / 2) * THREADS);
-                    acc[r][j] = add2(acc[r][j], pack_f2(v.x, v.y));
-                    acc[r][j + 1] = add2(acc[r][j + 1], pack_f2(v.z, v.w));
+                    float4 v;
+                    unpack_f2(acc[r][j], v.x, v.y);
+                    unpack_f2(acc[r][j + 1], v.z, v.w);
+                    __stcg(sums + (int64_t)piece * TILE_VECS + (r * (J / 2) + j / 2) * THREADS, v);
                 }
+            __threadfence();
+            __syncthreads();
+            if (t == 0) last = atomicAdd(p.arrived + cut, 1u) == (unsigned int)(pieces - 1);
+            __syncthreads();
+            complete = last;
+            if (complete) {
+                __threadfence();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < J; ++j) acc[i][j] = 0;
+                for (int q = 0; q < pieces; ++q) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+#pragma unroll
+                        for (int j = 0; j < J; j += 2) {
+                            const float4 v = __ldcg(sums + (int64_t)q * TILE_VECS + (r * (J / 2) + j / 2) * THREADS);
+                            acc[r][j] = add2(acc[r][j], pack_f2(v.x, v.y));
+                            acc[r][j + 1] = add2(acc[r][j + 1], pack_f2(v.z, v.w));
+                        }
+                }
+                if (t == 0) p.arrived[cut] = 0u;
+            }
         }
-        finish();
-        if (t == 0) p.arrived[tile] = 0u;
+        if (complete) finish();
+        if (t == 0) turn = atomicAdd(p.taken, 1u);
+        __syncthreads();
+        work = (int)(gridDim.x + turn);
+        __syncthreads();             // read by all before it is written again
+    }
+    // the last block to leave finds every turn taken
+    if (t == 0) {
+        __threadfence();
+        if (atomicAdd(p.left, 1u) == gridDim.x - 1) {
+            *p.taken = 0u;
+            *p.left = 0u;
+        }
     }
 }
 
@@ -381,7 +386,8 @@ namespace {
 // How a product is cut; rows and columns of one output, K of one operand pair.
 struct FloatShape {
     int threads;
-    int64_t tiles_m, tiles_item, tiles, grid, rounds, sharers;
+    int64_t tiles_m, tiles_item, tiles, grid, whole, works;
+    int pieces;
     int source_slices, slices;
 };
 FloatShape float_shape(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
@@ -391,16 +397,26 @@ FloatShape float_shape(int mode, int64_t M, int64_t N, int64_t K, int sm_count) 
     f.tiles = f.tiles_item * (mode == DW ? 2 : 1);
     f.source_slices = (int)ceil_div(K, f32::KS);
     f.slices = f.source_slices * (mode == DX ? 2 : 1);
-    // less than a round of the blocks that multiply fastest: twice the warps on
-    // a tile, 8 x 8 accumulators a thread ([300, 1000] x [1000, 2730]: 91 us,
-    // with 64 threads 107; [16, 1024] x [1024, 2816]: 32 and 40; [2048, 2048] x
-    // [2048, 5632]: 1755 and 1700)
-    f.threads = f.tiles < (int64_t)f32::per_sm(64) * sm_count ? 128 : 64;
-    f.grid = max64(1, min64((int64_t)f32::per_sm(f.threads) * sm_count, f.tiles * max64(1, f.slices / 4)));
-    f.rounds = f.tiles / f.grid;
-    // no share is empty, and at most about 16 meet in a tile
-    const int64_t least = max64(4, f.slices / 16);
-    f.sharers = max64(1, min64(f.grid, (f.tiles - f.rounds * f.grid) * f.slices / least));
+    // less than half a round of the blocks that multiply fastest: twice the warps
+    // on a tile, 8 x 8 accumulators a thread ([300, 1000] x [1000, 2730]: 98 us,
+    // with 64 threads 118; [16, 1024] x [1024, 2816]: 30 and 35; the gradient of
+    // [2048, 2048] x [2048, 5632], 512 tiles: 3630 and 3510)
+    f.threads = 2 * f.tiles < (int64_t)f32::per_sm(64) * sm_count ? 128 : 64;
+    const int64_t resident = (int64_t)f32::per_sm(f.threads) * sm_count;
+    f.whole = f.tiles / resident * resident;
+    const int64_t cut = f.tiles - f.whole;
+    // Pieces of a tile, each at least four slices, at most 16: as many as cost
+    // least, which is rounds x a piece's slices and some three more for its fill
+    // and its sums ([1024, 1024] x [1024, 2816], 96 tiles cut: 6 pieces 221 us, 12
+    // 226, 16 223; [2048, 2048] x [2048, 5632], 384 tiles: 3 pieces 1566, whole
+    // 1643).
+    const int64_t most = min64(16, f.slices / 4);
+    f.pieces = 1;
+    auto cost = [&](int64_t n) { return ceil_div(cut * n, resident) * (ceil_div(f.slices, n) + 3); };
+    for (int n = 2; n <= (int)most; ++n)
+        if (cost(n) < cost(f.pieces)) f.pieces = n;
+    f.works = f.whole + cut * f.pieces;
+    f.grid = min64(resident, f.works);
     return f;
 }
 
@@ -416,13 +432,13 @@ cudaError_t launch_float_as(const f32::Params& p, bool vec, const FloatShape& f,
 
 }  // namespace
 
-size_t float_share_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
+size_t float_sum_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count) {
     const FloatShape f = float_shape(mode, M, N, K, sm_count);
-    return f.tiles == f.rounds * f.grid ? 0 : (size_t)f.grid * 2 * f32::TILE_VECS * sizeof(float4);
+    return f.pieces == 1 ? 0 : (size_t)(f.works - f.whole) * f32::TILE_VECS * sizeof(float4);
 }
-size_t float_counter_bytes(int sm_count) { return (size_t)f32::per_sm(64) * sm_count * sizeof(unsigned int); }
+size_t float_counter_bytes(int sm_count) { return ((size_t)f32::per_sm(64) * sm_count + 2) * sizeof(unsigned int); }
 
-cudaError_t launch_float(const Product& w, void* shares, unsigned int* counters, int sm_count, cudaStream_t s) {
+cudaError_t launch_float(const Product& w, void* sums, unsigned int* counters, int sm_count, cudaStream_t s) {
     const FloatShape f = float_shape(w.mode, w.M, w.N, w.K, sm_count);
     f32::Params p;
     // whole vectors: every row of every operand and result starts on a 16-byte
@@ -446,13 +462,16 @@ cudaError_t launch_float(const Product& w, void* shares, unsigned int* counters,
     p.tiles_m = f.tiles_m;
     p.tiles_item = f.tiles_item;
     p.tiles = f.tiles;
-    p.rounds = f.rounds;
-    p.sharers = f.sharers;
+    p.whole = f.whole;
+    p.works = f.works;
+    p.pieces = f.pieces;
     p.source_slices = f.source_slices;
     p.slices = f.slices;
     p.act = w.act;
-    p.shares = static_cast<float4*>(shares);
-    p.arrived = counters;
+    p.sums = static_cast<float4*>(sums);
+    p.taken = counters;
+    p.left = counters + 1;
+    p.arrived = counters + 2;
     switch (w.mode) {
         case FWD:
             return w.b_k ? launch_float_as<FWD, false, true>(p, vec, f, s)

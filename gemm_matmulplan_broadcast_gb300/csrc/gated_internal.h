@@ -90,11 +90,11 @@ inline bool takes_few(int64_t M, int64_t F, int sm_count) {
 cudaError_t launch_few(olc_dtype dt, const Product& w, int sm_count, cudaStream_t s);
 
 // FLOAT: gated_float.cu; operands of any alignment to their elements.
-// shares: float_share_bytes of device memory; counters: float_counter_bytes
+// sums: float_sum_bytes of device memory; counters: float_counter_bytes
 // of it, zero before the first call (and after every call).
-size_t float_share_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count);
+size_t float_sum_bytes(int mode, int64_t M, int64_t N, int64_t K, int sm_count);
 size_t float_counter_bytes(int sm_count);
-cudaError_t launch_float(const Product& w, void* shares, unsigned int* counters, int sm_count, cudaStream_t s);
+cudaError_t launch_float(const Product& w, void* sums, unsigned int* counters, int sm_count, cudaStream_t s);
 
 }  // namespace gated
 }  // namespace olc

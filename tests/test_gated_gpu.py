@@ -322,3 +322,18 @@ def test_operands_of_any_alignment_equal_aligned_ones(m, d, f, offset):
 @pytest.mark.parametrize("m,d,f,trans_w", [(33, 72, 9800, False), (64, 65, 9736, True), (32, 200, 131, False), (48, 40, 10000, True)])
 def test_forward_around_the_few_row_kernel(m, d, f, trans_w):
     check_forward(m, d, f, "float16" if trans_w else "bfloat16", "silu", trans_w)
+
+
+@pytest.mark.parametrize("m,d,f", [(70, 2000, 100), (1100, 300, 3000), (513, 1030, 515)])
+def test_float_results_do_not_depend_on_who_computes_which_piece(m, d, f):
+    x, wg, wu = (t.cuda() for t in inputs(m, d, f, "float32", False, 95))
+    g, u, dh = (normal((m, f), "float32", 96 + i).cuda() for i in range(3))
+    with GatedPlan(m, d, f, "float32") as plan:
+        seen = []
+        for _ in range(4):
+            o = [torch.empty_like(dh), torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)]
+            plan.forward(x, wg, wu, o[0])
+            plan.backward(dh, x, wg, wu, g, u, *o[1:])
+            seen.append(o)
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in seen[1:] for a, b in zip(o, seen[0]))
