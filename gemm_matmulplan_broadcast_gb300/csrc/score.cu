@@ -362,8 +362,11 @@ __device__ __forceinline__ unsigned long long key_index(uint32_t key, int i) {
 }
 __device__ __forceinline__ int index_of(unsigned long long c) { return (int)(0x7FFFFFFFu - (uint32_t)c); }
 
-// the consumers' barrier
-__device__ __forceinline__ void sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+// the consumers' barrier, by whole warps
+__device__ __forceinline__ void sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
 
 // The functions below run on one warp.
 
@@ -640,10 +643,13 @@ __device__ __forceinline__ void give_first(const void* local, uint32_t value) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(local)));
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(value) : "memory");
 }
+// (by whole warps: one lane's work may come before either)
 __device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -685,8 +691,7 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
             const int part = (int)(u % parts);       // = the block's rank in its cluster
             const Slice<T> slice = slice_of(static_cast<const T*>(p.logits) + row * p.pitch, p.vocab, part, parts);
             const Given given = parts == 1 ? given_of<T>(p, row) : Given{0, 0.f};
-            if (!tc::mbar_wait(&sh.row_full[buf], phase, abort_flag, p.err)) break;
-            __syncwarp();
+            if (!tc::warp_wait(&sh.row_full[buf], phase, abort_flag, p.err)) break;
             const Sums q = join_row(sh.row[buf]);
             if (p.top > 0) top_of_slice(slice, sh.row[buf], q.s == q.s, p.top, best);
             __syncwarp();
@@ -773,10 +778,10 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
         int left = a_slot, slot = 0;
         float slot_top = -INFINITY;
         // the buffer's last row has been finished
-        const bool ok = tc::mbar_wait(&sh.row_empty[buf], row_phase ^ 1, abort_flag, p.err);
+        const bool ok = tc::warp_wait(&sh.row_empty[buf], row_phase ^ 1, abort_flag, p.err);
         Row& r = sh.row[buf];
         for (int v = slice.v0; v < slice.v1 && ok; v += kChunk) {
-            if (tc::mbar_wait(&sh.full[stage], phase, abort_flag, p.err)) {
+            if (tc::warp_wait(&sh.full[stage], phase, abort_flag, p.err)) {
                 const uint4* chunk = reinterpret_cast<const uint4*>(ring + stage * (kChunk * 16)) + t;
                 const int mine = slice.v1 - v - t;   // this thread's packs: at 0, kThreads, ... below this
                 uint4 k[kUnroll];

@@ -73,6 +73,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// The wait of a warp that goes on to warp-wide instructions (.aligned barriers,
+// tcgen05.ld, ldmatrix): its lanes go on, or give up, together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned int* err) {
+    const bool ok = mbar_wait(bar, parity, abort_flag, err);
+    return __all_sync(0xffffffffu, ok);
+}
+
 // Bounded wait used while draining after an abort (no abort check).
 __device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity) {
     const uint64_t t0 = globaltimer();
