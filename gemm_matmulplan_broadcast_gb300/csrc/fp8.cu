@@ -235,6 +235,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile 
         }
     }
 }
+// the wait of a warp that goes on to warp-wide instructions: all lanes or none
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                          unsigned int* err) {
+    const bool ok = bar_wait(b, parity, abort_flag, err);
+    return __all_sync(0xffffffffu, ok);
+}
 __device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
     while (!bar_try(b, parity))
@@ -398,7 +404,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CU
         for (int64_t t = blockIdx.x; t < p.total_tiles; t += gridDim.x) {
             int64_t mb, nb;
             tile_of(p, t, mb, nb);
-            if (!bar_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err)) break;
+            if (!warp_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err)) break;
             fence_after();
             const int64_t row = mb * BM + row_in_tile;
             const bool row_ok = row < p.M;
@@ -436,6 +442,7 @@ tc_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CU
     }
 
     fence_before();
+    __syncwarp();            // one lane's work may come before the barriers
     __syncthreads();
     fence_after();
     if (warp == 1)
@@ -679,8 +686,8 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_consta
             int slice;
             unit_of(p, u, tile, slice, kb0, kb1);
             for (int64_t kb = kb0; kb < kb1 && !p.pre_t; ++kb) {
-                if (!bar_wait(&s->full[st], ph, abort_flag, p.err) ||
-                    !bar_wait(&s->bt_empty[tb], tph ^ 1, abort_flag, p.err)) {
+                if (!warp_wait(&s->full[st], ph, abort_flag, p.err) ||
+                    !warp_wait(&s->bt_empty[tb], tph ^ 1, abort_flag, p.err)) {
                     ok = false;
                     break;
                 }
@@ -714,7 +721,7 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_consta
             }
             if (!ok) break;
             // epilogue of the unit: TMEM lane = output column, column = row of A
-            if (!bar_wait(&s->acc_full[acc], acc_ph, abort_flag, p.err)) break;
+            if (!warp_wait(&s->acc_full[acc], acc_ph, abort_flag, p.err)) break;
             fence_after();
             uint32_t r[16];
             tmem_ld16(tmem_base + ((uint32_t)(lane_group * 32) << 16) + acc * MR, r);
@@ -775,6 +782,7 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_consta
     }
 
     fence_before();
+    __syncwarp();            // one lane's work may come before the barriers
     __syncthreads();
     fence_after();
     if (warp == 1)

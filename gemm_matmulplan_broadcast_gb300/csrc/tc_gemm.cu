@@ -468,6 +468,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if (warp == 1) tmem_alloc(&s->tmem_base, C::TMEM_COLS);
     if (warp >= 1) {
         tc_fence_before();
+        __syncwarp();
         asm volatile("bar.sync 2, %0;" ::"n"(THREADS - 32) : "memory");
         tc_fence_after();
         tmem_base = s->tmem_base;
@@ -622,7 +623,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
             tile_coords(p, tile, item, mb, nb);
             if (!SWAP && (!SPLIT || parts == 1) && mb * BM + row_in_tile < p.M)
                 prefetch_residual(p, item, mb * BM + row_in_tile, nb * BN, min64(BN, p.N - nb * BN));
-            if (!mbar_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err)) break;
+            if (!warp_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err)) break;
             tc_fence_after();
             const int64_t row = mb * BM + row_in_tile;
             const int64_t rows_total = SWAP ? p.N : p.M;    // extent of the TMEM-lane dimension
@@ -777,6 +778,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
 
     tc_fence_before();
+    __syncwarp();            // one lane's work may come before the barriers
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
@@ -1031,7 +1033,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if (!F8 && mb * 256 + rank * 128 + row_in_tile < p.M)
                 prefetch_residual(p, item, mb * 256 + rank * 128 + row_in_tile, cbase,
                                   min64(width, p.N - cbase));
-            if (!mbar_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err)) break;
+            if (!warp_wait(&s->acc_full[acc], acc_phase, abort_flag, p.err)) break;
             tc_fence_after();
             const int64_t row = mb * 256 + rank * 128 + row_in_tile;
             const bool row_ok = row < p.M;
@@ -1164,6 +1166,7 @@ tc_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
 
     tc_fence_before();
+    __syncwarp();            // one lane's work may come before the barriers
     __syncthreads();
     cluster_sync();          // no remote arrival may target a CTA that has left
     tc_fence_after();
@@ -1243,9 +1246,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 __device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
@@ -1345,7 +1350,7 @@ splitk_tiny_kernel(const __grid_constant__ CUtensorMap tmap_a,
         for (int c = 0; c < nchunks; ++c) {
             const int st = c % STAGES;
             const uint32_t ph = (uint32_t)(c / STAGES) & 1u;
-            if (!mbar_wait(&s->full[st], ph, abort_flag, p.err)) break;
+            if (!warp_wait(&s->full[st], ph, abort_flag, p.err)) break;
             const uint32_t a_base = smem_u32(base + st * CHUNK);
             const uint32_t b_base = a_base + A_CHUNK;
             uint32_t a[2][4], b[2][4];
@@ -1595,7 +1600,7 @@ csplit_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
         // the rows past M are never read back)
         const int lane_group = warp & 3;
         const int row_in_tile = lane_group * 32 + lane;
-        if (mbar_wait(&s->acc_full, 0, abort_flag, p.err)) {
+        if (warp_wait(&s->acc_full, 0, abort_flag, p.err)) {
             tc_fence_after();
             const uint32_t t_base = tmem_base + ((uint32_t)(lane_group * 32) << 16);
             float4* prow = reinterpret_cast<float4*>(part + row_in_tile * PART_PITCH);
@@ -1611,6 +1616,7 @@ csplit_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
         }
     }
     tc_fence_before();
+    __syncwarp();            // one lane's work may come before the barriers
     __syncthreads();
     // the valid rows of the partial tile to the plan's workspace (rows of
     // 256 floats; consecutive threads write consecutive 16-byte groups)

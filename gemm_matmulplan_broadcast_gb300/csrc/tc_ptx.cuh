@@ -172,6 +172,7 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 
 // the four epilogue warps only (named barrier 1)
 __device__ __forceinline__ void epi_sync() {
+    __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
 }
 
@@ -223,6 +224,7 @@ __device__ __forceinline__ uint32_t cluster_count() {
     return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();            // one lane's work may come before it
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -46,3 +46,19 @@ def test_score_roles_leave_their_waits_together():
     # the loading warp's one lane waits for `empty`; every other wait is a whole warp's
     text = "\n".join(source("score.cu"))
     assert re.findall(r"mbar_wait\(&sh\.(\w+)", text) == ["empty"]
+
+
+@pytest.mark.parametrize("name", ["tc_ptx.cuh", "tc_gemm.cu", "fp8.cu"])
+def test_barriers_of_the_matrix_tiles_are_met_by_whole_warps(name):
+    assert apart(name) == []
+
+
+@pytest.mark.parametrize("name", ["tc_gemm.cu", "fp8.cu"])
+def test_matrix_tiles_leave_their_waits_together(name):
+    # an accumulator is read by whole warps (tcgen05.ld): its wait is a vote
+    assert not re.search(r"\b(mbar_wait|bar_wait)\(&s->acc_full", "\n".join(source(name)))
+    # the roles of one lane meet the last barriers with the rest of their warp
+    text = "\n".join(source(name))
+    ends = re.findall(r"fence_before\(\);\n(.*)\n    __syncthreads\(\);\n    (?!tc_fence_after\(\);\n    const|fence_after\(\);\n    const)",
+                      text)
+    assert ends and all("__syncwarp();" in e for e in ends)
