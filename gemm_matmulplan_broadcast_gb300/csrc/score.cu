@@ -111,6 +111,17 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
+// For probabilities that are results themselves: FLOAT keeps those below 2^-126
+// (log p, some -90 there, lifts their gradient back into the normal range);
+// 16-bit gradients let them go, and the instructions with them.
+template <typename T>
+__device__ __forceinline__ float probability(float x) {
+    if constexpr (sizeof(T) < 4) return exp2_fast(x);
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // A running softmax over some elements of a row, in units of log 2: with
 // R = m log2(e) (rounded; 0 while m is -inf), s = sum 2^(z log2(e) - R) and
 // a = sum (z log2(e) - R) 2^(z log2(e) - R).  The rounding of R cancels:
@@ -884,7 +895,7 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     const float shift = -lse * kLog2e, c = fmaf(dh, h - lse, dlp);
     auto grad = [&](float v, int i) -> float {           // any values
         if (nothing) return 0.f;
-        const float logp = v - lse, q = exp2_fast(logp * kLog2e);
+        const float logp = v - lse, q = probability<T>(logp * kLog2e);
         // a probability of zero contributes nothing, whatever its logarithm
         float g = q == 0.f && dlp == dlp ? 0.f : -q * fmaf(dh, logp + h, dlp);
         if (i == token) g += dlp;
@@ -911,7 +922,7 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
                 const F2 x = pair_of<T>(w, j);
                 float lo, hi;
                 unpack_f2(fma2(x, scale2, shift2), lo, hi);
-                g[j] = mul2(pack_f2(exp2_fast(lo), exp2_fast(hi)), fma2(x, dh2, c2));
+                g[j] = mul2(pack_f2(probability<T>(lo), probability<T>(hi)), fma2(x, dh2, c2));
             }
             if ((unsigned)(token - at) < (unsigned)V) {
 #pragma unroll
