@@ -122,25 +122,32 @@ __device__ __forceinline__ float probability(float x) {
     return r;
 }
 
-// A running softmax over some elements of a row, in units of log 2: with
-// R = m log2(e) (rounded; 0 while m is -inf), s = sum 2^(z log2(e) - R) and
-// a = sum (z log2(e) - R) 2^(z log2(e) - R).  The rounding of R cancels:
-// every result takes R, s and a together.  Maxima whose R could overflow are
-// subtracted before the scaling instead.
+// A running softmax over some elements of a row, in units of log 2: with a
+// distance d_j from the largest element m, s = sum 2^d_j and a = sum d_j 2^d_j.
+// Near zero, where most logits are, d_j = z_j log2(e) - R with the rounded
+// R = m log2(e): one fused operation an element.  All distances then have R's
+// rounding, residue(m), too much, at most 2^-8 there.  Farther out (logits or
+// finite masks of any size; R's rounding would grow with them) m is subtracted
+// first, which is exact for elements close to it: d_j = (z_j - m) log2(e).
 struct Sums {
     float m, s, a;
 };
-__device__ __forceinline__ bool extreme(float m) { return fabsf(m) >= 1.0e38f && m != -INFINITY; }
-__device__ __forceinline__ float scaled_max(float m) { return m == -INFINITY ? 0.f : m * kLog2e; }
-// z log2(e) - R, not below kFar
+constexpr float kNear = 49152.f;        // and kNear - kFar is a value that FLOAT16 holds
+__device__ __forceinline__ bool near_zero(float m) { return fabsf(m) < kNear; }
+__device__ __forceinline__ float residue(float m) {
+    return near_zero(m) ? fmaf(m, kLog2e, -__fmul_rn(m, kLog2e)) : 0.f;
+}
+// what elements are taken from: -inf, the maximum of nothing, keeps them as they are
+__device__ __forceinline__ float origin(float m) { return m == -INFINITY ? 0.f : m; }
+// an element's distance, not below kFar
 __device__ __forceinline__ float distance(float z, float m) {
-    return max_nan(extreme(m) ? (z - m) * kLog2e : fmaf(z, kLog2e, -scaled_max(m)), kFar);
+    return max_nan(near_zero(m) ? fmaf(z, kLog2e, -__fmul_rn(m, kLog2e)) : (z - origin(m)) * kLog2e, kFar);
 }
 
 // the same sums around another maximum (m >= q.m)
 __device__ __forceinline__ void move_to(Sums& q, float m) {
     if (q.m != -INFINITY) {          // else nothing but zeros, or a NaN to keep
-        const float d = max_nan(extreme(q.m) || extreme(m) ? (q.m - m) * kLog2e : scaled_max(q.m) - scaled_max(m), kFar);
+        const float d = max_nan(fmaf(q.m - m, kLog2e, residue(m) - residue(q.m)), kFar);
         const float c = exp2_fast(d);
         q.a = c * fmaf(d, q.s, q.a);
         q.s *= c;
@@ -200,16 +207,12 @@ __device__ __forceinline__ F2 pair_of(const uint32_t (&w)[4], int i) {
         return pack_f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
 }
-// A row's values that lie kFar below `top` weigh nothing and are raised to
-// that floor, so that no infinity meets a zero; for a `top` in this range the
-// floor is a finite value of the type and nothing overflows.
-template <typename T>
-__device__ __forceinline__ bool has_floor(float top) {
-    return top > (std::is_same_v<T, __half> ? -5.0e4f : -1.0e38f) && top < 1.0e38f;      // not for NaN
-}
+// A row's values that lie kFar below a `top` near zero weigh nothing and are
+// raised to that floor, so that no infinity meets a zero: a value of every
+// type, rounded by 128 at most.
 template <typename T>
 __device__ __forceinline__ uint32_t floor_of(float top) {
-    return splat<T>(std::is_same_v<T, __half> ? fmaxf(top + kFar, -65504.f) : top + kFar);
+    return splat<T>(top + kFar);
 }
 
 template <typename T>
@@ -295,36 +298,43 @@ __device__ __forceinline__ float take(Sums& q, const uint4 (&k)[N]) {
         top = max_word<T>(top, max_word<T>(max_word<T>(k[i].x, k[i].y), max_word<T>(k[i].z, k[i].w)));
     const float m = word_max<T>(top);
     if (m > q.m) move_to(q, m);
-    if (!has_floor<T>(q.m)) {
-        // no maximum yet, or one near the type's lowest value
-#pragma unroll 1
-        for (int i = 0; i < N; ++i) {
-            uint4 w = k[0];
-#pragma unroll
-            for (int j = 1; j < N; ++j) w = i == j ? k[j] : w;
-            float z[Slice<T>::V];
-            unpack<T>(w, z);
-#pragma unroll
-            for (int j = 0; j < Slice<T>::V; ++j) take(q, z[j]);
-        }
-        return m;
-    }
-    const uint32_t low = floor_of<T>(q.m);
-    const float r = -q.m * kLog2e;
-    const F2 scale = pack_f2(kLog2e, kLog2e), shift = pack_f2(r, r);
+    const F2 scale = pack_f2(kLog2e, kLog2e);
     F2 s = pack_f2(0.f, 0.f), a = s;
+    if (near_zero(q.m)) {
+        const uint32_t low = floor_of<T>(q.m);
+        const float r = -__fmul_rn(q.m, kLog2e);
+        const F2 shift = pack_f2(r, r);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint32_t w[4] = {floor_word<T>(k[i].x, low), floor_word<T>(k[i].y, low), floor_word<T>(k[i].z, low),
-                               floor_word<T>(k[i].w, low)};
+        for (int i = 0; i < N; ++i) {
+            const uint32_t w[4] = {floor_word<T>(k[i].x, low), floor_word<T>(k[i].y, low), floor_word<T>(k[i].z, low),
+                                   floor_word<T>(k[i].w, low)};
 #pragma unroll
-        for (int j = 0; j < (int)(8 / sizeof(T)); ++j) {
-            const F2 d = fma2(pair_of<T>(w, j), scale, shift);
-            float lo, hi;
-            unpack_f2(d, lo, hi);
-            const F2 e = pack_f2(exp2_fast(lo), exp2_fast(hi));
-            s = add2(s, e);
-            a = fma2(d, e, a);
+            for (int j = 0; j < (int)(8 / sizeof(T)); ++j) {
+                const F2 d = fma2(pair_of<T>(w, j), scale, shift);
+                float lo, hi;
+                unpack_f2(d, lo, hi);
+                const F2 e = pack_f2(exp2_fast(lo), exp2_fast(hi));
+                s = add2(s, e);
+                a = fma2(d, e, a);
+            }
+        }
+    } else {
+        // masks alone so far, or logits far from zero
+        const float r = -origin(q.m);
+        const F2 shift = pack_f2(r, r);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t w[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
+#pragma unroll
+            for (int j = 0; j < (int)(8 / sizeof(T)); ++j) {
+                float lo, hi;
+                unpack_f2(mul2(add2(pair_of<T>(w, j), shift), scale), lo, hi);
+                lo = max_nan(lo, kFar);
+                hi = max_nan(hi, kFar);
+                const F2 e = pack_f2(exp2_fast(lo), exp2_fast(hi));
+                s = add2(s, e);
+                a = fma2(pack_f2(lo, hi), e, a);
+            }
         }
     }
     float lo, hi;
@@ -631,7 +641,7 @@ __device__ __forceinline__ void write_row(const Params& p, int64_t row, const Gi
                                           int t) {
     const bool nothing = q.m == -INFINITY && q.s == 0.f;         // every logit is -inf
     const float log_s = log2f(q.s);
-    const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, extreme(q.m) ? q.m : scaled_max(q.m) * kLn2);
+    const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, near_zero(q.m) ? q.m * kLog2e * kLn2 : q.m);
     if (t < p.top) {
         const float v = key_value(sh.best_key[t]);
         if (p.top_logprob) p.top_logprob[row * p.top + t] = nothing ? -INFINITY : v - lse;
@@ -903,7 +913,7 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     };
     if (t < s.head) d[t] = Num<T>::from_acc(grad(Num<T>::to_acc(z[t]), t));
     const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-    const bool quick = has_floor<T>(lse) && same;
+    const bool quick = near_zero(lse) && same;
     const uint32_t low = floor_of<T>(quick ? lse : 0.f);
     const F2 scale2 = pack_f2(kLog2e, kLog2e), shift2 = pack_f2(shift, shift), c2 = pack_f2(-c, -c),
              dh2 = pack_f2(-dh, -dh);

@@ -1,11 +1,13 @@
 """Log probabilities of tokens over the whole range of their logits and
-probabilities.  References and tolerances are those of the tests beside this
-one."""
+probabilities: finite masks of -1e9 and the like, rows of nothing else, logits
+around large values.  References and tolerances are those of the tests beside
+this one."""
 
 import pytest
 import torch
 
-from test_token_log_probs_gpu import check_backward
+from layers_ref import DTYPES, TORCH, normal
+from test_token_log_probs_gpu import check_backward, check_forward, tokens_of
 
 pytestmark = pytest.mark.gpu
 
@@ -15,3 +17,70 @@ def test_backward_keeps_the_smallest_probabilities():
     z = torch.linspace(0.0, -110.0, 4000).expand(3, 4000).contiguous()
     check_backward(3, 4000, "float32", z=z)
     check_backward(3, 4000, "float32", z=z, offset=1, d_offset=2)
+
+
+INF = float("inf")
+#: finite masks and offsets; FLOAT16 reaches 65504
+FAR = {"float32": [1e5, 1e9, 1e10, 1e12, 1e30, 1e37], "bfloat16": [1e5, 1e9, 1e10, 1e12, 1e30, 1e37],
+       "float16": [1e4, 3e4, 49000.0, 5e4, 6e4]}
+
+
+def far_rows(vocab, dtype, v, seed):
+    t = TORCH[dtype]
+    z = normal((14, vocab), dtype, seed, 3.0)
+    z[0] = -v                                            # nothing but the mask
+    z[1, :vocab // 2] = -v                               # whole slices of it
+    few = z[2, [1, vocab // 3, vocab - 2]].clone()
+    z[2] = -v                                            # three tokens left
+    z[2, [1, vocab // 3, vocab - 2]] = few
+    z[3, ::2] = -v
+    z[4] = -v                                            # masks of both kinds and nothing else
+    z[4, ::3] = -INF
+    z[5, vocab // 2:] = -v                               # and beside what is left
+    z[5, :vocab // 4] = -INF
+    z[6, 3 * vocab // 4:] = -v
+    z[7, vocab // 2] = v                                 # one token far above
+    z[8, vocab // 2] = v                                 # the same, the rest masked
+    z[8, :vocab // 2] = -INF
+    z[8, vocab // 2 + 1:] = -v
+    # neighbours of +-v in the type
+    scale = float(torch.tensor(v, dtype=t)) * torch.finfo(t).eps
+    z[9] = (normal((vocab,), "float32", seed + 1, 3.0).double() * min(scale, 1e300) + v).clamp(-float(torch.finfo(t).max), float(torch.finfo(t).max)).to(t)
+    z[10] = -z[9]
+    z[11] = -v
+    z[11, vocab - 1] = float(torch.tensor(-v, dtype=t)) * (1 + 8 * torch.finfo(t).eps)
+    # a ramp through the values where the sums change their unit
+    ramp = torch.linspace(49000.0, 49300.0, vocab)
+    z[12], z[13] = ramp.to(t), (-ramp).to(t)
+    return z
+
+
+@pytest.mark.parametrize("vocab", [600, 30000, 120000])
+@pytest.mark.parametrize("dtype,v", [(d, v) for d in DTYPES for v in FAR[d]])
+def test_finite_masks_and_far_logits(dtype, v, vocab):
+    z = far_rows(vocab, dtype, v, 61)
+    tokens = tokens_of(14, vocab, 62)
+    tokens[2], tokens[5], tokens[8] = 1, vocab - 1, vocab // 2
+    check_forward(z, tokens, dtype, 20)
+    check_forward(z, tokens, dtype, 0, pitch=vocab + 3, offset=1)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("vocab", [700, 40000])
+def test_maxima_that_move_far_within_a_row(vocab, dtype):
+    # ascending and descending steps over many magnitudes, so that running maxima pass every unit
+    z = torch.empty(4, vocab)
+    steps = torch.tensor([-1e30, -1e10, -2e5, -49153.0, -49151.0, -40.0, 0.0, 40.0, 49151.0, 49153.0, 2e5, 1e10, 1e30])
+    z[0] = steps[torch.arange(vocab) * 13 // vocab]
+    z[1] = z[0].flip(0)
+    z[2] = steps[:6][torch.arange(vocab) * 6 // vocab] + normal((vocab,), "float32", 63)
+    z[3] = z[2].flip(0)
+    z = z.to(TORCH[dtype])
+    check_forward(z, tokens_of(4, vocab, 64), dtype, 5)
+
+
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("dtype,v", [(d, v) for d in DTYPES for v in FAR[d]])
+def test_backward_of_finite_masks_and_far_logits(dtype, v, same):
+    for vocab, kw in ((4000, {}), (4001, {"pitch": 4009, "offset": 3})):
+        check_backward(14, vocab, dtype, z=far_rows(vocab, dtype, v, 65), same=same, **kw)
