@@ -3,7 +3,7 @@
 // gradient.
 //
 //   m = max_j z_j,  s = sum_j e^(z_j - m),  a = sum_j (z_j - m) e^(z_j - m)
-//   lse = m + log s,  logprob = z_token - lse,  H = log s - a / s
+//   lse = m + log s,  logprob = (z_token - m) - log s,  H = log s - a / s
 //   (the sums in units of log 2, which is what the exponential unit takes)
 //   dz_j = dlogprob (1[j = token] - p_j) - dH p_j (log p_j + H)
 //
@@ -640,21 +640,24 @@ __device__ __forceinline__ Given given_of(const Params& p, int64_t row) {
 __device__ __forceinline__ void write_row(const Params& p, int64_t row, const Given& g, const Sums& q, const Best& sh,
                                           int t) {
     const bool nothing = q.m == -INFINITY && q.s == 0.f;         // every logit is -inf
-    const float log_s = log2f(q.s);
-    const float lse = nothing ? -INFINITY : fmaf(log_s, kLn2, near_zero(q.m) ? q.m * kLog2e * kLn2 : q.m);
+    const float log2_s = log2f(q.s);
+    // log s with the distances' common residue taken out again: lse and the log
+    // probabilities start from m itself, not from m scaled there and back
+    const float log_s = (log2_s - residue(q.m)) * kLn2;
+    const float lse = nothing ? -INFINITY : q.m + log_s;
     if (t < p.top) {
         const float v = key_value(sh.best_key[t]);
-        if (p.top_logprob) p.top_logprob[row * p.top + t] = nothing ? -INFINITY : v - lse;
+        if (p.top_logprob) p.top_logprob[row * p.top + t] = nothing ? -INFINITY : (v - q.m) - log_s;
         if (p.top_index) p.top_index[row * p.top + t] = sh.best_index[t];
     }
     if (t == 0) {
         float lp;
         if (g.token < 0) lp = 0.f;                               // ignored
         else if (g.token >= p.vocab) lp = __uint_as_float(0x7FC00000u);
-        else lp = nothing ? -INFINITY : g.logit - lse;
+        else lp = nothing ? -INFINITY : (g.logit - q.m) - log_s;
         p.logprob[row] = lp;
         if (p.lse) p.lse[row] = lse;
-        if (p.entropy) p.entropy[row] = nothing ? 0.f : (log_s - q.a / q.s) * kLn2;
+        if (p.entropy) p.entropy[row] = nothing ? 0.f : (log2_s - q.a / q.s) * kLn2;
     }
 }
 

@@ -1,13 +1,14 @@
 """Log probabilities of tokens over the whole range of their logits and
 probabilities: finite masks of -1e9 and the like, rows of nothing else, logits
-around large values.  References and tolerances are those of the tests beside
-this one."""
+around large values, one token that holds everything, rows with an offset.
+References and tolerances are those of the tests beside this one."""
 
 import pytest
 import torch
 
-from layers_ref import DTYPES, TORCH, normal
-from test_token_log_probs_gpu import check_backward, check_forward, tokens_of
+from gemm_matmulplan_broadcast_gb300 import TokenLogProbsPlan
+from layers_ref import DTYPES, F32, TORCH, assert_near, normal
+from test_token_log_probs_gpu import check_backward, check_forward, reference, rel_of, run_forward, tokens_of
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,44 @@ def test_maxima_that_move_far_within_a_row(vocab, dtype):
 def test_backward_of_finite_masks_and_far_logits(dtype, v, same):
     for vocab, kw in ((4000, {}), (4001, {"pitch": 4009, "offset": 3})):
         check_backward(14, vocab, dtype, z=far_rows(vocab, dtype, v, 65), same=same, **kw)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [300, 50257])
+def test_a_single_token_left_has_all_of_the_probability(vocab, dtype):
+    """logprob is log 1, and lse that token's logit: off by the sum's own
+    error (one exponential of 1: 2^-21) and lse's one rounding, not by
+    roundings of the logit's size."""
+    rows = 200
+    value = normal((rows,), dtype, 71, 300.0)
+    tokens = tokens_of(rows, vocab, 72)
+    for mask in (-INF, -30000.0):
+        z = torch.full((rows, vocab), mask).to(TORCH[dtype])
+        z[torch.arange(rows), tokens] = value
+        logprob, entropy, lse, best, index = run_forward(z, tokens, dtype, 1)
+        assert float(logprob.abs().max()) <= 2.0 ** -21
+        assert float(best.abs().max()) <= 2.0 ** -21 and torch.equal(index[:, 0].cpu(), tokens)
+        assert_near(lse, value.double(), 2.0 ** -21 + F32 * value.double().abs(), "lse")
+        assert float(entropy.abs().max()) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shift", [-900.0, 1500.0, 30000.0])
+@pytest.mark.parametrize("rows,vocab", [(5, 700), (2, 60000), (400, 1003)])
+def test_log_probabilities_do_not_depend_on_an_offset(rows, vocab, shift, dtype):
+    """logprob = (z - m) - log s takes no rounding of lse's size: off by the
+    sum's error and roundings of its own size alone."""
+    z = normal((rows, vocab), dtype, 73, 3.0, shift)
+    tokens = tokens_of(rows, vocab, 74)
+    got = run_forward(z, tokens, dtype, 7)
+    logprob, entropy, lse, best, order = reference(z, tokens, 7)
+    rel = rel_of(vocab)
+    assert_near(got[0], logprob, rel + 4 * F32 * logprob.abs(), "logprob")
+    assert_near(got[3], best, rel + 4 * F32 * best.abs(), "alternatives' log probabilities")
+    assert_near(got[2], lse, rel + F32 * lse.abs(), "lse")
+    assert torch.equal(got[4].cpu(), order)
+    d = torch.empty(rows, vocab, dtype=TORCH[dtype], device="cuda")
+    one = torch.ones(rows, device="cuda")
+    with TokenLogProbsPlan(rows, vocab, dtype) as plan:         # a gradient's entries add up to nothing
+        plan.backward(z.cuda(), tokens.cuda(), lse.float().cuda(), None, one, d)
+    assert float(d.double().sum(-1).abs().max()) <= 2.0 ** -7 * 2 + 4 * F32 * abs(shift) * 2
