@@ -10,7 +10,8 @@
 // About ten operations an element against two or three elements moved: the
 // bytes bound it.  Each row is read once and stays in registers, so that the
 // variance is the sum of squared distances from the finished mean (no
-// cancellation for rows far from zero); rows too long for the registers are
+// cancellation for rows far from zero, whose mean is corrected by the sum of the
+// distances as well); rows too long for the registers are
 // read again, mostly from L2.  All sums and statistics are float32; y, dx,
 // dgamma and dbeta are rounded to the element type once.  Measured, BF16 [16384,
 // 4096]: forward 43.7 us (6.1 TB/s, a plain copy of the tensor 41 to 43.5),
@@ -34,7 +35,7 @@ struct FwdParams {
     int64_t x_pitch, y_pitch;
     int64_t rows, cols;
     float eps;
-    float inv_cols;
+    float count, inv_cols;  // cols, 1 / cols
 };
 
 struct BwdParams {
@@ -136,6 +137,13 @@ __device__ __forceinline__ void add_elements(F2& s, const Pack<T, V>& k) {
     for (int i = 0; i < pairs<V>(); ++i) s = add2(s, x[i]);
 }
 template <typename T, int V>
+__device__ __forceinline__ void add_distances(F2& s, const Pack<T, V>& k, F2 minus_mean) {
+    F2 x[pairs<V>()];
+    widen<T, V>(x, k);
+#pragma unroll
+    for (int i = 0; i < pairs<V>(); ++i) s = add2(s, add2(x[i], minus_mean));
+}
+template <typename T, int V>
 __device__ __forceinline__ void add_squares(F2& s, const Pack<T, V>& k, F2 minus_mean) {
     F2 x[pairs<V>()];
     widen<T, V>(x, k);
@@ -172,6 +180,31 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
 #pragma unroll
     for (int i = 0; i < W; ++i) s += slot[i];
     return s;
+}
+
+// A row's sum over its count, the nearest value of the quotient: the product
+// with the rounded 1 / count, corrected by what it leaves (infinities and NaN
+// as they are).
+__device__ __forceinline__ float mean_of(float sum, const FwdParams& p) {
+    const float q = sum * p.inv_cols, rest = fmaf(-q, p.count, sum);
+    return rest == rest ? fmaf(rest, p.inv_cols, q) : q;
+}
+// The mean's error, a few roundings of it, shows where the row's spread is small
+// beside it: below 2^-6 of the mean (there it is 2^-16 of the spread).  Such rows
+// sum the distances from it too, and take their mean out of the mean and of the
+// squares (Chan, Golub and LeVeque's corrected two-pass algorithm), which leaves
+// the mean's one rounding, and nothing of a row of equal values.  The test costs
+// [16384, 4096] BF16 some 0.5 us; the distances in every row 1.5.
+__device__ __forceinline__ bool far_from_zero(float mean, float squares, const FwdParams& p) {
+    return __builtin_expect(squares * 4096.f < mean * mean * p.count, 0);   // not for NaN
+}
+__device__ __forceinline__ void correct(float& mean, float& squares, float distances, const FwdParams& p) {
+    const float shift = distances * p.inv_cols;
+    mean += shift;
+    squares = fmaxf(fmaf(-distances, shift, squares), 0.f);
+}
+__device__ __forceinline__ float rstd_of(float squares, const FwdParams& p) {
+    return 1.0f / sqrtf(fmaf(squares, p.inv_cols, p.eps));
 }
 
 // A thread's columns of a row: packs of V at (base + i stride) V, or, for rows of
@@ -229,13 +262,14 @@ struct Columns {
 };
 
 // W warps on a row, NV packs (or pairs of elements) a thread, in registers.
-// W == 1: blocks of four independent warps.
+// W == 1: blocks of four independent warps (nine of them an SM with four packs
+// a thread: [16384, 1024] BF16 14.0 us, eight 14.6).
 template <typename T, int V, int W, int NV>
-__global__ void __launch_bounds__(W == 1 ? 128 : W * 32)
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, V == 8 && W == 1 && NV == 4 ? 9 : 0)
 forward_kernel(const FwdParams p) {
     using C = Columns<T, V>;
     constexpr int P = C::P, TPR = W * 32;
-    __shared__ float slots[2][W];
+    __shared__ float slots[3][W];
     const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
     if (row >= p.rows) return;      // whole warps (W == 1); never with W > 1
@@ -254,8 +288,8 @@ forward_kernel(const FwdParams p) {
 #pragma unroll
         for (int q = 0; q < P; ++q) s = add2(s, v[q]);     // zeros past the row's end
     }
-    const float mean = block_sum<W>(sum_of<2>(s), slots[0]) * p.inv_cols;
-    const F2 minus_mean = both(-mean);
+    float mean = mean_of(block_sum<W>(sum_of<2>(s), slots[0]), p);
+    F2 minus_mean = both(-mean);
     s = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -276,7 +310,15 @@ forward_kernel(const FwdParams p) {
             }
         }
     }
-    const float rstd = 1.0f / sqrtf(fmaf(block_sum<W>(sum_of<2>(s), slots[1]), p.inv_cols, p.eps));
+    float squares = block_sum<W>(sum_of<2>(s), slots[1]);
+    if (far_from_zero(mean, squares, p)) {          // the whole row's threads
+        float distances = 0.f;
+#pragma unroll 1
+        for (int c = t; c < cols; c += TPR) distances += Num<T>::to_acc(x[c]) - mean;      // read again: few rows do
+        correct(mean, squares, block_sum<W>(distances, slots[2]), p);
+        minus_mean = both(-mean);
+    }
+    const float rstd = rstd_of(squares, p);
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -334,14 +376,29 @@ __global__ void __launch_bounds__(128) forward_short_kernel(const FwdParams p) {
         widen<T, V>(x, k[r]);
 #pragma unroll
         for (int q = 0; q < P; ++q) s = add2(s, x[q]);
-        const float mean = sum(s) * p.inv_cols;
+        float mean = mean_of(sum(s), p);
         s = 0;
 #pragma unroll
         for (int q = 0; q < P; ++q) {
             x[q] = add2(x[q], both(-mean));
             if (in) s = fma2(x[q], x[q], s);
         }
-        const float rstd = 1.0f / sqrtf(fmaf(sum(s), p.inv_cols, p.eps));
+        float squares = sum(s);
+        const bool far = far_from_zero(mean, squares, p);
+        if (__any_sync(0xffffffffu, far)) {         // any of the warp's rows: the whole warp sums
+            s = 0;
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+                if (in) s = add2(s, x[q]);
+            const float distances = sum(s);
+            if (far) {
+                const float before = mean;
+                correct(mean, squares, distances, p);
+#pragma unroll
+                for (int q = 0; q < P; ++q) x[q] = add2(x[q], both(before - mean));
+            }
+        }
+        const float rstd = rstd_of(squares, p);
         if (row >= p.rows) continue;
         if (c == 0) {
             if (p.mean) p.mean[row] = mean;
@@ -360,7 +417,7 @@ __global__ void __launch_bounds__(128) forward_short_kernel(const FwdParams p) {
 // Rows longer than the registers of a block hold: three passes over the row.
 template <typename T, int V>
 __global__ void __launch_bounds__(1024) forward_long_kernel(const FwdParams p) {
-    __shared__ float slots[2][32];
+    __shared__ float slots[3][32];
     const T* gamma = static_cast<const T*>(p.gamma);
     const T* beta = static_cast<const T*>(p.beta);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -369,12 +426,20 @@ __global__ void __launch_bounds__(1024) forward_long_kernel(const FwdParams p) {
         F2 s = 0;
 #pragma unroll 4
         for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) add_elements<T, V>(s, load<T, V>(x + c));
-        const float mean = block_sum<32>(sum_of<V>(s), slots[0]) * p.inv_cols;
+        float mean = mean_of(block_sum<32>(sum_of<V>(s), slots[0]), p);
         s = 0;
 #pragma unroll 4
         for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V)
             add_squares<T, V>(s, load<T, V>(x + c), both(-mean));
-        const float rstd = 1.0f / sqrtf(fmaf(block_sum<32>(sum_of<V>(s), slots[1]), p.inv_cols, p.eps));
+        float squares = block_sum<32>(sum_of<V>(s), slots[1]);
+        if (far_from_zero(mean, squares, p)) {      // the whole block
+            s = 0;
+#pragma unroll 1
+            for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V)
+                add_distances<T, V>(s, load<T, V>(x + c), both(-mean));
+            correct(mean, squares, block_sum<32>(sum_of<V>(s), slots[2]), p);
+        }
+        const float rstd = rstd_of(squares, p);
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
@@ -1126,7 +1191,7 @@ olc_status olc_layer_norm_forward(olc_layer_norm_plan* plan, const void* X, int6
     const olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
     norm::FwdParams p{X, gamma, beta, Y, mean, rstd, x_pitch, y_pitch, plan->rows, plan->cols, plan->eps,
-                      (float)(1.0 / (double)plan->cols)};
+                      (float)plan->cols, (float)(1.0 / (double)plan->cols)};
     // 16-byte packs need every row of every operand on a 16-byte boundary
     const bool wide = plan->cols * eb % 16 == 0 && plan_aligned16(X) && plan_aligned16(Y) && plan_aligned16(gamma) &&
                       plan_aligned16(beta) && (plan->rows == 1 || (x_pitch * eb % 16 == 0 && y_pitch * eb % 16 == 0));

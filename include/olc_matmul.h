@@ -405,10 +405,11 @@ typedef struct olc_layer_norm_plan olc_layer_norm_plan;
  * Layer norm of each row of X [rows, cols]: with n = cols,
  *     mean = sum_j x_j / n,   rstd = 1 / sqrt(sum_j (x_j - mean)^2 / n + eps),
  *     y_j = (x_j - mean) * rstd * gamma_j + beta_j.
- * rows >= 0, 1 <= cols < 2^31 - 65536, eps >= 0 (a row of equal values with
- * eps = 0 gives NaN).  Errors: OLC_ERR_NULL, OLC_ERR_DTYPE,
- * OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID (no columns, too many, a negative or
- * NaN eps, more than 2^62 bytes), OLC_ERR_OOM.
+ * A row of equal values has them as its mean, and y = beta; with eps = 0 there
+ * is no variance to divide by: NaN (beta, where the sum of the values rounds).
+ * rows >= 0, 1 <= cols < 2^31 - 65536, 0 <= eps <= 3e38.  Errors:
+ * OLC_ERR_NULL, OLC_ERR_DTYPE, OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID (no
+ * columns, too many, another eps, more than 2^62 bytes), OLC_ERR_OOM.
  */
 olc_status olc_layer_norm_plan_create(int64_t rows, int64_t cols, double eps, olc_dtype dtype,
                                       olc_layer_norm_plan** out);
