@@ -56,7 +56,7 @@ struct Num<__nv_bfloat16> {
 // erfc(|z|) for z < 0, which avoids cancellation on the negative side.  The
 // body is short because the epilogue inlines it once per accumulator
 // register of its unrolled store loop.
-__device__ __forceinline__ float gelu_one_plus_erf_f32(float y) {
+__device__ __forceinline__ float gelu_f32(float y) {
     const float z = y * 0.70710678118654752f;
     const float az = fabsf(z);
     const float t = __fdividef(1.0f, fmaf(0.3275911f, az, 1.0f));
@@ -65,10 +65,7 @@ __device__ __forceinline__ float gelu_one_plus_erf_f32(float y) {
     q = fmaf(q, t, -0.284496736f);
     q = fmaf(q, t, 0.254829592f);
     const float c = q * t * __expf(-az * az);            // erfc(|z|)
-    return z >= 0.f ? 2.0f - c : c;                      // NaN takes the second arm
-}
-__device__ __forceinline__ float gelu_f32(float y) {
-    const float one_plus_erf = gelu_one_plus_erf_f32(y);
+    const float one_plus_erf = z >= 0.f ? 2.0f - c : c;  // NaN takes the second arm
     return 0.5f * y * one_plus_erf;
 }
 
