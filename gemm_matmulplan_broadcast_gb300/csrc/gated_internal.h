@@ -70,9 +70,11 @@ __device__ __forceinline__ void gate_slope(float g, float& value, float& slope) 
         value = g < 0.f ? 0.f : g;
         slope = g > 0.f ? 1.f : 0.f;
     } else {
-        const float s = sigmoid<EXACT>(g);
-        value = s;
-        slope = s * (1.0f - s);
+        // s(|g|) = 1 / (1 + e) with e = e^-|g| leaves 1 - s = e s, which 1 - s itself would cancel
+        const float e = EXACT ? expf(-fabsf(g)) : __expf(-fabsf(g));
+        const float s = EXACT ? 1.0f / (1.0f + e) : __fdividef(1.0f, 1.0f + e);
+        value = g < 0.f ? e * s : s;
+        slope = e * s * s;
     }
 }
 // f(the activation as a constant): one branch around a whole
