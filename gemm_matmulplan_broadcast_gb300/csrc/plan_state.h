@@ -27,6 +27,7 @@ inline bool plan_fits(int64_t a, int64_t b, int64_t bytes) {
     return !__builtin_mul_overflow(a, b, &n) && !__builtin_mul_overflow(n, bytes, &n) && n <= kPlanMaxBytes;
 }
 
+#ifdef __CUDACC__
 // A launch in full stream order.  The kernels of these plans neither start
 // before their predecessor has ended nor let a successor start early
 // (programmatic dependent launch): blocks that start early and wait hold
@@ -38,6 +39,7 @@ inline cudaError_t plan_launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
     kernel<<<grid, block, smem, s>>>(static_cast<KArgs>(args)...);
     return cudaGetLastError();
 }
+#endif
 
 inline int64_t plan_elem_bytes(olc_dtype dt) { return dt == OLC_FLOAT ? 4 : 2; }
 inline bool plan_dtype_ok(int dt) { return dt == OLC_FLOAT || dt == OLC_FLOAT16 || dt == OLC_BFLOAT16; }
@@ -49,7 +51,9 @@ inline bool plan_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(
 // Device binding and the plan's own device memory.  Calls that use that
 // memory are ordered across streams: one on another stream than the last
 // such call waits for it on the GPU (an event, created at the first use).
-// While a stream is capturing a graph nothing is recorded or waited for.
+// Streams are told apart by their identity: a handle may name another stream
+// later (the default stream of each host thread, a stream made after one was
+// destroyed).  While a stream is capturing a graph nothing is recorded or waited for.
 struct PlanState {
     struct Earlier {
         void* memory;
@@ -61,7 +65,7 @@ struct PlanState {
     size_t bytes;
     Earlier* earlier;        // smaller blocks that `memory` has replaced
     cudaEvent_t event;
-    cudaStream_t stream;
+    unsigned long long stream;      // identity of the last call's
     int event_live;
 
     void init() {
@@ -103,11 +107,14 @@ struct PlanState {
     }
 
     cudaError_t before_use(cudaStream_t s) {
-        if (!event_live || stream == s) return cudaSuccess;
+        if (!event_live) return cudaSuccess;
         cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
         cudaError_t e = cudaStreamIsCapturing(s, &cs);
         if (e != cudaSuccess) return e;
         if (cs != cudaStreamCaptureStatusNone) return cudaSuccess;
+        unsigned long long id = 0;      // (asking would break a capture)
+        e = cudaStreamGetId(s, &id);
+        if (e != cudaSuccess || id == stream) return e;
         return cudaStreamWaitEvent(s, event, 0);
     }
 
@@ -123,9 +130,11 @@ struct PlanState {
                 return e;
             }
         }
-        e = cudaEventRecord(event, s);
+        unsigned long long id = 0;
+        e = cudaStreamGetId(s, &id);
+        if (e == cudaSuccess) e = cudaEventRecord(event, s);
         if (e != cudaSuccess) return e;
-        stream = s;
+        stream = id;
         event_live = 1;
         return cudaSuccess;
     }

@@ -1,0 +1,55 @@
+"""How the layer plans order calls that share their memory (csrc/plan_state.h),
+compiled here against a stand-in for the CUDA runtime that writes down waits
+and records with the identity of the stream."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from gemm_matmulplan_broadcast_gb300.build import CSRC, INCLUDE
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+def run(tmp_path, body):
+    if not shutil.which("g++"):
+        pytest.skip("no g++")
+    src = tmp_path / "t.cpp"
+    src.write_text('#include "plan_state.h"\nint main() {\n    olc::PlanState p;\n    p.init();\n%s\n    p.destroy();\n'
+                   '    std::puts(fake::log.c_str());\n}\n' % body)
+    exe = str(tmp_path / "t")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", os.path.join(HERE, "fake_cuda"), "-I", CSRC, "-I", INCLUDE,
+                    str(src), "-o", exe], check=True)
+    return subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()
+
+
+CALL = "p.before_use(%s); p.after_use(%s);"
+
+
+def test_one_stream_does_not_wait_for_itself(tmp_path):
+    log = run(tmp_path, "FakeStream a{7, false};" + 3 * (CALL % ("&a", "&a")))
+    assert log == ["record7"] * 3
+
+
+def test_another_stream_waits(tmp_path):
+    log = run(tmp_path, "FakeStream a{7, false}, b{8, false};" + CALL % ("&a", "&a") + CALL % ("&b", "&b") + CALL % ("&a", "&a"))
+    assert log == ["record7", "wait8", "record8", "wait7", "record7"]
+
+
+def test_the_default_streams_of_two_threads_are_two_streams(tmp_path):
+    one = CALL % ("fake::per_thread", "fake::per_thread")
+    log = run(tmp_path, one + "fake::thread_stream_id = 1001;" + one)
+    assert log == ["record1000", "wait1001", "record1001"]
+
+
+def test_a_handle_that_names_a_new_stream_waits_for_the_old_one(tmp_path):
+    log = run(tmp_path, "FakeStream a{7, false};" + CALL % ("&a", "&a") + "a.id = 9;" + CALL % ("&a", "&a"))
+    assert log == ["record7", "wait9", "record9"]
+
+
+def test_captures_are_left_alone(tmp_path):
+    log = run(tmp_path, "FakeStream a{7, false}, b{8, true};" + CALL % ("&a", "&a") +
+              "if (p.before_use(&b) || p.after_use(&b)) return 1;" + CALL % ("&a", "&a"))
+    assert log == ["record7", "record7"]
