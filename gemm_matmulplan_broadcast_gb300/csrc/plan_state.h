@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "olc_matmul.h"
+#include "stream_order.h"
 
 namespace olc {
 
@@ -48,13 +49,9 @@ inline bool plan_misaligned(const void* p, int64_t bytes) {
 }
 inline bool plan_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Device binding and the plan's own device memory.  Calls that use that
-// memory are ordered across streams: one on another stream than the last
-// such call waits for it on the GPU (an event, created at the first use).
-// Streams are told apart by their identity: a handle may name another stream
-// later (the default stream of each host thread, a stream made after one was
-// destroyed).  While a stream is capturing a graph nothing is recorded or waited for.
-struct PlanState {
+// Device binding and the plan's own device memory, with the order of the calls
+// that use it.
+struct PlanState : StreamOrder {
     struct Earlier {
         void* memory;
         Earlier* next;
@@ -64,9 +61,6 @@ struct PlanState {
     void* memory;
     size_t bytes;
     Earlier* earlier;        // smaller blocks that `memory` has replaced
-    cudaEvent_t event;
-    unsigned long long stream;      // identity of the last call's
-    int event_live;
 
     void init() {
         std::memset(this, 0, sizeof *this);
@@ -104,39 +98,6 @@ struct PlanState {
         memory = larger;
         bytes = want;
         return OLC_OK;
-    }
-
-    cudaError_t before_use(cudaStream_t s) {
-        if (!event_live) return cudaSuccess;
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-        cudaError_t e = cudaStreamIsCapturing(s, &cs);
-        if (e != cudaSuccess) return e;
-        if (cs != cudaStreamCaptureStatusNone) return cudaSuccess;
-        unsigned long long id = 0;      // (asking would break a capture)
-        e = cudaStreamGetId(s, &id);
-        if (e != cudaSuccess || id == stream) return e;
-        return cudaStreamWaitEvent(s, event, 0);
-    }
-
-    cudaError_t after_use(cudaStream_t s) {
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-        cudaError_t e = cudaStreamIsCapturing(s, &cs);
-        if (e != cudaSuccess) return e;
-        if (cs != cudaStreamCaptureStatusNone) return cudaSuccess;
-        if (!event) {
-            e = cudaEventCreateWithFlags(&event, cudaEventDisableTiming);
-            if (e != cudaSuccess) {
-                event = nullptr;
-                return e;
-            }
-        }
-        unsigned long long id = 0;
-        e = cudaStreamGetId(s, &id);
-        if (e == cudaSuccess) e = cudaEventRecord(event, s);
-        if (e != cudaSuccess) return e;
-        stream = id;
-        event_live = 1;
-        return cudaSuccess;
     }
 
     // free another piece of device memory of the plan (null: nothing)

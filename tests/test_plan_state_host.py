@@ -53,3 +53,13 @@ def test_captures_are_left_alone(tmp_path):
     log = run(tmp_path, "FakeStream a{7, false}, b{8, true};" + CALL % ("&a", "&a") +
               "if (p.before_use(&b) || p.after_use(&b)) return 1;" + CALL % ("&a", "&a"))
     assert log == ["record7", "record7"]
+
+
+def test_every_plan_with_memory_follows_this_order():
+    # the matrix plans hold the same order; nobody keeps a handle to compare
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        if name == "api.cpp":
+            assert "StreamOrder order;" in text and "order.before_use(s)" in text
+        assert "state_stream" not in text and "stream == s" not in text, name
