@@ -596,15 +596,14 @@ olc_status run(const olc_matmul_plan* p, const void* A, const void* B, void* Y, 
     const olc_dtype dt = p->dtype;
     const Route rt = route_of(p, A, B, Y, R);
     const int algo = rt.algo;
-    cudaError_t e = cudaSuccess;
     const bool uses_state = p->workspace != nullptr || rt.need.a || rt.need.b;
-    if (uses_state) {
-        e = mp->order.before_use(s);
-        if (e != cudaSuccess) return from_cuda(e);
-    }
+    if (algo < OLC_ALGO_DIRECT || algo > OLC_ALGO_GENERAL_SIMT) return OLC_ERR_INVALID;
     if (rt.need.a || rt.need.b) {
         const olc_status st = ensure_stage(mp, rt.need.a_bytes + rt.need.b_bytes);
         if (st != OLC_OK) return st;
+    }
+    auto enqueue = [&] {
+        cudaError_t e = cudaSuccess;
         unsigned char* base = static_cast<unsigned char*>(p->stage);
         // copy one operand: padded rows for the general tiles, one dense run
         // otherwise; `ld` receives the row pitch the kernels read (0: dense)
@@ -618,24 +617,22 @@ olc_status run(const olc_matmul_plan* p, const void* A, const void* B, void* Y, 
         };
         if (rt.need.a) {
             e = stage(A, base, stored_a(p), pr.a_ld);
-            if (e != cudaSuccess) return from_cuda(e);
+            if (e != cudaSuccess) return e;
             pr.A = base;
         }
         if (rt.need.b) {
             e = stage(B, base + rt.need.a_bytes, stored_b(p), pr.b_ld);
-            if (e != cudaSuccess) return from_cuda(e);
+            if (e != cudaSuccess) return e;
             pr.B = base + rt.need.a_bytes;
         }
-    }
-    if (rt.b_padded) {
-        pr.B = p->const_b_pad;
-        pr.b_ld = pad8(stored_b(p).cols);
-    }
-    pr.y_unaligned = rt.y_unaligned ? 1 : 0;
-    if (algo < OLC_ALGO_DIRECT || algo > OLC_ALGO_GENERAL_SIMT) return OLC_ERR_INVALID;
-    e = launch_route(p, pr, dt, algo, B, s);
-    if (e == cudaSuccess && uses_state) e = mp->order.after_use(s);
-    return from_cuda(e);
+        if (rt.b_padded) {
+            pr.B = p->const_b_pad;
+            pr.b_ld = pad8(stored_b(p).cols);
+        }
+        pr.y_unaligned = rt.y_unaligned ? 1 : 0;
+        return launch_route(p, pr, dt, algo, B, s);
+    };
+    return from_cuda(uses_state ? mp->order.use(s, enqueue) : enqueue());
 }
 
 cudaError_t launch_route(const olc_matmul_plan* p, const Problem& pr, olc_dtype dt, int algo,

@@ -989,8 +989,6 @@ olc_status forward16(olc_gated_plan* p, const void* X, const void* Wg, const voi
         }
     }
     const bool uses = x.copy || wg.copy || wu.copy || partial;
-    cudaError_t e = uses ? p->state.before_use(s) : cudaSuccess;
-    if (e == cudaSuccess) e = fill({&x, &wg, &wu}, p->state.sm_count, s);
     gated::Product w;
     std::memset(&w, 0, sizeof w);
     w.M = p->M;
@@ -1004,11 +1002,13 @@ olc_status forward16(olc_gated_plan* p, const void* X, const void* Wg, const voi
     w.Y[1] = G;
     w.Y[2] = U;
     w.act = p->act;
-    if (e == cudaSuccess)
-        e = few ? gated::launch_few(p->dtype, w, p->state.sm_count, s)
-                : gated::launch_product<gated::FWD>(p->dtype, w, part, p->state.sm_count, s);
-    if (e == cudaSuccess && uses) e = p->state.after_use(s);
-    return plan_status(e);
+    auto run = [&] {
+        const cudaError_t e = fill({&x, &wg, &wu}, p->state.sm_count, s);
+        if (e != cudaSuccess) return e;
+        return few ? gated::launch_few(p->dtype, w, p->state.sm_count, s)
+                   : gated::launch_product<gated::FWD>(p->dtype, w, part, p->state.sm_count, s);
+    };
+    return plan_status(uses ? p->state.use(s, run) : run());
 }
 
 olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const void* Wg, const void* Wu, const void* G,
@@ -1039,45 +1039,44 @@ olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const vo
             if (st != OLC_OK) return st;
         }
     }
-    cudaError_t e = p->state.before_use(s);
-    if (e == cudaSuccess)
-        e = p->dtype == OLC_BFLOAT16
-                ? gated::launch_slope<__nv_bfloat16>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s)
-                : gated::launch_slope<__half>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s);
-    const gated::Stored sg{dg, p->M, p->F, pitch}, su{du, p->M, p->F, pitch};
-    gated::Product w;
-    if (dX) {
-        if (e == cudaSuccess) e = fill({&wg, &wu}, sms, s);
-        std::memset(&w, 0, sizeof w);
-        w.M = p->M;
-        w.N = p->D;
-        w.K = p->F;
-        w.a[0] = sg;
-        w.a[1] = su;
-        w.b[0] = wg.stored();
-        w.b[1] = wu.stored();
-        w.b_k = !p->trans_w;
-        w.Y[0] = dX;
-        if (e == cudaSuccess) e = gated::launch_product<gated::DX>(p->dtype, w, part, sms, s);
-    }
-    if (dWg) {
-        if (e == cudaSuccess) e = fill({&x}, sms, s);
-        std::memset(&w, 0, sizeof w);
-        w.M = wm;
-        w.N = wn;
-        w.K = p->M;
-        const gated::Stored sx = x.stored();
-        w.a[0] = p->trans_w ? sg : sx;
-        w.a[1] = p->trans_w ? su : sx;
-        w.b[0] = p->trans_w ? sx : sg;
-        w.b[1] = p->trans_w ? sx : su;
-        w.a_mn = true;
-        w.Y[0] = dWg;
-        w.Y[1] = dWu;
-        if (e == cudaSuccess) e = gated::launch_product<gated::DW>(p->dtype, w, part, sms, s);
-    }
-    if (e == cudaSuccess) e = p->state.after_use(s);
-    return plan_status(e);
+    return plan_status(p->state.use(s, [&] {
+        cudaError_t e = p->dtype == OLC_BFLOAT16
+                            ? gated::launch_slope<__nv_bfloat16>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s)
+                            : gated::launch_slope<__half>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s);
+        const gated::Stored sg{dg, p->M, p->F, pitch}, su{du, p->M, p->F, pitch};
+        gated::Product w;
+        if (dX && e == cudaSuccess) {
+            e = fill({&wg, &wu}, sms, s);
+            std::memset(&w, 0, sizeof w);
+            w.M = p->M;
+            w.N = p->D;
+            w.K = p->F;
+            w.a[0] = sg;
+            w.a[1] = su;
+            w.b[0] = wg.stored();
+            w.b[1] = wu.stored();
+            w.b_k = !p->trans_w;
+            w.Y[0] = dX;
+            if (e == cudaSuccess) e = gated::launch_product<gated::DX>(p->dtype, w, part, sms, s);
+        }
+        if (dWg && e == cudaSuccess) {
+            e = fill({&x}, sms, s);
+            std::memset(&w, 0, sizeof w);
+            w.M = wm;
+            w.N = wn;
+            w.K = p->M;
+            const gated::Stored sx = x.stored();
+            w.a[0] = p->trans_w ? sg : sx;
+            w.a[1] = p->trans_w ? su : sx;
+            w.b[0] = p->trans_w ? sx : sg;
+            w.b[1] = p->trans_w ? sx : su;
+            w.a_mn = true;
+            w.Y[0] = dWg;
+            w.Y[1] = dWu;
+            if (e == cudaSuccess) e = gated::launch_product<gated::DW>(p->dtype, w, part, sms, s);
+        }
+        return e;
+    }));
 }
 
 // FLOAT, few rows and weights [D, F]: the matrix plan's row kernels stream
@@ -1096,18 +1095,18 @@ olc_status forward32_few(olc_gated_plan* p, const void* X, const void* Wg, const
     // what is not kept: g in the plan's memory, u in H
     if (st == OLC_OK && !G) st = p->state.ensure((size_t)n * sizeof(float));
     if (st != OLC_OK) return st;
-    cudaError_t e = G ? cudaSuccess : p->state.before_use(s);
-    if (e != cudaSuccess) return plan_status(e);
     void* g = G ? G : p->state.memory;
     void* u = U ? U : H;
-    st = olc_matmul_execute(p->forward, X, Wg, g, s);
-    if (st == OLC_OK) st = olc_matmul_execute(p->forward, X, Wu, u, s);
-    if (st != OLC_OK) return st;
-    e = plan_launch(gated::product_kernel, dim3((unsigned)min64(ceil_div(n, 256), (int64_t)p->state.sm_count * 16)),
-                    dim3(256), 0, s, static_cast<const float*>(g), static_cast<const float*>(u), static_cast<float*>(H),
-                    n, p->act);
-    if (e == cudaSuccess && !G) e = p->state.after_use(s);
-    return plan_status(e);
+    auto run = [&] {
+        st = olc_matmul_execute(p->forward, X, Wg, g, s);
+        if (st == OLC_OK) st = olc_matmul_execute(p->forward, X, Wu, u, s);
+        if (st != OLC_OK) return cudaSuccess;
+        return plan_launch(gated::product_kernel,
+                           dim3((unsigned)min64(ceil_div(n, 256), (int64_t)p->state.sm_count * 16)), dim3(256), 0, s,
+                           static_cast<const float*>(g), static_cast<const float*>(u), static_cast<float*>(H), n, p->act);
+    };
+    const olc_status ran = plan_status(G ? run() : p->state.use(s, run));
+    return st != OLC_OK ? st : ran;
 }
 
 olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
@@ -1132,11 +1131,9 @@ olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const voi
     w.Y[1] = G;
     w.Y[2] = U;
     w.act = p->act;
-    cudaError_t e = p->state.before_use(s);          // the counters, if nothing else
-    if (e == cudaSuccess)
-        e = gated::launch_float(w, p->state.memory, static_cast<unsigned int*>(p->counters), sms, s);
-    if (e == cudaSuccess) e = p->state.after_use(s);
-    return plan_status(e);
+    return plan_status(p->state.use(s, [&] {         // the counters, if nothing else
+        return gated::launch_float(w, p->state.memory, static_cast<unsigned int*>(p->counters), sms, s);
+    }));
 }
 
 olc_status backward32(olc_gated_plan* p, const void* dH, const void* X, const void* Wg, const void* Wu, const void* G,
@@ -1154,41 +1151,41 @@ olc_status backward32(olc_gated_plan* p, const void* dH, const void* X, const vo
     unsigned char* memory = static_cast<unsigned char*>(p->state.memory);
     void *dg = memory, *du = memory + half, *part = memory + 2 * half;
     unsigned int* counters = static_cast<unsigned int*>(p->counters);
-    cudaError_t e = p->state.before_use(s);
-    if (e == cudaSuccess) e = gated::launch_slope<float>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s);
     const gated::Stored sg{dg, p->M, p->F, pitch}, su{du, p->M, p->F, pitch}, sx{X, p->M, p->D, p->D};
-    gated::Product w;
-    if (dX) {
-        std::memset(&w, 0, sizeof w);
-        w.mode = gated::DX;
-        w.M = p->M;
-        w.N = p->D;
-        w.K = p->F;
-        w.a[0] = sg;
-        w.a[1] = su;
-        w.b[0] = gated::Stored{Wg, wr, wc, wc};
-        w.b[1] = gated::Stored{Wu, wr, wc, wc};
-        w.b_k = !p->trans_w;
-        w.Y[0] = dX;
-        if (e == cudaSuccess) e = gated::launch_float(w, part, counters, sms, s);
-    }
-    if (dWg) {
-        std::memset(&w, 0, sizeof w);
-        w.mode = gated::DW;
-        w.M = wr;
-        w.N = wc;
-        w.K = p->M;
-        w.a[0] = p->trans_w ? sg : sx;
-        w.a[1] = p->trans_w ? su : sx;
-        w.b[0] = p->trans_w ? sx : sg;
-        w.b[1] = p->trans_w ? sx : su;
-        w.a_mn = true;
-        w.Y[0] = dWg;
-        w.Y[1] = dWu;
-        if (e == cudaSuccess) e = gated::launch_float(w, part, counters, sms, s);
-    }
-    if (e == cudaSuccess) e = p->state.after_use(s);
-    return plan_status(e);
+    return plan_status(p->state.use(s, [&] {
+        cudaError_t e = gated::launch_slope<float>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s);
+        gated::Product w;
+        if (dX && e == cudaSuccess) {
+            std::memset(&w, 0, sizeof w);
+            w.mode = gated::DX;
+            w.M = p->M;
+            w.N = p->D;
+            w.K = p->F;
+            w.a[0] = sg;
+            w.a[1] = su;
+            w.b[0] = gated::Stored{Wg, wr, wc, wc};
+            w.b[1] = gated::Stored{Wu, wr, wc, wc};
+            w.b_k = !p->trans_w;
+            w.Y[0] = dX;
+            e = gated::launch_float(w, part, counters, sms, s);
+        }
+        if (dWg && e == cudaSuccess) {
+            std::memset(&w, 0, sizeof w);
+            w.mode = gated::DW;
+            w.M = wr;
+            w.N = wc;
+            w.K = p->M;
+            w.a[0] = p->trans_w ? sg : sx;
+            w.a[1] = p->trans_w ? su : sx;
+            w.b[0] = p->trans_w ? sx : sg;
+            w.b[1] = p->trans_w ? sx : su;
+            w.a_mn = true;
+            w.Y[0] = dWg;
+            w.Y[1] = dWu;
+            e = gated::launch_float(w, part, counters, sms, s);
+        }
+        return e;
+    }));
 }
 
 }  // namespace

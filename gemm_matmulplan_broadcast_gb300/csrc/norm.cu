@@ -1243,16 +1243,15 @@ olc_status olc_layer_norm_backward(olc_layer_norm_plan* plan, const void* dY, in
         st = plan->state.ensure((size_t)blocks * 2 * (size_t)cols * sizeof(float));
         if (st != OLC_OK) return st;
         p.partial = static_cast<float*>(plan->state.memory);
-        const cudaError_t e = plan->state.before_use(s);
-        if (e != cudaSuccess) return plan_status(e);
     }
     return norm::by_type(plan->dtype, [&](auto tag) {
         using T = decltype(tag);
         T *dg = static_cast<T*>(dgamma), *db = static_cast<T*>(dbeta);
-        cudaError_t e = wide ? norm::backward_as<T, 16 / sizeof(T)>(p, plan->state.sm_count, dg, db, s)
-                             : norm::backward_as<T, 1>(p, plan->state.sm_count, dg, db, s);
-        if (e == cudaSuccess && weights) e = plan->state.after_use(s);
-        return plan_status(e);
+        auto run = [&] {
+            return wide ? norm::backward_as<T, 16 / sizeof(T)>(p, plan->state.sm_count, dg, db, s)
+                        : norm::backward_as<T, 1>(p, plan->state.sm_count, dg, db, s);
+        };
+        return plan_status(weights ? plan->state.use(s, run) : run());
     });
 }
 

@@ -50,6 +50,18 @@ struct StreamOrder {
         event_live = 1;
         return cudaSuccess;
     }
+
+    // f enqueues the call's work, and all that it did enqueue is recorded: work
+    // that went ahead of a failure uses the memory like any other.  The first
+    // error.
+    template <typename F>
+    cudaError_t use(cudaStream_t s, F&& f) {
+        const cudaError_t before = before_use(s);
+        if (before != cudaSuccess) return before;
+        const cudaError_t e = f();
+        const cudaError_t after = after_use(s);
+        return e != cudaSuccess ? e : after;
+    }
 };
 
 }  // namespace olc

@@ -61,5 +61,22 @@ def test_every_plan_with_memory_follows_this_order():
         with open(os.path.join(CSRC, name)) as f:
             text = f.read()
         if name == "api.cpp":
-            assert "StreamOrder order;" in text and "order.before_use(s)" in text
+            assert "StreamOrder order;" in text and "order." in text
         assert "state_stream" not in text and "stream == s" not in text, name
+
+
+def test_what_went_ahead_of_a_failure_is_recorded(tmp_path):
+    log = run(tmp_path, "FakeStream a{7, false}, b{8, false};"
+              "const cudaError_t e = p.use(&a, [] { fake::log += \"work \"; return cudaErrorLaunchFailure; });"
+              "if (e != cudaErrorLaunchFailure) return 1;"
+              "if (p.use(&b, [] { fake::log += \"work \"; return cudaSuccess; })) return 1;")
+    assert log == ["work", "record7", "wait8", "work", "record8"]
+
+
+def test_plans_enqueue_under_the_order_alone():
+    # no call notes its use by hand, where an early return could leave it out
+    for name in sorted(os.listdir(CSRC)):
+        if name != "stream_order.h":
+            with open(os.path.join(CSRC, name)) as f:
+                text = f.read()
+            assert "before_use(" not in text and "after_use(" not in text, name
