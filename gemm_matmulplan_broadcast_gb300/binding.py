@@ -8,6 +8,7 @@ has not been built -- there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -162,6 +163,17 @@ def _stream_handle(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _memory_of(stream):
+    """Context in which torch allocates from the memory of ``stream`` (a torch
+    stream or a handle; None: the current one), for outputs that are written
+    there: a block of the current stream may still be in use by work that is
+    queued on it."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def _ptr(t) -> Optional[int]:
@@ -376,8 +388,9 @@ class Plan:
         import torch
         from .synth import TORCH_DTYPES, output_dtype
         if out is None:
-            out = torch.empty(self.output_shape, dtype=TORCH_DTYPES[output_dtype(self.dtype)],
-                              device=A.device)
+            with _memory_of(stream):
+                out = torch.empty(self.output_shape, dtype=TORCH_DTYPES[output_dtype(self.dtype)],
+                                  device=A.device)
         return self.execute(A, B, out, stream)
 
 
@@ -516,7 +529,8 @@ def gemm(A, B, C=None, alpha=1.0, beta=1.0, trans_a=False, trans_b=False, out=No
     with GemmPlan(A.shape, B.shape, inv[A.dtype], trans_a, trans_b, alpha, beta,
                   None if C is None else C.shape) as plan:
         if out is None:
-            out = torch.empty(plan.output_shape, dtype=A.dtype, device=A.device)
+            with _memory_of(stream):
+                out = torch.empty(plan.output_shape, dtype=A.dtype, device=A.device)
         return plan.execute(A, B, out, stream=stream, C=C)
 
 

@@ -7,14 +7,17 @@ A plan is made for fixed sizes and one element type ("float32", "float16" or
 "bfloat16"); its calls take CUDA tensors and outputs that the caller owns and
 enqueue kernels on ``stream`` (torch's current stream by default).  Row
 tensors are [rows, cols] (any leading dimensions when contiguous) with
-unit-stride columns; a two-dimensional one may have any row pitch.
+unit-stride columns; a two-dimensional one may have any row pitch.  The
+one-shot functions return memory of ``stream``, and read their inputs there:
+where it is not torch's current stream, the two have to be ordered by the
+caller (``wait_stream``), as for torch's own operators.
 """
 
 from __future__ import annotations
 
 import ctypes
 
-from .binding import DTYPE_CODES, GATES, _check, _stream_handle, load
+from .binding import DTYPE_CODES, GATES, _check, _memory_of, _stream_handle, load
 
 ROW_DTYPES = ("float32", "float16", "bfloat16")
 
@@ -245,7 +248,8 @@ def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out=None, stream=Non
     """Layer norm of a CUDA tensor over its last axis through a fresh plan."""
     import torch
     if out is None:
-        out = torch.empty_like(X, memory_format=torch.contiguous_format)
+        with _memory_of(stream):
+            out = torch.empty_like(X, memory_format=torch.contiguous_format)
     cols = X.shape[-1] if X.dim() else 0
     rows = X.numel() // cols if cols else 0
     with LayerNormPlan(rows, cols, str(X.dtype).replace("torch.", ""), eps) as plan:
@@ -257,7 +261,8 @@ def gated(X, Wg, Wu, act: str = "silu", trans_w: bool = False, out=None, stream=
     import torch
     d, f = reversed(Wg.shape) if trans_w else Wg.shape
     if out is None:
-        out = torch.empty(X.shape[:-1] + (f,), dtype=X.dtype, device=X.device)
+        with _memory_of(stream):
+            out = torch.empty(X.shape[:-1] + (f,), dtype=X.dtype, device=X.device)
     with GatedPlan(X.numel() // d if d else X.shape[0], d, f, str(X.dtype).replace("torch.", ""), act, trans_w) as plan:
         return plan.forward(X, Wg, Wu, out, stream=stream)
 
@@ -268,8 +273,9 @@ def token_log_probs(logits, tokens, top: int = 0, stream=None):
     import torch
     rows, vocab = logits.shape
     make = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=logits.device)  # noqa: E731
-    logprob, entropy = make(rows), make(rows)
-    best = (make(rows, top), make(rows, top, dtype=torch.int64)) if top else (None, None)
+    with _memory_of(stream):
+        logprob, entropy = make(rows), make(rows)
+        best = (make(rows, top), make(rows, top, dtype=torch.int64)) if top else (None, None)
     with TokenLogProbsPlan(rows, vocab, str(logits.dtype).replace("torch.", ""), top) as plan:
         plan.forward(logits, tokens, logprob, entropy=entropy, top_logprob=best[0], top_index=best[1], stream=stream)
     return (logprob, entropy) + (best if top else ())
