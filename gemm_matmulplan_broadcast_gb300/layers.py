@@ -263,7 +263,7 @@ def gated(X, Wg, Wu, act: str = "silu", trans_w: bool = False, out=None, stream=
     if out is None:
         with _memory_of(stream):
             out = torch.empty(X.shape[:-1] + (f,), dtype=X.dtype, device=X.device)
-    with GatedPlan(X.numel() // d if d else X.shape[0], d, f, str(X.dtype).replace("torch.", ""), act, trans_w) as plan:
+    with GatedPlan(X.shape[:-1].numel(), d, f, str(X.dtype).replace("torch.", ""), act, trans_w) as plan:
         return plan.forward(X, Wg, Wu, out, stream=stream)
 
 
