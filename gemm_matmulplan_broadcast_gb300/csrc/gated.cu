@@ -909,7 +909,10 @@ struct olc_gated_plan {
 
 namespace {
 
-// the FLOAT counters, made when first needed; zero before any stream goes on
+// The FLOAT counters, made with the plan (or, where no device was visible then,
+// at the first call) and zero before any stream goes on.  They are cleared on a
+// stream of their own: the legacy stream would wait for every other one, and
+// break a capture that one of them is in.
 olc_status float_counters(olc_gated_plan* p) {
     if (p->counters) return OLC_OK;
     const size_t bytes = gated::float_counter_bytes(p->state.sm_count);
@@ -918,8 +921,13 @@ olc_status float_counters(olc_gated_plan* p) {
         cudaGetLastError();
         return OLC_ERR_OOM;
     }
-    cudaError_t e = cudaMemset(counters, 0, bytes);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
+    cudaStream_t own;
+    cudaError_t e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+    if (e == cudaSuccess) {
+        e = cudaMemsetAsync(counters, 0, bytes, own);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+        cudaStreamDestroy(own);
+    }
     if (e == cudaSuccess) p->counters = counters;
     else p->state.release(counters);
     return plan_status(e);
@@ -1213,6 +1221,13 @@ olc_status olc_gated_plan_create(int64_t rows, int64_t d_in, int64_t d_hidden, i
     p->F = d_hidden;
     p->act = activation;
     p->trans_w = trans_w ? 1 : 0;
+    if (dtype == OLC_FLOAT && p->state.device >= 0 && rows > 0 && d_in > 0 && d_hidden > 0) {
+        const olc_status st = float_counters(p);
+        if (st != OLC_OK) {
+            olc_gated_plan_destroy(p);
+            return st;
+        }
+    }
     *out = p;
     return OLC_OK;
 }

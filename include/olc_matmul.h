@@ -480,11 +480,11 @@ void olc_gated_plan_destroy(olc_gated_plan* plan);
  * Forward.  G, U [rows, d_hidden]: the two products, rounded to the plan's
  * type, for the backward call; NULL for what is not kept (H is formed from
  * the unrounded products either way).  No output may overlap another tensor.
- * Operand copies, K slices and FLOAT's intermediate products live in device
- * memory that the plan allocates at the first call that needs it (a larger
- * need later takes a new block; earlier ones stay until the plan is
- * destroyed, for graphs that captured them): make that call before any
- * stream capture.  Errors: OLC_ERR_NULL, OLC_ERR_INVALID,
+ * Operand copies, K slices and FLOAT's intermediate products and partial sums
+ * live in device memory that the plan allocates at the first call that needs it
+ * (a larger need later takes a new block; earlier ones stay until the plan is
+ * destroyed, for graphs that captured them): make that call before any stream
+ * capture.  Errors: OLC_ERR_NULL, OLC_ERR_INVALID,
  * OLC_ERR_WRONG_DEVICE, OLC_ERR_OOM, OLC_ERR_CUDA.
  */
 olc_status olc_gated_forward(olc_gated_plan* plan, const void* X, const void* Wg, const void* Wu, void* H, void* G,
