@@ -917,12 +917,10 @@ olc_status float_counters(olc_gated_plan* p) {
     if (p->counters) return OLC_OK;
     const size_t bytes = gated::float_counter_bytes(p->state.sm_count);
     void* counters = nullptr;
-    if (cudaMalloc(&counters, bytes) != cudaSuccess) {
-        cudaGetLastError();
-        return OLC_ERR_OOM;
-    }
+    cudaError_t e = cudaMalloc(&counters, bytes);
+    if (e != cudaSuccess) return plan_status(e);
     cudaStream_t own;
-    cudaError_t e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+    e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
     if (e == cudaSuccess) {
         e = cudaMemsetAsync(counters, 0, bytes, own);
         if (e == cudaSuccess) e = cudaStreamSynchronize(own);

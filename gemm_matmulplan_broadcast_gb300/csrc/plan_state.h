@@ -89,10 +89,10 @@ struct PlanState : StreamOrder {
         if (want <= bytes) return OLC_OK;
         Earlier* const keep = memory ? new (std::nothrow) Earlier{memory, earlier} : nullptr;
         void* larger = nullptr;
-        if ((memory && !keep) || cudaMalloc(&larger, want) != cudaSuccess) {
+        const cudaError_t e = memory && !keep ? cudaErrorMemoryAllocation : cudaMalloc(&larger, want);
+        if (e != cudaSuccess) {
             delete keep;
-            cudaGetLastError();
-            return OLC_ERR_OOM;
+            return plan_status(e);
         }
         if (keep) earlier = keep;
         memory = larger;

@@ -23,6 +23,7 @@ namespace fake {
 inline std::string log;
 inline FakeStream* const per_thread = reinterpret_cast<FakeStream*>(2);      // one handle, a stream a thread
 inline unsigned long long thread_stream_id = 1000;
+inline cudaError_t malloc_result = cudaSuccess;
 inline const FakeStream* of(cudaStream_t s) {
     static FakeStream own{0, false};
     if (s != per_thread) return s;
@@ -37,7 +38,10 @@ inline cudaError_t cudaGetDeviceCount(int* n) { *n = 1; return cudaSuccess; }
 inline cudaError_t cudaGetDevice(int* d) { *d = 0; return cudaSuccess; }
 inline cudaError_t cudaSetDevice(int) { return cudaSuccess; }
 inline cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) { *v = 152; return cudaSuccess; }
-inline cudaError_t cudaMalloc(void** p, size_t n) { *p = std::malloc(n); return cudaSuccess; }
+inline cudaError_t cudaMalloc(void** p, size_t n) {
+    if (fake::malloc_result == cudaSuccess) *p = std::malloc(n);
+    return fake::malloc_result;
+}
 inline cudaError_t cudaFree(void* p) { std::free(p); return cudaSuccess; }
 inline cudaError_t cudaStreamIsCapturing(cudaStream_t s, cudaStreamCaptureStatus* c) {
     *c = fake::of(s)->capturing ? cudaStreamCaptureStatusActive : cudaStreamCaptureStatusNone;

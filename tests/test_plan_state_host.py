@@ -80,3 +80,16 @@ def test_plans_enqueue_under_the_order_alone():
             with open(os.path.join(CSRC, name)) as f:
                 text = f.read()
             assert "before_use(" not in text and "after_use(" not in text, name
+
+
+def test_an_allocation_that_fails_says_why_and_keeps_what_is_there(tmp_path):
+    log = run(tmp_path, "if (p.ensure(100) != OLC_OK) return 1;"
+              "void* const before = p.memory;"
+              "fake::malloc_result = cudaErrorMemoryAllocation;"
+              "if (p.ensure(200) != OLC_ERR_OOM) return 1;"
+              "fake::malloc_result = cudaErrorLaunchFailure;      // refused for another reason: a capture, say\n"
+              "if (p.ensure(200) != OLC_ERR_CUDA) return 1;"
+              "if (p.memory != before || p.bytes != 100 || p.earlier) return 1;"
+              "fake::malloc_result = cudaSuccess;"
+              "if (p.ensure(200) != OLC_OK || p.bytes != 200 || !p.earlier) return 1;")
+    assert log == []
