@@ -87,7 +87,8 @@ def test_an_allocation_that_fails_says_why_and_keeps_what_is_there(tmp_path):
               "void* const before = p.memory;"
               "fake::malloc_result = cudaErrorMemoryAllocation;"
               "if (p.ensure(200) != OLC_ERR_OOM) return 1;"
-              "fake::malloc_result = cudaErrorLaunchFailure;      // refused for another reason: a capture, say\n"
+              # refused for another reason: a capture, say
+              "fake::malloc_result = cudaErrorLaunchFailure;"
               "if (p.ensure(200) != OLC_ERR_CUDA) return 1;"
               "if (p.memory != before || p.bytes != 100 || p.earlier) return 1;"
               "fake::malloc_result = cudaSuccess;"
