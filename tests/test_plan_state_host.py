@@ -20,7 +20,7 @@ def run(tmp_path, body):
     src.write_text('#include "plan_state.h"\nint main() {\n    olc::PlanState p;\n    p.init();\n%s\n    p.destroy();\n'
                    '    std::puts(fake::log.c_str());\n}\n' % body)
     exe = str(tmp_path / "t")
-    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", os.path.join(HERE, "fake_cuda"), "-I", CSRC, "-I", INCLUDE,
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-Wno-misleading-indentation", "-I", os.path.join(HERE, "fake_cuda"), "-I", CSRC, "-I", INCLUDE,
                     str(src), "-o", exe], check=True)
     return subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()
 
