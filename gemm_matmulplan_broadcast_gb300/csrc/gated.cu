@@ -904,31 +904,68 @@ struct olc_gated_plan {
     int64_t M, D, F;
     int act, trans_w;
     olc_matmul_plan* forward;    // FLOAT, few rows: X W
-    void* counters;              // FLOAT: arrivals at shared tiles
+    unsigned int* counters;      // FLOAT: arrivals at shared tiles, in the memory's first block
+    int reserved;
 };
 
 namespace {
 
-// The FLOAT counters, made with the plan (or, where no device was visible then,
-// at the first call) and zero before any stream goes on.  They are cleared on a
-// stream of their own: the legacy stream would wait for every other one, and
-// break a capture that one of them is in.
-olc_status float_counters(olc_gated_plan* p) {
-    if (p->counters) return OLC_OK;
-    const size_t bytes = gated::float_counter_bytes(p->state.sm_count);
-    void* counters = nullptr;
-    cudaError_t e = cudaMalloc(&counters, bytes);
-    if (e != cudaSuccess) return plan_status(e);
-    cudaStream_t own;
-    e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
-    if (e == cudaSuccess) {
-        e = cudaMemsetAsync(counters, 0, bytes, own);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(own);
-        cudaStreamDestroy(own);
+// FLOAT, few rows and weights [D, F]: the matrix plan's row kernels stream
+// each weight once, where a 64-row tile would multiply mostly nothing (us of
+// [rows, 1024] x [1024, 2816], device: 4 rows 15.8 against 30, 8 rows 31.7
+// against 30, 16 rows 90 against 30).
+constexpr int64_t kFewFloatRows = 4;
+bool few_float(const olc_gated_plan* p) { return p->M <= kFewFloatRows && !p->trans_w; }
+
+// The start of a FLOAT plan's memory holds the counters of its first block.
+size_t counter_room(const olc_gated_plan* p) {
+    return p->dtype == OLC_FLOAT ? gated::round256(gated::float_counter_bytes(p->state.sm_count)) : 0;
+}
+// of the plan's memory, what follows them
+unsigned char* memory_of(const olc_gated_plan* p) {
+    return p->state.memory ? static_cast<unsigned char*>(p->state.memory) + counter_room(p) : nullptr;
+}
+olc_status ensure(olc_gated_plan* p, size_t bytes) {
+    return bytes ? p->state.ensure(counter_room(p) + bytes) : OLC_OK;
+}
+
+// What every forward call needs, made with the plan (where no device was visible
+// then, at the first call): K slices or partial sums, and FLOAT's counters, zero
+// before any stream goes on.  They are cleared on a stream of their own: the
+// legacy stream would wait for every other one, and break a capture that one of
+// them is in.  What depends on the operands' alignment, and what the gradient
+// needs, comes with the first call that needs it: a plan may never see one.
+olc_status reserve(olc_gated_plan* p) {
+    if (p->reserved) return OLC_OK;
+    const int sms = p->state.sm_count;
+    size_t bytes = 0;
+    olc_status st = OLC_OK;
+    if (p->dtype != OLC_FLOAT) {
+        if (!gated::takes_few(p->M, p->F, sms)) bytes = gated::product_partial_bytes(gated::FWD, p->M, p->F, p->D, sms);
+        if (bytes) st = p->state.ensure(bytes);
+    } else {
+        if (few_float(p)) {
+            bytes = (size_t)(p->M * p->F) * sizeof(float);
+            const int64_t x[2] = {p->M, p->D}, w[2] = {p->D, p->F};
+            if (!p->forward) st = olc_matmul_plan_create(x, 2, w, 2, OLC_FLOAT, &p->forward);
+        } else {
+            bytes = gated::float_sum_bytes(gated::FWD, p->M, p->F, p->D, sms);
+        }
+        if (st == OLC_OK) st = p->state.ensure(counter_room(p) + bytes);
+        if (st == OLC_OK) {
+            cudaStream_t own;
+            cudaError_t e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+            if (e == cudaSuccess) {
+                e = cudaMemsetAsync(p->state.memory, 0, counter_room(p), own);
+                if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+                cudaStreamDestroy(own);
+            }
+            st = plan_status(e);
+        }
+        if (st == OLC_OK) p->counters = static_cast<unsigned int*>(p->state.memory);
     }
-    if (e == cudaSuccess) p->counters = counters;
-    else p->state.release(counters);
-    return plan_status(e);
+    if (st == OLC_OK) p->reserved = 1;
+    return st;
 }
 
 // One call's use of the plan's memory: pieces are taken in order, first to
@@ -1085,23 +1122,12 @@ olc_status backward16(olc_gated_plan* p, const void* dH, const void* X, const vo
     }));
 }
 
-// FLOAT, few rows and weights [D, F]: the matrix plan's row kernels stream
-// each weight once, where a 64-row tile would multiply mostly nothing (us of
-// [rows, 1024] x [1024, 2816], device: 4 rows 15.8 against 30, 8 rows 31.7
-// against 30, 16 rows 90 against 30).
-constexpr int64_t kFewFloatRows = 4;
 olc_status forward32_few(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                          cudaStream_t s) {
     olc_status st = OLC_OK;
-    if (!p->forward) {
-        const int64_t x[2] = {p->M, p->D}, w[2] = {p->D, p->F};
-        st = olc_matmul_plan_create(x, 2, w, 2, OLC_FLOAT, &p->forward);
-    }
     const int64_t n = p->M * p->F;
     // what is not kept: g in the plan's memory, u in H
-    if (st == OLC_OK && !G) st = p->state.ensure((size_t)n * sizeof(float));
-    if (st != OLC_OK) return st;
-    void* g = G ? G : p->state.memory;
+    void* g = G ? G : memory_of(p);
     void* u = U ? U : H;
     auto run = [&] {
         st = olc_matmul_execute(p->forward, X, Wg, g, s);
@@ -1117,11 +1143,8 @@ olc_status forward32_few(olc_gated_plan* p, const void* X, const void* Wg, const
 
 olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const void* Wu, void* H, void* G, void* U,
                      cudaStream_t s) {
-    if (p->M <= kFewFloatRows && !p->trans_w) return forward32_few(p, X, Wg, Wu, H, G, U, s);
+    if (few_float(p)) return forward32_few(p, X, Wg, Wu, H, G, U, s);
     const int sms = p->state.sm_count;
-    olc_status st = float_counters(p);
-    if (st == OLC_OK) st = p->state.ensure(gated::float_sum_bytes(gated::FWD, p->M, p->F, p->D, sms));
-    if (st != OLC_OK) return st;
     gated::Product w;
     std::memset(&w, 0, sizeof w);
     w.mode = gated::FWD;
@@ -1138,7 +1161,7 @@ olc_status forward32(olc_gated_plan* p, const void* X, const void* Wg, const voi
     w.Y[2] = U;
     w.act = p->act;
     return plan_status(p->state.use(s, [&] {         // the counters, if nothing else
-        return gated::launch_float(w, p->state.memory, static_cast<unsigned int*>(p->counters), sms, s);
+        return gated::launch_float(w, memory_of(p), p->counters, sms, s);
     }));
 }
 
@@ -1151,12 +1174,11 @@ olc_status backward32(olc_gated_plan* p, const void* dH, const void* X, const vo
     const size_t more = dWg ? gated::float_sum_bytes(gated::DW, wr, wc, p->M, sms) : 0;
     if (more > sums) sums = more;
     const size_t half = gated::round256((size_t)(p->M * pitch) * sizeof(float));
-    olc_status st = float_counters(p);
-    if (st == OLC_OK) st = p->state.ensure(2 * half + sums);
+    const olc_status st = ensure(p, 2 * half + sums);
     if (st != OLC_OK) return st;
-    unsigned char* memory = static_cast<unsigned char*>(p->state.memory);
+    unsigned char* memory = memory_of(p);
     void *dg = memory, *du = memory + half, *part = memory + 2 * half;
-    unsigned int* counters = static_cast<unsigned int*>(p->counters);
+    unsigned int* counters = p->counters;
     const gated::Stored sg{dg, p->M, p->F, pitch}, su{du, p->M, p->F, pitch}, sx{X, p->M, p->D, p->D};
     return plan_status(p->state.use(s, [&] {
         cudaError_t e = gated::launch_slope<float>(dH, G, U, dg, du, p->M, p->F, pitch, p->act, sms, s);
@@ -1219,8 +1241,8 @@ olc_status olc_gated_plan_create(int64_t rows, int64_t d_in, int64_t d_hidden, i
     p->F = d_hidden;
     p->act = activation;
     p->trans_w = trans_w ? 1 : 0;
-    if (dtype == OLC_FLOAT && p->state.device >= 0 && rows > 0 && d_in > 0 && d_hidden > 0) {
-        const olc_status st = float_counters(p);
+    if (p->state.device >= 0 && rows > 0 && d_in > 0 && d_hidden > 0) {
+        const olc_status st = reserve(p);
         if (st != OLC_OK) {
             olc_gated_plan_destroy(p);
             return st;
@@ -1233,7 +1255,6 @@ olc_status olc_gated_plan_create(int64_t rows, int64_t d_in, int64_t d_hidden, i
 void olc_gated_plan_destroy(olc_gated_plan* plan) {
     if (!plan) return;
     olc_matmul_plan_destroy(plan->forward);
-    plan->state.release(plan->counters);
     plan->state.destroy();
     delete plan;
 }
@@ -1256,6 +1277,8 @@ olc_status olc_gated_forward(olc_gated_plan* plan, const void* X, const void* Wg
             if (y && e == cudaSuccess) e = launch_zero_fill(y, p->M * p->F * eb, s);
         return plan_status(e);
     }
+    const olc_status ready = reserve(p);
+    if (ready != OLC_OK) return ready;
     return p->dtype == OLC_FLOAT ? forward32(p, X, Wg, Wu, H, G, U, s) : forward16(p, X, Wg, Wu, H, G, U, s);
 }
 
@@ -1281,6 +1304,8 @@ olc_status olc_gated_backward(olc_gated_plan* plan, const void* dH, const void* 
         if (dWg && e == cudaSuccess) e = launch_zero_fill(dWu, p->D * p->F * eb, s);
         return plan_status(e);
     }
+    const olc_status ready = reserve(p);
+    if (ready != OLC_OK) return ready;
     return p->dtype == OLC_FLOAT ? backward32(p, dH, X, Wg, Wu, G, U, dX, dWg, dWu, s)
                                  : backward16(p, dH, X, Wg, Wu, G, U, dX, dWg, dWu, s);
 }

@@ -468,7 +468,8 @@ typedef struct olc_gated_plan olc_gated_plan;
  * copied into the plan's memory.  FLOAT runs on the FMA pipes.
  * Extents of 0 are allowed (d_in = 0: g = u = 0).  Errors: OLC_ERR_NULL,
  * OLC_ERR_DTYPE, OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID (an extent of 2^31 -
- * 65536 or more, an unknown activation, more than 2^62 bytes), OLC_ERR_OOM.
+ * 65536 or more, an unknown activation, more than 2^62 bytes), OLC_ERR_OOM,
+ * OLC_ERR_CUDA.
  */
 olc_status olc_gated_plan_create(int64_t rows, int64_t d_in, int64_t d_hidden, int activation, int trans_w,
                                  olc_dtype dtype, olc_gated_plan** out);
@@ -480,11 +481,12 @@ void olc_gated_plan_destroy(olc_gated_plan* plan);
  * Forward.  G, U [rows, d_hidden]: the two products, rounded to the plan's
  * type, for the backward call; NULL for what is not kept (H is formed from
  * the unrounded products either way).  No output may overlap another tensor.
- * Operand copies, K slices and FLOAT's intermediate products and partial sums
- * live in device memory that the plan allocates at the first call that needs it
- * (a larger need later takes a new block; earlier ones stay until the plan is
- * destroyed, for graphs that captured them): make that call before any stream
- * capture.  Errors: OLC_ERR_NULL, OLC_ERR_INVALID,
+ * K slices and FLOAT's intermediate products and partial sums live in device
+ * memory that the plan allocates when it is made (or, made while no device was
+ * visible, at its first call).  Copies of operands come with the first call
+ * that needs them (a larger need takes a new block; earlier ones stay until the
+ * plan is destroyed, for graphs that captured them): make that one before any
+ * stream capture.  Errors: OLC_ERR_NULL, OLC_ERR_INVALID,
  * OLC_ERR_WRONG_DEVICE, OLC_ERR_OOM, OLC_ERR_CUDA.
  */
 olc_status olc_gated_forward(olc_gated_plan* plan, const void* X, const void* Wg, const void* Wu, void* H, void* G,
@@ -496,9 +498,11 @@ olc_status olc_gated_forward(olc_gated_plan* plan, const void* X, const void* Wg
  *     dX = dg Wg' + du Wu',  dWg = X' dg,  dWu = X' du  (stored as the weights).
  * dX NULL skips it; dWg and dWu are both given or both NULL.  dg and du are
  * kept in the plan's memory (2 x rows x d_hidden elements) and, for FLOAT16 /
- * BFLOAT16, rounded to the type, which the tensor cores read; all sums are
- * float32, in an order that depends on the sizes and the device alone.
- * Errors: as forward.
+ * BFLOAT16, rounded to the type, which the tensor cores read (FLOAT16: beyond
+ * 65504 they are infinite and below 2^-14 lose bits, so the loss is scaled as
+ * for any FLOAT16 gradient); all sums are float32, in an order that depends on
+ * the sizes and the device alone.  The memory comes with the first call: make
+ * it before any stream capture.  Errors: as forward.
  */
 olc_status olc_gated_backward(olc_gated_plan* plan, const void* dH, const void* X, const void* Wg, const void* Wu,
                               const void* G, const void* U, void* dX, void* dWg, void* dWu, void* stream);
