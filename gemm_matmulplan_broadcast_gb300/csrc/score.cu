@@ -105,18 +105,15 @@ constexpr float kLn2 = 0.69314718055994531f;
 // lowest value alike.
 constexpr float kFar = -1.0e4f;
 
+// the exponential unit, good to 2^-22 of the result
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
-// For probabilities that are results themselves: FLOAT keeps those below 2^-126
-// (log p, some -90 there, lifts their gradient back into the normal range);
-// 16-bit gradients let them go, and the instructions with them.
-template <typename T>
-__device__ __forceinline__ float probability(float x) {
-    if constexpr (sizeof(T) < 4) return exp2_fast(x);
+// the same without the flush of results below 2^-126
+__device__ __forceinline__ float exp2_small(float x) {
     float r;
     asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
@@ -881,8 +878,11 @@ __global__ void __launch_bounds__(kBlockThreads, kBlocksPerSm) forward_kernel(co
 }
 
 // One block takes a stretch of a row.  Every element is read and written by
-// the same thread, so dlogits may be the logits.  With c = dlogprob + dH (H -
-// lse), dz = -p (c + dH z), and dlogprob more at the token.
+// the same thread, so dlogits may be the logits.  With log p = z - lse and c =
+// dlogprob + dH H, dz = -p (c + dH log p), and dlogprob more at the token: lse is
+// subtracted first, so that errors are of the size of log p and not of lse.  p is
+// formed 2^24 times too large and the bracket as much too small: log p, some -90
+// where p passes 2^-126, lifts such gradients back into the normal range.
 template <typename T>
 __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     constexpr int V = 16 / sizeof(T);
@@ -905,10 +905,10 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     const float dh = p.dentropy ? p.dentropy[row] : 0.f;
     const float h = p.dentropy ? p.entropy[row] : 0.f;
     const bool nothing = lse == -INFINITY;
-    const float shift = -lse * kLog2e, c = fmaf(dh, h - lse, dlp);
+    const float c = fmaf(dh, h, dlp);
     auto grad = [&](float v, int i) -> float {           // any values
         if (nothing) return 0.f;
-        const float logp = v - lse, q = probability<T>(logp * kLog2e);
+        const float logp = v - lse, q = exp2_small(logp * kLog2e);
         // a probability of zero contributes nothing, whatever its logarithm
         float g = q == 0.f && dlp == dlp ? 0.f : -q * fmaf(dh, logp + h, dlp);
         if (i == token) g += dlp;
@@ -916,10 +916,13 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
     };
     if (t < s.head) d[t] = Num<T>::from_acc(grad(Num<T>::to_acc(z[t]), t));
     const bool same = ((reinterpret_cast<uintptr_t>(d) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-    const bool quick = near_zero(lse) && same;
+    constexpr float LARGER = 16777216.f, LEAST = 0x1p-100f;      // (brackets that 2^-24 leaves all their digits)
+    const bool digits = (fabsf(c) >= LEAST || c == 0.f) && (fabsf(dh) >= LEAST || dh == 0.f);
+    const bool quick = near_zero(lse) && same && (digits || c != c);
     const uint32_t low = floor_of<T>(quick ? lse : 0.f);
-    const F2 scale2 = pack_f2(kLog2e, kLog2e), shift2 = pack_f2(shift, shift), c2 = pack_f2(-c, -c),
-             dh2 = pack_f2(-dh, -dh);
+    const float c_less = -c / LARGER, dh_less = -dh / LARGER;
+    const F2 scale2 = pack_f2(kLog2e, kLog2e), larger2 = pack_f2(24.f, 24.f), minus_lse2 = pack_f2(-lse, -lse),
+             c2 = pack_f2(c_less, c_less), dh2 = pack_f2(dh_less, dh_less);
 #pragma unroll
     for (int pack = 0; pack < kGradPacks; ++pack) {
         const int v = s.v0 + t + pack * 256;
@@ -932,10 +935,10 @@ __global__ void __launch_bounds__(256) backward_kernel(const GradParams p) {
             F2 g[V / 2];
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
-                const F2 x = pair_of<T>(w, j);
+                const F2 logp = add2(pair_of<T>(w, j), minus_lse2);
                 float lo, hi;
-                unpack_f2(fma2(x, scale2, shift2), lo, hi);
-                g[j] = mul2(pack_f2(probability<T>(lo), probability<T>(hi)), fma2(x, dh2, c2));
+                unpack_f2(fma2(logp, scale2, larger2), lo, hi);
+                g[j] = mul2(pack_f2(exp2_fast(lo), exp2_fast(hi)), fma2(logp, dh2, c2));
             }
             if ((unsigned)(token - at) < (unsigned)V) {
 #pragma unroll

@@ -126,3 +126,33 @@ def test_log_probabilities_do_not_depend_on_an_offset(rows, vocab, shift, dtype)
     with TokenLogProbsPlan(rows, vocab, dtype) as plan:         # a gradient's entries add up to nothing
         plan.backward(z.cuda(), tokens.cuda(), lse.float().cuda(), None, one, d)
     assert float(d.double().sum(-1).abs().max()) <= 2.0 ** -7 * 2 + 4 * F32 * abs(shift) * 2
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shift", [0.0, 50.0, 300.0, -2000.0])
+@pytest.mark.parametrize("rows,vocab", [(107, 18), (24, 880), (11, 16468), (3, 57298)])
+def test_backward_of_peaked_rows_with_an_offset(rows, vocab, shift, dtype):
+    # one token near certain, the rest down to the smallest probabilities: errors of log p's size, not of lse's
+    z = normal((rows, vocab), dtype, 81, 20.0, shift)
+    check_backward(rows, vocab, dtype, z=z)
+    check_backward(rows, vocab, dtype, z=z, with_lp=False)
+    check_backward(rows, vocab, dtype, z=z, offset=3, d_offset=1)
+
+
+def test_backward_of_tiny_gradients():
+    # dlogprob and dentropy near float32's smallest values keep their digits
+    rows, vocab = 4, 500
+    z = normal((rows, vocab), "float32", 82, 3.0)
+    tokens = tokens_of(rows, vocab, 83).cuda()
+    lse, entropy = (v.float().cuda() for v in (lambda r: (r[2], r[1]))(reference(z, tokens.cpu(), 0)))
+    d, e = (torch.empty(rows, vocab, device="cuda") for _ in range(2))
+    dlp, dh = normal((rows,), "float32", 84).cuda(), normal((rows,), "float32", 85).cuda()
+    small = 2.0 ** -104
+    with TokenLogProbsPlan(rows, vocab, "float32") as plan:
+        plan.backward(z.cuda(), tokens, lse, entropy, dlp, d, dentropy=dh)
+        plan.backward(z.cuda(), tokens, lse, entropy, dlp * small, e, dentropy=dh * small)
+    # a few roundings of each term: p is off by 2^-21 + |log p| 2^-23 of itself, the bracket's terms by as much
+    terms = (dlp.abs() + dh.abs() * 40)[:, None].double()
+    assert ((e.double() / small - d.double()).abs() <= 2.0 ** -18 * terms).all()
+    big = d.abs() > 2.0 ** -12
+    assert ((e.double() / small / d.double())[big] - 1).abs().max() <= 2.0 ** -8 and int(big.sum()) > 100
