@@ -1061,6 +1061,7 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
         b.blocks = max64(1, min64(ceil_div(rows, kLeastRows * b.groups), (int64_t)sm_count * (b.tpr > 256 ? 2 : 1)));
         return b;
     }
+    // packs: fewer than kRingCols columns, so four (FLOAT) or eight a thread
     b.kind = BwdShape::ANY;
     const int least = V == 1 ? 2 : V;            // columns of a pack, or of a pair of single elements
     b.per_thread = least;
@@ -1117,13 +1118,13 @@ cudaError_t backward_as(BwdParams p, int sm_count, T* dgamma, T* dbeta, cudaStre
             else
                 e = full ? backward_ring<T, 16, true>(p, b, s) : backward_ring<T, 16, false>(p, b, s);
         }
-    } else if (b.per_thread == 16) {
-        e = backward_rows<T, V, V == 1 ? 8 : 16 / V>(p, b, s);
     } else if (b.per_thread == 8) {
         e = backward_rows<T, V, V == 1 ? 4 : 8 / V>(p, b, s);
-    } else if constexpr (V <= 4) {
-        if (b.per_thread == 4) e = backward_rows<T, V, V == 1 ? 2 : 1>(p, b, s);
-        else if constexpr (V == 1) e = backward_rows<T, 1, 1>(p, b, s);
+    } else if constexpr (V == 1) {
+        e = b.per_thread == 16 ? backward_rows<T, 1, 8>(p, b, s)
+                               : (b.per_thread == 4 ? backward_rows<T, 1, 2>(p, b, s) : backward_rows<T, 1, 1>(p, b, s));
+    } else if constexpr (V == 4) {
+        e = backward_rows<T, 4, 1>(p, b, s);
     }
     if (e == cudaSuccess && p.partial) {
         auto run = [&](auto kernel, int c) {
