@@ -11,11 +11,11 @@
 // bytes bound it.  Each row is read once and stays in registers, so that the
 // variance is the sum of squared distances from the finished mean (no
 // cancellation for rows far from zero, whose mean is corrected by the sum of the
-// distances as well); rows too long for the registers are
-// read again, mostly from L2.  All sums and statistics are float32; y, dx,
-// dgamma and dbeta are rounded to the element type once.  Measured, BF16 [16384,
-// 4096]: forward 43.7 us (6.1 TB/s, a plain copy of the tensor 41 to 43.5),
-// backward 66.6 us (6.0 TB/s) with the column sums' 4 us.
+// distances as well); rows too long for the registers are read again, mostly
+// from L2.  All sums and statistics are float32; y, dx, dgamma and dbeta are
+// rounded to the element type once.  Measured, BF16 [16384, 4096]: forward 44.3 us
+// (6.1 TB/s, a plain copy of the tensor 41 to 43.5), backward 66.5 us (6.1 TB/s)
+// with the column sums' 4 us.
 #include <new>
 #include <type_traits>
 

@@ -31,9 +31,11 @@ inline bool plan_fits(int64_t a, int64_t b, int64_t bytes) {
 #ifdef __CUDACC__
 // A launch in full stream order.  The kernels of these plans neither start
 // before their predecessor has ended nor let a successor start early
-// (programmatic dependent launch): blocks that start early and wait hold
-// places on the SMs, and where kernels of many small blocks did so around
-// clusters that needed whole pairs of SMs, a stream came to a standstill.
+// (programmatic dependent launch).  An earlier form of them did, and under a
+// stress of the gated product's gradient its stream once stood still.  Which
+// part did it was not shown: roles that met .aligned barriers with their warps
+// apart were mended in the same days, and a dependent grid's blocks are only
+// placed when all of its predecessor's are.  Full order needs no such answer.
 template <typename... KArgs, typename... Args>
 inline cudaError_t plan_launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                                Args&&... args) {

@@ -433,13 +433,14 @@ olc_status olc_layer_norm_forward(olc_layer_norm_plan* plan, const void* X, int6
  * Backward: with xh = (x - mean) rstd and dxh = dy gamma,
  *     dx = rstd (dxh - mean_j(dxh) - xh mean_j(dxh xh)),
  *     dgamma = sum over rows of dy xh,   dbeta = sum over rows of dy.
- * mean, rstd: the forward call's.  dX [rows, cols] (may be dY or X itself),
- * dgamma, dbeta [cols]: NULL to skip any of them.  The column sums are
- * float32 and are formed in an order that depends on the sizes and the
- * device alone, so that results repeat bit for bit; with rows == 0 they are
- * zeros.  The first call with dgamma or dbeta allocates the partial sums
- * (cudaMalloc, kept by the plan): make it before any stream capture.
- * Errors: as forward, and OLC_ERR_OOM.
+ * mean, rstd: the forward call's.  dX [rows, cols] (may be dY or X itself:
+ * same pointer and pitch), dgamma, dbeta [cols]: NULL to skip any of them.
+ * The column sums are float32 and are formed in an order that depends on the
+ * sizes, on whether rows lie on 16-byte boundaries and on the device alone,
+ * so that results repeat bit for bit; with rows == 0 they are zeros.  The
+ * first call with dgamma or dbeta allocates the partial sums (cudaMalloc, kept
+ * by the plan): make it before any stream capture.  Errors: as forward, and
+ * OLC_ERR_OOM.
  */
 olc_status olc_layer_norm_backward(olc_layer_norm_plan* plan, const void* dY, int64_t dy_pitch, const void* X,
                                    int64_t x_pitch, const void* gamma, const float* mean, const float* rstd, void* dX,
@@ -520,7 +521,9 @@ typedef struct olc_token_log_probs_plan olc_token_log_probs_plan;
  *     entropy = -sum_j p_j log p_j  with p_j = e^(z_j - lse),
  * and the `top` largest logits as log probabilities z_j - lse with their
  * indices, in descending order, equal values by the lower index.
- * Masked logits may be -inf or the type's lowest value.  A row of nothing but
+ * Masked logits may be -inf or any finite value, alone in a row too.  Log
+ * probabilities are formed as (z_j - max) - log sum, so that an offset of the
+ * row costs them nothing; exponentials are good to 2^-22 of themselves.  A row of nothing but
  * -inf gives lse = logprob = top_logprob = -inf and entropy 0, and a zero
  * gradient.  A negative token marks a row to ignore: its logprob is 0 and has
  * no gradient.  A token of vocab or more gives NaN (logprob, and the row's
