@@ -9,8 +9,9 @@ raises (build with ``python -m gemm_matmulplan_broadcast_gb300.build``).
 
 from .binding import ALGORITHMS, GemmPlan, GroupedPlan, OlcError, Plan, gemm, load, matmul  # noqa: F401
 
-from .layers import (GatedPlan, LayerNormPlan, TokenLogProbsPlan, gated, layer_norm,  # noqa: F401
-                     token_log_probs)
+from .layers import (EmbeddingPlan, GatedPlan, LayerNormPlan, ResidualNormPlan, SamplePlan,  # noqa: F401
+                     TokenLogProbsPlan, embedding, gated, layer_norm, residual_norm, sample, token_log_probs)
 
 __all__ = ["Plan", "GemmPlan", "GroupedPlan", "LayerNormPlan", "GatedPlan", "TokenLogProbsPlan",
-           "matmul", "layer_norm", "gated", "token_log_probs", "gemm", "load", "OlcError", "ALGORITHMS"]
+           "EmbeddingPlan", "ResidualNormPlan", "SamplePlan", "matmul", "layer_norm", "gated", "token_log_probs",
+           "embedding", "residual_norm", "sample", "gemm", "load", "OlcError", "ALGORITHMS"]

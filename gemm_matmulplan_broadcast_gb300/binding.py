@@ -37,6 +37,7 @@ STATUS = {
     16: "OLC_ERR_NEEDS_RESIDUAL",
 }
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2}
+NORMS = {"layer": 0, "rms": 1}
 GATES = {"silu": 0, "gelu": 1, "relu": 2, "sigmoid": 3}
 MAX_RANK = 8
 
@@ -131,6 +132,21 @@ def load():
             "olc_token_log_probs_plan_destroy": ([vp], None),
             "olc_token_log_probs_forward": ([vp, vp, i64, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
             "olc_token_log_probs_backward": ([vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp], ctypes.c_int),
+            "olc_embedding_plan_create": ([i64, i64, i64, ctypes.c_double, ctypes.c_int, ctypes.POINTER(vp)],
+                                          ctypes.c_int),
+            "olc_embedding_plan_destroy": ([vp], None),
+            "olc_embedding_forward": ([vp, vp, i64, vp, vp, i64, vp], ctypes.c_int),
+            "olc_embedding_backward": ([vp, vp, i64, vp, vp, i64, ctypes.c_int, vp], ctypes.c_int),
+            "olc_residual_norm_plan_create": ([i64, i64, ctypes.c_double, ctypes.c_double, ctypes.c_int, ctypes.c_int,
+                                               ctypes.c_int, ctypes.POINTER(vp)], ctypes.c_int),
+            "olc_residual_norm_plan_destroy": ([vp], None),
+            "olc_residual_norm_forward": ([vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp],
+                                          ctypes.c_int),
+            "olc_residual_norm_backward": ([vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, vp, vp, vp, i64, vp,
+                                            i64, vp, i64, vp, vp, vp, vp, vp], ctypes.c_int),
+            "olc_sample_plan_create": ([i64, i64, ctypes.c_int, ctypes.POINTER(vp)], ctypes.c_int),
+            "olc_sample_plan_destroy": ([vp], None),
+            "olc_sample_forward": ([vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
             "olc_layer_norm_plan_create": ([i64, i64, ctypes.c_double, ctypes.c_int,
                                             ctypes.POINTER(vp)], ctypes.c_int),
             "olc_layer_norm_plan_destroy": ([vp], None),

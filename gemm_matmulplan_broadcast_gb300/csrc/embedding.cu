@@ -1,0 +1,547 @@
+// Rows of a table by token id, scaled, and the table's gradient.
+//
+//   y_i = s E[t_i]                       (t_i < 0: zeros, a place without a token)
+//   dE_v = s sum_{i: t_i = v} dy_i       (zeros, or what is there, for tokens that do not occur)
+//
+// One multiplication an element moved: the bytes bound both directions.
+//
+// Backward.  Sums in an order that does not change from run to run need the
+// places of each token together and in order: a stable counting sort by token
+// (sort_kernel, one launch: a block owns a range of the vocabulary and reads all
+// ids).  The sums then go over chunks of equal length of the sorted places, so that a
+// token that fills half of the batch costs no block more than any other
+// (sum_kernel); a token whose places cross chunks leaves partial sums that
+// join_kernel adds in chunk order.  The rows of tokens that do not occur are
+// cleared by further blocks of sum_kernel while its chunks are summed.
+#include <new>
+
+#include "plan_state.h"
+#include "row_packs.cuh"
+
+namespace olc {
+namespace embedding {
+
+constexpr int kThreads = 256;
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kMaxBins = 1536;          // tokens of a sort block: a counter for each and each warp, 202 KB
+constexpr int kClearRows = 8;           // rows a group of threads clears
+constexpr int kJoinChunks = 8;          // chunks whose ends a join block looks at
+
+struct Tile {
+    int log_tx;             // threads on a row: 1 << log_tx; the block's others take further rows
+    int64_t packs;          // of a row
+    int64_t col_tiles;
+};
+
+struct FwdParams {
+    const void* table;
+    const int64_t* tokens;
+    void* Y;
+    int64_t table_pitch, y_pitch;
+    int64_t n, vocab;
+    float scale;
+    Tile tile;
+    int64_t units;
+};
+
+// What the sort leaves: the places of all tokens, sorted by token and place.
+struct Sorted {
+    int* start;             // [vocab + 1]: where each token's places begin
+    int* place;             // [n]
+    int* token;             // [n]
+};
+
+struct BwdParams {
+    const void* dY;
+    void* dE;
+    float* partial;         // [chunks][2][cols]: of the run that began before the chunk, of the one that goes on after it
+    int64_t dy_pitch, e_pitch;
+    int64_t vocab, cols;
+    float scale;
+    int accumulate;
+    int length;             // places of a chunk, a multiple of 4
+    int64_t chunks;
+    Sorted s;
+    Tile tile;
+    int64_t sum_units, units;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void fill(T* to, float v) {
+    F2 o[pairs<V>()];
+#pragma unroll
+    for (int q = 0; q < pairs<V>(); ++q) o[q] = both(v);
+    store<T, V>(to, o);
+}
+
+// PK packs a thread, all of them on their way at once
+template <typename T, int V, int PK>
+__global__ void __launch_bounds__(kThreads) forward_kernel(const FwdParams p) {
+    const int tx = threadIdx.x & ((1 << p.tile.log_tx) - 1), ty = threadIdx.x >> p.tile.log_tx;
+    const int rows = kThreads >> p.tile.log_tx;
+    for (int64_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
+        const int64_t row_tile = unit / p.tile.col_tiles;
+        const int64_t row = row_tile * rows + ty;
+        const int64_t first = ((unit - row_tile * p.tile.col_tiles) * PK << p.tile.log_tx) + tx;
+        if (row >= p.n) continue;
+        const int64_t token = p.tokens[row];
+        T* y = static_cast<T*>(p.Y) + row * p.y_pitch;
+        if (token < 0 || token >= p.vocab) {
+#pragma unroll
+            for (int i = 0; i < PK; ++i) {
+                const int64_t c = first + ((int64_t)i << p.tile.log_tx);
+                if (c < p.tile.packs) fill<T, V>(y + c * V, token < 0 ? 0.f : __uint_as_float(0x7FC00000u));
+            }
+            continue;
+        }
+        const T* e = static_cast<const T*>(p.table) + token * p.table_pitch;
+        Pack<T, V> k[PK];
+#pragma unroll
+        for (int i = 0; i < PK; ++i) {
+            const int64_t c = first + ((int64_t)i << p.tile.log_tx);
+            if (c < p.tile.packs) k[i] = load<T, V>(e + c * V);
+        }
+#pragma unroll
+        for (int i = 0; i < PK; ++i) {
+            const int64_t c = first + ((int64_t)i << p.tile.log_tx);
+            if (c >= p.tile.packs) continue;
+            F2 v[pairs<V>()];
+            widen<T, V>(v, k[i]);
+#pragma unroll
+            for (int q = 0; q < pairs<V>(); ++q) v[q] = mul2(v[q], both(p.scale));
+            store<T, V>(y + c * V, v);
+        }
+    }
+}
+
+// A block sorts the places of the tokens [bins blockIdx.x, ...): each warp
+// counts its own stretch of the ids by token, a scan over warps and tokens turns
+// the counts into positions, and the warps go over their stretches again.  Within
+// 32 ids the lanes with the same token take consecutive positions.
+// [16384 ids, 50257 tokens]: each block reads the 128 KB of ids twice, from L2.
+__global__ void __launch_bounds__(kSortThreads)
+sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, Sorted s) {
+    extern __shared__ int counts[];                 // [kSortWarps][bins]
+    __shared__ int scan[kSortWarps + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t v0 = (int64_t)blockIdx.x * bins;
+    const int own = (int)min64(bins, vocab - v0);   // at least 1
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0;
+    __syncthreads();
+    const int stretch = (int)(ceil_div(ceil_div(n, kSortWarps), 32) * 32);      // at most n + 31
+    const int64_t begin = min64((int64_t)warp * stretch, n), end = min64(begin + stretch, n);
+    int* const mine = counts + warp * bins;
+    // four groups of 32 ids at a time; -1 past the end and for ids that are no tokens
+    auto read = [&](int64_t base, int64_t (&t)[4]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = base + u * 32 + lane;
+            t[u] = i < end ? tokens[i] : -1;
+            if (t[u] >= vocab) t[u] = -1;
+        }
+    };
+    int below = 0;
+    for (int64_t base = begin; base < end; base += 128) {
+        int64_t t[4];
+        read(base, t);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            below += t[u] >= 0 && t[u] < v0;
+            if (t[u] >= v0 && t[u] < v0 + own) atomicAdd(&mine[(int)(t[u] - v0)], 1);
+        }
+    }
+    below = __reduce_add_sync(0xffffffffu, below);
+    if (lane == 0) scan[warp] = below;
+    __syncthreads();
+    int position = 0;                               // where the block's first place goes
+    for (int w = 0; w < kSortWarps; ++w) position += scan[w];
+    __syncthreads();
+    // a thread's consecutive tokens: over the warps, then over the tokens
+    constexpr int PER = (kMaxBins + kSortThreads - 1) / kSortThreads;
+    int total[PER], sum = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int b = threadIdx.x * PER + j;
+        total[j] = 0;
+        if (b < own)
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int c = counts[w * bins + b];
+                counts[w * bins + b] = total[j];
+                total[j] += c;
+            }
+        sum += total[j];
+    }
+    int before = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += o;
+    }
+    if (lane == 31) scan[warp] = before;
+    __syncthreads();
+    before -= sum;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+    position += before;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int b = threadIdx.x * PER + j;
+        if (b >= own) continue;
+        s.start[v0 + b] = position;
+        for (int w = 0; w < kSortWarps; ++w) counts[w * bins + b] += position;
+        position += total[j];
+        if (v0 + b == vocab - 1) s.start[vocab] = position;
+    }
+    __syncthreads();
+    for (int64_t base = begin; base < end; base += 128) {
+        int64_t t[4];
+        read(base, t);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int b = t[u] >= v0 && t[u] < v0 + own ? (int)(t[u] - v0) : -1;
+            if (!__any_sync(0xffffffffu, b >= 0)) continue;
+            const unsigned same = __match_any_sync(0xffffffffu, b);
+            int at = 0;
+            if (b >= 0) at = mine[b] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (b >= 0) {
+                s.place[at] = (int)(base + u * 32 + lane);
+                s.token[at] = (int)t[u];
+                if ((same >> lane) == 1u) mine[b] = at + 1;         // the last of them
+            }
+            __syncwarp();
+        }
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void add_pack(F2 (&acc)[pairs<V>()], const Pack<T, V>& k) {
+    F2 v[pairs<V>()];
+    widen<T, V>(v, k);
+#pragma unroll
+    for (int q = 0; q < pairs<V>(); ++q) acc[q] = add2(acc[q], v[q]);
+}
+
+// float32 partial sums of V columns
+template <int V>
+__device__ __forceinline__ void put_partial(float* to, const F2 (&acc)[pairs<V>()]) {
+    if constexpr (V == 1) {
+        float lo, hi;
+        unpack_f2(acc[0], lo, hi);
+        *to = lo;
+    } else {
+#pragma unroll
+        for (int q = 0; q < V / 2; q += 2) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(acc[q], acc[q + 1]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void add_partial(F2 (&acc)[pairs<V>()], const float* from) {
+    if constexpr (V == 1) {
+        acc[0] = add2(acc[0], pack_f2(*from, 0.f));
+    } else {
+#pragma unroll
+        for (int q = 0; q < V / 2; q += 2) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(from + 2 * q);
+            acc[q] = add2(acc[q], v.x);
+            acc[q + 1] = add2(acc[q + 1], v.y);
+        }
+    }
+}
+
+// a token's finished sum
+template <typename T, int V>
+__device__ __forceinline__ void finish(const BwdParams& p, int64_t token, int64_t c, F2 (&acc)[pairs<V>()]) {
+    T* to = static_cast<T*>(p.dE) + token * p.e_pitch + c;
+    if (p.accumulate) {
+        F2 old[pairs<V>()];
+        widen<T, V>(old, load<T, V>(to));
+#pragma unroll
+        for (int q = 0; q < pairs<V>(); ++q) acc[q] = fma2(acc[q], both(p.scale), old[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < pairs<V>(); ++q) acc[q] = mul2(acc[q], both(p.scale));
+    }
+    store<T, V>(to, acc);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) sum_kernel(const BwdParams p) {
+    const int tx = threadIdx.x & ((1 << p.tile.log_tx) - 1), ty = threadIdx.x >> p.tile.log_tx;
+    const int groups = kThreads >> p.tile.log_tx;
+    const T* dY = static_cast<const T*>(p.dY);
+    for (int64_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
+        const bool sums = unit < p.sum_units;
+        const int64_t u = sums ? unit : unit - p.sum_units;
+        const int64_t group = u / p.tile.col_tiles * groups + ty;
+        const int64_t pack = ((u % p.tile.col_tiles) << p.tile.log_tx) + tx;
+        if (pack >= p.tile.packs) continue;
+        const int64_t c = pack * V;
+        if (!sums) {
+            const int64_t v0 = group * kClearRows;
+            if (v0 >= p.vocab) continue;
+            int starts[kClearRows + 1];
+#pragma unroll
+            for (int i = 0; i <= kClearRows; ++i) starts[i] = p.s.start[min64(v0 + i, p.vocab)];
+#pragma unroll
+            for (int i = 0; i < kClearRows; ++i)
+                if (v0 + i < p.vocab && starts[i] == starts[i + 1])
+                    fill<T, V>(static_cast<T*>(p.dE) + (v0 + i) * p.e_pitch + c, 0.f);
+            continue;
+        }
+        const int64_t n = p.s.start[p.vocab], p0 = group * p.length, p1 = min64(p0 + p.length, n);
+        if (p0 >= n) continue;
+        F2 acc[pairs<V>()];
+        auto clear = [&] {
+#pragma unroll
+            for (int q = 0; q < pairs<V>(); ++q) acc[q] = both(0.f);
+        };
+        clear();
+        int current = p.s.token[p0];
+        auto leave = [&] {
+            const int begin = p.s.start[current], end = p.s.start[current + 1];
+            if (begin >= p0 && end <= p1) finish<T, V>(p, current, c, acc);
+            else put_partial<V>(p.partial + (group * 2 + (begin >= p0)) * p.cols + c, acc);
+        };
+        for (int64_t at = p0; at < p1; at += 4) {
+            // (the arrays' lengths are multiples of 4; what lies past the last place is not used)
+            const int4 token = *reinterpret_cast<const int4*>(p.s.token + at);
+            const int4 place = *reinterpret_cast<const int4*>(p.s.place + at);
+            const int tokens[4] = {token.x, token.y, token.z, token.w}, places[4] = {place.x, place.y, place.z, place.w};
+            Pack<T, V> k[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (at + j < p1) k[j] = load<T, V>(dY + (int64_t)places[j] * p.dy_pitch + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (at + j >= p1) break;
+                if (tokens[j] != current) {
+                    leave();
+                    clear();
+                    current = tokens[j];
+                }
+                add_pack<T, V>(acc, k[j]);
+            }
+        }
+        leave();
+    }
+}
+
+// Tokens whose places cross a chunk's end: the partial sums of the chunk in which
+// they begin and of those after it, in order.  `groups` groups of threads take
+// every groups-th of them each and are added in group order.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) join_kernel(const BwdParams p) {
+    constexpr int LOG_TX = 7, GROUPS = kThreads >> LOG_TX;
+    __shared__ int found[kJoinChunks];
+    __shared__ alignas(16) float sums[GROUPS - 1][1 << LOG_TX][V];
+    const int tx = threadIdx.x & ((1 << LOG_TX) - 1), group = threadIdx.x >> LOG_TX;
+    const int64_t tiles = ceil_div(p.tile.packs, 1 << LOG_TX);
+    for (int64_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
+        const int64_t c0 = unit / tiles * kJoinChunks;
+        const int64_t pack = (unit % tiles << LOG_TX) + tx;
+        if (threadIdx.x < kJoinChunks) {
+            const int64_t chunk = c0 + threadIdx.x, next = (chunk + 1) * p.length;
+            int token = -1;
+            if (next < p.s.start[p.vocab]) {
+                const int t = p.s.token[next - 1];
+                if (p.s.start[t] >= next - p.length && p.s.start[t + 1] > next) token = t;
+            }
+            found[threadIdx.x] = token;
+        }
+        __syncthreads();
+        for (int i = 0; i < kJoinChunks; ++i) {
+            const int token = found[i];
+            if (token < 0) continue;                        // the whole block
+            const int64_t chunk = c0 + i, last = (p.s.start[token + 1] - 1) / p.length;
+            const bool in = pack < p.tile.packs;
+            const int64_t c = pack * V;
+            F2 acc[pairs<V>()];
+#pragma unroll
+            for (int q = 0; q < pairs<V>(); ++q) acc[q] = both(0.f);
+            if (in) {
+                if (group == 0) add_partial<V>(acc, p.partial + (chunk * 2 + 1) * p.cols + c);
+#pragma unroll 4
+                for (int64_t k = chunk + 1 + group; k <= last; k += GROUPS) add_partial<V>(acc, p.partial + k * 2 * p.cols + c);
+                if (group > 0) put_partial<V>(&sums[group - 1][tx][0], acc);
+            }
+            __syncthreads();
+            if (in && group == 0) {
+                for (int g = 1; g < GROUPS; ++g) add_partial<V>(acc, &sums[g - 1][tx][0]);
+                finish<T, V>(p, token, c, acc);
+            }
+            __syncthreads();
+        }
+        __syncthreads();
+    }
+}
+
+// ---- host side -------------------------------------------------------------
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+// 2^log threads on a row of `packs`, `each` packs a thread, at most a block
+inline Tile tile_of(int64_t packs, int each) {
+    int log = 0;
+    while ((1 << log) < kThreads && ((int64_t)each << log) < packs) ++log;
+    return Tile{log, packs, ceil_div(packs, (int64_t)each << log)};
+}
+
+inline dim3 grid_of(int64_t units) { return dim3((unsigned)min64(units, kMaxGrid)); }
+
+// Four packs a thread where that still leaves each SM several blocks; else one.
+template <typename T, int V>
+cudaError_t forward_as(FwdParams p, int64_t cols, int sm_count, cudaStream_t s) {
+    const int64_t packs = cols / V;
+    auto run = [&](auto kernel, int each) {
+        p.tile = tile_of(packs, each);
+        p.units = ceil_div(p.n, kThreads >> p.tile.log_tx) * p.tile.col_tiles;
+        return plan_launch(kernel, grid_of(p.units), dim3(kThreads), 0, s, p);
+    };
+    return p.n * packs >= (int64_t)sm_count * 4 * kThreads * 4 ? run(forward_kernel<T, V, 4>, 4)
+                                                               : run(forward_kernel<T, V, 1>, 1);
+}
+
+// Places of a chunk: 32 where that leaves four blocks an SM, fewer for fewer
+// places, at least 4.
+inline int chunk_length(int64_t n, int64_t cols, int64_t bytes, int sm_count) {
+    const int64_t threads = n * ceil_div(cols * bytes, 16);     // one place each
+    int length = 32;
+    while (length > 4 && threads / length < (int64_t)sm_count * 4 * kThreads) length /= 2;
+    return length;
+}
+
+inline int sort_bins(int64_t vocab, int sm_count) { return (int)min64(kMaxBins, ceil_div(vocab, sm_count)); }
+
+struct Layout {
+    size_t place, token, partial, bytes;
+};
+inline Layout layout_of(int64_t n, int64_t vocab, int64_t cols, int64_t chunks) {
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    Layout l;
+    l.place = up((size_t)(vocab + 1) * 4);
+    l.token = l.place + up((size_t)n * 4);
+    l.partial = l.token + up((size_t)n * 4);
+    l.bytes = l.partial + (size_t)chunks * 2 * (size_t)cols * 4;
+    return l;
+}
+
+template <typename T, int V>
+cudaError_t backward_as(BwdParams p, const int64_t* tokens, int64_t n, int sm_count, cudaStream_t s) {
+    const int bins = sort_bins(p.vocab, sm_count);
+    const size_t smem = (size_t)kSortWarps * bins * 4;
+    cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(sort_kernel), kSortWarps * kMaxBins * 4);
+    if (e == cudaSuccess)
+        e = plan_launch(sort_kernel, dim3((unsigned)ceil_div(p.vocab, bins)), dim3(kSortThreads), smem, s, tokens, (int)n,
+                        p.vocab, bins, p.s);
+    if (e != cudaSuccess) return e;
+    p.tile = tile_of(p.cols / V, 1);
+    const int groups = kThreads >> p.tile.log_tx;
+    p.sum_units = ceil_div(p.chunks, groups) * p.tile.col_tiles;
+    p.units = p.sum_units + (p.accumulate ? 0 : ceil_div(p.vocab, groups * kClearRows) * p.tile.col_tiles);
+    e = plan_launch(sum_kernel<T, V>, grid_of(p.units), dim3(kThreads), 0, s, p);
+    if (e != cudaSuccess || p.chunks <= 1) return e;
+    p.units = ceil_div(p.chunks - 1, kJoinChunks) * ceil_div(p.tile.packs, 128);
+    return plan_launch(join_kernel<T, V>, grid_of(p.units), dim3(kThreads), 0, s, p);
+}
+
+}  // namespace embedding
+}  // namespace olc
+
+using namespace olc;
+
+struct olc_embedding_plan {
+    PlanState state;
+    olc_dtype dtype;
+    int64_t n, vocab, cols;
+    float scale;
+};
+
+extern "C" {
+
+olc_status olc_embedding_plan_create(int64_t tokens, int64_t vocab, int64_t cols, double scale, olc_dtype dtype,
+                                     olc_embedding_plan** out) {
+    if (!out) return OLC_ERR_NULL;
+    *out = nullptr;
+    if (!plan_dtype_ok(dtype)) return OLC_ERR_DTYPE;
+    if (tokens < 0 || vocab < 0 || cols < 0) return OLC_ERR_NEGATIVE_DIM;
+    // places and tokens are 32-bit in the kernels
+    constexpr int64_t most = (int64_t(1) << 31) - 65536;
+    if (tokens >= most || vocab >= most || cols >= most || !(scale >= -3e38 && scale <= 3e38)) return OLC_ERR_INVALID;
+    if (!plan_fits(tokens, cols, 4) || !plan_fits(vocab, cols, 4)) return OLC_ERR_INVALID;
+    olc_embedding_plan* p = new (std::nothrow) olc_embedding_plan;
+    if (!p) return OLC_ERR_OOM;
+    p->state.init();
+    p->dtype = dtype;
+    p->n = tokens;
+    p->vocab = vocab;
+    p->cols = cols;
+    p->scale = (float)scale;
+    *out = p;
+    return OLC_OK;
+}
+
+void olc_embedding_plan_destroy(olc_embedding_plan* plan) {
+    if (!plan) return;
+    plan->state.destroy();
+    delete plan;
+}
+
+olc_status olc_embedding_forward(olc_embedding_plan* plan, const void* table, int64_t table_pitch,
+                                 const int64_t* tokens, void* Y, int64_t y_pitch, void* stream) {
+    if (!plan) return OLC_ERR_NULL;
+    const int64_t eb = plan_elem_bytes(plan->dtype), n = plan->n, cols = plan->cols;
+    if (n == 0 || cols == 0) return OLC_OK;
+    if ((!table && plan->vocab > 0) || !tokens || !Y) return OLC_ERR_NULL;
+    if ((plan->vocab > 1 && (table_pitch < cols || !plan_fits(plan->vocab, table_pitch, eb))) ||
+        (n > 1 && (y_pitch < cols || !plan_fits(n, y_pitch, eb))))
+        return OLC_ERR_INVALID;
+    if (plan_misaligned(table, eb) || plan_misaligned(tokens, 8) || plan_misaligned(Y, eb)) return OLC_ERR_INVALID;
+    const olc_status st = plan->state.bind();
+    if (st != OLC_OK) return st;
+    const embedding::FwdParams p{table, tokens, Y, table_pitch, y_pitch, n, plan->vocab, plan->scale, {}, 0};
+    const bool wide = cols * eb % 16 == 0 && plan_aligned16(table) && plan_aligned16(Y) &&
+                      (plan->vocab <= 1 || table_pitch * eb % 16 == 0) && (n == 1 || y_pitch * eb % 16 == 0);
+    return by_type(plan->dtype, [&](auto tag) {
+        using T = decltype(tag);
+        const cudaStream_t s = static_cast<cudaStream_t>(stream);
+        return plan_status(wide ? embedding::forward_as<T, 16 / sizeof(T)>(p, cols, plan->state.sm_count, s)
+                                : embedding::forward_as<T, 1>(p, cols, plan->state.sm_count, s));
+    });
+}
+
+olc_status olc_embedding_backward(olc_embedding_plan* plan, const void* dY, int64_t dy_pitch, const int64_t* tokens,
+                                  void* dtable, int64_t dtable_pitch, int accumulate, void* stream) {
+    if (!plan) return OLC_ERR_NULL;
+    const int64_t eb = plan_elem_bytes(plan->dtype), n = plan->n, vocab = plan->vocab, cols = plan->cols;
+    if (vocab == 0 || cols == 0 || (accumulate && n == 0)) return OLC_OK;
+    if (!dtable || (n > 0 && (!dY || !tokens))) return OLC_ERR_NULL;
+    if ((n > 1 && (dy_pitch < cols || !plan_fits(n, dy_pitch, eb))) ||
+        (vocab > 1 && (dtable_pitch < cols || !plan_fits(vocab, dtable_pitch, eb))))
+        return OLC_ERR_INVALID;
+    if (plan_misaligned(dY, eb) || plan_misaligned(tokens, 8) || plan_misaligned(dtable, eb)) return OLC_ERR_INVALID;
+    olc_status st = plan->state.bind();
+    if (st != OLC_OK) return st;
+    const int sms = plan->state.sm_count;
+    const int length = embedding::chunk_length(n, cols, eb, sms);
+    const int64_t chunks = ceil_div(n, length);
+    const embedding::Layout l = embedding::layout_of(n, vocab, cols, chunks);
+    st = plan->state.ensure(l.bytes);
+    if (st != OLC_OK) return st;
+    char* const m = static_cast<char*>(plan->state.memory);
+    const embedding::BwdParams p{dY, dtable, reinterpret_cast<float*>(m + l.partial), dy_pitch, dtable_pitch, vocab, cols,
+                                 plan->scale, accumulate != 0, length, chunks,
+                                 {reinterpret_cast<int*>(m), reinterpret_cast<int*>(m + l.place),
+                                  reinterpret_cast<int*>(m + l.token)},
+                                 {}, 0, 0};
+    const bool wide = cols * eb % 16 == 0 && plan_aligned16(dY) && plan_aligned16(dtable) &&
+                      (n <= 1 || dy_pitch * eb % 16 == 0) && (vocab == 1 || dtable_pitch * eb % 16 == 0);
+    return by_type(plan->dtype, [&](auto tag) {
+        using T = decltype(tag);
+        const cudaStream_t s = static_cast<cudaStream_t>(stream);
+        return plan_status(plan->state.use(s, [&] {
+            return wide ? embedding::backward_as<T, 16 / sizeof(T)>(p, tokens, n, sms, s)
+                        : embedding::backward_as<T, 1>(p, tokens, n, sms, s);
+        }));
+    });
+}
+
+}  // extern "C"

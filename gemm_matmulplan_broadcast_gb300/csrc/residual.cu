@@ -1,0 +1,965 @@
+// The step between two blocks of a model, with its norms:
+//
+//   n = norm(f) ag + ab  (or n = f),   y = x + scale gate n,   z = norm(y) g + b
+//
+// forward and backward.  Backward, with hats for the normalised rows, J' of a
+// norm being v -> rstd (v - mean(v) - hat mean(v hat)) (without mean(v) for RMS):
+//
+//   dx = dY + J_y'(dZ g),  dn = scale gate dx,  df = J_f'(dn ag),  dgate = scale n dx
+//   dg = sum dZ yhat, db = sum dZ, dag = sum dn fhat, dab = sum dn   (over the rows)
+//
+// Four tensors move forward, six backward (one or two more with a gate for each
+// element), with 20 to 40 operations an element: the bytes bound both.  A row is
+// read once and stays in registers from its first sum to its last use; rows wider
+// than that are read again.  Statistics and sums are float32; a mean is corrected by
+// the sum of the distances from it, in the same pass as the squares (Chan, Golub and
+// LeVeque's two-pass algorithm), so that rows far from zero keep their digits.
+#include <new>
+
+#include "plan_state.h"
+#include "row_packs.cuh"
+
+namespace olc {
+namespace residual {
+
+struct FwdParams {
+    const void* X;
+    const void* F;
+    const void* gate;       // may be null: 1
+    const void* ag;         // weights of the norm of f; may be null: 1, 0
+    const void* ab;
+    const void* g;          // weights of the norm of y; may be null: 1, 0
+    const void* b;
+    void* Y;
+    void* Z;                // may be null
+    float* stats;           // may be null
+    int64_t x_pitch, f_pitch, gate_pitch, y_pitch, z_pitch;
+    int64_t rows, cols;
+    float eps, scale, inv_cols;
+    int after, rms;
+};
+
+enum Sum { DG = 0, DB, DAG, DAB, DGATE, SUMS };
+
+struct BwdParams {
+    const void* dY;         // may be null: 0
+    const void* dZ;         // may be null: no norm of y
+    const void* F;
+    const void* Y;
+    const float* stats;
+    const void* gate;       // may be null: 1
+    const void* ag;
+    const void* ab;
+    const void* g;
+    void* dX;               // may be null
+    void* dF;               // may be null
+    void* dgate;            // of each element; may be null
+    float* partial;         // [blocks][SUMS][cols]: what a block adds to each column sum; null: none is wanted
+    float* row_sums;        // [4][rows]: the means that J of y and of f subtract (rows wider than a block)
+    int64_t dy_pitch, dz_pitch, f_pitch, y_pitch, gate_pitch, dx_pitch, df_pitch, dgate_pitch;
+    int64_t rows, cols;
+    float scale, inv_cols;
+    int after, rms, channel_gate_sum;
+    int threads_per_row;
+};
+
+// sums of two values over the W warps of a block; every thread gets them.
+// Consecutive calls take different slots.
+template <int W>
+__device__ __forceinline__ float2 block_sums(float2 v, float2* slot) {
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if constexpr (W == 1) return v;
+    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        s.x += slot[i].x;
+        s.y += slot[i].y;
+    }
+    return s;
+}
+
+struct Stats {
+    float mean, rstd;
+};
+// from the sums of the squared distances and of the distances from `mean`
+__device__ __forceinline__ Stats stats_of(float mean, float2 sums, const FwdParams& p) {
+    const float shift = p.rms ? 0.f : sums.y * p.inv_cols;
+    float squares = p.rms ? sums.x : fmaf(-sums.y, shift, sums.x);
+    if (squares < 0.f) squares = 0.f;       // NaN stays
+    return Stats{mean + shift, 1.0f / sqrtf(fmaf(squares, p.inv_cols, p.eps))};
+}
+
+// W warps on a row, NV packs (or pairs of elements) a thread, in registers.
+// W == 1: blocks of four independent warps.
+template <typename T, int V, int W, int NV>
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32) forward_kernel(const FwdParams p) {
+    using C = Columns<T, V>;
+    constexpr int P = C::P, TPR = W * 32;
+    __shared__ float slots1[2][W];
+    __shared__ float2 slots2[2][W];
+    const int t = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
+    const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    if (row >= p.rows) return;      // whole warps (W == 1); never with W > 1
+    const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
+    const T* f = static_cast<const T*>(p.F) + row * p.f_pitch;
+    const int cols = (int)p.cols, whole = V == 1 && W > 1 ? cols / (2 * TPR) : 0;
+    auto read = [&](const void* from, int i) {
+        return C::read(static_cast<const T*>(from), t, i, TPR, cols, true, i < whole);
+    };
+    typename C::Raw kx[NV], kf[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) kf[i] = read(f, i);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) kx[i] = read(x, i);
+
+    F2 y[NV][P];                     // f, then n, then y, then z
+    // the statistics of what y holds; columns past the row's end hold zeros
+    auto statistics = [&](int k) {
+        float mean = 0.f;
+        if (!p.rms) {
+            F2 s = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int q = 0; q < P; ++q) s = add2(s, y[i][q]);
+            mean = block_sum<W>(sum_of<2>(s), slots1[k]) * p.inv_cols;
+        }
+        const F2 minus_mean = both(-mean);
+        F2 squares = 0, distances = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const F2 d = C::inside(add2(y[i][q], minus_mean), t, i, q, TPR, cols, i < whole);
+                squares = fma2(d, d, squares);
+                distances = add2(distances, d);
+            }
+        return stats_of(mean, block_sums<W>(make_float2(sum_of<2>(squares), sum_of<2>(distances)), slots2[k]), p);
+    };
+    auto normalise = [&](Stats s, const void* weight, const void* bias) {
+        const F2 minus_mean = both(-s.mean), scale = both(s.rstd);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int q = 0; q < P; ++q) y[i][q] = mul2(add2(y[i][q], minus_mean), scale);
+            F2 w[P];
+            if (weight) {
+                C::pairs_of(w, read(weight, i));
+#pragma unroll
+                for (int q = 0; q < P; ++q) y[i][q] = mul2(y[i][q], w[q]);
+            }
+            if (bias) {
+                C::pairs_of(w, read(bias, i));
+#pragma unroll
+                for (int q = 0; q < P; ++q) y[i][q] = add2(y[i][q], w[q]);
+            }
+        }
+    };
+    auto keep = [&](Stats s, int k) {
+        if (p.stats && t == 0) {
+            p.stats[2 * k * p.rows + row] = s.mean;
+            p.stats[(2 * k + 1) * p.rows + row] = s.rstd;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) C::pairs_of(y[i], kf[i]);
+    if (p.after) {
+        const Stats s = statistics(0);
+        keep(s, 1);
+        normalise(s, p.ag, p.ab);
+    }
+    const F2 scale = both(p.scale);
+    const T* gate = static_cast<const T*>(p.gate) + (p.gate ? row * p.gate_pitch : 0);
+    T* out = static_cast<T*>(p.Y) + row * p.y_pitch;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        F2 v[P], w[P];
+        C::pairs_of(v, kx[i]);
+        if (p.gate) C::pairs_of(w, read(gate, i));
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            y[i][q] = C::inside(fma2(p.gate ? mul2(scale, w[q]) : scale, y[i][q], v[q]), t, i, q, TPR, cols, i < whole);
+        C::write(out, t, i, TPR, cols, y[i], i < whole);
+    }
+    if (!p.Z) return;
+    const Stats s = statistics(1);
+    keep(s, 0);
+    normalise(s, p.g, p.b);
+    T* z = static_cast<T*>(p.Z) + row * p.z_pitch;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) C::write(z, t, i, TPR, cols, y[i], i < whole);
+}
+
+// Rows longer than the registers of a block hold: each step reads the row again.
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) forward_long_kernel(const FwdParams p) {
+    constexpr int P = pairs<V>();
+    __shared__ float slots1[2][32];
+    __shared__ float2 slots2[2][32];
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const T* x = static_cast<const T*>(p.X) + row * p.x_pitch;
+        const T* f = static_cast<const T*>(p.F) + row * p.f_pitch;
+        const T* gate = static_cast<const T*>(p.gate) + (p.gate ? row * p.gate_pitch : 0);
+        auto affine = [&](F2 (&v)[P], Stats s, const void* weight, const void* bias, int64_t c) {
+            F2 w[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) v[q] = mul2(add2(v[q], both(-s.mean)), both(s.rstd));
+            if (weight) {
+                widen<T, V>(w, load<T, V>(static_cast<const T*>(weight) + c));
+#pragma unroll
+                for (int q = 0; q < P; ++q) v[q] = mul2(v[q], w[q]);
+            }
+            if (bias) {
+                widen<T, V>(w, load<T, V>(static_cast<const T*>(bias) + c));
+#pragma unroll
+                for (int q = 0; q < P; ++q) v[q] = add2(v[q], w[q]);
+            }
+        };
+        auto statistics = [&](int k, auto&& value) {
+            float mean = 0.f;
+            F2 v[P];
+            if (!p.rms) {
+                F2 s = 0;
+                for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
+                    value(v, c);
+#pragma unroll
+                    for (int q = 0; q < P; ++q) s = add2(s, v[q]);
+                }
+                mean = block_sum<32>(sum_of<V>(s), slots1[k]) * p.inv_cols;
+            }
+            F2 squares = 0, distances = 0;
+            for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
+                value(v, c);
+#pragma unroll
+                for (int q = 0; q < P; ++q) {
+                    const F2 d = add2(v[q], both(-mean));
+                    squares = fma2(d, d, squares);
+                    distances = add2(distances, d);
+                }
+            }
+            const Stats s = stats_of(mean, block_sums<32>(make_float2(sum_of<V>(squares), sum_of<V>(distances)), slots2[k]), p);
+            if (p.stats && threadIdx.x == 0) {
+                p.stats[(k ? 0 : 2) * p.rows + row] = s.mean;
+                p.stats[(k ? 1 : 3) * p.rows + row] = s.rstd;
+            }
+            return s;
+        };
+        auto of_f = [&](F2 (&v)[P], int64_t c) { widen<T, V>(v, load<T, V>(f + c)); };
+        Stats sf{0.f, 1.f};
+        if (p.after) sf = statistics(0, of_f);
+        auto of_y = [&](F2 (&v)[P], int64_t c) {
+            F2 w[P];
+            of_f(v, c);
+            if (p.after) affine(v, sf, p.ag, p.ab, c);
+            if (p.gate) {
+                widen<T, V>(w, load<T, V>(gate + c));
+#pragma unroll
+                for (int q = 0; q < P; ++q) w[q] = mul2(both(p.scale), w[q]);
+            }
+            F2 u[P];
+            widen<T, V>(u, load<T, V>(x + c));
+#pragma unroll
+            for (int q = 0; q < P; ++q) v[q] = fma2(p.gate ? w[q] : both(p.scale), v[q], u[q]);
+        };
+        Stats sy{0.f, 1.f};
+        if (p.Z) sy = statistics(1, of_y);
+        for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
+            F2 v[P];
+            of_y(v, c);
+            store<T, V>(static_cast<T*>(p.Y) + row * p.y_pitch + c, v);
+            if (p.Z) {
+                affine(v, sy, p.g, p.b, c);
+                store<T, V>(static_cast<T*>(p.Z) + row * p.z_pitch + c, v);
+            }
+        }
+        __syncthreads();             // the slots serve the next row
+    }
+}
+
+// ---- backward -----------------------------------------------------------------
+
+// What a thread holds of a row: P pairs of columns.  The steps are the same for
+// rows in registers and for rows read again.
+template <int P>
+struct Grads {
+    F2 yh[P], dz[P];        // yhat; dZ g
+    F2 fh[P], dn[P];        // fhat (or f); dn, then dn ag
+};
+
+template <int P>
+__device__ __forceinline__ void add_products(F2& s1, F2& s2, const F2 (&a)[P], const F2 (&b)[P]) {
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        s1 = add2(s1, a[q]);
+        s2 = fma2(a[q], b[q], s2);
+    }
+}
+// v -> rstd (v - m1 - hat m2), added to `to`
+template <int P>
+__device__ __forceinline__ void add_through_norm(F2 (&to)[P], const F2 (&v)[P], const F2 (&hat)[P], F2 minus_m1,
+                                                 F2 minus_m2, F2 rstd) {
+#pragma unroll
+    for (int q = 0; q < P; ++q) to[q] = fma2(add2(fma2(hat[q], minus_m2, v[q]), minus_m1), rstd, to[q]);
+}
+
+// A block is `groups` groups of threads_per_row threads; a thread keeps the same
+// columns (16 bytes of 16-bit types; eight of FLOAT) of every row its group
+// takes, so that the column sums stay in its registers until the block's last row; the groups'
+// sums are then added in group order.  The next row's loads are on their way while
+// this one's two row sums (one after the other: the second needs dx) are formed.
+constexpr int kColsPerThread = 8;
+constexpr int kThreads = 512;
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(kThreads) backward_kernel(const BwdParams p) {
+    using C = Columns<T, V>;
+    constexpr int P = C::P, Q = NV * P;
+    extern __shared__ float shared[];
+    __shared__ alignas(16) float2 slots[4][16];
+    const int tpr = p.threads_per_row;
+    const int groups = blockDim.x / tpr, warps = tpr >> 5;
+    const int grp = threadIdx.x / tpr, t = threadIdx.x - grp * tpr;
+    const int cols = (int)p.cols;
+    // single elements: a warp's columns lie together, so that their offsets are constants
+    const int warp_base = (t >> 5) * (64 * NV);
+    const int base = V == 1 ? warp_base + (t & 31) : t, stride = V == 1 ? 32 : tpr;
+    const int whole = V == 1 ? (cols - warp_base) / 64 : 0;
+    struct Raw {
+        typename C::Raw r[NV];
+    };
+    auto read = [&](Raw& k, const void* from, int64_t at, bool live) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            k.r[i] = C::read(static_cast<const T*>(from) + at, base, i, stride, cols, live, i < whole);
+    };
+    auto widen_all = [&](F2 (&out)[Q], const Raw& k) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            F2 v[P];
+            C::pairs_of(v, k.r[i]);
+#pragma unroll
+            for (int q = 0; q < P; ++q) out[i * P + q] = v[q];
+        }
+    };
+    auto weights = [&](F2 (&out)[Q], const void* from, float none) {
+        if (!from) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) out[q] = both(none);
+            return;
+        }
+        Raw k;
+        read(k, from, 0, true);
+        widen_all(out, k);
+    };
+    auto write = [&](void* to, int64_t at, const F2 (&v)[Q]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            F2 o[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) o[q] = v[i * P + q];
+            C::write(static_cast<T*>(to) + at, base, i, stride, cols, o, i < whole);
+        }
+    };
+    F2 sums[SUMS][Q];
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) sums[k][q] = 0;
+    const bool need_f = p.after || p.dgate || p.channel_gate_sum;
+    Raw kdy{}, kdz{}, kf{}, ky{}, kg{};
+    Stats sy{0.f, 0.f}, sf{0.f, 0.f};
+    // columns past a row's end, and rows past the last one, have gradients of 0 and add nothing
+    auto fetch = [&](int64_t row) {
+        const bool live = row < p.rows;
+        if (p.dZ) {
+            read(kdz, p.dZ, row * p.dz_pitch, live);
+            read(ky, p.Y, row * p.y_pitch, live);
+            sy = live ? Stats{p.stats[row], p.stats[p.rows + row]} : Stats{0.f, 0.f};
+        }
+        if (p.dY) read(kdy, p.dY, row * p.dy_pitch, live);
+        if (need_f) read(kf, p.F, row * p.f_pitch, live);
+        if (p.after) sf = live ? Stats{p.stats[2 * p.rows + row], p.stats[3 * p.rows + row]} : Stats{0.f, 0.f};
+        if (p.gate && p.gate_pitch) read(kg, p.gate, row * p.gate_pitch, live);
+    };
+    auto row_means = [&](F2 s1, F2 s2, int slot) {
+        float2 c = make_float2(warp_sum(sum_of<2>(s1)), warp_sum(sum_of<2>(s2)));
+        if (warps > 1) {
+            if ((threadIdx.x & 31) == 0) slots[slot][threadIdx.x >> 5] = c;
+            __syncthreads();
+            c = make_float2(0.f, 0.f);
+            for (int w = 0; w < warps; ++w) {
+                const float2 v = slots[slot][grp * warps + w];
+                c.x += v.x;
+                c.y += v.y;
+            }
+        }
+        if (p.rms) c.x = 0.f;
+        return make_float2(-c.x * p.inv_cols, -c.y * p.inv_cols);
+    };
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + grp;
+    fetch(row);
+    int buf = 0;
+    // every group runs the same number of turns: the barriers are the block's
+    for (int64_t first = (int64_t)blockIdx.x * groups; first < p.rows; first += step, row += step, buf ^= 2) {
+        const bool live = row < p.rows;
+        F2 dx[Q], w[Q];
+        widen_all(dx, kdy);                           // zeros without dY
+        if (p.dZ) {
+            F2 dz[Q], yh[Q];
+            widen_all(dz, kdz);
+            widen_all(yh, ky);
+            const F2 rstd = both(sy.rstd), minus_mean = both(-sy.mean);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                yh[q] = mul2(add2(yh[q], minus_mean), rstd);
+                sums[DG][q] = fma2(dz[q], yh[q], sums[DG][q]);
+                sums[DB][q] = add2(sums[DB][q], dz[q]);
+            }
+            if (p.g) {
+                weights(w, p.g, 1.f);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) dz[q] = mul2(dz[q], w[q]);
+            }
+            F2 s1 = 0, s2 = 0;
+            add_products<Q>(s1, s2, dz, yh);
+            const float2 m = row_means(s1, s2, buf);
+            add_through_norm<Q>(dx, dz, yh, both(m.x), both(m.y), rstd);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) dx[q] = C::inside(dx[q], base, q / P, q % P, stride, cols, q / P < whole);
+        }
+        F2 f[Q], gate[Q];
+        widen_all(f, kf);
+        if (p.gate && p.gate_pitch) {
+            widen_all(gate, kg);
+        } else {
+            weights(gate, p.gate, 1.f);
+        }
+        const Stats now = sf;
+        fetch(row + step);
+        if (live && p.dX) write(p.dX, row * p.dx_pitch, dx);
+        const F2 scale = both(p.scale), rstd = both(now.rstd), minus_mean = both(-now.mean);
+        if (p.after) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) f[q] = mul2(add2(f[q], minus_mean), rstd);
+        }
+        if (p.dgate || p.channel_gate_sum) {
+            F2 n[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) n[q] = f[q];
+            if (p.after) {
+                weights(w, p.ag, 1.f);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) n[q] = mul2(n[q], w[q]);
+                weights(w, p.ab, 0.f);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) n[q] = add2(n[q], w[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                n[q] = mul2(mul2(n[q], scale), dx[q]);
+                sums[DGATE][q] = add2(sums[DGATE][q], n[q]);
+            }
+            if (live && p.dgate) write(p.dgate, row * p.dgate_pitch, n);
+        }
+        if (!p.after && !p.dF) continue;              // uniform over the grid
+        F2 dn[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) dn[q] = mul2(mul2(scale, gate[q]), dx[q]);
+        if (p.after) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                sums[DAG][q] = fma2(dn[q], f[q], sums[DAG][q]);
+                sums[DAB][q] = add2(sums[DAB][q], dn[q]);
+            }
+            if (!p.dF) continue;
+            if (p.ag) {
+                weights(w, p.ag, 1.f);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) dn[q] = mul2(dn[q], w[q]);
+            }
+            F2 s1 = 0, s2 = 0;
+            add_products<Q>(s1, s2, dn, f);
+            const float2 m = row_means(s1, s2, buf + 1);
+            F2 df[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) df[q] = 0;
+            add_through_norm<Q>(df, dn, f, both(m.x), both(m.y), rstd);
+            if (live) write(p.dF, row * p.df_pitch, df);
+        } else if (live) {
+            write(p.dF, row * p.df_pitch, dn);
+        }
+    }
+    if (!p.partial) return;
+    float* out = p.partial + (int64_t)blockIdx.x * SUMS * cols;
+#pragma unroll
+    for (int which = 0; which < SUMS; ++which) {
+        if (groups > 1) __syncthreads();
+        float* to = groups > 1 ? shared + grp * cols : out + which * cols;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                float v[2];
+                unpack_f2(sums[which][i * P + q], v[0], v[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (C::at(base, i, 2 * q + h, stride) < cols) to[C::at(base, i, 2 * q + h, stride)] = v[h];
+            }
+        if (groups == 1) continue;
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+            float s = 0.f;
+            for (int k = 0; k < groups; ++k) s += shared[k * cols + c];
+            out[which * cols + c] = s;
+        }
+    }
+}
+
+// Rows wider than a block keeps: first the row sums (two passes over the row) ...
+template <typename T, int V>
+struct LongRow {
+    static constexpr int P = pairs<V>();
+    const BwdParams& p;
+    int64_t row;
+    Stats sy, sf;
+    __device__ __forceinline__ LongRow(const BwdParams& params, int64_t r) : p(params), row(r), sy{0, 0}, sf{0, 0} {
+        if (p.dZ) sy = Stats{p.stats[row], p.stats[p.rows + row]};
+        if (p.after) sf = Stats{p.stats[2 * p.rows + row], p.stats[3 * p.rows + row]};
+    }
+    __device__ __forceinline__ void get(F2 (&v)[P], const void* from, int64_t pitch, int64_t c) const {
+        widen<T, V>(v, load<T, V>(static_cast<const T*>(from) + row * pitch + c));
+    }
+    __device__ __forceinline__ void put(void* to, int64_t pitch, int64_t c, const F2 (&v)[P]) const {
+        store<T, V>(static_cast<T*>(to) + row * pitch + c, v);
+    }
+    static __device__ __forceinline__ void weigh(F2 (&v)[P], const void* w, int64_t c) {
+        if (!w) return;
+        F2 k[P];
+        widen<T, V>(k, load<T, V>(static_cast<const T*>(w) + c));
+#pragma unroll
+        for (int q = 0; q < P; ++q) v[q] = mul2(v[q], k[q]);
+    }
+    __device__ __forceinline__ void hat(F2 (&v)[P], Stats s) const {
+#pragma unroll
+        for (int q = 0; q < P; ++q) v[q] = mul2(add2(v[q], both(-s.mean)), both(s.rstd));
+    }
+    // dZ (to dz) and yhat
+    __device__ __forceinline__ void norm_inputs(F2 (&dz)[P], F2 (&yh)[P], int64_t c) const {
+        get(dz, p.dZ, p.dz_pitch, c);
+        get(yh, p.Y, p.y_pitch, c);
+        hat(yh, sy);
+    }
+    // dx, from dZ g and yhat
+    __device__ __forceinline__ void dx_of(F2 (&dx)[P], const F2 (&dz)[P], const F2 (&yh)[P], float2 m, int64_t c) const {
+        if (p.dY) get(dx, p.dY, p.dy_pitch, c);
+        else
+#pragma unroll
+            for (int q = 0; q < P; ++q) dx[q] = 0;
+        if (p.dZ) add_through_norm<P>(dx, dz, yh, both(m.x), both(m.y), both(sy.rstd));
+    }
+    // scale gate dx
+    __device__ __forceinline__ void dn_of(F2 (&dn)[P], const F2 (&dx)[P], int64_t c) const {
+#pragma unroll
+        for (int q = 0; q < P; ++q) dn[q] = both(p.scale);
+        if (p.gate) weigh(dn, static_cast<const T*>(p.gate) + row * p.gate_pitch, c);
+#pragma unroll
+        for (int q = 0; q < P; ++q) dn[q] = mul2(dn[q], dx[q]);
+    }
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) backward_long_sums_kernel(const BwdParams p) {
+    using L = LongRow<T, V>;
+    constexpr int P = L::P;
+    __shared__ float2 slots[2][32];
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const L r(p, row);
+        auto means = [&](F2 s1, F2 s2, int k) {
+            float2 c = block_sums<32>(make_float2(sum_of<V>(s1), sum_of<V>(s2)), slots[k]);
+            c = make_float2(p.rms ? 0.f : -c.x * p.inv_cols, -c.y * p.inv_cols);
+            if (threadIdx.x == 0) {
+                p.row_sums[2 * k * p.rows + row] = c.x;
+                p.row_sums[(2 * k + 1) * p.rows + row] = c.y;
+            }
+            return c;
+        };
+        F2 dz[P], yh[P], s1 = 0, s2 = 0;
+        float2 m = make_float2(0.f, 0.f);
+        if (p.dZ) {
+            for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
+                r.norm_inputs(dz, yh, c);
+                r.weigh(dz, p.g, c);
+                add_products<P>(s1, s2, dz, yh);
+            }
+            m = means(s1, s2, 0);
+        }
+        if (p.after) {
+            s1 = s2 = 0;
+            for (int64_t c = (int64_t)threadIdx.x * V; c < p.cols; c += 1024 * V) {
+                F2 dx[P], dn[P], fh[P];
+                if (p.dZ) {
+                    r.norm_inputs(dz, yh, c);
+                    r.weigh(dz, p.g, c);
+                }
+                r.dx_of(dx, dz, yh, m, c);
+                r.dn_of(dn, dx, c);
+                r.weigh(dn, p.ag, c);
+                r.get(fh, p.F, p.f_pitch, c);
+                r.hat(fh, r.sf);
+                add_products<P>(s1, s2, dn, fh);
+            }
+            means(s1, s2, 1);
+        }
+        __syncthreads();             // the slots serve the next row
+    }
+}
+
+// ... then everything else, by threads that keep a pack of columns over a share of
+// the rows (blockIdx.y).
+template <typename T, int V>
+__global__ void __launch_bounds__(128) backward_long_kernel(const BwdParams p) {
+    using L = LongRow<T, V>;
+    constexpr int P = L::P;
+    const int64_t c = ((int64_t)blockIdx.x * 128 + threadIdx.x) * V;
+    if (c >= p.cols) return;
+    const int64_t r0 = p.rows * blockIdx.y / gridDim.y, r1 = p.rows * (blockIdx.y + 1) / gridDim.y;
+    F2 sums[SUMS][P];
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k)
+#pragma unroll
+        for (int q = 0; q < P; ++q) sums[k][q] = 0;
+    for (int64_t row = r0; row < r1; ++row) {
+        const L r(p, row);
+        F2 dz[P], yh[P], dx[P];
+        float2 m = make_float2(0.f, 0.f);
+        if (p.dZ) {
+            r.norm_inputs(dz, yh, c);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                sums[DG][q] = fma2(dz[q], yh[q], sums[DG][q]);
+                sums[DB][q] = add2(sums[DB][q], dz[q]);
+            }
+            r.weigh(dz, p.g, c);
+            m = make_float2(p.row_sums[row], p.row_sums[p.rows + row]);
+        }
+        r.dx_of(dx, dz, yh, m, c);
+        F2 f[P], dn[P];
+        if (p.after || p.dgate || p.channel_gate_sum) r.get(f, p.F, p.f_pitch, c);
+        r.dn_of(dn, dx, c);                            // reads the gate before dgate may replace it
+        if (p.dX) r.put(p.dX, p.dx_pitch, c, dx);
+        if (p.after) r.hat(f, r.sf);
+        if (p.dgate || p.channel_gate_sum) {
+            F2 n[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) n[q] = f[q];
+            if (p.after) {
+                r.weigh(n, p.ag, c);
+                if (p.ab) {
+                    F2 k[P];
+                    widen<T, V>(k, load<T, V>(static_cast<const T*>(p.ab) + c));
+#pragma unroll
+                    for (int q = 0; q < P; ++q) n[q] = add2(n[q], k[q]);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                n[q] = mul2(mul2(n[q], both(p.scale)), dx[q]);
+                sums[DGATE][q] = add2(sums[DGATE][q], n[q]);
+            }
+            if (p.dgate) r.put(p.dgate, p.dgate_pitch, c, n);
+        }
+        if (p.after) {
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                sums[DAG][q] = fma2(dn[q], f[q], sums[DAG][q]);
+                sums[DAB][q] = add2(sums[DAB][q], dn[q]);
+            }
+            r.weigh(dn, p.ag, c);
+            F2 df[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) df[q] = 0;
+            add_through_norm<P>(df, dn, f, both(p.row_sums[2 * p.rows + row]), both(p.row_sums[3 * p.rows + row]),
+                                both(r.sf.rstd));
+            if (p.dF) r.put(p.dF, p.df_pitch, c, df);
+        } else if (p.dF) {
+            r.put(p.dF, p.df_pitch, c, dn);
+        }
+    }
+    if (!p.partial) return;
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k) {
+        float* out = p.partial + ((int64_t)blockIdx.y * SUMS + k) * p.cols + c;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            float lo, hi;
+            unpack_f2(sums[k][q], lo, hi);
+            out[2 * q] = lo;
+            if (V > 1) out[2 * q + 1] = hi;
+        }
+    }
+}
+
+struct Outputs {
+    void* to[SUMS];         // null: not wanted
+};
+
+// Column sums over the blocks' partial sums, C columns a block: in block order
+// within each share of them and then in share order, the same for every run.
+template <typename T, int C>
+__global__ void __launch_bounds__(1024)
+column_sum_kernel(const float* __restrict__ partial, int blocks, int64_t cols, const Outputs outputs) {
+    constexpr int SHARES = 1024 / C;
+    __shared__ float sums[SHARES][C + 1];
+    T* out = static_cast<T*>(outputs.to[blockIdx.y]);
+    if (!out) return;
+    const int col = threadIdx.x % C, share = threadIdx.x / C;
+    const int64_t c = (int64_t)blockIdx.x * C + col;
+    float s = 0.f;
+    if (c < cols) {
+#pragma unroll 10
+        for (int b = share; b < blocks; b += SHARES) s += partial[((int64_t)b * SUMS + blockIdx.y) * cols + c];
+    }
+    sums[share][col] = s;
+    __syncthreads();
+    // a warp a column
+    const int lane = threadIdx.x & 31, mine = threadIdx.x >> 5;
+    if (mine >= C) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < SHARES / 32; ++i) s += sums[lane + 32 * i][mine];
+    s = warp_sum(s);
+    const int64_t to = (int64_t)blockIdx.x * C + mine;
+    if (lane == 0 && to < cols) out[to] = Num<T>::from_acc(s);
+}
+
+// ---- host side -------------------------------------------------------------
+
+// Threads a row: with many rows a thread takes up to four packs, with few rows more
+// warps share one.  One warp needs no block barrier.
+template <typename T, int V>
+cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
+    // single elements go in pairs, twice as many a thread as packs
+    const int64_t n = ceil_div(p.cols, V == 1 ? 4 : V);
+    constexpr int M = V == 1 ? 2 : 1;
+    const bool few = p.rows < 4 * (int64_t)sm_count;
+#define OLC_FWD(W, NV)                                                                                          \
+    return plan_launch(forward_kernel<T, V, W, NV * M>, dim3((unsigned)(W == 1 ? ceil_div(p.rows, 4) : p.rows)), \
+                      dim3(W == 1 ? 128 : W * 32), 0, s, p)
+    if (p.rows <= 0x7fffffff) {
+        if (n <= 32) OLC_FWD(1, 1);
+        if (n <= 64) OLC_FWD(1, 2);
+        if (n <= 256 && !few) OLC_FWD(4, 2);
+        if (n <= 256) OLC_FWD(8, 1);
+        if (n <= 512 && !few) OLC_FWD(4, 4);
+        if (n <= 512) OLC_FWD(16, 1);
+        if (n <= 1024) OLC_FWD(8, 4);
+        if (n <= 2048) OLC_FWD(16, 4);
+        if (n <= 4096) OLC_FWD(32, 4);
+    }
+#undef OLC_FWD
+    const int64_t grid = min64(p.rows, (int64_t)sm_count * 2);
+    return plan_launch(forward_long_kernel<T, V>, dim3((unsigned)grid), dim3(1024), 0, s, p);
+}
+
+// the backward launch of one shape
+struct BwdShape {
+    bool wide = false;      // rows wider than a block keeps
+    int tpr = 0, groups = 1;
+    int64_t blocks = 0;     // that leave partial sums
+};
+template <int V>
+BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
+    BwdShape b;
+    if (cols > kThreads * kColsPerThread) {
+        b.wide = true;
+        const int64_t across = ceil_div(ceil_div(cols, V), 128);
+        b.blocks = max64(1, min64(min64(ceil_div(rows, 4), 65535), 8 * (int64_t)sm_count / across));
+        return b;
+    }
+    b.tpr = (int)(ceil_div(ceil_div(cols, kColsPerThread), 32) * 32);
+    b.groups = (int)max64(1, min64(kThreads / b.tpr, ceil_div(rows, sm_count)));
+    b.blocks = max64(1, min64(ceil_div(rows, b.groups), sm_count));
+    return b;
+}
+
+template <typename T, int V>
+cudaError_t backward_as(BwdParams p, int sm_count, const Outputs& outputs, cudaStream_t s) {
+    const BwdShape b = backward_shape<V>(p.rows, p.cols, sm_count);
+    cudaError_t e = cudaSuccess;
+    p.threads_per_row = b.tpr;
+    if (b.wide) {
+        if (p.dZ || p.after)
+            e = plan_launch(backward_long_sums_kernel<T, V>, dim3((unsigned)min64(p.rows, (int64_t)sm_count * 2)),
+                            dim3(1024), 0, s, p);
+        if (e == cudaSuccess)
+            e = plan_launch(backward_long_kernel<T, V>,
+                            dim3((unsigned)ceil_div(ceil_div(p.cols, V), 128), (unsigned)b.blocks), dim3(128), 0, s, p);
+    } else {
+        constexpr int NV = V == 1 ? kColsPerThread / 2 : kColsPerThread / V;
+        const size_t smem = b.groups > 1 ? (size_t)b.groups * p.cols * sizeof(float) : 0;
+        e = plan_launch(backward_kernel<T, V, NV>, dim3((unsigned)b.blocks), dim3((unsigned)(b.tpr * b.groups)), smem, s, p);
+    }
+    if (e != cudaSuccess || !p.partial) return e;
+    return plan_launch(column_sum_kernel<T, 16>, dim3((unsigned)ceil_div(p.cols, 16), SUMS), dim3(1024), 0, s,
+                       (const float*)p.partial, (int)b.blocks, p.cols, outputs);
+}
+
+}  // namespace residual
+}  // namespace olc
+
+using namespace olc;
+
+struct olc_residual_norm_plan {
+    PlanState state;
+    olc_dtype dtype;
+    int64_t rows, cols;
+    float eps, scale;
+    int rms, after;
+};
+
+extern "C" {
+
+olc_status olc_residual_norm_plan_create(int64_t rows, int64_t cols, double eps, double scale, int norm, int after,
+                                         olc_dtype dtype, olc_residual_norm_plan** out) {
+    if (!out) return OLC_ERR_NULL;
+    *out = nullptr;
+    if (!plan_dtype_ok(dtype)) return OLC_ERR_DTYPE;
+    if (rows < 0 || cols < 0) return OLC_ERR_NEGATIVE_DIM;
+    // the mean of no elements is undefined; columns are 32-bit in the kernels
+    if (cols == 0 || cols >= (int64_t(1) << 31) - 65536 || !(eps >= 0.0) || eps > 3e38) return OLC_ERR_INVALID;
+    if (!(scale >= -3e38 && scale <= 3e38) || (norm != OLC_NORM_LAYER && norm != OLC_NORM_RMS)) return OLC_ERR_INVALID;
+    if (!plan_fits(rows, cols, 4) || !plan_fits(rows, 16, 4)) return OLC_ERR_INVALID;
+    olc_residual_norm_plan* p = new (std::nothrow) olc_residual_norm_plan;
+    if (!p) return OLC_ERR_OOM;
+    p->state.init();
+    p->dtype = dtype;
+    p->rows = rows;
+    p->cols = cols;
+    p->eps = (float)eps;
+    p->scale = (float)scale;
+    p->rms = norm == OLC_NORM_RMS;
+    p->after = after != 0;
+    *out = p;
+    return OLC_OK;
+}
+
+void olc_residual_norm_plan_destroy(olc_residual_norm_plan* plan) {
+    if (!plan) return;
+    plan->state.destroy();
+    delete plan;
+}
+
+// A [rows, cols] operand: refused, and whether its rows start on 16-byte
+// boundaries (null: nothing to say against it)
+static bool bad_rows(const olc_residual_norm_plan* plan, const void* m, int64_t pitch) {
+    const int64_t eb = plan_elem_bytes(plan->dtype);
+    return m && ((plan->rows > 1 && (pitch < plan->cols || !plan_fits(plan->rows, pitch, eb))) || plan_misaligned(m, eb));
+}
+static bool bad_gate(const olc_residual_norm_plan* plan, const void* m, int64_t pitch) {
+    return pitch == 0 ? plan_misaligned(m, plan_elem_bytes(plan->dtype)) : bad_rows(plan, m, pitch);
+}
+static bool wide_rows(const olc_residual_norm_plan* plan, const void* m, int64_t pitch) {
+    return plan_aligned16(m) && (!m || plan->rows == 1 || pitch * plan_elem_bytes(plan->dtype) % 16 == 0);
+}
+
+olc_status olc_residual_norm_forward(olc_residual_norm_plan* plan, const void* X, int64_t x_pitch, const void* F,
+                                     int64_t f_pitch, const void* gate, int64_t gate_pitch, const void* after_gamma,
+                                     const void* after_beta, const void* gamma, const void* beta, void* Y,
+                                     int64_t y_pitch, void* Z, int64_t z_pitch, float* stats, void* stream) {
+    if (!plan) return OLC_ERR_NULL;
+    if (plan->rows == 0) return OLC_OK;
+    if (!X || !F || !Y) return OLC_ERR_NULL;
+    const int64_t eb = plan_elem_bytes(plan->dtype);
+    if (bad_rows(plan, X, x_pitch) || bad_rows(plan, F, f_pitch) || bad_gate(plan, gate, gate_pitch) ||
+        bad_rows(plan, Y, y_pitch) || bad_rows(plan, Z, z_pitch) || plan_misaligned(after_gamma, eb) ||
+        plan_misaligned(after_beta, eb) || plan_misaligned(gamma, eb) || plan_misaligned(beta, eb) ||
+        plan_misaligned(stats, 4))
+        return OLC_ERR_INVALID;
+    const olc_status st = plan->state.bind();
+    if (st != OLC_OK) return st;
+    const residual::FwdParams p{X, F, gate, after_gamma, after_beta, gamma, beta, Y, Z, stats, x_pitch, f_pitch,
+                                gate_pitch, y_pitch, z_pitch, plan->rows, plan->cols, plan->eps, plan->scale,
+                                (float)(1.0 / (double)plan->cols), plan->after, plan->rms};
+    // 16-byte packs need every row of every operand on a 16-byte boundary
+    const bool wide = plan->cols * eb % 16 == 0 && wide_rows(plan, X, x_pitch) && wide_rows(plan, F, f_pitch) &&
+                      wide_rows(plan, gate, gate_pitch) && wide_rows(plan, Y, y_pitch) && wide_rows(plan, Z, z_pitch) &&
+                      plan_aligned16(after_gamma) && plan_aligned16(after_beta) && plan_aligned16(gamma) &&
+                      plan_aligned16(beta);
+    return by_type(plan->dtype, [&](auto tag) {
+        using T = decltype(tag);
+        const cudaStream_t s = static_cast<cudaStream_t>(stream);
+        return plan_status(wide ? residual::forward_as<T, 16 / sizeof(T)>(p, plan->state.sm_count, s)
+                                : residual::forward_as<T, 1>(p, plan->state.sm_count, s));
+    });
+}
+
+olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* dY, int64_t dy_pitch, const void* dZ,
+                                      int64_t dz_pitch, const void* F, int64_t f_pitch, const void* Y, int64_t y_pitch,
+                                      const float* stats, const void* gate, int64_t gate_pitch,
+                                      const void* after_gamma, const void* after_beta, const void* gamma, void* dX,
+                                      int64_t dx_pitch, void* dF, int64_t df_pitch, void* dgate, int64_t dgate_pitch,
+                                      void* dgamma, void* dbeta, void* dafter_gamma, void* dafter_beta, void* stream) {
+    if (!plan) return OLC_ERR_NULL;
+    if (!dX && !dF && !dgate && !dgamma && !dbeta && !dafter_gamma && !dafter_beta) return OLC_OK;
+    const int64_t eb = plan_elem_bytes(plan->dtype), rows = plan->rows, cols = plan->cols;
+    if (!plan->after && (dafter_gamma || dafter_beta)) return OLC_ERR_INVALID;
+    const bool channel_sum = dgate && gate_pitch == 0;
+    if (rows > 0) {
+        if (!dY && !dZ) return OLC_ERR_NULL;
+        if (!dZ && (dgamma || dbeta)) return OLC_ERR_NULL;
+        if (dgate && !gate) return OLC_ERR_NULL;
+        if (((plan->after || dgate) && !F) || (dZ && !Y) || ((dZ || plan->after) && !stats)) return OLC_ERR_NULL;
+    }
+    if (bad_rows(plan, dY, dy_pitch) || bad_rows(plan, dZ, dz_pitch) || bad_rows(plan, F, f_pitch) ||
+        bad_rows(plan, Y, y_pitch) || bad_gate(plan, gate, gate_pitch) || bad_rows(plan, dX, dx_pitch) ||
+        bad_rows(plan, dF, df_pitch) || (channel_sum ? plan_misaligned(dgate, eb) : bad_rows(plan, dgate, dgate_pitch)) ||
+        plan_misaligned(stats, 4) || plan_misaligned(after_gamma, eb) || plan_misaligned(after_beta, eb) ||
+        plan_misaligned(gamma, eb) || plan_misaligned(dgamma, eb) || plan_misaligned(dbeta, eb) ||
+        plan_misaligned(dafter_gamma, eb) || plan_misaligned(dafter_beta, eb))
+        return OLC_ERR_INVALID;
+    olc_status st = plan->state.bind();
+    if (st != OLC_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const residual::Outputs outputs{{dgamma, dbeta, dafter_gamma, dafter_beta, channel_sum ? dgate : nullptr}};
+    bool sums = false;
+    for (void* o : outputs.to) sums = sums || o;
+    if (rows == 0) {                        // empty sums
+        cudaError_t e = cudaSuccess;
+        for (void* o : outputs.to)
+            if (e == cudaSuccess && o) e = launch_zero_fill(o, cols * eb, s);
+        return plan_status(e);
+    }
+    const bool wide = cols * eb % 16 == 0 && wide_rows(plan, dY, dy_pitch) && wide_rows(plan, dZ, dz_pitch) &&
+                      wide_rows(plan, F, f_pitch) && wide_rows(plan, Y, y_pitch) && wide_rows(plan, gate, gate_pitch) &&
+                      wide_rows(plan, dX, dx_pitch) && wide_rows(plan, dF, df_pitch) &&
+                      (channel_sum || wide_rows(plan, dgate, dgate_pitch)) && plan_aligned16(after_gamma) &&
+                      plan_aligned16(after_beta) && plan_aligned16(gamma);
+    residual::BwdParams p{dY, dZ, F, Y, stats, gate, after_gamma, after_beta, gamma, dX, dF, channel_sum ? nullptr : dgate,
+                          nullptr, nullptr, dy_pitch, dz_pitch, f_pitch, y_pitch, gate_pitch, dx_pitch, df_pitch,
+                          dgate_pitch, rows, cols, plan->scale, (float)(1.0 / (double)cols), plan->after, plan->rms,
+                          channel_sum, 0};
+    // both layouts' partial sums fit: a call with other alignment or other
+    // outputs does not have to allocate again
+    const int sms = plan->state.sm_count;
+    const residual::BwdShape a = plan->dtype == OLC_FLOAT ? residual::backward_shape<4>(rows, cols, sms)
+                                                          : residual::backward_shape<8>(rows, cols, sms);
+    const residual::BwdShape b = residual::backward_shape<1>(rows, cols, sms);
+    const size_t row_floats = a.wide ? (size_t)rows * 4 : 0;
+    const size_t floats = row_floats + (size_t)max64(a.blocks, b.blocks) * residual::SUMS * (size_t)cols;
+    st = plan->state.ensure(floats * sizeof(float));
+    if (st != OLC_OK) return st;
+    p.row_sums = static_cast<float*>(plan->state.memory);
+    if (sums) p.partial = p.row_sums + row_floats;
+    return by_type(plan->dtype, [&](auto tag) {
+        using T = decltype(tag);
+        return plan_status(plan->state.use(s, [&] {
+            return wide ? residual::backward_as<T, 16 / sizeof(T)>(p, sms, outputs, s)
+                        : residual::backward_as<T, 1>(p, sms, outputs, s);
+        }));
+    });
+}
+
+}  // extern "C"

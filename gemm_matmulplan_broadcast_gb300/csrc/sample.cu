@@ -1,0 +1,968 @@
+// One token for each row of logits [rows, vocab] from one uniform number u a row:
+// temperature, top-k, top-p and min-p, then the inverse of the distribution that is left.
+//
+//   w_j = e^((z_j - m) / T),  m = max_j z_j
+//   kept: a prefix of the order (value, then the lower index); where it ends is the
+//         strictest of the k-th token, the first whose prefix weighs top_p of the k
+//         tokens' weight, and the last with w_j >= min_p
+//   token: the lowest kept j with  sum_{kept i <= j} w_i > u sum_kept w
+//
+// Choices hang on sums next to borders, so the weights are 64-bit integers
+// (2^43 for the largest): their sums are the same in any order, across warps, blocks
+// and passes.  Weights above 2^-12 are good to 2^-38 of themselves (x = (z - m) log2(e) / T
+// in two float32s, a table of 2^(i/64), and the rest of the exponential in two parts);
+// smaller ones to float32's rounding, 2^-36 of the largest weight.
+//
+// A row is a cluster of blocks, each with a slice of it.  Passes over the row:
+//   1 the maximum;
+//   2 (top-k or top-p) a histogram of counts over 8192 equal steps of x, 45 octaves.
+//     It gives the k-th token's step exactly, and the top-p step by the weight at the
+//     steps' middles, to a fraction of a percent;
+//   3 the tokens of the steps in question go into a list (up to 2048, sorted in the
+//     first block), and the weights of those above them are summed: the cut is found exactly
+//     there.  A list that holds all that is kept gives the token as well;
+//   4 otherwise sums over the kept tokens by slices, warps and packs lead to the token.
+// Steps that hold more than the list (many equal logits) are cut by bisection over
+// values with a sum over the row each, then by a search for the last of the equal ones.
+#include <cmath>
+#include <new>
+
+#include "plan_state.h"
+#include "row_packs.cuh"
+
+namespace olc {
+namespace sample {
+
+using u64 = unsigned long long;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 8192;
+constexpr int kOctaves = 45;            // below 2^-45 of the largest a weight is 0
+constexpr int kList = 2048;
+constexpr int kOne = 43;                // the largest weight is 2^43; vocab <= 2^20
+constexpr float kHeavy = -12.f;         // x from which on weights are formed in two parts
+
+struct Power {                          // 2^(i/64)
+    u64 fixed;                          // scaled by 2^43
+    float hi, lo;
+};
+
+struct Params {
+    const void* logits;
+    const float* uniforms;
+    const float* temperature;   // may be null: 1
+    const int* top_k;           // may be null: all
+    const float* top_p;         // may be null: 1
+    const float* min_p;         // may be null: 0
+    int64_t* tokens;
+    float* logprob;             // may be null
+    int64_t pitch;
+    int vocab;
+    int cluster;
+    Power powers[64];
+};
+
+// The row's scale: x = (z - m) c with c = log2(e) / T in two parts
+struct Scale {
+    float m, hi, lo;
+    float least;            // z - m is not taken below this one (x = -64, where weights are 0)
+    float per_step;         // bins: (m - z) per_step
+};
+
+// what one block tells the others of its cluster
+struct Found {
+    u64 a, b, c;
+    int i, j;
+};
+
+struct Shared {
+    Power powers[64];
+    u64 warp[kWarps], warp2[kWarps];
+    u64 exchange[2][2];         // [parity]: sums of this block
+    Found found[2];             // of the first block: [parity]
+    int listed;                 // entries of this block's list
+    Scale scale;
+    double min_distance;
+    unsigned min_key;
+    alignas(16) unsigned bins[kBins];   // counts of this block, then (its share of the bins) of the cluster; later
+                                        // weights by rank
+    alignas(16) u64 list[kList];        // key above ~index; the first block's takes the others' in
+    u64 weight[kList];
+};
+
+// ---- values and weights -------------------------------------------------------
+
+// Unsigned order of the values: -inf lowest, -0 equal to +0 (no NaN comes here)
+__device__ __forceinline__ unsigned order_key(float z) {
+    const unsigned b = __float_as_uint(z + 0.0f);
+    return (b >> 31) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(unsigned k) { return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k); }
+__device__ __forceinline__ u64 entry_of(float z, int i) { return ((u64)order_key(z) << 32) | (unsigned)~i; }
+__device__ __forceinline__ int index_of(u64 entry) { return (int)~(unsigned)entry; }
+__device__ __forceinline__ float value_of(u64 entry) { return key_value((unsigned)(entry >> 32)); }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// By one thread: double precision costs 64 times as much.  `min_distance`: w >= min_p
+// <=> z - m >= it.
+__device__ __forceinline__ Scale scale_of(float temperature, float min_p, double& min_distance) {
+    Scale s;
+    s.m = 0.f;
+    const double heat = (double)fminf(fmaxf(temperature, 0x1p-96f), 0x1p96f);
+    const double c = 1.4426950408889634 / heat;
+    s.hi = (float)c;
+    s.lo = (float)(c - (double)s.hi);
+    s.least = -64.f / s.hi;
+    s.per_step = s.hi * ((float)kBins / kOctaves);
+    min_distance = min_p > 0.f ? heat * log((double)min_p) : 0.0;
+    return s;
+}
+
+__device__ __forceinline__ float step_of(float z, const Scale& s) { return (s.m - z) * s.per_step; }
+
+// x in two parts
+__device__ __forceinline__ void exponent(float z, const Scale& s, float& hi, float& lo) {
+    float d = z - s.m;
+    const float b = z - d;                      // Knuth's two-sum: what the difference lost
+    float e = (z - (d + b)) + (b - s.m);
+    if (!(d >= s.least)) {
+        d = s.least;
+        e = 0.f;
+    }
+    hi = d * s.hi;
+    lo = fmaf(e, s.hi, fmaf(d, s.lo, fmaf(d, s.hi, -hi)));
+}
+
+constexpr float kMagic = 12582912.f;            // 1.5 2^23: adding it rounds to an integer in the low bits
+constexpr float kLn2 = 0.69314718055994531f, kLn2Lo = 0.69314718055994531 - (double)0.69314718055994531f;
+
+// 2^x, x = hi + lo in [kHeavy, 0]: 2^(i/64) (1 + e), e = 2^r - 1 with |r| <= 2^-7
+__device__ __forceinline__ u64 heavy_weight(float hi, float lo, const Power* powers) {
+    const float rounded = fmaf(hi, 64.f, kMagic);
+    const int k = __float_as_int(rounded) - __float_as_int(kMagic);
+    const float r = fmaf(rounded - kMagic, -0x1p-6f, hi);       // exact
+    const Power t = powers[k & 63];
+    // r ln 2 in two parts, and the higher terms of the exponential's series
+    const float ph = r * kLn2;
+    const float pl = fmaf(lo, kLn2, fmaf(r, kLn2Lo, fmaf(r, kLn2, -ph)));
+    const float s = ph + pl;
+    const float q = s * s * fmaf(s, fmaf(s, 1.f / 24.f, 1.f / 6.f), 0.5f);
+    const float a = t.hi * ph;
+    const float rest = fmaf(t.lo, ph, fmaf(t.hi, pl + q, fmaf(t.hi, ph, -a)));
+    const long long w = (long long)t.fixed + __float2ll_rn(a * 0x1p43f) + __float2int_rn(rest * 0x1p43f);
+    const int down = -(k >> 6);
+    return (u64)(w + ((1ll << down) >> 1)) >> down;
+}
+
+// 2^x below 2^-12: the series to the seventh power, |f| <= ln(2) / 2 (the next term is
+// 2^-27 at most)
+__device__ __forceinline__ unsigned light_weight(float hi, float lo) {
+    const float rounded = hi + kMagic;
+    const int n = __float_as_int(rounded) - __float_as_int(kMagic);
+    const float f = ((hi - (rounded - kMagic)) + lo) * kLn2;
+    float p = fmaf(f, 1.f / 5040.f, 1.f / 720.f);
+    p = fmaf(p, f, 1.f / 120.f);
+    p = fmaf(p, f, 1.f / 24.f);
+    p = fmaf(p, f, 1.f / 6.f);
+    p = fmaf(p, f, 0.5f);
+    p = fmaf(p, f, 1.f);
+    p = fmaf(p, f, 1.f);
+    return __float2uint_rn(__int_as_float(__float_as_int(p) + ((n + kOne) << 23)));
+}
+
+__device__ __forceinline__ u64 weight_of(float z, const Scale& s, const Power* powers) {
+    float hi, lo;
+    exponent(z, s, hi, lo);
+    return hi >= kHeavy ? heavy_weight(hi, lo, powers) : light_weight(hi, lo);
+}
+
+// ---- a block's part of the row --------------------------------------------------
+
+// The row as 16-byte packs from the boundary at or before its start; places
+// outside of the row read as -inf.
+template <typename T>
+struct Row {
+    static constexpr int V = 16 / sizeof(T);
+    const T* row;
+    int off, vocab, packs;
+    int v0, v1;             // this block's
+    __device__ __forceinline__ Row(const Params& p, int64_t r, int rank) {
+        row = static_cast<const T*>(p.logits) + r * p.pitch;
+        vocab = p.vocab;
+        off = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+        packs = (off + vocab + V - 1) / V;
+        v0 = (int)((int64_t)packs * rank / p.cluster);
+        v1 = (int)((int64_t)packs * (rank + 1) / p.cluster);
+    }
+    __device__ __forceinline__ int first_index(int v) const { return v * V - off; }
+    __device__ __forceinline__ void get(int v, float (&z)[V]) const {
+        const int i = first_index(v);
+        if (i >= 0 && i + V <= vocab) {
+            const uint4 k = __ldg(reinterpret_cast<const uint4*>(row + i));
+            const T* e = reinterpret_cast<const T*>(&k);
+#pragma unroll
+            for (int q = 0; q < V; ++q) z[q] = Num<T>::to_acc(e[q]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < V; ++q)
+                z[q] = i + q >= 0 && i + q < vocab ? Num<T>::to_acc(row[i + q]) : -INFINITY;
+        }
+    }
+};
+
+// ---- the cluster ------------------------------------------------------------------
+
+__device__ __forceinline__ unsigned remote(const void* local, int rank) {
+    unsigned at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(local)), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ u64 read64(const u64* local, int rank) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(local, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned read32(const void* local, int rank) {
+    unsigned v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(local, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void write64(u64* local, int rank, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(local, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void write32(int* local, int rank, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote(local, rank)), "r"(v) : "memory");
+}
+// A block's view of its cluster.  Every call is made by all threads of all blocks.
+struct Team {
+    Shared& sh;
+    int rank, size;
+    int parity;
+
+    // all blocks' writes to shared memory before it are seen after it
+    __device__ __forceinline__ void barrier() {
+        if (size == 1) {
+            __syncthreads();
+            return;
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    static __device__ __forceinline__ u64 warp_add(u64 v) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        return v;
+    }
+    // Sums over the cluster; `before`: over the lower ranks.  The warps' sums stay in
+    // sh.warp (and warp2) until the next call.
+    __device__ __forceinline__ void sum(u64& a, u64& b, u64& a_before, u64& b_before) {
+        const u64 wa = warp_add(a), wb = warp_add(b);
+        __syncthreads();                        // the last call's sh.warp has been read
+        if ((threadIdx.x & 31) == 0) {
+            sh.warp[threadIdx.x >> 5] = wa;
+            sh.warp2[threadIdx.x >> 5] = wb;
+        }
+        __syncthreads();
+        a = b = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            a += sh.warp[w];
+            b += sh.warp2[w];
+        }
+        a_before = b_before = 0;
+        if (size == 1) return;
+        parity ^= 1;
+        if (threadIdx.x == 0) {
+            sh.exchange[parity][0] = a;
+            sh.exchange[parity][1] = b;
+        }
+        barrier();
+        a = b = 0;
+        for (int r = 0; r < size; ++r) {
+            if (r == rank) {
+                a_before = a;
+                b_before = b;
+            }
+            a += read64(&sh.exchange[parity][0], r);
+            b += read64(&sh.exchange[parity][1], r);
+        }
+    }
+    __device__ __forceinline__ u64 sum(u64 a) {
+        u64 b = 0, x, y;
+        sum(a, b, x, y);
+        return a;
+    }
+    __device__ __forceinline__ float maximum(float v) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
+        if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = __float_as_uint(v);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v = max_nan(v, __uint_as_float((unsigned)sh.warp[w]));
+        if (size == 1) return v;
+        parity ^= 1;
+        if (threadIdx.x == 0) sh.exchange[parity][0] = __float_as_uint(v);
+        barrier();
+        for (int r = 0; r < size; ++r) v = max_nan(v, __uint_as_float((unsigned)read64(&sh.exchange[parity][0], r)));
+        return v;
+    }
+    // One thread of the cluster has told what it found (below); all get it.
+    __device__ __forceinline__ Found told() {
+        barrier();
+        Found f;
+        const Found& at = sh.found[parity];
+        f.a = read64(&at.a, 0);
+        f.b = read64(&at.b, 0);
+        f.c = read64(&at.c, 0);
+        f.i = (int)read32(&at.i, 0);
+        f.j = (int)read32(&at.j, 0);
+        parity ^= 1;                            // the next one goes elsewhere
+        return f;
+    }
+    __device__ __forceinline__ void tell(Found f) {
+        Found& at = sh.found[parity];
+        write64(&at.a, 0, f.a);
+        write64(&at.b, 0, f.b);
+        write64(&at.c, 0, f.c);
+        write32(&at.i, 0, f.i);
+        write32(&at.j, 0, f.j);
+    }
+};
+
+// inclusive sum over the lanes below and this one
+__device__ __forceinline__ u64 warp_scan(u64 v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const u64 o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// Exclusive sums over the block's threads in order, and over `slot`'s warps.
+__device__ __forceinline__ u64 block_scan(u64 v, u64* slot) {
+    const u64 inclusive = warp_scan(v);
+    // (lane 0 stores: with the store in lane 31, as nvcc 13.0 compiled this function, the
+    // place of an 8-byte word was off its boundary)
+    const u64 total = __shfl_sync(0xffffffffu, inclusive, 31);
+    const int warp = threadIdx.x >> 5;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) slot[warp] = total;
+    __syncthreads();
+    u64 before = inclusive - v;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const u64 other = slot[w];
+        before += w < warp ? other : 0;
+    }
+    return before;
+}
+
+// The sum of value(z, index) over the row.
+template <typename T, typename F>
+__device__ __forceinline__ u64 row_sum(const Row<T>& row, Team& team, F&& value) {
+    u64 s = 0;
+    for (int v = row.v0 + (int)threadIdx.x; v < row.v1; v += kThreads) {
+        float z[Row<T>::V];
+        row.get(v, z);
+#pragma unroll
+        for (int q = 0; q < Row<T>::V; ++q) s += value(z[q], row.first_index(v) + q);
+    }
+    return team.sum(s);
+}
+
+// The lowest index at which the running sum of value(z, index) exceeds `target`
+// (below the total): i, the value there: a, the total: b, and j, the bits of z.
+// target_of(total) gives the target.
+template <typename T, typename F, typename G>
+__device__ __forceinline__ Found locate(const Row<T>& row, Team& team, F&& value, G&& target_of) {
+    constexpr int V = Row<T>::V;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto part = [&](int begin, int end) {       // of packs, by one warp
+        u64 s = 0;
+        for (int v = begin + lane; v < end; v += 32) {
+            float z[V];
+            row.get(v, z);
+#pragma unroll
+            for (int q = 0; q < V; ++q) s += value(z[q], row.first_index(v) + q);
+        }
+        return s;
+    };
+    auto cut = [](int begin, int end, int k) { return begin + (int)((int64_t)(end - begin) * k / kWarps); };
+    u64 own = part(cut(row.v0, row.v1, warp), cut(row.v0, row.v1, warp + 1));
+    u64 sum = own, none = 0, before, none_before;
+    team.sum(sum, none, before, none_before);
+    const u64 total = sum;
+    u64 target = target_of(total);
+    u64 mine = 0;
+    for (int w = 0; w < kWarps; ++w) mine += team.sh.warp[w];
+    if (target >= before && target < before + mine) {        // the whole block
+        target -= before;
+        int at = 0;
+        while (at < kWarps - 1 && target >= team.sh.warp[at]) target -= team.sh.warp[at++];
+        const int b1 = cut(row.v0, row.v1, at), e1 = cut(row.v0, row.v1, at + 1);
+        __syncthreads();
+        own = Team::warp_add(part(cut(b1, e1, warp), cut(b1, e1, warp + 1)));
+        if (lane == 0) team.sh.warp[warp] = own;
+        __syncthreads();
+        at = 0;
+        while (at < kWarps - 1 && target >= team.sh.warp[at]) target -= team.sh.warp[at++];
+        if (warp == 0) {
+            const int b2 = cut(b1, e1, at), e2 = cut(b1, e1, at + 1);
+            bool done = false;
+            for (int base = b2; base < e2 && !done; base += 32) {
+                // a pack a lane
+                float z[V];
+                u64 w[V], s = 0;
+#pragma unroll
+                for (int q = 0; q < V; ++q) z[q] = -INFINITY;
+                if (base + lane < e2) row.get(base + lane, z);
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    w[q] = base + lane < e2 ? value(z[q], row.first_index(base + lane) + q) : 0;
+                    s += w[q];
+                }
+                const u64 sums = warp_scan(s);
+                const unsigned past = __ballot_sync(0xffffffffu, sums > target);
+                if (past && lane == __ffs(past) - 1) {
+                    u64 reach = sums - s;
+                    bool found = false;
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        reach += w[q];
+                        if (!found && reach > target) {
+                            found = true;
+                            team.tell(Found{w[q], total, 0, row.first_index(base + lane) + q, (int)__float_as_uint(z[q])});
+                        }
+                    }
+                }
+                done = past != 0;
+                target -= __shfl_sync(0xffffffffu, sums, 31);        // used only where nothing was found
+            }
+        }
+    }
+    return team.told();
+}
+
+// ---- the list ----------------------------------------------------------------------
+
+// descending order of n entries, by the block (n <= kList)
+__device__ __forceinline__ int sort_list(u64* list, int n) {
+    int size = 32;
+    while (size < n) size *= 2;
+    for (int i = n + (int)threadIdx.x; i < size; i += kThreads) list[i] = 0;
+    __syncthreads();
+    for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+                const int i = 2 * t - (t & (j - 1));
+                const u64 x = list[i], y = list[i + j];
+                if ((x < y) == ((i & k) == 0)) {
+                    list[i] = y;
+                    list[i + j] = x;
+                }
+            }
+            __syncthreads();
+        }
+    return size;
+}
+
+// sh.weight: running sums of the first n
+__device__ __forceinline__ void scan_weights(Shared& sh, int n) {
+    constexpr int PER = kList / kThreads;
+    const int first = threadIdx.x * PER;
+    u64 w[PER], s = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        w[i] = first + i < n ? sh.weight[first + i] : 0;
+        s += w[i];
+    }
+    u64 before = block_scan(s, sh.warp);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        before += w[i];
+        if (first + i < n) sh.weight[first + i] = before;
+    }
+    __syncthreads();
+}
+
+// the first of n running sums that is at least `least` (n if none)
+__device__ __forceinline__ int first_reaching(const u64* sums, int n, u64 least) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (sums[mid] >= least) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// ---- shares -------------------------------------------------------------------------
+
+// p = mantissa 2^-shift, 0 < p < 1
+__device__ __forceinline__ void parts_of(float p, u64& mantissa, int& shift) {
+    const unsigned b = __float_as_uint(p);
+    const int e = (int)(b >> 23);
+    mantissa = e ? (b & 0x7FFFFFu) | 0x800000u : b & 0x7FFFFFu;
+    shift = 150 - (e ? e : 1);
+}
+// floor(p s) and ceil(p s)
+__device__ __forceinline__ u64 share_floor(float p, u64 s) {
+    if (!(p > 0.f)) return 0;
+    u64 m;
+    int shift;
+    parts_of(fminf(p, 0x1.fffffep-1f), m, shift);
+    return shift >= 128 ? 0 : (u64)(((unsigned __int128)m * s) >> shift);
+}
+__device__ __forceinline__ u64 share_ceil(float p, u64 s) {
+    u64 m;
+    int shift;
+    parts_of(p, m, shift);
+    if (shift >= 100) return s ? 1 : 0;         // m s is below 2^87
+    const unsigned __int128 v = (unsigned __int128)m * s, one = (unsigned __int128)1 << shift;
+    return (u64)((v + one - 1) >> shift);
+}
+
+__device__ __forceinline__ void write_result(const Params& p, int64_t row, int token, float z, u64 w, u64 total,
+                                             const Scale& s) {
+    p.tokens[row] = token;
+    if (!p.logprob) return;
+    const float other = (float)(total - w) / (float)total;
+    float lp;
+    if (other < 0.5f) {
+        lp = log1pf(-other);
+    } else {
+        float hi, lo;
+        exponent(z, s, hi, lo);
+        const int e = 63 - __clzll((long long)total);
+        const float mantissa = (float)total * __int_as_float((127 - e) << 23);
+        lp = ((hi - (float)(e - kOne)) + (lo - log2f(mantissa))) * kLn2;
+    }
+    p.logprob[row] = lp;
+}
+
+// ---- the kernel ----------------------------------------------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(128) unsigned char memory[];
+    Shared& sh = *reinterpret_cast<Shared*>(memory);
+    constexpr int V = Row<T>::V;
+    const int64_t r = blockIdx.x / (unsigned)p.cluster;
+    Team team{sh, (int)(blockIdx.x % (unsigned)p.cluster), p.cluster, 0};
+    const Row<T> row(p, r, team.rank);
+    const int t = threadIdx.x;
+    const float temperature = p.temperature ? p.temperature[r] : 1.f, u = p.uniforms[r];
+    const float top_p = p.top_p ? p.top_p[r] : 1.f, min_p = p.min_p ? p.min_p[r] : 0.f;
+    const int given_k = p.top_k ? p.top_k[r] : 0;
+    const int top_k = given_k > 0 && given_k < p.vocab ? given_k : 0;
+    if (t < 64) sh.powers[t] = p.powers[t];
+    if (t == 0) {
+        sh.listed = 0;
+        sh.scale = scale_of(temperature, min_p, sh.min_distance);
+    }
+    const bool counts = top_k > 0 || top_p < 1.f;
+    if (counts)
+        for (int i = t; i < kBins; i += kThreads) sh.bins[i] = 0;
+
+    float m = -INFINITY;
+    for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+        float z[V];
+        row.get(v, z);
+#pragma unroll
+        for (int q = 0; q < V; ++q) m = max_nan(m, z[q]);
+    }
+    m = team.maximum(m);
+    const bool wrong = !(m < INFINITY) || !(temperature >= 0.f && temperature < INFINITY) || u != u || top_p != top_p ||
+                       min_p != min_p;
+    if (wrong || m == -INFINITY) {                           // the whole cluster
+        if (team.rank == 0 && t == 0) {
+            p.tokens[r] = -1;
+            if (p.logprob) p.logprob[r] = wrong ? __uint_as_float(0x7FC00000u) : -INFINITY;
+        }
+        team.barrier();                                      // nobody leaves while others read its memory
+        return;
+    }
+    if (t == 0) {
+        sh.scale.m = m;
+        sh.min_key = min_p > 0.f ? order_key(__double2float_ru((double)m + sh.min_distance)) : 0;
+    }
+    __syncthreads();
+    const Scale s = sh.scale;
+    const unsigned max_key = order_key(m);
+    if (temperature == 0.f || top_k == 1 || !(top_p > 0.f) || min_p > 1.f) {
+        // the first of the order
+        const Found f = locate(row, team, [&](float z, int) -> u64 { return order_key(z) == max_key; }, [](u64) -> u64 { return 0; });
+        if (team.rank == 0 && t == 0) {
+            p.tokens[r] = f.i;
+            if (p.logprob) p.logprob[r] = 0.f;
+        }
+        team.barrier();
+        return;
+    }
+    // the last entry of the order that is kept, by top-k and top-p so far and by min_p
+    u64 cut = 0;
+    const u64 min_cut = (u64)sh.min_key << 32;
+    if (counts) {
+        // 2: the histogram.  Each block takes a share of the bins afterwards, each thread
+        // `each` in a row; bin b lies where the threads' b-th bins are side by side.
+        const int log_each = 31 - __clz(kBins / kThreads / team.size), each = 1 << log_each;
+        const int stride = kBins >> log_each, mine = team.rank * kThreads + t;
+        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+            float z[V];
+            row.get(v, z);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float f = step_of(z[q], s);
+                if (f < (float)kBins) {
+                    const int b = (int)f;
+                    atomicAdd(&sh.bins[(b & (each - 1)) * stride + (b >> log_each)], 1u);
+                }
+            }
+        }
+        team.barrier();
+        u64 count = 0, mass = 0;
+        auto bin_weight = [](int b) { return (u64)(exp2f((b + 0.5f) * -((float)kOctaves / kBins)) * 0x1p43f) + 1; };
+        for (int i = 0; i < each; ++i) {
+            unsigned* const at = &sh.bins[i * stride + mine];
+            unsigned k = *at;
+            if (team.size > 1) {
+                for (int other = 1; other < team.size; ++other) k += read32(at, (team.rank + other) & (team.size - 1));
+                *at = k;                        // only this block reads its share of its bins
+            }
+            count += k;
+            mass += k * bin_weight(mine * each + i);
+        }
+        // running counts and weights over the cluster
+        u64 counted = count, weighed = mass, c0, m0;
+        team.sum(counted, weighed, c0, m0);
+        c0 += block_scan(count, sh.warp);
+        m0 += block_scan(mass, sh.warp2);
+        // calls f(bin, count before it, weight before it) for this thread's bins in order
+        auto bins_in_order = [&](auto&& f) {
+            u64 c = c0, w = m0;
+            for (int i = 0; i < each; ++i) {
+                const unsigned k = sh.bins[i * stride + mine];
+                const int b = mine * each + i;
+                f(b, c, w, k);
+                c += k;
+                w += k * bin_weight(b);
+            }
+        };
+        // Tokens of steps [from, to) that `cut` keeps go into the block's list; the
+        // weights of all that it keeps are added to `all`, those of lower steps to `above`.
+        auto collect = [&](float from, float to, bool weigh, u64& all, u64& above) {
+            for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+                float z[V];
+                row.get(v, z);
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    const float f = step_of(z[q], s);
+                    const u64 entry = entry_of(z[q], row.first_index(v) + q);
+                    if (!(f < (float)kBins) || entry < cut) continue;
+                    if (f >= from && f < to) {
+                        const int at = atomicAdd(&sh.listed, 1);
+                        if (at < kList) sh.list[at] = entry;
+                    }
+                    if (!weigh) continue;
+                    const u64 w = weight_of(z[q], s, sh.powers);
+                    all += w;
+                    if (f < from) above += w;
+                }
+            }
+        };
+        // (the first block) takes in the other blocks' entries, which are kList together at
+        // most; their number
+        auto gather = [&] {
+            int size = min(sh.listed, kList);
+            for (int k = 1; k < team.size; ++k) {
+                const int more = min((int)read32(&sh.listed, k), kList - size);
+                for (int i = t; i < more; i += kThreads) sh.list[size + i] = read64(&sh.list[i], k);
+                size += more;
+            }
+            return size;
+        };
+        // the list's order and running weights
+        auto order_list = [&](int size) {
+            sort_list(sh.list, size);
+            for (int i = t; i < size; i += kThreads) sh.weight[i] = weight_of(value_of(sh.list[i]), s, sh.powers);
+            __syncthreads();
+            scan_weights(sh, size);
+        };
+        // The list holds, in order, all that is kept, `size` entries of it: the token (first block)
+        auto choose = [&](int size) {
+            const u64 total = sh.weight[size - 1];
+            // single weights again, and the entries by index
+            u64 w[kList / kThreads];
+#pragma unroll
+            for (int k = 0; k < kList / kThreads; ++k) {
+                const int i = t + k * kThreads;
+                w[k] = i < size ? sh.weight[i] - (i ? sh.weight[i - 1] : 0) : 0;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kList / kThreads; ++k) {
+                const int i = t + k * kThreads;
+                if (i < size) sh.list[i] = (sh.list[i] << 32) | (unsigned)i;
+            }
+            __syncthreads();
+            u64* const by_rank = reinterpret_cast<u64*>(sh.bins);        // the counts are done with
+            static_assert(sizeof(sh.bins) >= sizeof(sh.weight), "");
+#pragma unroll
+            for (int k = 0; k < kList / kThreads; ++k)
+                if (t + k * kThreads < size) by_rank[t + k * kThreads] = w[k];
+            sort_list(sh.list, size);
+            for (int i = t; i < size; i += kThreads) sh.weight[i] = by_rank[(int)(sh.list[i] & 0xFFFFFFFFu)];
+            __syncthreads();
+            scan_weights(sh, size);
+            if (t == 0) {
+                const int at = first_reaching(sh.weight, size, share_floor(u, total) + 1);
+                const int token = (int)~(unsigned)(sh.list[at] >> 32);
+                const u64 weight = sh.weight[at] - (at ? sh.weight[at - 1] : 0);
+                const T* z = row.row;
+                write_result(p, r, token, Num<T>::to_acc(z[token]), weight, total, s);
+            }
+        };
+        // how many of the list's first `size` entries min_p keeps
+        auto kept_of = [&](int size) {
+            int lo = 0, hi = size;                              // descending order
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (sh.list[mid] < min_cut) hi = mid;
+                else lo = mid + 1;
+            }
+            return lo;                                          // at least 1: the largest
+        };
+        // The cut at which the sum of value(z) over kept entries reaches `least`, by
+        // bisection over keys, then among equal ones by index.
+        auto bisect = [&](auto&& value, u64 least) {
+            unsigned lo = 0, hi = max_key;                      // sum(key >= lo) >= least
+            while (lo < hi) {
+                const unsigned mid = hi - (hi - lo) / 2;
+                const u64 sum = row_sum(row, team, [&](float z, int i) -> u64 {
+                    return order_key(z) >= mid && entry_of(z, i) >= cut ? value(z) : 0;
+                });
+                if (sum >= least) lo = mid;
+                else hi = mid - 1;
+            }
+            const u64 above = row_sum(row, team, [&](float z, int i) -> u64 {
+                return order_key(z) > lo && entry_of(z, i) >= cut ? value(z) : 0;
+            });
+            const Found f = locate(
+                row, team,
+                [&](float z, int i) -> u64 { return order_key(z) == lo && entry_of(z, i) >= cut ? value(z) : 0; },
+                [&](u64) -> u64 { return least - above - 1; });
+            cut = ((u64)lo << 32) | (unsigned)~f.i;
+        };
+        // the first block is done with the list; `entry` is the new cut
+        auto cut_at = [&](u64 entry, bool good) {
+            __syncthreads();                                    // the block has read what it needs
+            if (t == 0) team.tell(Found{entry, 0, 0, good, 0});
+        };
+        // ... and every block hears of it, and empties its list for the next collection
+        auto cut_told = [&] {
+            const Found f = team.told();
+            if (t == 0) sh.listed = 0;
+            return f;
+        };
+
+        u64 unused = 0;
+        u64 known = weighed;                                    // estimate of the k tokens' weight
+        if (top_k && counted > (u64)top_k) {
+            bins_in_order([&](int b, u64 c, u64 w, unsigned k) {
+                if (c < (u64)top_k && c + k >= (u64)top_k)
+                    team.tell(Found{c, c + k, w + ((u64)top_k - c) * bin_weight(b), b, 0});
+            });
+            const Found f = team.told();
+            known = f.c;
+            const bool whole = f.b <= (u64)kList;               // the list holds all of them
+            if (whole || f.b - f.a <= (u64)kList) {
+                collect(whole ? 0.f : (float)f.i, (float)(f.i + 1), false, unused, unused);
+                team.barrier();
+                if (team.rank == 0) {
+                    const int size = gather();
+                    order_list(size);
+                    if (whole) {
+                        int keep = min(top_k, size);
+                        if (top_p < 1.f)
+                            keep = min(keep, first_reaching(sh.weight, keep, share_ceil(top_p, sh.weight[keep - 1])) + 1);
+                        choose(min(keep, kept_of(keep)));
+                    } else {
+                        cut_at(sh.list[top_k - 1 - (int)f.a], true);
+                    }
+                }
+                if (whole) {
+                    team.barrier();                             // nobody leaves before the list is written
+                    return;
+                }
+                cut = cut_told().a;
+            } else {
+                bisect([](float) -> u64 { return 1; }, (u64)top_k);
+            }
+        }
+        if (top_p < 1.f) {
+            // the steps around the estimate; wider ones where it was not good enough
+            for (float off = 0x1p-10f;; off *= 8.f) {
+                const float near = (float)known * top_p;
+                const u64 last = weighed - 1;
+                const u64 least = min((u64)(near * fmaxf(1.f - off, 0.f)), last), most = min((u64)(near * (1.f + off)), last);
+                bins_in_order([&](int b, u64 c, u64 w, unsigned k) {
+                    if (w <= least && least < w + k * bin_weight(b)) team.tell(Found{c, 0, 0, b, 0});
+                });
+                Found low = team.told();
+                bins_in_order([&](int b, u64 c, u64 w, unsigned k) {
+                    if (w <= most && most < w + k * bin_weight(b)) team.tell(Found{c + k, 0, 0, b, 0});
+                });
+                const Found high = team.told();
+                if (high.a <= (u64)kList) low = Found{0, 0, 0, 0, 0};        // all of the prefix
+                if (high.a - low.a > (u64)kList || off > 8.f) {
+                    const u64 all = row_sum(row, team, [&](float z, int i) -> u64 {
+                        return entry_of(z, i) >= cut ? weight_of(z, s, sh.powers) : 0;
+                    });
+                    bisect([&](float z) { return weight_of(z, s, sh.powers); }, share_ceil(top_p, all));
+                    break;
+                }
+                u64 all = 0, above = 0, b1, b2;
+                collect((float)low.i, (float)(high.i + 1), true, all, above);
+                team.sum(all, above, b1, b2);
+                if (team.rank == 0) {
+                    const int size = gather();
+                    const u64 target = share_ceil(top_p, all);
+                    order_list(size);
+                    const bool good = size > 0 && above < target && target - above <= sh.weight[size - 1];
+                    const int at = good ? first_reaching(sh.weight, size, target - above) : 0;
+                    if (good && low.i == 0) choose(min(at + 1, kept_of(at + 1)));
+                    cut_at(good ? sh.list[at] : 0, good);
+                }
+                const Found f = cut_told();
+                if (!f.i) continue;
+                if (low.i == 0) {                               // chosen
+                    team.barrier();                             // nobody leaves while others read its memory
+                    return;
+                }
+                cut = f.a;
+                break;
+            }
+        }
+    }
+    // 4: the token by sums over all that is kept
+    cut = max(cut, min_cut);
+    const Found f = locate(
+        row, team,
+        [&](float z, int i) -> u64 { return entry_of(z, i) >= cut ? weight_of(z, s, sh.powers) : 0; },
+        [&](u64 sum) -> u64 { return share_floor(u, sum); });
+    if (team.rank == 0 && t == 0) write_result(p, r, f.i, __int_as_float(f.j), f.a, f.b, s);
+    team.barrier();
+}
+
+// ---- host side -------------------------------------------------------------
+
+// Blocks a row: as many as keep every block resident, two an SM, with two rounds of
+// packs each or more.
+inline int cluster_of(int64_t rows, int64_t packs, int sm_count) {
+    int c = 1;
+    while (c < kMaxCluster && rows * c * 2 <= 2 * (int64_t)sm_count && packs >= (int64_t)c * 2 * 2 * kThreads) c *= 2;
+    return c;
+}
+
+template <typename T>
+cudaError_t forward_as(Params p, int64_t rows, int sm_count, cudaStream_t s) {
+    p.cluster = cluster_of(rows, ceil_div(p.vocab, 16 / sizeof(T)), sm_count);
+    for (int i = 0; i < 64; ++i) {
+        const double v = std::exp2(i / 64.0);
+        p.powers[i].fixed = (u64)std::llrint(std::ldexp(v, kOne));
+        p.powers[i].hi = (float)v;
+        p.powers[i].lo = (float)(v - (double)p.powers[i].hi);
+    }
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(sample_kernel<T>), (int)sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * p.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
+}
+
+}  // namespace sample
+}  // namespace olc
+
+using namespace olc;
+
+struct olc_sample_plan {
+    PlanState state;
+    olc_dtype dtype;
+    int64_t rows, vocab;
+};
+
+extern "C" {
+
+olc_status olc_sample_plan_create(int64_t rows, int64_t vocab, olc_dtype dtype, olc_sample_plan** out) {
+    if (!out) return OLC_ERR_NULL;
+    *out = nullptr;
+    if (!plan_dtype_ok(dtype)) return OLC_ERR_DTYPE;
+    if (rows < 0 || vocab < 0) return OLC_ERR_NEGATIVE_DIM;
+    if (rows >= (int64_t(1) << 27) || vocab == 0 || vocab > (int64_t(1) << 20)) return OLC_ERR_INVALID;
+    olc_sample_plan* p = new (std::nothrow) olc_sample_plan;
+    if (!p) return OLC_ERR_OOM;
+    p->state.init();
+    p->dtype = dtype;
+    p->rows = rows;
+    p->vocab = vocab;
+    *out = p;
+    return OLC_OK;
+}
+
+void olc_sample_plan_destroy(olc_sample_plan* plan) {
+    if (!plan) return;
+    plan->state.destroy();
+    delete plan;
+}
+
+olc_status olc_sample_forward(olc_sample_plan* plan, const void* logits, int64_t pitch, const float* uniforms,
+                              const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                              int64_t* tokens, float* logprob, void* stream) {
+    if (!plan) return OLC_ERR_NULL;
+    if (plan->rows == 0) return OLC_OK;
+    if (!logits || !uniforms || !tokens) return OLC_ERR_NULL;
+    const int64_t eb = plan_elem_bytes(plan->dtype);
+    if (plan->rows > 1 && (pitch < plan->vocab || !plan_fits(plan->rows, pitch, eb))) return OLC_ERR_INVALID;
+    if (plan_misaligned(logits, eb) || plan_misaligned(uniforms, 4) || plan_misaligned(temperature, 4) ||
+        plan_misaligned(top_k, 4) || plan_misaligned(top_p, 4) || plan_misaligned(min_p, 4) ||
+        plan_misaligned(tokens, 8) || plan_misaligned(logprob, 4))
+        return OLC_ERR_INVALID;
+    const olc_status st = plan->state.bind();
+    if (st != OLC_OK) return st;
+    sample::Params p{};
+    p.logits = logits;
+    p.uniforms = uniforms;
+    p.temperature = temperature;
+    p.top_k = top_k;
+    p.top_p = top_p;
+    p.min_p = min_p;
+    p.tokens = tokens;
+    p.logprob = logprob;
+    p.pitch = pitch;
+    p.vocab = (int)plan->vocab;
+    return by_type(plan->dtype, [&](auto tag) {
+        return plan_status(sample::forward_as<decltype(tag)>(p, plan->rows, plan->state.sm_count,
+                                                             static_cast<cudaStream_t>(stream)));
+    });
+}
+
+}  // extern "C"

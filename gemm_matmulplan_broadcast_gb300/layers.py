@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import DTYPE_CODES, GATES, _check, _memory_of, _stream_handle, load
+from .binding import DTYPE_CODES, GATES, NORMS, _check, _memory_of, _stream_handle, load
 
 ROW_DTYPES = ("float32", "float16", "bfloat16")
 
@@ -244,6 +244,145 @@ class TokenLogProbsPlan(_PlanHandle):
         return dlogits
 
 
+class EmbeddingPlan(_PlanHandle):
+    """Rows of a table [vocab, cols] by ``tokens`` ids (int64; a negative one
+    marks a place without a token), scaled, and the table's gradient."""
+
+    _destroy = "olc_embedding_plan_destroy"
+
+    def __init__(self, tokens: int, vocab: int, cols: int, dtype: str, scale: float = 1.0):
+        import torch
+        self.tokens, self.vocab, self.cols = int(tokens), int(vocab), int(cols)
+        self.dtype, self.scale = dtype, float(scale)
+        self._t, self._i64 = _torch_dtype(dtype), torch.int64
+        self._create("olc_embedding_plan_create", self.tokens, self.vocab, self.cols, self.scale, DTYPE_CODES[dtype])
+
+    def forward(self, table, tokens, Y, stream=None):
+        """Y[i] = scale * table[tokens[i]], zeros for a negative id."""
+        e, ep = _rows("table", table, self.vocab, self.cols, self._t)
+        y, yp = _rows("Y", Y, self.tokens, self.cols, self._t)
+        st = self.lib.olc_embedding_forward(self._h, e, ep, _flat("tokens", tokens, self.tokens, self._i64), y, yp,
+                                            _raw_stream(stream))
+        _check(st, "olc_embedding_forward")
+        return Y
+
+    def backward(self, dY, tokens, dtable, accumulate: bool = False, stream=None):
+        """dtable[v] = scale * the sum of dY over the places of token v (added
+        to what dtable holds with ``accumulate``)."""
+        dy, dyp = _rows("dY", dY, self.tokens, self.cols, self._t)
+        de, dep = _rows("dtable", dtable, self.vocab, self.cols, self._t)
+        st = self.lib.olc_embedding_backward(self._h, dy, dyp, _flat("tokens", tokens, self.tokens, self._i64), de, dep,
+                                             int(accumulate), _raw_stream(stream))
+        _check(st, "olc_embedding_backward")
+        return dtable
+
+
+class ResidualNormPlan(_PlanHandle):
+    """The step between two blocks, on the residual stream X and a block's
+    output F [rows, cols]: Y = X + scale * gate * n with n the norm of F
+    (``after``) or F itself, and Z = norm of Y for the next block; and its
+    gradients.  norm: layer or rms."""
+
+    _destroy = "olc_residual_norm_plan_destroy"
+
+    def __init__(self, rows: int, cols: int, dtype: str, eps: float = 1e-5, scale: float = 1.0, norm: str = "layer",
+                 after: bool = False):
+        import torch
+        if norm not in NORMS:
+            raise ValueError("norm must be one of %s" % sorted(NORMS))
+        self.rows, self.cols, self.dtype = int(rows), int(cols), dtype
+        self.eps, self.scale, self.norm, self.after = float(eps), float(scale), norm, bool(after)
+        self._t, self._f32 = _torch_dtype(dtype), torch.float32
+        self._create("olc_residual_norm_plan_create", self.rows, self.cols, self.eps, self.scale, NORMS[norm],
+                     int(self.after), DTYPE_CODES[dtype])
+
+    def _matrix(self, name, t):
+        return (None, self.cols) if t is None else _rows(name, t, self.rows, self.cols, self._t)
+
+    def _gate(self, name, t):
+        """A gate for each column has the pitch 0."""
+        if t is not None and t.dim() == 1:
+            return _flat(name, t, self.cols, self._t), 0
+        return self._matrix(name, t)
+
+    def _stats(self, t):
+        return _flat("stats", t, (4 if self.after else 2) * self.rows, self._f32)
+
+    def forward(self, X, F, Y, Z=None, gate=None, gamma=None, beta=None, after_gamma=None, after_beta=None, stats=None,
+                stream=None):
+        """Y and (unless None) Z.  gate: [cols], [rows, cols] or None; the
+        norms' weights: [cols] or None; stats: float32 [2, rows] (mean and rstd
+        of Y's rows; with ``after`` [4, rows], then those of F's) for the
+        backward call, or None."""
+        cols, t = self.cols, self._t
+        x, xp = _rows("X", X, self.rows, cols, t)
+        f, fp = _rows("F", F, self.rows, cols, t)
+        y, yp = _rows("Y", Y, self.rows, cols, t)
+        z, zp = self._matrix("Z", Z)
+        g, gp = self._gate("gate", gate)
+        st = self.lib.olc_residual_norm_forward(
+            self._h, x, xp, f, fp, g, gp, _flat("after_gamma", after_gamma, cols, t),
+            _flat("after_beta", after_beta, cols, t), _flat("gamma", gamma, cols, t), _flat("beta", beta, cols, t), y, yp,
+            z, zp, self._stats(stats), _raw_stream(stream))
+        _check(st, "olc_residual_norm_forward")
+        return Y
+
+    def backward(self, dY, dZ, F, Y, stats, gate=None, gamma=None, after_gamma=None, after_beta=None, dX=None, dF=None,
+                 dgate=None, dgamma=None, dbeta=None, dafter_gamma=None, dafter_beta=None, stream=None):
+        """The gradients of X, F, the gate and the norms' weights (each None to
+        skip it) from those of Y (None: zeros) and of Z (None: there is none),
+        the forward call's Y and stats, F, the gate and the weights."""
+        cols, t = self.cols, self._t
+        dy, dyp = self._matrix("dY", dY)
+        dz, dzp = self._matrix("dZ", dZ)
+        f, fp = self._matrix("F", F)
+        y, yp = self._matrix("Y", Y)
+        g, gp = self._gate("gate", gate)
+        dx, dxp = self._matrix("dX", dX)
+        df, dfp = self._matrix("dF", dF)
+        dg, dgp = self._gate("dgate", dgate)
+        if dgate is not None and gate is not None and (gp == 0) != (dgp == 0):
+            raise ValueError("dgate has shape %s, the gate %s" % (tuple(dgate.shape), tuple(gate.shape)))
+        st = self.lib.olc_residual_norm_backward(
+            self._h, dy, dyp, dz, dzp, f, fp, y, yp, self._stats(stats), g, gp, _flat("after_gamma", after_gamma, cols, t),
+            _flat("after_beta", after_beta, cols, t), _flat("gamma", gamma, cols, t), dx, dxp, df, dfp, dg, dgp,
+            _flat("dgamma", dgamma, cols, t), _flat("dbeta", dbeta, cols, t), _flat("dafter_gamma", dafter_gamma, cols, t),
+            _flat("dafter_beta", dafter_beta, cols, t), _raw_stream(stream))
+        _check(st, "olc_residual_norm_backward")
+        return dX, dF
+
+
+class SamplePlan(_PlanHandle):
+    """One token for each row of logits [rows, vocab] from one uniform number
+    a row, with temperature, top-k, top-p and min-p of the row's own."""
+
+    _destroy = "olc_sample_plan_destroy"
+
+    def __init__(self, rows: int, vocab: int, dtype: str):
+        import torch
+        self.rows, self.vocab, self.dtype = int(rows), int(vocab), dtype
+        self._t, self._f32 = _torch_dtype(dtype), torch.float32
+        self._i32, self._i64 = torch.int32, torch.int64
+        self._create("olc_sample_plan_create", self.rows, self.vocab, DTYPE_CODES[dtype])
+
+    def forward(self, logits, uniforms, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprob=None,
+                stream=None):
+        """tokens (int64 [rows]) and, unless None, logprob (float32 [rows]: the
+        log probability of each token among those that were left).  uniforms:
+        float32 [rows] in [0, 1); temperature, top_p, min_p: float32 [rows],
+        top_k: int32 [rows], or None (1, 1, 0, all); a temperature of 0 takes
+        the likeliest token, a top_k of 0 or less takes all.  A row that leaves
+        no token gives -1."""
+        rows, f32 = self.rows, self._f32
+        z, pitch = _rows("logits", logits, rows, self.vocab, self._t)
+        st = self.lib.olc_sample_forward(
+            self._h, z, pitch, _flat("uniforms", uniforms, rows, f32), _flat("temperature", temperature, rows, f32),
+            _flat("top_k", top_k, rows, self._i32), _flat("top_p", top_p, rows, f32), _flat("min_p", min_p, rows, f32),
+            _flat("tokens", tokens, rows, self._i64), _flat("logprob", logprob, rows, f32), _raw_stream(stream))
+        _check(st, "olc_sample_forward")
+        return tokens
+
+
 def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out=None, stream=None):
     """Layer norm of a CUDA tensor over its last axis through a fresh plan."""
     import torch
@@ -279,3 +418,47 @@ def token_log_probs(logits, tokens, top: int = 0, stream=None):
     with TokenLogProbsPlan(rows, vocab, str(logits.dtype).replace("torch.", ""), top) as plan:
         plan.forward(logits, tokens, logprob, entropy=entropy, top_logprob=best[0], top_index=best[1], stream=stream)
     return (logprob, entropy) + (best if top else ())
+
+
+def embedding(table, tokens, scale: float = 1.0, out=None, stream=None):
+    """scale * table[tokens] of a CUDA table [vocab, cols] and int64 ids of any
+    shape, through a fresh plan."""
+    import torch
+    vocab, cols = table.shape
+    if out is None:
+        with _memory_of(stream):
+            out = torch.empty(tokens.shape + (cols,), dtype=table.dtype, device=table.device)
+    with EmbeddingPlan(tokens.numel(), vocab, cols, str(table.dtype).replace("torch.", ""), scale) as plan:
+        return plan.forward(table, tokens, out, stream=stream)
+
+
+def residual_norm(X, F, gamma=None, beta=None, gate=None, after_gamma=None, after_beta=None, eps: float = 1e-5,
+                  scale: float = 1.0, norm: str = "layer", after: bool = False, stream=None):
+    """(Y, Z) of CUDA tensors through a fresh plan: Y = X + scale * gate * n
+    with n the norm of F (``after``) or F, Z = norm of Y."""
+    import torch
+    with _memory_of(stream):
+        Y, Z = (torch.empty_like(X, memory_format=torch.contiguous_format) for _ in range(2))
+    cols = X.shape[-1] if X.dim() else 0
+    rows = X.numel() // cols if cols else 0
+    with ResidualNormPlan(rows, cols, str(X.dtype).replace("torch.", ""), eps, scale, norm, after) as plan:
+        plan.forward(X, F, Y, Z=Z, gate=gate, gamma=gamma, beta=beta, after_gamma=after_gamma, after_beta=after_beta,
+                     stream=stream)
+    return Y, Z
+
+
+def sample(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+    """(tokens, logprob) of CUDA logits [rows, vocab] through a fresh plan; the
+    settings are numbers for all rows, or tensors [rows]."""
+    import torch
+    rows, vocab = logits.shape
+    with _memory_of(stream):
+        make = lambda of: torch.empty(rows, dtype=of, device=logits.device)  # noqa: E731
+        tokens, logprob = make(torch.int64), make(torch.float32)
+        each = lambda v, of, none: None if not torch.is_tensor(v) and v == none else (  # noqa: E731
+            v if torch.is_tensor(v) else make(of).fill_(v))
+        settings = {"temperature": each(temperature, torch.float32, 1), "top_k": each(top_k, torch.int32, 0),
+                    "top_p": each(top_p, torch.float32, 1), "min_p": each(min_p, torch.float32, 0)}
+    with SamplePlan(rows, vocab, str(logits.dtype).replace("torch.", "")) as plan:
+        plan.forward(logits, uniforms, tokens, logprob=logprob, stream=stream, **settings)
+    return tokens, logprob

@@ -562,6 +562,158 @@ olc_status olc_token_log_probs_backward(olc_token_log_probs_plan* plan, const vo
                                         const float* dlogprob, const float* dentropy, void* dlogits, int64_t d_pitch,
                                         void* stream);
 
+/* ---- embedding ------------------------------------------------------------- */
+
+typedef struct olc_embedding_plan olc_embedding_plan;
+
+/*
+ * Rows of a table E [vocab, cols] by token id, and the table's gradient:
+ *     y_i = scale E[t_i],     dE_v = scale sum_{i: t_i = v} dy_i
+ * for `tokens` ids t (int64).  A negative id marks a place without a token: its
+ * y is 0 and it adds nothing.  An id of vocab or more gives a row of NaN and adds
+ * nothing.  0 <= tokens, vocab, cols < 2^31 - 65536, |scale| <= 3e38.  Errors:
+ * OLC_ERR_NULL, OLC_ERR_DTYPE, OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID,
+ * OLC_ERR_OOM.
+ */
+olc_status olc_embedding_plan_create(int64_t tokens, int64_t vocab, int64_t cols, double scale, olc_dtype dtype,
+                                     olc_embedding_plan** out);
+
+/* NULL is accepted. */
+void olc_embedding_plan_destroy(olc_embedding_plan* plan);
+
+/*
+ * Forward.  Y [tokens, cols] may not overlap the table.  Uses no device memory
+ * of the plan.  Errors: OLC_ERR_NULL, OLC_ERR_INVALID (a pitch below cols, a
+ * misaligned pointer), OLC_ERR_WRONG_DEVICE, OLC_ERR_CUDA.
+ */
+olc_status olc_embedding_forward(olc_embedding_plan* plan, const void* table, int64_t table_pitch,
+                                 const int64_t* tokens, void* Y, int64_t y_pitch, void* stream);
+
+/*
+ * Backward.  dtable [vocab, cols] gets the gradient, zeros for tokens that do
+ * not occur; with accumulate != 0 it is added to what dtable holds (one rounding
+ * of the float32 sum), and rows of tokens that do not occur are neither read nor
+ * written.  The sums are float32, in the order of the ids' places within pieces
+ * that depend on the sizes, the device and the ids alone, so that results repeat
+ * bit for bit.  dY may not overlap dtable.  The first call allocates the sorted
+ * places and partial sums (cudaMalloc, kept by the plan): make it before any
+ * stream capture.  Errors: as forward, and OLC_ERR_OOM.
+ */
+olc_status olc_embedding_backward(olc_embedding_plan* plan, const void* dY, int64_t dy_pitch, const int64_t* tokens,
+                                  void* dtable, int64_t dtable_pitch, int accumulate, void* stream);
+
+/* ---- residual step with its norms --------------------------------------------- */
+
+/* Layer norm as above, or RMS norm: the same with a mean of 0. */
+typedef enum {
+    OLC_NORM_LAYER = 0,
+    OLC_NORM_RMS = 1
+} olc_norm;
+
+typedef struct olc_residual_norm_plan olc_residual_norm_plan;
+
+/*
+ * The step between two blocks of a model, for the residual stream x and the
+ * output f of a block, both [rows, cols]:
+ *     n = norm(f) after_gamma + after_beta   (after != 0), or n = f
+ *     y = x + scale gate n                   (elementwise; no gate: 1)
+ *     z = norm(y) gamma + beta               what the next block reads
+ * norm(v) = (v - mean) rstd, rstd = 1 / sqrt(sum_j (v_j - mean)^2 / cols + eps),
+ * with the row's mean (OLC_NORM_LAYER) or mean = 0 (OLC_NORM_RMS).  z is formed
+ * from the unrounded y.  The gate has a value for each column (gate_pitch 0: one
+ * row [cols] for all rows) or for each element (gate_pitch >= cols; not read
+ * otherwise for a single row).  rows >= 0, 1 <= cols < 2^31 - 65536,
+ * 0 <= eps <= 3e38, |scale| <= 3e38.  Errors: OLC_ERR_NULL, OLC_ERR_DTYPE,
+ * OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID, OLC_ERR_OOM.
+ */
+olc_status olc_residual_norm_plan_create(int64_t rows, int64_t cols, double eps, double scale, int norm, int after,
+                                         olc_dtype dtype, olc_residual_norm_plan** out);
+
+/* NULL is accepted. */
+void olc_residual_norm_plan_destroy(olc_residual_norm_plan* plan);
+
+/*
+ * Forward.  gate, after_gamma, after_beta, gamma, beta: NULL for ones and zeros
+ * (after_* are not read without the norm of f).  Z: NULL where no norm follows.
+ * stats: float32 [2][rows], mean and rstd of y's rows (not written without Z),
+ * with `after` [4][rows], then those of f's; what the backward call reads; NULL to
+ * skip.  Y may be X, and Z may be F (same pointer and pitch); outputs overlap
+ * nothing else.  Uses no device memory of the plan.  Errors: OLC_ERR_NULL,
+ * OLC_ERR_INVALID (a pitch below cols, a misaligned pointer),
+ * OLC_ERR_WRONG_DEVICE, OLC_ERR_CUDA.
+ */
+olc_status olc_residual_norm_forward(olc_residual_norm_plan* plan, const void* X, int64_t x_pitch, const void* F,
+                                     int64_t f_pitch, const void* gate, int64_t gate_pitch, const void* after_gamma,
+                                     const void* after_beta, const void* gamma, const void* beta, void* Y,
+                                     int64_t y_pitch, void* Z, int64_t z_pitch, float* stats, void* stream);
+
+/*
+ * Backward, from the gradients dY of y (its other uses; NULL for zeros) and dZ
+ * of z (NULL: y goes into no norm): with J the norms' derivatives at the forward
+ * call's stats,
+ *     dx = dY + J(y)' (dZ gamma)
+ *     dgate = scale n dx          (summed over the rows for a gate [cols])
+ *     dn = scale gate dx,   df = J(f)' (dn after_gamma), or df = dn
+ *     dgamma = sum dZ norm(y), dbeta = sum dZ,
+ *     dafter_gamma = sum dn norm(f), dafter_beta = sum dn     (over the rows).
+ * F is read with `after` or dgate, Y and stats with dZ, after_beta with dgate.
+ * dX, dF, dgate and the weights' gradients: NULL to skip any (dgamma and dbeta
+ * need dZ, dgate needs the gate: OLC_ERR_NULL; dafter_* need `after`:
+ * OLC_ERR_INVALID).  dX may be dY or dZ, dF may be dZ or F, and dgate, for a
+ * matrix, may be the gate (same pointer and pitch); outputs overlap nothing else.
+ * Sums are float32 in an order that depends on the sizes, the arguments given,
+ * their alignment and the device alone, so that results repeat bit for bit; with rows
+ * == 0 they are zeros.  The first call allocates partial sums and row sums
+ * (cudaMalloc, kept by the plan): make it before any stream capture.  Errors: as
+ * forward, and OLC_ERR_OOM.
+ */
+olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* dY, int64_t dy_pitch, const void* dZ,
+                                      int64_t dz_pitch, const void* F, int64_t f_pitch, const void* Y, int64_t y_pitch,
+                                      const float* stats, const void* gate, int64_t gate_pitch,
+                                      const void* after_gamma, const void* after_beta, const void* gamma, void* dX,
+                                      int64_t dx_pitch, void* dF, int64_t df_pitch, void* dgate, int64_t dgate_pitch,
+                                      void* dgamma, void* dbeta, void* dafter_gamma, void* dafter_beta, void* stream);
+
+/* ---- sampling ------------------------------------------------------------------ */
+
+typedef struct olc_sample_plan olc_sample_plan;
+
+/*
+ * One token for each row z of logits [rows, vocab], from one uniform number u of
+ * the row's own.  The logits' order is by value, equal ones by the lower index.
+ *     w_j = e^((z_j - max z) / temperature)
+ *     K   = the first top_k of the order             (top_k <= 0: all)
+ *     P   = the shortest prefix of K whose weights sum to top_p of K's or more
+ *           (top_p >= 1: all of K; top_p <= 0: the first alone)
+ *     S   = the tokens of P with w_j >= min_p, and the first of the order
+ *     token   = the lowest j of S with sum_{i in S, i <= j} w_i > u sum_S w
+ *     logprob = log(w_token / sum_S w)
+ * A temperature of 0 takes the first of the order (logprob 0); others are held to
+ * 2^-96 ... 2^96.  u below 0 counts as 0, u >= 1 as the largest value
+ * below 1.  Logits of -inf have no weight.  A row of nothing but -inf gives token -1 and
+ * logprob -inf; a NaN or +inf logit, a NaN among the row's settings, or a
+ * temperature that is negative or infinite give token -1 and logprob NaN.
+ * Weights are 64-bit integers, the largest 2^43, good to 2^-36 of the largest
+ * (above 2^-12 to 2^-38 of themselves), so that their sums and the results depend neither on an order
+ * of summation nor on the other rows.
+ * 0 <= rows < 2^27, 1 <= vocab <= 2^20.  Errors: OLC_ERR_NULL, OLC_ERR_DTYPE,
+ * OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID, OLC_ERR_OOM.
+ */
+olc_status olc_sample_plan_create(int64_t rows, int64_t vocab, olc_dtype dtype, olc_sample_plan** out);
+
+/* NULL is accepted. */
+void olc_sample_plan_destroy(olc_sample_plan* plan);
+
+/*
+ * uniforms, temperature, top_p, min_p: [rows] float32; top_k: [rows] int32; each
+ * of the last four may be NULL (1, all, 1, 0).  tokens: [rows] int64; logprob:
+ * [rows] float32 or NULL.  Errors: OLC_ERR_NULL, OLC_ERR_INVALID (a pitch below
+ * vocab, a misaligned pointer), OLC_ERR_WRONG_DEVICE, OLC_ERR_OOM, OLC_ERR_CUDA.
+ */
+olc_status olc_sample_forward(olc_sample_plan* plan, const void* logits, int64_t pitch, const float* uniforms,
+                              const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                              int64_t* tokens, float* logprob, void* stream);
+
 /* ---- queries ----------------------------------------------------------- */
 
 /* Output shape: writes up to `capacity` extents into shape[] and the rank
