@@ -61,6 +61,7 @@ struct BwdParams {
     float scale, inv_cols;
     int after, rms, channel_gate_sum;
     int threads_per_row;
+    unsigned int* err;
 };
 
 // sums of two values over the W warps of a block; every thread gets them.
@@ -518,6 +519,269 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdParams p) {
     }
 }
 
+// Rows of 16-byte packs: a group of threads takes one row at a time, its operands
+// copied ahead into the group's own ring by bulk copies.  A row has two pairs of row sums,
+// one after the other; with 16 columns a thread two rows of 4096 share an SM, and one
+// works while the other waits for its sums.  The sums of the biases and of a channel's
+// gate do not fit beside that: with them (ALL) a thread has 8 columns.
+// The second barrier of a row also tells that every thread has read it: its buffer
+// takes another.  The groups' column sums are joined in group order.
+constexpr int kMaxGroups = 16;        // a warp or more on a row
+constexpr int kMaxAhead = 4;
+constexpr int kRingSmem = 200 * 1024;
+// The weights lie in shared memory: what the ring leaves of the L1 cache does not hold them.
+template <typename T, int NV, bool ALL, bool GATED>
+__global__ void __launch_bounds__(kThreads) backward_ring_kernel(const BwdParams p, int ahead) {
+    constexpr int V = 16 / sizeof(T), P = V / 2, Q = NV * P, WARPS = kThreads / 32, N = ALL ? SUMS : 2;
+    extern __shared__ __align__(128) unsigned char memory[];
+    __shared__ alignas(16) float2 all_slots[2][2][WARPS];
+    __shared__ uint64_t all_full[kMaxGroups][kMaxAhead];
+    __shared__ int abort_flag;
+    const int threads = p.threads_per_row, groups = blockDim.x / threads, warps = threads >> 5;
+    const int grp = threadIdx.x / threads, t = threadIdx.x - grp * threads;
+    const int cols = (int)p.cols;
+    const bool need_f = p.after || (GATED && (p.dgate || p.channel_gate_sum)), gate_rows = GATED && p.gate && p.gate_pitch;
+    const uint32_t row_bytes = (uint32_t)cols * sizeof(T);
+    const int at_dy = p.dZ ? 2 : 0, at_f = at_dy + (p.dY ? 1 : 0), at_gate = at_f + need_f, operands = at_gate + gate_rows;
+    const uint32_t stage_bytes = operands * row_bytes;
+    // the weights first: g, ag, and with a gate ab and one that all rows share
+    T* const weights = reinterpret_cast<T*>(memory);
+    const void* const given[4] = {p.g, p.after ? p.ag : nullptr, GATED && p.gate && p.after ? p.ab : nullptr,
+                                  GATED && !gate_rows ? p.gate : nullptr};
+    const T* w_at[4];
+    int held = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w_at[k] = nullptr;
+        if (!given[k]) continue;
+        for (int c = threadIdx.x * V; c < cols; c += blockDim.x * V)
+            *reinterpret_cast<Pack<T, V>*>(weights + held * cols + c) = load<T, V>(static_cast<const T*>(given[k]) + c);
+        w_at[k] = weights + held++ * cols;
+    }
+    unsigned char* const rings = memory + (size_t)held * row_bytes;
+    unsigned char* const ring = rings + (size_t)grp * ahead * stage_bytes;
+    uint64_t* const full = all_full[grp];
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (t == 0) {
+        for (int i = 0; i < ahead; ++i) tc::mbar_init(&full[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    auto fetch = [&](int64_t row, int stage) {    // one thread
+        if (row >= p.rows) return;
+        unsigned char* to = ring + (size_t)stage * stage_bytes;
+        tc::mbar_arrive_expect_tx(&full[stage], stage_bytes);
+        auto copy = [&](int k, const void* from, int64_t pitch) {
+            bulk_copy(to + (size_t)k * row_bytes, static_cast<const T*>(from) + row * pitch, row_bytes, &full[stage]);
+        };
+        if (p.dZ) {
+            copy(0, p.dZ, p.dz_pitch);
+            copy(1, p.Y, p.y_pitch);
+        }
+        if (p.dY) copy(at_dy, p.dY, p.dy_pitch);
+        if (need_f) copy(at_f, p.F, p.f_pitch);
+        if (gate_rows) copy(at_gate, p.gate, p.gate_pitch);
+    };
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + grp;
+    if (t == 0)
+        for (int i = 0; i < ahead; ++i) fetch(row + i * step, i);
+    F2 sums[N][Q];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) sums[k][q] = 0;
+    constexpr int OF_AG = ALL ? (int)DAG : 1;
+    // (a thread's packs, zeros past the row's end)
+    auto get = [&](F2 (&out)[Q], const void* from) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * threads) * V;
+            F2 v[P];
+            if (c < cols) {
+                widen<T, V>(v, load<T, V>(static_cast<const T*>(from) + c));
+            } else {
+#pragma unroll
+                for (int q = 0; q < P; ++q) v[q] = 0;
+            }
+#pragma unroll
+            for (int q = 0; q < P; ++q) out[i * P + q] = v[q];
+        }
+    };
+    auto put = [&](void* to, int64_t at, const F2 (&v)[Q]) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * threads) * V;
+            F2 o[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) o[q] = v[i * P + q];
+            if (c < cols) store<T, V>(static_cast<T*>(to) + at + c, o);
+        }
+    };
+    auto barrier = [&] {                          // the group (named barriers 1 to 15 suffice: 16 groups are warps)
+        __syncwarp();
+        if (threads > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(threads) : "memory");
+    };
+    auto row_means = [&](F2 s1, F2 s2, float2 (&slots)[WARPS]) {
+        const float2 own = make_float2(warp_sum(sum_of<2>(s1)), warp_sum(sum_of<2>(s2)));
+        if ((t & 31) == 0) slots[threadIdx.x >> 5] = own;
+        barrier();
+        F2 s = 0;
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) s = add2(s, *reinterpret_cast<const F2*>(&slots[grp * warps + w]));
+        float2 c;
+        unpack_f2(s, c.x, c.y);
+        return make_float2(p.rms ? 0.f : -c.x * p.inv_cols, -c.y * p.inv_cols);
+    };
+    int stage = 0, phase = 0, buf = 0;
+    auto stats_at = [&](int64_t r, int k) {
+        return r < p.rows ? Stats{p.stats[2 * k * p.rows + r], p.stats[(2 * k + 1) * p.rows + r]} : Stats{0.f, 0.f};
+    };
+    Stats sy{0.f, 0.f}, sf{0.f, 0.f};
+    if (p.dZ) sy = stats_at(row, 0);
+    if (p.after) sf = stats_at(row, 1);
+    for (; row < p.rows; row += step, buf ^= 1) {
+        // a wait that runs out: the row's sums are of what is there, the error word tells
+        tc::mbar_wait(&full[stage], phase, &abort_flag, p.err);
+        const T* in = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes);
+        F2 dx[Q];
+        if (p.dZ) {
+            F2 dz[Q], yh[Q];
+            get(dz, in);
+            get(yh, in + cols);
+            const F2 rstd = both(sy.rstd), minus_mean = both(-sy.mean);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                yh[q] = mul2(add2(yh[q], minus_mean), rstd);
+                sums[DG][q] = fma2(dz[q], yh[q], sums[DG][q]);
+                if constexpr (ALL) sums[DB][q] = add2(sums[DB][q], dz[q]);
+            }
+            if (w_at[0]) {
+                F2 w[Q];
+                get(w, w_at[0]);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) dz[q] = mul2(dz[q], w[q]);
+            }
+            F2 s1 = 0, s2 = 0;
+            add_products<Q>(s1, s2, dz, yh);
+            sy = stats_at(row + step, 0);
+            const float2 m = row_means(s1, s2, all_slots[buf][0]);
+            if (p.dY) get(dx, in + at_dy * cols);
+            else
+#pragma unroll
+                for (int q = 0; q < Q; ++q) dx[q] = 0;
+            add_through_norm<Q>(dx, dz, yh, both(m.x), both(m.y), rstd);
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if ((t + q / P * threads) * V >= cols) dx[q] = 0;
+        } else {
+            get(dx, in + at_dy * cols);
+        }
+        if (p.dX) put(p.dX, row * p.dx_pitch, dx);
+        F2 f[Q], dn[Q];
+        if (need_f) get(f, in + at_f * cols);
+        const F2 scale = both(p.scale), rstd = both(sf.rstd);
+        if (p.after) {
+            const F2 minus_mean = both(-sf.mean);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) f[q] = mul2(add2(f[q], minus_mean), rstd);
+            sf = stats_at(row + step, 1);
+        }
+        const bool gated = gate_rows || w_at[3];
+        if (gated) get(dn, gate_rows ? in + at_gate * cols : w_at[3]);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) dn[q] = mul2(gated ? mul2(scale, dn[q]) : scale, dx[q]);
+        if (GATED && (p.dgate || p.channel_gate_sum)) {
+            F2 n[Q], w[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) n[q] = f[q];
+            if (w_at[1]) {
+                get(w, w_at[1]);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) n[q] = mul2(n[q], w[q]);
+            }
+            if (w_at[2]) {
+                get(w, w_at[2]);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) n[q] = add2(n[q], w[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                n[q] = mul2(mul2(n[q], scale), dx[q]);
+                if constexpr (ALL) sums[DGATE][q] = add2(sums[DGATE][q], n[q]);
+            }
+            if (p.dgate) put(p.dgate, row * p.dgate_pitch, n);
+        }
+        float2 m = make_float2(0.f, 0.f);
+        if (p.after) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                sums[OF_AG][q] = fma2(dn[q], f[q], sums[OF_AG][q]);
+                if constexpr (ALL) sums[DAB][q] = add2(sums[DAB][q], dn[q]);
+            }
+            if (w_at[1]) {
+                F2 w[Q];
+                get(w, w_at[1]);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) dn[q] = mul2(dn[q], w[q]);
+            }
+            F2 s1 = 0, s2 = 0;
+            add_products<Q>(s1, s2, dn, f);
+            m = row_means(s1, s2, all_slots[buf][1]);
+        } else {
+            barrier();
+        }
+        if (t == 0) fetch(row + ahead * step, stage);
+        if (++stage == ahead) {
+            stage = 0;
+            phase ^= 1;
+        }
+        if (p.dF) {
+            if (p.after) {
+                const F2 m1 = both(m.x), m2 = both(m.y);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) dn[q] = mul2(add2(fma2(f[q], m2, dn[q]), m1), rstd);
+            }
+            put(p.dF, row * p.df_pitch, dn);
+        }
+    }
+    if (t == 0 && abort_flag) {
+        // nothing may land after the block has left: one more wait each for what was asked for
+        for (int i = 0; i < ahead; ++i) {
+            tc::mbar_wait_drain(&full[i], 0);
+            tc::mbar_wait_drain(&full[i], 1);
+        }
+    }
+    if (!p.partial) return;
+    __syncthreads();                                 // every row has been read: the memory is free
+    float* const joined = reinterpret_cast<float*>(memory);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * threads) * V;
+            if (c >= cols) continue;
+            float* const to = joined + ((size_t)grp * N + k) * cols + c;
+#pragma unroll
+            for (int q = 0; q < P; ++q) *reinterpret_cast<F2*>(to + 2 * q) = sums[k][i * P + q];
+        }
+    __syncthreads();
+    for (int i = threadIdx.x * 4; i < N * cols; i += blockDim.x * 4) {
+        float4 a = *reinterpret_cast<const float4*>(joined + i);
+        for (int g = 1; g < groups; ++g) {
+            const float4 b = *reinterpret_cast<const float4*>(joined + (size_t)g * N * cols + i);
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+        }
+        const int k = i / cols;
+        const int sum = ALL ? k : (k == 0 ? (int)DG : (int)DAG);
+        *reinterpret_cast<float4*>(p.partial + ((int64_t)blockIdx.x * SUMS + sum) * cols + (i - k * cols)) = a;
+    }
+}
+
 // Rows wider than a block keeps: first the row sums (two passes over the row) ...
 template <typename T, int V>
 struct LongRow {
@@ -766,31 +1030,70 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
 
 // the backward launch of one shape
 struct BwdShape {
-    bool wide = false;      // rows wider than a block keeps
-    int tpr = 0, groups = 1;
-    int64_t blocks = 0;     // that leave partial sums
+    enum Kind { LONG, RING, ANY } kind = LONG;      // LONG: rows wider than a block keeps
+    int per_thread = kColsPerThread;                // columns
+    int tpr = 0, groups = 1, ahead = 0;
+    int64_t blocks = 0;                             // that leave partial sums
+    size_t smem = 0;
 };
+// `operands`: matrices that a row reads; `weights`: vectors; `all`: every column sum
 template <int V>
-BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count) {
+BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count, int operands, int weights, bool gated, bool all) {
     BwdShape b;
+    if (V > 1) {
+        // (a gate takes registers, too: 16 columns then only where 8 do not reach)
+        b.per_thread = all || (gated && cols <= 8 * kThreads) ? 8 : 16;
+        const int64_t row = cols * (16 / V) * operands, held = cols * (16 / V) * weights, room = kRingSmem - held;
+        b.tpr = (int)min64(ceil_div(ceil_div(cols, b.per_thread), 32) * 32, 2 * kThreads);
+        if (b.tpr <= kThreads && 2 * row <= room) {
+            b.kind = BwdShape::RING;
+            b.groups = (int)max64(1, min64(kThreads / b.tpr, ceil_div(rows, sm_count)));
+            while (b.groups > 1 && 2 * row * b.groups > room) --b.groups;
+            b.ahead = (int)min64(kMaxAhead, room / (row * b.groups));
+            b.blocks = max64(1, min64(ceil_div(rows, b.groups), sm_count));
+            b.smem = (size_t)max64(held + row * b.groups * b.ahead, (int64_t)b.groups * (all ? SUMS : 2) * cols * 4);
+            return b;
+        }
+    }
+    b.per_thread = kColsPerThread;
     if (cols > kThreads * kColsPerThread) {
-        b.wide = true;
         const int64_t across = ceil_div(ceil_div(cols, V), 128);
         b.blocks = max64(1, min64(min64(ceil_div(rows, 4), 65535), 8 * (int64_t)sm_count / across));
         return b;
     }
+    b.kind = BwdShape::ANY;
     b.tpr = (int)(ceil_div(ceil_div(cols, kColsPerThread), 32) * 32);
     b.groups = (int)max64(1, min64(kThreads / b.tpr, ceil_div(rows, sm_count)));
     b.blocks = max64(1, min64(ceil_div(rows, b.groups), sm_count));
+    b.smem = b.groups > 1 ? (size_t)b.groups * cols * sizeof(float) : 0;
     return b;
+}
+
+template <typename T, int C, bool ALL, bool GATED>
+cudaError_t backward_ring(const BwdParams& p, const BwdShape& b, cudaStream_t s) {
+    auto* kernel = backward_ring_kernel<T, C * sizeof(T) / 16, ALL, GATED>;
+    const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), kRingSmem);
+    if (e != cudaSuccess) return e;
+    return plan_launch(kernel, dim3((unsigned)b.blocks), dim3((unsigned)(b.tpr * b.groups)), b.smem, s, p, b.ahead);
 }
 
 template <typename T, int V>
 cudaError_t backward_as(BwdParams p, int sm_count, const Outputs& outputs, cudaStream_t s) {
-    const BwdShape b = backward_shape<V>(p.rows, p.cols, sm_count);
+    const bool all = outputs.to[DB] || outputs.to[DAB] || outputs.to[DGATE];
+    const int operands = (p.dZ ? 2 : 0) + (p.dY ? 1 : 0) + (p.after || p.dgate || p.channel_gate_sum ? 1 : 0) +
+                         (p.gate && p.gate_pitch ? 1 : 0);
+    const int weights = (p.g ? 1 : 0) + (p.after && p.ag ? 1 : 0) + (p.gate && p.after && p.ab ? 1 : 0) +
+                        (p.gate && !p.gate_pitch ? 1 : 0);
+    const BwdShape b = backward_shape<V>(p.rows, p.cols, sm_count, operands, weights, p.gate != nullptr, all);
     cudaError_t e = cudaSuccess;
     p.threads_per_row = b.tpr;
-    if (b.wide) {
+    if (b.kind == BwdShape::RING) {
+        if constexpr (V > 1)
+            e = all ? backward_ring<T, 8, true, true>(p, b, s)
+                : !p.gate ? backward_ring<T, 16, false, false>(p, b, s)
+                : b.per_thread == 8 ? backward_ring<T, 8, false, true>(p, b, s)
+                                    : backward_ring<T, 16, false, true>(p, b, s);
+    } else if (b.kind == BwdShape::LONG) {
         if (p.dZ || p.after)
             e = plan_launch(backward_long_sums_kernel<T, V>, dim3((unsigned)min64(p.rows, (int64_t)sm_count * 2)),
                             dim3(1024), 0, s, p);
@@ -798,9 +1101,9 @@ cudaError_t backward_as(BwdParams p, int sm_count, const Outputs& outputs, cudaS
             e = plan_launch(backward_long_kernel<T, V>,
                             dim3((unsigned)ceil_div(ceil_div(p.cols, V), 128), (unsigned)b.blocks), dim3(128), 0, s, p);
     } else {
+        // rows of packs whose operands overfill the ring come here as single elements do
         constexpr int NV = V == 1 ? kColsPerThread / 2 : kColsPerThread / V;
-        const size_t smem = b.groups > 1 ? (size_t)b.groups * p.cols * sizeof(float) : 0;
-        e = plan_launch(backward_kernel<T, V, NV>, dim3((unsigned)b.blocks), dim3((unsigned)(b.tpr * b.groups)), smem, s, p);
+        e = plan_launch(backward_kernel<T, V, NV>, dim3((unsigned)b.blocks), dim3((unsigned)(b.tpr * b.groups)), b.smem, s, p);
     }
     if (e != cudaSuccess || !p.partial) return e;
     return plan_launch(column_sum_kernel<T, 16>, dim3((unsigned)ceil_div(p.cols, 16), SUMS), dim3(1024), 0, s,
@@ -940,15 +1243,21 @@ olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* 
     residual::BwdParams p{dY, dZ, F, Y, stats, gate, after_gamma, after_beta, gamma, dX, dF, channel_sum ? nullptr : dgate,
                           nullptr, nullptr, dy_pitch, dz_pitch, f_pitch, y_pitch, gate_pitch, dx_pitch, df_pitch,
                           dgate_pitch, rows, cols, plan->scale, (float)(1.0 / (double)cols), plan->after, plan->rms,
-                          channel_sum, 0};
-    // both layouts' partial sums fit: a call with other alignment or other
+                          channel_sum, 0, device_error_word()};
+    // the partial sums of every kernel fit: a call with other alignment, operands or
     // outputs does not have to allocate again
     const int sms = plan->state.sm_count;
-    const residual::BwdShape a = plan->dtype == OLC_FLOAT ? residual::backward_shape<4>(rows, cols, sms)
-                                                          : residual::backward_shape<8>(rows, cols, sms);
-    const residual::BwdShape b = residual::backward_shape<1>(rows, cols, sms);
-    const size_t row_floats = a.wide ? (size_t)rows * 4 : 0;
-    const size_t floats = row_floats + (size_t)max64(a.blocks, b.blocks) * residual::SUMS * (size_t)cols;
+    int64_t blocks = 0;
+    for (int which = 0; which < 5 * 5 * 4; ++which) {
+        const int operands = 1 + which % 5, weights = which / 5 % 5;
+        const bool gated = which / 25 & 1, all = which / 50;
+        auto of = [&](auto shape) { blocks = max64(blocks, shape(rows, cols, sms, operands, weights, gated, all).blocks); };
+        of(residual::backward_shape<1>);
+        if (plan->dtype == OLC_FLOAT) of(residual::backward_shape<4>);
+        else of(residual::backward_shape<8>);
+    }
+    const size_t row_floats = cols > residual::kThreads * residual::kColsPerThread ? ((size_t)rows * 4 + 3) / 4 * 4 : 0;
+    const size_t floats = row_floats + (size_t)blocks * residual::SUMS * (size_t)cols;
     st = plan->state.ensure(floats * sizeof(float));
     if (st != OLC_OK) return st;
     p.row_sums = static_cast<float*>(plan->state.memory);
