@@ -526,18 +526,18 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdParams p) {
 // gate do not fit beside that: with them (ALL) a thread has 8 columns.
 // The second barrier of a row also tells that every thread has read it: its buffer
 // takes another.  The groups' column sums are joined in group order.
-constexpr int kMaxGroups = 16;        // a warp or more on a row
+constexpr int kMaxGroups = 15;        // named barriers
 constexpr int kMaxAhead = 4;
-constexpr int kRingSmem = 200 * 1024;
-// The weights lie in shared memory: what the ring leaves of the L1 cache does not hold them.
-template <typename T, int NV, bool ALL, bool GATED>
+constexpr int kRingSmem = 212 * 1024;
+// FULL: every thread has NV packs.  The weights lie in shared memory: what the ring leaves of the L1 cache does not hold them.
+template <typename T, int NV, bool ALL, bool GATED, bool FULL>
 __global__ void __launch_bounds__(kThreads) backward_ring_kernel(const BwdParams p, int ahead) {
-    constexpr int V = 16 / sizeof(T), P = V / 2, Q = NV * P, WARPS = kThreads / 32, N = ALL ? SUMS : 2;
+    constexpr int V = 16 / sizeof(T), P = V / 2, Q = NV * P, N = ALL ? SUMS : 2, WARPS = kThreads / 32;
     extern __shared__ __align__(128) unsigned char memory[];
-    __shared__ alignas(16) float2 all_slots[2][2][WARPS];
+    __shared__ alignas(16) float all_slots[kMaxGroups][2][2][2][WARPS];     // [buffer][norm][sum]; those of absent warps hold 0
     __shared__ uint64_t all_full[kMaxGroups][kMaxAhead];
     __shared__ int abort_flag;
-    const int threads = p.threads_per_row, groups = blockDim.x / threads, warps = threads >> 5;
+    const int threads = p.threads_per_row, groups = blockDim.x / threads;
     const int grp = threadIdx.x / threads, t = threadIdx.x - grp * threads;
     const int cols = (int)p.cols;
     const bool need_f = p.after || (GATED && (p.dgate || p.channel_gate_sum)), gate_rows = GATED && p.gate && p.gate_pitch;
@@ -561,7 +561,9 @@ __global__ void __launch_bounds__(kThreads) backward_ring_kernel(const BwdParams
     unsigned char* const rings = memory + (size_t)held * row_bytes;
     unsigned char* const ring = rings + (size_t)grp * ahead * stage_bytes;
     uint64_t* const full = all_full[grp];
+    float(&slots)[2][2][2][WARPS] = all_slots[grp];
     if (threadIdx.x == 0) abort_flag = 0;
+    for (int i = threadIdx.x; i < kMaxGroups * 8 * WARPS; i += blockDim.x) (&all_slots[0][0][0][0][0])[i] = 0.f;
     if (t == 0) {
         for (int i = 0; i < ahead; ++i) tc::mbar_init(&full[i], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -594,21 +596,28 @@ __global__ void __launch_bounds__(kThreads) backward_ring_kernel(const BwdParams
         for (int q = 0; q < Q; ++q) sums[k][q] = 0;
     constexpr int OF_AG = ALL ? (int)DAG : 1;
     // (a thread's packs, zeros past the row's end)
-    auto get = [&](F2 (&out)[Q], const void* from) {
+    struct Raw {
+        uint4 k[NV];
+    };
+    auto fetch_raw = [&](const void* from) {
+        Raw r{};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * threads) * V;
-            F2 v[P];
-            if (c < cols) {
-                widen<T, V>(v, load<T, V>(static_cast<const T*>(from) + c));
-            } else {
+            if (FULL || c < cols) r.k[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(from) + c);
+        }
+        return r;
+    };
+    auto widen_raw = [&](F2 (&out)[Q], const Raw& r) {
 #pragma unroll
-                for (int q = 0; q < P; ++q) v[q] = 0;
-            }
+        for (int i = 0; i < NV; ++i) {
+            F2 v[P];
+            widen<T, V>(v, *reinterpret_cast<const Pack<T, V>*>(&r.k[i]));
 #pragma unroll
             for (int q = 0; q < P; ++q) out[i * P + q] = v[q];
         }
     };
+    auto get = [&](F2 (&out)[Q], const void* from) { widen_raw(out, fetch_raw(from)); };
     auto put = [&](void* to, int64_t at, const F2 (&v)[Q]) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -616,23 +625,35 @@ __global__ void __launch_bounds__(kThreads) backward_ring_kernel(const BwdParams
             F2 o[P];
 #pragma unroll
             for (int q = 0; q < P; ++q) o[q] = v[i * P + q];
-            if (c < cols) store<T, V>(static_cast<T*>(to) + at + c, o);
+            if (FULL || c < cols) store<T, V>(static_cast<T*>(to) + at + c, o);
         }
     };
-    auto barrier = [&] {                          // the group (named barriers 1 to 15 suffice: 16 groups are warps)
+    auto barrier = [&] {                          // the group
         __syncwarp();
         if (threads > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(threads) : "memory");
     };
-    auto row_means = [&](F2 s1, F2 s2, float2 (&slots)[WARPS]) {
-        const float2 own = make_float2(warp_sum(sum_of<2>(s1)), warp_sum(sum_of<2>(s2)));
-        if ((t & 31) == 0) slots[threadIdx.x >> 5] = own;
+    // the two sums over the row, over its columns
+    auto row_means = [&](F2 s1, F2 s2, float (&slots)[2][WARPS]) {
+        // half of the lanes go on with one of the sums each
+        const int lane = t & 31;
+        const float a = sum_of<2>(s1), b = sum_of<2>(s2);
+        float v = (lane & 16 ? b : a) + __shfl_xor_sync(0xffffffffu, lane & 16 ? a : b, 16);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if ((lane & 15) == 0) slots[lane >> 4][t >> 5] = v;
         barrier();
-        F2 s = 0;
-#pragma unroll 4
-        for (int w = 0; w < warps; ++w) s = add2(s, *reinterpret_cast<const F2*>(&slots[grp * warps + w]));
-        float2 c;
-        unpack_f2(s, c.x, c.y);
-        return make_float2(p.rms ? 0.f : -c.x * p.inv_cols, -c.y * p.inv_cols);
+        float c[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            F2 s = 0;
+#pragma unroll
+            for (int w = 0; w < WARPS; w += 4) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&slots[k][w]);
+                s = add2(add2(s, x.x), x.y);
+            }
+            c[k] = sum_of<2>(s);
+        }
+        return make_float2(p.rms ? 0.f : -c[0] * p.inv_cols, -c[1] * p.inv_cols);
     };
     int stage = 0, phase = 0, buf = 0;
     auto stats_at = [&](int64_t r, int k) {
@@ -646,6 +667,7 @@ __global__ void __launch_bounds__(kThreads) backward_ring_kernel(const BwdParams
         tc::mbar_wait(&full[stage], phase, &abort_flag, p.err);
         const T* in = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes);
         F2 dx[Q];
+        Raw raw_f{};
         if (p.dZ) {
             F2 dz[Q], yh[Q];
             get(dz, in);
@@ -666,21 +688,22 @@ __global__ void __launch_bounds__(kThreads) backward_ring_kernel(const BwdParams
             F2 s1 = 0, s2 = 0;
             add_products<Q>(s1, s2, dz, yh);
             sy = stats_at(row + step, 0);
-            const float2 m = row_means(s1, s2, all_slots[buf][0]);
-            if (p.dY) get(dx, in + at_dy * cols);
-            else
-#pragma unroll
-                for (int q = 0; q < Q; ++q) dx[q] = 0;
+            Raw dy{};                              // on their way during the sums
+            if (p.dY) dy = fetch_raw(in + at_dy * cols);
+            if (need_f) raw_f = fetch_raw(in + at_f * cols);
+            const float2 m = row_means(s1, s2, slots[buf][0]);
+            widen_raw(dx, dy);
             add_through_norm<Q>(dx, dz, yh, both(m.x), both(m.y), rstd);
 #pragma unroll
             for (int q = 0; q < Q; ++q)
-                if ((t + q / P * threads) * V >= cols) dx[q] = 0;
+                if (!FULL && (t + q / P * threads) * V >= cols) dx[q] = 0;
         } else {
             get(dx, in + at_dy * cols);
+            if (need_f) raw_f = fetch_raw(in + at_f * cols);
         }
         if (p.dX) put(p.dX, row * p.dx_pitch, dx);
         F2 f[Q], dn[Q];
-        if (need_f) get(f, in + at_f * cols);
+        widen_raw(f, raw_f);
         const F2 scale = both(p.scale), rstd = both(sf.rstd);
         if (p.after) {
             const F2 minus_mean = both(-sf.mean);
@@ -728,7 +751,7 @@ __global__ void __launch_bounds__(kThreads) backward_ring_kernel(const BwdParams
             }
             F2 s1 = 0, s2 = 0;
             add_products<Q>(s1, s2, dn, f);
-            m = row_means(s1, s2, all_slots[buf][1]);
+            m = row_means(s1, s2, slots[buf][1]);
         } else {
             barrier();
         }
@@ -968,6 +991,7 @@ __global__ void __launch_bounds__(128) backward_long_kernel(const BwdParams p) {
 
 struct Outputs {
     void* to[SUMS];         // null: not wanted
+    int wanted[SUMS];       // those that are, in order
 };
 
 // Column sums over the blocks' partial sums, C columns a block: in block order
@@ -977,14 +1001,14 @@ __global__ void __launch_bounds__(1024)
 column_sum_kernel(const float* __restrict__ partial, int blocks, int64_t cols, const Outputs outputs) {
     constexpr int SHARES = 1024 / C;
     __shared__ float sums[SHARES][C + 1];
-    T* out = static_cast<T*>(outputs.to[blockIdx.y]);
-    if (!out) return;
+    const int which = outputs.wanted[blockIdx.y];
+    T* out = static_cast<T*>(outputs.to[which]);
     const int col = threadIdx.x % C, share = threadIdx.x / C;
     const int64_t c = (int64_t)blockIdx.x * C + col;
     float s = 0.f;
     if (c < cols) {
 #pragma unroll 10
-        for (int b = share; b < blocks; b += SHARES) s += partial[((int64_t)b * SUMS + blockIdx.y) * cols + c];
+        for (int b = share; b < blocks; b += SHARES) s += partial[((int64_t)b * SUMS + which) * cols + c];
     }
     sums[share][col] = s;
     __syncthreads();
@@ -1028,6 +1052,9 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     return plan_launch(forward_long_kernel<T, V>, dim3((unsigned)grid), dim3(1024), 0, s, p);
 }
 
+// Up to this width the column sums are split eight columns a block, above it 32.
+constexpr int64_t kNarrowCols = 2048;
+
 // the backward launch of one shape
 struct BwdShape {
     enum Kind { LONG, RING, ANY } kind = LONG;      // LONG: rows wider than a block keeps
@@ -1047,7 +1074,7 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count, int operands, 
         b.tpr = (int)min64(ceil_div(ceil_div(cols, b.per_thread), 32) * 32, 2 * kThreads);
         if (b.tpr <= kThreads && 2 * row <= room) {
             b.kind = BwdShape::RING;
-            b.groups = (int)max64(1, min64(kThreads / b.tpr, ceil_div(rows, sm_count)));
+            b.groups = (int)max64(1, min64(min64(kThreads / b.tpr, kMaxGroups), ceil_div(rows, sm_count)));
             while (b.groups > 1 && 2 * row * b.groups > room) --b.groups;
             b.ahead = (int)min64(kMaxAhead, room / (row * b.groups));
             b.blocks = max64(1, min64(ceil_div(rows, b.groups), sm_count));
@@ -1071,7 +1098,9 @@ BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count, int operands, 
 
 template <typename T, int C, bool ALL, bool GATED>
 cudaError_t backward_ring(const BwdParams& p, const BwdShape& b, cudaStream_t s) {
-    auto* kernel = backward_ring_kernel<T, C * sizeof(T) / 16, ALL, GATED>;
+    constexpr int NV = C * sizeof(T) / 16;
+    auto* kernel = p.cols == (int64_t)b.tpr * C ? backward_ring_kernel<T, NV, ALL, GATED, true>
+                                                : backward_ring_kernel<T, NV, ALL, GATED, false>;
     const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kernel), kRingSmem);
     if (e != cudaSuccess) return e;
     return plan_launch(kernel, dim3((unsigned)b.blocks), dim3((unsigned)(b.tpr * b.groups)), b.smem, s, p, b.ahead);
@@ -1106,8 +1135,15 @@ cudaError_t backward_as(BwdParams p, int sm_count, const Outputs& outputs, cudaS
         e = plan_launch(backward_kernel<T, V, NV>, dim3((unsigned)b.blocks), dim3((unsigned)(b.tpr * b.groups)), b.smem, s, p);
     }
     if (e != cudaSuccess || !p.partial) return e;
-    return plan_launch(column_sum_kernel<T, 16>, dim3((unsigned)ceil_div(p.cols, 16), SUMS), dim3(1024), 0, s,
-                       (const float*)p.partial, (int)b.blocks, p.cols, outputs);
+    Outputs o = outputs;
+    int n = 0;
+    for (int k = 0; k < SUMS; ++k)
+        if (o.to[k]) o.wanted[n++] = k;
+    auto run = [&](auto kernel, int c) {
+        return plan_launch(kernel, dim3((unsigned)ceil_div(p.cols, c), (unsigned)n), dim3(1024), 0, s,
+                           (const float*)p.partial, (int)b.blocks, p.cols, o);
+    };
+    return p.cols <= kNarrowCols ? run(column_sum_kernel<T, 8>, 8) : run(column_sum_kernel<T, 32>, 32);
 }
 
 }  // namespace residual
@@ -1226,7 +1262,7 @@ olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* 
     olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const residual::Outputs outputs{{dgamma, dbeta, dafter_gamma, dafter_beta, channel_sum ? dgate : nullptr}};
+    const residual::Outputs outputs{{dgamma, dbeta, dafter_gamma, dafter_beta, channel_sum ? dgate : nullptr}, {}};
     bool sums = false;
     for (void* o : outputs.to) sums = sums || o;
     if (rows == 0) {                        // empty sums
