@@ -15,6 +15,7 @@
 // the sum of the distances from it, in the same pass as the squares (Chan, Golub and
 // LeVeque's two-pass algorithm), so that rows far from zero keep their digits.
 #include <new>
+#include <type_traits>
 
 #include "plan_state.h"
 #include "row_packs.cuh"
@@ -93,11 +94,36 @@ __device__ __forceinline__ Stats stats_of(float mean, float2 sums, const FwdPara
     return Stats{mean + shift, 1.0f / sqrtf(fmaf(squares, p.inv_cols, p.eps))};
 }
 
+// A thread's columns as packs that stay the words they were loaded as until they
+// are widened (arrays of 16-bit elements cost moves and registers: [16384, 4096] BF16
+// 96.7 us, so 79.6).
+template <typename T, int V>
+struct Words {
+    static constexpr int P = V / 2;
+    using Raw = uint4;
+    static __device__ __forceinline__ bool in(int base, int i, int, int stride, int cols) {
+        return (base + i * stride) * V < cols;
+    }
+    static __device__ __forceinline__ Raw read(const T* row, int base, int i, int stride, int cols, bool, bool) {
+        if (in(base, i, 0, stride, cols)) return *reinterpret_cast<const uint4*>(row + (base + i * stride) * V);
+        return uint4{0, 0, 0, 0};
+    }
+    static __device__ __forceinline__ void pairs_of(F2 (&out)[P], const Raw& r) {
+        widen<T, V>(out, *reinterpret_cast<const Pack<T, V>*>(&r));
+    }
+    static __device__ __forceinline__ F2 inside(F2 v, int base, int i, int, int stride, int cols, bool) {
+        return in(base, i, 0, stride, cols) ? v : 0;
+    }
+    static __device__ __forceinline__ void write(T* row, int base, int i, int stride, int cols, const F2 (&o)[P], bool) {
+        if (in(base, i, 0, stride, cols)) store<T, V>(row + (base + i * stride) * V, o);
+    }
+};
+
 // W warps on a row, NV packs (or pairs of elements) a thread, in registers.
 // W == 1: blocks of four independent warps.
 template <typename T, int V, int W, int NV>
-__global__ void __launch_bounds__(W == 1 ? 128 : W * 32) forward_kernel(const FwdParams p) {
-    using C = Columns<T, V>;
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, V > 1 && W == 4 && NV == 4 ? 7 : 0) forward_kernel(const FwdParams p) {
+    using C = std::conditional_t<V == 1, Columns<T, V>, Words<T, V == 1 ? 4 : V>>;
     constexpr int P = C::P, TPR = W * 32;
     __shared__ float slots1[2][W];
     __shared__ float2 slots2[2][W];
@@ -1025,8 +1051,13 @@ column_sum_kernel(const float* __restrict__ partial, int blocks, int64_t cols, c
 
 // ---- host side -------------------------------------------------------------
 
-// Threads a row: with many rows a thread takes up to four packs, with few rows more
-// warps share one.  One warp needs no block barrier.
+// Threads a row: with many rows a thread takes four packs, so that enough of the row
+// is on its way at once and enough blocks reside ([16384, 4096] BF16, us: 4 warps x 4
+// packs 79.6, 8 x 2 92.6, 2 x 8 81.0; [32768, 2048]: 2 x 4 78.8, 4 x 2 83.7, 8 x 1 110.9;
+// [32768, 1024]: 1 x 4 42.6, 4 x 1 53.2, 2 x 4 66.8); with few rows more warps share a
+// short one ([500, 1024] FP16: 4 x 1 2.9, 1 x 4 3.4; [64, 2048]: 8 x 1 2.7, 2 x 4 3.3;
+// [4, 4096]: 4 x 4 3.3, 16 x 1 3.2; [300, 4096]: 3.8 and 4.0).  One warp needs no block
+// barrier.
 template <typename T, int V>
 cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     // single elements go in pairs, twice as many a thread as packs
@@ -1039,10 +1070,11 @@ cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
     if (p.rows <= 0x7fffffff) {
         if (n <= 32) OLC_FWD(1, 1);
         if (n <= 64) OLC_FWD(1, 2);
-        if (n <= 256 && !few) OLC_FWD(4, 2);
+        if (n <= 128 && !few) OLC_FWD(1, 4);
+        if (n <= 128) OLC_FWD(4, 1);
+        if (n <= 256 && !few) OLC_FWD(2, 4);
         if (n <= 256) OLC_FWD(8, 1);
-        if (n <= 512 && !few) OLC_FWD(4, 4);
-        if (n <= 512) OLC_FWD(16, 1);
+        if (n <= 512) OLC_FWD(4, 4);
         if (n <= 1024) OLC_FWD(8, 4);
         if (n <= 2048) OLC_FWD(16, 4);
         if (n <= 4096) OLC_FWD(32, 4);
