@@ -26,6 +26,7 @@ constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1536;          // tokens of a sort block: a counter for each and each warp, 202 KB
 constexpr int kClearRows = 8;           // rows a group of threads clears
 constexpr int kJoinChunks = 8;          // chunks whose ends a join block looks at
+constexpr int kJoinLogTx = 5;           // its threads on a row: eight groups share a token's partial sums
 
 struct Tile {
     int log_tx;             // threads on a row: 1 << log_tx; the block's others take further rows
@@ -156,39 +157,43 @@ sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, 
     int position = 0;                               // where the block's first place goes
     for (int w = 0; w < kSortWarps; ++w) position += scan[w];
     __syncthreads();
-    // a thread's consecutive tokens: over the warps, then over the tokens
-    constexpr int PER = (kMaxBins + kSortThreads - 1) / kSortThreads;
-    int total[PER], sum = 0;
+    // a thread's consecutive tokens (one, where they suffice): their totals over the
+    // warps, the sum of those over the tokens before, then every warp's first position
+    const int per = (own + kSortThreads - 1) / kSortThreads;
+    auto over_warps = [&](int b, int first, bool write) {
+        int c[kSortWarps];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int b = threadIdx.x * PER + j;
-        total[j] = 0;
-        if (b < own)
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int c = counts[w * bins + b];
-                counts[w * bins + b] = total[j];
-                total[j] += c;
-            }
-        sum += total[j];
-    }
+        for (int w = 0; w < kSortWarps; ++w) c[w] = counts[w * bins + b];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            if (write) counts[w * bins + b] = first;
+            first += c[w];
+        }
+        return first;
+    };
+    int sum = 0;
+    for (int j = 0; j < per; ++j)
+        if (threadIdx.x * per + j < own) sum = over_warps(threadIdx.x * per + j, sum, false);
     int before = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, before, d);
         if (lane >= d) before += o;
     }
-    if (lane == 31) scan[warp] = before;
+    const int warps_sum = __shfl_sync(0xffffffffu, before, 31);
+    if (lane == 0) scan[warp] = warps_sum;
     __syncthreads();
-    before -= sum;
-    for (int w = 0; w < warp; ++w) before += scan[w];
-    position += before;
+    position += before - sum;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int b = threadIdx.x * PER + j;
+    for (int w = 0; w < kSortWarps; ++w) {
+        const int c = scan[w];
+        position += w < warp ? c : 0;
+    }
+    for (int j = 0; j < per; ++j) {
+        const int b = threadIdx.x * per + j;
         if (b >= own) continue;
         s.start[v0 + b] = position;
-        for (int w = 0; w < kSortWarps; ++w) counts[w * bins + b] += position;
-        position += total[j];
+        position = over_warps(b, position, true);
         if (v0 + b == vocab - 1) s.start[vocab] = position;
     }
     __syncthreads();
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const BwdParams p) {
 // every groups-th of them each and are added in group order.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) join_kernel(const BwdParams p) {
-    constexpr int LOG_TX = 7, GROUPS = kThreads >> LOG_TX;
+    constexpr int LOG_TX = kJoinLogTx, GROUPS = kThreads >> LOG_TX;
     __shared__ int found[kJoinChunks];
     __shared__ alignas(16) float sums[GROUPS - 1][1 << LOG_TX][V];
     const int tx = threadIdx.x & ((1 << LOG_TX) - 1), group = threadIdx.x >> LOG_TX;
@@ -401,11 +406,10 @@ cudaError_t forward_as(FwdParams p, int64_t cols, int sm_count, cudaStream_t s) 
 }
 
 // Places of a chunk: 32 where that leaves four blocks an SM, fewer for fewer
-// places, at least 4.
-inline int chunk_length(int64_t n, int64_t cols, int64_t bytes, int sm_count) {
-    const int64_t threads = n * ceil_div(cols * bytes, 16);     // one place each
+// places, at least 8.
+inline int chunk_length(int64_t n, int64_t packs, int sm_count) {
     int length = 32;
-    while (length > 4 && threads / length < (int64_t)sm_count * 4 * kThreads) length /= 2;
+    while (length > 8 && n * packs / length < (int64_t)sm_count * 4 * kThreads) length /= 2;
     return length;
 }
 
@@ -439,7 +443,7 @@ cudaError_t backward_as(BwdParams p, const int64_t* tokens, int64_t n, int sm_co
     p.units = p.sum_units + (p.accumulate ? 0 : ceil_div(p.vocab, groups * kClearRows) * p.tile.col_tiles);
     e = plan_launch(sum_kernel<T, V>, grid_of(p.units), dim3(kThreads), 0, s, p);
     if (e != cudaSuccess || p.chunks <= 1) return e;
-    p.units = ceil_div(p.chunks - 1, kJoinChunks) * ceil_div(p.tile.packs, 128);
+    p.units = ceil_div(p.chunks - 1, kJoinChunks) * ceil_div(p.tile.packs, 1 << kJoinLogTx);
     return plan_launch(join_kernel<T, V>, grid_of(p.units), dim3(kThreads), 0, s, p);
 }
 
@@ -521,9 +525,14 @@ olc_status olc_embedding_backward(olc_embedding_plan* plan, const void* dY, int6
     olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
     const int sms = plan->state.sm_count;
-    const int length = embedding::chunk_length(n, cols, eb, sms);
-    const int64_t chunks = ceil_div(n, length);
-    const embedding::Layout l = embedding::layout_of(n, vocab, cols, chunks);
+    const bool wide = cols * eb % 16 == 0 && plan_aligned16(dY) && plan_aligned16(dtable) &&
+                      (n <= 1 || dy_pitch * eb % 16 == 0) && (vocab == 1 || dtable_pitch * eb % 16 == 0);
+    // (the memory is for the shortest chunks, so that a call with other alignment does not
+    // have to allocate again)
+    const int64_t packs = ceil_div(cols * eb, 16);
+    const int length = embedding::chunk_length(n, wide ? packs : cols, sms);
+    const int64_t chunks = ceil_div(n, length), most = ceil_div(n, embedding::chunk_length(n, packs, sms));
+    const embedding::Layout l = embedding::layout_of(n, vocab, cols, most);
     st = plan->state.ensure(l.bytes);
     if (st != OLC_OK) return st;
     char* const m = static_cast<char*>(plan->state.memory);
@@ -532,8 +541,6 @@ olc_status olc_embedding_backward(olc_embedding_plan* plan, const void* dY, int6
                                  {reinterpret_cast<int*>(m), reinterpret_cast<int*>(m + l.place),
                                   reinterpret_cast<int*>(m + l.token)},
                                  {}, 0, 0};
-    const bool wide = cols * eb % 16 == 0 && plan_aligned16(dY) && plan_aligned16(dtable) &&
-                      (n <= 1 || dy_pitch * eb % 16 == 0) && (vocab == 1 || dtable_pitch * eb % 16 == 0);
     return by_type(plan->dtype, [&](auto tag) {
         using T = decltype(tag);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -26,6 +26,7 @@
 // values with a sum over the row each, then by a search for the last of the equal ones.
 #include <cmath>
 #include <new>
+#include <type_traits>
 
 #include "plan_state.h"
 #include "row_packs.cuh"
@@ -82,6 +83,7 @@ struct Shared {
     u64 exchange[2][2];         // [parity]: sums of this block
     Found found[2];             // of the first block: [parity]
     int listed;                 // entries of this block's list
+    u64 light[kWarps];          // sums of the warps' parts without the listed entries
     Scale scale;
     double min_distance;
     unsigned min_key;
@@ -153,33 +155,131 @@ __device__ __forceinline__ u64 heavy_weight(float hi, float lo, const Power* pow
     const float pl = fmaf(lo, kLn2, fmaf(r, kLn2Lo, fmaf(r, kLn2, -ph)));
     const float s = ph + pl;
     const float q = s * s * fmaf(s, fmaf(s, 1.f / 24.f, 1.f / 6.f), 0.5f);
+    // 2^(i/64) e: its upper part as an integer of 2^-28, then what is left of it
     const float a = t.hi * ph;
-    const float rest = fmaf(t.lo, ph, fmaf(t.hi, pl + q, fmaf(t.hi, ph, -a)));
-    const long long w = (long long)t.fixed + __float2ll_rn(a * 0x1p43f) + __float2int_rn(rest * 0x1p43f);
+    const float upper = fmaf(a, 0x1p28f, kMagic);
+    const float rest = fmaf(upper - kMagic, -0x1p-28f, a) +
+                       fmaf(t.lo, ph, fmaf(t.hi, pl + q, fmaf(t.hi, ph, -a)));
+    const long long w = (long long)t.fixed + ((long long)(__float_as_int(upper) - __float_as_int(kMagic)) << (kOne - 28)) +
+                        __float2int_rn(rest * 0x1p43f);
     const int down = -(k >> 6);
     return (u64)(w + ((1ll << down) >> 1)) >> down;
 }
 
-// 2^x below 2^-12: the series to the seventh power, |f| <= ln(2) / 2 (the next term is
-// 2^-27 at most)
+// 2^x below 2^-12, scaled by 2^43: 2^f by a polynomial fitted to it on [-1/2, 1/2]
+// (Remez' exchange, relative error 2^-29 before its roundings) and the integer part added to the exponent
+__device__ __forceinline__ constexpr float poly(int i) {
+    constexpr float c[7] = {0x1.000000p+0f, 0x1.62e430p-1f, 0x1.ebfbdap-3f, 0x1.c6aed4p-5f,
+                            0x1.3b2dbcp-7f, 0x1.5f456ap-10f, 0x1.41d334p-13f};
+    return c[i] * 0x1p43f;
+}
 __device__ __forceinline__ unsigned light_weight(float hi, float lo) {
     const float rounded = hi + kMagic;
-    const int n = __float_as_int(rounded) - __float_as_int(kMagic);
-    const float f = ((hi - (rounded - kMagic)) + lo) * kLn2;
-    float p = fmaf(f, 1.f / 5040.f, 1.f / 720.f);
-    p = fmaf(p, f, 1.f / 120.f);
-    p = fmaf(p, f, 1.f / 24.f);
-    p = fmaf(p, f, 1.f / 6.f);
-    p = fmaf(p, f, 0.5f);
-    p = fmaf(p, f, 1.f);
-    p = fmaf(p, f, 1.f);
-    return __float2uint_rn(__int_as_float(__float_as_int(p) + ((n + kOne) << 23)));
+    const float f = (hi - (rounded - kMagic)) + lo;
+    float p = poly(6);
+#pragma unroll
+    for (int i = 5; i >= 0; --i) p = fmaf(p, f, poly(i));
+    return __float2uint_rn(__int_as_float(__float_as_int(p) + (__float_as_int(rounded) << 23)));
 }
 
 __device__ __forceinline__ u64 weight_of(float z, const Scale& s, const Power* powers) {
     float hi, lo;
     exponent(z, s, hi, lo);
     return hi >= kHeavy ? heavy_weight(hi, lo, powers) : light_weight(hi, lo);
+}
+
+// ---- two elements at a time -------------------------------------------------------
+// The same arithmetic as weight_of's, operation by operation, on the words of a pack.
+
+template <typename T>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    uint32_t r;
+    if constexpr (std::is_same_v<T, __half>) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t max_nan_word(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    uint32_t r;
+    if constexpr (std::is_same_v<T, __half>) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// an element of a word (float32: the word)
+template <typename T>
+__device__ __forceinline__ float of_word(uint32_t w, int half) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) return __uint_as_float(half ? w & 0xFFFF0000u : w << 16);
+    const unsigned short b = (unsigned short)(half ? w >> 16 : w);
+    return Num<T>::to_acc(*reinterpret_cast<const T*>(&b));
+}
+// the largest of a word's elements, NaN if one is
+template <typename T>
+__device__ __forceinline__ float word_max(uint32_t w) {
+    return sizeof(T) == 4 ? __uint_as_float(w) : max_nan(of_word<T>(w, 0), of_word<T>(w, 1));
+}
+// both halves of a word hold the largest value that is not above v (float32: v)
+template <typename T>
+__device__ __forceinline__ uint32_t splat_down(float v) {
+    if constexpr (sizeof(T) == 4) return __float_as_uint(v);
+    unsigned short b;
+    if constexpr (std::is_same_v<T, __half>) b = __half_as_ushort(__float2half_rd(v));
+    else b = __bfloat16_as_ushort(__float2bfloat16_rd(v));
+    return b | ((uint32_t)b << 16);
+}
+// whether an element of the word reaches the other's
+template <typename T>
+__device__ __forceinline__ bool reaches(uint32_t w, uint32_t least) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w) >= __uint_as_float(least);
+    else if constexpr (std::is_same_v<T, __half>)
+        return __hge2_mask(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&least)) != 0;
+    else
+        return __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&least)) != 0;
+}
+// pair i of a pack's elements
+template <typename T>
+__device__ __forceinline__ F2 pair_of(const uint32_t (&w)[4], int i) {
+    if constexpr (sizeof(T) == 4) return pack_f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    if constexpr (std::is_same_v<T, __half>) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        return pack_f2(f.x, f.y);
+    } else {
+        return pack_f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+}
+
+__device__ __forceinline__ F2 two(float v) { return pack_f2(v, v); }
+
+// The weights of two elements, not below m - 128 / c and below the heavy ones
+__device__ __forceinline__ u64 light_weights(F2 z, const Scale& s) {
+    const F2 minus = two(-1.f), m = two(-s.m), c = two(s.hi);
+    const F2 d = add2(z, m);
+    const F2 b = fma2(d, minus, z);
+    const F2 e = add2(fma2(add2(d, b), minus, z), add2(b, m));
+    const F2 hi = mul2(d, c);
+    const F2 lo = fma2(e, c, fma2(d, two(s.lo), fma2(d, c, mul2(hi, minus))));
+    const F2 rounded = add2(hi, two(kMagic));
+    const F2 f = add2(fma2(add2(rounded, two(-kMagic)), minus, hi), lo);
+    F2 p = two(poly(6));
+#pragma unroll
+    for (int i = 5; i >= 0; --i) p = fma2(p, f, two(poly(i)));
+    float p0, p1, r0, r1;
+    unpack_f2(p, p0, p1);
+    unpack_f2(rounded, r0, r1);
+    const unsigned w0 = __float2uint_rn(__int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23)));
+    const unsigned w1 = __float2uint_rn(__int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23)));
+    return (u64)(w0 + w1);                      // each below 2^31
+}
+
+// What the words of a row are compared with (see Shared): rows whose maximum is so
+// far from zero, in units of the temperature, that the type's steps there span
+// several octaves are not worked on in pairs.
+template <typename T>
+__device__ __forceinline__ bool in_pairs(const Scale& s) {
+    if (std::is_same_v<T, __half> && s.m + s.least < -60000.f) return false;       // no value for a weight of 0
+    return fabsf(s.m) * s.hi < (sizeof(T) == 4 ? 0x1p24f : 0x1p9f);
 }
 
 // ---- a block's part of the row --------------------------------------------------
@@ -201,6 +301,14 @@ struct Row {
         v1 = (int)((int64_t)packs * (rank + 1) / p.cluster);
     }
     __device__ __forceinline__ int first_index(int v) const { return v * V - off; }
+    __device__ __forceinline__ uint4 words(int v) const {
+        const int i = first_index(v);
+        if (i >= 0 && i + V <= vocab) return __ldg(reinterpret_cast<const uint4*>(row + i));
+        alignas(16) T e[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) e[q] = i + q >= 0 && i + q < vocab ? row[i + q] : Num<T>::from_acc(-INFINITY);
+        return *reinterpret_cast<const uint4*>(e);
+    }
     __device__ __forceinline__ void get(int v, float (&z)[V]) const {
         const int i = first_index(v);
         if (i >= 0 && i + V <= vocab) {
@@ -380,6 +488,44 @@ __device__ __forceinline__ u64 row_sum(const Row<T>& row, Team& team, F&& value)
     return team.sum(s);
 }
 
+// One warp: the element of packs [begin, end) at which the running sum of value(z,
+// index) exceeds `target`; tells its index, the value there, `total` and z.
+template <typename T, typename F>
+__device__ __forceinline__ void find_in(const Row<T>& row, Team& team, int begin, int end, u64 target, u64 total,
+                                        F&& value) {
+    constexpr int V = Row<T>::V;
+    const int lane = threadIdx.x & 31;
+    for (int base = begin; base < end; base += 32) {
+        // a pack a lane
+        float z[V];
+        u64 w[V], s = 0;
+#pragma unroll
+        for (int q = 0; q < V; ++q) z[q] = -INFINITY;
+        if (base + lane < end) row.get(base + lane, z);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            w[q] = base + lane < end ? value(z[q], row.first_index(base + lane) + q) : 0;
+            s += w[q];
+        }
+        const u64 sums = warp_scan(s);
+        const unsigned past = __ballot_sync(0xffffffffu, sums > target);
+        if (past && lane == __ffs(past) - 1) {
+            u64 reach = sums - s;
+            bool found = false;
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                reach += w[q];
+                if (!found && reach > target) {
+                    found = true;
+                    team.tell(Found{w[q], total, 0, row.first_index(base + lane) + q, (int)__float_as_uint(z[q])});
+                }
+            }
+        }
+        if (past) break;
+        target -= __shfl_sync(0xffffffffu, sums, 31);
+    }
+}
+
 // The lowest index at which the running sum of value(z, index) exceeds `target`
 // (below the total): i, the value there: a, the total: b, and j, the bits of z.
 // target_of(total) gives the target.
@@ -416,39 +562,7 @@ __device__ __forceinline__ Found locate(const Row<T>& row, Team& team, F&& value
         __syncthreads();
         at = 0;
         while (at < kWarps - 1 && target >= team.sh.warp[at]) target -= team.sh.warp[at++];
-        if (warp == 0) {
-            const int b2 = cut(b1, e1, at), e2 = cut(b1, e1, at + 1);
-            bool done = false;
-            for (int base = b2; base < e2 && !done; base += 32) {
-                // a pack a lane
-                float z[V];
-                u64 w[V], s = 0;
-#pragma unroll
-                for (int q = 0; q < V; ++q) z[q] = -INFINITY;
-                if (base + lane < e2) row.get(base + lane, z);
-#pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    w[q] = base + lane < e2 ? value(z[q], row.first_index(base + lane) + q) : 0;
-                    s += w[q];
-                }
-                const u64 sums = warp_scan(s);
-                const unsigned past = __ballot_sync(0xffffffffu, sums > target);
-                if (past && lane == __ffs(past) - 1) {
-                    u64 reach = sums - s;
-                    bool found = false;
-#pragma unroll
-                    for (int q = 0; q < V; ++q) {
-                        reach += w[q];
-                        if (!found && reach > target) {
-                            found = true;
-                            team.tell(Found{w[q], total, 0, row.first_index(base + lane) + q, (int)__float_as_uint(z[q])});
-                        }
-                    }
-                }
-                done = past != 0;
-                target -= __shfl_sync(0xffffffffu, sums, 31);        // used only where nothing was found
-            }
-        }
+        if (warp == 0) find_in(row, team, cut(b1, e1, at), cut(b1, e1, at + 1), target, total, value);
     }
     return team.told();
 }
@@ -560,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int64_t r = blockIdx.x / (unsigned)p.cluster;
     Team team{sh, (int)(blockIdx.x % (unsigned)p.cluster), p.cluster, 0};
     const Row<T> row(p, r, team.rank);
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const float temperature = p.temperature ? p.temperature[r] : 1.f, u = p.uniforms[r];
     const float top_p = p.top_p ? p.top_p[r] : 1.f, min_p = p.min_p ? p.min_p[r] : 0.f;
     const int given_k = p.top_k ? p.top_k[r] : 0;
@@ -575,11 +689,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         for (int i = t; i < kBins; i += kThreads) sh.bins[i] = 0;
 
     float m = -INFINITY;
-    for (int v = row.v0 + t; v < row.v1; v += kThreads) {
-        float z[V];
-        row.get(v, z);
-#pragma unroll
-        for (int q = 0; q < V; ++q) m = max_nan(m, z[q]);
+    {
+        uint32_t top = splat_down<T>(-INFINITY);
+        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+            const uint4 k = row.words(v);
+            top = max_nan_word<T>(top, max_nan_word<T>(max_nan_word<T>(k.x, k.y), max_nan_word<T>(k.z, k.w)));
+        }
+        m = word_max<T>(top);
     }
     m = team.maximum(m);
     const bool wrong = !(m < INFINITY) || !(temperature >= 0.f && temperature < INFINITY) || u != u || top_p != top_p ||
@@ -612,6 +728,200 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // the last entry of the order that is kept, by top-k and top-p so far and by min_p
     u64 cut = 0;
     const u64 min_cut = (u64)sh.min_key << 32;
+    // (the first block) takes in the other blocks' entries, which are kList together at
+    // most; their number
+    auto gather = [&] {
+        int size = min(sh.listed, kList);
+        for (int k = 1; k < team.size; ++k) {
+            const int more = min((int)read32(&sh.listed, k), kList - size);
+            for (int i = t; i < more; i += kThreads) sh.list[size + i] = read64(&sh.list[i], k);
+            size += more;
+        }
+        return size;
+    };
+    // the list's order and running weights
+    auto order_list = [&](int size) {
+        sort_list(sh.list, size);
+        for (int i = t; i < size; i += kThreads) sh.weight[i] = weight_of(value_of(sh.list[i]), s, sh.powers);
+        __syncthreads();
+        scan_weights(sh, size);
+    };
+    // The list holds, in order, all that is kept, `size` entries of it: the token (first block)
+    auto choose = [&](int size) {
+        const u64 total = sh.weight[size - 1];
+        // single weights again, and the entries by index
+        u64 w[kList / kThreads];
+#pragma unroll
+        for (int k = 0; k < kList / kThreads; ++k) {
+            const int i = t + k * kThreads;
+            w[k] = i < size ? sh.weight[i] - (i ? sh.weight[i - 1] : 0) : 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kList / kThreads; ++k) {
+            const int i = t + k * kThreads;
+            if (i < size) sh.list[i] = (sh.list[i] << 32) | (unsigned)i;
+        }
+        __syncthreads();
+        u64* const by_rank = reinterpret_cast<u64*>(sh.bins);        // the counts are done with
+        static_assert(sizeof(sh.bins) >= sizeof(sh.weight), "");
+#pragma unroll
+        for (int k = 0; k < kList / kThreads; ++k)
+            if (t + k * kThreads < size) by_rank[t + k * kThreads] = w[k];
+        sort_list(sh.list, size);
+        for (int i = t; i < size; i += kThreads) sh.weight[i] = by_rank[(int)(sh.list[i] & 0xFFFFFFFFu)];
+        __syncthreads();
+        scan_weights(sh, size);
+        if (t == 0) {
+            const int at = first_reaching(sh.weight, size, share_floor(u, total) + 1);
+            const int token = (int)~(unsigned)(sh.list[at] >> 32);
+            const u64 weight = sh.weight[at] - (at ? sh.weight[at - 1] : 0);
+            const T* z = row.row;
+            write_result(p, r, token, Num<T>::to_acc(z[token]), weight, total, s);
+        }
+    };
+    // how many of the list's first `size` entries min_p keeps
+    auto kept_of = [&](int size) {
+        int lo = 0, hi = size;                              // descending order
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (sh.list[mid] < min_cut) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;                                          // at least 1: the largest
+    };
+    // 2: in pairs of elements, the sum of the light weights; the heavy ones go into the list
+    const bool weigh = top_p < 1.f || top_k == 0;
+    if (in_pairs<T>(s)) {
+        const uint32_t least = splat_down<T>(__fadd_rd(m, s.least)), heavy = splat_down<T>(__fadd_rd(m, 1.001f * kHeavy / s.hi));
+        // one warp's packs [begin, end); entries are listed the first time alone
+        auto light_part = [&](int begin, int end, bool list) {
+            u64 sum = 0;
+            for (int v = begin + lane; v < end; v += 32) {
+                const uint4 k = row.words(v);
+                uint32_t w[4] = {k.x, k.y, k.z, k.w};
+                if (reaches<T>(max_word<T>(max_word<T>(w[0], w[1]), max_word<T>(w[2], w[3])), heavy)) {
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        constexpr int PER = 4 / sizeof(T);
+                        const float z = of_word<T>(w[q / PER], q % PER);
+                        float hi, lo;
+                        exponent(z, s, hi, lo);
+                        if (!(hi >= kHeavy)) continue;
+                        if (list) {
+                            const int at = atomicAdd(&sh.listed, 1);
+                            if (at < kList) sh.list[at] = entry_of(z, row.first_index(v) + q);
+                        }
+                        if constexpr (sizeof(T) == 4) w[q] = least;
+                        else w[q / 2] = q % 2 ? (w[q / 2] & 0xFFFFu) | (least & 0xFFFF0000u) : (w[q / 2] & 0xFFFF0000u) | (least & 0xFFFFu);
+                    }
+                }
+                if (!weigh) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = max_word<T>(w[i], least);
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) sum += light_weights(pair_of<T>(w, i), s);
+            }
+            return Team::warp_add(sum);
+        };
+        auto cut_of = [](int begin, int end, int k) { return begin + (int)((int64_t)(end - begin) * k / kWarps); };
+        u64 own = light_part(cut_of(row.v0, row.v1, warp), cut_of(row.v0, row.v1, warp + 1), true);
+        if (lane == 0) sh.light[warp] = own;
+        __syncthreads();
+        u64 light = 0, listed = sh.listed, x, y;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) light += sh.light[w];
+        light = t == 0 ? light : 0;
+        listed = t == 0 ? listed : 0;
+        team.sum(light, listed, x, y);
+        if (listed <= (u64)kList) {
+            // the list holds every heavy token: what is kept may end within it
+            enum { DONE, ALL, OTHER };
+            if (team.rank == 0) {
+                const int size = gather();
+                order_list(size);
+                if (t == 0) sh.listed = size;
+                const u64 weight = sh.weight[size - 1];
+                const bool k_here = top_k > 0 && top_k <= size, all = !k_here && top_k > 0;
+                int keep = k_here ? top_k : size + 1;               // size + 1: beyond the list
+                const u64 total = k_here ? sh.weight[keep - 1] : light + weight;
+                if (top_p < 1.f && !all) {
+                    const int at = first_reaching(sh.weight, size, share_ceil(top_p, total));
+                    if (at < size) keep = min(keep, at + 1);
+                }
+                const int least_p = kept_of(size);
+                if (least_p < size && !(all && top_p < 1.f)) keep = min(keep, least_p);
+                const int what = keep <= size ? DONE : (top_k == 0 && !(top_p < 1.f) && min_cut == 0 ? ALL : OTHER);
+                if (what == DONE) choose(keep);
+                __syncthreads();
+                if (t == 0) team.tell(Found{light + weight, 0, 0, what, 0});
+            }
+            const Found f = team.told();
+            if (f.i == DONE) {
+                team.barrier();                                     // nobody leaves while others read its memory
+                return;
+            }
+            if (f.i == ALL) {
+                // the token by sums over the row: the parts' light sums, and the listed tokens of each
+                auto add_listed = [&](int begin, int end) {         // sh.warp: by sixteenths of [begin, end)
+                    const int size = sh.listed;
+                    for (int i = t; i < size; i += kThreads) {
+                        const u64 entry = sh.list[i];
+                        const int v = (index_of(entry) + row.off) / V;
+                        if (v < begin || v >= end) continue;
+                        int k = (int)((int64_t)(v - begin) * kWarps / (end - begin));
+                        while (k > 0 && v < cut_of(begin, end, k)) --k;
+                        while (k < kWarps - 1 && v >= cut_of(begin, end, k + 1)) ++k;
+                        atomicAdd(&sh.warp[k], weight_of(value_of(entry), s, sh.powers));
+                    }
+                    __syncthreads();
+                };
+                u64 target = share_floor(u, f.a);
+                __syncthreads();
+                if (t < kWarps) sh.warp[t] = sh.light[t];
+                __syncthreads();
+                add_listed(row.v0, row.v1);
+                u64 mine = 0;
+                for (int w = 0; w < kWarps; ++w) mine += sh.warp[w];
+                u64 before = 0, none = 0, none_before;
+                u64 sum = t == 0 ? mine : 0;
+                const u64 parts = lane < kWarps ? sh.warp[lane] : 0;        // (the cluster's sums take sh.warp)
+                team.sum(sum, none, before, none_before);
+                if (target >= before && target < before + mine) {           // the whole block
+                    target -= before;
+                    int begin = row.v0, end = row.v1;
+                    u64 part = parts;
+                    for (int level = 0; level < 2; ++level) {
+                        int at = 0;
+                        while (at < kWarps - 1) {
+                            const u64 p = __shfl_sync(0xffffffffu, part, at);
+                            if (target < p) break;
+                            target -= p;
+                            ++at;
+                        }
+                        const int b = cut_of(begin, end, at), e = cut_of(begin, end, at + 1);
+                        begin = b;
+                        end = e;
+                        if (level == 1) break;
+                        own = light_part(cut_of(begin, end, warp), cut_of(begin, end, warp + 1), false);
+                        __syncthreads();
+                        if (lane == 0) sh.warp[warp] = own;
+                        __syncthreads();
+                        add_listed(begin, end);
+                        part = lane < kWarps ? sh.warp[lane] : 0;
+                    }
+                    if (warp == 0) find_in(row, team, begin, end, target, f.a, [&](float z, int) { return weight_of(z, s, sh.powers); });
+                }
+                const Found at = team.told();
+                if (team.rank == 0 && t == 0) write_result(p, r, at.i, __int_as_float(at.j), at.a, at.b, s);
+                team.barrier();
+                return;
+            }
+        }
+        // everything else: the list starts anew
+        if (t == 0) sh.listed = 0;
+        team.barrier();
+    }
     if (counts) {
         // 2: the histogram.  Each block takes a share of the bins afterwards, each thread
         // `each` in a row; bin b lies where the threads' b-th bins are side by side.
@@ -631,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         team.barrier();
         u64 count = 0, mass = 0;
-        auto bin_weight = [](int b) { return (u64)(exp2f((b + 0.5f) * -((float)kOctaves / kBins)) * 0x1p43f) + 1; };
+        auto bin_weight = [](int b) { return ((u64)__float2uint_rz(exp2f((b + 0.5f) * -((float)kOctaves / kBins)) * 0x1p31f) << 12) + 1; };
         for (int i = 0; i < each; ++i) {
             unsigned* const at = &sh.bins[i * stride + mine];
             unsigned k = *at;
@@ -679,68 +989,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                     if (f < from) above += w;
                 }
             }
-        };
-        // (the first block) takes in the other blocks' entries, which are kList together at
-        // most; their number
-        auto gather = [&] {
-            int size = min(sh.listed, kList);
-            for (int k = 1; k < team.size; ++k) {
-                const int more = min((int)read32(&sh.listed, k), kList - size);
-                for (int i = t; i < more; i += kThreads) sh.list[size + i] = read64(&sh.list[i], k);
-                size += more;
-            }
-            return size;
-        };
-        // the list's order and running weights
-        auto order_list = [&](int size) {
-            sort_list(sh.list, size);
-            for (int i = t; i < size; i += kThreads) sh.weight[i] = weight_of(value_of(sh.list[i]), s, sh.powers);
-            __syncthreads();
-            scan_weights(sh, size);
-        };
-        // The list holds, in order, all that is kept, `size` entries of it: the token (first block)
-        auto choose = [&](int size) {
-            const u64 total = sh.weight[size - 1];
-            // single weights again, and the entries by index
-            u64 w[kList / kThreads];
-#pragma unroll
-            for (int k = 0; k < kList / kThreads; ++k) {
-                const int i = t + k * kThreads;
-                w[k] = i < size ? sh.weight[i] - (i ? sh.weight[i - 1] : 0) : 0;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kList / kThreads; ++k) {
-                const int i = t + k * kThreads;
-                if (i < size) sh.list[i] = (sh.list[i] << 32) | (unsigned)i;
-            }
-            __syncthreads();
-            u64* const by_rank = reinterpret_cast<u64*>(sh.bins);        // the counts are done with
-            static_assert(sizeof(sh.bins) >= sizeof(sh.weight), "");
-#pragma unroll
-            for (int k = 0; k < kList / kThreads; ++k)
-                if (t + k * kThreads < size) by_rank[t + k * kThreads] = w[k];
-            sort_list(sh.list, size);
-            for (int i = t; i < size; i += kThreads) sh.weight[i] = by_rank[(int)(sh.list[i] & 0xFFFFFFFFu)];
-            __syncthreads();
-            scan_weights(sh, size);
-            if (t == 0) {
-                const int at = first_reaching(sh.weight, size, share_floor(u, total) + 1);
-                const int token = (int)~(unsigned)(sh.list[at] >> 32);
-                const u64 weight = sh.weight[at] - (at ? sh.weight[at - 1] : 0);
-                const T* z = row.row;
-                write_result(p, r, token, Num<T>::to_acc(z[token]), weight, total, s);
-            }
-        };
-        // how many of the list's first `size` entries min_p keeps
-        auto kept_of = [&](int size) {
-            int lo = 0, hi = size;                              // descending order
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (sh.list[mid] < min_cut) hi = mid;
-                else lo = mid + 1;
-            }
-            return lo;                                          // at least 1: the largest
         };
         // The cut at which the sum of value(z) over kept entries reaches `least`, by
         // bisection over keys, then among equal ones by index.
