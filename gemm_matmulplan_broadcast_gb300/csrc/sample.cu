@@ -41,6 +41,9 @@ constexpr int kMaxCluster = 8;
 constexpr int kBins = 8192;
 constexpr int kOctaves = 45;            // below 2^-45 of the largest a weight is 0
 constexpr int kList = 2048;
+constexpr int kSmall = 192;             // entries up to which a list is ordered by counting
+constexpr int kBracket = 1024;          // tokens of the steps in which top-p's cut lies
+constexpr int kMostK = kThreads * 7 / 8;    // the largest top_k that the threads' maxima bound
 constexpr int kOne = 43;                // the largest weight is 2^43; vocab <= 2^20
 constexpr float kHeavy = -12.f;         // x from which on weights are formed in two parts
 
@@ -68,7 +71,7 @@ struct Params {
 struct Scale {
     float m, hi, lo;
     float least;            // z - m is not taken below this one (x = -64, where weights are 0)
-    float per_step;         // bins: (m - z) per_step
+    int exact;              // the light weights' differences z - m in two parts
 };
 
 // what one block tells the others of its cluster
@@ -83,6 +86,7 @@ struct Shared {
     u64 exchange[2][2];         // [parity]: sums of this block
     Found found[2];             // of the first block: [parity]
     int listed;                 // entries of this block's list
+    int listed2;
     u64 light[kWarps];          // sums of the warps' parts without the listed entries
     Scale scale;
     double min_distance;
@@ -91,6 +95,8 @@ struct Shared {
                                         // weights by rank
     alignas(16) u64 list[kList];        // key above ~index; the first block's takes the others' in
     u64 weight[kList];
+    alignas(16) u64 list2[kBracket];
+    u64 weight2[kBracket];
 };
 
 // ---- values and weights -------------------------------------------------------
@@ -121,12 +127,14 @@ __device__ __forceinline__ Scale scale_of(float temperature, float min_p, double
     s.hi = (float)c;
     s.lo = (float)(c - (double)s.hi);
     s.least = -64.f / s.hi;
-    s.per_step = s.hi * ((float)kBins / kOctaves);
+    s.exact = 1;
     min_distance = min_p > 0.f ? heat * log((double)min_p) : 0.0;
     return s;
 }
 
-__device__ __forceinline__ float step_of(float z, const Scale& s) { return (s.m - z) * s.per_step; }
+// steps of x, 0 at the maximum (an infinity for z = -inf)
+constexpr float kStepsPerOctave = (float)kBins / kOctaves;
+__device__ __forceinline__ float step_of(float z, const Scale& s) { return (z - s.m) * -s.hi * kStepsPerOctave; }
 
 // x in two parts
 __device__ __forceinline__ void exponent(float z, const Scale& s, float& hi, float& lo) {
@@ -138,7 +146,9 @@ __device__ __forceinline__ void exponent(float z, const Scale& s, float& hi, flo
         e = 0.f;
     }
     hi = d * s.hi;
-    lo = fmaf(e, s.hi, fmaf(d, s.lo, fmaf(d, s.hi, -hi)));
+    if (hi < kHeavy && !s.exact) e = 0.f;
+    lo = fmaf(d, s.lo, fmaf(d, s.hi, -hi));
+    lo = fmaf(e, s.hi, lo);
 }
 
 constexpr float kMagic = 12582912.f;            // 1.5 2^23: adding it rounds to an integer in the low bits
@@ -252,24 +262,34 @@ __device__ __forceinline__ F2 pair_of(const uint32_t (&w)[4], int i) {
 
 __device__ __forceinline__ F2 two(float v) { return pack_f2(v, v); }
 
-// The weights of two elements, not below m - 128 / c and below the heavy ones
-__device__ __forceinline__ u64 light_weights(F2 z, const Scale& s) {
+// The light weights of two elements (z above m - 128 / c); masked: those of steps below
+// `low`.  FP32 operations bound it: 14 an element, 19 with EXACT differences.
+template <bool EXACT>
+__device__ __forceinline__ u64 light_weights(F2 z, const Scale& s, bool masked, float low) {
     const F2 minus = two(-1.f), m = two(-s.m), c = two(s.hi);
     const F2 d = add2(z, m);
-    const F2 b = fma2(d, minus, z);
-    const F2 e = add2(fma2(add2(d, b), minus, z), add2(b, m));
-    const F2 hi = mul2(d, c);
-    const F2 lo = fma2(e, c, fma2(d, two(s.lo), fma2(d, c, mul2(hi, minus))));
-    const F2 rounded = add2(hi, two(kMagic));
-    const F2 f = add2(fma2(add2(rounded, two(-kMagic)), minus, hi), lo);
+    const F2 down = mul2(d, two(-s.hi));                        // -hi
+    F2 lo = fma2(d, two(s.lo), fma2(d, c, down));
+    if constexpr (EXACT) {
+        const F2 b = fma2(d, minus, z);
+        lo = fma2(add2(fma2(add2(d, b), minus, z), add2(b, m)), c, lo);
+    }
+    const F2 rounded = fma2(down, minus, two(kMagic));
+    const F2 f = fma2(add2(add2(rounded, two(-kMagic)), down), minus, lo);
     F2 p = two(poly(6));
 #pragma unroll
     for (int i = 5; i >= 0; --i) p = fma2(p, f, two(poly(i)));
     float p0, p1, r0, r1;
     unpack_f2(p, p0, p1);
     unpack_f2(rounded, r0, r1);
-    const unsigned w0 = __float2uint_rn(__int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23)));
-    const unsigned w1 = __float2uint_rn(__int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23)));
+    unsigned w0 = __float2uint_rn(__int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23)));
+    unsigned w1 = __float2uint_rn(__int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23)));
+    if (masked) {
+        float d0, d1;
+        unpack_f2(mul2(down, two(kStepsPerOctave)), d0, d1);
+        if (!(d0 < low)) w0 = 0;
+        if (!(d1 < low)) w1 = 0;
+    }
     return (u64)(w0 + w1);                      // each below 2^31
 }
 
@@ -590,21 +610,21 @@ __device__ __forceinline__ int sort_list(u64* list, int n) {
     return size;
 }
 
-// sh.weight: running sums of the first n
-__device__ __forceinline__ void scan_weights(Shared& sh, int n) {
+// running sums of the first n
+__device__ __forceinline__ void scan_weights(u64* weight, int n, u64* slot) {
     constexpr int PER = kList / kThreads;
     const int first = threadIdx.x * PER;
     u64 w[PER], s = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        w[i] = first + i < n ? sh.weight[first + i] : 0;
+        w[i] = first + i < n ? weight[first + i] : 0;
         s += w[i];
     }
-    u64 before = block_scan(s, sh.warp);
+    u64 before = block_scan(s, slot);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         before += w[i];
-        if (first + i < n) sh.weight[first + i] = before;
+        if (first + i < n) weight[first + i] = before;
     }
     __syncthreads();
 }
@@ -664,8 +684,408 @@ __device__ __forceinline__ void write_result(const Params& p, int64_t row, int t
     p.logprob[row] = lp;
 }
 
-// ---- the kernel ----------------------------------------------------------------------
+// ---- the list, by the first block ------------------------------------------------------
 
+// takes in the other blocks' entries, which are `most` together at most; their number
+__device__ __forceinline__ int gather(Team& team, u64* list, const int* listed, int most) {
+    int size = min(*listed, most);
+    for (int k = 1; k < team.size; ++k) {
+        const int more = min((int)read32(listed, k), most - size);
+        for (int i = threadIdx.x; i < more; i += kThreads) list[size + i] = read64(&list[i], k);
+        size += more;
+    }
+    return size;
+}
+
+// threads that share one of `size` entries: 2^this, within a warp
+__device__ __forceinline__ int log_share(int size) {
+    int log = 5;
+    while (log > 0 && (size << log) > kThreads) --log;
+    return log;
+}
+
+// the list's order, and the weights' running sums in it
+__device__ __forceinline__ void order_list(u64* list, u64* weight, int size, const Scale& s, Shared& sh) {
+    const int t = threadIdx.x;
+    if (size <= kSmall) {
+        // each entry's place is the number of larger ones (their weights are summed on the way)
+        const int log = log_share(size), each = 1 << log, i = t >> log;
+        __syncthreads();
+        if (t < size) weight[t] = weight_of(value_of(list[t]), s, sh.powers);
+        __syncthreads();
+        const u64 own = i < size ? list[i] : 0;
+        u64 before = 0;
+        int place = 0;
+        if (i < size)
+            for (int j = t & (each - 1); j < size; j += each)
+                if (list[j] > own) {
+                    before += weight[j];
+                    ++place;
+                }
+        for (int d = 1; d < each; d <<= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, d);
+            place += __shfl_xor_sync(0xffffffffu, place, d);
+        }
+        if (i < size) before += weight[i];
+        __syncthreads();
+        if (i < size && (t & (each - 1)) == 0) {
+            list[place] = own;
+            weight[place] = before;
+        }
+        __syncthreads();
+        return;
+    }
+    sort_list(list, size);
+    for (int i = t; i < size; i += kThreads) weight[i] = weight_of(value_of(list[i]), s, sh.powers);
+    __syncthreads();
+    scan_weights(weight, size, sh.warp);
+}
+
+// The list's first `size` entries, in order, are all that is kept: the token.
+template <typename T>
+__device__ __forceinline__ void choose(const Params& p, int64_t r, const Row<T>& row, float u, int size, const Scale& s,
+                                       Shared& sh) {
+    const int t = threadIdx.x;
+    const u64 total = sh.weight[size - 1];
+    const u64 target = share_floor(u, total);
+    if (size <= kSmall) {
+        // the entry whose weight, behind those of lower indices, reaches over the target
+        const int log = log_share(size), each = 1 << log, i = t >> log;
+        u64 before = 0, own = 0;
+        unsigned mine = 0;
+        if (i < size) {
+            mine = (unsigned)sh.list[i];                // ~index
+            own = sh.weight[i] - (i ? sh.weight[i - 1] : 0);
+            for (int j = t & (each - 1); j < size; j += each)
+                if ((unsigned)sh.list[j] > mine) before += sh.weight[j] - (j ? sh.weight[j - 1] : 0);
+        }
+        for (int d = 1; d < each; d <<= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+        if (i < size && (t & (each - 1)) == 0 && before <= target && target < before + own)
+            write_result(p, r, (int)~mine, value_of(sh.list[i]), own, total, s);
+        return;
+    }
+    // single weights again, and the entries by index
+    u64 w[kList / kThreads];
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k) {
+        const int i = t + k * kThreads;
+        w[k] = i < size ? sh.weight[i] - (i ? sh.weight[i - 1] : 0) : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k) {
+        const int i = t + k * kThreads;
+        if (i < size) sh.list[i] = (sh.list[i] << 32) | (unsigned)i;
+    }
+    __syncthreads();
+    u64* const by_rank = reinterpret_cast<u64*>(sh.bins);        // the counts are done with
+    static_assert(sizeof(sh.bins) >= sizeof(sh.weight), "");
+#pragma unroll
+    for (int k = 0; k < kList / kThreads; ++k)
+        if (t + k * kThreads < size) by_rank[t + k * kThreads] = w[k];
+    sort_list(sh.list, size);
+    for (int i = t; i < size; i += kThreads) sh.weight[i] = by_rank[(int)(sh.list[i] & 0xFFFFFFFFu)];
+    __syncthreads();
+    scan_weights(sh.weight, size, sh.warp);
+    if (t == 0) {
+        const int at = first_reaching(sh.weight, size, target + 1);
+        const int token = (int)~(unsigned)(sh.list[at] >> 32);
+        const u64 weight = sh.weight[at] - (at ? sh.weight[at - 1] : 0);
+        write_result(p, r, token, Num<T>::to_acc(row.row[token]), weight, total, s);
+    }
+}
+
+// how many of the first `size` entries of an ordered list are not below `cut`
+__device__ __forceinline__ int kept_of(const u64* list, int size, u64 cut) {
+    int lo = 0, hi = size;                                  // descending order
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (list[mid] < cut) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+// ---- the histogram ---------------------------------------------------------------------
+
+// Counts of tokens by steps.  Each block takes a share of the bins when they are counted, each
+// thread `each` in a row; bin b lies where the threads' b-th bins are side by side.
+struct Bins {
+    Team& team;
+    int log_each, each, stride, mine;
+    u64 before_count, before_mass;      // this thread's bins'
+    u64 count, mass;                    // the cluster's
+
+    __device__ __forceinline__ explicit Bins(Team& t) : team(t) {
+        log_each = 31 - __clz(kBins / kThreads / team.size);
+        each = 1 << log_each;
+        stride = kBins >> log_each;
+        mine = team.rank * kThreads + threadIdx.x;
+    }
+    __device__ __forceinline__ void clear() {
+        for (int i = threadIdx.x; i < kBins; i += kThreads) team.sh.bins[i] = 0;
+        __syncthreads();
+    }
+    __device__ __forceinline__ void add(float step) {
+        const int b = (int)step;
+        atomicAdd(&team.sh.bins[(b & (each - 1)) * stride + (b >> log_each)], 1u);
+    }
+    // the weight in a step's middle, at least 1
+    static __device__ __forceinline__ u64 weight(int b) {
+        return ((u64)__float2uint_rz(exp2f((b + 0.5f) * (-1.f / kStepsPerOctave)) * 0x1p31f) << 12) + 1;
+    }
+    __device__ __forceinline__ void sum() {
+        team.barrier();
+        u64 c = 0, w = 0;
+        for (int i = 0; i < each; ++i) {
+            unsigned* const at = &team.sh.bins[i * stride + mine];
+            unsigned k = *at;
+            if (team.size > 1) {
+                for (int other = 1; other < team.size; ++other) k += read32(at, (team.rank + other) & (team.size - 1));
+                *at = k;                        // only this block reads its share of its bins
+            }
+            c += k;
+            w += k * weight(mine * each + i);
+        }
+        count = c;
+        mass = w;
+        team.sum(count, mass, before_count, before_mass);
+        before_count += block_scan(c, team.sh.warp);
+        before_mass += block_scan(w, team.sh.warp2);
+    }
+    // f(bin, count before it, weight before it, its count) for this thread's bins in order
+    template <typename F>
+    __device__ __forceinline__ void in_order(F&& f) {
+        u64 c = before_count, w = before_mass;
+        for (int i = 0; i < each; ++i) {
+            const unsigned k = team.sh.bins[i * stride + mine];
+            const int b = mine * each + i;
+            f(b, c, w, k);
+            c += k;
+            w += k * weight(b);
+        }
+    }
+    // the bin in which the estimated weight reaches over `target`: i, and the counts before it
+    // and up to its end: a, b
+    __device__ __forceinline__ Found reaching(u64 target) {
+        in_order([&](int b, u64 c, u64 w, unsigned k) {
+            if (w <= target && target < w + k * weight(b)) team.tell(Found{c, c + k, 0, b, 0});
+        });
+        return team.told();
+    }
+};
+
+// ---- any row ---------------------------------------------------------------------------
+
+struct Settings {
+    float u, top_p;
+    int top_k;              // 0: all
+    unsigned max_key;
+    u64 min_cut;            // the last entry that min_p keeps
+};
+
+// Single elements, whatever their values: rows far from zero, rows with more tokens at
+// a cut than the lists hold, k beyond the threads' maxima.
+template <typename T>
+__device__ __noinline__ void any_row(const Params& p, int64_t r, const Row<T>& row, Team& team, const Scale& s,
+                                     const Settings& o) {
+    constexpr int V = Row<T>::V;
+    Shared& sh = team.sh;
+    const int t = threadIdx.x;
+    if (t == 0) sh.listed = 0;
+    u64 cut = 0;                                            // the last entry that is kept so far
+    // Tokens of steps [from, to) that `cut` keeps go into the block's list; the
+    // weights of all that it keeps are added to `all`, those of lower steps to `above`.
+    auto collect = [&](float from, float to, bool weigh, u64& all, u64& above) {
+        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+            float z[V];
+            row.get(v, z);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float f = step_of(z[q], s);
+                const u64 entry = entry_of(z[q], row.first_index(v) + q);
+                if (!(f < (float)kBins) || entry < cut) continue;
+                if (f >= from && f < to) {
+                    const int at = atomicAdd(&sh.listed, 1);
+                    if (at < kList) sh.list[at] = entry;
+                }
+                if (!weigh) continue;
+                const u64 w = weight_of(z[q], s, sh.powers);
+                all += w;
+                if (f < from) above += w;
+            }
+        }
+    };
+    // The cut at which the sum of value(z) over kept entries reaches `least`, by
+    // bisection over keys, then among equal ones by index.
+    auto bisect = [&](auto&& value, u64 least) {
+        unsigned lo = 0, hi = o.max_key;                    // sum(key >= lo) >= least
+        while (lo < hi) {
+            const unsigned mid = hi - (hi - lo) / 2;
+            const u64 sum = row_sum(row, team, [&](float z, int i) -> u64 {
+                return order_key(z) >= mid && entry_of(z, i) >= cut ? value(z) : 0;
+            });
+            if (sum >= least) lo = mid;
+            else hi = mid - 1;
+        }
+        const u64 above = row_sum(row, team, [&](float z, int i) -> u64 {
+            return order_key(z) > lo && entry_of(z, i) >= cut ? value(z) : 0;
+        });
+        const Found f = locate(
+            row, team, [&](float z, int i) -> u64 { return order_key(z) == lo && entry_of(z, i) >= cut ? value(z) : 0; },
+            [&](u64) -> u64 { return least - above - 1; });
+        cut = ((u64)lo << 32) | (unsigned)~f.i;
+    };
+    auto weight = [&](float z) { return weight_of(z, s, sh.powers); };
+    // the first block is done with the list; `entry` is the new cut.  Every block hears of it,
+    // and empties its list for the next collection.
+    auto cut_told = [&](u64 entry, bool good) {
+        __syncthreads();                                    // the block has read what it needs
+        if (team.rank == 0 && t == 0) team.tell(Found{entry, 0, 0, good, 0});
+        const Found f = team.told();
+        if (t == 0) sh.listed = 0;
+        return f;
+    };
+    if (o.top_k > 0 || o.top_p < 1.f) {
+        Bins bins(team);
+        bins.clear();
+        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+            float z[V];
+            row.get(v, z);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float f = step_of(z[q], s);
+                if (f < (float)kBins) bins.add(f);
+            }
+        }
+        bins.sum();
+        u64 unused = 0;
+        u64 known = bins.mass;                              // estimate of the k tokens' weight
+        if (o.top_k && bins.count > (u64)o.top_k) {
+            bins.in_order([&](int b, u64 c, u64 w, unsigned k) {
+                if (c < (u64)o.top_k && c + k >= (u64)o.top_k)
+                    team.tell(Found{c, c + k, w + ((u64)o.top_k - c) * Bins::weight(b), b, 0});
+            });
+            const Found f = team.told();
+            known = f.c;
+            if (f.b - f.a <= (u64)kList) {
+                collect((float)f.i, (float)(f.i + 1), false, unused, unused);
+                team.barrier();
+                u64 last = 0;
+                if (team.rank == 0) {
+                    order_list(sh.list, sh.weight, gather(team, sh.list, &sh.listed, kList), s, sh);
+                    last = sh.list[o.top_k - 1 - (int)f.a];
+                }
+                cut = cut_told(last, true).a;
+            } else {
+                bisect([](float) -> u64 { return 1; }, (u64)o.top_k);
+            }
+        }
+        if (o.top_p < 1.f) {
+            // the steps around the estimate; wider ones where it was not good enough
+            for (float off = 0x1p-10f;; off *= 8.f) {
+                const float near = (float)known * o.top_p;
+                const u64 last = bins.mass - 1;
+                const Found low = bins.reaching(min((u64)(near * fmaxf(1.f - off, 0.f)), last));
+                const Found high = bins.reaching(min((u64)(near * (1.f + off)), last));
+                if (high.b - low.a > (u64)kList || off > 8.f) {
+                    const u64 all = row_sum(row, team, [&](float z, int i) -> u64 { return entry_of(z, i) >= cut ? weight(z) : 0; });
+                    bisect(weight, share_ceil(o.top_p, all));
+                    break;
+                }
+                u64 all = 0, above = 0, b1, b2, last_kept = 0;
+                collect((float)low.i, (float)(high.i + 1), true, all, above);
+                team.sum(all, above, b1, b2);
+                bool good = false;
+                if (team.rank == 0) {
+                    const int size = gather(team, sh.list, &sh.listed, kList);
+                    const u64 target = share_ceil(o.top_p, all);
+                    order_list(sh.list, sh.weight, size, s, sh);
+                    good = size > 0 && above < target && target - above <= sh.weight[size - 1];
+                    if (good) last_kept = sh.list[first_reaching(sh.weight, size, target - above)];
+                }
+                const Found f = cut_told(last_kept, good);
+                if (!f.i) continue;
+                cut = f.a;
+                break;
+            }
+        }
+    }
+    // the token by sums over all that is kept
+    cut = max(cut, o.min_cut);
+    const Found f = locate(
+        row, team, [&](float z, int i) -> u64 { return entry_of(z, i) >= cut ? weight(z) : 0; },
+        [&](u64 sum) -> u64 { return share_floor(o.u, sum); });
+    if (team.rank == 0 && t == 0) write_result(p, r, f.i, __int_as_float(f.j), f.a, f.b, s);
+    team.barrier();                                         // nobody leaves while others read its memory
+}
+
+// ---- rows near zero, in pairs ------------------------------------------------------------
+
+// What a pass over the light elements does beside summing their weights.
+struct Pass {
+    bool heavy_to_list;     // lists the heavy tokens
+    bool masked;            // sums the steps below `low` only
+    bool steps_to_list2;    // lists the light tokens of steps [low, high)
+    float low, high;
+    uint32_t least, heavy;  // words: what elements are raised to, what no heavy one is below
+};
+
+// One warp's packs [begin, end): the sum of the light weights.
+template <typename T, bool EXACT>
+__device__ __noinline__ u64 light_part(const Row<T>& row, Shared& sh, int begin, int end, const Pass& pass) {
+    constexpr int V = Row<T>::V, PER = 4 / sizeof(T);
+    const Scale s = sh.scale;
+    const Pass what = pass;
+    u64 sum = 0;
+    for (int v = begin + (int)(threadIdx.x & 31); v < end; v += 32) {
+        const uint4 k = row.words(v);
+        uint32_t w[4] = {k.x, k.y, k.z, k.w};
+        if (reaches<T>(max_word<T>(max_word<T>(w[0], w[1]), max_word<T>(w[2], w[3])), what.heavy)) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float z = of_word<T>(w[q / PER], q % PER);
+                if (!((z - s.m) * s.hi >= kHeavy)) continue;
+                if (what.heavy_to_list) {
+                    const int at = atomicAdd(&sh.listed, 1);
+                    if (at < kList) sh.list[at] = entry_of(z, row.first_index(v) + q);
+                }
+                if constexpr (PER == 1) w[q] = what.least;
+                else w[q / 2] = q % 2 ? (w[q / 2] & 0xFFFFu) | (what.least & 0xFFFF0000u) : (w[q / 2] & 0xFFFF0000u) | (what.least & 0xFFFFu);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = max_word<T>(w[i], what.least);
+        if (what.steps_to_list2) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float z = of_word<T>(w[q / PER], q % PER), f = step_of(z, s);
+                if (f < what.low || !(f < what.high)) continue;
+                const int at = atomicAdd(&sh.listed2, 1);
+                if (at < kBracket) sh.list2[at] = entry_of(z, row.first_index(v) + q);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) sum += light_weights<EXACT>(pair_of<T>(w, i), s, what.masked, what.low);
+    }
+    return Team::warp_add(sum);
+}
+
+// The kth largest of the threads' maxima or a little less: k elements or more are not
+// below it.
+__device__ __forceinline__ float bound_of(unsigned key, unsigned max_key, int k) {
+    unsigned lo = 0, hi = max_key;                          // k threads or more reach lo
+    while (lo < hi) {
+        const unsigned mid = hi - (hi - lo) / 2;
+        const int n = __syncthreads_count(key >= mid);
+        if (n >= k) lo = mid;
+        else hi = mid - 1;
+        if (n >= k && n <= k + k / 8) break;
+    }
+    return key_value(lo);
+}
+
+// ---- the kernel ----------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) unsigned char memory[];
@@ -681,13 +1101,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int top_k = given_k > 0 && given_k < p.vocab ? given_k : 0;
     if (t < 64) sh.powers[t] = p.powers[t];
     if (t == 0) {
-        sh.listed = 0;
+        sh.listed = sh.listed2 = 0;
         sh.scale = scale_of(temperature, min_p, sh.min_distance);
     }
-    const bool counts = top_k > 0 || top_p < 1.f;
-    if (counts)
-        for (int i = t; i < kBins; i += kThreads) sh.bins[i] = 0;
-
     float m = -INFINITY;
     {
         uint32_t top = splat_down<T>(-INFINITY);
@@ -697,6 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         m = word_max<T>(top);
     }
+    const float own_max = m;
     m = team.maximum(m);
     const bool wrong = !(m < INFINITY) || !(temperature >= 0.f && temperature < INFINITY) || u != u || top_p != top_p ||
                        min_p != min_p;
@@ -710,6 +1127,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     if (t == 0) {
         sh.scale.m = m;
+        // differences z - m lose bits that count where m is small beside them, or in 32 bits
+        sh.scale.exact = sizeof(T) == 4 || fabsf(m) * sh.scale.hi < 0x1p-5f;
         sh.min_key = min_p > 0.f ? order_key(__double2float_ru((double)m + sh.min_distance)) : 0;
     }
     __syncthreads();
@@ -725,390 +1144,193 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         team.barrier();
         return;
     }
-    // the last entry of the order that is kept, by top-k and top-p so far and by min_p
-    u64 cut = 0;
-    const u64 min_cut = (u64)sh.min_key << 32;
-    // (the first block) takes in the other blocks' entries, which are kList together at
-    // most; their number
-    auto gather = [&] {
-        int size = min(sh.listed, kList);
-        for (int k = 1; k < team.size; ++k) {
-            const int more = min((int)read32(&sh.listed, k), kList - size);
-            for (int i = t; i < more; i += kThreads) sh.list[size + i] = read64(&sh.list[i], k);
-            size += more;
-        }
-        return size;
-    };
-    // the list's order and running weights
-    auto order_list = [&](int size) {
-        sort_list(sh.list, size);
-        for (int i = t; i < size; i += kThreads) sh.weight[i] = weight_of(value_of(sh.list[i]), s, sh.powers);
-        __syncthreads();
-        scan_weights(sh, size);
-    };
-    // The list holds, in order, all that is kept, `size` entries of it: the token (first block)
-    auto choose = [&](int size) {
-        const u64 total = sh.weight[size - 1];
-        // single weights again, and the entries by index
-        u64 w[kList / kThreads];
-#pragma unroll
-        for (int k = 0; k < kList / kThreads; ++k) {
-            const int i = t + k * kThreads;
-            w[k] = i < size ? sh.weight[i] - (i ? sh.weight[i - 1] : 0) : 0;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kList / kThreads; ++k) {
-            const int i = t + k * kThreads;
-            if (i < size) sh.list[i] = (sh.list[i] << 32) | (unsigned)i;
-        }
-        __syncthreads();
-        u64* const by_rank = reinterpret_cast<u64*>(sh.bins);        // the counts are done with
-        static_assert(sizeof(sh.bins) >= sizeof(sh.weight), "");
-#pragma unroll
-        for (int k = 0; k < kList / kThreads; ++k)
-            if (t + k * kThreads < size) by_rank[t + k * kThreads] = w[k];
-        sort_list(sh.list, size);
-        for (int i = t; i < size; i += kThreads) sh.weight[i] = by_rank[(int)(sh.list[i] & 0xFFFFFFFFu)];
-        __syncthreads();
-        scan_weights(sh, size);
-        if (t == 0) {
-            const int at = first_reaching(sh.weight, size, share_floor(u, total) + 1);
-            const int token = (int)~(unsigned)(sh.list[at] >> 32);
-            const u64 weight = sh.weight[at] - (at ? sh.weight[at - 1] : 0);
-            const T* z = row.row;
-            write_result(p, r, token, Num<T>::to_acc(z[token]), weight, total, s);
-        }
-    };
-    // how many of the list's first `size` entries min_p keeps
-    auto kept_of = [&](int size) {
-        int lo = 0, hi = size;                              // descending order
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (sh.list[mid] < min_cut) hi = mid;
-            else lo = mid + 1;
-        }
-        return lo;                                          // at least 1: the largest
-    };
-    // 2: in pairs of elements, the sum of the light weights; the heavy ones go into the list
-    const bool weigh = top_p < 1.f || top_k == 0;
-    if (in_pairs<T>(s)) {
-        const uint32_t least = splat_down<T>(__fadd_rd(m, s.least)), heavy = splat_down<T>(__fadd_rd(m, 1.001f * kHeavy / s.hi));
-        // one warp's packs [begin, end); entries are listed the first time alone
-        auto light_part = [&](int begin, int end, bool list) {
-            u64 sum = 0;
-            for (int v = begin + lane; v < end; v += 32) {
-                const uint4 k = row.words(v);
-                uint32_t w[4] = {k.x, k.y, k.z, k.w};
-                if (reaches<T>(max_word<T>(max_word<T>(w[0], w[1]), max_word<T>(w[2], w[3])), heavy)) {
-#pragma unroll
-                    for (int q = 0; q < V; ++q) {
-                        constexpr int PER = 4 / sizeof(T);
-                        const float z = of_word<T>(w[q / PER], q % PER);
-                        float hi, lo;
-                        exponent(z, s, hi, lo);
-                        if (!(hi >= kHeavy)) continue;
-                        if (list) {
-                            const int at = atomicAdd(&sh.listed, 1);
-                            if (at < kList) sh.list[at] = entry_of(z, row.first_index(v) + q);
-                        }
-                        if constexpr (sizeof(T) == 4) w[q] = least;
-                        else w[q / 2] = q % 2 ? (w[q / 2] & 0xFFFFu) | (least & 0xFFFF0000u) : (w[q / 2] & 0xFFFF0000u) | (least & 0xFFFFu);
-                    }
-                }
-                if (!weigh) continue;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = max_word<T>(w[i], least);
-#pragma unroll
-                for (int i = 0; i < V / 2; ++i) sum += light_weights(pair_of<T>(w, i), s);
-            }
-            return Team::warp_add(sum);
-        };
-        auto cut_of = [](int begin, int end, int k) { return begin + (int)((int64_t)(end - begin) * k / kWarps); };
-        u64 own = light_part(cut_of(row.v0, row.v1, warp), cut_of(row.v0, row.v1, warp + 1), true);
-        if (lane == 0) sh.light[warp] = own;
-        __syncthreads();
-        u64 light = 0, listed = sh.listed, x, y;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) light += sh.light[w];
-        light = t == 0 ? light : 0;
-        listed = t == 0 ? listed : 0;
-        team.sum(light, listed, x, y);
-        if (listed <= (u64)kList) {
-            // the list holds every heavy token: what is kept may end within it
-            enum { DONE, ALL, OTHER };
-            if (team.rank == 0) {
-                const int size = gather();
-                order_list(size);
-                if (t == 0) sh.listed = size;
-                const u64 weight = sh.weight[size - 1];
-                const bool k_here = top_k > 0 && top_k <= size, all = !k_here && top_k > 0;
-                int keep = k_here ? top_k : size + 1;               // size + 1: beyond the list
-                const u64 total = k_here ? sh.weight[keep - 1] : light + weight;
-                if (top_p < 1.f && !all) {
-                    const int at = first_reaching(sh.weight, size, share_ceil(top_p, total));
-                    if (at < size) keep = min(keep, at + 1);
-                }
-                const int least_p = kept_of(size);
-                if (least_p < size && !(all && top_p < 1.f)) keep = min(keep, least_p);
-                const int what = keep <= size ? DONE : (top_k == 0 && !(top_p < 1.f) && min_cut == 0 ? ALL : OTHER);
-                if (what == DONE) choose(keep);
-                __syncthreads();
-                if (t == 0) team.tell(Found{light + weight, 0, 0, what, 0});
-            }
-            const Found f = team.told();
-            if (f.i == DONE) {
-                team.barrier();                                     // nobody leaves while others read its memory
-                return;
-            }
-            if (f.i == ALL) {
-                // the token by sums over the row: the parts' light sums, and the listed tokens of each
-                auto add_listed = [&](int begin, int end) {         // sh.warp: by sixteenths of [begin, end)
-                    const int size = sh.listed;
-                    for (int i = t; i < size; i += kThreads) {
-                        const u64 entry = sh.list[i];
-                        const int v = (index_of(entry) + row.off) / V;
-                        if (v < begin || v >= end) continue;
-                        int k = (int)((int64_t)(v - begin) * kWarps / (end - begin));
-                        while (k > 0 && v < cut_of(begin, end, k)) --k;
-                        while (k < kWarps - 1 && v >= cut_of(begin, end, k + 1)) ++k;
-                        atomicAdd(&sh.warp[k], weight_of(value_of(entry), s, sh.powers));
-                    }
-                    __syncthreads();
-                };
-                u64 target = share_floor(u, f.a);
-                __syncthreads();
-                if (t < kWarps) sh.warp[t] = sh.light[t];
-                __syncthreads();
-                add_listed(row.v0, row.v1);
-                u64 mine = 0;
-                for (int w = 0; w < kWarps; ++w) mine += sh.warp[w];
-                u64 before = 0, none = 0, none_before;
-                u64 sum = t == 0 ? mine : 0;
-                const u64 parts = lane < kWarps ? sh.warp[lane] : 0;        // (the cluster's sums take sh.warp)
-                team.sum(sum, none, before, none_before);
-                if (target >= before && target < before + mine) {           // the whole block
-                    target -= before;
-                    int begin = row.v0, end = row.v1;
-                    u64 part = parts;
-                    for (int level = 0; level < 2; ++level) {
-                        int at = 0;
-                        while (at < kWarps - 1) {
-                            const u64 p = __shfl_sync(0xffffffffu, part, at);
-                            if (target < p) break;
-                            target -= p;
-                            ++at;
-                        }
-                        const int b = cut_of(begin, end, at), e = cut_of(begin, end, at + 1);
-                        begin = b;
-                        end = e;
-                        if (level == 1) break;
-                        own = light_part(cut_of(begin, end, warp), cut_of(begin, end, warp + 1), false);
-                        __syncthreads();
-                        if (lane == 0) sh.warp[warp] = own;
-                        __syncthreads();
-                        add_listed(begin, end);
-                        part = lane < kWarps ? sh.warp[lane] : 0;
-                    }
-                    if (warp == 0) find_in(row, team, begin, end, target, f.a, [&](float z, int) { return weight_of(z, s, sh.powers); });
-                }
-                const Found at = team.told();
-                if (team.rank == 0 && t == 0) write_result(p, r, at.i, __int_as_float(at.j), at.a, at.b, s);
-                team.barrier();
-                return;
-            }
-        }
-        // everything else: the list starts anew
-        if (t == 0) sh.listed = 0;
-        team.barrier();
+    const Settings o{u, top_p, top_k, max_key, (u64)sh.min_key << 32};
+    if (!in_pairs<T>(s) || top_k > kMostK) {
+        any_row(p, r, row, team, s, o);
+        return;
     }
-    if (counts) {
-        // 2: the histogram.  Each block takes a share of the bins afterwards, each thread
-        // `each` in a row; bin b lies where the threads' b-th bins are side by side.
-        const int log_each = 31 - __clz(kBins / kThreads / team.size), each = 1 << log_each;
-        const int stride = kBins >> log_each, mine = team.rank * kThreads + t;
+    const uint32_t least = splat_down<T>(__fadd_rd(m, s.least));
+    if (top_k > 0) {
+        // The list takes every token that may be among the k (or has no weight): all that
+        // follows is about it.
+        const float bound = team.maximum(fmaxf(bound_of(order_key(own_max), max_key, top_k), __fadd_rd(m, s.least)));
+        const uint32_t from = splat_down<T>(bound);
         for (int v = row.v0 + t; v < row.v1; v += kThreads) {
-            float z[V];
-            row.get(v, z);
+            const uint4 k = row.words(v);
+            const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+            if (!reaches<T>(max_word<T>(max_word<T>(w[0], w[1]), max_word<T>(w[2], w[3])), from)) continue;
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                const float f = step_of(z[q], s);
-                if (f < (float)kBins) {
-                    const int b = (int)f;
-                    atomicAdd(&sh.bins[(b & (each - 1)) * stride + (b >> log_each)], 1u);
-                }
+                const float z = of_word<T>(w[q * (int)sizeof(T) / 4], q % (4 / (int)sizeof(T)));
+                if (!(z >= bound)) continue;
+                const int at = atomicAdd(&sh.listed, 1);
+                if (at < kList) sh.list[at] = entry_of(z, row.first_index(v) + q);
             }
         }
-        team.barrier();
-        u64 count = 0, mass = 0;
-        auto bin_weight = [](int b) { return ((u64)__float2uint_rz(exp2f((b + 0.5f) * -((float)kOctaves / kBins)) * 0x1p31f) << 12) + 1; };
-        for (int i = 0; i < each; ++i) {
-            unsigned* const at = &sh.bins[i * stride + mine];
-            unsigned k = *at;
-            if (team.size > 1) {
-                for (int other = 1; other < team.size; ++other) k += read32(at, (team.rank + other) & (team.size - 1));
-                *at = k;                        // only this block reads its share of its bins
-            }
-            count += k;
-            mass += k * bin_weight(mine * each + i);
+        __syncthreads();
+        const u64 listed = team.sum(t == 0 ? sh.listed : 0);
+        if (listed > (u64)kList) {
+            any_row(p, r, row, team, s, o);
+            return;
         }
-        // running counts and weights over the cluster
-        u64 counted = count, weighed = mass, c0, m0;
-        team.sum(counted, weighed, c0, m0);
-        c0 += block_scan(count, sh.warp);
-        m0 += block_scan(mass, sh.warp2);
-        // calls f(bin, count before it, weight before it) for this thread's bins in order
-        auto bins_in_order = [&](auto&& f) {
-            u64 c = c0, w = m0;
-            for (int i = 0; i < each; ++i) {
-                const unsigned k = sh.bins[i * stride + mine];
-                const int b = mine * each + i;
-                f(b, c, w, k);
-                c += k;
-                w += k * bin_weight(b);
-            }
-        };
-        // Tokens of steps [from, to) that `cut` keeps go into the block's list; the
-        // weights of all that it keeps are added to `all`, those of lower steps to `above`.
-        auto collect = [&](float from, float to, bool weigh, u64& all, u64& above) {
-            for (int v = row.v0 + t; v < row.v1; v += kThreads) {
-                float z[V];
-                row.get(v, z);
+        if (team.rank == 0) {
+            const int size = gather(team, sh.list, &sh.listed, kList);
+            order_list(sh.list, sh.weight, size, s, sh);
+            int keep = min(top_k, size);
+            if (top_p < 1.f) keep = min(keep, first_reaching(sh.weight, keep, share_ceil(top_p, sh.weight[keep - 1])) + 1);
+            choose(p, r, row, u, min(keep, kept_of(sh.list, size, o.min_cut)), s, sh);
+        }
+        team.barrier();                                      // nobody leaves while others read its memory
+        return;
+    }
+    // The light weights' sum, and a list of the heavy tokens.
+    Pass pass{true, false, false, 0.f, 0.f, least, splat_down<T>(__fadd_rd(m, 1.001f * kHeavy / s.hi))};
+    auto part_of = [](int begin, int end, int k) { return begin + (int)((int64_t)(end - begin) * k / kWarps); };
+    auto light_sum = [&](int begin, int end) {              // of the block's warps' parts, into sh.light
+        const int b = part_of(begin, end, warp), e = part_of(begin, end, warp + 1);
+        const u64 sum = sizeof(T) == 4 || s.exact ? light_part<T, true>(row, sh, b, e, pass) : light_part<T, sizeof(T) == 4>(row, sh, b, e, pass);
+        __syncthreads();
+        if (lane == 0) sh.light[warp] = sum;
+        __syncthreads();
+        u64 all = 0;
 #pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    const float f = step_of(z[q], s);
-                    const u64 entry = entry_of(z[q], row.first_index(v) + q);
-                    if (!(f < (float)kBins) || entry < cut) continue;
-                    if (f >= from && f < to) {
-                        const int at = atomicAdd(&sh.listed, 1);
-                        if (at < kList) sh.list[at] = entry;
-                    }
-                    if (!weigh) continue;
-                    const u64 w = weight_of(z[q], s, sh.powers);
-                    all += w;
-                    if (f < from) above += w;
-                }
-            }
-        };
-        // The cut at which the sum of value(z) over kept entries reaches `least`, by
-        // bisection over keys, then among equal ones by index.
-        auto bisect = [&](auto&& value, u64 least) {
-            unsigned lo = 0, hi = max_key;                      // sum(key >= lo) >= least
-            while (lo < hi) {
-                const unsigned mid = hi - (hi - lo) / 2;
-                const u64 sum = row_sum(row, team, [&](float z, int i) -> u64 {
-                    return order_key(z) >= mid && entry_of(z, i) >= cut ? value(z) : 0;
-                });
-                if (sum >= least) lo = mid;
-                else hi = mid - 1;
-            }
-            const u64 above = row_sum(row, team, [&](float z, int i) -> u64 {
-                return order_key(z) > lo && entry_of(z, i) >= cut ? value(z) : 0;
-            });
-            const Found f = locate(
-                row, team,
-                [&](float z, int i) -> u64 { return order_key(z) == lo && entry_of(z, i) >= cut ? value(z) : 0; },
-                [&](u64) -> u64 { return least - above - 1; });
-            cut = ((u64)lo << 32) | (unsigned)~f.i;
-        };
-        // the first block is done with the list; `entry` is the new cut
-        auto cut_at = [&](u64 entry, bool good) {
-            __syncthreads();                                    // the block has read what it needs
-            if (t == 0) team.tell(Found{entry, 0, 0, good, 0});
-        };
-        // ... and every block hears of it, and empties its list for the next collection
-        auto cut_told = [&] {
-            const Found f = team.told();
-            if (t == 0) sh.listed = 0;
-            return f;
-        };
-
-        u64 unused = 0;
-        u64 known = weighed;                                    // estimate of the k tokens' weight
-        if (top_k && counted > (u64)top_k) {
-            bins_in_order([&](int b, u64 c, u64 w, unsigned k) {
-                if (c < (u64)top_k && c + k >= (u64)top_k)
-                    team.tell(Found{c, c + k, w + ((u64)top_k - c) * bin_weight(b), b, 0});
-            });
-            const Found f = team.told();
-            known = f.c;
-            const bool whole = f.b <= (u64)kList;               // the list holds all of them
-            if (whole || f.b - f.a <= (u64)kList) {
-                collect(whole ? 0.f : (float)f.i, (float)(f.i + 1), false, unused, unused);
-                team.barrier();
-                if (team.rank == 0) {
-                    const int size = gather();
-                    order_list(size);
-                    if (whole) {
-                        int keep = min(top_k, size);
-                        if (top_p < 1.f)
-                            keep = min(keep, first_reaching(sh.weight, keep, share_ceil(top_p, sh.weight[keep - 1])) + 1);
-                        choose(min(keep, kept_of(keep)));
-                    } else {
-                        cut_at(sh.list[top_k - 1 - (int)f.a], true);
-                    }
-                }
-                if (whole) {
-                    team.barrier();                             // nobody leaves before the list is written
-                    return;
-                }
-                cut = cut_told().a;
-            } else {
-                bisect([](float) -> u64 { return 1; }, (u64)top_k);
+        for (int w = 0; w < kWarps; ++w) all += sh.light[w];
+        return t == 0 ? all : 0;
+    };
+    u64 light = light_sum(row.v0, row.v1), listed = t == 0 ? sh.listed : 0, b1, b2;
+    team.sum(light, listed, b1, b2);
+    if (listed > (u64)kList) {
+        any_row(p, r, row, team, s, o);
+        return;
+    }
+    // what is kept may end within the list
+    enum { DONE, ALL, TOP_P, OTHER };
+    if (team.rank == 0) {
+        const int size = gather(team, sh.list, &sh.listed, kList);
+        order_list(sh.list, sh.weight, size, s, sh);
+        if (t == 0) sh.listed = size;
+        const u64 heavy = sh.weight[size - 1], target = top_p < 1.f ? share_ceil(top_p, light + heavy) : ~0ull;
+        const int least_p = kept_of(sh.list, size, o.min_cut);
+        const int keep = min(first_reaching(sh.weight, size, target) + 1, least_p < size ? least_p : size + 1);
+        const int what = keep <= size ? DONE : (o.min_cut > 0 ? OTHER : (top_p < 1.f ? TOP_P : ALL));
+        if (what == DONE) choose(p, r, row, u, keep, s, sh);
+        __syncthreads();
+        if (t == 0) team.tell(Found{heavy, target, 0, what, 0});
+    }
+    const Found f = team.told();
+    if (f.i == DONE) {
+        team.barrier();                                      // nobody leaves while others read its memory
+        return;
+    }
+    if (f.i == OTHER) {
+        any_row(p, r, row, team, s, o);
+        return;
+    }
+    u64 total = light + f.a, cut = 0;
+    pass.heavy_to_list = false;
+    if (f.i == TOP_P) {
+        // The cut lies among the light tokens: a histogram of their steps shows where, to a
+        // fraction of a percent of their weight; the tokens of those steps go into a
+        // second list.
+        const u64 target = f.b - f.a;                        // of the light weights
+        Bins bins(team);
+        bins.clear();
+        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+            const uint4 k = row.words(v);
+            const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float z = of_word<T>(w[q * (int)sizeof(T) / 4], q % (4 / (int)sizeof(T)));
+                const float step = step_of(z, s);
+                if (step < (float)kBins && !((z - s.m) * s.hi >= kHeavy)) bins.add(step);
             }
         }
-        if (top_p < 1.f) {
-            // the steps around the estimate; wider ones where it was not good enough
-            for (float off = 0x1p-10f;; off *= 8.f) {
-                const float near = (float)known * top_p;
-                const u64 last = weighed - 1;
-                const u64 least = min((u64)(near * fmaxf(1.f - off, 0.f)), last), most = min((u64)(near * (1.f + off)), last);
-                bins_in_order([&](int b, u64 c, u64 w, unsigned k) {
-                    if (w <= least && least < w + k * bin_weight(b)) team.tell(Found{c, 0, 0, b, 0});
-                });
-                Found low = team.told();
-                bins_in_order([&](int b, u64 c, u64 w, unsigned k) {
-                    if (w <= most && most < w + k * bin_weight(b)) team.tell(Found{c + k, 0, 0, b, 0});
-                });
-                const Found high = team.told();
-                if (high.a <= (u64)kList) low = Found{0, 0, 0, 0, 0};        // all of the prefix
-                if (high.a - low.a > (u64)kList || off > 8.f) {
-                    const u64 all = row_sum(row, team, [&](float z, int i) -> u64 {
-                        return entry_of(z, i) >= cut ? weight_of(z, s, sh.powers) : 0;
-                    });
-                    bisect([&](float z) { return weight_of(z, s, sh.powers); }, share_ceil(top_p, all));
-                    break;
+        bins.sum();
+        const float near = (float)target / (float)light * (float)bins.mass;
+        for (float off = 0x1p-10f;; off *= 8.f) {
+            const u64 last = bins.mass - 1;
+            const Found low = bins.reaching(min((u64)(near * fmaxf(1.f - off, 0.f)), last));
+            const Found high = bins.reaching(min((u64)(near * (1.f + off)), last));
+            if (high.b - low.a > (u64)kBracket || off > 8.f) {
+                any_row(p, r, row, team, s, o);
+                return;
+            }
+            pass.masked = pass.steps_to_list2 = true;
+            pass.low = (float)low.i;
+            pass.high = (float)(high.i + 1);
+            u64 above = light_sum(row.v0, row.v1);
+            above = team.sum(above);
+            if (team.rank == 0) {
+                const int size = gather(team, sh.list2, &sh.listed2, kBracket);
+                order_list(sh.list2, sh.weight2, size, s, sh);
+                const bool good = size > 0 && above < target && target - above <= sh.weight2[size - 1];
+                const int at = good ? first_reaching(sh.weight2, size, target - above) : 0;
+                __syncthreads();
+                if (t == 0) {
+                    sh.listed2 = size;
+                    team.tell(Found{good ? sh.list2[at] : 0, good ? f.a + above + sh.weight2[at] : 0, 0, good, 0});
                 }
-                u64 all = 0, above = 0, b1, b2;
-                collect((float)low.i, (float)(high.i + 1), true, all, above);
-                team.sum(all, above, b1, b2);
-                if (team.rank == 0) {
-                    const int size = gather();
-                    const u64 target = share_ceil(top_p, all);
-                    order_list(size);
-                    const bool good = size > 0 && above < target && target - above <= sh.weight[size - 1];
-                    const int at = good ? first_reaching(sh.weight, size, target - above) : 0;
-                    if (good && low.i == 0) choose(min(at + 1, kept_of(at + 1)));
-                    cut_at(good ? sh.list[at] : 0, good);
-                }
-                const Found f = cut_told();
-                if (!f.i) continue;
-                if (low.i == 0) {                               // chosen
-                    team.barrier();                             // nobody leaves while others read its memory
-                    return;
-                }
-                cut = f.a;
+            }
+            const Found g = team.told();
+            if (g.i) {
+                cut = g.a;
+                total = g.b;
                 break;
             }
+            if (t == 0) sh.listed2 = 0;
         }
+        pass.steps_to_list2 = false;
     }
-    // 4: the token by sums over all that is kept
-    cut = max(cut, min_cut);
-    const Found f = locate(
-        row, team,
-        [&](float z, int i) -> u64 { return entry_of(z, i) >= cut ? weight_of(z, s, sh.powers) : 0; },
-        [&](u64 sum) -> u64 { return share_floor(u, sum); });
-    if (team.rank == 0 && t == 0) write_result(p, r, f.i, __int_as_float(f.j), f.a, f.b, s);
+    // The token by sums over the row: the light sums of its parts, and the listed tokens of each.
+    auto add_listed = [&](int begin, int end) {              // sh.warp: by sixteenths of [begin, end)
+        auto add = [&](const u64* list, int size, u64 least_entry) {
+            for (int i = t; i < size; i += kThreads) {
+                const u64 entry = list[i];
+                const int v = (index_of(entry) + row.off) / V;
+                if (entry < least_entry || v < begin || v >= end) continue;
+                int k = (int)((int64_t)(v - begin) * kWarps / (end - begin));
+                while (k > 0 && v < part_of(begin, end, k)) --k;
+                while (k < kWarps - 1 && v >= part_of(begin, end, k + 1)) ++k;
+                atomicAdd(&sh.warp[k], weight_of(value_of(entry), s, sh.powers));
+            }
+        };
+        __syncthreads();
+        if (t < kWarps) sh.warp[t] = sh.light[t];
+        __syncthreads();
+        add(sh.list, sh.listed, 0);
+        add(sh.list2, sh.listed2, cut);
+        __syncthreads();
+        const u64 part = lane < kWarps ? sh.warp[lane] : 0;
+        __syncthreads();
+        return part;
+    };
+    u64 target = share_floor(u, total), part = add_listed(row.v0, row.v1);
+    const u64 mine = Team::warp_add(part);
+    u64 sum = t == 0 ? mine : 0, none = 0, before, none_before;
+    team.sum(sum, none, before, none_before);
+    if (target >= before && target < before + mine) {         // the whole block
+        target -= before;
+        int begin = row.v0, end = row.v1;
+        for (int level = 0;; ++level) {
+            int at = 0;
+            for (; at < kWarps - 1; ++at) {
+                const u64 w = __shfl_sync(0xffffffffu, part, at);
+                if (target < w) break;
+                target -= w;
+            }
+            const int b = part_of(begin, end, at), e = part_of(begin, end, at + 1);
+            begin = b;
+            end = e;
+            if (level == 1) break;
+            light_sum(begin, end);
+            part = add_listed(begin, end);
+        }
+        if (warp == 0)
+            find_in(row, team, begin, end, target, total,
+                    [&](float z, int i) -> u64 { return entry_of(z, i) >= cut ? weight_of(z, s, sh.powers) : 0; });
+    }
+    const Found at = team.told();
+    if (team.rank == 0 && t == 0) write_result(p, r, at.i, __int_as_float(at.j), at.a, at.b, s);
     team.barrier();
 }
 
