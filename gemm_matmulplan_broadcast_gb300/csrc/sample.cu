@@ -9,21 +9,32 @@
 //
 // Choices hang on sums next to borders, so the weights are 64-bit integers
 // (2^43 for the largest): their sums are the same in any order, across warps, blocks
-// and passes.  Weights above 2^-12 are good to 2^-38 of themselves (x = (z - m) log2(e) / T
-// in two float32s, a table of 2^(i/64), and the rest of the exponential in two parts);
-// smaller ones to float32's rounding, 2^-36 of the largest weight.
+// and passes.  Tokens within 12 octaves of the largest are heavy: weights good to 2^-38 of
+// themselves (x = (z - m) log2(e) / T in two float32s, a table of 2^(i/64), the rest of the
+// exponential in two parts).  The light ones have float32's rounding, 2^-35 of the largest
+// weight.  A row with more than 1024 heavy tokens counts fewer of them as heavy.
 //
-// A row is a cluster of blocks, each with a slice of it.  Passes over the row:
-//   1 the maximum;
-//   2 (top-k or top-p) a histogram of counts over 8192 equal steps of x, 45 octaves.
-//     It gives the k-th token's step exactly, and the top-p step by the weight at the
-//     steps' middles, to a fraction of a percent;
-//   3 the tokens of the steps in question go into a list (up to 2048, sorted in the
-//     first block), and the weights of those above them are summed: the cut is found exactly
-//     there.  A list that holds all that is kept gives the token as well;
-//   4 otherwise sums over the kept tokens by slices, warps and packs lead to the token.
-// Steps that hold more than the list (many equal logits) are cut by bisection over
-// values with a sum over the row each, then by a search for the last of the equal ones.
+// A row is a cluster of blocks, each with a slice of it, read again by each pass, from L2:
+//   the maximum; then
+//   top-k: a bound that the k largest reach (the k-th largest of the threads' own maxima),
+//     the list of the tokens that reach it, and everything else on that list;
+//   or the list of the heavy tokens with the light weights' sum, for top-p to 2^-15 of it
+//     alone by the exponential unit.  If what is kept ends among the heavy tokens wherever
+//     the sum lies within that, the list gives the token.  Otherwise the sum again, as
+//     accurate as the weights, with a histogram of counts over 4096 equal steps of x, 45
+//     octaves: it shows to a fraction of a percent in which steps the light
+//     weights reach top-p, a second list takes those steps' tokens, the weights above
+//     them are summed, and the cut is found exactly;
+//   without a list that holds all that is kept, sums by slices, warps and packs,
+//     the listed tokens added to each, lead to the token.
+// Rows that none of this fits (far from zero in units of the temperature, many equal logits,
+// large k) go element by element: a histogram, or bisection over values.
+//
+// Bound by instructions and, with few rows, by the passes' latency: about 25 issue slots an
+// element for the accurate sum, 12 for the rough one.  Measured: BF16 [1024, 50257] with
+// top-p 181 us (the logits' bytes: 15.5; one row in eight has its cut among the light
+// tokens and takes 100 us of its SM's quarter), FLOAT [64, 131072] unfiltered 54 us, BF16
+// [256, 50257] of mixed settings 85 us, one row of 50257 15 us.
 #include <cmath>
 #include <new>
 #include <type_traits>
@@ -36,16 +47,18 @@ namespace sample {
 
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBlocksPerSm = 4;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 8192;
+constexpr int kBins = 4096;
 constexpr int kOctaves = 45;            // below 2^-45 of the largest a weight is 0
-constexpr int kList = 2048;
-constexpr int kSmall = 192;             // entries up to which a list is ordered by counting
-constexpr int kBracket = 1024;          // tokens of the steps in which top-p's cut lies
+constexpr int kList = 1024;
+constexpr int kSmall = 128;             // entries up to which a list is ordered by counting
+constexpr int kBracket = 512;           // tokens of the steps in which top-p's cut lies
+constexpr int kTurns = 6;               // tries to find the steps of a cut
 constexpr int kMostK = kThreads * 7 / 8;    // the largest top_k that the threads' maxima bound
 constexpr int kOne = 43;                // the largest weight is 2^43; vocab <= 2^20
-constexpr float kHeavy = -12.f;         // x from which on weights are formed in two parts
+constexpr float kHeavy = -12.f;         // x from which on weights are formed in two parts (or nearer to 0: Scale)
 
 struct Power {                          // 2^(i/64)
     u64 fixed;                          // scaled by 2^43
@@ -72,6 +85,8 @@ struct Scale {
     float m, hi, lo;
     float least;            // z - m is not taken below this one (x = -64, where weights are 0)
     int exact;              // the light weights' differences z - m in two parts
+    float heavy;            // x from which on tokens are heavy: kHeavy, nearer to 0 in rows with too many of those
+    int shift;              // light weights are scaled by 2^(43 - shift): below 2^31
 };
 
 // what one block tells the others of its cluster
@@ -128,6 +143,8 @@ __device__ __forceinline__ Scale scale_of(float temperature, float min_p, double
     s.lo = (float)(c - (double)s.hi);
     s.least = -64.f / s.hi;
     s.exact = 1;
+    s.heavy = kHeavy;
+    s.shift = 0;
     min_distance = min_p > 0.f ? heat * log((double)min_p) : 0.0;
     return s;
 }
@@ -136,19 +153,11 @@ __device__ __forceinline__ Scale scale_of(float temperature, float min_p, double
 constexpr float kStepsPerOctave = (float)kBins / kOctaves;
 __device__ __forceinline__ float step_of(float z, const Scale& s) { return (z - s.m) * -s.hi * kStepsPerOctave; }
 
-// x in two parts
-__device__ __forceinline__ void exponent(float z, const Scale& s, float& hi, float& lo) {
-    float d = z - s.m;
-    const float b = z - d;                      // Knuth's two-sum: what the difference lost
-    float e = (z - (d + b)) + (b - s.m);
-    if (!(d >= s.least)) {
-        d = s.least;
-        e = 0.f;
-    }
-    hi = d * s.hi;
-    if (hi < kHeavy && !s.exact) e = 0.f;
-    lo = fmaf(d, s.lo, fmaf(d, s.hi, -hi));
-    lo = fmaf(e, s.hi, lo);
+// the exponential unit, good to 2^-22 of the result
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 constexpr float kMagic = 12582912.f;            // 1.5 2^23: adding it rounds to an integer in the low bits
@@ -183,23 +192,33 @@ __device__ __forceinline__ constexpr float poly(int i) {
                             0x1.3b2dbcp-7f, 0x1.5f456ap-10f, 0x1.41d334p-13f};
     return c[i] * 0x1p43f;
 }
-__device__ __forceinline__ unsigned light_weight(float hi, float lo) {
-    const float rounded = hi + kMagic;
-    const float f = (hi - (rounded - kMagic)) + lo;
+// (d = z - m, e what it lost; x - n is one fused operation's rounding of 2^-26)
+template <bool EXACT>
+__device__ __forceinline__ unsigned light_weight(float d, float e, const Scale& s) {
+    const float magic = kMagic - (float)s.shift, rounded = fmaf(d, s.hi, magic);
+    float f = fmaf(d, s.lo, fmaf(d, s.hi, magic - rounded));
+    if constexpr (EXACT) f = fmaf(e, s.hi, f);
     float p = poly(6);
 #pragma unroll
     for (int i = 5; i >= 0; --i) p = fmaf(p, f, poly(i));
     return __float2uint_rn(__int_as_float(__float_as_int(p) + (__float_as_int(rounded) << 23)));
 }
-
-__device__ __forceinline__ u64 weight_of(float z, const Scale& s, const Power* powers) {
-    float hi, lo;
-    exponent(z, s, hi, lo);
-    return hi >= kHeavy ? heavy_weight(hi, lo, powers) : light_weight(hi, lo);
+// z - m, and what that lost (Knuth's two-sum)
+__device__ __forceinline__ float difference(float z, float m, float& lost) {
+    const float d = z - m, b = z - d;
+    lost = (z - (d + b)) + (b - m);
+    return d;
 }
 
-// ---- two elements at a time -------------------------------------------------------
-// The same arithmetic as weight_of's, operation by operation, on the words of a pack.
+__device__ __forceinline__ u64 weight_of(float z, const Scale& s, const Power* powers) {
+    float e;
+    const float d = difference(z, s.m, e), hi = d * s.hi;
+    if (hi >= s.heavy) return heavy_weight(hi, fmaf(e, s.hi, fmaf(d, s.lo, fmaf(d, s.hi, -hi))), powers);
+    if (!(d >= s.least)) return 0;
+    return (u64)(s.exact ? light_weight<true>(d, e, s) : light_weight<false>(d, 0.f, s)) << s.shift;
+}
+
+// ---- words of a pack ----------------------------------------------------------------
 
 template <typename T>
 __device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
@@ -248,56 +267,66 @@ __device__ __forceinline__ bool reaches(uint32_t w, uint32_t least) {
     else
         return __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&least)) != 0;
 }
-// pair i of a pack's elements
+// all bits of the elements of w that reach least's
 template <typename T>
-__device__ __forceinline__ F2 pair_of(const uint32_t (&w)[4], int i) {
-    if constexpr (sizeof(T) == 4) return pack_f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-    if constexpr (std::is_same_v<T, __half>) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        return pack_f2(f.x, f.y);
-    } else {
-        return pack_f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-    }
+__device__ __forceinline__ uint32_t reach_mask(uint32_t w, uint32_t least) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w) >= __uint_as_float(least) ? 0xFFFFFFFFu : 0u;
+    else if constexpr (std::is_same_v<T, __half>)
+        return __hge2_mask(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&least));
+    else
+        return __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w), *reinterpret_cast<const __nv_bfloat162*>(&least));
 }
-
-__device__ __forceinline__ F2 two(float v) { return pack_f2(v, v); }
-
-// The light weights of two elements (z above m - 128 / c); masked: those of steps below
-// `low`.  FP32 operations bound it: 14 an element, 19 with EXACT differences.
-template <bool EXACT>
-__device__ __forceinline__ u64 light_weights(F2 z, const Scale& s, bool masked, float low) {
-    const F2 minus = two(-1.f), m = two(-s.m), c = two(s.hi);
-    const F2 d = add2(z, m);
-    const F2 down = mul2(d, two(-s.hi));                        // -hi
-    F2 lo = fma2(d, two(s.lo), fma2(d, c, down));
+// The least value of the type that is heavy, as a word (by one warp): by a search
+// over the order of the type's values, in which what is heavy grows.
+template <typename T>
+__device__ __forceinline__ uint32_t heavy_word(const Scale& s) {
+    constexpr uint32_t SIGN = sizeof(T) == 4 ? 0x80000000u : 0x8000u, ALL = SIGN | (SIGN - 1);
+    auto place = [](uint32_t b) { return b & SIGN ? ~b & ALL : b | SIGN; };
+    auto bits = [](uint32_t k) { return k & SIGN ? k & ~SIGN : ~k & ALL; };
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t lo = place(splat_down<T>(__fadd_rd(s.m, 1.01f * s.heavy / s.hi)) & ALL), hi = place(splat_down<T>(s.m) & ALL);
+    while (lo < hi) {                                   // hi is heavy, lo may be
+        const uint32_t each = (hi - lo) / 32 + 1, mine = min(lo + lane * each, hi);
+        const unsigned heavy = __ballot_sync(0xffffffffu, (of_word<T>(bits(mine), 0) - s.m) * s.hi >= s.heavy);
+        const int first = heavy ? __ffs(heavy) - 1 : 32;
+        const uint32_t from = lo;
+        if (first < 32) hi = min(hi, from + first * each);
+        if (first > 0) lo = min(hi, from + (first - 1) * each + 1);
+    }
+    return sizeof(T) == 4 ? bits(lo) : bits(lo) * 0x10001u;
+}
+// light_weight of two elements, the same operations in the same order; MASKED: those of
+// steps below `low`.  11 paired FP32 operations, 17 with EXACT differences.
+template <bool EXACT, bool MASKED>
+__device__ __forceinline__ u64 light_weights(F2 z, const Scale& s, float low) {
+    const F2 minus = both(-1.f), minus_m = both(-s.m), c = both(s.hi), magic = both(kMagic - (float)s.shift);
+    const F2 d = add2(z, minus_m), rounded = fma2(d, c, magic);
+    F2 f = fma2(d, both(s.lo), fma2(d, c, fma2(rounded, minus, magic)));
     if constexpr (EXACT) {
         const F2 b = fma2(d, minus, z);
-        lo = fma2(add2(fma2(add2(d, b), minus, z), add2(b, m)), c, lo);
+        f = fma2(add2(fma2(add2(d, b), minus, z), add2(b, minus_m)), c, f);
     }
-    const F2 rounded = fma2(down, minus, two(kMagic));
-    const F2 f = fma2(add2(add2(rounded, two(-kMagic)), down), minus, lo);
-    F2 p = two(poly(6));
+    F2 p = both(poly(6));
 #pragma unroll
-    for (int i = 5; i >= 0; --i) p = fma2(p, f, two(poly(i)));
+    for (int i = 5; i >= 0; --i) p = fma2(p, f, both(poly(i)));
     float p0, p1, r0, r1;
     unpack_f2(p, p0, p1);
     unpack_f2(rounded, r0, r1);
     unsigned w0 = __float2uint_rn(__int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23)));
     unsigned w1 = __float2uint_rn(__int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23)));
-    if (masked) {
+    if constexpr (MASKED) {
         float d0, d1;
-        unpack_f2(mul2(down, two(kStepsPerOctave)), d0, d1);
-        if (!(d0 < low)) w0 = 0;
-        if (!(d1 < low)) w1 = 0;
+        unpack_f2(d, d0, d1);
+        if (!(d0 * -s.hi * kStepsPerOctave < low)) w0 = 0;
+        if (!(d1 * -s.hi * kStepsPerOctave < low)) w1 = 0;
     }
     return (u64)(w0 + w1);                      // each below 2^31
 }
 
-// What the words of a row are compared with (see Shared): rows whose maximum is so
-// far from zero, in units of the temperature, that the type's steps there span
-// several octaves are not worked on in pairs.
+// Rows whose maximum is so far from zero, in units of the temperature, that the type's steps
+// there span several octaves are not worked on by words.
 template <typename T>
-__device__ __forceinline__ bool in_pairs(const Scale& s) {
+__device__ __forceinline__ bool by_words(const Scale& s) {
     if (std::is_same_v<T, __half> && s.m + s.least < -60000.f) return false;       // no value for a weight of 0
     return fabsf(s.m) * s.hi < (sizeof(T) == 4 ? 0x1p24f : 0x1p9f);
 }
@@ -413,15 +442,17 @@ struct Team {
             sh.exchange[parity][1] = b;
         }
         barrier();
-        a = b = 0;
-        for (int r = 0; r < size; ++r) {
-            if (r == rank) {
-                a_before = a;
-                b_before = b;
-            }
-            a += read64(&sh.exchange[parity][0], r);
-            b += read64(&sh.exchange[parity][1], r);
+        // a block a lane: one trip to the others' memory
+        const int r = threadIdx.x & 31;
+        u64 x = 0, y = 0;
+        if (r < size) {
+            x = read64(&sh.exchange[parity][0], r);
+            y = read64(&sh.exchange[parity][1], r);
         }
+        a = warp_add(x);
+        b = warp_add(y);
+        a_before = warp_add(r < rank ? x : 0);
+        b_before = warp_add(r < rank ? y : 0);
     }
     __device__ __forceinline__ u64 sum(u64 a) {
         u64 b = 0, x, y;
@@ -439,7 +470,10 @@ struct Team {
         parity ^= 1;
         if (threadIdx.x == 0) sh.exchange[parity][0] = __float_as_uint(v);
         barrier();
-        for (int r = 0; r < size; ++r) v = max_nan(v, __uint_as_float((unsigned)read64(&sh.exchange[parity][0], r)));
+        const int r = threadIdx.x & 31;
+        if (r < size) v = __uint_as_float((unsigned)read64(&sh.exchange[parity][0], r));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, d));
         return v;
     }
     // One thread of the cluster has told what it found (below); all get it.
@@ -589,25 +623,64 @@ __device__ __forceinline__ Found locate(const Row<T>& row, Team& team, F&& value
 
 // ---- the list ----------------------------------------------------------------------
 
-// descending order of n entries, by the block (n <= kList)
-__device__ __forceinline__ int sort_list(u64* list, int n) {
-    int size = 32;
-    while (size < n) size *= 2;
-    for (int i = n + (int)threadIdx.x; i < size; i += kThreads) list[i] = 0;
+// Descending order of n entries (n <= E kThreads), by the block: a bitonic sort of E
+// entries a thread, i = t + e kThreads.  Partners are in the thread, in the warp, or meet in
+// `list` and `other` by turns.
+template <int E>
+__device__ __forceinline__ void sort_entries(u64* list, u64* other, int n) {
+    const int t = threadIdx.x;
+    u64 x[E];
     __syncthreads();
-    for (int k = 2; k <= size; k *= 2)
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = t + e * kThreads < n ? list[t + e * kThreads] : 0;
+    __syncthreads();
+    u64* buffer = other;
+    for (int k = 2; k <= E * kThreads; k *= 2)
         for (int j = k / 2; j > 0; j /= 2) {
-            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-                const int i = 2 * t - (t & (j - 1));
-                const u64 x = list[i], y = list[i + j];
-                if ((x < y) == ((i & k) == 0)) {
-                    list[i] = y;
-                    list[i + j] = x;
+            if (j >= kThreads) {
+                if constexpr (E > 1) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+#pragma unroll
+                        for (int o = e + 1; o < E; ++o)
+                            if ((e ^ o) * kThreads == j) {
+                                const u64 a = max(x[e], x[o]), b = min(x[e], x[o]);
+                                const bool down = ((t + e * kThreads) & k) == 0;
+                                x[e] = down ? a : b;
+                                x[o] = down ? b : a;
+                            }
                 }
+                continue;
             }
-            __syncthreads();
+            u64 y[E];
+            if (j < 32) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = __shfl_xor_sync(0xffffffffu, x[e], j);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) buffer[t + e * kThreads] = x[e];
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = buffer[(t ^ j) + e * kThreads];
+                buffer = buffer == list ? other : list;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const bool down = ((t + e * kThreads) & k) == 0, low = (t & j) == 0;
+                x[e] = down == low ? max(x[e], y[e]) : min(x[e], y[e]);
+            }
         }
-    return size;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) list[t + e * kThreads] = x[e];
+    __syncthreads();
+}
+// (lists and the buffers beside them are whole numbers of kThreads long)
+__device__ __noinline__ void sort_list(u64* list, u64* other, int n) {
+    static_assert(kList == 4 * kThreads && kBracket == 2 * kThreads, "");
+    if (n <= kThreads) sort_entries<1>(list, other, n);
+    else if (n <= 2 * kThreads) sort_entries<2>(list, other, n);
+    else sort_entries<4>(list, other, n);
 }
 
 // running sums of the first n
@@ -675,8 +748,9 @@ __device__ __forceinline__ void write_result(const Params& p, int64_t row, int t
     if (other < 0.5f) {
         lp = log1pf(-other);
     } else {
-        float hi, lo;
-        exponent(z, s, hi, lo);
+        // x - log2(total), each in two parts
+        float lost;
+        const float d = difference(z, s.m, lost), hi = d * s.hi, lo = fmaf(lost, s.hi, fmaf(d, s.lo, fmaf(d, s.hi, -hi)));
         const int e = 63 - __clzll((long long)total);
         const float mantissa = (float)total * __int_as_float((127 - e) << 23);
         lp = ((hi - (float)(e - kOne)) + (lo - log2f(mantissa))) * kLn2;
@@ -688,11 +762,30 @@ __device__ __forceinline__ void write_result(const Params& p, int64_t row, int t
 
 // takes in the other blocks' entries, which are `most` together at most; their number
 __device__ __forceinline__ int gather(Team& team, u64* list, const int* listed, int most) {
-    int size = min(*listed, most);
-    for (int k = 1; k < team.size; ++k) {
-        const int more = min((int)read32(listed, k), most - size);
-        for (int i = threadIdx.x; i < more; i += kThreads) list[size + i] = read64(&list[i], k);
-        size += more;
+    if (team.size == 1) return min(*listed, most);
+    // every block's number, a block a lane, and where its entries go
+    const int lane = threadIdx.x & 31;
+    const int own = lane < team.size ? min((int)read32(listed, lane), most) : 0;
+    int after = own;
+#pragma unroll
+    for (int d = 1; d < kMaxCluster; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, after, d);
+        if (lane >= d) after += o;
+    }
+    const int size = min(__shfl_sync(0xffffffffu, after, kMaxCluster - 1), most);
+    const int first = __shfl_sync(0xffffffffu, own, 0);     // this block's own stay where they are
+    for (int base = first; base < size; base += kThreads) {
+        const int i = base + (int)threadIdx.x;
+        int block = 0, start = 0;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+            const int end = __shfl_sync(0xffffffffu, after, k);
+            if (i >= end) {
+                block = k + 1;
+                start = end;
+            }
+        }
+        if (i < size) list[i] = read64(&list[i - start], block);
     }
     return size;
 }
@@ -735,7 +828,7 @@ __device__ __forceinline__ void order_list(u64* list, u64* weight, int size, con
         __syncthreads();
         return;
     }
-    sort_list(list, size);
+    sort_list(list, weight, size);
     for (int i = t; i < size; i += kThreads) weight[i] = weight_of(value_of(list[i]), s, sh.powers);
     __syncthreads();
     scan_weights(weight, size, sh.warp);
@@ -783,7 +876,7 @@ __device__ __forceinline__ void choose(const Params& p, int64_t r, const Row<T>&
 #pragma unroll
     for (int k = 0; k < kList / kThreads; ++k)
         if (t + k * kThreads < size) by_rank[t + k * kThreads] = w[k];
-    sort_list(sh.list, size);
+    sort_list(sh.list, sh.weight, size);
     for (int i = t; i < size; i += kThreads) sh.weight[i] = by_rank[(int)(sh.list[i] & 0xFFFFFFFFu)];
     __syncthreads();
     scan_weights(sh.weight, size, sh.warp);
@@ -826,9 +919,9 @@ struct Bins {
         for (int i = threadIdx.x; i < kBins; i += kThreads) team.sh.bins[i] = 0;
         __syncthreads();
     }
-    __device__ __forceinline__ void add(float step) {
+    static __device__ __forceinline__ void add(Shared& sh, float step, int log_each) {
         const int b = (int)step;
-        atomicAdd(&team.sh.bins[(b & (each - 1)) * stride + (b >> log_each)], 1u);
+        atomicAdd(&sh.bins[(b & ((1 << log_each) - 1)) * (kBins >> log_each) + (b >> log_each)], 1u);
     }
     // the weight in a step's middle, at least 1
     static __device__ __forceinline__ u64 weight(int b) {
@@ -865,13 +958,29 @@ struct Bins {
             w += k * weight(b);
         }
     }
-    // the bin in which the estimated weight reaches over `target`: i, and the counts before it
-    // and up to its end: a, b
+    // the bin in which the estimated weight reaches over `target`: i, the counts before it and
+    // up to its end: a, b, the estimate before it: c
     __device__ __forceinline__ Found reaching(u64 target) {
+        target = min(target, mass - 1);
         in_order([&](int b, u64 c, u64 w, unsigned k) {
-            if (w <= target && target < w + k * weight(b)) team.tell(Found{c, c + k, 0, b, 0});
+            if (w <= target && target < w + k * weight(b)) team.tell(Found{c, c + k, w, b, 0});
         });
         return team.told();
+    }
+    // the bins around the one that reaches over `near`, 2^-13 of the weight on either side, or that one
+    // where those hold more than `most` tokens; false where it does, too
+    __device__ __forceinline__ bool bracket(u64 near, u64 most, Found& low, Found& high) {
+        const u64 off = mass >> 13;
+        low = reaching(near > off ? near - off : 0);
+        high = reaching(near + off);
+        if (high.b - low.a <= most) return true;
+        low = high = reaching(near);
+        return high.b - low.a <= most;
+    }
+    // where to look next: the exact weight above the bracket is known now
+    static __device__ __forceinline__ u64 corrected(const Found& low, u64 target, u64 above) {
+        const long long near = (long long)low.c + (long long)(target - above);
+        return near > 0 ? (u64)near : 0;
     }
 };
 
@@ -887,8 +996,8 @@ struct Settings {
 // Single elements, whatever their values: rows far from zero, rows with more tokens at
 // a cut than the lists hold, k beyond the threads' maxima.
 template <typename T>
-__device__ __noinline__ void any_row(const Params& p, int64_t r, const Row<T>& row, Team& team, const Scale& s,
-                                     const Settings& o) {
+__device__ __noinline__ void any_row(const Params& p, int64_t r, const Row<T> row, Team team, const Scale s,
+                                     const Settings o) {
     constexpr int V = Row<T>::V;
     Shared& sh = team.sh;
     const int t = threadIdx.x;
@@ -955,7 +1064,7 @@ __device__ __noinline__ void any_row(const Params& p, int64_t r, const Row<T>& r
 #pragma unroll
             for (int q = 0; q < V; ++q) {
                 const float f = step_of(z[q], s);
-                if (f < (float)kBins) bins.add(f);
+                if (f < (float)kBins) Bins::add(sh, f, bins.log_each);
             }
         }
         bins.sum();
@@ -982,13 +1091,11 @@ __device__ __noinline__ void any_row(const Params& p, int64_t r, const Row<T>& r
             }
         }
         if (o.top_p < 1.f) {
-            // the steps around the estimate; wider ones where it was not good enough
-            for (float off = 0x1p-10f;; off *= 8.f) {
-                const float near = (float)known * o.top_p;
-                const u64 last = bins.mass - 1;
-                const Found low = bins.reaching(min((u64)(near * fmaxf(1.f - off, 0.f)), last));
-                const Found high = bins.reaching(min((u64)(near * (1.f + off)), last));
-                if (high.b - low.a > (u64)kList || off > 8.f) {
+            // the steps around the estimate, then around what the sums above them say
+            u64 near = (u64)((float)known * o.top_p);
+            for (int turn = 0;; ++turn) {
+                Found low, high;
+                if (!bins.bracket(near, kList, low, high) || turn == kTurns) {
                     const u64 all = row_sum(row, team, [&](float z, int i) -> u64 { return entry_of(z, i) >= cut ? weight(z) : 0; });
                     bisect(weight, share_ceil(o.top_p, all));
                     break;
@@ -996,10 +1103,11 @@ __device__ __noinline__ void any_row(const Params& p, int64_t r, const Row<T>& r
                 u64 all = 0, above = 0, b1, b2, last_kept = 0;
                 collect((float)low.i, (float)(high.i + 1), true, all, above);
                 team.sum(all, above, b1, b2);
+                const u64 target = share_ceil(o.top_p, all);
+                near = Bins::corrected(low, target, above);
                 bool good = false;
                 if (team.rank == 0) {
                     const int size = gather(team, sh.list, &sh.listed, kList);
-                    const u64 target = share_ceil(o.top_p, all);
                     order_list(sh.list, sh.weight, size, s, sh);
                     good = size > 0 && above < target && target - above <= sh.weight[size - 1];
                     if (good) last_kept = sh.list[first_reaching(sh.weight, size, target - above)];
@@ -1020,43 +1128,66 @@ __device__ __noinline__ void any_row(const Params& p, int64_t r, const Row<T>& r
     team.barrier();                                         // nobody leaves while others read its memory
 }
 
-// ---- rows near zero, in pairs ------------------------------------------------------------
+// ---- rows near zero, by words ------------------------------------------------------------
 
 // What a pass over the light elements does beside summing their weights.
 struct Pass {
     bool heavy_to_list;     // lists the heavy tokens
+    bool histogram;         // counts the light tokens by their steps
+    bool roughly;           // (with heavy_to_list) sums to 2^-15 of the sum alone, at a third of the cost
     bool masked;            // sums the steps below `low` only
     bool steps_to_list2;    // lists the light tokens of steps [low, high)
+    int log_each;           // of the histogram (Bins)
     float low, high;
-    uint32_t least, heavy;  // words: what elements are raised to, what no heavy one is below
+    uint32_t least, heavy;  // words: what elements are raised to, the least heavy value
 };
 
 // One warp's packs [begin, end): the sum of the light weights.
-template <typename T, bool EXACT>
-__device__ __noinline__ u64 light_part(const Row<T>& row, Shared& sh, int begin, int end, const Pass& pass) {
+template <typename T, bool EXACT, bool MASKED>
+__device__ __noinline__ u64 light_part(const Row<T> row, Shared& sh, int begin, int end, const Pass what) {
     constexpr int V = Row<T>::V, PER = 4 / sizeof(T);
     const Scale s = sh.scale;
-    const Pass what = pass;
     u64 sum = 0;
-    for (int v = begin + (int)(threadIdx.x & 31); v < end; v += 32) {
-        const uint4 k = row.words(v);
-        uint32_t w[4] = {k.x, k.y, k.z, k.w};
-        if (reaches<T>(max_word<T>(max_word<T>(w[0], w[1]), max_word<T>(w[2], w[3])), what.heavy)) {
+    float rough = 0.f;
+    int v = begin + (int)(threadIdx.x & 31);
+    uint4 next[2]{};                                        // on their way
+    if (v < end) next[0] = row.words(v);
+    if (v + 32 < end) next[1] = row.words(v + 32);
+    for (; v < end; v += 32) {
+        uint32_t w[4] = {next[0].x, next[0].y, next[0].z, next[0].w};
+        next[0] = next[1];
+        if (v + 64 < end) next[1] = row.words(v + 64);
+        uint32_t heavy[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            heavy[i] = reach_mask<T>(w[i], what.heavy);
+            if (MASKED || !what.heavy_to_list) w[i] = (w[i] & ~heavy[i]) | (what.least & heavy[i]);
+        }
+        if (!MASKED && what.heavy_to_list && (heavy[0] | heavy[1] | heavy[2] | heavy[3])) {
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                const float z = of_word<T>(w[q / PER], q % PER);
-                if (!((z - s.m) * s.hi >= kHeavy)) continue;
-                if (what.heavy_to_list) {
-                    const int at = atomicAdd(&sh.listed, 1);
-                    if (at < kList) sh.list[at] = entry_of(z, row.first_index(v) + q);
-                }
-                if constexpr (PER == 1) w[q] = what.least;
-                else w[q / 2] = q % 2 ? (w[q / 2] & 0xFFFFu) | (what.least & 0xFFFF0000u) : (w[q / 2] & 0xFFFF0000u) | (what.least & 0xFFFFu);
+                if (!(heavy[q / PER] >> (q % PER * 16) & 1)) continue;
+                const int at = atomicAdd(&sh.listed, 1);
+                if (at < kList) sh.list[at] = entry_of(of_word<T>(w[q / PER], q % PER), row.first_index(v) + q);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = (w[i] & ~heavy[i]) | (what.least & heavy[i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = max_word<T>(w[i], what.least);
-        if (what.steps_to_list2) {
+        if (!MASKED && what.roughly) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) rough += exp2_fast((of_word<T>(w[q / PER], q % PER) - s.m) * s.hi);
+            continue;
+        }
+        if (!MASKED && what.histogram) {
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float step = step_of(of_word<T>(w[q / PER], q % PER), s);
+                if (step < (float)kBins) Bins::add(sh, step, what.log_each);
+            }
+        }
+        if (MASKED && what.steps_to_list2) {
 #pragma unroll
             for (int q = 0; q < V; ++q) {
                 const float z = of_word<T>(w[q / PER], q % PER), f = step_of(z, s);
@@ -1066,9 +1197,11 @@ __device__ __noinline__ u64 light_part(const Row<T>& row, Shared& sh, int begin,
             }
         }
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) sum += light_weights<EXACT>(pair_of<T>(w, i), s, what.masked, what.low);
+        for (int q = 0; q < V; q += 2)
+            sum += light_weights<EXACT, MASKED>(
+                pack_f2(of_word<T>(w[q / PER], q % PER), of_word<T>(w[(q + 1) / PER], (q + 1) % PER)), s, what.low);
     }
-    return Team::warp_add(sum);
+    return Team::warp_add(!MASKED && what.roughly ? (u64)__float2ull_rz(rough * 0x1p43f) : sum << s.shift);
 }
 
 // The kth largest of the threads' maxima or a little less: k elements or more are not
@@ -1087,7 +1220,7 @@ __device__ __forceinline__ float bound_of(unsigned key, unsigned max_key, int k)
 
 // ---- the kernel ----------------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) unsigned char memory[];
     Shared& sh = *reinterpret_cast<Shared*>(memory);
     constexpr int V = Row<T>::V;
@@ -1107,6 +1240,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     float m = -INFINITY;
     {
         uint32_t top = splat_down<T>(-INFINITY);
+#pragma unroll 2
         for (int v = row.v0 + t; v < row.v1; v += kThreads) {
             const uint4 k = row.words(v);
             top = max_nan_word<T>(top, max_nan_word<T>(max_nan_word<T>(k.x, k.y), max_nan_word<T>(k.z, k.w)));
@@ -1132,7 +1266,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         sh.min_key = min_p > 0.f ? order_key(__double2float_ru((double)m + sh.min_distance)) : 0;
     }
     __syncthreads();
-    const Scale s = sh.scale;
+    Scale s = sh.scale;
     const unsigned max_key = order_key(m);
     if (temperature == 0.f || top_k == 1 || !(top_p > 0.f) || min_p > 1.f) {
         // the first of the order
@@ -1145,7 +1279,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         return;
     }
     const Settings o{u, top_p, top_k, max_key, (u64)sh.min_key << 32};
-    if (!in_pairs<T>(s) || top_k > kMostK) {
+    if (!by_words<T>(s) || top_k > kMostK) {
         any_row(p, r, row, team, s, o);
         return;
     }
@@ -1153,8 +1287,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (top_k > 0) {
         // The list takes every token that may be among the k (or has no weight): all that
         // follows is about it.
-        const float bound = team.maximum(fmaxf(bound_of(order_key(own_max), max_key, top_k), __fadd_rd(m, s.least)));
+        // A bound below which none of them lies: in every block its share of k threads reach it.
+        const int share = (top_k + team.size - 1) / team.size;
+        float bound = fmaxf(bound_of(order_key(own_max), max_key, share), __fadd_rd(m, s.least));
+        if (team.size > 1) bound = -team.maximum(-bound);
         const uint32_t from = splat_down<T>(bound);
+#pragma unroll 2
         for (int v = row.v0 + t; v < row.v1; v += kThreads) {
             const uint4 k = row.words(v);
             const uint32_t w[4] = {k.x, k.y, k.z, k.w};
@@ -1184,11 +1322,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         return;
     }
     // The light weights' sum, and a list of the heavy tokens.
-    Pass pass{true, false, false, 0.f, 0.f, least, splat_down<T>(__fadd_rd(m, 1.001f * kHeavy / s.hi))};
+    Pass pass{true, false, top_p < 1.f, false, false, 0, 0.f, 0.f, least, heavy_word<T>(s)};
     auto part_of = [](int begin, int end, int k) { return begin + (int)((int64_t)(end - begin) * k / kWarps); };
     auto light_sum = [&](int begin, int end) {              // of the block's warps' parts, into sh.light
         const int b = part_of(begin, end, warp), e = part_of(begin, end, warp + 1);
-        const u64 sum = sizeof(T) == 4 || s.exact ? light_part<T, true>(row, sh, b, e, pass) : light_part<T, sizeof(T) == 4>(row, sh, b, e, pass);
+        constexpr bool MAY = sizeof(T) == 4;                  // FLOAT: exact always
+        const u64 sum = pass.masked ? (MAY || s.exact ? light_part<T, true, true>(row, sh, b, e, pass)
+                                                      : light_part<T, MAY, true>(row, sh, b, e, pass))
+                                    : (MAY || s.exact ? light_part<T, true, false>(row, sh, b, e, pass)
+                                                      : light_part<T, MAY, false>(row, sh, b, e, pass));
         __syncthreads();
         if (lane == 0) sh.light[warp] = sum;
         __syncthreads();
@@ -1200,24 +1342,73 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     u64 light = light_sum(row.v0, row.v1), listed = t == 0 ? sh.listed : 0, b1, b2;
     team.sum(light, listed, b1, b2);
     if (listed > (u64)kList) {
-        any_row(p, r, row, team, s, o);
-        return;
-    }
-    // what is kept may end within the list
-    enum { DONE, ALL, TOP_P, OTHER };
-    if (team.rank == 0) {
-        const int size = gather(team, sh.list, &sh.listed, kList);
-        order_list(sh.list, sh.weight, size, s, sh);
-        if (t == 0) sh.listed = size;
-        const u64 heavy = sh.weight[size - 1], target = top_p < 1.f ? share_ceil(top_p, light + heavy) : ~0ull;
-        const int least_p = kept_of(sh.list, size, o.min_cut);
-        const int keep = min(first_reaching(sh.weight, size, target) + 1, least_p < size ? least_p : size + 1);
-        const int what = keep <= size ? DONE : (o.min_cut > 0 ? OTHER : (top_p < 1.f ? TOP_P : ALL));
-        if (what == DONE) choose(p, r, row, u, keep, s, sh);
+        // A flat row: as many tokens are heavy as the list holds, those within 6, 3, 1.5 or
+        // 0.75 octaves of the largest.  (Weights below 2^heavy are then good to 2^-24 of that.)
+        u64 n6_3 = 0, n2_1 = 0;                             // two counts each
+#pragma unroll 2
+        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+            const uint4 k = row.words(v);
+            const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float x = (of_word<T>(w[q * (int)sizeof(T) / 4], q % (4 / (int)sizeof(T))) - m) * s.hi;
+                n6_3 += (u64)(x >= -6.f) + ((u64)(x >= -3.f) << 32);
+                n2_1 += (u64)(x >= -1.5f) + ((u64)(x >= -0.75f) << 32);
+            }
+        }
+        team.sum(n6_3, n2_1, b1, b2);
+        const float heavy = (unsigned)n6_3 <= kList ? -6.f : (n6_3 >> 32) <= kList ? -3.f
+                          : (unsigned)n2_1 <= kList ? -1.5f : (n2_1 >> 32) <= kList ? -0.75f : 0.f;
+        if (heavy == 0.f) {                                  // more tokens, or equal ones
+            any_row(p, r, row, team, s, o);
+            return;
+        }
         __syncthreads();
-        if (t == 0) team.tell(Found{heavy, target, 0, what, 0});
+        s.heavy = heavy;
+        s.shift = 12 - (int)-heavy;
+        if (t == 0) {
+            sh.listed = 0;
+            sh.scale = s;
+        }
+        pass.heavy = heavy_word<T>(s);
+        __syncthreads();
+        light = team.sum(light_sum(row.v0, row.v1));
     }
-    const Found f = team.told();
+    // What is kept may end within the list.  For that the light weights' sum need be known
+    // so well only that the place of the cut is.
+    enum { DONE, ALL, TOP_P, OTHER, ROUGH };
+    Bins bins(team);
+    Found f;
+    for (;;) {
+        if (team.rank == 0) {
+            int size = sh.listed;
+            if (pass.heavy_to_list) {                        // the first time
+                size = gather(team, sh.list, &sh.listed, kList);
+                order_list(sh.list, sh.weight, size, s, sh);
+                if (t == 0) sh.listed = size;
+            }
+            const u64 heavy = sh.weight[size - 1], off = pass.roughly ? (light >> 15) + 1 : 0;
+            const u64 target = top_p < 1.f ? share_ceil(top_p, heavy + light - min(light, off)) : ~0ull;
+            const int reach = first_reaching(sh.weight, size, target), least_p = kept_of(sh.list, size, o.min_cut);
+            const int keep = min(reach + 1, least_p < size ? least_p : size + 1);
+            int what = keep <= size ? DONE : (o.min_cut > 0 ? OTHER : (top_p < 1.f ? TOP_P : ALL));
+            if (pass.roughly && (what == TOP_P || (keep == reach + 1 &&
+                                                   first_reaching(sh.weight, size, share_ceil(top_p, heavy + light + off)) != reach)))
+                what = ROUGH;
+            if (what == DONE) choose(p, r, row, u, keep, s, sh);
+            __syncthreads();
+            if (t == 0) team.tell(Found{heavy, target, 0, what, 0});
+        }
+        f = team.told();
+        if (f.i != ROUGH) break;
+        // to 2^-36 then, with a histogram of the light tokens' steps: the cut may lie among them
+        bins.clear();
+        pass.heavy_to_list = pass.roughly = false;
+        pass.histogram = true;
+        pass.log_each = bins.log_each;
+        light = team.sum(light_sum(row.v0, row.v1));
+        pass.histogram = false;
+    }
     if (f.i == DONE) {
         team.barrier();                                      // nobody leaves while others read its memory
         return;
@@ -1229,29 +1420,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     u64 total = light + f.a, cut = 0;
     pass.heavy_to_list = false;
     if (f.i == TOP_P) {
-        // The cut lies among the light tokens: a histogram of their steps shows where, to a
-        // fraction of a percent of their weight; the tokens of those steps go into a
-        // second list.
+        // The cut lies among the light tokens: the histogram shows where, to a fraction of a percent
+        // of their weight; the tokens of those steps go into a second list.
         const u64 target = f.b - f.a;                        // of the light weights
-        Bins bins(team);
-        bins.clear();
-        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
-            const uint4 k = row.words(v);
-            const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float z = of_word<T>(w[q * (int)sizeof(T) / 4], q % (4 / (int)sizeof(T)));
-                const float step = step_of(z, s);
-                if (step < (float)kBins && !((z - s.m) * s.hi >= kHeavy)) bins.add(step);
-            }
-        }
         bins.sum();
-        const float near = (float)target / (float)light * (float)bins.mass;
-        for (float off = 0x1p-10f;; off *= 8.f) {
-            const u64 last = bins.mass - 1;
-            const Found low = bins.reaching(min((u64)(near * fmaxf(1.f - off, 0.f)), last));
-            const Found high = bins.reaching(min((u64)(near * (1.f + off)), last));
-            if (high.b - low.a > (u64)kBracket || off > 8.f) {
+        u64 near = (u64)((float)target / (float)light * (float)bins.mass);
+        for (int turn = 0;; ++turn) {
+            Found low, high;
+            if (!bins.bracket(near, kBracket, low, high) || turn == kTurns) {
                 any_row(p, r, row, team, s, o);
                 return;
             }
@@ -1260,6 +1436,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             pass.high = (float)(high.i + 1);
             u64 above = light_sum(row.v0, row.v1);
             above = team.sum(above);
+            near = Bins::corrected(low, target, above);
             if (team.rank == 0) {
                 const int size = gather(team, sh.list2, &sh.listed2, kBracket);
                 order_list(sh.list2, sh.weight2, size, s, sh);
@@ -1336,11 +1513,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 // ---- host side -------------------------------------------------------------
 
-// Blocks a row: as many as keep every block resident, two an SM, with two rounds of
-// packs each or more.
+// Blocks a row: as many as keep every block resident, with two rounds of packs each
+// or more.
 inline int cluster_of(int64_t rows, int64_t packs, int sm_count) {
     int c = 1;
-    while (c < kMaxCluster && rows * c * 2 <= 2 * (int64_t)sm_count && packs >= (int64_t)c * 2 * 2 * kThreads) c *= 2;
+    while (c < kMaxCluster && rows * c * 2 <= kBlocksPerSm * (int64_t)sm_count && packs >= (int64_t)c * 2 * 2 * kThreads) c *= 2;
     return c;
 }
 
