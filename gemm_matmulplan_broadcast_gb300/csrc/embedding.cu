@@ -25,8 +25,8 @@ constexpr int kThreads = 256;
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1536;          // tokens of a sort block: a counter for each and each warp, 202 KB
 constexpr int kClearRows = 8;           // rows a group of threads clears
-constexpr int kJoinChunks = 8;          // chunks whose ends a join block looks at
-constexpr int kJoinLogTx = 5;           // its threads on a row: eight groups share a token's partial sums
+constexpr int kJoinLogTx = 5;           // threads of a join block's group
+constexpr int kJoinChunks = kThreads >> kJoinLogTx;     // groups, and chunks whose ends it looks at
 
 struct Tile {
     int log_tx;             // threads on a row: 1 << log_tx; the block's others take further rows
@@ -331,47 +331,63 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const BwdParams p) {
 }
 
 // Tokens whose places cross a chunk's end: the partial sums of the chunk in which
-// they begin and of those after it, in order.  `groups` groups of threads take
-// every groups-th of them each and are added in group order.
+// they begin and of those after it, in order.  A block looks at the ends of kJoinChunks
+// chunks, one for each of its groups of threads; a group alone adds up to kAlone
+// partial sums, of more of them every group takes every kJoinChunks-th, and those are added
+// in group order.
+constexpr int kAlone = 16;
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) join_kernel(const BwdParams p) {
     constexpr int LOG_TX = kJoinLogTx, GROUPS = kThreads >> LOG_TX;
-    __shared__ int found[kJoinChunks];
+    static_assert(GROUPS == kJoinChunks, "");
+    __shared__ int shared_by_all[kJoinChunks];
     __shared__ alignas(16) float sums[GROUPS - 1][1 << LOG_TX][V];
     const int tx = threadIdx.x & ((1 << LOG_TX) - 1), group = threadIdx.x >> LOG_TX;
     const int64_t tiles = ceil_div(p.tile.packs, 1 << LOG_TX);
     for (int64_t unit = blockIdx.x; unit < p.units; unit += gridDim.x) {
         const int64_t c0 = unit / tiles * kJoinChunks;
-        const int64_t pack = (unit % tiles << LOG_TX) + tx;
-        if (threadIdx.x < kJoinChunks) {
-            const int64_t chunk = c0 + threadIdx.x, next = (chunk + 1) * p.length;
-            int token = -1;
-            if (next < p.s.start[p.vocab]) {
-                const int t = p.s.token[next - 1];
-                if (p.s.start[t] >= next - p.length && p.s.start[t + 1] > next) token = t;
+        const int64_t pack = (unit % tiles << LOG_TX) + tx, c = pack * V;
+        const bool in = pack < p.tile.packs;
+        F2 acc[pairs<V>()];
+        auto clear = [&] {
+#pragma unroll
+            for (int q = 0; q < pairs<V>(); ++q) acc[q] = both(0.f);
+        };
+        const int64_t chunk = c0 + group, next = (chunk + 1) * p.length;
+        int token = -1;
+        int64_t last = 0;
+        if (next < p.s.start[p.vocab]) {
+            const int t = p.s.token[next - 1], end = p.s.start[t + 1];
+            if (p.s.start[t] >= next - p.length && end > next) {
+                token = t;
+                last = (end - 1) / p.length;
             }
-            found[threadIdx.x] = token;
+        }
+        const bool alone = last - chunk < kAlone;
+        if (tx == 0) shared_by_all[group] = alone ? -1 : token;
+        if (token >= 0 && alone && in) {
+            clear();
+            add_partial<V>(acc, p.partial + (chunk * 2 + 1) * p.cols + c);
+#pragma unroll 4
+            for (int64_t k = chunk + 1; k <= last; ++k) add_partial<V>(acc, p.partial + k * 2 * p.cols + c);
+            finish<T, V>(p, token, c, acc);
         }
         __syncthreads();
         for (int i = 0; i < kJoinChunks; ++i) {
-            const int token = found[i];
-            if (token < 0) continue;                        // the whole block
-            const int64_t chunk = c0 + i, last = (p.s.start[token + 1] - 1) / p.length;
-            const bool in = pack < p.tile.packs;
-            const int64_t c = pack * V;
-            F2 acc[pairs<V>()];
-#pragma unroll
-            for (int q = 0; q < pairs<V>(); ++q) acc[q] = both(0.f);
+            const int t = shared_by_all[i];
+            if (t < 0) continue;                            // the whole block
+            const int64_t from = c0 + i, to = (p.s.start[t + 1] - 1) / p.length;
+            clear();
             if (in) {
-                if (group == 0) add_partial<V>(acc, p.partial + (chunk * 2 + 1) * p.cols + c);
+                if (group == 0) add_partial<V>(acc, p.partial + (from * 2 + 1) * p.cols + c);
 #pragma unroll 4
-                for (int64_t k = chunk + 1 + group; k <= last; k += GROUPS) add_partial<V>(acc, p.partial + k * 2 * p.cols + c);
+                for (int64_t k = from + 1 + group; k <= to; k += GROUPS) add_partial<V>(acc, p.partial + k * 2 * p.cols + c);
                 if (group > 0) put_partial<V>(&sums[group - 1][tx][0], acc);
             }
             __syncthreads();
             if (in && group == 0) {
                 for (int g = 1; g < GROUPS; ++g) add_partial<V>(acc, &sums[g - 1][tx][0]);
-                finish<T, V>(p, token, c, acc);
+                finish<T, V>(p, t, c, acc);
             }
             __syncthreads();
         }
@@ -413,6 +429,7 @@ inline int chunk_length(int64_t n, int64_t packs, int sm_count) {
     return length;
 }
 
+// A sort block an SM; more where its counters hold no more tokens.
 inline int sort_bins(int64_t vocab, int sm_count) { return (int)min64(kMaxBins, ceil_div(vocab, sm_count)); }
 
 struct Layout {
