@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const FwdParams p) {
 // counts its own stretch of the ids by token, a scan over warps and tokens turns
 // the counts into positions, and the warps go over their stretches again.  Within
 // 32 ids the lanes with the same token take consecutive positions.
-// [16384 ids, 50257 tokens]: each block reads the 128 KB of ids twice, from L2.
 __global__ void __launch_bounds__(kSortThreads)
 sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, Sorted s) {
     extern __shared__ int counts[];                 // [kSortWarps][bins]
@@ -132,24 +131,28 @@ sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, 
     const int stretch = (int)(ceil_div(ceil_div(n, kSortWarps), 32) * 32);      // at most n + 31
     const int64_t begin = min64((int64_t)warp * stretch, n), end = min64(begin + stretch, n);
     int* const mine = counts + warp * bins;
-    // four groups of 32 ids at a time; -1 past the end and for ids that are no tokens
-    auto read = [&](int64_t base, int64_t (&t)[4]) {
+    // 512 ids at a time, all on their way at once: the block's tokens among them, counted from
+    // its first one, or -1
+    constexpr int EACH = 16;
+    int own_ids[EACH], below = 0;
+    auto read = [&](int64_t base, bool count) {
+        int64_t id[EACH];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < EACH; ++u) {
             const int64_t i = base + u * 32 + lane;
-            t[u] = i < end ? tokens[i] : -1;
-            if (t[u] >= vocab) t[u] = -1;
+            id[u] = i < end ? tokens[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < EACH; ++u) {
+            own_ids[u] = id[u] >= v0 && id[u] < v0 + own ? (int)(id[u] - v0) : -1;
+            if (count) below += id[u] >= 0 && id[u] < v0;
         }
     };
-    int below = 0;
-    for (int64_t base = begin; base < end; base += 128) {
-        int64_t t[4];
-        read(base, t);
+    for (int64_t base = begin; base < end; base += 32 * EACH) {
+        read(base, true);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            below += t[u] >= 0 && t[u] < v0;
-            if (t[u] >= v0 && t[u] < v0 + own) atomicAdd(&mine[(int)(t[u] - v0)], 1);
-        }
+        for (int u = 0; u < EACH; ++u)
+            if (own_ids[u] >= 0) atomicAdd(&mine[own_ids[u]], 1);
     }
     below = __reduce_add_sync(0xffffffffu, below);
     if (lane == 0) scan[warp] = below;
@@ -197,12 +200,11 @@ sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, 
         if (v0 + b == vocab - 1) s.start[vocab] = position;
     }
     __syncthreads();
-    for (int64_t base = begin; base < end; base += 128) {
-        int64_t t[4];
-        read(base, t);
+    for (int64_t base = begin; base < end; base += 32 * EACH) {
+        if (end - begin > 32 * EACH) read(base, false);     // (else they are still there)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int b = t[u] >= v0 && t[u] < v0 + own ? (int)(t[u] - v0) : -1;
+        for (int u = 0; u < EACH; ++u) {
+            const int b = own_ids[u];
             if (!__any_sync(0xffffffffu, b >= 0)) continue;
             const unsigned same = __match_any_sync(0xffffffffu, b);
             int at = 0;
@@ -210,7 +212,7 @@ sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, 
             __syncwarp();
             if (b >= 0) {
                 s.place[at] = (int)(base + u * 32 + lane);
-                s.token[at] = (int)t[u];
+                s.token[at] = (int)v0 + b;
                 if ((same >> lane) == 1u) mine[b] = at + 1;         // the last of them
             }
             __syncwarp();
