@@ -13,6 +13,7 @@
 // (sum_kernel); a token whose places cross chunks leaves partial sums that
 // join_kernel adds in chunk order.  The rows of tokens that do not occur are
 // cleared by further blocks of sum_kernel while its chunks are summed.
+#include <initializer_list>
 #include <new>
 
 #include "plan_state.h"
@@ -45,9 +46,10 @@ struct FwdParams {
     int64_t units;
 };
 
-// What the sort leaves: the places of all tokens, sorted by token and place.
+// What the sort leaves: each token's places together, in order.
 struct Sorted {
-    int* start;             // [vocab + 1]: where each token's places begin
+    int2* range;            // [vocab]: where each token's places begin and end
+    int* total;             // of all tokens
     int* place;             // [n]
     int* token;             // [n]
 };
@@ -115,24 +117,25 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const FwdParams p) {
     }
 }
 
-// A block sorts the places of the tokens [bins blockIdx.x, ...): each warp
+// A block sorts the places of every 2^log_blocks-th token from blockIdx.x on (frequent
+// tokens often have low ids: they are shared out): each warp
 // counts its own stretch of the ids by token, a scan over warps and tokens turns
 // the counts into positions, and the warps go over their stretches again.  Within
 // 32 ids the lanes with the same token take consecutive positions.
 __global__ void __launch_bounds__(kSortThreads)
-sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, Sorted s) {
+sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int log_blocks, int bins, Sorted s) {
     extern __shared__ int counts[];                 // [kSortWarps][bins]
     __shared__ int scan[kSortWarps + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t v0 = (int64_t)blockIdx.x * bins;
-    const int own = (int)min64(bins, vocab - v0);   // at least 1
+    const int residue = (int)blockIdx.x, mask = (1 << log_blocks) - 1;
+    const int own = (int)((vocab - residue + mask) >> log_blocks);      // tokens; at least 1, at most bins
     for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) counts[i] = 0;
     __syncthreads();
     const int stretch = (int)(ceil_div(ceil_div(n, kSortWarps), 32) * 32);      // at most n + 31
     const int64_t begin = min64((int64_t)warp * stretch, n), end = min64(begin + stretch, n);
     int* const mine = counts + warp * bins;
-    // 512 ids at a time, all on their way at once: the block's tokens among them, counted from
-    // its first one, or -1
+    // 512 ids at a time, all on their way at once: the block's tokens among them, as its
+    // first, second, ... one, or -1
     constexpr int EACH = 16;
     int own_ids[EACH], below = 0;
     auto read = [&](int64_t base, bool count) {
@@ -144,8 +147,10 @@ sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, 
         }
 #pragma unroll
         for (int u = 0; u < EACH; ++u) {
-            own_ids[u] = id[u] >= v0 && id[u] < v0 + own ? (int)(id[u] - v0) : -1;
-            if (count) below += id[u] >= 0 && id[u] < v0;
+            const bool known = id[u] >= 0 && id[u] < vocab;
+            const int r = (int)id[u] & mask;
+            own_ids[u] = known && r == residue ? (int)(id[u] >> log_blocks) : -1;
+            if (count) below += known && r < residue;
         }
     };
     for (int64_t base = begin; base < end; base += 32 * EACH) {
@@ -195,9 +200,10 @@ sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, 
     for (int j = 0; j < per; ++j) {
         const int b = threadIdx.x * per + j;
         if (b >= own) continue;
-        s.start[v0 + b] = position;
+        const int begin = position;
         position = over_warps(b, position, true);
-        if (v0 + b == vocab - 1) s.start[vocab] = position;
+        s.range[((int64_t)b << log_blocks) + residue] = make_int2(begin, position);
+        if (residue == (int)gridDim.x - 1 && b == own - 1) *s.total = position;
     }
     __syncthreads();
     for (int64_t base = begin; base < end; base += 32 * EACH) {
@@ -212,7 +218,7 @@ sort_kernel(const int64_t* __restrict__ tokens, int n, int64_t vocab, int bins, 
             __syncwarp();
             if (b >= 0) {
                 s.place[at] = (int)(base + u * 32 + lane);
-                s.token[at] = (int)v0 + b;
+                s.token[at] = (b << log_blocks) + residue;
                 if ((same >> lane) == 1u) mine[b] = at + 1;         // the last of them
             }
             __syncwarp();
@@ -236,8 +242,10 @@ __device__ __forceinline__ void put_partial(float* to, const F2 (&acc)[pairs<V>(
         unpack_f2(acc[0], lo, hi);
         *to = lo;
     } else {
+        if constexpr (V == 2) *reinterpret_cast<F2*>(to) = acc[0];
+        else
 #pragma unroll
-        for (int q = 0; q < V / 2; q += 2) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(acc[q], acc[q + 1]);
+            for (int q = 0; q < V / 2; q += 2) *reinterpret_cast<ulonglong2*>(to + 2 * q) = make_ulonglong2(acc[q], acc[q + 1]);
     }
 }
 template <int V>
@@ -245,6 +253,8 @@ __device__ __forceinline__ void add_partial(F2 (&acc)[pairs<V>()], const float* 
     if constexpr (V == 1) {
         acc[0] = add2(acc[0], pack_f2(*from, 0.f));
     } else {
+        if constexpr (V == 2) acc[0] = add2(acc[0], *reinterpret_cast<const F2*>(from));
+        else
 #pragma unroll
         for (int q = 0; q < V / 2; q += 2) {
             const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(from + 2 * q);
@@ -285,16 +295,16 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const BwdParams p) {
         if (!sums) {
             const int64_t v0 = group * kClearRows;
             if (v0 >= p.vocab) continue;
-            int starts[kClearRows + 1];
+            int2 range[kClearRows];
 #pragma unroll
-            for (int i = 0; i <= kClearRows; ++i) starts[i] = p.s.start[min64(v0 + i, p.vocab)];
+            for (int i = 0; i < kClearRows; ++i) range[i] = p.s.range[min64(v0 + i, p.vocab - 1)];
 #pragma unroll
             for (int i = 0; i < kClearRows; ++i)
-                if (v0 + i < p.vocab && starts[i] == starts[i + 1])
+                if (v0 + i < p.vocab && range[i].x == range[i].y)
                     fill<T, V>(static_cast<T*>(p.dE) + (v0 + i) * p.e_pitch + c, 0.f);
             continue;
         }
-        const int64_t n = p.s.start[p.vocab], p0 = group * p.length, p1 = min64(p0 + p.length, n);
+        const int64_t n = *p.s.total, p0 = group * p.length, p1 = min64(p0 + p.length, n);
         if (p0 >= n) continue;
         F2 acc[pairs<V>()];
         auto clear = [&] {
@@ -304,9 +314,9 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const BwdParams p) {
         clear();
         int current = p.s.token[p0];
         auto leave = [&] {
-            const int begin = p.s.start[current], end = p.s.start[current + 1];
-            if (begin >= p0 && end <= p1) finish<T, V>(p, current, c, acc);
-            else put_partial<V>(p.partial + (group * 2 + (begin >= p0)) * p.cols + c, acc);
+            const int2 range = p.s.range[current];
+            if (range.x >= p0 && range.y <= p1) finish<T, V>(p, current, c, acc);
+            else put_partial<V>(p.partial + (group * 2 + (range.x >= p0)) * p.cols + c, acc);
         };
         for (int64_t at = p0; at < p1; at += 4) {
             // (the arrays' lengths are multiples of 4; what lies past the last place is not used)
@@ -358,11 +368,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BwdParams p) {
         const int64_t chunk = c0 + group, next = (chunk + 1) * p.length;
         int token = -1;
         int64_t last = 0;
-        if (next < p.s.start[p.vocab]) {
-            const int t = p.s.token[next - 1], end = p.s.start[t + 1];
-            if (p.s.start[t] >= next - p.length && end > next) {
+        if (next < *p.s.total) {
+            const int t = p.s.token[next - 1];
+            const int2 range = p.s.range[t];
+            if (range.x >= next - p.length && range.y > next) {
                 token = t;
-                last = (end - 1) / p.length;
+                last = (range.y - 1) / p.length;
             }
         }
         const bool alone = last - chunk < kAlone;
@@ -378,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BwdParams p) {
         for (int i = 0; i < kJoinChunks; ++i) {
             const int t = shared_by_all[i];
             if (t < 0) continue;                            // the whole block
-            const int64_t from = c0 + i, to = (p.s.start[t + 1] - 1) / p.length;
+            const int64_t from = c0 + i, to = (p.s.range[t].y - 1) / p.length;
             clear();
             if (in) {
                 if (group == 0) add_partial<V>(acc, p.partial + (from * 2 + 1) * p.cols + c);
@@ -431,30 +442,45 @@ inline int chunk_length(int64_t n, int64_t packs, int sm_count) {
     return length;
 }
 
-// A sort block an SM; more where its counters hold no more tokens.
-inline int sort_bins(int64_t vocab, int sm_count) { return (int)min64(kMaxBins, ceil_div(vocab, sm_count)); }
+// Sort blocks: a power of two, 128 (nearly one an SM), more where their counters hold no more
+// tokens, no more than there are tokens.
+inline int sort_log_blocks(int64_t vocab) {
+    int log = 7;
+    while (ceil_div(vocab, int64_t(1) << log) > kMaxBins) ++log;
+    while (log > 0 && (int64_t(1) << log) > vocab) --log;
+    return log;
+}
 
 struct Layout {
-    size_t place, token, partial, bytes;
+    size_t total, place, token, partial, bytes;
 };
 inline Layout layout_of(int64_t n, int64_t vocab, int64_t cols, int64_t chunks) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     Layout l;
-    l.place = up((size_t)(vocab + 1) * 4);
+    l.total = up((size_t)vocab * 8);
+    l.place = l.total + 256;
     l.token = l.place + up((size_t)n * 4);
     l.partial = l.token + up((size_t)n * 4);
     l.bytes = l.partial + (size_t)chunks * 2 * (size_t)cols * 4;
     return l;
 }
 
+// Elements that every row's start and length divide by: 16 bytes of them, 4, or one.
+inline int pack_bytes(int64_t bytes, std::initializer_list<const void*> pointers, std::initializer_list<int64_t> pitches) {
+    uint64_t all = (uint64_t)bytes;
+    for (const void* p : pointers) all |= (uint64_t)reinterpret_cast<uintptr_t>(p);
+    for (int64_t p : pitches) all |= (uint64_t)p;
+    return all % 16 == 0 ? 16 : (all % 4 == 0 ? 4 : 2);
+}
+
 template <typename T, int V>
-cudaError_t backward_as(BwdParams p, const int64_t* tokens, int64_t n, int sm_count, cudaStream_t s) {
-    const int bins = sort_bins(p.vocab, sm_count);
+cudaError_t backward_as(BwdParams p, const int64_t* tokens, int64_t n, cudaStream_t s) {
+    const int log_blocks = sort_log_blocks(p.vocab), bins = (int)ceil_div(p.vocab, int64_t(1) << log_blocks);
     const size_t smem = (size_t)kSortWarps * bins * 4;
     cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(sort_kernel), kSortWarps * kMaxBins * 4);
     if (e == cudaSuccess)
-        e = plan_launch(sort_kernel, dim3((unsigned)ceil_div(p.vocab, bins)), dim3(kSortThreads), smem, s, tokens, (int)n,
-                        p.vocab, bins, p.s);
+        e = plan_launch(sort_kernel, dim3(1u << log_blocks), dim3(kSortThreads), smem, s, tokens, (int)n, p.vocab,
+                        log_blocks, bins, p.s);
     if (e != cudaSuccess) return e;
     p.tile = tile_of(p.cols / V, 1);
     const int groups = kThreads >> p.tile.log_tx;
@@ -521,13 +547,15 @@ olc_status olc_embedding_forward(olc_embedding_plan* plan, const void* table, in
     const olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
     const embedding::FwdParams p{table, tokens, Y, table_pitch, y_pitch, n, plan->vocab, plan->scale, {}, 0};
-    const bool wide = cols * eb % 16 == 0 && plan_aligned16(table) && plan_aligned16(Y) &&
-                      (plan->vocab <= 1 || table_pitch * eb % 16 == 0) && (n == 1 || y_pitch * eb % 16 == 0);
+    const int bytes = embedding::pack_bytes(cols * eb, {table, Y},
+                                            {plan->vocab <= 1 ? 0 : table_pitch * eb, n == 1 ? 0 : y_pitch * eb});
     return by_type(plan->dtype, [&](auto tag) {
         using T = decltype(tag);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
-        return plan_status(wide ? embedding::forward_as<T, 16 / sizeof(T)>(p, cols, plan->state.sm_count, s)
-                                : embedding::forward_as<T, 1>(p, cols, plan->state.sm_count, s));
+        const int sms = plan->state.sm_count;
+        if (bytes == 16) return plan_status(embedding::forward_as<T, 16 / sizeof(T)>(p, cols, sms, s));
+        if (sizeof(T) == 2 && bytes == 4) return plan_status(embedding::forward_as<T, 2>(p, cols, sms, s));
+        return plan_status(embedding::forward_as<T, 1>(p, cols, sms, s));
     });
 }
 
@@ -544,12 +572,13 @@ olc_status olc_embedding_backward(olc_embedding_plan* plan, const void* dY, int6
     olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
     const int sms = plan->state.sm_count;
-    const bool wide = cols * eb % 16 == 0 && plan_aligned16(dY) && plan_aligned16(dtable) &&
-                      (n <= 1 || dy_pitch * eb % 16 == 0) && (vocab == 1 || dtable_pitch * eb % 16 == 0);
+    const int bytes = embedding::pack_bytes(cols * eb, {dY, dtable},
+                                            {n <= 1 ? 0 : dy_pitch * eb, vocab == 1 ? 0 : dtable_pitch * eb});
+    const int elements = bytes == 16 ? (int)(16 / eb) : (eb == 2 && bytes == 4 ? 2 : 1);
     // (the memory is for the shortest chunks, so that a call with other alignment does not
     // have to allocate again)
     const int64_t packs = ceil_div(cols * eb, 16);
-    const int length = embedding::chunk_length(n, wide ? packs : cols, sms);
+    const int length = embedding::chunk_length(n, cols / elements, sms);
     const int64_t chunks = ceil_div(n, length), most = ceil_div(n, embedding::chunk_length(n, packs, sms));
     const embedding::Layout l = embedding::layout_of(n, vocab, cols, most);
     st = plan->state.ensure(l.bytes);
@@ -557,15 +586,16 @@ olc_status olc_embedding_backward(olc_embedding_plan* plan, const void* dY, int6
     char* const m = static_cast<char*>(plan->state.memory);
     const embedding::BwdParams p{dY, dtable, reinterpret_cast<float*>(m + l.partial), dy_pitch, dtable_pitch, vocab, cols,
                                  plan->scale, accumulate != 0, length, chunks,
-                                 {reinterpret_cast<int*>(m), reinterpret_cast<int*>(m + l.place),
-                                  reinterpret_cast<int*>(m + l.token)},
+                                 {reinterpret_cast<int2*>(m), reinterpret_cast<int*>(m + l.total),
+                                  reinterpret_cast<int*>(m + l.place), reinterpret_cast<int*>(m + l.token)},
                                  {}, 0, 0};
     return by_type(plan->dtype, [&](auto tag) {
         using T = decltype(tag);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
         return plan_status(plan->state.use(s, [&] {
-            return wide ? embedding::backward_as<T, 16 / sizeof(T)>(p, tokens, n, sms, s)
-                        : embedding::backward_as<T, 1>(p, tokens, n, sms, s);
+            if (elements == 16 / (int)sizeof(T)) return embedding::backward_as<T, 16 / sizeof(T)>(p, tokens, n, s);
+            if (sizeof(T) == 2 && elements == 2) return embedding::backward_as<T, 2>(p, tokens, n, s);
+            return embedding::backward_as<T, 1>(p, tokens, n, s);
         }));
     });
 }
