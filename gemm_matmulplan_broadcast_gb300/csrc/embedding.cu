@@ -554,7 +554,8 @@ olc_status olc_embedding_forward(olc_embedding_plan* plan, const void* table, in
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
         const int sms = plan->state.sm_count;
         if (bytes == 16) return plan_status(embedding::forward_as<T, 16 / sizeof(T)>(p, cols, sms, s));
-        if (sizeof(T) == 2 && bytes == 4) return plan_status(embedding::forward_as<T, 2>(p, cols, sms, s));
+        if constexpr (sizeof(T) == 2)
+            if (bytes == 4) return plan_status(embedding::forward_as<T, 2>(p, cols, sms, s));
         return plan_status(embedding::forward_as<T, 1>(p, cols, sms, s));
     });
 }
@@ -594,7 +595,8 @@ olc_status olc_embedding_backward(olc_embedding_plan* plan, const void* dY, int6
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
         return plan_status(plan->state.use(s, [&] {
             if (elements == 16 / (int)sizeof(T)) return embedding::backward_as<T, 16 / sizeof(T)>(p, tokens, n, s);
-            if (sizeof(T) == 2 && elements == 2) return embedding::backward_as<T, 2>(p, tokens, n, s);
+            if constexpr (sizeof(T) == 2)
+                if (elements == 2) return embedding::backward_as<T, 2>(p, tokens, n, s);
             return embedding::backward_as<T, 1>(p, tokens, n, s);
         }));
     });

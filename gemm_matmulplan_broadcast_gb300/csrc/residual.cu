@@ -122,8 +122,8 @@ struct Words {
 // W warps on a row, NV packs (or pairs of elements) a thread, in registers.
 // W == 1: blocks of four independent warps.
 template <typename T, int V, int W, int NV>
-__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, V > 1 && W == 4 && NV == 4 ? 7 : 0) forward_kernel(const FwdParams p) {
-    using C = std::conditional_t<V == 1, Columns<T, V>, Words<T, V == 1 ? 4 : V>>;
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, V > 2 && W == 4 && NV == 4 ? 7 : 0) forward_kernel(const FwdParams p) {
+    using C = std::conditional_t<(V <= 2), Columns<T, V>, Words<T, V <= 2 ? 4 : V>>;
     constexpr int P = C::P, TPR = W * 32;
     __shared__ float slots1[2][W];
     __shared__ float2 slots2[2][W];
@@ -1060,9 +1060,12 @@ column_sum_kernel(const float* __restrict__ partial, int blocks, int64_t cols, c
 // barrier.
 template <typename T, int V>
 cudaError_t forward_as(const FwdParams& p, int sm_count, cudaStream_t s) {
-    // single elements go in pairs, twice as many a thread as packs
-    const int64_t n = ceil_div(p.cols, V == 1 ? 4 : V);
-    constexpr int M = V == 1 ? 2 : 1;
+    // Single elements go in pairs, and pairs (rows of 16-bit elements on 4-byte boundaries)
+    // one by one: twice as many a thread as packs.  BF16, layer norm before and after, as
+    // single elements and as pairs: [1167, 2058] 19.0 and 16.8 us, [5415, 350] 14.9 and
+    // 10.9, [10000, 1350] 67.7 and 54.1, [16384, 4098] 433 and 354.
+    const int64_t n = ceil_div(p.cols, V <= 2 ? 4 : V);
+    constexpr int M = V <= 2 ? 2 : 1;
     const bool few = p.rows < 4 * (int64_t)sm_count;
 #define OLC_FWD(W, NV)                                                                                          \
     return plan_launch(forward_kernel<T, V, W, NV * M>, dim3((unsigned)(W == 1 ? ceil_div(p.rows, 4) : p.rows)), \
@@ -1099,7 +1102,7 @@ struct BwdShape {
 template <int V>
 BwdShape backward_shape(int64_t rows, int64_t cols, int sm_count, int operands, int weights, bool gated, bool all) {
     BwdShape b;
-    if (V > 1) {
+    if (V > 2) {
         // (a gate takes registers, too: 16 columns then only where 8 do not reach)
         b.per_thread = all || (gated && cols <= 8 * kThreads) ? 8 : 16;
         const int64_t row = cols * (16 / V) * operands, held = cols * (16 / V) * weights, room = kRingSmem - held;
@@ -1149,7 +1152,7 @@ cudaError_t backward_as(BwdParams p, int sm_count, const Outputs& outputs, cudaS
     cudaError_t e = cudaSuccess;
     p.threads_per_row = b.tpr;
     if (b.kind == BwdShape::RING) {
-        if constexpr (V > 1)
+        if constexpr (V > 2)
             e = all ? backward_ring<T, 8, true, true>(p, b, s)
                 : !p.gate ? backward_ring<T, 16, false, false>(p, b, s)
                 : b.per_thread == 8 ? backward_ring<T, 8, false, true>(p, b, s)
@@ -1162,9 +1165,12 @@ cudaError_t backward_as(BwdParams p, int sm_count, const Outputs& outputs, cudaS
             e = plan_launch(backward_long_kernel<T, V>,
                             dim3((unsigned)ceil_div(ceil_div(p.cols, V), 128), (unsigned)b.blocks), dim3(128), 0, s, p);
     } else {
-        // rows of packs whose operands overfill the ring come here as single elements do
-        constexpr int NV = V == 1 ? kColsPerThread / 2 : kColsPerThread / V;
-        e = plan_launch(backward_kernel<T, V, NV>, dim3((unsigned)b.blocks), dim3((unsigned)(b.tpr * b.groups)), b.smem, s, p);
+        // Rows of packs whose operands overfill the ring come here as single elements do.
+        // Pairs (V == 2) go as single elements: [10000, 1350] BF16 takes 127 us so and 139
+        // as pairs, whose offsets are not constants ([1167, 2058]: 40 and 38; rows wider
+        // than a block keeps gain: [16384, 4098] 1189 as single elements and 819 as pairs).
+        constexpr int E = V == 2 ? 1 : V, NV = E == 1 ? kColsPerThread / 2 : kColsPerThread / E;
+        e = plan_launch(backward_kernel<T, E, NV>, dim3((unsigned)b.blocks), dim3((unsigned)(b.tpr * b.groups)), b.smem, s, p);
     }
     if (e != cudaSuccess || !p.partial) return e;
     Outputs o = outputs;
@@ -1223,8 +1229,7 @@ void olc_residual_norm_plan_destroy(olc_residual_norm_plan* plan) {
     delete plan;
 }
 
-// A [rows, cols] operand: refused, and whether its rows start on 16-byte
-// boundaries (null: nothing to say against it)
+// A [rows, cols] operand that is refused
 static bool bad_rows(const olc_residual_norm_plan* plan, const void* m, int64_t pitch) {
     const int64_t eb = plan_elem_bytes(plan->dtype);
     return m && ((plan->rows > 1 && (pitch < plan->cols || !plan_fits(plan->rows, pitch, eb))) || plan_misaligned(m, eb));
@@ -1232,9 +1237,26 @@ static bool bad_rows(const olc_residual_norm_plan* plan, const void* m, int64_t 
 static bool bad_gate(const olc_residual_norm_plan* plan, const void* m, int64_t pitch) {
     return pitch == 0 ? plan_misaligned(m, plan_elem_bytes(plan->dtype)) : bad_rows(plan, m, pitch);
 }
-static bool wide_rows(const olc_residual_norm_plan* plan, const void* m, int64_t pitch) {
-    return plan_aligned16(m) && (!m || plan->rows == 1 || pitch * plan_elem_bytes(plan->dtype) % 16 == 0);
-}
+// What the starts of all rows of the given operands divide by: 16, 4 or less
+struct Bytes {
+    const olc_residual_norm_plan* plan;
+    uint64_t all;
+    explicit Bytes(const olc_residual_norm_plan* p) : plan(p), all((uint64_t)(p->cols * plan_elem_bytes(p->dtype))) {}
+    Bytes& rows(const void* m, int64_t pitch) {
+        all |= (uint64_t)reinterpret_cast<uintptr_t>(m);
+        if (m && plan->rows > 1) all |= (uint64_t)(pitch * plan_elem_bytes(plan->dtype));
+        return *this;
+    }
+    Bytes& vector(const void* v) {
+        all |= (uint64_t)reinterpret_cast<uintptr_t>(v);
+        return *this;
+    }
+    // elements of a pack
+    int elements() const {
+        const int eb = (int)plan_elem_bytes(plan->dtype);
+        return all % 16 == 0 ? 16 / eb : (eb == 2 && all % 4 == 0 ? 2 : 1);
+    }
+};
 
 olc_status olc_residual_norm_forward(olc_residual_norm_plan* plan, const void* X, int64_t x_pitch, const void* F,
                                      int64_t f_pitch, const void* gate, int64_t gate_pitch, const void* after_gamma,
@@ -1254,16 +1276,16 @@ olc_status olc_residual_norm_forward(olc_residual_norm_plan* plan, const void* X
     const residual::FwdParams p{X, F, gate, after_gamma, after_beta, gamma, beta, Y, Z, stats, x_pitch, f_pitch,
                                 gate_pitch, y_pitch, z_pitch, plan->rows, plan->cols, plan->eps, plan->scale,
                                 (float)(1.0 / (double)plan->cols), plan->after, plan->rms};
-    // 16-byte packs need every row of every operand on a 16-byte boundary
-    const bool wide = plan->cols * eb % 16 == 0 && wide_rows(plan, X, x_pitch) && wide_rows(plan, F, f_pitch) &&
-                      wide_rows(plan, gate, gate_pitch) && wide_rows(plan, Y, y_pitch) && wide_rows(plan, Z, z_pitch) &&
-                      plan_aligned16(after_gamma) && plan_aligned16(after_beta) && plan_aligned16(gamma) &&
-                      plan_aligned16(beta);
+    const int elements = Bytes(plan).rows(X, x_pitch).rows(F, f_pitch).rows(gate, gate_pitch).rows(Y, y_pitch).rows(Z, z_pitch)
+                             .vector(after_gamma).vector(after_beta).vector(gamma).vector(beta).elements();
     return by_type(plan->dtype, [&](auto tag) {
         using T = decltype(tag);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
-        return plan_status(wide ? residual::forward_as<T, 16 / sizeof(T)>(p, plan->state.sm_count, s)
-                                : residual::forward_as<T, 1>(p, plan->state.sm_count, s));
+        const int sms = plan->state.sm_count;
+        if (elements == 16 / (int)sizeof(T)) return plan_status(residual::forward_as<T, 16 / sizeof(T)>(p, sms, s));
+        if constexpr (sizeof(T) == 2)
+            if (elements == 2) return plan_status(residual::forward_as<T, 2>(p, sms, s));
+        return plan_status(residual::forward_as<T, 1>(p, sms, s));
     });
 }
 
@@ -1303,11 +1325,10 @@ olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* 
             if (e == cudaSuccess && o) e = launch_zero_fill(o, cols * eb, s);
         return plan_status(e);
     }
-    const bool wide = cols * eb % 16 == 0 && wide_rows(plan, dY, dy_pitch) && wide_rows(plan, dZ, dz_pitch) &&
-                      wide_rows(plan, F, f_pitch) && wide_rows(plan, Y, y_pitch) && wide_rows(plan, gate, gate_pitch) &&
-                      wide_rows(plan, dX, dx_pitch) && wide_rows(plan, dF, df_pitch) &&
-                      (channel_sum || wide_rows(plan, dgate, dgate_pitch)) && plan_aligned16(after_gamma) &&
-                      plan_aligned16(after_beta) && plan_aligned16(gamma);
+    const int elements = Bytes(plan).rows(dY, dy_pitch).rows(dZ, dz_pitch).rows(F, f_pitch).rows(Y, y_pitch)
+                             .rows(gate, gate_pitch).rows(dX, dx_pitch).rows(dF, df_pitch)
+                             .rows(channel_sum ? nullptr : dgate, dgate_pitch).vector(after_gamma).vector(after_beta)
+                             .vector(gamma).elements();
     residual::BwdParams p{dY, dZ, F, Y, stats, gate, after_gamma, after_beta, gamma, dX, dF, channel_sum ? nullptr : dgate,
                           nullptr, nullptr, dy_pitch, dz_pitch, f_pitch, y_pitch, gate_pitch, dx_pitch, df_pitch,
                           dgate_pitch, rows, cols, plan->scale, (float)(1.0 / (double)cols), plan->after, plan->rms,
@@ -1321,8 +1342,12 @@ olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* 
         const bool gated = which / 25 & 1, all = which / 50;
         auto of = [&](auto shape) { blocks = max64(blocks, shape(rows, cols, sms, operands, weights, gated, all).blocks); };
         of(residual::backward_shape<1>);
-        if (plan->dtype == OLC_FLOAT) of(residual::backward_shape<4>);
-        else of(residual::backward_shape<8>);
+        if (plan->dtype == OLC_FLOAT) {
+            of(residual::backward_shape<4>);
+        } else {
+            of(residual::backward_shape<2>);
+            of(residual::backward_shape<8>);
+        }
     }
     const size_t row_floats = cols > residual::kThreads * residual::kColsPerThread ? ((size_t)rows * 4 + 3) / 4 * 4 : 0;
     const size_t floats = row_floats + (size_t)blocks * residual::SUMS * (size_t)cols;
@@ -1333,8 +1358,10 @@ olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* 
     return by_type(plan->dtype, [&](auto tag) {
         using T = decltype(tag);
         return plan_status(plan->state.use(s, [&] {
-            return wide ? residual::backward_as<T, 16 / sizeof(T)>(p, sms, outputs, s)
-                        : residual::backward_as<T, 1>(p, sms, outputs, s);
+            if (elements == 16 / (int)sizeof(T)) return residual::backward_as<T, 16 / sizeof(T)>(p, sms, outputs, s);
+            if constexpr (sizeof(T) == 2)
+                if (elements == 2) return residual::backward_as<T, 2>(p, sms, outputs, s);
+            return residual::backward_as<T, 1>(p, sms, outputs, s);
         }));
     });
 }

@@ -18,7 +18,7 @@ pytestmark = pytest.mark.gpu
 #: ids, tokens, columns: one of each; odd widths; places that cross many chunks; a sparse
 #: vocabulary; more tokens than one sort block takes; several turns of the sort's loops
 SIZES = [(1, 1, 1), (5, 7, 33), (700, 50, 64), (4096, 3, 96), (3000, 40000, 40), (33, 5000, 1000), (20000, 911, 16),
-         (64, 300000, 8), (513, 2, 2049), (2500, 100, 4096)]
+         (64, 300000, 8), (513, 2, 2049), (2500, 100, 4096), (900, 130, 1350), (70, 9, 2)]
 
 
 def ids_of(n, vocab, seed, strange=True):
@@ -102,7 +102,7 @@ def test_backward_of_uneven_ids(ids, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("pitch,offset", [(72, 0), (67, 0), (64, 1), (80, 3), (72, 8)])
+@pytest.mark.parametrize("pitch,offset", [(72, 0), (67, 0), (64, 1), (80, 3), (72, 8), (66, 2), (74, 6)])
 def test_pitches_and_offsets(pitch, offset, dtype):
     n, vocab, cols = 300, 90, 64
     table, dy, ids = normal((vocab, cols), dtype, 7), normal((n, cols), dtype, 8), ids_of(n, vocab, 9)

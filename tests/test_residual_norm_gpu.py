@@ -114,6 +114,20 @@ def test_forward(rows, cols, form, dtype):
     check_forward(inputs(rows, cols, dtype, form), dtype, form)
 
 
+#: rows of 16-bit elements on 4-byte boundaries
+EVEN = [(40, 1002), (3, 5002), (700, 94), (2, 40002), (160, 2)]
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("rows,cols", EVEN)
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_of_pairs(rows, cols, form, dtype):
+    check_forward(inputs(rows, cols, dtype, form), dtype, form)
+    check_backward(rows, cols, dtype, form)
+    check_forward(inputs(rows, cols, dtype, form), dtype, form, pitch=cols + 2, offset=2)
+    check_backward(rows, cols, dtype, form, pitch=cols + 6, offset=6)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("pitch,offset", [(1040, 0), (1033, 0), (1032, 1), (1032, 8)])
 @pytest.mark.parametrize("same", [False, True])
