@@ -1339,9 +1339,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         for (int w = 0; w < kWarps; ++w) all += sh.light[w];
         return t == 0 ? all : 0;
     };
-    u64 light = light_sum(row.v0, row.v1), listed = t == 0 ? sh.listed : 0, b1, b2;
+    // Nothing is cut: the blocks' lists stay where they are, and need no order.
+    const bool all = !(top_p < 1.f) && o.min_cut == 0;
+    u64 light = light_sum(row.v0, row.v1), listed = 0, b1, b2;
+    if (t == 0) listed = all ? (u64)(sh.listed > kList) : sh.listed;
     team.sum(light, listed, b1, b2);
-    if (listed > (u64)kList) {
+    if (listed > (u64)(all ? 0 : kList)) {
         // A flat row: as many tokens are heavy as the list holds, those within 6, 3, 1.5 or
         // 0.75 octaves of the largest.  (Weights below 2^heavy are then good to 2^-24 of that.)
         u64 n6_3 = 0, n2_1 = 0;                             // two counts each
@@ -1376,10 +1379,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
     }
     // What is kept may end within the list.  For that the light weights' sum need be known
     // so well only that the place of the cut is.
-    enum { DONE, ALL, TOP_P, OTHER, ROUGH };
+    enum { DONE, TOP_P, OTHER, ROUGH };
     Bins bins(team);
-    Found f;
-    for (;;) {
+    Found f{};
+    while (!all) {
         if (team.rank == 0) {
             int size = sh.listed;
             if (pass.heavy_to_list) {                        // the first time
@@ -1391,7 +1394,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
             const u64 target = top_p < 1.f ? share_ceil(top_p, heavy + light - min(light, off)) : ~0ull;
             const int reach = first_reaching(sh.weight, size, target), least_p = kept_of(sh.list, size, o.min_cut);
             const int keep = min(reach + 1, least_p < size ? least_p : size + 1);
-            int what = keep <= size ? DONE : (o.min_cut > 0 ? OTHER : (top_p < 1.f ? TOP_P : ALL));
+            int what = keep <= size ? DONE : (o.min_cut > 0 ? OTHER : TOP_P);
             if (pass.roughly && (what == TOP_P || (keep == reach + 1 &&
                                                    first_reaching(sh.weight, size, share_ceil(top_p, heavy + light + off)) != reach)))
                 what = ROUGH;
@@ -1409,7 +1412,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         light = team.sum(light_sum(row.v0, row.v1));
         pass.histogram = false;
     }
-    if (f.i == DONE) {
+    if (!all && f.i == DONE) {
         team.barrier();                                      // nobody leaves while others read its memory
         return;
     }
@@ -1417,9 +1420,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         any_row(p, r, row, team, s, o);
         return;
     }
-    u64 total = light + f.a, cut = 0;
+    u64 cut = 0;
     pass.heavy_to_list = false;
-    if (f.i == TOP_P) {
+    if (!all) {
         // The cut lies among the light tokens: the histogram shows where, to a fraction of a percent
         // of their weight; the tokens of those steps go into a second list.
         const u64 target = f.b - f.a;                        // of the light weights
@@ -1445,13 +1448,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
                 __syncthreads();
                 if (t == 0) {
                     sh.listed2 = size;
-                    team.tell(Found{good ? sh.list2[at] : 0, good ? f.a + above + sh.weight2[at] : 0, 0, good, 0});
+                    team.tell(Found{good ? sh.list2[at] : 0, 0, 0, good, 0});
                 }
             }
             const Found g = team.told();
             if (g.i) {
                 cut = g.a;
-                total = g.b;
                 break;
             }
             if (t == 0) sh.listed2 = 0;
@@ -1481,10 +1483,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         __syncthreads();
         return part;
     };
-    u64 target = share_floor(u, total), part = add_listed(row.v0, row.v1);
+    u64 part = add_listed(row.v0, row.v1);
     const u64 mine = Team::warp_add(part);
-    u64 sum = t == 0 ? mine : 0, none = 0, before, none_before;
-    team.sum(sum, none, before, none_before);
+    u64 total = t == 0 ? mine : 0, none = 0, before, none_before;
+    team.sum(total, none, before, none_before);
+    u64 target = share_floor(u, total);
     if (target >= before && target < before + mine) {         // the whole block
         target -= before;
         int begin = row.v0, end = row.v1;
