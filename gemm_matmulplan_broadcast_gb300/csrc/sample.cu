@@ -58,6 +58,7 @@ constexpr int kBracket = 512;           // tokens of the steps in which top-p's 
 constexpr int kTurns = 6;               // tries to find the steps of a cut
 constexpr int kMostK = kThreads * 7 / 8;    // the largest top_k that the threads' maxima bound
 constexpr int kOne = 43;                // the largest weight is 2^43; vocab <= 2^20
+constexpr float kLeastHeavy = -0.75f;
 constexpr float kHeavy = -12.f;         // x from which on weights are formed in two parts (or nearer to 0: Scale)
 
 struct Power {                          // 2^(i/64)
@@ -1321,6 +1322,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         team.barrier();                                      // nobody leaves while others read its memory
         return;
     }
+    // Rows that are too flat for the list are mostly seen before it is made: from the share of
+    // the threads whose maximum is heavy (1 - e^-x of them where x tokens a thread are).
+    auto heavy_from = [&](float x) {
+        __syncthreads();
+        s.heavy = x;
+        s.shift = 12 - (int)-x;
+        if (t == 0) sh.scale = s;
+        __syncthreads();
+    };
+    {
+        const int some = 3 * kList / (4 * team.size), most = (int)(kThreads * (1.f - __expf((float)-some / kThreads)));
+        float x = kHeavy;
+        while (__syncthreads_count((own_max - m) * s.hi >= x) > most && x < kLeastHeavy) x *= 0.5f;
+        if (team.size > 1) x = team.maximum(x);
+        if (x > kHeavy) heavy_from(x);
+    }
     // The light weights' sum, and a list of the heavy tokens.
     Pass pass{true, false, top_p < 1.f, false, false, 0, 0.f, 0.f, least, heavy_word<T>(s)};
     auto part_of = [](int begin, int end, int k) { return begin + (int)((int64_t)(end - begin) * k / kWarps); };
@@ -1366,15 +1383,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
             any_row(p, r, row, team, s, o);
             return;
         }
-        __syncthreads();
-        s.heavy = heavy;
-        s.shift = 12 - (int)-heavy;
-        if (t == 0) {
-            sh.listed = 0;
-            sh.scale = s;
-        }
+        if (t == 0) sh.listed = 0;
+        heavy_from(heavy);
         pass.heavy = heavy_word<T>(s);
-        __syncthreads();
         light = team.sum(light_sum(row.v0, row.v1));
     }
     // What is kept may end within the list.  For that the light weights' sum need be known
