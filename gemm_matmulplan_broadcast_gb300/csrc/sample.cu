@@ -12,7 +12,7 @@
 // and passes.  Tokens within 12 octaves of the largest are heavy: weights good to 2^-38 of
 // themselves (x = (z - m) log2(e) / T in two float32s, a table of 2^(i/64), the rest of the
 // exponential in two parts).  The light ones have float32's rounding, 2^-35 of the largest
-// weight.  A row with more than 1024 heavy tokens counts fewer of them as heavy.
+// weight.  A row with more than 512 heavy tokens counts fewer of them as heavy.
 //
 // A row is a cluster of blocks, each with a slice of it, read again by each pass, from L2:
 //   the maximum; then
@@ -30,11 +30,14 @@
 // Rows that none of this fits (far from zero in units of the temperature, many equal logits,
 // large k) go element by element: a histogram, or bisection over values.
 //
+// Rows that nothing cuts need no order: every block's list stays its own.
+//
 // Bound by instructions and, with few rows, by the passes' latency: about 25 issue slots an
 // element for the accurate sum, 12 for the rough one.  Measured: BF16 [1024, 50257] with
-// top-p 181 us (the logits' bytes: 15.5; one row in eight has its cut among the light
-// tokens and takes 100 us of its SM's quarter), FLOAT [64, 131072] unfiltered 54 us, BF16
-// [256, 50257] of mixed settings 85 us, one row of 50257 15 us.
+// top-p 171 us (the logits' bytes: 15.5; one row in eight has its cut among the light
+// tokens and takes 90 us of its SM's quarter), FLOAT [64, 131072] unfiltered 41 us, BF16
+// [256, 50257] of mixed settings 74 to 88 us (the SM that gets the most such rows), one
+// row of 50257 16 us.
 #include <cmath>
 #include <new>
 #include <type_traits>
@@ -53,12 +56,12 @@ constexpr int kMaxCluster = 8;
 constexpr int kBins = 4096;
 constexpr int kOctaves = 45;            // below 2^-45 of the largest a weight is 0
 constexpr int kList = 1024;
+constexpr int kMostHeavy = 512;         // of a row: the list is ordered, so that more cost more than the cuts they decide save
 constexpr int kSmall = 128;             // entries up to which a list is ordered by counting
 constexpr int kBracket = 512;           // tokens of the steps in which top-p's cut lies
 constexpr int kTurns = 6;               // tries to find the steps of a cut
 constexpr int kMostK = kThreads * 7 / 8;    // the largest top_k that the threads' maxima bound
 constexpr int kOne = 43;                // the largest weight is 2^43; vocab <= 2^20
-constexpr float kLeastHeavy = -0.75f;
 constexpr float kHeavy = -12.f;         // x from which on weights are formed in two parts (or nearer to 0: Scale)
 
 struct Power {                          // 2^(i/64)
@@ -1322,21 +1325,50 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         team.barrier();                                      // nobody leaves while others read its memory
         return;
     }
-    // Rows that are too flat for the list are mostly seen before it is made: from the share of
-    // the threads whose maximum is heavy (1 - e^-x of them where x tokens a thread are).
-    auto heavy_from = [&](float x) {
+    // A flat row: kMostHeavy tokens are heavy at most, those within 6, 3, 1.5 or 0.75 octaves
+    // of the largest.  (Weights below 2^heavy are then good to 2^-24 of that.)
+    // False where more tokens are, or equal ones.
+    auto fewer_heavy = [&] {
+        auto packed = [](bool a, bool b, bool c) { return (u64)a + ((u64)b << 21) + ((u64)c << 42); };
+        auto few = [](u64 counts, int k) { return (unsigned)(counts >> (21 * k) & 0x1FFFFF) <= kMostHeavy; };
+        u64 n12_6_3 = 0, n2_1 = 0, b1, b2;
+#pragma unroll 2
+        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
+            const uint4 k = row.words(v);
+            const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const float x = (of_word<T>(w[q * (int)sizeof(T) / 4], q % (4 / (int)sizeof(T))) - m) * s.hi;
+                n12_6_3 += packed(x >= -12.f, x >= -6.f, x >= -3.f);
+                n2_1 += packed(x >= -1.5f, x >= -0.75f, false);
+            }
+        }
+        team.sum(n12_6_3, n2_1, b1, b2);
+        const float heavy = few(n12_6_3, 0) ? kHeavy : few(n12_6_3, 1) ? -6.f : few(n12_6_3, 2) ? -3.f
+                          : few(n2_1, 0) ? -1.5f : few(n2_1, 1) ? -0.75f : 0.f;
+        if (heavy == 0.f) return false;
         __syncthreads();
-        s.heavy = x;
-        s.shift = 12 - (int)-x;
-        if (t == 0) sh.scale = s;
+        s.heavy = heavy;
+        s.shift = 12 - (int)-heavy;
+        if (t == 0) {
+            sh.listed = 0;
+            sh.scale = s;
+        }
         __syncthreads();
+        return true;
     };
-    {
-        const int some = 3 * kList / (4 * team.size), most = (int)(kThreads * (1.f - __expf((float)-some / kThreads)));
-        float x = kHeavy;
-        while (__syncthreads_count((own_max - m) * s.hi >= x) > most && x < kLeastHeavy) x *= 0.5f;
-        if (team.size > 1) x = team.maximum(x);
-        if (x > kHeavy) heavy_from(x);
+    // Flat rows are mostly known from the share of the threads whose maximum is heavy
+    // (1 - e^-x of them where x tokens a thread are): those are counted before the list is
+    // made.  Otherwise the first sum is in vain: FLOAT [106, 96364] with top-p 100 us, so 91
+    // (BF16 [1024, 50257] 184 and 171; with up to 1024 heavy tokens 182, with 128 174).
+    // (The counts alone decide what is heavy, so that a row's token does not depend on how many
+    // blocks share the row.)
+    const int most = (int)(kThreads * (1.f - __expf(-0.75f * kMostHeavy / (float)(kThreads * team.size))));
+    bool flat = __syncthreads_count((own_max - m) * s.hi >= kHeavy) > most;
+    if (team.size > 1) flat = team.maximum(flat) > 0.f;
+    if (flat && !fewer_heavy()) {
+        any_row(p, r, row, team, s, o);
+        return;
     }
     // The light weights' sum, and a list of the heavy tokens.
     Pass pass{true, false, top_p < 1.f, false, false, 0, 0.f, 0.f, least, heavy_word<T>(s)};
@@ -1356,38 +1388,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         for (int w = 0; w < kWarps; ++w) all += sh.light[w];
         return t == 0 ? all : 0;
     };
-    // Nothing is cut: the blocks' lists stay where they are, and need no order.
-    const bool all = !(top_p < 1.f) && o.min_cut == 0;
-    u64 light = light_sum(row.v0, row.v1), listed = 0, b1, b2;
-    if (t == 0) listed = all ? (u64)(sh.listed > kList) : sh.listed;
+    u64 light = light_sum(row.v0, row.v1), listed = t == 0 ? sh.listed : 0, b1, b2;
     team.sum(light, listed, b1, b2);
-    if (listed > (u64)(all ? 0 : kList)) {
-        // A flat row: as many tokens are heavy as the list holds, those within 6, 3, 1.5 or
-        // 0.75 octaves of the largest.  (Weights below 2^heavy are then good to 2^-24 of that.)
-        u64 n6_3 = 0, n2_1 = 0;                             // two counts each
-#pragma unroll 2
-        for (int v = row.v0 + t; v < row.v1; v += kThreads) {
-            const uint4 k = row.words(v);
-            const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const float x = (of_word<T>(w[q * (int)sizeof(T) / 4], q % (4 / (int)sizeof(T))) - m) * s.hi;
-                n6_3 += (u64)(x >= -6.f) + ((u64)(x >= -3.f) << 32);
-                n2_1 += (u64)(x >= -1.5f) + ((u64)(x >= -0.75f) << 32);
-            }
-        }
-        team.sum(n6_3, n2_1, b1, b2);
-        const float heavy = (unsigned)n6_3 <= kList ? -6.f : (n6_3 >> 32) <= kList ? -3.f
-                          : (unsigned)n2_1 <= kList ? -1.5f : (n2_1 >> 32) <= kList ? -0.75f : 0.f;
-        if (heavy == 0.f) {                                  // more tokens, or equal ones
+    if (listed > (u64)kMostHeavy) {
+        if (!fewer_heavy()) {
             any_row(p, r, row, team, s, o);
             return;
         }
-        if (t == 0) sh.listed = 0;
-        heavy_from(heavy);
         pass.heavy = heavy_word<T>(s);
         light = team.sum(light_sum(row.v0, row.v1));
     }
+    // Nothing is cut: the blocks' lists stay where they are, and need no order.
+    const bool all = !(top_p < 1.f) && o.min_cut == 0;
     // What is kept may end within the list.  For that the light weights' sum need be known
     // so well only that the place of the cut is.
     enum { DONE, TOP_P, OTHER, ROUGH };

@@ -278,3 +278,17 @@ def test_refusals():
         with pytest.raises(OlcError) as e:
             SamplePlan(rows, vocab, "float16")
         assert e.value.name == "OLC_ERR_INVALID"
+
+
+@pytest.mark.parametrize("heat", [1.0, 3.0, 20.0, 300.0])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("top_p", [1.0, 0.7])
+def test_a_flat_row_alone_and_among_others(top_p, dtype, heat):
+    """Blocks of 1, 2 and 8 a row: the same token and the same bits of its log probability."""
+    logits, u = draw(640, 20011, dtype, 71)
+    of = lambda rows: run(logits[rows], u[rows], dtype, temperature=heat, top_p=top_p)  # noqa: E731
+    tokens, logprob = of(slice(0, 640))
+    for rows in (slice(0, 200), slice(0, 3), slice(100, 101), slice(630, 640)):
+        some = of(rows)
+        assert torch.equal(some[0], tokens[rows])
+        assert torch.equal(some[1].view(torch.int32), logprob[rows].view(torch.int32))
