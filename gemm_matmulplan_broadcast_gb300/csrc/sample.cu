@@ -1540,10 +1540,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
 // ---- host side -------------------------------------------------------------
 
 // Blocks a row: as many as keep every block resident, with two rounds of packs each
-// or more.
+// or more; twice as many where each still has eight rounds, so that rows with more passes
+// than others hold fewer SMs up (us, resident and twice: FP16 [334, 51426] top-p 110 and 93,
+// FLOAT [106, 96364] 91 and 81; with fewer rounds FLOAT [243, 9822] 48 and 55; four times as
+// many: BF16 [1024, 50257] 182, twice 169).
 inline int cluster_of(int64_t rows, int64_t packs, int sm_count) {
+    const int64_t resident = kBlocksPerSm * (int64_t)sm_count;
     int c = 1;
-    while (c < kMaxCluster && rows * c * 2 <= kBlocksPerSm * (int64_t)sm_count && packs >= (int64_t)c * 2 * 2 * kThreads) c *= 2;
+    while (c < kMaxCluster) {
+        const int64_t blocks = rows * c * 2, rounds = packs / ((int64_t)c * 2 * kThreads);
+        if (blocks > 2 * resident || rounds < (blocks > resident ? 8 : 2)) break;
+        c *= 2;
+    }
     return c;
 }
 
