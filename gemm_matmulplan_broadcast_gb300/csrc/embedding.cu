@@ -432,7 +432,9 @@ inline dim3 grid_of(int64_t units) { return dim3((unsigned)min64(units, kMaxGrid
 
 // Four packs a thread where one each would be two blocks an SM or more; else one (BF16,
 // one pack and four: [2400, 4096] 8.2 and 4.9 us, [300, 4096] 2.4 and 2.2, [1000, 64] 1.9
-// and 2.3).
+// and 2.3).  Eight of the small packs of 16-bit rows off 16-byte boundaries (BF16, four and
+// eight: [16384, 1001] 24.7 and 21.9, [16384, 2050] 46.9 and 38.1; not of FLOAT elements:
+// [16384, 4097] 130 and 168).
 template <typename T, int V>
 cudaError_t forward_as(FwdParams p, int64_t cols, int sm_count, cudaStream_t s) {
     const int64_t packs = cols / V;
@@ -441,8 +443,9 @@ cudaError_t forward_as(FwdParams p, int64_t cols, int sm_count, cudaStream_t s) 
         p.units = ceil_div(p.n, kThreads >> p.tile.log_tx) * p.tile.col_tiles;
         return plan_launch(kernel, grid_of(p.units), dim3(kThreads), 0, s, p);
     };
-    return p.n * packs >= (int64_t)sm_count * 2 * kThreads ? run(forward_kernel<T, V, 4>, 4)
-                                                               : run(forward_kernel<T, V, 1>, 1);
+    constexpr int EACH = sizeof(T) == 2 && V <= 2 ? 8 : 4;
+    return p.n * packs >= (int64_t)sm_count * 2 * kThreads ? run(forward_kernel<T, V, EACH>, EACH)
+                                                           : run(forward_kernel<T, V, 1>, 1);
 }
 
 // Places of a chunk.  A thread adds a chunk's rows one after the other: with few places

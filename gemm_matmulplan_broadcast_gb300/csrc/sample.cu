@@ -34,9 +34,9 @@
 //
 // Bound by instructions and, with few rows, by the passes' latency: about 25 issue slots an
 // element for the accurate sum, 12 for the rough one.  Measured: BF16 [1024, 50257] with
-// top-p 171 us (the logits' bytes: 15.5; one row in eight has its cut among the light
-// tokens and takes 90 us of its SM's quarter), FLOAT [64, 131072] unfiltered 41 us, BF16
-// [256, 50257] of mixed settings 74 to 88 us (the SM that gets the most such rows), one
+// top-p 172 us (the logits' bytes: 15.5; one row in eight has its cut among the light
+// tokens and takes 90 us of its SM's quarter), FLOAT [64, 131072] unfiltered 40 us, BF16
+// [256, 50257] of mixed settings 75 to 90 us (the SM that gets the most such rows), one
 // row of 50257 16 us.
 #include <cmath>
 #include <new>
