@@ -1196,6 +1196,7 @@ struct olc_residual_norm_plan {
     PlanState state;
     olc_dtype dtype;
     int64_t rows, cols;
+    int64_t most_blocks;    // of a gradient call; 0: none yet
     float eps, scale;
     int rms, after;
 };
@@ -1218,6 +1219,7 @@ olc_status olc_residual_norm_plan_create(int64_t rows, int64_t cols, double eps,
     p->dtype = dtype;
     p->rows = rows;
     p->cols = cols;
+    p->most_blocks = 0;
     p->eps = (float)eps;
     p->scale = (float)scale;
     p->rms = norm == OLC_NORM_RMS;
@@ -1292,6 +1294,26 @@ olc_status olc_residual_norm_forward(olc_residual_norm_plan* plan, const void* X
     });
 }
 
+// Blocks that leave partial sums, at most, whatever a call's alignment, operands and
+// outputs: a later call does not have to allocate again.  (Once for a plan: 300 launch
+// shapes are 1.6 us of a call.)
+static int64_t most_blocks(olc_dtype dtype, int64_t rows, int64_t cols, int sms) {
+    int64_t blocks = 0;
+    for (int which = 0; which < 5 * 5 * 4; ++which) {
+        const int operands = 1 + which % 5, weights = which / 5 % 5;
+        const bool gated = which / 25 & 1, all = which / 50;
+        auto of = [&](auto shape) { blocks = max64(blocks, shape(rows, cols, sms, operands, weights, gated, all).blocks); };
+        of(residual::backward_shape<1>);
+        if (dtype == OLC_FLOAT) {
+            of(residual::backward_shape<4>);
+        } else {
+            of(residual::backward_shape<2>);
+            of(residual::backward_shape<8>);
+        }
+    }
+    return blocks;
+}
+
 olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* dY, int64_t dy_pitch, const void* dZ,
                                       int64_t dz_pitch, const void* F, int64_t f_pitch, const void* Y, int64_t y_pitch,
                                       const float* stats, const void* gate, int64_t gate_pitch,
@@ -1336,22 +1358,9 @@ olc_status olc_residual_norm_backward(olc_residual_norm_plan* plan, const void* 
                           nullptr, nullptr, dy_pitch, dz_pitch, f_pitch, y_pitch, gate_pitch, dx_pitch, df_pitch,
                           dgate_pitch, rows, cols, plan->scale, (float)(1.0 / (double)cols), plan->after, plan->rms,
                           channel_sum, 0, device_error_word()};
-    // the partial sums of every kernel fit: a call with other alignment, operands or
-    // outputs does not have to allocate again
     const int sms = plan->state.sm_count;
-    int64_t blocks = 0;
-    for (int which = 0; which < 5 * 5 * 4; ++which) {
-        const int operands = 1 + which % 5, weights = which / 5 % 5;
-        const bool gated = which / 25 & 1, all = which / 50;
-        auto of = [&](auto shape) { blocks = max64(blocks, shape(rows, cols, sms, operands, weights, gated, all).blocks); };
-        of(residual::backward_shape<1>);
-        if (plan->dtype == OLC_FLOAT) {
-            of(residual::backward_shape<4>);
-        } else {
-            of(residual::backward_shape<2>);
-            of(residual::backward_shape<8>);
-        }
-    }
+    if (plan->most_blocks == 0) plan->most_blocks = most_blocks(plan->dtype, rows, cols, sms);
+    const int64_t blocks = plan->most_blocks;
     const size_t row_floats = cols > residual::kThreads * residual::kColsPerThread ? ((size_t)rows * 4 + 3) / 4 * 4 : 0;
     const size_t floats = row_floats + (size_t)blocks * residual::SUMS * (size_t)cols;
     st = plan->state.ensure(floats * sizeof(float));

@@ -37,8 +37,9 @@
 // top-p 172 us (the logits' bytes: 15.5; one row in eight has its cut among the light
 // tokens and takes 90 us of its SM's quarter), FLOAT [64, 131072] unfiltered 40 us, BF16
 // [256, 50257] of mixed settings 75 to 90 us (the SM that gets the most such rows), one
-// row of 50257 16 us.
+// row of 50257 14 us.
 #include <cmath>
+#include <cstring>
 #include <new>
 #include <type_traits>
 
@@ -1555,15 +1556,23 @@ inline int cluster_of(int64_t rows, int64_t packs, int sm_count) {
     return c;
 }
 
+struct Powers {
+    Power of[64];
+    Powers() {
+        for (int i = 0; i < 64; ++i) {
+            const double v = std::exp2(i / 64.0);
+            of[i].fixed = (u64)std::llrint(std::ldexp(v, kOne));
+            of[i].hi = (float)v;
+            of[i].lo = (float)(v - (double)of[i].hi);
+        }
+    }
+};
+
 template <typename T>
 cudaError_t forward_as(Params p, int64_t rows, int sm_count, cudaStream_t s) {
     p.cluster = cluster_of(rows, ceil_div(p.vocab, 16 / sizeof(T)), sm_count);
-    for (int i = 0; i < 64; ++i) {
-        const double v = std::exp2(i / 64.0);
-        p.powers[i].fixed = (u64)std::llrint(std::ldexp(v, kOne));
-        p.powers[i].hi = (float)v;
-        p.powers[i].lo = (float)(v - (double)p.powers[i].hi);
-    }
+    static const Powers powers;
+    std::memcpy(p.powers, powers.of, sizeof powers.of);
     const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(sample_kernel<T>), (int)sizeof(Shared));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
