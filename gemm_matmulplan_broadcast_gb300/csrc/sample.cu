@@ -91,7 +91,7 @@ struct Scale {
     float least;            // z - m is not taken below this one (x = -64, where weights are 0)
     int exact;              // the light weights' differences z - m in two parts
     float heavy;            // x from which on tokens are heavy: kHeavy, nearer to 0 in rows with too many of those
-    int shift;              // light weights are scaled by 2^(43 - shift): below 2^31
+    int shift;              // light weights are scaled by 2^(43 - shift): 2^31 at the limit of the heavy ones
 };
 
 // what one block tells the others of its cluster
@@ -325,7 +325,7 @@ __device__ __forceinline__ u64 light_weights(F2 z, const Scale& s, float low) {
         if (!(d0 * -s.hi * kStepsPerOctave < low)) w0 = 0;
         if (!(d1 * -s.hi * kStepsPerOctave < low)) w1 = 0;
     }
-    return (u64)(w0 + w1);                      // each below 2^31
+    return (u64)w0 + w1;                        // (next to the limit of the heavy tokens both may round to 2^31)
 }
 
 // Rows whose maximum is so far from zero, in units of the temperature, that the type's steps
