@@ -548,7 +548,8 @@ __device__ __forceinline__ u64 row_sum(const Row<T>& row, Team& team, F&& value)
 }
 
 // One warp: the element of packs [begin, end) at which the running sum of value(z,
-// index) exceeds `target`; tells its index, the value there, `total` and z.
+// index) exceeds `target`; tells its index, the value there, `total` and z (-1, 0 and NaN
+// where the sum never does).
 template <typename T, typename F>
 __device__ __forceinline__ void find_in(const Row<T>& row, Team& team, int begin, int end, u64 target, u64 total,
                                         F&& value) {
@@ -580,9 +581,10 @@ __device__ __forceinline__ void find_in(const Row<T>& row, Team& team, int begin
                 }
             }
         }
-        if (past) break;
+        if (past) return;
         target -= __shfl_sync(0xffffffffu, sums, 31);
     }
+    if (lane == 0) team.tell(Found{0, total, 0, -1, 0x7FC00000});
 }
 
 // The lowest index at which the running sum of value(z, index) exceeds `target`
@@ -1324,6 +1326,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
             choose(p, r, row, u, min(keep, kept_of(sh.list, size, o.min_cut)), s, sh);
         }
         team.barrier();                                      // nobody leaves while others read its memory
+        return;
+    }
+    // FLOAT16's values are 2^-24 apart near zero.  Where that is four octaves or more, a word that is
+    // raised to `least` may lie far below x = -64, out of the light weights' range.
+    if (std::is_same_v<T, __half> && s.hi >= 0x1p26f) {
+        any_row(p, r, row, team, s, o);
         return;
     }
     // A flat row: kMostHeavy tokens are heavy at most, those within 6, 3, 1.5 or 0.75 octaves
