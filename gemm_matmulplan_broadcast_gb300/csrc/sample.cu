@@ -18,9 +18,9 @@
 //   the maximum; then
 //   top-k: a bound that the k largest reach (the k-th largest of the threads' own maxima),
 //     the list of the tokens that reach it, and everything else on that list;
-//   or the list of the heavy tokens with the light weights' sum, for top-p to 2^-15 of it
-//     alone by the exponential unit.  If what is kept ends among the heavy tokens wherever
-//     the sum lies within that, the list gives the token.  Otherwise the sum again, as
+//   or the list of the heavy tokens with the light weights' sum, for top-p alone by the
+//     exponential unit, good to 2^-16 of it (2^-12 with 4096 terms a thread).  If what is kept ends
+//     among the heavy tokens wherever the sum lies within that, the list gives the token.  Otherwise the sum again, as
 //     accurate as the weights, with a histogram of counts over 4096 equal steps of x, 45
 //     octaves: it shows to a fraction of a percent in which steps the light
 //     weights reach top-p, a second list takes those steps' tokens, the weights above
@@ -1141,7 +1141,7 @@ __device__ __noinline__ void any_row(const Params& p, int64_t r, const Row<T> ro
 struct Pass {
     bool heavy_to_list;     // lists the heavy tokens
     bool histogram;         // counts the light tokens by their steps
-    bool roughly;           // (with heavy_to_list) sums to 2^-15 of the sum alone, at a third of the cost
+    bool roughly;           // (with heavy_to_list) sums by the exponential unit alone, at a third of the cost
     bool masked;            // sums the steps below `low` only
     bool steps_to_list2;    // lists the light tokens of steps [low, high)
     int log_each;           // of the histogram (Bins)
@@ -1412,6 +1412,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
     // What is kept may end within the list.  For that the light weights' sum need be known
     // so well only that the place of the cut is.
     enum { DONE, TOP_P, OTHER, ROUGH };
+    // How far it may be off when formed roughly.  A thread adds up `terms` of float32; each is off by
+    // 2^-22 by the exponential unit and by three roundings of an x down to -44, together and with the
+    // weights' own error below 128 2^-24; what lies below that x is less than a unit of the weights each.
+    const u64 terms = V * ((row.packs - 1) / (kThreads * team.size) + 1);
+    auto rough_off = [&] { return ((light >> 24) + 1) * (terms + 128) + ((u64)p.vocab << s.shift); };
     Bins bins(team);
     Found f{};
     while (!all) {
@@ -1422,7 +1427,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
                 order_list(sh.list, sh.weight, size, s, sh);
                 if (t == 0) sh.listed = size;
             }
-            const u64 heavy = sh.weight[size - 1], off = pass.roughly ? (light >> 15) + 1 : 0;
+            const u64 heavy = sh.weight[size - 1], off = pass.roughly ? rough_off() : 0;
             const u64 target = top_p < 1.f ? share_ceil(top_p, heavy + light - min(light, off)) : ~0ull;
             const int reach = first_reaching(sh.weight, size, target), least_p = kept_of(sh.list, size, o.min_cut);
             const int keep = min(reach + 1, least_p < size ? least_p : size + 1);
