@@ -40,7 +40,9 @@ class TokenModel:
     """Plans and activations for ``rows`` ids.  ``forward`` takes int64 ids and
     targets [rows] (negative: ignored) and a dict of parameters; ``backward``
     gives a dict of their gradients; ``next_tokens`` draws a token for each id
-    from one uniform number each."""
+    from one uniform number each.  All use the same activations: after
+    ``logits`` or ``next_tokens``, ``backward`` raises until the next
+    ``forward``."""
 
     def __init__(self, rows: int, layers: int, d_model: int, d_hidden: int, vocab: int, dtype: str = "bfloat16",
                  act: str = "silu", device="cuda"):
@@ -65,11 +67,11 @@ class TokenModel:
         self.stats = [new(4, rows, of=f32) for _ in range(layers)]
         self.mean, self.rstd, self.logprob, self.entropy, self.lse, self.drawn = (new(rows, of=f32) for _ in range(6))
         self.z = new(rows, vocab)
-        self._back = None
+        self.targets = self._back = None
 
     def logits(self, ids, p):
         """[rows, vocab], from the ids alone."""
-        self.ids, self.p = ids, p
+        self.ids, self.p, self.targets = ids, p, None
         self.embed.forward(p["table"], ids, self.x[0])
         self.norm.forward(self.x[0], p["gamma0"], p["beta0"], self.n[0], mean=self.mean, rstd=self.rstd)
         for i in range(self.layers):
@@ -83,8 +85,8 @@ class TokenModel:
 
     def forward(self, ids, targets, p):
         """(logprob, entropy) of the targets behind the ids, float32 [rows]."""
-        self.targets = targets
         self.score.forward(self.logits(ids, p), targets, self.logprob, entropy=self.entropy, lse=self.lse)
+        self.targets = targets
         return self.logprob, self.entropy
 
     def next_tokens(self, ids, uniforms, p, temperature=None, top_k=None, top_p=None, min_p=None):
@@ -109,6 +111,8 @@ class TokenModel:
     def backward(self, dlogprob, dentropy=None):
         """Gradients of every parameter of the last ``forward``."""
         import torch
+        if self.targets is None:
+            raise RuntimeError("backward follows forward: the activations are another call's")
         p, plans = self.p, self._backward_plans()
         like = torch.empty_like
         grads = {k: like(p[k]) for k in parameter_names(self.layers)}
