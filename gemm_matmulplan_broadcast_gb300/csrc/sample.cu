@@ -11,8 +11,10 @@
 // (2^43 for the largest): their sums are the same in any order, across warps, blocks
 // and passes.  Tokens within 12 octaves of the largest are heavy: weights good to 2^-38 of
 // themselves (x = (z - m) log2(e) / T in two float32s, a table of 2^(i/64), the rest of the
-// exponential in two parts).  The light ones have float32's rounding, 2^-35 of the largest
-// weight.  A row with more than 512 heavy tokens counts fewer of them as heavy.
+// exponential in two parts).  The light ones have float32's rounding, 2^-23 of themselves, so
+// 2^-35 of the largest weight.  A row with more than 512 heavy tokens counts fewer of them as heavy,
+// down to those within 0.75 octaves; its light weights are scaled to stay within 32 bits, so that their
+// unit is up to 2^-31 of the largest weight: they have half of that on top, and those below it are 0.
 //
 // A row is a cluster of blocks, each with a slice of it, read again by each pass, from L2:
 //   the maximum; then
@@ -518,8 +520,8 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {
 // Exclusive sums over the block's threads in order, and over `slot`'s warps.
 __device__ __forceinline__ u64 block_scan(u64 v, u64* slot) {
     const u64 inclusive = warp_scan(v);
-    // (lane 0 stores: with the store in lane 31, as nvcc 13.0 compiled this function, the
-    // place of an 8-byte word was off its boundary)
+    // (Lane 0 stores a total that all lanes have.  With the store in lane 31, of its own sum, calls
+    // ended with a misaligned address here; what made it so is not known.  This form has not.)
     const u64 total = __shfl_sync(0xffffffffu, inclusive, 31);
     const int warp = threadIdx.x >> 5;
     __syncthreads();
@@ -1335,7 +1337,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         return;
     }
     // A flat row: kMostHeavy tokens are heavy at most, those within 6, 3, 1.5 or 0.75 octaves
-    // of the largest.  (Weights below 2^heavy are then good to 2^-24 of that.)
+    // of the largest.  (Weights below 2^heavy are then good to 2^-23 of themselves and half a unit
+    // of 2^(shift - 43), 2^-32 at most.)
     // False where more tokens are, or equal ones.
     auto fewer_heavy = [&] {
         auto packed = [](bool a, bool b, bool c) { return (u64)a + ((u64)b << 21) + ((u64)c << 42); };

@@ -693,8 +693,9 @@ typedef struct olc_sample_plan olc_sample_plan;
  * below 1.  Logits of -inf have no weight.  A row of nothing but -inf gives token -1 and
  * logprob -inf; a NaN or +inf logit, a NaN among the row's settings, or a
  * temperature that is negative or infinite give token -1 and logprob NaN.
- * Weights are 64-bit integers, the largest 2^43, good to 2^-35 of the largest, or,
- * in rows with more than 512 tokens above 2^-12 of it, to 2^-24 of themselves; their
+ * Weights are 64-bit integers, the largest 2^43, good to 2^-35 of the largest.  In
+ * rows with more than 512 tokens above 2^-12 of it they are good to 2^-23 of themselves
+ * and 2^-32 of the largest besides (lighter ones than that may count as 0).  Their
  * sums and the results depend neither on an order of summation nor on the other rows.
  * 0 <= rows < 2^27, 1 <= vocab <= 2^20.  Errors: OLC_ERR_NULL, OLC_ERR_DTYPE,
  * OLC_ERR_NEGATIVE_DIM, OLC_ERR_INVALID, OLC_ERR_OOM.
