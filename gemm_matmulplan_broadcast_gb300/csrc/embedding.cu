@@ -11,7 +11,7 @@
 //
 // Backward.  Sums in an order that does not change from run to run need the
 // places of each token together and in order: a stable counting sort by token
-// (sort_kernel, one launch: a block owns a range of the vocabulary and reads all
+// (sort_kernel, one launch: a block owns every 128th token, or fewer, and reads all
 // ids).  The sums then go over chunks of equal length of the sorted places, so that a
 // token that fills half of the batch costs no block more than any other
 // (sum_kernel); a token whose places cross chunks leaves partial sums that
@@ -500,12 +500,14 @@ inline Layout layout_of(int64_t n, int64_t vocab, int64_t cols, int64_t chunks) 
     return l;
 }
 
-// Elements that every row's start and length divide by: 16 bytes of them, 4, or one.
-inline int pack_bytes(int64_t bytes, std::initializer_list<const void*> pointers, std::initializer_list<int64_t> pitches) {
-    uint64_t all = (uint64_t)bytes;
+// Elements of eb bytes in a pack: 16 bytes of them, a pair of 16-bit ones, or one, on a boundary of
+// whose size every row starts and ends.
+inline int pack_elements(int64_t eb, int64_t cols, std::initializer_list<const void*> pointers,
+                         std::initializer_list<int64_t> pitches) {
+    uint64_t all = (uint64_t)(cols * eb);
     for (const void* p : pointers) all |= (uint64_t)reinterpret_cast<uintptr_t>(p);
-    for (int64_t p : pitches) all |= (uint64_t)p;
-    return all % 16 == 0 ? 16 : (all % 4 == 0 ? 4 : 2);
+    for (int64_t p : pitches) all |= (uint64_t)(p * eb);
+    return all % 16 == 0 ? (int)(16 / eb) : (eb == 2 && all % 4 == 0 ? 2 : 1);
 }
 
 template <typename T, int V>
@@ -584,15 +586,15 @@ olc_status olc_embedding_forward(olc_embedding_plan* plan, const void* table, in
     const olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
     const embedding::FwdParams p{table, tokens, Y, table_pitch, y_pitch, n, plan->vocab, plan->scale, {}, 0};
-    const int bytes = embedding::pack_bytes(cols * eb, {table, Y},
-                                            {plan->vocab <= 1 ? 0 : table_pitch * eb, n == 1 ? 0 : y_pitch * eb});
+    const int elements = embedding::pack_elements(eb, cols, {table, Y},
+                                                  {plan->vocab <= 1 ? 0 : table_pitch, n == 1 ? 0 : y_pitch});
     return by_type(plan->dtype, [&](auto tag) {
         using T = decltype(tag);
         const cudaStream_t s = static_cast<cudaStream_t>(stream);
         const int sms = plan->state.sm_count;
-        if (bytes == 16) return plan_status(embedding::forward_as<T, 16 / sizeof(T)>(p, cols, sms, s));
+        if (elements == 16 / (int)sizeof(T)) return plan_status(embedding::forward_as<T, 16 / sizeof(T)>(p, cols, sms, s));
         if constexpr (sizeof(T) == 2)
-            if (bytes == 4) return plan_status(embedding::forward_as<T, 2>(p, cols, sms, s));
+            if (elements == 2) return plan_status(embedding::forward_as<T, 2>(p, cols, sms, s));
         return plan_status(embedding::forward_as<T, 1>(p, cols, sms, s));
     });
 }
@@ -609,9 +611,8 @@ olc_status olc_embedding_backward(olc_embedding_plan* plan, const void* dY, int6
     if (plan_misaligned(dY, eb) || plan_misaligned(tokens, 8) || plan_misaligned(dtable, eb)) return OLC_ERR_INVALID;
     olc_status st = plan->state.bind();
     if (st != OLC_OK) return st;
-    const int bytes = embedding::pack_bytes(cols * eb, {dY, dtable},
-                                            {n <= 1 ? 0 : dy_pitch * eb, vocab == 1 ? 0 : dtable_pitch * eb});
-    const int elements = bytes == 16 ? (int)(16 / eb) : (eb == 2 && bytes == 4 ? 2 : 1);
+    const int elements = embedding::pack_elements(eb, cols, {dY, dtable},
+                                                  {n <= 1 ? 0 : dy_pitch, vocab == 1 ? 0 : dtable_pitch});
     const int length = embedding::chunk_length(n);
     const int64_t chunks = ceil_div(n, length);
     const embedding::Layout l = embedding::layout_of(n, vocab, cols, chunks);

@@ -8,8 +8,9 @@
 
 namespace olc {
 
-// V elements of T in one access (V = 1: any alignment; else 16 bytes), and
-// the same as pairs of float32 (V = 1: the second of the pair is not used).
+// V elements of T in one access on a boundary of its V sizeof(T) bytes: 16 bytes, the 4 of a pair
+// of 16-bit elements, or one element; and the same as pairs of float32 (V = 1: the second of
+// the pair is not used).
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
     T v[V];
@@ -92,8 +93,8 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
     return s;
 }
 
-// A thread's columns of a row: packs of V at (base + i stride) V, or, for rows of
-// any alignment (V = 1), pairs of single elements `stride` apart: two elements
+// A thread's columns of a row: packs of V at (base + i stride) V on boundaries of their size, or,
+// for rows of any alignment (V = 1), pairs of single elements `stride` apart: two elements
 // an instruction either way.  Single elements are addressed and tested one by
 // one only where the row ends: `full` tells that the i-th pair of every lane of
 // the warp lies inside the row.
