@@ -36,10 +36,10 @@
 //
 // Bound by instructions and, with few rows, by the passes' latency: about 25 issue slots an
 // element for the accurate sum, 12 for the rough one.  Measured: BF16 [1024, 50257] with
-// top-p 172 us (the logits' bytes: 15.5; one row in eight has its cut among the light
+// top-p 173 us (the logits' bytes: 15.5; one row in eight has its cut among the light
 // tokens and takes 90 us of its SM's quarter), FLOAT [64, 131072] unfiltered 40 us, BF16
-// [256, 50257] of mixed settings 75 to 90 us (the SM that gets the most such rows), one
-// row of 50257 14 us.
+// [256, 50257] of mixed settings 82 us (the SM that gets the most such rows), one
+// row of 50257 16 us.
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -1444,7 +1444,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const __
         }
         f = team.told();
         if (f.i != ROUGH) break;
-        // to 2^-36 then, with a histogram of the light tokens' steps: the cut may lie among them
+        // as well as the weights then, with a histogram of the light tokens' steps: the cut may lie among them
         bins.clear();
         pass.heavy_to_list = pass.roughly = false;
         pass.histogram = true;

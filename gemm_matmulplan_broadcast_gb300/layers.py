@@ -5,10 +5,11 @@
 
 A plan is made for fixed sizes and one element type ("float32", "float16" or
 "bfloat16"); its calls take CUDA tensors and outputs that the caller owns and
-enqueue kernels on ``stream`` (torch's current stream by default).  Row
-tensors are [rows, cols] (any leading dimensions when contiguous) with
-unit-stride columns; a two-dimensional one may have any row pitch.  The
-one-shot functions return memory of ``stream``, and read their inputs there:
+enqueue kernels on ``stream`` (torch's current stream by default).  A plan's
+first gradient call may allocate device memory that the plan keeps: make it
+before a graph capture.  Row tensors are [rows, cols] (any leading dimensions
+when contiguous) with unit-stride columns; a two-dimensional one may have any
+row pitch.  The one-shot functions return memory of ``stream``, and read their inputs there:
 where it is not torch's current stream, the two have to be ordered by the
 caller (``wait_stream``), as for torch's own operators.
 """
